@@ -17,3 +17,11 @@ from .binding import (  # noqa: F401
     B_KN,
     B_NK,
 )
+from .groups import (  # noqa: F401
+    gemm_relu_grouped,
+    gemm_relu_grouped_backward,
+    gemm_relu_adapters,
+    grouped_workspace_bytes,
+    grouped_backward_workspace_bytes,
+    adapters_workspace_bytes,
+)

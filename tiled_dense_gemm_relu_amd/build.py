@@ -24,7 +24,8 @@ STREAM_CEILING_PATH = os.path.join(PKG, "stream_ceiling")
 KERNEL_TIMELINE_PATH = os.path.join(PKG, "kernel_timeline")
 ARCH = "gfx950"
 
-SOURCES = ["gemm_relu_api.hip", "kernels_f16.hip", "kernels_bf16.hip"]
+SOURCES = ["gemm_relu_api.hip", "kernels_f16.hip", "kernels_bf16.hip", "groups_api.hip", "groups_f16.hip",
+           "groups_bf16.hip"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",

@@ -3,12 +3,12 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
 
 #include "../../include/gemm_relu.h"
+#include "device.hpp"
 #include "kernel_table.hpp"
 
 namespace gemm_relu_hip {
@@ -44,13 +44,6 @@ int vec_width(const void* p, int64_t row_len)
     for (int v = 8; v > 1; v /= 2)
         if (row_len % v == 0 && addr % (uintptr_t)(2 * v) == 0) return v;
     return 1;
-}
-
-bool overlaps(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes)
-{
-    if (a_bytes <= 0 || b_bytes <= 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + (uintptr_t)b_bytes && b0 < a0 + (uintptr_t)a_bytes;
 }
 
 // Every check that needs no device.  Fills `plan` on success.
@@ -361,30 +354,6 @@ int device_scratch(void** out)
     return GEMM_RELU_OK;
 }
 
-// Per-device cache: 0 unknown, > 0 gfx950 with that many CUs, -1 something else.
-std::atomic<int> g_device_cus[64];
-
-// Checks that the current device is a gfx950 and returns its CU count in *cus.
-int check_device(int* cus)
-{
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return GEMM_RELU_ERR_NO_DEVICE;
-    if (dev < 64) {
-        const int known = g_device_cus[dev].load(std::memory_order_relaxed);
-        if (known != 0) {
-            *cus = known;
-            return known > 0 ? GEMM_RELU_OK : GEMM_RELU_ERR_NO_DEVICE;
-        }
-    }
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return GEMM_RELU_ERR_NO_DEVICE;
-    const bool ok = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 && prop.multiProcessorCount > 0;
-    const int value = ok ? prop.multiProcessorCount : -1;
-    if (dev < 64) g_device_cus[dev].store(value, std::memory_order_relaxed);
-    *cus = value;
-    return ok ? GEMM_RELU_OK : GEMM_RELU_ERR_NO_DEVICE;
-}
-
 int launch(const Plan& p, const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int dtype,
            int cus, void* workspace, hipStream_t stream)
 {
@@ -558,14 +527,14 @@ const char* gemm_relu_strerror(int code)
     case GEMM_RELU_OK: return "ok";
     case GEMM_RELU_ERR_INVALID_ARG: return "invalid argument (null pointer or negative dimension)";
     case GEMM_RELU_ERR_BAD_DTYPE: return "unsupported dtype (expected GEMM_RELU_F16 or GEMM_RELU_BF16)";
-    case GEMM_RELU_ERR_ALIAS: return "C overlaps A or B";
+    case GEMM_RELU_ERR_ALIAS: return "an output (C, a gradient or the workspace) overlaps another argument";
     case GEMM_RELU_ERR_MISALIGNED: return "pointer not 2-byte aligned";
     case GEMM_RELU_ERR_NO_DEVICE: return "no current HIP device, or the device is not gfx950";
     case GEMM_RELU_ERR_LAUNCH: return "kernel launch failed";
     case GEMM_RELU_ERR_TOO_LARGE: return "dimensions exceed the supported range";
     case GEMM_RELU_ERR_BAD_CONFIG: return "unknown kernel configuration id";
     case GEMM_RELU_ERR_BAD_LAYOUT: return "unknown B layout (expected GEMM_RELU_B_KN or GEMM_RELU_B_NK)";
-    case GEMM_RELU_ERR_WORKSPACE: return "split-K workspace missing, too small or not 256-byte aligned";
+    case GEMM_RELU_ERR_WORKSPACE: return "workspace missing, too small or not 256-byte aligned";
     case GEMM_RELU_ERR_SCRATCH:
         return "split-K partials of this call exceed the library's static scratch (gemm_relu_splitk_noalloc)";
     default: return "unknown error code";

@@ -1,0 +1,282 @@
+// C ABI of the products whose rows choose their weights (gemm_relu_groups.h):
+// argument checks, kernel choice and launch.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/gemm_relu_groups.h"
+#include "device.hpp"
+#include "groups_table.hpp"
+#include "kernel_table.hpp"
+
+namespace gemm_relu_hip {
+namespace {
+
+constexpr int64_t kMaxDim = int64_t(1) << 20;
+constexpr int64_t kMaxGroups = 65535;
+constexpr int64_t kMaxRank = 256;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+// One matrix (or stack of matrices) argument.
+struct Span {
+    const void* p;
+    int64_t bytes;
+};
+
+bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+// Checks shared by all entry points: inputs and outputs present, aligned, and
+// no output (or the workspace) sharing bytes with anything else.
+int check_spans(const Span* in, int n_in, const Span* words, int n_words, const Span* out, int n_out)
+{
+    for (int i = 0; i < n_in; ++i) {
+        if (in[i].bytes > 0 && !in[i].p) return GEMM_RELU_ERR_INVALID_ARG;
+        if (in[i].bytes > 0 && !aligned(in[i].p, 2)) return GEMM_RELU_ERR_MISALIGNED;
+    }
+    for (int i = 0; i < n_words; ++i) {
+        if (words[i].bytes > 0 && !words[i].p) return GEMM_RELU_ERR_INVALID_ARG;
+        if (words[i].bytes > 0 && !aligned(words[i].p, 4)) return GEMM_RELU_ERR_MISALIGNED;
+    }
+    for (int i = 0; i < n_out; ++i) {
+        if (out[i].bytes > 0 && !out[i].p) return GEMM_RELU_ERR_INVALID_ARG;
+        if (out[i].bytes > 0 && !aligned(out[i].p, 2)) return GEMM_RELU_ERR_MISALIGNED;
+        for (int j = 0; j < n_in; ++j)
+            if (overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return GEMM_RELU_ERR_ALIAS;
+        for (int j = 0; j < n_words; ++j)
+            if (overlaps(out[i].p, out[i].bytes, words[j].p, words[j].bytes)) return GEMM_RELU_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return GEMM_RELU_ERR_ALIAS;
+    }
+    return GEMM_RELU_OK;
+}
+
+int check_shape(int64_t M, int64_t N, int64_t K, int64_t groups, int dtype, int b_layout)
+{
+    if (dtype != GEMM_RELU_F16 && dtype != GEMM_RELU_BF16) return GEMM_RELU_ERR_BAD_DTYPE;
+    if (b_layout != GEMM_RELU_B_KN && b_layout != GEMM_RELU_B_NK) return GEMM_RELU_ERR_BAD_LAYOUT;
+    if (M < 0 || N < 0 || K < 0 || groups < 1) return GEMM_RELU_ERR_INVALID_ARG;
+    if (M > kMaxDim || N > kMaxDim || K > kMaxDim || groups > kMaxGroups) return GEMM_RELU_ERR_TOO_LARGE;
+    return GEMM_RELU_OK;
+}
+
+int check_workspace(void* workspace, int64_t bytes, int64_t need)
+{
+    if (need == 0) return GEMM_RELU_OK;
+    return !workspace || bytes < need || !aligned(workspace, 256) ? GEMM_RELU_ERR_WORKSPACE : GEMM_RELU_OK;
+}
+
+// Index of the widest load (kLoadWidths) that every given row length and address allows.
+int load_width(std::initializer_list<Span> operands)
+{
+    for (int w = 0; w < kNumLoadWidths; ++w) {
+        bool ok = true;
+        for (const Span& s : operands)   // bytes: here the row length in elements
+            ok = ok && s.bytes % kLoadWidths[w] == 0 && aligned(s.p, 2 * kLoadWidths[w]);
+        if (ok) return w;
+    }
+    return kNumLoadWidths - 1;
+}
+
+int store_width(const void* c, int64_t n) { return n % 8 == 0 && aligned(c, 16) ? 2 : n % 4 == 0 && aligned(c, 8) ? 1 : 0; }
+
+const GroupKernels& kernels(int dtype) { return dtype == GEMM_RELU_F16 ? group_kernels_f16() : group_kernels_bf16(); }
+
+int enqueue(const void* fn, int64_t grid, int grid_y, int threads, void** args, hipStream_t stream)
+{
+    const hipError_t err = hipLaunchKernel(fn, dim3((unsigned)grid, (unsigned)grid_y), dim3((unsigned)threads), args, 0, stream);
+    return err == hipSuccess ? GEMM_RELU_OK : GEMM_RELU_ERR_LAUNCH;
+}
+
+int zero_fill(void* p, int64_t halves, hipStream_t stream)
+{
+    if (halves <= 0) return GEMM_RELU_OK;
+    size_t count = (size_t)halves;
+    void* args[] = {&p, &count};
+    return enqueue(zero_fill_kernel(), std::min<int64_t>(ceil_div(halves, 256), 65536), 1, 256, args, stream);
+}
+
+// Row tiles that `groups` groups (and the rows of none) can have among M rows:
+// whole tiles, and one partial tile for each.
+int64_t most_row_tiles(int64_t M, int64_t groups, int64_t rows) { return std::min(M, M / rows + groups + 1); }
+
+// A product over row groups (M, N, K > 0).
+int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, hipStream_t stream)
+{
+    const int64_t grid = most_row_tiles(a.m, a.groups, 128) * ceil_div(a.n, 128);
+    if (grid > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
+    a.c_vec = store_width(a.c, a.n);
+    const int w = load_width({{a.a, a.k}, {a.b, b_layout == GEMM_RELU_B_NK ? a.k : a.n}});
+    void* args[] = {&a, &ad};
+    return enqueue(kernels(dtype).rows_tiled[b_layout][w], grid, 1, 256, args, stream);
+}
+
+// Sums over each group's rows (I, J > 0).
+int launch_weights(WeightArgs a, int dtype, hipStream_t stream)
+{
+    const int64_t grid = int64_t(a.groups) * ceil_div(a.i, 128) * ceil_div(a.j, 128);
+    if (grid > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
+    a.c_vec = store_width(a.out, a.j);
+    const int w = load_width({{a.p, a.i}, {a.q, a.j}});
+    void* args[] = {&a};
+    return enqueue(kernels(dtype).weight_tiled[w], grid, 1, 256, args, stream);
+}
+
+// Workspace layout: the counters, then each operator's intermediates.
+struct AdapterSpace {
+    int64_t rank_pad, t, factor, bytes;
+};
+AdapterSpace adapter_space(int64_t M, int64_t rank)
+{
+    AdapterSpace s;
+    s.rank_pad = round_up(rank, 32);
+    s.t = GEMM_RELU_GROUPS_COUNTER_BYTES;
+    s.factor = s.t + round_up(M * 2 * s.rank_pad * 2, 256);
+    s.bytes = s.factor + round_up(M * (s.rank_pad / 32) * 4, 256);
+    return s;
+}
+
+}  // namespace
+}  // namespace gemm_relu_hip
+
+using namespace gemm_relu_hip;
+
+extern "C" {
+
+int64_t gemm_relu_grouped_workspace(int64_t M, int64_t N, int64_t K, int64_t groups, int dtype, int b_layout)
+{
+    const int rc = check_shape(M, N, K, groups, dtype, b_layout);
+    return rc;
+}
+
+int gemm_relu_grouped(const void* A, const void* B, const int32_t* ends, void* C, int64_t M, int64_t N,
+                      int64_t K, int64_t groups, int dtype, int b_layout, int relu, void* workspace,
+                      int64_t workspace_bytes, void* stream)
+{
+    const int64_t need = gemm_relu_grouped_workspace(M, N, K, groups, dtype, b_layout);
+    if (need < 0) return (int)need;
+    if (relu != 0 && relu != 1) return GEMM_RELU_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return GEMM_RELU_OK;
+    const Span in[] = {{A, 2 * M * K}, {B, 2 * groups * K * N}}, words[] = {{ends, 4 * groups}};
+    const Span out[] = {{C, 2 * M * N}, {workspace, need}};
+    int rc = check_spans(in, 2, words, 1, out, need > 0 ? 2 : 1);
+    if (rc == GEMM_RELU_OK) rc = check_workspace(workspace, workspace_bytes, need);
+    if (rc != GEMM_RELU_OK) return rc;
+    int cus = 0;
+    if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (K == 0) return zero_fill(C, M * N, s);
+    RowsArgs a{static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), static_cast<uint16_t*>(C), ends,
+               (int)M, (int)N, (int)K, (int)groups, relu, 0};
+    return launch_rows(a, AdapterArgs{}, dtype, b_layout, s);
+}
+
+int64_t gemm_relu_grouped_backward_workspace(int64_t M, int64_t N, int64_t K, int64_t groups, int dtype,
+                                             int b_layout, int relu)
+{
+    const int rc = check_shape(M, N, K, groups, dtype, b_layout);
+    if (rc != GEMM_RELU_OK) return rc;
+    if (relu != 0 && relu != 1) return GEMM_RELU_ERR_INVALID_ARG;
+    return GEMM_RELU_GROUPS_COUNTER_BYTES + (relu ? round_up(2 * M * N, 256) : 0);
+}
+
+int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, const void* B, const int32_t* ends,
+                               void* dA, void* dB, int64_t M, int64_t N, int64_t K, int64_t groups, int dtype,
+                               int b_layout, int relu, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    const int64_t need = gemm_relu_grouped_backward_workspace(M, N, K, groups, dtype, b_layout, relu);
+    if (need < 0) return (int)need;
+    const bool want_a = dA != nullptr, want_b = dB != nullptr;
+    if (!want_a && !want_b && K > 0) return GEMM_RELU_ERR_INVALID_ARG;
+    if (K == 0) return GEMM_RELU_OK;                 // both gradients are empty
+    const int64_t mn = M * N, mk = M * K, gkn = groups * K * N;
+    const Span in[] = {{dC, 2 * mn}, {relu ? C : nullptr, relu ? 2 * mn : 0}, {want_b ? A : nullptr, want_b ? 2 * mk : 0},
+                       {want_a ? B : nullptr, want_a ? 2 * gkn : 0}};
+    const Span words[] = {{ends, 4 * groups}};
+    const Span out[] = {{dA, want_a ? 2 * mk : 0}, {dB, want_b ? 2 * gkn : 0}, {workspace, need}};
+    int rc = check_spans(in, 4, words, 1, out, 2);
+    if (rc == GEMM_RELU_OK) rc = check_workspace(workspace, workspace_bytes, need);
+    if (rc == GEMM_RELU_OK) rc = check_spans(in, 4, words, 1, out, 3);
+    if (rc != GEMM_RELU_OK) return rc;
+    int cus = 0;
+    if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (mn == 0) {                                   // empty sums
+        if (want_a) rc = zero_fill(dA, mk, s);
+        if (want_b && rc == GEMM_RELU_OK) rc = zero_fill(dB, gkn, s);
+        return rc;
+    }
+    const uint16_t* d = static_cast<const uint16_t*>(dC);
+    if (relu) {
+        uint16_t* masked = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + GEMM_RELU_GROUPS_COUNTER_BYTES);
+        MaskArgs m{d, static_cast<const uint16_t*>(C), masked, mn, aligned(dC, 16) && aligned(C, 16)};
+        void* args[] = {&m};
+        rc = enqueue(kernels(dtype).mask, std::min<int64_t>(ceil_div(mn, 2048), 4096), 1, 256, args, s);
+        d = masked;
+    }
+    if (want_a && rc == GEMM_RELU_OK) {
+        // D (M, N) times B^T: B as stored (K, N) is the transposed weight of this product
+        RowsArgs a{d, static_cast<const uint16_t*>(B), static_cast<uint16_t*>(dA), ends,
+                   (int)M, (int)K, (int)N, (int)groups, 0, 0};
+        rc = launch_rows(a, AdapterArgs{}, dtype, b_layout == GEMM_RELU_B_KN ? GEMM_RELU_B_NK : GEMM_RELU_B_KN, s);
+    }
+    if (want_b && rc == GEMM_RELU_OK && gkn > 0) {
+        const uint16_t* x = static_cast<const uint16_t*>(A);
+        const bool kn = b_layout == GEMM_RELU_B_KN;
+        WeightArgs a{kn ? x : d, kn ? d : x, static_cast<uint16_t*>(dB), ends,
+                     (int)M, (int)(kn ? K : N), (int)(kn ? N : K), (int)groups, 0};
+        rc = launch_weights(a, dtype, s);
+    }
+    return rc;
+}
+
+int64_t gemm_relu_adapters_workspace(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t adapters,
+                                     int64_t segments, int dtype, int b_layout)
+{
+    const int rc = check_shape(M, N, K, segments, dtype, b_layout);
+    if (rc != GEMM_RELU_OK) return rc;
+    if (rank < 1 || adapters < 1) return GEMM_RELU_ERR_INVALID_ARG;
+    if (rank > kMaxRank || adapters > kMaxGroups) return GEMM_RELU_ERR_TOO_LARGE;
+    return adapter_space(M, rank).bytes;
+}
+
+int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* V, const float* scales,
+                       const int32_t* ends, const int32_t* ids, void* C, int64_t M, int64_t N, int64_t K,
+                       int64_t rank, int64_t adapters, int64_t segments, int dtype, int b_layout, int relu,
+                       void* workspace, int64_t workspace_bytes, void* stream)
+{
+    const int64_t need = gemm_relu_adapters_workspace(M, N, K, rank, adapters, segments, dtype, b_layout);
+    if (need < 0) return (int)need;
+    if (relu != 0 && relu != 1) return GEMM_RELU_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return GEMM_RELU_OK;
+    const Span in[] = {{X, 2 * M * K}, {W, 2 * K * N}, {U, 2 * adapters * K * rank}, {V, 2 * adapters * rank * N}};
+    const Span words[] = {{ends, 4 * segments}, {ids, 4 * segments}, {scales, 4 * adapters}};
+    const Span out[] = {{C, 2 * M * N}, {workspace, need}};
+    int rc = check_spans(in, 4, words, 3, out, 1);
+    if (rc == GEMM_RELU_OK) rc = check_workspace(workspace, workspace_bytes, need);
+    if (rc == GEMM_RELU_OK) rc = check_spans(in, 4, words, 3, out, 2);
+    if (rc != GEMM_RELU_OK) return rc;
+    int cus = 0;
+    if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (K == 0) return zero_fill(C, M * N, s);
+    const AdapterSpace space = adapter_space(M, rank);
+    uint16_t* t = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + space.t);
+    float* factor = reinterpret_cast<float*>(static_cast<char*>(workspace) + space.factor);
+    ShrinkArgs sh{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(U), scales, ends, ids, t, factor,
+                  (int)M, (int)K, (int)segments, (int)adapters, (int)rank, (int)space.rank_pad};
+    const int w = b_layout == GEMM_RELU_B_NK ? load_width({{X, K}, {U, K}}) : load_width({{X, K}});
+    void* args[] = {&sh};
+    rc = enqueue(kernels(dtype).shrink[b_layout][w], most_row_tiles(M, segments, kShrinkRows),
+                 (int)(space.rank_pad / kShrinkCols), kShrinkThreads, args, s);
+    if (rc != GEMM_RELU_OK) return rc;
+    RowsArgs a{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(W), static_cast<uint16_t*>(C), nullptr,
+               (int)M, (int)N, (int)K, 1, relu, 0};
+    AdapterArgs ad{static_cast<const uint16_t*>(V), t, factor, ends, ids, (int)segments, (int)adapters, (int)rank,
+                   (int)space.rank_pad, rank % 8 == 0 && aligned(V, 16)};
+    return launch_rows(a, ad, dtype, b_layout, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,524 @@
+// gfx950 kernels of the products whose rows choose their weights
+// (gemm_relu_groups.h): products grouped by expert, their gradients, and
+// low-rank adapters beside a shared projection.
+//
+// The groups' ends are in device memory and the host never learns them.  A
+// kernel finds its part of the work itself: lane l of a wave takes group l, a
+// scan over the wave turns the groups' row counts into running tile counts,
+// and a ballot finds the group that holds a given tile (find_row_tile).
+//
+// All kernels compute blocks of C^T with 16x16x32 MFMAs (the MFMA "A" operand
+// is the weights' side), so lane l of a block holds 4 consecutive columns of
+// row l % 16: see store_cols.
+#pragma once
+
+#include "gemm_relu_kernels.hpp"
+#include "groups_table.hpp"
+
+namespace gemm_relu_hip {
+
+// ---------------------------------------------------------------- row table
+
+// Rows begin .. end - 1 of the matrices, a tile of group `group`; group ==
+// groups: rows of no group.  group < 0: there is no such tile.
+struct RowTile {
+    int group, begin, end;
+};
+
+// Inclusive scans over the wave's 64 lanes.
+__device__ __forceinline__ int wave_scan_max(int v, int lane)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(v, d);
+        if (lane >= d) v = max(v, o);
+    }
+    return v;
+}
+
+__device__ __forceinline__ int wave_scan_sum(int v, int lane)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// The rows of lane l's group g0 + l, for 64 groups from g0 on; `start` is where
+// group g0 begins.  Group `groups` is made of the rows past the last end, later
+// ones are empty.  The running maximum keeps groups apart whatever `ends` holds.
+struct GroupRows {
+    int begin, end;
+};
+__device__ __forceinline__ GroupRows load_group_rows(const int* __restrict__ ends, int groups, int M, int g0,
+                                                     int start, int lane)
+{
+    const int g = g0 + lane;
+    int e = M;
+    if (g < groups) e = ends ? min(max(ends[g], 0), M) : M;
+    e = max(wave_scan_max(e, lane), start);
+    const int b = __shfl_up(e, 1);
+    return GroupRows{lane == 0 ? start : b, e};
+}
+
+// Tile number `unit` when every group's rows are cut into tiles of `rows` rows.
+__device__ inline RowTile find_row_tile(const int* __restrict__ ends, int groups, int M, int rows, int unit, int lane)
+{
+    int tiles_before = 0, start = 0;
+    for (int g0 = 0; g0 <= groups; g0 += 64) {
+        const GroupRows r = load_group_rows(ends, groups, M, g0, start, lane);
+        const int tiles = (r.end - r.begin + rows - 1) / rows;
+        const int incl = tiles_before + wave_scan_sum(tiles, lane);
+        const uint64_t mask = __ballot(unit < incl);
+        if (mask) {
+            const int l = __builtin_ctzll(mask);
+            const int begin = __builtin_amdgcn_readlane(r.begin, l) +
+                              (unit - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(tiles, l))) * rows;
+            return RowTile{g0 + l, begin, min(begin + rows, __builtin_amdgcn_readlane(r.end, l))};
+        }
+        tiles_before = __builtin_amdgcn_readlane(incl, 63);
+        start = __builtin_amdgcn_readlane(r.end, 63);
+    }
+    return RowTile{-1, 0, 0};
+}
+
+// ---------------------------------------------------------------- epilogue
+
+// An fp32 sum in C's dtype (round to nearest even), after ReLU if asked for.
+template <int DT>
+__device__ __forceinline__ uint16_t act_cast(float x, bool relu)
+{
+    if (relu) x = x > 0.0f ? x : 0.0f;
+    if constexpr (DT == kF16)
+        return __builtin_bit_cast(uint16_t, (_Float16)x);
+    else
+        return __builtin_bit_cast(uint16_t, (__bf16)x);
+}
+
+template <int DT>
+__device__ __forceinline__ float to_float(uint16_t h)
+{
+    if constexpr (DT == kF16)
+        return (float)__builtin_bit_cast(_Float16, h);
+    else
+        return __builtin_bit_cast(float, (uint32_t)h << 16);
+}
+
+// Store one 16x16 block of C^T: lane l holds row m = (block's first row) + l % 16
+// and columns n .. n + 3.  Rows from m_end and columns from n_end on are dropped.
+// c_vec > 0: row lengths and C allow 8-byte stores.
+template <int DT>
+__device__ __forceinline__ void store_cols(uint16_t* __restrict__ C, floatx4 acc, int m, int n, int m_end, int n_end,
+                                           bool relu, int c_vec)
+{
+    if (m >= m_end) return;
+    uint16_t* p = C + (size_t)m * (size_t)n_end + n;
+    const uint16_t h0 = act_cast<DT>(acc[0], relu), h1 = act_cast<DT>(acc[1], relu);
+    const uint16_t h2 = act_cast<DT>(acc[2], relu), h3 = act_cast<DT>(acc[3], relu);
+    if (c_vec > 0 && n + 3 < n_end) {
+        *reinterpret_cast<u32x2*>(p) = u32x2{(uint32_t)h0 | ((uint32_t)h1 << 16), (uint32_t)h2 | ((uint32_t)h3 << 16)};
+    } else {
+        if (n + 0 < n_end) p[0] = h0;
+        if (n + 1 < n_end) p[1] = h1;
+        if (n + 2 < n_end) p[2] = h2;
+        if (n + 3 < n_end) p[3] = h3;
+    }
+}
+
+// ---------------------------------------------------------------- adapters
+
+// 8 consecutive k (from k on, zero past `rank`) of column n of V_i, as an MFMA operand.
+template <bool B_NK>
+__device__ __forceinline__ u32x4 load_v(const AdapterArgs& ad, int id, int n, int N, int k)
+{
+    u32x4 r = {0u, 0u, 0u, 0u};
+    if (n >= N) return r;
+    if constexpr (B_NK) {
+        const uint16_t* p = ad.v + ((size_t)id * (size_t)N + (size_t)n) * (size_t)ad.rank + k;
+        if (ad.v_vec) {                       // rank % 8 == 0: a chunk is wholly in or out
+            if (k < ad.rank) r = *reinterpret_cast<const u32x4*>(p);
+            return r;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (k + e < ad.rank) r[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+    } else {
+        const uint16_t* p = ad.v + ((size_t)id * (size_t)ad.rank + (size_t)k) * (size_t)N + n;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (k + e < ad.rank) r[e / 2] |= (uint32_t)p[(size_t)e * (size_t)N] << (16 * (e & 1));
+    }
+    return r;
+}
+
+// Add the low-rank terms of rows m_base .. (those below m_end) to FN x FM blocks
+// of C^T, block (i, j): rows m_base + 16j .. +15, columns n_base + 16i .. +15.
+//  The rows of a 16-row block may belong to several segments.  For each of
+// them the block's product with that segment's adapter is summed in registers
+// of its own, and a lane takes it over only if its row is in the segment: rows
+// never see another request's weights, not even as 0 * infinity.
+template <int DT, bool B_NK, int FN, int FM>
+__device__ inline void add_adapters(floatx4 (&acc)[FN][FM], const AdapterArgs& ad, int m_base, int m_end, int M,
+                                    int n_base, int N, int lane)
+{
+    const int r16 = lane & 15, kg = lane >> 4;
+    int start = 0;
+    for (int s0 = 0; s0 < ad.segments && start < m_end; s0 += 64) {
+        const GroupRows seg = load_group_rows(ad.ends, ad.segments, M, s0, start, lane);
+        const int id = s0 + lane < ad.segments ? ad.ids[s0 + lane] : -1;
+        const bool used = id >= 0 && id < ad.adapters;
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            const int mb = m_base + 16 * j, me = min(mb + 16, m_end);
+            uint64_t todo = __ballot(used && seg.begin < me && seg.end > mb && seg.begin < seg.end);
+            while (todo) {
+                const int l = __builtin_ctzll(todo);
+                todo &= todo - 1;
+                const int lo = __builtin_amdgcn_readlane(seg.begin, l), hi = __builtin_amdgcn_readlane(seg.end, l);
+                const int i_ad = __builtin_amdgcn_readlane(id, l);
+                const int m = mb + r16;
+                const bool in = m >= lo && m < min(hi, m_end);
+                const uint16_t* trow = ad.t + (size_t)m * (size_t)(2 * ad.rank_pad) + 8 * kg;
+                for (int k = 0; k < ad.rank_pad; k += 32) {
+                    u32x4 t_hi = {0u, 0u, 0u, 0u}, t_lo = t_hi;
+                    float f = 0.0f;
+                    if (in) {
+                        t_hi = *reinterpret_cast<const u32x4*>(trow + k);
+                        t_lo = *reinterpret_cast<const u32x4*>(trow + ad.rank_pad + k);
+                        f = ad.factor[(size_t)m * (size_t)(ad.rank_pad / 32) + k / 32];
+                    }
+#pragma unroll
+                    for (int i = 0; i < FN; ++i) {
+                        const u32x4 v = load_v<B_NK>(ad, i_ad, n_base + 16 * i + r16, N, k + 8 * kg);
+                        floatx4 p = mfma_16x16x32<DT>(v, t_hi, floatx4{0.0f, 0.0f, 0.0f, 0.0f});
+                        p = mfma_16x16x32<DT>(v, t_lo, p);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[i][j][e] = in ? acc[i][j][e] + f * p[e] : acc[i][j][e];
+                    }
+                }
+            }
+        }
+        start = __builtin_amdgcn_readlane(seg.end, 63);
+    }
+}
+
+// The intermediates of the low-rank terms.  For row m of a segment with adapter
+// i, z = scales[i] * (X[m] @ U_i) is summed in fp32, and each 32 of its entries
+// (rank_pad = rank rounded up to 32, zeros past rank) are stored as
+//     z = factor[m][block] * (t[m][hi][..] + t[m][lo][..]),
+// factor a power of two of the block's largest |z|, hi the nearest 16-bit value
+// to z / factor (at most 1 in size) and lo that to what is left.
+//  One workgroup per 16 rows of a segment and 32 columns of rank: its 8 waves
+// take the K-steps (32 k) in turn and their sums are added in wave order in LDS.
+template <int DT, bool U_NK, int VEC>
+__global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs a)
+{
+    constexpr int WAVES = kShrinkThreads / 64;
+    __shared__ float part[WAVES][kShrinkCols][kShrinkRows + 1];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const RowTile tile = find_row_tile(a.ends, a.segments, a.m, kShrinkRows, blockIdx.x, lane);
+    if (tile.group < 0 || tile.group >= a.segments) return;
+    const int id = a.ids[tile.group];
+    if (id < 0 || id >= a.adapters) return;
+    const int rows = tile.end - tile.begin, r_base = blockIdx.y * kShrinkCols;
+    const int r16 = lane & 15, kg = lane >> 4;
+    const size_t k_len = (size_t)a.k, rank = (size_t)a.rank;
+
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)tile.begin * k_len, (uint32_t)rows * (uint32_t)a.k * 2u);
+    const uint16_t* u = a.u + (size_t)id * k_len * rank;
+    // U stored (rank, K): this workgroup's rows r_base .. of U^T
+    const int u_rows = min(kShrinkCols, a.rank - r_base);
+    const __amdgpu_buffer_rsrc_t ru =
+        make_rsrc(u + (U_NK ? (size_t)r_base * k_len : 0), U_NK ? (uint32_t)u_rows * (uint32_t)a.k * 2u : 0u);
+    floatx4 acc[2] = {floatx4{0}, floatx4{0}};
+    const int steps = (a.k + 31) / 32;
+    for (int s = wave; s < steps; s += WAVES) {
+        const int k = 32 * s + 8 * kg;
+        const u32x4 x = load_chunk<VEC>(rx, ((uint32_t)r16 * (uint32_t)a.k + (uint32_t)k) * 2u,
+                                        [&](int p) { return k + p * VEC < a.k; });
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            u32x4 w = {0u, 0u, 0u, 0u};
+            const int r = 16 * i + r16;
+            if constexpr (U_NK) {
+                w = load_chunk<VEC>(ru, ((uint32_t)r * (uint32_t)a.k + (uint32_t)k) * 2u,
+                                    [&](int p) { return k + p * VEC < a.k; });
+            } else if (r_base + r < a.rank) {
+                const uint16_t* p = u + (size_t)k * rank + r_base + r;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (k + e < a.k) w[e / 2] |= (uint32_t)p[(size_t)e * rank] << (16 * (e & 1));
+            }
+            acc[i] = mfma_16x16x32<DT>(w, x, acc[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[wave][16 * i + 4 * kg + e][r16] = acc[i][e];
+    __syncthreads();
+    // 512 threads: 16 rows x 32 columns; a row's 32 columns are one half of a wave
+    const int row = threadIdx.x >> 5, col = threadIdx.x & 31;
+    float z = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) z += part[w][col][row];
+    // columns past rank are zero, whatever X holds (0 * infinity is not)
+    z = r_base + col < a.rank ? z * a.scales[id] : 0.0f;
+    float top = fabsf(z);
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+    // 2^e > top: the scaled values are below 1.  Zeros (and, with nothing to
+    // scale by, infinities) keep factor 1; e stays where 2^-e is a normal number.
+    int e = 0;
+    if (top > 0.0f && top < __builtin_inff()) {
+        (void)frexpf(top, &e);
+        e = min(max(e, -125), 125);
+    }
+    const float scaled = ldexpf(z, -e);
+    const uint16_t hi = act_cast<DT>(scaled, false);
+    const float rest = scaled - to_float<DT>(hi);
+    if (row < rows) {
+        const size_t m = (size_t)(tile.begin + row);
+        uint16_t* t = a.t + m * (size_t)(2 * a.rank_pad) + r_base + col;
+        t[0] = hi;
+        // an infinite hi leaves inf - inf: such an entry has no second part
+        t[a.rank_pad] = fabsf(scaled) < __builtin_inff() ? act_cast<DT>(rest, false) : (uint16_t)0;
+        if (col == 0) a.factor[m * (size_t)(a.rank_pad / 32) + blockIdx.y] = ldexpf(1.0f, e);
+    }
+}
+
+// ---------------------------------------------------------------- register-staged kernel
+
+// One operand of the register-staged kernels: a 128-row tile of a matrix whose
+// product index k runs along its rows (K_ROWS = false: rows of the tile are rows
+// of the matrix, k-contiguous) or down its columns (K_ROWS = true: rows of the
+// matrix are k; transposed on the way into LDS).  Either way LDS holds 128 rows
+// of 64 consecutive k, swizzled by lds_off.
+template <bool K_ROWS, int VEC>
+struct StagedOperand {
+    static constexpr int ROWS = 128, BK = 64, THREADS = 256;
+    const uint16_t* base;   // K_ROWS: the matrix; else the tile's first row
+    uint32_t ld;            // row length of the matrix
+    int first, limit;       // K_ROWS: the tile's first column and their number in all; else 0 and its valid rows
+    u32x4 r[4];
+
+    __device__ __forceinline__ void load(int k0, int k_end, int tid)
+    {
+        if constexpr (K_ROWS) {
+            const int col = first + (tid % 16) * 8, kb = (tid / 16) * 4;
+            const int valid = max(0, min(BK, k_end - k0));
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(base + (size_t)k0 * ld, (uint32_t)valid * ld * 2u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                r[i] = load_chunk<VEC>(rs, ((uint32_t)(kb + i) * ld + (uint32_t)col) * 2u,
+                                       [&](int p) { return kb + i < valid && col + p * VEC < limit; });
+        } else {
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, (uint32_t)limit * ld * 2u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int q = tid + i * THREADS, row = q / 8, k = k0 + (q % 8) * 8;
+                r[i] = load_chunk<VEC>(rs, ((uint32_t)row * ld + (uint32_t)k) * 2u,
+                                       [&](int p) { return k + p * VEC < k_end; });
+            }
+        }
+    }
+
+    __device__ __forceinline__ void store(uint8_t* lds, int tid) const
+    {
+        if constexpr (K_ROWS) {
+            const int nb = tid % 16, kb = tid / 16;      // 8 columns, 4 k
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const uint32_t sel = (n & 1) ? 0x07060302u : 0x05040100u;
+                u32x2 v;
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    v[p] = __builtin_amdgcn_perm(r[2 * p + 1][n >> 1], r[2 * p][n >> 1], sel);
+                *reinterpret_cast<u32x2*>(lds + lds_off(nb * 8 + n, kb >> 1) + (kb & 1) * 8) = v;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int q = tid + i * THREADS;
+                *reinterpret_cast<u32x4*>(lds + lds_off(q / 8, q % 8)) = r[i];
+            }
+        }
+    }
+};
+
+// The 128 x 128 product of two staged operands over k_begin .. k_end - 1, by 4
+// waves of 64 x 64: two LDS stages, the next K-step's loads in flight (in
+// registers) while the current one's MFMAs run.
+template <int DT, class OpM, class OpN>
+__device__ __forceinline__ void staged_product(floatx4 (&acc)[4][4], OpM& rows, OpN& cols, int k_begin, int k_end,
+                                               uint8_t* smem)
+{
+    constexpr int TILE = 128 * 128;    // bytes of one operand's stage
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int wm = wave >> 1, wn = wave & 1;
+    const int steps = (k_end - k_begin + 63) / 64;
+    if (steps <= 0) return;
+    rows.load(k_begin, k_end, tid);
+    cols.load(k_begin, k_end, tid);
+    rows.store(smem, tid);
+    cols.store(smem + TILE, tid);
+    __syncthreads();
+    for (int s = 0; s < steps; ++s) {
+        const uint8_t* stage = smem + (s & 1) * 2 * TILE;
+        if (s + 1 < steps) {
+            rows.load(k_begin + 64 * (s + 1), k_end, tid);
+            cols.load(k_begin + 64 * (s + 1), k_end, tid);
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            const int chunk = ks * 4 + kgroup16(lane >> 4);
+            u32x4 fn[4], fm[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                fn[i] = *reinterpret_cast<const u32x4*>(stage + TILE + lds_off(wn * 64 + i * 16 + (lane & 15), chunk));
+                fm[i] = *reinterpret_cast<const u32x4*>(stage + lds_off(wm * 64 + i * 16 + (lane & 15), chunk));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = mfma_16x16x32<DT>(fn[i], fm[j], acc[i][j]);
+        }
+        if (s + 1 < steps) {
+            uint8_t* next = smem + ((s + 1) & 1) * 2 * TILE;
+            rows.store(next, tid);
+            cols.store(next + TILE, tid);
+        }
+        __syncthreads();
+    }
+}
+
+// C = act(rows of A @ their group's B [+ their adapters' terms]), 128 x 128
+// tiles, any row length and alignment (VEC: elements per load, dividing the row
+// lengths).  Workgroup b: column tile b % tiles_n of row tile b / tiles_n.
+template <int DT, bool B_NK, int VEC>
+__global__ __launch_bounds__(256) void rows_tiled(RowsArgs a, AdapterArgs ad)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t smem[4 * 128 * 128];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tiles_n = (a.n + 127) / 128;
+    const RowTile tile = find_row_tile(a.ends, a.groups, a.m, 128, blockIdx.x / tiles_n, lane);
+    if (tile.group < 0) return;
+    const int n0 = (blockIdx.x % tiles_n) * 128;
+    const size_t k_len = (size_t)a.k, n_len = (size_t)a.n;
+
+    floatx4 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int m_base = tile.begin + (wave >> 1) * 64, n_base = n0 + (wave & 1) * 64;
+    if (tile.group < a.groups) {
+        const uint16_t* b = a.b + (size_t)tile.group * k_len * n_len;
+        StagedOperand<false, VEC> rows{a.a + (size_t)tile.begin * k_len, (uint32_t)a.k, 0, tile.end - tile.begin, {}};
+        StagedOperand<!B_NK, VEC> cols{B_NK ? b + (size_t)n0 * k_len : b, (uint32_t)(B_NK ? a.k : a.n),
+                                       B_NK ? 0 : n0, B_NK ? min(128, a.n - n0) : a.n, {}};
+        staged_product<DT>(acc, rows, cols, 0, a.k, smem);
+        if (ad.v) add_adapters<DT, B_NK>(acc, ad, m_base, tile.end, a.m, n_base, a.n, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            store_cols<DT>(a.c, acc[i][j], m_base + 16 * j + (lane & 15), n_base + 16 * i + 4 * (lane >> 4), tile.end,
+                           a.n, a.relu != 0, a.c_vec);
+}
+
+// out[g] = p^T q over group g's rows, 128 x 128 tiles, any row length and
+// alignment.  Workgroup b: tile b % tiles of group b / tiles.
+template <int DT, int VEC>
+__global__ __launch_bounds__(256) void weight_tiled(WeightArgs a)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t smem[4 * 128 * 128];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tiles_j = (a.j + 127) / 128, tiles = (a.i + 127) / 128 * tiles_j;
+    const int g = blockIdx.x / tiles, t = blockIdx.x % tiles;
+    const int i0 = t / tiles_j * 128, j0 = t % tiles_j * 128;
+    // The group's rows: the running maximum of the ends before it and with it.
+    int begin = 0, end = 0;
+    for (int g0 = 0, start = 0; g0 <= g; g0 += 64) {
+        const GroupRows r = load_group_rows(a.ends, a.groups, a.m, g0, start, lane);
+        begin = __builtin_amdgcn_readlane(r.begin, min(g - g0, 63));
+        end = __builtin_amdgcn_readlane(r.end, min(g - g0, 63));
+        start = end;
+    }
+    floatx4 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    StagedOperand<true, VEC> rows{a.p, (uint32_t)a.i, i0, a.i, {}};
+    StagedOperand<true, VEC> cols{a.q, (uint32_t)a.j, j0, a.j, {}};
+    staged_product<DT>(acc, rows, cols, begin, end, smem);
+    const int m_base = i0 + (wave >> 1) * 64, n_base = j0 + (wave & 1) * 64;
+    uint16_t* out = a.out + (size_t)g * (size_t)a.i * (size_t)a.j;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            store_cols<DT>(out, acc[i][j], m_base + 16 * j + (lane & 15), n_base + 16 * i + 4 * (lane >> 4), a.i, a.j,
+                           false, a.c_vec);
+}
+
+// ---------------------------------------------------------------- ReLU's gradient
+
+// d = dc where c > 0, else +0.0 (c's sign decides: 16-bit floats above zero are
+// the patterns 0x0001 .. infinity; NaN counts as not above zero).
+template <int DT>
+__device__ __forceinline__ uint16_t mask_one(uint16_t dc, uint16_t c)
+{
+    constexpr uint16_t inf = DT == kF16 ? 0x7c00 : 0x7f80;
+    return (uint16_t)(c - 1) < inf ? dc : (uint16_t)0;
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void relu_mask(MaskArgs a)
+{
+    const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+    const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const int64_t chunks = a.vec ? a.count / 8 : 0;
+    for (int64_t q = first; q < chunks; q += stride) {
+        const u32x4 g = reinterpret_cast<const u32x4*>(a.dc)[q], c = reinterpret_cast<const u32x4*>(a.c)[q];
+        u32x4 r;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            r[w] = (uint32_t)mask_one<DT>((uint16_t)g[w], (uint16_t)c[w]) |
+                   ((uint32_t)mask_one<DT>((uint16_t)(g[w] >> 16), (uint16_t)(c[w] >> 16)) << 16);
+        reinterpret_cast<u32x4*>(a.d)[q] = r;
+    }
+    for (int64_t q = chunks * 8 + first; q < a.count; q += stride) a.d[q] = mask_one<DT>(a.dc[q], a.c[q]);
+}
+
+// ---------------------------------------------------------------- instances
+
+template <int DT, int W>
+void fill_group_width(GroupKernels& t)
+{
+    constexpr int VEC = kLoadWidths[W];
+    t.rows_tiled[0][W] = (const void*)&rows_tiled<DT, false, VEC>;
+    t.rows_tiled[1][W] = (const void*)&rows_tiled<DT, true, VEC>;
+    t.weight_tiled[W] = (const void*)&weight_tiled<DT, VEC>;
+    t.shrink[0][W] = (const void*)&adapter_shrink<DT, false, VEC>;
+    t.shrink[1][W] = (const void*)&adapter_shrink<DT, true, VEC>;
+}
+
+template <int DT>
+GroupKernels make_group_table()
+{
+    GroupKernels t{};
+    fill_group_width<DT, 0>(t);
+    fill_group_width<DT, 1>(t);
+    fill_group_width<DT, 2>(t);
+    fill_group_width<DT, 3>(t);
+    t.mask = (const void*)&relu_mask<DT>;
+    return t;
+}
+
+}  // namespace gemm_relu_hip

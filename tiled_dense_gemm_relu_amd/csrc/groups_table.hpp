@@ -1,0 +1,77 @@
+// Kernel arguments and the host-side table of kernel instances of the products
+// whose rows choose their weights (gemm_relu_groups.h), filled by one
+// translation unit per dtype and read by groups_api.hip.
+#pragma once
+
+#include <stdint.h>
+
+namespace gemm_relu_hip {
+
+// A product over groups of rows.  ends == nullptr: all rows are group 0.
+struct RowsArgs {
+    const uint16_t* a;     // (M, K)
+    const uint16_t* b;     // (groups, K, N) or (groups, N, K)
+    uint16_t* c;           // (M, N)
+    const int* ends;
+    int m, n, k, groups;
+    int relu;
+    int c_vec;             // rows of C allow 2: 16-byte, 1: 8-byte, 0: 2-byte stores
+};
+
+// The low-rank term of each row (v == nullptr: none).  Row m's intermediate is
+// t[m][hi | lo][rank_pad] times factor[m][rank_pad / 32], see adapter_shrink.
+struct AdapterArgs {
+    const uint16_t* v;     // (adapters, rank, N) or (adapters, N, rank)
+    const uint16_t* t;
+    const float* factor;
+    const int* ends;
+    const int* ids;
+    int segments, adapters, rank, rank_pad;
+    int v_vec;             // V's rows allow 16-byte loads
+};
+
+struct ShrinkArgs {
+    const uint16_t* x;     // (M, K)
+    const uint16_t* u;     // (adapters, K, rank) or (adapters, rank, K)
+    const float* scales;
+    const int* ends;
+    const int* ids;
+    uint16_t* t;
+    float* factor;
+    int m, k, segments, adapters, rank, rank_pad;
+};
+
+// dB[g] = sum of p[m]^T q[m] over group g's rows: p (M, I), q (M, J), out (groups, I, J).
+struct WeightArgs {
+    const uint16_t* p;
+    const uint16_t* q;
+    uint16_t* out;
+    const int* ends;
+    int m, i, j, groups;
+    int c_vec;
+};
+
+struct MaskArgs {
+    const uint16_t* dc;
+    const uint16_t* c;
+    uint16_t* d;
+    int64_t count;
+    int vec;               // 16-byte aligned pointers
+};
+
+// Load widths with an instance of the register-staged kernels, widest first.
+constexpr int kNumLoadWidths = 4;
+constexpr int kLoadWidths[kNumLoadWidths] = {8, 4, 2, 1};
+constexpr int kShrinkRows = 16, kShrinkCols = 32, kShrinkThreads = 512;
+
+struct GroupKernels {
+    const void* rows_tiled[2][kNumLoadWidths];    // [B layout][load width]
+    const void* weight_tiled[kNumLoadWidths];
+    const void* mask;
+    const void* shrink[2][kNumLoadWidths];        // [U layout][load width of X and of U^T]
+};
+
+const GroupKernels& group_kernels_f16();
+const GroupKernels& group_kernels_bf16();
+
+}  // namespace gemm_relu_hip

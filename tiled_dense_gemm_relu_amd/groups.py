@@ -1,0 +1,280 @@
+"""Products whose rows choose their weights (the C ABI in include/gemm_relu_groups.h).
+
+``gemm_relu_grouped``: rows grouped by expert, with ``gemm_relu_grouped_backward`` for its gradients;
+``gemm_relu_adapters``: a projection shared by all rows with the low-rank adapters of many requests.
+As in binding.py this is argument marshalling only, with no fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+import threading
+
+from . import binding
+from .binding import B_KN, B_NK, _check, _dtype_code, _stream_handle
+
+COUNTER_BYTES = 65536      # GEMM_RELU_GROUPS_COUNTER_BYTES
+
+_lock = threading.Lock()
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        lib = binding.load_library()
+        with _lock:
+            vp, i64, ci = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+            lib.gemm_relu_grouped.argtypes = [vp] * 4 + [i64] * 4 + [ci] * 3 + [vp, i64, vp]
+            lib.gemm_relu_grouped.restype = ci
+            lib.gemm_relu_grouped_workspace.argtypes = [i64] * 4 + [ci] * 2
+            lib.gemm_relu_grouped_workspace.restype = i64
+            lib.gemm_relu_grouped_backward.argtypes = [vp] * 7 + [i64] * 4 + [ci] * 3 + [vp, i64, vp]
+            lib.gemm_relu_grouped_backward.restype = ci
+            lib.gemm_relu_grouped_backward_workspace.argtypes = [i64] * 4 + [ci] * 3
+            lib.gemm_relu_grouped_backward_workspace.restype = i64
+            lib.gemm_relu_adapters.argtypes = [vp] * 8 + [i64] * 6 + [ci] * 3 + [vp, i64, vp]
+            lib.gemm_relu_adapters.restype = ci
+            lib.gemm_relu_adapters_workspace.argtypes = [i64] * 6 + [ci] * 2
+            lib.gemm_relu_adapters_workspace.restype = i64
+            _lib = lib
+    return _lib
+
+
+@functools.lru_cache(maxsize=4096)
+def _bytes(function: str, *args) -> int:
+    """What a *_workspace function returns (pure host arithmetic on the sizes)."""
+    n = getattr(_library(), function)(*args)
+    if n < 0:
+        _check(int(n))
+    return n
+
+
+def grouped_workspace_bytes(M: int, N: int, K: int, groups: int, dtype: int, b_layout: int = B_KN) -> int:
+    """Workspace of gemm_relu_grouped for these sizes (host only)."""
+    return _bytes("gemm_relu_grouped_workspace", M, N, K, groups, dtype, b_layout)
+
+
+def grouped_backward_workspace_bytes(M: int, N: int, K: int, groups: int, dtype: int, b_layout: int = B_KN,
+                                     relu: bool = True) -> int:
+    """Workspace of gemm_relu_grouped_backward for these sizes (host only)."""
+    return _bytes("gemm_relu_grouped_backward_workspace", M, N, K, groups, dtype, b_layout, int(relu))
+
+
+def adapters_workspace_bytes(M: int, N: int, K: int, rank: int, adapters: int, segments: int, dtype: int,
+                             b_layout: int = B_KN) -> int:
+    """Workspace of gemm_relu_adapters for these sizes (host only)."""
+    return _bytes("gemm_relu_adapters_workspace", M, N, K, rank, adapters, segments, dtype, b_layout)
+
+
+def _check_tensor(name, t, dim, dev, dtype):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"gemm_relu: {name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"gemm_relu: {name} must be a GPU tensor, got {t.device}")
+    if t.dim() != dim:
+        raise ValueError(f"gemm_relu: {name} must be {dim}-D, got shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"gemm_relu: {name} must be contiguous (row-major)")
+    if t.dtype != dtype:
+        raise TypeError(f"gemm_relu: {name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"gemm_relu: {name} must be on the same device as the other tensors")
+
+
+def _check_shape(name, t, shape):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"gemm_relu: {name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _first(name, t):
+    """Dtype and device that the other tensors have to share."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"gemm_relu: {name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"gemm_relu: {name} must be a GPU tensor, got {t.device}")
+    return _dtype_code(t), t.get_device()
+
+
+def _check_layout(b_layout):
+    if b_layout not in (B_KN, B_NK):
+        raise ValueError(f"gemm_relu: b_layout must be B_KN or B_NK, got {b_layout}")
+
+
+def _new(shape, like, stream):
+    """An output for work on ``stream``: allocated for that stream, so that its memory is not one
+    that still belongs to other work there."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+
+
+def _workspace(given, need, like, handle, stream):
+    """(pointer, bytes) of the workspace: ``given``, or the cached one of this stream, which
+    gemm_relu_splitk's calls use too.  A capture takes memory of its own graph, so that replays stay
+    valid when the cached buffer is replaced by a larger one."""
+    import torch
+    if need == 0:
+        return None, 0, None
+    if given is None:
+        if torch.cuda.is_current_stream_capturing():
+            given = torch.empty(need, dtype=torch.uint8, device=like.device)
+            given[:COUNTER_BYTES].zero_()
+        else:
+            given = binding._workspaces.get((like.device, handle))
+            if given is None or given.numel() < need:
+                s = stream if stream is not None else torch.cuda.current_stream(like.device)
+                given = binding.splitk_workspace(like.device, s, need)
+        return given.data_ptr(), given.numel(), given
+    if not isinstance(given, torch.Tensor) or not given.is_cuda or not given.is_contiguous():
+        raise TypeError("gemm_relu: workspace must be a contiguous GPU tensor")
+    if given.get_device() != like.get_device():
+        raise ValueError("gemm_relu: workspace must be on the same device as the other tensors")
+    return given.data_ptr(), given.numel() * given.element_size(), given
+
+
+def _call(function, dev, *args):
+    """The library launches on the current device: make it the tensors' one."""
+    import torch
+    if torch.cuda.current_device() == dev:
+        rc = function(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = function(*args)
+    if rc != 0:
+        _check(rc)
+
+
+def gemm_relu_grouped(a, b, ends, out=None, b_layout: int = B_KN, relu: bool = True, workspace=None, stream=None):
+    """C[m] = ReLU(a[m] @ B[g]) for every row m of group g (``relu=False``: without the ReLU).
+
+    ``a`` (M, K), fp16 or bf16; ``b`` (groups, K, N), or (groups, N, K) with B_NK; ``ends`` (groups,)
+    int32 on the GPU, non-decreasing: group g holds rows ends[g-1] .. ends[g]-1 (a running sum of
+    row counts).  Rows past the last end get zeros.  ``out`` (M, N) is written if given.
+    ``workspace``: at least grouped_workspace_bytes(...) bytes whose first 65536 are zero, or None
+    for a cached one per stream.
+    """
+    import torch
+    code, dev = _first("a", a)
+    _check_layout(b_layout)
+    _check_tensor("a", a, 2, dev, a.dtype)
+    _check_tensor("b", b, 3, dev, a.dtype)
+    _check_tensor("ends", ends, 1, dev, torch.int32)
+    M, K = a.shape
+    groups, N = b.shape[0], b.shape[1 if b_layout == B_NK else 2]
+    if b.shape[2 if b_layout == B_NK else 1] != K:
+        raise ValueError(f"gemm_relu: inner dimensions differ: a {tuple(a.shape)}, b {tuple(b.shape)}")
+    if ends.shape[0] != groups:
+        raise ValueError(f"gemm_relu: ends must have one entry for each of {groups} groups, got {ends.shape[0]}")
+    if out is None:
+        out = _new((M, N), a, stream)
+    else:
+        _check_tensor("out", out, 2, dev, a.dtype)
+        _check_shape("out", out, (M, N))
+    handle = _stream_handle(stream, dev)
+    ws, ws_bytes, keep = _workspace(workspace, grouped_workspace_bytes(M, N, K, groups, code, b_layout), a, handle,
+                                    stream)
+    _call(_library().gemm_relu_grouped, dev, a.data_ptr(), b.data_ptr(), ends.data_ptr(), out.data_ptr(), M, N, K,
+          groups, code, b_layout, 1 if relu else 0, ws, ws_bytes, handle or None)
+    return out
+
+
+def gemm_relu_grouped_backward(dc, c, a, b, ends, b_layout: int = B_KN, relu: bool = True, da=None, db=None,
+                               need_da: bool = True, need_db: bool = True, workspace=None, stream=None):
+    """Gradients (da, db) of gemm_relu_grouped's C = ``c`` for its gradient ``dc``, both (M, N).
+
+    da has a's shape (zeros in rows of no group), db has b's (zeros for empty groups).
+    ``need_da=False`` / ``need_db=False`` leave one out (None is returned for it, and ``b`` / ``a``
+    may be None).  ``c`` is only read with ``relu=True`` and may be None without.
+    """
+    import torch
+    code, dev = _first("dc", dc)
+    _check_layout(b_layout)
+    _check_tensor("dc", dc, 2, dev, dc.dtype)
+    _check_tensor("ends", ends, 1, dev, torch.int32)
+    if not need_da and not need_db:
+        raise ValueError("gemm_relu: neither gradient is asked for")
+    M, N = dc.shape
+    groups = ends.shape[0]
+    if relu:
+        _check_tensor("c", c, 2, dev, dc.dtype)
+        _check_shape("c", c, (M, N))
+    if need_db:
+        _check_tensor("a", a, 2, dev, dc.dtype)
+        K = a.shape[1]
+        _check_shape("a", a, (M, K))
+    if need_da:
+        _check_tensor("b", b, 3, dev, dc.dtype)
+        if not need_db:
+            K = b.shape[2 if b_layout == B_NK else 1]
+        _check_shape("b", b, (groups, N, K) if b_layout == B_NK else (groups, K, N))
+        if da is None:
+            da = _new((M, K), dc, stream)
+        else:
+            _check_tensor("da", da, 2, dev, dc.dtype)
+            _check_shape("da", da, (M, K))
+    if need_db:
+        shape = (groups, N, K) if b_layout == B_NK else (groups, K, N)
+        if db is None:
+            db = _new(shape, dc, stream)
+        else:
+            _check_tensor("db", db, 3, dev, dc.dtype)
+            _check_shape("db", db, shape)
+    handle = _stream_handle(stream, dev)
+    ws, ws_bytes, keep = _workspace(workspace, grouped_backward_workspace_bytes(M, N, K, groups, code, b_layout, relu),
+                                    dc, handle, stream)
+    # An empty gradient still needs an address to be asked for.
+    _call(_library().gemm_relu_grouped_backward, dev, dc.data_ptr(), c.data_ptr() if relu else None,
+          a.data_ptr() if need_db else None, b.data_ptr() if need_da else None, ends.data_ptr(),
+          (da.data_ptr() or 256) if need_da else None, (db.data_ptr() or 256) if need_db else None, M, N, K, groups,
+          code, b_layout, 1 if relu else 0, ws, ws_bytes, handle or None)
+    return (da if need_da else None), (db if need_db else None)
+
+
+def gemm_relu_adapters(x, w, u, v, scales, ends, ids, out=None, b_layout: int = B_KN, relu: bool = True,
+                       workspace=None, stream=None):
+    """C[m] = ReLU(x[m] @ W + scales[i] (x[m] @ U_i) @ V_i), i = ids[segment of row m].
+
+    ``x`` (M, K); B_KN: ``w`` (K, N), ``u`` (adapters, K, rank), ``v`` (adapters, rank, N); B_NK:
+    ``w`` (N, K), ``u`` (adapters, rank, K), ``v`` (adapters, N, rank); ``scales`` (adapters,) float32.
+    ``ends`` and ``ids`` (segments,) int32: segment s holds rows ends[s-1] .. ends[s]-1 and uses adapter
+    ids[s]; an id outside 0 .. adapters-1, and rows past the last end, use none.  ``relu=False``
+    leaves the ReLU out.
+    """
+    import torch
+    code, dev = _first("x", x)
+    _check_layout(b_layout)
+    nk = b_layout == B_NK
+    dtype = x.dtype
+    _check_tensor("x", x, 2, dev, dtype)
+    _check_tensor("w", w, 2, dev, dtype)
+    _check_tensor("u", u, 3, dev, dtype)
+    _check_tensor("v", v, 3, dev, dtype)
+    _check_tensor("scales", scales, 1, dev, torch.float32)
+    _check_tensor("ends", ends, 1, dev, torch.int32)
+    _check_tensor("ids", ids, 1, dev, torch.int32)
+    M, K = x.shape
+    N = w.shape[0 if nk else 1]
+    adapters, rank = u.shape[0], u.shape[1 if nk else 2]
+    _check_shape("w", w, (N, K) if nk else (K, N))
+    _check_shape("u", u, (adapters, rank, K) if nk else (adapters, K, rank))
+    _check_shape("v", v, (adapters, N, rank) if nk else (adapters, rank, N))
+    _check_shape("scales", scales, (adapters,))
+    segments = ends.shape[0]
+    _check_shape("ids", ids, (segments,))
+    if out is None:
+        out = _new((M, N), x, stream)
+    else:
+        _check_tensor("out", out, 2, dev, dtype)
+        _check_shape("out", out, (M, N))
+    handle = _stream_handle(stream, dev)
+    ws, ws_bytes, keep = _workspace(workspace, adapters_workspace_bytes(M, N, K, rank, adapters, segments, code,
+                                                                        b_layout), x, handle, stream)
+    _call(_library().gemm_relu_adapters, dev, x.data_ptr(), w.data_ptr(), u.data_ptr(), v.data_ptr(),
+          scales.data_ptr(), ends.data_ptr(), ids.data_ptr(), out.data_ptr(), M, N, K, rank, adapters, segments,
+          code, b_layout, 1 if relu else 0, ws, ws_bytes, handle or None)
+    return out
