@@ -55,14 +55,26 @@ extern "C" {
 
 #define GEMM_RELU_GROUPS_COUNTER_BYTES ((int64_t)65536)
 
+/* Kernels of the products below (`config_id`).  AUTO picks by size and
+ * alignment; the DMA kernels need row lengths that are multiples of 8 elements
+ * and 16-byte aligned operands, and a request that the arguments do not allow
+ * falls back to TILED.  Sums may be added in another order by another kernel. */
+enum {
+    GEMM_RELU_GROUPS_AUTO = -1,
+    GEMM_RELU_GROUPS_TILED = 0,   /* 128x128 tiles staged through registers: any row length and alignment */
+    GEMM_RELU_GROUPS_DMA_256 = 1, /* 256x256 tiles, 2 direct-to-LDS stages of 64 k, 8 waves */
+    GEMM_RELU_GROUPS_DMA_128 = 2, /* 128x128 tiles, 4 stages, 4 compute waves and 4 that only load */
+    GEMM_RELU_GROUPS_DMA_64 = 3   /* 64x64 tiles, 4 stages, 4 compute waves and 4 that only load */
+};
+
 /*
  * C[m] = act(A[m] @ B[g]) for every row m of group g; rows of no group are set
  * to +0.0.  A (M, K), C (M, N).  M == 0 or N == 0: nothing to do.  K == 0: C is
  * filled with +0.0.
  */
 int gemm_relu_grouped(const void* A, const void* B, const int32_t* ends, void* C, int64_t M, int64_t N,
-                      int64_t K, int64_t groups, int dtype, int b_layout, int relu, void* workspace,
-                      int64_t workspace_bytes, void* stream);
+                      int64_t K, int64_t groups, int dtype, int b_layout, int relu, int config_id,
+                      void* workspace, int64_t workspace_bytes, void* stream);
 int64_t gemm_relu_grouped_workspace(int64_t M, int64_t N, int64_t K, int64_t groups, int dtype, int b_layout);
 
 /*
@@ -77,7 +89,8 @@ int64_t gemm_relu_grouped_workspace(int64_t M, int64_t N, int64_t K, int64_t gro
  */
 int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, const void* B, const int32_t* ends,
                                void* dA, void* dB, int64_t M, int64_t N, int64_t K, int64_t groups, int dtype,
-                               int b_layout, int relu, void* workspace, int64_t workspace_bytes, void* stream);
+                               int b_layout, int relu, int config_id, void* workspace, int64_t workspace_bytes,
+                               void* stream);
 int64_t gemm_relu_grouped_backward_workspace(int64_t M, int64_t N, int64_t K, int64_t groups, int dtype,
                                              int b_layout, int relu);
 
@@ -97,7 +110,7 @@ int64_t gemm_relu_grouped_backward_workspace(int64_t M, int64_t N, int64_t K, in
 int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* V, const float* scales,
                        const int32_t* ends, const int32_t* ids, void* C, int64_t M, int64_t N, int64_t K,
                        int64_t rank, int64_t adapters, int64_t segments, int dtype, int b_layout, int relu,
-                       void* workspace, int64_t workspace_bytes, void* stream);
+                       int config_id, void* workspace, int64_t workspace_bytes, void* stream);
 int64_t gemm_relu_adapters_workspace(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t adapters,
                                      int64_t segments, int dtype, int b_layout);
 

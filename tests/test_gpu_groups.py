@@ -135,6 +135,48 @@ def test_grouped(shape, dtype, layout, relu):
         assert (out[-spare:].view(torch.int16) == 0).all()        # +0.0
 
 
+# Every kernel on shapes whose rows are 16-byte multiples (the others fall back to TILED): K-steps
+# with and without a tail, fewer steps than stages, tiles that end inside a group, several tiles of
+# work for a workgroup, more than 64 groups.
+CONFIGS = [groups.CONFIG_TILED, groups.CONFIG_DMA_256, groups.CONFIG_DMA_128, groups.CONFIG_DMA_64]
+CONFIG_SHAPES = [
+    ([1, 0, 4], 1, 64, 64),
+    ([40, 0, 256, 300], 3, 264, 136),
+    ([513, 130], 0, 520, 320),
+    ([0, 1, 5, 0, 70] * 17, 2, 136, 200),
+    ([2000, 0, 1300], 30, 2056, 64),
+]
+
+
+@pytest.mark.parametrize("layout", [gr.B_KN, gr.B_NK])
+@pytest.mark.parametrize("config", CONFIGS)
+@pytest.mark.parametrize("shape", range(len(CONFIG_SHAPES)))
+def test_grouped_kernels(shape, config, layout):
+    sizes, spare, N, K = CONFIG_SHAPES[shape]
+    M, dt = sum(sizes) + spare, (torch.float16, torch.bfloat16)[shape % 2]
+    say(f"[grouped] {sizes[:6]} M={M} N={N} K={K} {dt} layout={layout} config={config}")
+    a, b = normal((M, K), dt, 11 + shape), weights(len(sizes), N, K, dt, layout, 12 + shape)
+    ends = ends_of(sizes).cuda()
+    ref, err = grouped_reference(a, b, sizes, layout, True)
+    out, whole = guarded((M, N), dt)
+    gr.gemm_relu_grouped(a.cuda(), b.cuda(), ends, out=out, b_layout=layout, config=config)
+    torch.cuda.synchronize()
+    assert whole()
+    assert_close(out, ref, err, "C")
+    if spare:
+        assert (out[-spare:].view(torch.int16) == 0).all()
+    dc, c = normal((M, N), dt, 13 + shape), normal((M, N), dt, 14 + shape).clamp_min(0)
+    ra, ea, rb, eb = backward_reference(dc, c, a, b, sizes, layout, True)
+    da, whole_a = guarded((M, K), dt)
+    db, whole_b = guarded(tuple(b.shape), dt)
+    gr.gemm_relu_grouped_backward(dc.cuda(), c.cuda(), a.cuda(), b.cuda(), ends, b_layout=layout, da=da, db=db,
+                                  config=config)
+    torch.cuda.synchronize()
+    assert whole_a() and whole_b()
+    assert_close(da, ra, ea, "dA")
+    assert_close(db, rb, eb, "dB")
+
+
 @pytest.mark.parametrize("layout", [gr.B_KN, gr.B_NK])
 @pytest.mark.parametrize("N,K", [(64, 64), (66, 70), (40, 52)])
 def test_grouped_unaligned_matrices(N, K, layout):
@@ -386,6 +428,22 @@ def test_adapters(shape, dtype, layout, relu):
     ref, err = adapter_reference(x, w, u, v, scales, sizes, ids, layout, relu)
     out, whole = guarded((x.shape[0], N), DT[dtype])
     gr.gemm_relu_adapters(*(t.cuda() for t in (x, w, u, v, scales, ends, ids)), out=out, b_layout=layout, relu=relu)
+    torch.cuda.synchronize()
+    assert whole()
+    assert_close(out, ref, err, "C")
+
+
+@pytest.mark.parametrize("layout", [gr.B_KN, gr.B_NK])
+@pytest.mark.parametrize("config", CONFIGS)
+@pytest.mark.parametrize("sizes,N,K,rank", [([1] * 37 + [100, 0, 300], 264, 136, 16), ([1500, 1300], 2056, 64, 40),
+                                            ([1] * 90, 64, 320, 64)])
+def test_adapter_kernels(sizes, N, K, rank, config, layout):
+    dt = torch.bfloat16 if rank == 16 else torch.float16
+    say(f"[adapters] {sizes[:3]} N={N} K={K} rank={rank} {dt} layout={layout} config={config}")
+    x, w, u, v, scales, ends, ids = adapter_inputs(sizes, 1, N, K, rank, 6, dt, layout, 65)
+    ref, err = adapter_reference(x, w, u, v, scales, sizes, ids, layout, True)
+    out, whole = guarded((x.shape[0], N), dt)
+    gr.gemm_relu_adapters(*(t.cuda() for t in (x, w, u, v, scales, ends, ids)), out=out, b_layout=layout, config=config)
     torch.cuda.synchronize()
     assert whole()
     assert_close(out, ref, err, "C")

@@ -31,25 +31,27 @@ def test_library_exports_every_declared_symbol(lib):
         assert ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
 
 
-def grouped(lib, a=A, b=B, ends=E, c=C, M=4, N=8, K=8, groups=2, dtype=0, layout=0, relu=1, ws=W, ws_bytes=1 << 30):
-    return lib.gemm_relu_grouped(a, b, ends, c, M, N, K, groups, dtype, layout, relu, ws, ws_bytes, None)
+def grouped(lib, a=A, b=B, ends=E, c=C, M=4, N=8, K=8, groups=2, dtype=0, layout=0, relu=1, config=-1, ws=W,
+            ws_bytes=1 << 30):
+    return lib.gemm_relu_grouped(a, b, ends, c, M, N, K, groups, dtype, layout, relu, config, ws, ws_bytes, None)
 
 
-def backward(lib, dc=D, c=C, a=A, b=B, ends=E, da=U, db=V, M=4, N=8, K=8, groups=2, dtype=0, layout=0, relu=1, ws=W,
-             ws_bytes=1 << 30):
-    return lib.gemm_relu_grouped_backward(dc, c, a, b, ends, da, db, M, N, K, groups, dtype, layout, relu, ws,
-                                          ws_bytes, None)
+def backward(lib, dc=D, c=C, a=A, b=B, ends=E, da=U, db=V, M=4, N=8, K=8, groups=2, dtype=0, layout=0, relu=1, config=-1,
+             ws=W, ws_bytes=1 << 30):
+    return lib.gemm_relu_grouped_backward(dc, c, a, b, ends, da, db, M, N, K, groups, dtype, layout, relu, config,
+                                          ws, ws_bytes, None)
 
 
 def adapters(lib, x=A, w=B, u=U, v=V, scales=D, ends=E, ids=E + 4096, c=C, M=4, N=8, K=8, rank=4, count=3, segments=2,
-             dtype=0, layout=0, relu=1, ws=W, ws_bytes=1 << 30):
+             dtype=0, layout=0, relu=1, config=-1, ws=W, ws_bytes=1 << 30):
     return lib.gemm_relu_adapters(x, w, u, v, scales, ends, ids, c, M, N, K, rank, count, segments, dtype, layout,
-                                  relu, ws, ws_bytes, None)
+                                  relu, config, ws, ws_bytes, None)
 
 
 COMMON = [({"dtype": 2}, -2), ({"dtype": -1}, -2), ({"layout": 2}, -9), ({"layout": -1}, -9), ({"M": -1}, -1),
           ({"N": -1}, -1), ({"K": -1}, -1), ({"relu": 2}, -1), ({"relu": -1}, -1), ({"M": (1 << 20) + 1}, -7),
-          ({"N": (1 << 20) + 1}, -7), ({"K": (1 << 20) + 1}, -7), ({"ends": 0}, -1), ({"ends": E + 2}, -4)]
+          ({"N": (1 << 20) + 1}, -7), ({"K": (1 << 20) + 1}, -7), ({"ends": 0}, -1), ({"ends": E + 2}, -4), ({"config": -2}, -8),
+          ({"config": 99}, -8)]
 
 
 @pytest.mark.parametrize("args,code", COMMON + [

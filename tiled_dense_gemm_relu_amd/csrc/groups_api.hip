@@ -102,26 +102,55 @@ int zero_fill(void* p, int64_t halves, hipStream_t stream)
 // whole tiles, and one partial tile for each.
 int64_t most_row_tiles(int64_t M, int64_t groups, int64_t rows) { return std::min(M, M / rows + groups + 1); }
 
-// A product over row groups (M, N, K > 0).
-int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, hipStream_t stream)
+bool known_config(int id) { return id >= GEMM_RELU_GROUPS_AUTO && id <= GEMM_RELU_GROUPS_DMA_64; }
+
+// Tile of an LDS-DMA product: the largest whose tiles are mostly full (`rows`:
+// a group's rows on average) and numerous enough to occupy the CUs.
+int dma_config(int64_t rows, int64_t tiles_256, int64_t tiles_128)
 {
-    const int64_t grid = most_row_tiles(a.m, a.groups, 128) * ceil_div(a.n, 128);
-    if (grid > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
+    if (rows >= 192 && tiles_256 >= 192) return GEMM_RELU_GROUPS_DMA_256;
+    if (rows >= 96 && tiles_128 >= 128) return GEMM_RELU_GROUPS_DMA_128;
+    return GEMM_RELU_GROUPS_DMA_64;
+}
+
+// A product over row groups (M, N, K > 0).
+int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config, int cus, hipStream_t stream)
+{
     a.c_vec = store_width(a.c, a.n);
     const int w = load_width({{a.a, a.k}, {a.b, b_layout == GEMM_RELU_B_NK ? a.k : a.n}});
+    if (w > 0) config = GEMM_RELU_GROUPS_TILED;
+    if (config == GEMM_RELU_GROUPS_AUTO) {
+        const int64_t used = std::min(a.groups, a.m), rows = a.m / used;
+        config = dma_config(rows, used * ceil_div(rows, 256) * ceil_div(a.n, 256), used * ceil_div(rows, 128) * ceil_div(a.n, 128));
+    }
+    if (config == GEMM_RELU_GROUPS_DMA_256 && ad.v) config = GEMM_RELU_GROUPS_DMA_128;
+    const int64_t rows = config == GEMM_RELU_GROUPS_TILED ? 128 : kGroupTile[config - 1];
+    const int64_t tiles = most_row_tiles(a.m, a.groups, rows) * ceil_div(a.n, rows);
+    if (tiles > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
     void* args[] = {&a, &ad};
-    return enqueue(kernels(dtype).rows_tiled[b_layout][w], grid, 1, 256, args, stream);
+    if (config == GEMM_RELU_GROUPS_TILED)
+        return enqueue(kernels(dtype).rows_tiled[b_layout][w], tiles, 1, 256, args, stream);
+    // persistent workgroups, one per CU
+    return enqueue(kernels(dtype).rows_dma[config - 1][b_layout][a.k % 64 != 0][ad.v != nullptr], std::min<int64_t>(tiles, cus), 1,
+                   kGroupThreads[config - 1], args, stream);
 }
 
 // Sums over each group's rows (I, J > 0).
-int launch_weights(WeightArgs a, int dtype, hipStream_t stream)
+int launch_weights(WeightArgs a, int dtype, int config, int cus, hipStream_t stream)
 {
-    const int64_t grid = int64_t(a.groups) * ceil_div(a.i, 128) * ceil_div(a.j, 128);
-    if (grid > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
     a.c_vec = store_width(a.out, a.j);
     const int w = load_width({{a.p, a.i}, {a.q, a.j}});
+    if (w > 0) config = GEMM_RELU_GROUPS_TILED;
+    if (config == GEMM_RELU_GROUPS_AUTO)
+        config = dma_config(a.i, a.groups * ceil_div(a.i, 256) * ceil_div(a.j, 256),
+                            a.groups * ceil_div(a.i, 128) * ceil_div(a.j, 128));
+    const int64_t rows = config == GEMM_RELU_GROUPS_TILED ? 128 : kGroupTile[config - 1];
+    const int64_t tiles = int64_t(a.groups) * ceil_div(a.i, rows) * ceil_div(a.j, rows);
+    if (tiles > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
     void* args[] = {&a};
-    return enqueue(kernels(dtype).weight_tiled[w], grid, 1, 256, args, stream);
+    if (config == GEMM_RELU_GROUPS_TILED) return enqueue(kernels(dtype).weight_tiled[w], tiles, 1, 256, args, stream);
+    return enqueue(kernels(dtype).weight_dma[config - 1], std::min<int64_t>(tiles, cus), 1, kGroupThreads[config - 1], args,
+                   stream);
 }
 
 // Workspace layout: the counters, then each operator's intermediates.
@@ -152,12 +181,13 @@ int64_t gemm_relu_grouped_workspace(int64_t M, int64_t N, int64_t K, int64_t gro
 }
 
 int gemm_relu_grouped(const void* A, const void* B, const int32_t* ends, void* C, int64_t M, int64_t N,
-                      int64_t K, int64_t groups, int dtype, int b_layout, int relu, void* workspace,
-                      int64_t workspace_bytes, void* stream)
+                      int64_t K, int64_t groups, int dtype, int b_layout, int relu, int config_id,
+                      void* workspace, int64_t workspace_bytes, void* stream)
 {
     const int64_t need = gemm_relu_grouped_workspace(M, N, K, groups, dtype, b_layout);
     if (need < 0) return (int)need;
     if (relu != 0 && relu != 1) return GEMM_RELU_ERR_INVALID_ARG;
+    if (!known_config(config_id)) return GEMM_RELU_ERR_BAD_CONFIG;
     if (M == 0 || N == 0) return GEMM_RELU_OK;
     const Span in[] = {{A, 2 * M * K}, {B, 2 * groups * K * N}}, words[] = {{ends, 4 * groups}};
     const Span out[] = {{C, 2 * M * N}, {workspace, need}};
@@ -170,7 +200,7 @@ int gemm_relu_grouped(const void* A, const void* B, const int32_t* ends, void* C
     if (K == 0) return zero_fill(C, M * N, s);
     RowsArgs a{static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), static_cast<uint16_t*>(C), ends,
                (int)M, (int)N, (int)K, (int)groups, relu, 0};
-    return launch_rows(a, AdapterArgs{}, dtype, b_layout, s);
+    return launch_rows(a, AdapterArgs{}, dtype, b_layout, config_id, cus, s);
 }
 
 int64_t gemm_relu_grouped_backward_workspace(int64_t M, int64_t N, int64_t K, int64_t groups, int dtype,
@@ -184,10 +214,12 @@ int64_t gemm_relu_grouped_backward_workspace(int64_t M, int64_t N, int64_t K, in
 
 int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, const void* B, const int32_t* ends,
                                void* dA, void* dB, int64_t M, int64_t N, int64_t K, int64_t groups, int dtype,
-                               int b_layout, int relu, void* workspace, int64_t workspace_bytes, void* stream)
+                               int b_layout, int relu, int config_id, void* workspace, int64_t workspace_bytes,
+                               void* stream)
 {
     const int64_t need = gemm_relu_grouped_backward_workspace(M, N, K, groups, dtype, b_layout, relu);
     if (need < 0) return (int)need;
+    if (!known_config(config_id)) return GEMM_RELU_ERR_BAD_CONFIG;
     const bool want_a = dA != nullptr, want_b = dB != nullptr;
     if (!want_a && !want_b && K > 0) return GEMM_RELU_ERR_INVALID_ARG;
     if (K == 0) return GEMM_RELU_OK;                 // both gradients are empty
@@ -220,14 +252,15 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
         // D (M, N) times B^T: B as stored (K, N) is the transposed weight of this product
         RowsArgs a{d, static_cast<const uint16_t*>(B), static_cast<uint16_t*>(dA), ends,
                    (int)M, (int)K, (int)N, (int)groups, 0, 0};
-        rc = launch_rows(a, AdapterArgs{}, dtype, b_layout == GEMM_RELU_B_KN ? GEMM_RELU_B_NK : GEMM_RELU_B_KN, s);
+        rc = launch_rows(a, AdapterArgs{}, dtype, b_layout == GEMM_RELU_B_KN ? GEMM_RELU_B_NK : GEMM_RELU_B_KN,
+                         config_id, cus, s);
     }
     if (want_b && rc == GEMM_RELU_OK && gkn > 0) {
         const uint16_t* x = static_cast<const uint16_t*>(A);
         const bool kn = b_layout == GEMM_RELU_B_KN;
         WeightArgs a{kn ? x : d, kn ? d : x, static_cast<uint16_t*>(dB), ends,
                      (int)M, (int)(kn ? K : N), (int)(kn ? N : K), (int)groups, 0};
-        rc = launch_weights(a, dtype, s);
+        rc = launch_weights(a, dtype, config_id, cus, s);
     }
     return rc;
 }
@@ -245,11 +278,12 @@ int64_t gemm_relu_adapters_workspace(int64_t M, int64_t N, int64_t K, int64_t ra
 int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* V, const float* scales,
                        const int32_t* ends, const int32_t* ids, void* C, int64_t M, int64_t N, int64_t K,
                        int64_t rank, int64_t adapters, int64_t segments, int dtype, int b_layout, int relu,
-                       void* workspace, int64_t workspace_bytes, void* stream)
+                       int config_id, void* workspace, int64_t workspace_bytes, void* stream)
 {
     const int64_t need = gemm_relu_adapters_workspace(M, N, K, rank, adapters, segments, dtype, b_layout);
     if (need < 0) return (int)need;
     if (relu != 0 && relu != 1) return GEMM_RELU_ERR_INVALID_ARG;
+    if (!known_config(config_id)) return GEMM_RELU_ERR_BAD_CONFIG;
     if (M == 0 || N == 0) return GEMM_RELU_OK;
     const Span in[] = {{X, 2 * M * K}, {W, 2 * K * N}, {U, 2 * adapters * K * rank}, {V, 2 * adapters * rank * N}};
     const Span words[] = {{ends, 4 * segments}, {ids, 4 * segments}, {scales, 4 * adapters}};
@@ -276,7 +310,7 @@ int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* 
                (int)M, (int)N, (int)K, 1, relu, 0};
     AdapterArgs ad{static_cast<const uint16_t*>(V), t, factor, ends, ids, (int)segments, (int)adapters, (int)rank,
                    (int)space.rank_pad, rank % 8 == 0 && aligned(V, 16)};
-    return launch_rows(a, ad, dtype, b_layout, s);
+    return launch_rows(a, ad, dtype, b_layout, config_id, cus, s);
 }
 
 }  // extern "C"

@@ -1,5 +1,5 @@
-// The kernel instances of gemm_relu_groups.h for one dtype.
-#include "groups_kernels.hpp"
+// The kernel instances of gemm_relu_groups.h for the f16 dtype.
+#include "groups_instances.hpp"
 
 namespace gemm_relu_hip {
 const GroupKernels& group_kernels_f16()

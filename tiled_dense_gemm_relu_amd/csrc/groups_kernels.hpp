@@ -496,29 +496,4 @@ __global__ __launch_bounds__(256) void relu_mask(MaskArgs a)
     for (int64_t q = chunks * 8 + first; q < a.count; q += stride) a.d[q] = mask_one<DT>(a.dc[q], a.c[q]);
 }
 
-// ---------------------------------------------------------------- instances
-
-template <int DT, int W>
-void fill_group_width(GroupKernels& t)
-{
-    constexpr int VEC = kLoadWidths[W];
-    t.rows_tiled[0][W] = (const void*)&rows_tiled<DT, false, VEC>;
-    t.rows_tiled[1][W] = (const void*)&rows_tiled<DT, true, VEC>;
-    t.weight_tiled[W] = (const void*)&weight_tiled<DT, VEC>;
-    t.shrink[0][W] = (const void*)&adapter_shrink<DT, false, VEC>;
-    t.shrink[1][W] = (const void*)&adapter_shrink<DT, true, VEC>;
-}
-
-template <int DT>
-GroupKernels make_group_table()
-{
-    GroupKernels t{};
-    fill_group_width<DT, 0>(t);
-    fill_group_width<DT, 1>(t);
-    fill_group_width<DT, 2>(t);
-    fill_group_width<DT, 3>(t);
-    t.mask = (const void*)&relu_mask<DT>;
-    return t;
-}
-
 }  // namespace gemm_relu_hip

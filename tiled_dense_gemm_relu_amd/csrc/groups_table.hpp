@@ -64,7 +64,15 @@ constexpr int kNumLoadWidths = 4;
 constexpr int kLoadWidths[kNumLoadWidths] = {8, 4, 2, 1};
 constexpr int kShrinkRows = 16, kShrinkCols = 32, kShrinkThreads = 512;
 
+// Square LDS-DMA tiles, by GEMM_RELU_GROUPS_DMA_* order, and their workgroups.
+constexpr int kNumGroupTiles = 3;
+constexpr int kGroupTile[kNumGroupTiles] = {256, 128, 64};
+constexpr int kGroupThreads[kNumGroupTiles] = {512, 512, 512};
+
 struct GroupKernels {
+    // [tile][B layout][K % 64 != 0][with adapters]; the 256 tile has no adapter instances
+    const void* rows_dma[kNumGroupTiles][2][2][2];
+    const void* weight_dma[kNumGroupTiles];
     const void* rows_tiled[2][kNumLoadWidths];    // [B layout][load width]
     const void* weight_tiled[kNumLoadWidths];
     const void* mask;

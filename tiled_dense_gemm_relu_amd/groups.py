@@ -15,6 +15,13 @@ from .binding import B_KN, B_NK, _check, _dtype_code, _stream_handle
 
 COUNTER_BYTES = 65536      # GEMM_RELU_GROUPS_COUNTER_BYTES
 
+# Kernels (GEMM_RELU_GROUPS_*).
+CONFIG_AUTO = -1
+CONFIG_TILED = 0
+CONFIG_DMA_256 = 1
+CONFIG_DMA_128 = 2
+CONFIG_DMA_64 = 3
+
 _lock = threading.Lock()
 _lib = None
 
@@ -25,15 +32,15 @@ def _library():
         lib = binding.load_library()
         with _lock:
             vp, i64, ci = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
-            lib.gemm_relu_grouped.argtypes = [vp] * 4 + [i64] * 4 + [ci] * 3 + [vp, i64, vp]
+            lib.gemm_relu_grouped.argtypes = [vp] * 4 + [i64] * 4 + [ci] * 4 + [vp, i64, vp]
             lib.gemm_relu_grouped.restype = ci
             lib.gemm_relu_grouped_workspace.argtypes = [i64] * 4 + [ci] * 2
             lib.gemm_relu_grouped_workspace.restype = i64
-            lib.gemm_relu_grouped_backward.argtypes = [vp] * 7 + [i64] * 4 + [ci] * 3 + [vp, i64, vp]
+            lib.gemm_relu_grouped_backward.argtypes = [vp] * 7 + [i64] * 4 + [ci] * 4 + [vp, i64, vp]
             lib.gemm_relu_grouped_backward.restype = ci
             lib.gemm_relu_grouped_backward_workspace.argtypes = [i64] * 4 + [ci] * 3
             lib.gemm_relu_grouped_backward_workspace.restype = i64
-            lib.gemm_relu_adapters.argtypes = [vp] * 8 + [i64] * 6 + [ci] * 3 + [vp, i64, vp]
+            lib.gemm_relu_adapters.argtypes = [vp] * 8 + [i64] * 6 + [ci] * 4 + [vp, i64, vp]
             lib.gemm_relu_adapters.restype = ci
             lib.gemm_relu_adapters_workspace.argtypes = [i64] * 6 + [ci] * 2
             lib.gemm_relu_adapters_workspace.restype = i64
@@ -149,14 +156,15 @@ def _call(function, dev, *args):
         _check(rc)
 
 
-def gemm_relu_grouped(a, b, ends, out=None, b_layout: int = B_KN, relu: bool = True, workspace=None, stream=None):
+def gemm_relu_grouped(a, b, ends, out=None, b_layout: int = B_KN, relu: bool = True, config: int = CONFIG_AUTO,
+                      workspace=None, stream=None):
     """C[m] = ReLU(a[m] @ B[g]) for every row m of group g (``relu=False``: without the ReLU).
 
     ``a`` (M, K), fp16 or bf16; ``b`` (groups, K, N), or (groups, N, K) with B_NK; ``ends`` (groups,)
     int32 on the GPU, non-decreasing: group g holds rows ends[g-1] .. ends[g]-1 (a running sum of
     row counts).  Rows past the last end get zeros.  ``out`` (M, N) is written if given.
     ``workspace``: at least grouped_workspace_bytes(...) bytes whose first 65536 are zero, or None
-    for a cached one per stream.
+    for a cached one per stream.  ``config``: a kernel (CONFIG_*), by default the library's choice.
     """
     import torch
     code, dev = _first("a", a)
@@ -179,12 +187,13 @@ def gemm_relu_grouped(a, b, ends, out=None, b_layout: int = B_KN, relu: bool = T
     ws, ws_bytes, keep = _workspace(workspace, grouped_workspace_bytes(M, N, K, groups, code, b_layout), a, handle,
                                     stream)
     _call(_library().gemm_relu_grouped, dev, a.data_ptr(), b.data_ptr(), ends.data_ptr(), out.data_ptr(), M, N, K,
-          groups, code, b_layout, 1 if relu else 0, ws, ws_bytes, handle or None)
+          groups, code, b_layout, 1 if relu else 0, config, ws, ws_bytes, handle or None)
     return out
 
 
 def gemm_relu_grouped_backward(dc, c, a, b, ends, b_layout: int = B_KN, relu: bool = True, da=None, db=None,
-                               need_da: bool = True, need_db: bool = True, workspace=None, stream=None):
+                               need_da: bool = True, need_db: bool = True, config: int = CONFIG_AUTO, workspace=None,
+                               stream=None):
     """Gradients (da, db) of gemm_relu_grouped's C = ``c`` for its gradient ``dc``, both (M, N).
 
     da has a's shape (zeros in rows of no group), db has b's (zeros for empty groups).
@@ -231,12 +240,12 @@ def gemm_relu_grouped_backward(dc, c, a, b, ends, b_layout: int = B_KN, relu: bo
     _call(_library().gemm_relu_grouped_backward, dev, dc.data_ptr(), c.data_ptr() if relu else None,
           a.data_ptr() if need_db else None, b.data_ptr() if need_da else None, ends.data_ptr(),
           (da.data_ptr() or 256) if need_da else None, (db.data_ptr() or 256) if need_db else None, M, N, K, groups,
-          code, b_layout, 1 if relu else 0, ws, ws_bytes, handle or None)
+          code, b_layout, 1 if relu else 0, config, ws, ws_bytes, handle or None)
     return (da if need_da else None), (db if need_db else None)
 
 
 def gemm_relu_adapters(x, w, u, v, scales, ends, ids, out=None, b_layout: int = B_KN, relu: bool = True,
-                       workspace=None, stream=None):
+                       config: int = CONFIG_AUTO, workspace=None, stream=None):
     """C[m] = ReLU(x[m] @ W + scales[i] (x[m] @ U_i) @ V_i), i = ids[segment of row m].
 
     ``x`` (M, K); B_KN: ``w`` (K, N), ``u`` (adapters, K, rank), ``v`` (adapters, rank, N); B_NK:
@@ -276,5 +285,5 @@ def gemm_relu_adapters(x, w, u, v, scales, ends, ids, out=None, b_layout: int = 
                                                                         b_layout), x, handle, stream)
     _call(_library().gemm_relu_adapters, dev, x.data_ptr(), w.data_ptr(), u.data_ptr(), v.data_ptr(),
           scales.data_ptr(), ends.data_ptr(), ids.data_ptr(), out.data_ptr(), M, N, K, rank, adapters, segments,
-          code, b_layout, 1 if relu else 0, ws, ws_bytes, handle or None)
+          code, b_layout, 1 if relu else 0, config, ws, ws_bytes, handle or None)
     return out
