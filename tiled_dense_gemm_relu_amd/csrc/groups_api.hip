@@ -84,9 +84,9 @@ int store_width(const void* c, int64_t n) { return n % 8 == 0 && aligned(c, 16) 
 
 const GroupKernels& kernels(int dtype) { return dtype == GEMM_RELU_F16 ? group_kernels_f16() : group_kernels_bf16(); }
 
-int enqueue(const void* fn, int64_t grid, int grid_y, int threads, void** args, hipStream_t stream)
+int enqueue(const void* fn, dim3 grid, int threads, void** args, hipStream_t stream)
 {
-    const hipError_t err = hipLaunchKernel(fn, dim3((unsigned)grid, (unsigned)grid_y), dim3((unsigned)threads), args, 0, stream);
+    const hipError_t err = hipLaunchKernel(fn, grid, dim3((unsigned)threads), args, 0, stream);
     return err == hipSuccess ? GEMM_RELU_OK : GEMM_RELU_ERR_LAUNCH;
 }
 
@@ -95,7 +95,7 @@ int zero_fill(void* p, int64_t halves, hipStream_t stream)
     if (halves <= 0) return GEMM_RELU_OK;
     size_t count = (size_t)halves;
     void* args[] = {&p, &count};
-    return enqueue(zero_fill_kernel(), std::min<int64_t>(ceil_div(halves, 256), 65536), 1, 256, args, stream);
+    return enqueue(zero_fill_kernel(), dim3((unsigned)std::min<int64_t>(ceil_div(halves, 256), 65536)), 256, args, stream);
 }
 
 // Row tiles that `groups` groups (and the rows of none) can have among M rows:
@@ -129,10 +129,10 @@ int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config,
     if (tiles > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
     void* args[] = {&a, &ad};
     if (config == GEMM_RELU_GROUPS_TILED)
-        return enqueue(kernels(dtype).rows_tiled[b_layout][w], tiles, 1, 256, args, stream);
+        return enqueue(kernels(dtype).rows_tiled[b_layout][w], dim3((unsigned)tiles), 256, args, stream);
     // persistent workgroups, one per CU
-    return enqueue(kernels(dtype).rows_dma[config - 1][b_layout][a.k % 64 != 0][ad.v != nullptr], std::min<int64_t>(tiles, cus), 1,
-                   kGroupThreads[config - 1], args, stream);
+    return enqueue(kernels(dtype).rows_dma[config - 1][b_layout][a.k % 64 != 0][ad.v != nullptr],
+                   dim3((unsigned)std::min<int64_t>(tiles, cus)), kGroupThreads[config - 1], args, stream);
 }
 
 // Sums over each group's rows (I, J > 0).
@@ -148,24 +148,32 @@ int launch_weights(WeightArgs a, int dtype, int config, int cus, hipStream_t str
     const int64_t tiles = int64_t(a.groups) * ceil_div(a.i, rows) * ceil_div(a.j, rows);
     if (tiles > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
     void* args[] = {&a};
-    if (config == GEMM_RELU_GROUPS_TILED) return enqueue(kernels(dtype).weight_tiled[w], tiles, 1, 256, args, stream);
-    return enqueue(kernels(dtype).weight_dma[config - 1], std::min<int64_t>(tiles, cus), 1, kGroupThreads[config - 1], args,
+    if (config == GEMM_RELU_GROUPS_TILED) return enqueue(kernels(dtype).weight_tiled[w], dim3((unsigned)tiles), 256, args, stream);
+    return enqueue(kernels(dtype).weight_dma[config - 1], dim3((unsigned)std::min<int64_t>(tiles, cus)), kGroupThreads[config - 1], args,
                    stream);
 }
 
-// Workspace layout: the counters, then each operator's intermediates.
+// Workspace of the adapters: the counters, the intermediates, each row's
+// adapter, and the partial sums of a K that is cut into `splits` parts: as many
+// as make 512 workgroups, while each of their 8 waves has a piece of K.
 struct AdapterSpace {
-    int64_t rank_pad, t, factor, bytes;
+    int64_t rank_pad, tiles, splits, t, factor, row_id, part, bytes;
 };
-AdapterSpace adapter_space(int64_t M, int64_t rank)
+AdapterSpace adapter_space(int64_t M, int64_t K, int64_t rank, int64_t segments)
 {
     AdapterSpace s;
     s.rank_pad = round_up(rank, 32);
+    s.tiles = most_row_tiles(M, segments, kShrinkRows);
+    const int64_t slots = s.tiles * (s.rank_pad / kShrinkCols);
+    s.splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(K, 8 * kShrinkK), slots ? 512 / slots : 1));
     s.t = GEMM_RELU_GROUPS_COUNTER_BYTES;
     s.factor = s.t + round_up(M * 2 * s.rank_pad * 2, 256);
-    s.bytes = s.factor + round_up(M * (s.rank_pad / 32) * 4, 256);
+    s.row_id = s.factor + round_up(M * (s.rank_pad / 32) * 4, 256);
+    s.part = s.row_id + round_up(M * 4, 256);
+    s.bytes = s.part + (s.splits > 1 ? slots * s.splits * kShrinkThreads * 4 : 0);
     return s;
 }
+static_assert(512 * 4 <= GEMM_RELU_GROUPS_COUNTER_BYTES, "a counter for each slot of a split sum");
 
 }  // namespace
 }  // namespace gemm_relu_hip
@@ -245,7 +253,7 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
         uint16_t* masked = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + GEMM_RELU_GROUPS_COUNTER_BYTES);
         MaskArgs m{d, static_cast<const uint16_t*>(C), masked, mn, aligned(dC, 16) && aligned(C, 16)};
         void* args[] = {&m};
-        rc = enqueue(kernels(dtype).mask, std::min<int64_t>(ceil_div(mn, 2048), 4096), 1, 256, args, s);
+        rc = enqueue(kernels(dtype).mask, dim3((unsigned)std::min<int64_t>(ceil_div(mn, 2048), 4096)), 256, args, s);
         d = masked;
     }
     if (want_a && rc == GEMM_RELU_OK) {
@@ -272,7 +280,7 @@ int64_t gemm_relu_adapters_workspace(int64_t M, int64_t N, int64_t K, int64_t ra
     if (rc != GEMM_RELU_OK) return rc;
     if (rank < 1 || adapters < 1) return GEMM_RELU_ERR_INVALID_ARG;
     if (rank > kMaxRank || adapters > kMaxGroups) return GEMM_RELU_ERR_TOO_LARGE;
-    return adapter_space(M, rank).bytes;
+    return adapter_space(M, K, rank, segments).bytes;
 }
 
 int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* V, const float* scales,
@@ -296,20 +304,22 @@ int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* 
     if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (K == 0) return zero_fill(C, M * N, s);
-    const AdapterSpace space = adapter_space(M, rank);
-    uint16_t* t = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + space.t);
-    float* factor = reinterpret_cast<float*>(static_cast<char*>(workspace) + space.factor);
-    ShrinkArgs sh{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(U), scales, ends, ids, t, factor,
-                  (int)M, (int)K, (int)segments, (int)adapters, (int)rank, (int)space.rank_pad};
-    const int w = b_layout == GEMM_RELU_B_NK ? load_width({{X, K}, {U, K}}) : load_width({{X, K}});
+    const AdapterSpace space = adapter_space(M, K, rank, segments);
+    char* const ws = static_cast<char*>(workspace);
+    uint16_t* t = reinterpret_cast<uint16_t*>(ws + space.t);
+    float* factor = reinterpret_cast<float*>(ws + space.factor);
+    int* row_id = reinterpret_cast<int*>(ws + space.row_id);
+    ShrinkArgs sh{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(U), scales, ends, ids, t, factor, row_id,
+                  reinterpret_cast<float*>(ws + space.part), reinterpret_cast<int*>(ws), (int)M, (int)K, (int)segments,
+                  (int)adapters, (int)rank, (int)space.rank_pad};
     void* args[] = {&sh};
-    rc = enqueue(kernels(dtype).shrink[b_layout][w], most_row_tiles(M, segments, kShrinkRows),
-                 (int)(space.rank_pad / kShrinkCols), kShrinkThreads, args, s);
+    rc = enqueue(kernels(dtype).shrink[b_layout], dim3((unsigned)space.tiles, (unsigned)(space.rank_pad / kShrinkCols), (unsigned)space.splits),
+                 kShrinkThreads, args, s);
     if (rc != GEMM_RELU_OK) return rc;
     RowsArgs a{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(W), static_cast<uint16_t*>(C), nullptr,
                (int)M, (int)N, (int)K, 1, relu, 0};
-    AdapterArgs ad{static_cast<const uint16_t*>(V), t, factor, ends, ids, (int)segments, (int)adapters, (int)rank,
-                   (int)space.rank_pad, rank % 8 == 0 && aligned(V, 16)};
+    const bool v_fast = b_layout == GEMM_RELU_B_NK ? rank % 8 == 0 && aligned(V, 16) : N % 4 == 0 && aligned(V, 8);
+    AdapterArgs ad{static_cast<const uint16_t*>(V), t, factor, row_id, (int)rank, (int)space.rank_pad, v_fast};
     return launch_rows(a, ad, dtype, b_layout, config_id, cus, s);
 }
 

@@ -13,8 +13,6 @@
 //    K-steps of all its units through one ring.
 #pragma once
 
-#include <type_traits>
-
 #include "groups_kernels.hpp"
 
 namespace gemm_relu_hip {
@@ -34,6 +32,9 @@ struct GroupDmaConfig {
     static constexpr int LDS_BYTES = STAGES * (A_STAGE + B_STAGE);
     static constexpr bool C_STAGED = WTN % 64 == 0 && WTM % 32 == 0 && LDS_BYTES + WAVES * 4096 <= 160 * 1024;
     static constexpr int C_STAGE_BYTES = C_STAGED ? WAVES * 4096 : 0;
+    // Adapters stage V there too, or in strips of their own.
+    static constexpr int ADAPT_BYTES = C_STAGED ? 0 : WAVES * kAdapterStrip<FN>;
+    static_assert(!C_STAGED || kAdapterStrip<FN> <= 4096, "V's strip");
     static constexpr int QA = A_STAGE / 1024 / DMA_WAVES, QB = B_STAGE / 1024 / DMA_WAVES, NQ = QA + QB;
     static_assert(QA * DMA_WAVES * 1024 == A_STAGE && QB * DMA_WAVES * 1024 == B_STAGE, "whole DMA instructions");
     static_assert((STAGES & (STAGES - 1)) == 0 && STAGES >= 2 && LDS_BYTES <= 160 * 1024, "ring");
@@ -177,7 +178,7 @@ template <class Cfg, int DT, bool KTAIL, bool ADAPT, class Units>
 __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* __restrict__ A,
                                             const uint16_t* __restrict__ B, uint16_t* __restrict__ C, uint32_t lda,
                                             uint32_t ldb, size_t b_group, size_t c_group, int N, bool relu, int c_vec,
-                                            const AdapterArgs& ad, int M, uint8_t* smem)
+                                            const AdapterArgs& ad, uint8_t* smem)
 {
     constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK, S = Cfg::STAGES;
     constexpr int QA = Cfg::QA, QB = Cfg::QB, NQ = Cfg::NQ, FM = Cfg::FM, FN = Cfg::FN;
@@ -445,7 +446,9 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
         c_k += BK;
         if (c_k >= c.k_end) {
             const int m_base = c.m0 + wm * Cfg::WTM, n_base = c.n0 + wn * Cfg::WTN;
-            if constexpr (ADAPT) add_adapters<DT, !BKM>(acc, ad, m_base, c.m_end, M, n_base, N, lane);
+            if constexpr (ADAPT)
+                add_adapters<DT, !BKM>(acc, ad, m_base, c.m_end, n_base, N, lane,
+                                                  smem + Cfg::LDS_BYTES + wave * kAdapterStrip<FN>);
             uint16_t* out = C + (size_t)c.group * c_group;
             bool staged = false;
             if constexpr (Cfg::C_STAGED) {
@@ -488,12 +491,12 @@ __device__ __forceinline__ void zero_rows(const RowsArgs& a, int first)
 template <class Cfg, int DT, bool KTAIL, bool ADAPT>
 __global__ __launch_bounds__(Cfg::THREADS, 1) void rows_dma(RowsArgs a, AdapterArgs ad)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES + Cfg::C_STAGE_BYTES];
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES + Cfg::C_STAGE_BYTES + (ADAPT ? Cfg::ADAPT_BYTES : 0)];
     RowUnits<Cfg> units;
     units.init(a, threadIdx.x & 63);
     if (units.rows < a.m) zero_rows(a, units.rows);
     dma_product<Cfg, DT, KTAIL, ADAPT>(units, a.a, a.b, a.c, (uint32_t)a.k, (uint32_t)(Cfg::B_KMAJOR ? a.n : a.k),
-                                       (size_t)a.k * (size_t)a.n, 0, a.n, a.relu != 0, a.c_vec, ad, a.m, smem);
+                                       (size_t)a.k * (size_t)a.n, 0, a.n, a.relu != 0, a.c_vec, ad, smem);
 }
 
 template <class Cfg, int DT>
@@ -503,7 +506,7 @@ __global__ __launch_bounds__(Cfg::THREADS, 1) void weight_dma(WeightArgs a)
     WeightUnits<Cfg> units;
     units.init(a, 0);
     dma_product<Cfg, DT, false, false>(units, a.p, a.q, a.out, (uint32_t)a.i, (uint32_t)a.j, 0,
-                                       (size_t)a.i * (size_t)a.j, a.j, false, a.c_vec, AdapterArgs{}, a.m, smem);
+                                       (size_t)a.i * (size_t)a.j, a.j, false, a.c_vec, AdapterArgs{}, smem);
 }
 
 }  // namespace gemm_relu_hip

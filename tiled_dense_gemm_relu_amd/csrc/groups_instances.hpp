@@ -14,8 +14,6 @@ void fill_group_width(GroupKernels& t)
     t.rows_tiled[0][W] = (const void*)&rows_tiled<DT, false, VEC>;
     t.rows_tiled[1][W] = (const void*)&rows_tiled<DT, true, VEC>;
     t.weight_tiled[W] = (const void*)&weight_tiled<DT, VEC>;
-    t.shrink[0][W] = (const void*)&adapter_shrink<DT, false, VEC>;
-    t.shrink[1][W] = (const void*)&adapter_shrink<DT, true, VEC>;
 }
 
 // The LDS-DMA tile of a position of kGroupTile.
@@ -62,6 +60,8 @@ GroupKernels make_group_table()
     fill_group_tile<DT, 1>(t);
     fill_group_tile<DT, 2>(t);
     t.mask = (const void*)&relu_mask<DT>;
+    t.shrink[0] = (const void*)&adapter_shrink<DT, false>;
+    t.shrink[1] = (const void*)&adapter_shrink<DT, true>;
     return t;
 }
 

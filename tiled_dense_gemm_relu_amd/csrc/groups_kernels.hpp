@@ -12,6 +12,8 @@
 // row l % 16: see store_cols.
 #pragma once
 
+#include <type_traits>
+
 #include "gemm_relu_kernels.hpp"
 #include "groups_table.hpp"
 
@@ -127,81 +129,221 @@ __device__ __forceinline__ void store_cols(uint16_t* __restrict__ C, floatx4 acc
     }
 }
 
+// ---------------------------------------------------------------- rows of any alignment
+
+// A buffer over `bytes` bytes from p (2-byte aligned) on, from the 4-byte
+// boundary at or before p: `shift` (0 or 2) goes into every offset.  The last
+// dword counts as inside if any byte of it is, which touches no other dword.
+struct AnyRsrc {
+    __amdgpu_buffer_rsrc_t rsrc;
+    uint32_t shift;
+};
+__device__ __forceinline__ AnyRsrc make_any_rsrc(const uint16_t* p, uint32_t bytes)
+{
+    const uint32_t shift = (uint32_t)reinterpret_cast<uintptr_t>(p) & 2u;
+    return AnyRsrc{make_rsrc(reinterpret_cast<const uint8_t*>(p) - shift, bytes ? (bytes + shift + 3u) & ~3u : 0u), shift};
+}
+
+// 8 consecutive elements at an even byte offset, on their way: the 16 bytes
+// from the dword boundary on, and the dword after them, which only elements
+// that start inside a dword need.  chunk_value shifts them into place.
+struct AnyChunk {
+    u32x4 v;
+    uint32_t next, bits;
+};
+__device__ __forceinline__ AnyChunk load_any(const AnyRsrc& r, uint32_t off, bool valid)
+{
+    const uint32_t o = off + r.shift, at = valid ? o & ~3u : kOobOffset;
+    return AnyChunk{__builtin_amdgcn_raw_buffer_load_b128(r.rsrc, at, 0, 0),
+                    __builtin_amdgcn_raw_buffer_load_b32(r.rsrc, (o & 2u) ? at + 16u : kOobOffset, 0, 0), (o & 2u) * 8u};
+}
+__device__ __forceinline__ u32x4 chunk_value(const AnyChunk& c)
+{
+    return u32x4{__builtin_amdgcn_alignbit(c.v[1], c.v[0], c.bits), __builtin_amdgcn_alignbit(c.v[2], c.v[1], c.bits),
+                 __builtin_amdgcn_alignbit(c.v[3], c.v[2], c.bits), __builtin_amdgcn_alignbit(c.next, c.v[3], c.bits)};
+}
+
+// The first `valid` of 8 elements, zeros after them.
+__device__ __forceinline__ u32x4 keep_first(u32x4 v, int valid)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = valid >= 2 * i + 2 ? v[i] : valid == 2 * i + 1 ? v[i] & 0xffffu : 0u;
+    return v;
+}
+
+// 2 W consecutive elements from p (2-byte aligned) on, of which the first
+// `valid` (at least 1) exist: dword loads of dwords that hold one of them.
+template <int W>
+__device__ __forceinline__ void load_dwords_any(const uint16_t* p, int valid, uint32_t (&out)[W])
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    const int odd = (int)(a >> 1) & 1, last = (odd + valid - 1) >> 1;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(a & ~(uintptr_t)3);
+    uint32_t d[W + 1];
+#pragma unroll
+    for (int i = 0; i <= W; ++i) d[i] = q[min(i, last)];
+#pragma unroll
+    for (int i = 0; i < W; ++i) out[i] = __builtin_amdgcn_alignbit(d[i + 1], d[i], 16 * odd);
+}
+
 // ---------------------------------------------------------------- adapters
 
-// 8 consecutive k (from k on, zero past `rank`) of column n of V_i, as an MFMA operand.
-template <bool B_NK>
-__device__ __forceinline__ u32x4 load_v(const AdapterArgs& ad, int id, int n, int N, int k)
-{
-    u32x4 r = {0u, 0u, 0u, 0u};
-    if (n >= N) return r;
-    if constexpr (B_NK) {
-        const uint16_t* p = ad.v + ((size_t)id * (size_t)N + (size_t)n) * (size_t)ad.rank + k;
-        if (ad.v_vec) {                       // rank % 8 == 0: a chunk is wholly in or out
-            if (k < ad.rank) r = *reinterpret_cast<const u32x4*>(p);
-            return r;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (k + e < ad.rank) r[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
-    } else {
-        const uint16_t* p = ad.v + ((size_t)id * (size_t)ad.rank + (size_t)k) * (size_t)N + n;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (k + e < ad.rank) r[e / 2] |= (uint32_t)p[(size_t)e * (size_t)N] << (16 * (e & 1));
-    }
-    return r;
-}
+// Bytes of LDS that add_adapters stages V in, per wave: 32 k of its columns.
+template <int FN>
+constexpr int kAdapterStrip = 32 * FN * 16 * 2;
 
 // Add the low-rank terms of rows m_base .. (those below m_end) to FN x FM blocks
 // of C^T, block (i, j): rows m_base + 16j .. +15, columns n_base + 16i .. +15.
-//  The rows of a 16-row block may belong to several segments.  For each of
-// them the block's product with that segment's adapter is summed in registers
-// of its own, and a lane takes it over only if its row is in the segment: rows
-// never see another request's weights, not even as 0 * infinity.
+//  A row's term is (its intermediate, 32-entry pieces hi + lo times a power of
+// two) @ (its adapter's V).  Rows of a 16-row block may use several adapters:
+// for each of them the block's product is computed in registers of its own, and
+// a lane takes it over only if its row uses that adapter: rows never see
+// another request's weights, not even as 0 * infinity.  (The sums of a block
+// are added to acc once, outside all loops: loops that carry acc through them
+// made the compiler keep it twice, and spill.)
+//  A block whose rows use more than two adapters (single tokens of many
+// requests) would read a V for each, one after the other.  Its lanes compute
+// their own row's 4 columns instead, by fp32 multiply-adds over the rank, with
+// all loads of 8 rank entries in flight together.
 template <int DT, bool B_NK, int FN, int FM>
-__device__ inline void add_adapters(floatx4 (&acc)[FN][FM], const AdapterArgs& ad, int m_base, int m_end, int M,
-                                    int n_base, int N, int lane)
+__device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const AdapterArgs& ad, int m_base, int m_end,
+                                             int n_base, int N, int lane, uint8_t* strip)
 {
-    const int r16 = lane & 15, kg = lane >> 4;
-    int start = 0;
-    for (int s0 = 0; s0 < ad.segments && start < m_end; s0 += 64) {
-        const GroupRows seg = load_group_rows(ad.ends, ad.segments, M, s0, start, lane);
-        const int id = s0 + lane < ad.segments ? ad.ids[s0 + lane] : -1;
-        const bool used = id >= 0 && id < ad.adapters;
+    constexpr int ROW = FN * 32;                       // bytes of a strip's row of k
+    asm volatile("" : "+v"(lane));   // what follows from it is computed here, not kept through the caller's loop
+    const int r16 = lane & 15, kg = lane >> 4, kb = kgroup16(kg);
+    const uint32_t t_row = (uint32_t)ad.rank_pad * 4u, f_row = (uint32_t)ad.rank_pad / 8u;
+    const __amdgpu_buffer_rsrc_t rt = make_rsrc(ad.t, (uint32_t)m_end * t_row), rf = make_rsrc(ad.factor, (uint32_t)m_end * f_row);
 #pragma unroll
-        for (int j = 0; j < FM; ++j) {
-            const int mb = m_base + 16 * j, me = min(mb + 16, m_end);
-            uint64_t todo = __ballot(used && seg.begin < me && seg.end > mb && seg.begin < seg.end);
-            while (todo) {
-                const int l = __builtin_ctzll(todo);
-                todo &= todo - 1;
-                const int lo = __builtin_amdgcn_readlane(seg.begin, l), hi = __builtin_amdgcn_readlane(seg.end, l);
-                const int i_ad = __builtin_amdgcn_readlane(id, l);
-                const int m = mb + r16;
-                const bool in = m >= lo && m < min(hi, m_end);
-                const uint16_t* trow = ad.t + (size_t)m * (size_t)(2 * ad.rank_pad) + 8 * kg;
-                for (int k = 0; k < ad.rank_pad; k += 32) {
-                    u32x4 t_hi = {0u, 0u, 0u, 0u}, t_lo = t_hi;
-                    float f = 0.0f;
-                    if (in) {
-                        t_hi = *reinterpret_cast<const u32x4*>(trow + k);
-                        t_lo = *reinterpret_cast<const u32x4*>(trow + ad.rank_pad + k);
-                        f = ad.factor[(size_t)m * (size_t)(ad.rank_pad / 32) + k / 32];
+    for (int j = 0; j < FM; ++j) {
+        floatx4 sum[FN];
+#pragma unroll
+        for (int i = 0; i < FN; ++i) sum[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        const uint32_t m = (uint32_t)(m_base + 16 * j + r16);
+        const int id = (int)m < m_end ? ad.row_id[m] : -1;
+        const uint32_t all = (uint32_t)__ballot(id >= 0) & 0xffffu;    // rows with an adapter
+        uint32_t more = all;
+        for (int k = 0; k < 2 && more; ++k)
+            more &= ~(uint32_t)__ballot(id == __builtin_amdgcn_readlane(id, __builtin_ctz(more)));
+        uint32_t rest = more ? 0u : all;
+        while (rest) {
+            const int cur = __builtin_amdgcn_readlane(id, __builtin_ctz(rest));
+            rest &= ~(uint32_t)__ballot(id == cur);
+            const bool in = id == cur;
+            const AnyRsrc rv = make_any_rsrc(
+                ad.v + (size_t)cur * (size_t)ad.rank * (size_t)N + (B_NK ? (size_t)n_base * (size_t)ad.rank : 0),
+                (uint32_t)(B_NK ? max(0, min(16 * FN, N - n_base)) : N) * (uint32_t)ad.rank * 2u);
+            for (int k0 = 0; k0 < ad.rank_pad; k0 += 32) {
+                const uint32_t at = in ? m * t_row + (uint32_t)(k0 + 8 * kb) * 2u : kOobOffset;
+                const u32x4 t_hi = __builtin_amdgcn_raw_buffer_load_b128(rt, at, 0, 0);
+                const u32x4 t_lo = __builtin_amdgcn_raw_buffer_load_b128(rt, at, ad.rank_pad * 2, 0);
+                const float f = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                              rf, in ? m * f_row + (uint32_t)k0 / 8u : kOobOffset, 0, 0));
+                u32x4 v[FN];
+                if constexpr (B_NK) {
+                    const int k = k0 + 8 * kb;
+                    AnyChunk c[FN];
+#pragma unroll
+                    for (int i = 0; i < FN; ++i)
+                        c[i] = load_any(rv, ((uint32_t)(16 * i + r16) * (uint32_t)ad.rank + (uint32_t)k) * 2u, k < ad.rank);
+#pragma unroll
+                    for (int i = 0; i < FN; ++i) v[i] = keep_first(chunk_value(c[i]), ad.rank - k);
+                } else {
+                    constexpr int PIECES = ROW / 16, PER_LANE = 32 * PIECES / 64;
+                    AnyChunk c[PER_LANE];
+#pragma unroll
+                    for (int q = 0; q < PER_LANE; ++q) {
+                        const int p = lane + 64 * q, k = p / PIECES, n = n_base + 8 * (p % PIECES);
+                        c[q] = load_any(rv, ((uint32_t)(k0 + k) * (uint32_t)N + (uint32_t)n) * 2u, k0 + k < ad.rank && n < N);
                     }
+#pragma unroll
+                    for (int q = 0; q < PER_LANE; ++q) {
+                        const int p = lane + 64 * q, k = p / PIECES;
+                        *reinterpret_cast<u32x4*>(strip + k * ROW + 16 * ((p % PIECES) ^ b_swizzle<ROW, 16>(k))) = chunk_value(c[q]);
+                    }
+                    const int krow = 8 * kb + (r16 >> 2);
 #pragma unroll
                     for (int i = 0; i < FN; ++i) {
-                        const u32x4 v = load_v<B_NK>(ad, i_ad, n_base + 16 * i + r16, N, k + 8 * kg);
-                        floatx4 p = mfma_16x16x32<DT>(v, t_hi, floatx4{0.0f, 0.0f, 0.0f, 0.0f});
-                        p = mfma_16x16x32<DT>(v, t_lo, p);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[i][j][e] = in ? acc[i][j][e] + f * p[e] : acc[i][j][e];
+                        const int n = 16 * i + 4 * (r16 & 3);
+                        const uint8_t* p = strip + krow * ROW + 16 * ((n >> 3) ^ b_swizzle<ROW, 16>(krow)) + 8 * (r16 & 1);
+                        const u32x2 lo = ds_read_tr16(p), hi = ds_read_tr16(p + 4 * ROW);
+                        v[i] = u32x4{lo.x, lo.y, hi.x, hi.y};
                     }
+                }
+#pragma unroll
+                for (int i = 0; i < FN; ++i) {
+                    floatx4 p = mfma_16x16x32<DT>(v[i], t_hi, floatx4{0.0f, 0.0f, 0.0f, 0.0f});
+                    p = mfma_16x16x32<DT>(v[i], t_lo, p);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum[i][e] = in ? sum[i][e] + f * p[e] : sum[i][e];
                 }
             }
         }
-        start = __builtin_amdgcn_readlane(seg.end, 63);
+        auto lanes = [&](auto fast) __attribute__((always_inline)) {
+            constexpr bool FAST = decltype(fast)::value;
+            const uint16_t* vp = ad.v + (size_t)id * (size_t)ad.rank * (size_t)N;
+            for (int r0 = 0; r0 < ad.rank; r0 += 8) {
+                const uint32_t at = m * t_row + (uint32_t)r0 * 2u;
+                const u32x4 t_hi = __builtin_amdgcn_raw_buffer_load_b128(rt, at, 0, 0);
+                const u32x4 t_lo = __builtin_amdgcn_raw_buffer_load_b128(rt, at, ad.rank_pad * 2, 0);
+                const float f = __builtin_bit_cast(
+                    float, __builtin_amdgcn_raw_buffer_load_b32(rf, m * f_row + (uint32_t)(r0 / 32) * 4u, 0, 0));
+                float z[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    z[e] = f * (to_float<DT>((uint16_t)(t_hi[e / 2] >> (16 * (e & 1)))) +
+                                to_float<DT>((uint16_t)(t_lo[e / 2] >> (16 * (e & 1)))));
+                const int valid = min(8, ad.rank - r0);
+#pragma unroll
+                for (int i = 0; i < FN; ++i) {
+                    const int n = n_base + 16 * i + 4 * kg, cols = min(4, N - n);
+                    if (i % 2 == 0) __builtin_amdgcn_sched_barrier(0);   // loads of two blocks in registers at a time
+                    if (cols <= 0) continue;
+                    if constexpr (B_NK) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            // columns past N repeat the last one: their sums are not stored
+                            const uint16_t* p = vp + (size_t)(n + min(x, cols - 1)) * (size_t)ad.rank + r0;
+                            uint32_t w[4];
+                            if constexpr (FAST) {
+                                const u32x4 q = *reinterpret_cast<const u32x4*>(p);
+                                w[0] = q[0], w[1] = q[1], w[2] = q[2], w[3] = q[3];
+                            } else {
+                                load_dwords_any<4>(p, valid, w);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (e < valid) sum[i][x] += z[e] * to_float<DT>((uint16_t)(w[e / 2] >> (16 * (e & 1))));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint16_t* p = vp + (size_t)(r0 + min(e, valid - 1)) * (size_t)N + n;
+                            uint32_t w[2];
+                            if constexpr (FAST) {
+                                const u32x2 q = *reinterpret_cast<const u32x2*>(p);
+                                w[0] = q[0], w[1] = q[1];
+                            } else {
+                                load_dwords_any<2>(p, cols, w);
+                            }
+                            if (e < valid) {
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    sum[i][x] += z[e] * to_float<DT>((uint16_t)(w[x / 2] >> (16 * (x & 1))));
+                            }
+                        }
+                    }
+                }
+            }
+        };
+        if (more && id >= 0) {
+            if (ad.v_fast)
+                lanes(std::true_type{});
+            else
+                lanes(std::false_type{});
+        }
+#pragma unroll
+        for (int i = 0; i < FN; ++i) acc[i][j] += sum[i];
     }
 }
 
@@ -210,61 +352,120 @@ __device__ inline void add_adapters(floatx4 (&acc)[FN][FM], const AdapterArgs& a
 // (rank_pad = rank rounded up to 32, zeros past rank) are stored as
 //     z = factor[m][block] * (t[m][hi][..] + t[m][lo][..]),
 // factor a power of two of the block's largest |z|, hi the nearest 16-bit value
-// to z / factor (at most 1 in size) and lo that to what is left.
-//  One workgroup per 16 rows of a segment and 32 columns of rank: its 8 waves
-// take the K-steps (32 k) in turn and their sums are added in wave order in LDS.
-template <int DT, bool U_NK, int VEC>
+// to z / factor (at most 1 in size) and lo that to what is left.  row_id[m] is
+// the row's adapter, -1 for none.
+//  One workgroup per 16 rows of a segment, 32 columns of rank and part of K:
+// its 8 waves take pieces of 128 k in turn, each with all its loads in flight
+// at once, and their sums are added in wave order in LDS.  With few rows K is
+// cut into `splits` parts, whose sums go through device memory (device-scope
+// accesses: the parts run on different XCDs); the part that counts itself last
+// adds them in part order and finishes.  Nothing waits for another workgroup.
+template <int DT, bool U_NK>
 __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs a)
 {
-    constexpr int WAVES = kShrinkThreads / 64;
+    constexpr int WAVES = kShrinkThreads / 64, STEPS = kShrinkK / 32, ROW = kShrinkCols * 2;
+    constexpr int kDeviceScope = 16;   // cache policy sc1
     __shared__ float part[WAVES][kShrinkCols][kShrinkRows + 1];
+    __shared__ __attribute__((aligned(16))) uint8_t strips[U_NK ? 16 : WAVES * 32 * ROW];
+    __shared__ int before;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const RowTile tile = find_row_tile(a.ends, a.segments, a.m, kShrinkRows, blockIdx.x, lane);
-    if (tile.group < 0 || tile.group >= a.segments) return;
-    const int id = a.ids[tile.group];
-    if (id < 0 || id >= a.adapters) return;
+    if (tile.group < 0) return;
     const int rows = tile.end - tile.begin, r_base = blockIdx.y * kShrinkCols;
-    const int r16 = lane & 15, kg = lane >> 4;
+    int id = tile.group < a.segments ? a.ids[tile.group] : -1;
+    if (id >= a.adapters || id < 0) id = -1;
+    if (blockIdx.y == 0 && blockIdx.z == 0 && (int)threadIdx.x < rows) a.row_id[tile.begin + threadIdx.x] = id;
+    if (id < 0) return;
+    const int r16 = lane & 15, kb = kgroup16(lane >> 4);
     const size_t k_len = (size_t)a.k, rank = (size_t)a.rank;
 
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)tile.begin * k_len, (uint32_t)rows * (uint32_t)a.k * 2u);
-    const uint16_t* u = a.u + (size_t)id * k_len * rank;
+    const AnyRsrc rx = make_any_rsrc(a.x + (size_t)tile.begin * k_len, (uint32_t)rows * (uint32_t)a.k * 2u);
     // U stored (rank, K): this workgroup's rows r_base .. of U^T
-    const int u_rows = min(kShrinkCols, a.rank - r_base);
-    const __amdgpu_buffer_rsrc_t ru =
-        make_rsrc(u + (U_NK ? (size_t)r_base * k_len : 0), U_NK ? (uint32_t)u_rows * (uint32_t)a.k * 2u : 0u);
+    const AnyRsrc ru = make_any_rsrc(a.u + (size_t)id * k_len * rank + (U_NK ? (size_t)r_base * k_len : 0),
+                                     (uint32_t)(U_NK ? min(kShrinkCols, a.rank - r_base) : a.rank) * (uint32_t)a.k * 2u);
+    uint8_t* strip = strips + (U_NK ? 0 : wave * 32 * ROW);
     floatx4 acc[2] = {floatx4{0}, floatx4{0}};
-    const int steps = (a.k + 31) / 32;
-    for (int s = wave; s < steps; s += WAVES) {
-        const int k = 32 * s + 8 * kg;
-        const u32x4 x = load_chunk<VEC>(rx, ((uint32_t)r16 * (uint32_t)a.k + (uint32_t)k) * 2u,
-                                        [&](int p) { return k + p * VEC < a.k; });
+    const int pieces = (a.k + kShrinkK - 1) / kShrinkK;
+    const int p_end = (int)((int64_t)pieces * (blockIdx.z + 1) / gridDim.z);
+    for (int p = (int)((int64_t)pieces * blockIdx.z / gridDim.z) + wave; p < p_end; p += WAVES) {
+        const int k0 = p * kShrinkK;
+        AnyChunk x[STEPS], u[STEPS][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            u32x4 w = {0u, 0u, 0u, 0u};
-            const int r = 16 * i + r16;
-            if constexpr (U_NK) {
-                w = load_chunk<VEC>(ru, ((uint32_t)r * (uint32_t)a.k + (uint32_t)k) * 2u,
-                                    [&](int p) { return k + p * VEC < a.k; });
-            } else if (r_base + r < a.rank) {
-                const uint16_t* p = u + (size_t)k * rank + r_base + r;
+        for (int s = 0; s < STEPS; ++s) {
+            const int k = k0 + 32 * s + 8 * kb;
+            x[s] = load_any(rx, ((uint32_t)r16 * (uint32_t)a.k + (uint32_t)k) * 2u, k < a.k);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (k + e < a.k) w[e / 2] |= (uint32_t)p[(size_t)e * rank] << (16 * (e & 1));
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (U_NK) {
+                    u[s][i] = load_any(ru, ((uint32_t)(16 * i + r16) * (uint32_t)a.k + (uint32_t)k) * 2u, k < a.k);
+                } else {
+                    const int kr = k0 + 32 * s + 16 * i + (lane >> 2), r = r_base + 8 * (lane & 3);
+                    u[s][i] = load_any(ru, ((uint32_t)kr * (uint32_t)a.rank + (uint32_t)r) * 2u, kr < a.k && r < a.rank);
+                }
             }
-            acc[i] = mfma_16x16x32<DT>(w, x, acc[i]);
+        }
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int valid = a.k - (k0 + 32 * s + 8 * kb);
+            const u32x4 xv = keep_first(chunk_value(x[s]), valid);
+            u32x4 uv[2];
+            if constexpr (U_NK) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) uv[i] = keep_first(chunk_value(u[s][i]), valid);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int kr = 16 * i + (lane >> 2);
+                    *reinterpret_cast<u32x4*>(strip + kr * ROW + 16 * ((lane & 3) ^ b_swizzle<ROW, 16>(kr))) = chunk_value(u[s][i]);
+                }
+                const int kr = 8 * kb + (r16 >> 2);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 16 * i + 4 * (r16 & 3);
+                    const uint8_t* q = strip + kr * ROW + 16 * ((r >> 3) ^ b_swizzle<ROW, 16>(kr)) + 8 * (r16 & 1);
+                    const u32x2 lo = ds_read_tr16(q), hi = ds_read_tr16(q + 4 * ROW);
+                    uv[i] = u32x4{lo.x, lo.y, hi.x, hi.y};
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) acc[i] = mfma_16x16x32<DT>(uv[i], xv, acc[i]);
         }
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) part[wave][16 * i + 4 * kg + e][r16] = acc[i][e];
+        for (int e = 0; e < 4; ++e) part[wave][16 * i + 4 * (lane >> 4) + e][r16] = acc[i][e];
     __syncthreads();
     // 512 threads: 16 rows x 32 columns; a row's 32 columns are one half of a wave
     const int row = threadIdx.x >> 5, col = threadIdx.x & 31;
     float z = 0.0f;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) z += part[w][col][row];
+    if (gridDim.z > 1) {
+        const int splits = (int)gridDim.z, slot = (int)(blockIdx.x * gridDim.y + blockIdx.y);
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.part + (size_t)slot * (size_t)splits * kShrinkThreads,
+                                                    (uint32_t)splits * kShrinkThreads * 4u);
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, z), rs,
+                                              (blockIdx.z * kShrinkThreads + threadIdx.x) * 4u, 0, kDeviceScope);
+        wait_vmcnt<0>();               // this wave's sums have reached device scope
+        __syncthreads();
+        if (threadIdx.x == 0)
+            before = __hip_atomic_fetch_add(a.counters + slot, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (before != splits - 1) return;
+        asm volatile("" ::: "memory");   // the loads below stay after the count that allowed them
+        z = 0.0f;
+        for (int s0 = 0; s0 < splits; s0 += 4) {
+            float o[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s)   // parts past the last are out of range: zero
+                o[s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                     rs, ((uint32_t)(s0 + s) * kShrinkThreads + threadIdx.x) * 4u, 0, kDeviceScope));
+#pragma unroll
+            for (int s = 0; s < 4; ++s) z += o[s];
+        }
+        if (threadIdx.x == 0) __hip_atomic_store(a.counters + slot, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
     // columns past rank are zero, whatever X holds (0 * infinity is not)
     z = r_base + col < a.rank ? z * a.scales[id] : 0.0f;
     float top = fabsf(z);
@@ -421,7 +622,8 @@ __global__ __launch_bounds__(256) void rows_tiled(RowsArgs a, AdapterArgs ad)
         StagedOperand<!B_NK, VEC> cols{B_NK ? b + (size_t)n0 * k_len : b, (uint32_t)(B_NK ? a.k : a.n),
                                        B_NK ? 0 : n0, B_NK ? min(128, a.n - n0) : a.n, {}};
         staged_product<DT>(acc, rows, cols, 0, a.k, smem);
-        if (ad.v) add_adapters<DT, B_NK>(acc, ad, m_base, tile.end, a.m, n_base, a.n, lane);
+        if (ad.v)   // (every wave is past its last read of LDS)
+            add_adapters<DT, B_NK>(acc, ad, m_base, tile.end, n_base, a.n, lane, smem + wave * kAdapterStrip<4>);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)

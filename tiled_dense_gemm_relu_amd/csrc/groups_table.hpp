@@ -18,16 +18,16 @@ struct RowsArgs {
     int c_vec;             // rows of C allow 2: 16-byte, 1: 8-byte, 0: 2-byte stores
 };
 
-// The low-rank term of each row (v == nullptr: none).  Row m's intermediate is
-// t[m][hi | lo][rank_pad] times factor[m][rank_pad / 32], see adapter_shrink.
+// The low-rank term of each row (v == nullptr: none).  Row m's adapter is
+// row_id[m] (-1: none) and its intermediate t[m][hi | lo][rank_pad] times
+// factor[m][rank_pad / 32], see adapter_shrink.
 struct AdapterArgs {
     const uint16_t* v;     // (adapters, rank, N) or (adapters, N, rank)
     const uint16_t* t;
     const float* factor;
-    const int* ends;
-    const int* ids;
-    int segments, adapters, rank, rank_pad;
-    int v_vec;             // V's rows allow 16-byte loads
+    const int* row_id;
+    int rank, rank_pad;
+    int v_fast;            // V's rows allow the widest loads of a lane of its own: 8 bytes (4 columns), or 16 (8 rank entries)
 };
 
 struct ShrinkArgs {
@@ -38,6 +38,9 @@ struct ShrinkArgs {
     const int* ids;
     uint16_t* t;
     float* factor;
+    int* row_id;
+    float* part;           // [row tile][32 columns][split][16 x 32] sums
+    int* counters;         // one for each row tile and 32 columns
     int m, k, segments, adapters, rank, rank_pad;
 };
 
@@ -62,7 +65,7 @@ struct MaskArgs {
 // Load widths with an instance of the register-staged kernels, widest first.
 constexpr int kNumLoadWidths = 4;
 constexpr int kLoadWidths[kNumLoadWidths] = {8, 4, 2, 1};
-constexpr int kShrinkRows = 16, kShrinkCols = 32, kShrinkThreads = 512;
+constexpr int kShrinkRows = 16, kShrinkCols = 32, kShrinkK = 128, kShrinkThreads = 512;
 
 // Square LDS-DMA tiles, by GEMM_RELU_GROUPS_DMA_* order, and their workgroups.
 constexpr int kNumGroupTiles = 3;
@@ -76,7 +79,7 @@ struct GroupKernels {
     const void* rows_tiled[2][kNumLoadWidths];    // [B layout][load width]
     const void* weight_tiled[kNumLoadWidths];
     const void* mask;
-    const void* shrink[2][kNumLoadWidths];        // [U layout][load width of X and of U^T]
+    const void* shrink[2];                        // [U layout]
 };
 
 const GroupKernels& group_kernels_f16();
