@@ -15,7 +15,6 @@ namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 20;
 constexpr int64_t kMaxGroups = 65535;
-constexpr int64_t kMaxRank = 256;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
@@ -119,13 +118,21 @@ int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config,
     a.c_vec = store_width(a.c, a.n);
     const int w = load_width({{a.a, a.k}, {a.b, b_layout == GEMM_RELU_B_NK ? a.k : a.n}});
     if (w > 0) config = GEMM_RELU_GROUPS_TILED;
+    // With adapters the 256 tile cuts its rows at the segments' ends and streams V
+    // like B; the others take rows of many segments.
+    const auto auto_config = [&](int64_t groups) {
+        const int64_t used = std::min(groups, (int64_t)a.m), rows = a.m / used;
+        return dma_config(rows, used * ceil_div(rows, 256) * ceil_div(a.n, 256), used * ceil_div(rows, 128) * ceil_div(a.n, 128));
+    };
     if (config == GEMM_RELU_GROUPS_AUTO) {
-        const int64_t used = std::min(a.groups, a.m), rows = a.m / used;
-        config = dma_config(rows, used * ceil_div(rows, 256) * ceil_div(a.n, 256), used * ceil_div(rows, 128) * ceil_div(a.n, 128));
+        config = auto_config(ad.v ? ad.segments : a.groups);
+        if (ad.v && config != GEMM_RELU_GROUPS_DMA_256) config = std::max<int>(auto_config(1), GEMM_RELU_GROUPS_DMA_128);
     }
-    if (config == GEMM_RELU_GROUPS_DMA_256 && ad.v) config = GEMM_RELU_GROUPS_DMA_128;
+    const bool v_rows = b_layout == GEMM_RELU_B_KN || ad.rank % 8 == 0;
+    if (config == GEMM_RELU_GROUPS_DMA_256 && ad.v && !(v_rows && aligned(ad.v, 16))) config = GEMM_RELU_GROUPS_DMA_128;
+    const bool first = config == GEMM_RELU_GROUPS_DMA_256 && ad.v;
     const int64_t rows = config == GEMM_RELU_GROUPS_TILED ? 128 : kGroupTile[config - 1];
-    const int64_t tiles = most_row_tiles(a.m, a.groups, rows) * ceil_div(a.n, rows);
+    const int64_t tiles = most_row_tiles(a.m, first ? ad.segments : a.groups, rows) * ceil_div(a.n, rows);
     if (tiles > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
     void* args[] = {&a, &ad};
     if (config == GEMM_RELU_GROUPS_TILED)
@@ -162,18 +169,17 @@ struct AdapterSpace {
 AdapterSpace adapter_space(int64_t M, int64_t K, int64_t rank, int64_t segments)
 {
     AdapterSpace s;
-    s.rank_pad = round_up(rank, 32);
+    s.rank_pad = round_up(rank, 64);
     s.tiles = most_row_tiles(M, segments, kShrinkRows);
-    const int64_t slots = s.tiles * (s.rank_pad / kShrinkCols);
-    s.splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(K, 8 * kShrinkK), slots ? 512 / slots : 1));
+    s.splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(K, 8 * kShrinkK), s.tiles ? 512 / s.tiles : 1));
     s.t = GEMM_RELU_GROUPS_COUNTER_BYTES;
     s.factor = s.t + round_up(M * 2 * s.rank_pad * 2, 256);
-    s.row_id = s.factor + round_up(M * (s.rank_pad / 32) * 4, 256);
+    s.row_id = s.factor + round_up(M * 4, 256);
     s.part = s.row_id + round_up(M * 4, 256);
-    s.bytes = s.part + (s.splits > 1 ? slots * s.splits * kShrinkThreads * 4 : 0);
+    s.bytes = s.part + (s.splits > 1 ? s.tiles * s.splits * ceil_div(rank, kShrinkCols) * kShrinkThreads * 4 : 0);
     return s;
 }
-static_assert(512 * 4 <= GEMM_RELU_GROUPS_COUNTER_BYTES, "a counter for each slot of a split sum");
+static_assert(512 * 4 <= GEMM_RELU_GROUPS_COUNTER_BYTES, "a counter for each row tile of a split sum");
 
 }  // namespace
 }  // namespace gemm_relu_hip
@@ -313,13 +319,13 @@ int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* 
                   reinterpret_cast<float*>(ws + space.part), reinterpret_cast<int*>(ws), (int)M, (int)K, (int)segments,
                   (int)adapters, (int)rank, (int)space.rank_pad};
     void* args[] = {&sh};
-    rc = enqueue(kernels(dtype).shrink[b_layout], dim3((unsigned)space.tiles, (unsigned)(space.rank_pad / kShrinkCols), (unsigned)space.splits),
-                 kShrinkThreads, args, s);
+    rc = enqueue(kernels(dtype).shrink[b_layout], dim3((unsigned)space.tiles, (unsigned)space.splits), kShrinkThreads, args, s);
     if (rc != GEMM_RELU_OK) return rc;
     RowsArgs a{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(W), static_cast<uint16_t*>(C), nullptr,
                (int)M, (int)N, (int)K, 1, relu, 0};
     const bool v_fast = b_layout == GEMM_RELU_B_NK ? rank % 8 == 0 && aligned(V, 16) : N % 4 == 0 && aligned(V, 8);
-    AdapterArgs ad{static_cast<const uint16_t*>(V), t, factor, row_id, (int)rank, (int)space.rank_pad, v_fast};
+    AdapterArgs ad{static_cast<const uint16_t*>(V), t, factor, row_id, ends, ids, (int)segments, (int)adapters, (int)rank,
+                   (int)space.rank_pad, v_fast};
     return launch_rows(a, ad, dtype, b_layout, config_id, cus, s);
 }
 

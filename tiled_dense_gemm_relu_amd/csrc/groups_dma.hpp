@@ -43,8 +43,9 @@ struct GroupDmaConfig {
 
 // One output tile: rows m0 .. m_end - 1 (at most BM) and columns n0 .. of C,
 // summed over k0 .. k_end - 1, with the weights (or output) of `group`.
+// adapter >= 0: the sum starts from the rows' low-rank terms with that adapter.
 struct DmaUnit {
-    int m0, m_end, n0, group, k0, k_end;
+    int m0, m_end, n0, group, k0, k_end, adapter;
 };
 
 // The rows' products: unit -> row tile of a group (from the row table) and
@@ -54,28 +55,33 @@ template <class Cfg>
 struct RowUnits {
     const int* ends;
     int groups, M, K, tiles_n, lane;
-    int end, incl;           // per lane, groups <= 64
+    int listed;              // groups with tiles: all, and with `rest` the rows of none as one more
+    int end, incl;           // per lane, at most 64 groups
     int row_tiles, rows;     // tiles of all groups; rows in groups
+    const int* ids;          // the groups' adapters, or nullptr
+    int adapters;
 
     __device__ __forceinline__ int tiles_of(const GroupRows& r) const { return (r.end - r.begin + Cfg::BM - 1) / Cfg::BM; }
 
-    __device__ __forceinline__ void init(const RowsArgs& a, int lane_)
+    __device__ __forceinline__ void init(const RowsArgs& a, const int* ends_, int groups_, bool rest, int lane_)
     {
-        ends = a.ends;
-        groups = a.groups;
+        ends = ends_;
+        groups = groups_;
+        listed = groups + (rest ? 1 : 0);
+        ids = nullptr;
         M = a.m;
         K = a.k;
         tiles_n = (a.n + Cfg::BN - 1) / Cfg::BN;
         lane = lane_;
         row_tiles = 0;
         rows = 0;
-        for (int g0 = 0; g0 < groups; g0 += 64) {
+        for (int g0 = 0; g0 < listed; g0 += 64) {
             const GroupRows r = load_group_rows(ends, groups, M, g0, rows, lane);
-            const bool real = g0 + lane < groups;
+            const bool real = g0 + lane < listed;
             end = r.end;
             incl = row_tiles + wave_scan_sum(real ? tiles_of(r) : 0, lane);
             row_tiles = __builtin_amdgcn_readlane(incl, 63);
-            rows = __builtin_amdgcn_readlane(r.end, min(groups - 1 - g0, 63));
+            rows = __builtin_amdgcn_readlane(r.end, min(listed - 1 - g0, 63));
         }
     }
     __device__ __forceinline__ int total() const { return row_tiles * tiles_n; }
@@ -83,16 +89,21 @@ struct RowUnits {
     {
         int tm, tn;
         tile_coords(u, row_tiles, tiles_n, Cfg::GROUP_M, tm, tn);
-        if (groups <= 64) {
+        if (listed <= 64) {
             const int l = __builtin_ctzll(__ballot(tm < incl));
             const int e = __builtin_amdgcn_readlane(end, l);
             const int b = l ? __builtin_amdgcn_readlane(end, l - 1) : 0;
             const int before = l ? __builtin_amdgcn_readlane(incl, l - 1) : 0;
             const int m0 = b + (tm - before) * Cfg::BM;
-            return DmaUnit{m0, min(m0 + Cfg::BM, e), tn * Cfg::BN, l, 0, K};
+            return DmaUnit{m0, min(m0 + Cfg::BM, e), tn * Cfg::BN, l, 0, K, adapter(l)};
         }
         const RowTile t = find_row_tile(ends, groups, M, Cfg::BM, tm, lane);
-        return DmaUnit{t.begin, t.end, tn * Cfg::BN, t.group, 0, K};
+        return DmaUnit{t.begin, t.end, tn * Cfg::BN, t.group, 0, K, adapter(t.group)};
+    }
+    __device__ __forceinline__ int adapter(int group) const
+    {
+        const int id = ids && group < groups ? ids[group] : -1;
+        return id < adapters ? id : -1;
     }
 };
 
@@ -124,7 +135,7 @@ struct WeightUnits {
         tile_coords(pid - g * tiles, tiles_i, tiles_j, Cfg::GROUP_M, ti, tj, false);
         const int b = g ? min(max(ends[g - 1], 0), M) : 0;
         const int e = max(min(max(ends[g], 0), M), b);
-        return DmaUnit{ti * Cfg::BM, I, tj * Cfg::BN, g, b, e};
+        return DmaUnit{ti * Cfg::BM, I, tj * Cfg::BN, g, b, e, -1};
     }
 };
 
@@ -174,7 +185,14 @@ __device__ __forceinline__ void store_rows_staged(uint16_t* __restrict__ C, cons
 // The product loop.  A's rows are lda long, B's ldb; `b_group` and `c_group`
 // are the elements from one group's B and C to the next.  KTAIL: k_end need not
 // be a multiple of 64 for k-contiguous operands (but of 8).
-template <class Cfg, int DT, bool KTAIL, bool ADAPT, class Units>
+//  With adapters, kAdaptAfter adds a finished tile's low-rank terms to its sums
+// (add_adapters: tiles may hold rows of many segments).  kAdaptFirst is for
+// tiles cut at the segments' ends: before its K-steps over A and B a tile
+// streams K-steps over the intermediates (hi, then lo) and V through the same
+// ring, multiplies its sums by the rows' factors, and goes on from them, so
+// the low-rank product costs its K-steps and nothing else.
+enum { kAdaptNone = 0, kAdaptAfter = 1, kAdaptFirst = 2 };
+template <class Cfg, int DT, bool KTAIL, int ADAPT, class Units>
 __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* __restrict__ A,
                                             const uint16_t* __restrict__ B, uint16_t* __restrict__ C, uint32_t lda,
                                             uint32_t ldb, size_t b_group, size_t c_group, int N, bool relu, int c_vec,
@@ -183,7 +201,8 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
     constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK, S = Cfg::STAGES;
     constexpr int QA = Cfg::QA, QB = Cfg::QB, NQ = Cfg::NQ, FM = Cfg::FM, FN = Cfg::FN;
     constexpr int A_ROW = Cfg::A_ROW, B_ROW = Cfg::B_ROW, NKS = BK / 32;
-    constexpr bool AK = Cfg::A_KMAJOR, BKM = Cfg::B_KMAJOR, WS = Cfg::PRODUCERS > 0;
+    constexpr bool AK = Cfg::A_KMAJOR, BKM = Cfg::B_KMAJOR, WS = Cfg::PRODUCERS > 0, FIRST = ADAPT == kAdaptFirst;
+    static_assert(!FIRST || (KTAIL && !AK), "the rank need not be a multiple of BK");
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
@@ -197,7 +216,8 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
         const DmaUnit u = units.unit((int)blockIdx.x + i * (int)gridDim.x);
         return DmaUnit{__builtin_amdgcn_readfirstlane(u.m0),    __builtin_amdgcn_readfirstlane(u.m_end),
                        __builtin_amdgcn_readfirstlane(u.n0),    __builtin_amdgcn_readfirstlane(u.group),
-                       __builtin_amdgcn_readfirstlane(u.k0),    __builtin_amdgcn_readfirstlane(u.k_end)};
+                       __builtin_amdgcn_readfirstlane(u.k0),    __builtin_amdgcn_readfirstlane(u.k_end),
+                       __builtin_amdgcn_readfirstlane(u.adapter)};
     };
 
     const uint32_t lds_base = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)smem);
@@ -225,52 +245,68 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
             pos = (((byte % ROW) / 16) ^ a_swizzle<ROW>(row)) * 8;
         voff = pos < limit ? ((uint32_t)row * ld + (uint32_t)pos) * 2u : kOobOffset;
     };
+    uint32_t f_lda = lda, f_ldb = ldb;      // row lengths of the step's operands
     auto a_pieces = [&](int l, int limit) {
 #pragma unroll
         for (int q = 0; q < PA; ++q)
-            piece(l, q, QA, std::integral_constant<bool, AK>{}, std::integral_constant<int, A_ROW>{}, lda, limit,
+            piece(l, q, QA, std::integral_constant<bool, AK>{}, std::integral_constant<int, A_ROW>{}, f_lda, limit,
                   a_voff[q], a_pos[q]);
     };
     auto b_pieces = [&](int l, int limit) {
 #pragma unroll
         for (int q = 0; q < PB; ++q)
-            piece(l, q, QB, std::integral_constant<bool, BKM>{}, std::integral_constant<int, B_ROW>{}, ldb, limit,
+            piece(l, q, QB, std::integral_constant<bool, BKM>{}, std::integral_constant<int, B_ROW>{}, f_ldb, limit,
                   b_voff[q], b_pos[q]);
     };
-    if constexpr (!AK) a_pieces(lane, BK);
-    if constexpr (!BKM) b_pieces(lane, BK);
+    if constexpr (!AK && !FIRST) a_pieces(lane, BK);
+    if constexpr (!BKM && !FIRST) b_pieces(lane, BK);
 
     // The load side.  f_left: k still to load of the unit; past the last unit it
     // is 0 and the descriptors are empty, so nothing is fetched.  (All of it is
     // set on every path, without branches, which keeps it in scalar registers.)
-    int f_unit = 0, f_k = 0, f_left = 0, f_steps = 0;
+    // f_rank: K-steps over the intermediates and V still to load (kAdaptFirst).
+    int f_unit = 0, f_k = 0, f_left = 0, f_steps = 0, f_rank = 0;
     // k-contiguous: the tile's rows and how many there are; k-major: the step's first row.
     const uint16_t *f_ap = A, *f_bp = B;
     int f_arows = 0, f_brows = 0;
-    auto fill_setup = [&]() {
+    int f_kb = 0, f_left_b = 0;       // B's place and what it has left, where they differ from f_k and f_left
+    const int rank_steps = FIRST ? 2 * ad.rank_pad / BK : 0;
+    auto fill_setup = [&](bool start) {
         const int live = f_unit < n_units ? 1 : 0;
         const DmaUnit u = unit_at(live ? f_unit : n_units - 1);
+        const bool low = FIRST && start && live && u.adapter >= 0;
+        f_rank = low ? rank_steps : 0;
         f_k = u.k0;
         f_left = live * (u.k_end - u.k0);
-        const uint16_t* b = B + (size_t)u.group * b_group;
+        const uint16_t *a = A, *b = B + (size_t)u.group * b_group;
+        if constexpr (FIRST) {
+            f_kb = f_k;
+            f_left_b = low ? ad.rank : f_left;
+            f_lda = low ? 2u * (uint32_t)ad.rank_pad : lda;
+            a = low ? ad.t : A;
+            b = low ? ad.v + (size_t)u.adapter * (size_t)ad.rank * (size_t)N : B;
+            if constexpr (!BKM) f_ldb = low ? (uint32_t)ad.rank : ldb;
+        }
         int l = lane;
         asm volatile("" : "+v"(l));   // computed here for each tile, not kept in registers in between
         if constexpr (AK) {
-            f_ap = A + (size_t)u.k0 * lda + u.m0;
+            f_ap = a + (size_t)u.k0 * lda + u.m0;
             a_pieces(l, u.m_end - u.m0);
         } else {
-            f_ap = A + (size_t)u.m0 * lda;
+            f_ap = a + (size_t)u.m0 * f_lda;
             f_arows = live * (u.m_end - u.m0);
+            if constexpr (FIRST) a_pieces(l, BK);
         }
         if constexpr (BKM) {
             f_bp = b + (size_t)u.k0 * ldb + u.n0;
             b_pieces(l, N - u.n0);
         } else {
-            f_bp = b + (size_t)u.n0 * ldb;
+            f_bp = b + (size_t)u.n0 * f_ldb;
             f_brows = live * min(BN, N - u.n0);
+            if constexpr (FIRST) b_pieces(l, BK);
         }
     };
-    fill_setup();
+    fill_setup(true);
     // The descriptor of the rows from `skip` on of a stage with `rows` rows.
     auto rows_from = [](const uint16_t* p, int rows, int skip, uint32_t ld) {
         const int32x4_t r = rsrc_words(p + (size_t)skip * ld, (uint32_t)max(0, rows - skip) * ld * 2u);
@@ -283,29 +319,45 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
             const uint32_t vo = a_voff[q % PA];
             if constexpr (AK)
                 dma_b128(rows_from(f_ap, min(BK, f_left), q / 2 * A_PAIR, lda), lds, vo, 0u);
-            else
-                dma_b128(rows_from(f_ap, f_arows, q / 2 * A_PAIR, lda), lds,
-                         KTAIL && a_pos[q % PA] >= f_left ? kOobOffset : vo, (uint32_t)f_k * 2u);
+            else   // (the intermediates' rows are whole K-steps)
+                dma_b128(rows_from(f_ap, f_arows, q / 2 * A_PAIR, f_lda), lds,
+                         KTAIL && !(FIRST && f_rank) && a_pos[q % PA] >= f_left ? kOobOffset : vo, (uint32_t)f_k * 2u);
         } else {
             const int p = q - QA;
+            const int left = FIRST ? f_left_b : f_left;
             const uint32_t lds = lds_base + Cfg::B_REGION + slot * Cfg::B_STAGE + (dwave * QB + p) * 1024;
             const uint32_t vo = b_voff[p % PB];
             if constexpr (BKM)
-                dma_b128(rows_from(f_bp, min(BK, f_left), p / 2 * B_PAIR, ldb), lds, vo, 0u);
+                dma_b128(rows_from(f_bp, min(BK, left), p / 2 * B_PAIR, ldb), lds, vo, 0u);
             else
-                dma_b128(rows_from(f_bp, f_brows, p / 2 * B_PAIR, ldb), lds,
-                         KTAIL && b_pos[p % PB] >= f_left ? kOobOffset : vo, (uint32_t)f_k * 2u);
+                dma_b128(rows_from(f_bp, f_brows, p / 2 * B_PAIR, f_ldb), lds,
+                         KTAIL && b_pos[p % PB] >= left ? kOobOffset : vo, (uint32_t)(FIRST ? f_kb : f_k) * 2u);
         }
     };
     auto fill_advance = [&]() {
         if (f_unit >= n_units) return;
         ++f_steps;
-        if (f_left <= BK) {
+        if (FIRST && f_rank > 0) {
+            if (--f_rank == 0) {
+                fill_setup(false);
+                return;
+            }
+            // V's K-steps once for hi, once again for lo
+            const int next = f_kb + BK < ad.rank_pad ? f_kb + BK : 0;
+            if constexpr (BKM) f_bp += (ptrdiff_t)(next - f_kb) * (ptrdiff_t)ldb;
+            f_k += BK;
+            f_kb = next;
+            f_left_b = ad.rank - next;
+        } else if (f_left <= BK) {
             ++f_unit;
-            fill_setup();
+            fill_setup(true);
         } else {
             f_k += BK;
             f_left -= BK;
+            if constexpr (FIRST) {
+                f_kb = f_k;
+                f_left_b = f_left;
+            }
             if constexpr (AK) f_ap += (size_t)BK * lda;
             if constexpr (BKM) f_bp += (size_t)BK * ldb;
         }
@@ -404,7 +456,7 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
 
     int c_unit = 0, slot = 0;
     DmaUnit c = unit_at(0);
-    int c_k = c.k0;
+    int c_k = c.k0 - (FIRST && c.adapter >= 0 ? rank_steps * BK : 0);
     while (true) {
         const int slot_next = (slot + 1) & (S - 1);
         auto step_barrier = [&]() {
@@ -444,9 +496,25 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
         }
         slot = slot_next;
         c_k += BK;
+        if (FIRST && c_k == 0 && c.adapter >= 0) {
+            int l = j16;
+            asm volatile("" : "+v"(l));
+            float f[FM];
+#pragma unroll
+            for (int j = 0; j < FM; ++j) {
+                const int m = c.m0 + wm * Cfg::WTM + 16 * j + l;
+                f[j] = m < c.m_end ? ad.factor[m] : 1.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+#pragma unroll
+                for (int i = 0; i < FN; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] *= f[j];
+        }
         if (c_k >= c.k_end) {
             const int m_base = c.m0 + wm * Cfg::WTM, n_base = c.n0 + wn * Cfg::WTN;
-            if constexpr (ADAPT)
+            if constexpr (ADAPT == kAdaptAfter)
                 add_adapters<DT, !BKM>(acc, ad, m_base, c.m_end, n_base, N, lane,
                                                   smem + Cfg::LDS_BYTES + wave * kAdapterStrip<FN>);
             uint16_t* out = C + (size_t)c.group * c_group;
@@ -469,8 +537,8 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
             if (++c_unit >= n_units) break;
             clear();
             c = unit_at(c_unit);
-            c_k = c.k0;
-            if constexpr (ADAPT) {   // the registers of the next fragments were free meanwhile
+            c_k = c.k0 - (FIRST && c.adapter >= 0 ? rank_steps * BK : 0);
+            if constexpr (ADAPT == kAdaptAfter) {   // the registers of the next fragments were free meanwhile
 #pragma unroll
                 for (int u = 0; u < NF; ++u) read_unit(0, slot, 0, u);
             }
@@ -488,15 +556,23 @@ __device__ __forceinline__ void zero_rows(const RowsArgs& a, int first)
     for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < count; i += stride) p[i] = 0;
 }
 
-template <class Cfg, int DT, bool KTAIL, bool ADAPT>
+template <class Cfg, int DT, bool KTAIL, int ADAPT>
 __global__ __launch_bounds__(Cfg::THREADS, 1) void rows_dma(RowsArgs a, AdapterArgs ad)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES + Cfg::C_STAGE_BYTES + (ADAPT ? Cfg::ADAPT_BYTES : 0)];
+    __shared__ __attribute__((aligned(1024))) uint8_t
+        smem[Cfg::LDS_BYTES + Cfg::C_STAGE_BYTES + (ADAPT == kAdaptAfter ? Cfg::ADAPT_BYTES : 0)];
     RowUnits<Cfg> units;
-    units.init(a, threadIdx.x & 63);
-    if (units.rows < a.m) zero_rows(a, units.rows);
+    if constexpr (ADAPT == kAdaptFirst) {
+        units.init(a, ad.ends, ad.segments, true, threadIdx.x & 63);
+        units.ids = ad.ids;
+        units.adapters = ad.adapters;
+    } else {
+        units.init(a, a.ends, a.groups, false, threadIdx.x & 63);
+        if (units.rows < a.m) zero_rows(a, units.rows);
+    }
     dma_product<Cfg, DT, KTAIL, ADAPT>(units, a.a, a.b, a.c, (uint32_t)a.k, (uint32_t)(Cfg::B_KMAJOR ? a.n : a.k),
-                                       (size_t)a.k * (size_t)a.n, 0, a.n, a.relu != 0, a.c_vec, ad, smem);
+                                       ADAPT == kAdaptFirst ? 0 : (size_t)a.k * (size_t)a.n, 0, a.n, a.relu != 0, a.c_vec,
+                                       ad, smem);
 }
 
 template <class Cfg, int DT>
@@ -505,7 +581,7 @@ __global__ __launch_bounds__(Cfg::THREADS, 1) void weight_dma(WeightArgs a)
     __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES + Cfg::C_STAGE_BYTES];
     WeightUnits<Cfg> units;
     units.init(a, 0);
-    dma_product<Cfg, DT, false, false>(units, a.p, a.q, a.out, (uint32_t)a.i, (uint32_t)a.j, 0,
+    dma_product<Cfg, DT, false, kAdaptNone>(units, a.p, a.q, a.out, (uint32_t)a.i, (uint32_t)a.j, 0,
                                        (size_t)a.i * (size_t)a.j, a.j, false, a.c_vec, AdapterArgs{}, smem);
 }
 

@@ -32,11 +32,13 @@ void fill_rows_dma(GroupKernels& t)
     using Cfg = typename GroupTile<T, false, !B_NK>::Cfg;
     static_assert(Cfg::BM == kGroupTile[T] && Cfg::BN == kGroupTile[T] && Cfg::THREADS == kGroupThreads[T],
                   "host tile table out of date");
-    t.rows_dma[T][B_NK][0][0] = (const void*)&rows_dma<Cfg, DT, false, false>;
-    t.rows_dma[T][B_NK][1][0] = (const void*)&rows_dma<Cfg, DT, true, false>;
-    if constexpr (T > 0) {
-        t.rows_dma[T][B_NK][0][1] = (const void*)&rows_dma<Cfg, DT, false, true>;
-        t.rows_dma[T][B_NK][1][1] = (const void*)&rows_dma<Cfg, DT, true, true>;
+    t.rows_dma[T][B_NK][0][0] = (const void*)&rows_dma<Cfg, DT, false, kAdaptNone>;
+    t.rows_dma[T][B_NK][1][0] = (const void*)&rows_dma<Cfg, DT, true, kAdaptNone>;
+    if constexpr (T == 0) {
+        t.rows_dma[T][B_NK][0][1] = t.rows_dma[T][B_NK][1][1] = (const void*)&rows_dma<Cfg, DT, true, kAdaptFirst>;
+    } else {
+        t.rows_dma[T][B_NK][0][1] = (const void*)&rows_dma<Cfg, DT, false, kAdaptAfter>;
+        t.rows_dma[T][B_NK][1][1] = (const void*)&rows_dma<Cfg, DT, true, kAdaptAfter>;
     }
 }
 

@@ -194,8 +194,8 @@ constexpr int kAdapterStrip = 32 * FN * 16 * 2;
 
 // Add the low-rank terms of rows m_base .. (those below m_end) to FN x FM blocks
 // of C^T, block (i, j): rows m_base + 16j .. +15, columns n_base + 16i .. +15.
-//  A row's term is (its intermediate, 32-entry pieces hi + lo times a power of
-// two) @ (its adapter's V).  Rows of a 16-row block may use several adapters:
+//  A row's term is (its intermediate, hi + lo times a power of two) @ (its
+// adapter's V).  Rows of a 16-row block may use several adapters:
 // for each of them the block's product is computed in registers of its own, and
 // a lane takes it over only if its row uses that adapter: rows never see
 // another request's weights, not even as 0 * infinity.  (The sums of a block
@@ -212,8 +212,8 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
     constexpr int ROW = FN * 32;                       // bytes of a strip's row of k
     asm volatile("" : "+v"(lane));   // what follows from it is computed here, not kept through the caller's loop
     const int r16 = lane & 15, kg = lane >> 4, kb = kgroup16(kg);
-    const uint32_t t_row = (uint32_t)ad.rank_pad * 4u, f_row = (uint32_t)ad.rank_pad / 8u;
-    const __amdgpu_buffer_rsrc_t rt = make_rsrc(ad.t, (uint32_t)m_end * t_row), rf = make_rsrc(ad.factor, (uint32_t)m_end * f_row);
+    const uint32_t t_row = (uint32_t)ad.rank_pad * 4u;
+    const __amdgpu_buffer_rsrc_t rt = make_rsrc(ad.t, (uint32_t)m_end * t_row);
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
         floatx4 sum[FN];
@@ -221,6 +221,7 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
         for (int i = 0; i < FN; ++i) sum[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
         const uint32_t m = (uint32_t)(m_base + 16 * j + r16);
         const int id = (int)m < m_end ? ad.row_id[m] : -1;
+        const float f = id >= 0 ? ad.factor[m] : 0.0f;
         const uint32_t all = (uint32_t)__ballot(id >= 0) & 0xffffu;    // rows with an adapter
         uint32_t more = all;
         for (int k = 0; k < 2 && more; ++k)
@@ -233,12 +234,10 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
             const AnyRsrc rv = make_any_rsrc(
                 ad.v + (size_t)cur * (size_t)ad.rank * (size_t)N + (B_NK ? (size_t)n_base * (size_t)ad.rank : 0),
                 (uint32_t)(B_NK ? max(0, min(16 * FN, N - n_base)) : N) * (uint32_t)ad.rank * 2u);
-            for (int k0 = 0; k0 < ad.rank_pad; k0 += 32) {
+            for (int k0 = 0; k0 < ad.rank; k0 += 32) {
                 const uint32_t at = in ? m * t_row + (uint32_t)(k0 + 8 * kb) * 2u : kOobOffset;
                 const u32x4 t_hi = __builtin_amdgcn_raw_buffer_load_b128(rt, at, 0, 0);
                 const u32x4 t_lo = __builtin_amdgcn_raw_buffer_load_b128(rt, at, ad.rank_pad * 2, 0);
-                const float f = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                                              rf, in ? m * f_row + (uint32_t)k0 / 8u : kOobOffset, 0, 0));
                 u32x4 v[FN];
                 if constexpr (B_NK) {
                     const int k = k0 + 8 * kb;
@@ -286,8 +285,6 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
                 const uint32_t at = m * t_row + (uint32_t)r0 * 2u;
                 const u32x4 t_hi = __builtin_amdgcn_raw_buffer_load_b128(rt, at, 0, 0);
                 const u32x4 t_lo = __builtin_amdgcn_raw_buffer_load_b128(rt, at, ad.rank_pad * 2, 0);
-                const float f = __builtin_bit_cast(
-                    float, __builtin_amdgcn_raw_buffer_load_b32(rf, m * f_row + (uint32_t)(r0 / 32) * 4u, 0, 0));
                 float z[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -348,147 +345,168 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
 }
 
 // The intermediates of the low-rank terms.  For row m of a segment with adapter
-// i, z = scales[i] * (X[m] @ U_i) is summed in fp32, and each 32 of its entries
-// (rank_pad = rank rounded up to 32, zeros past rank) are stored as
-//     z = factor[m][block] * (t[m][hi][..] + t[m][lo][..]),
-// factor a power of two of the block's largest |z|, hi the nearest 16-bit value
+// i, z = scales[i] * (X[m] @ U_i) is summed in fp32 and stored as
+//     z = factor[m] * (t[m][hi][..] + t[m][lo][..]),  zeros from rank to rank_pad,
+// factor a power of two of the row's largest |z|, hi the nearest 16-bit value
 // to z / factor (at most 1 in size) and lo that to what is left.  row_id[m] is
 // the row's adapter, -1 for none.
-//  One workgroup per 16 rows of a segment, 32 columns of rank and part of K:
-// its 8 waves take pieces of 128 k in turn, each with all its loads in flight
-// at once, and their sums are added in wave order in LDS.  With few rows K is
-// cut into `splits` parts, whose sums go through device memory (device-scope
-// accesses: the parts run on different XCDs); the part that counts itself last
-// adds them in part order and finishes.  Nothing waits for another workgroup.
+//  One workgroup per 16 rows of a segment and part of K, 32 columns of rank at
+// a time: its 8 waves take pieces of 128 k in turn, each with all its loads in
+// flight at once, and their sums are added in wave order in LDS.  With few rows
+// K is cut into `splits` parts, whose sums go through device memory
+// (device-scope accesses: the parts run on different XCDs); the part that
+// counts itself last adds them in part order and finishes.  Nothing waits for
+// another workgroup.
 template <int DT, bool U_NK>
 __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs a)
 {
     constexpr int WAVES = kShrinkThreads / 64, STEPS = kShrinkK / 32, ROW = kShrinkCols * 2;
     constexpr int kDeviceScope = 16;   // cache policy sc1
     __shared__ float part[WAVES][kShrinkCols][kShrinkRows + 1];
+    __shared__ float sums[kMaxRank / kShrinkCols][kShrinkThreads];
     __shared__ __attribute__((aligned(16))) uint8_t strips[U_NK ? 16 : WAVES * 32 * ROW];
     __shared__ int before;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const RowTile tile = find_row_tile(a.ends, a.segments, a.m, kShrinkRows, blockIdx.x, lane);
     if (tile.group < 0) return;
-    const int rows = tile.end - tile.begin, r_base = blockIdx.y * kShrinkCols;
+    const int rows = tile.end - tile.begin;
     int id = tile.group < a.segments ? a.ids[tile.group] : -1;
     if (id >= a.adapters || id < 0) id = -1;
-    if (blockIdx.y == 0 && blockIdx.z == 0 && (int)threadIdx.x < rows) a.row_id[tile.begin + threadIdx.x] = id;
+    if (blockIdx.y == 0 && (int)threadIdx.x < rows) a.row_id[tile.begin + threadIdx.x] = id;
     if (id < 0) return;
     const int r16 = lane & 15, kb = kgroup16(lane >> 4);
     const size_t k_len = (size_t)a.k, rank = (size_t)a.rank;
-
-    const AnyRsrc rx = make_any_rsrc(a.x + (size_t)tile.begin * k_len, (uint32_t)rows * (uint32_t)a.k * 2u);
-    // U stored (rank, K): this workgroup's rows r_base .. of U^T
-    const AnyRsrc ru = make_any_rsrc(a.u + (size_t)id * k_len * rank + (U_NK ? (size_t)r_base * k_len : 0),
-                                     (uint32_t)(U_NK ? min(kShrinkCols, a.rank - r_base) : a.rank) * (uint32_t)a.k * 2u);
-    uint8_t* strip = strips + (U_NK ? 0 : wave * 32 * ROW);
-    floatx4 acc[2] = {floatx4{0}, floatx4{0}};
-    const int pieces = (a.k + kShrinkK - 1) / kShrinkK;
-    const int p_end = (int)((int64_t)pieces * (blockIdx.z + 1) / gridDim.z);
-    for (int p = (int)((int64_t)pieces * blockIdx.z / gridDim.z) + wave; p < p_end; p += WAVES) {
-        const int k0 = p * kShrinkK;
-        AnyChunk x[STEPS], u[STEPS][2];
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int k = k0 + 32 * s + 8 * kb;
-            x[s] = load_any(rx, ((uint32_t)r16 * (uint32_t)a.k + (uint32_t)k) * 2u, k < a.k);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if constexpr (U_NK) {
-                    u[s][i] = load_any(ru, ((uint32_t)(16 * i + r16) * (uint32_t)a.k + (uint32_t)k) * 2u, k < a.k);
-                } else {
-                    const int kr = k0 + 32 * s + 16 * i + (lane >> 2), r = r_base + 8 * (lane & 3);
-                    u[s][i] = load_any(ru, ((uint32_t)kr * (uint32_t)a.rank + (uint32_t)r) * 2u, kr < a.k && r < a.rank);
-                }
-            }
-        }
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int valid = a.k - (k0 + 32 * s + 8 * kb);
-            const u32x4 xv = keep_first(chunk_value(x[s]), valid);
-            u32x4 uv[2];
-            if constexpr (U_NK) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) uv[i] = keep_first(chunk_value(u[s][i]), valid);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int kr = 16 * i + (lane >> 2);
-                    *reinterpret_cast<u32x4*>(strip + kr * ROW + 16 * ((lane & 3) ^ b_swizzle<ROW, 16>(kr))) = chunk_value(u[s][i]);
-                }
-                const int kr = 8 * kb + (r16 >> 2);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = 16 * i + 4 * (r16 & 3);
-                    const uint8_t* q = strip + kr * ROW + 16 * ((r >> 3) ^ b_swizzle<ROW, 16>(kr)) + 8 * (r16 & 1);
-                    const u32x2 lo = ds_read_tr16(q), hi = ds_read_tr16(q + 4 * ROW);
-                    uv[i] = u32x4{lo.x, lo.y, hi.x, hi.y};
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) acc[i] = mfma_16x16x32<DT>(uv[i], xv, acc[i]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) part[wave][16 * i + 4 * (lane >> 4) + e][r16] = acc[i][e];
-    __syncthreads();
+    const int chunks = (a.rank + kShrinkCols - 1) / kShrinkCols;
     // 512 threads: 16 rows x 32 columns; a row's 32 columns are one half of a wave
     const int row = threadIdx.x >> 5, col = threadIdx.x & 31;
-    float z = 0.0f;
+
+    const AnyRsrc rx = make_any_rsrc(a.x + (size_t)tile.begin * k_len, (uint32_t)rows * (uint32_t)a.k * 2u);
+    uint8_t* strip = strips + (U_NK ? 0 : wave * 32 * ROW);
+    const int pieces = (a.k + kShrinkK - 1) / kShrinkK, splits = (int)gridDim.y;
+    const int p_begin = (int)((int64_t)pieces * blockIdx.y / splits) + wave;
+    const int p_end = (int)((int64_t)pieces * (blockIdx.y + 1) / splits);
+    for (int c = 0; c < chunks; ++c) {
+        const int r_base = c * kShrinkCols;
+        // U stored (rank, K): rows r_base .. of U^T
+        const AnyRsrc ru = make_any_rsrc(a.u + (size_t)id * k_len * rank + (U_NK ? (size_t)r_base * k_len : 0),
+                                         (uint32_t)(U_NK ? min(kShrinkCols, a.rank - r_base) : a.rank) * (uint32_t)a.k * 2u);
+        floatx4 acc[2] = {floatx4{0}, floatx4{0}};
+        for (int p = p_begin; p < p_end; p += WAVES) {
+            const int k0 = p * kShrinkK;
+            AnyChunk x[STEPS], u[STEPS][2];
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) z += part[w][col][row];
-    if (gridDim.z > 1) {
-        const int splits = (int)gridDim.z, slot = (int)(blockIdx.x * gridDim.y + blockIdx.y);
-        const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.part + (size_t)slot * (size_t)splits * kShrinkThreads,
-                                                    (uint32_t)splits * kShrinkThreads * 4u);
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, z), rs,
-                                              (blockIdx.z * kShrinkThreads + threadIdx.x) * 4u, 0, kDeviceScope);
+            for (int s = 0; s < STEPS; ++s) {
+                const int k = k0 + 32 * s + 8 * kb;
+                x[s] = load_any(rx, ((uint32_t)r16 * (uint32_t)a.k + (uint32_t)k) * 2u, k < a.k);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if constexpr (U_NK) {
+                        u[s][i] = load_any(ru, ((uint32_t)(16 * i + r16) * (uint32_t)a.k + (uint32_t)k) * 2u, k < a.k);
+                    } else {
+                        const int kr = k0 + 32 * s + 16 * i + (lane >> 2), r = r_base + 8 * (lane & 3);
+                        u[s][i] = load_any(ru, ((uint32_t)kr * (uint32_t)a.rank + (uint32_t)r) * 2u, kr < a.k && r < a.rank);
+                    }
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int valid = a.k - (k0 + 32 * s + 8 * kb);
+                const u32x4 xv = keep_first(chunk_value(x[s]), valid);
+                u32x4 uv[2];
+                if constexpr (U_NK) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) uv[i] = keep_first(chunk_value(u[s][i]), valid);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int kr = 16 * i + (lane >> 2);
+                        *reinterpret_cast<u32x4*>(strip + kr * ROW + 16 * ((lane & 3) ^ b_swizzle<ROW, 16>(kr))) = chunk_value(u[s][i]);
+                    }
+                    const int kr = 8 * kb + (r16 >> 2);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = 16 * i + 4 * (r16 & 3);
+                        const uint8_t* q = strip + kr * ROW + 16 * ((r >> 3) ^ b_swizzle<ROW, 16>(kr)) + 8 * (r16 & 1);
+                        const u32x2 lo = ds_read_tr16(q), hi = ds_read_tr16(q + 4 * ROW);
+                        uv[i] = u32x4{lo.x, lo.y, hi.x, hi.y};
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) acc[i] = mfma_16x16x32<DT>(uv[i], xv, acc[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) part[wave][16 * i + 4 * (lane >> 4) + e][r16] = acc[i][e];
+        __syncthreads();
+        float z = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) z += part[w][col][row];
+        sums[c][threadIdx.x] = z;
+        __syncthreads();
+    }
+    if (splits > 1) {
+        // part s of this row tile, 32 columns c: kShrinkThreads floats at (s * chunks + c) * kShrinkThreads
+        const uint32_t bytes = (uint32_t)chunks * kShrinkThreads * 4u;
+        const __amdgpu_buffer_rsrc_t rs =
+            make_rsrc(a.part + (size_t)blockIdx.x * (size_t)splits * (bytes / 4), (uint32_t)splits * bytes);
+        for (int c = 0; c < chunks; ++c)
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, sums[c][threadIdx.x]), rs,
+                                                  blockIdx.y * bytes + (uint32_t)(c * kShrinkThreads + threadIdx.x) * 4u, 0,
+                                                  kDeviceScope);
         wait_vmcnt<0>();               // this wave's sums have reached device scope
         __syncthreads();
         if (threadIdx.x == 0)
-            before = __hip_atomic_fetch_add(a.counters + slot, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            before = __hip_atomic_fetch_add(a.counters + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
         if (before != splits - 1) return;
         asm volatile("" ::: "memory");   // the loads below stay after the count that allowed them
-        z = 0.0f;
-        for (int s0 = 0; s0 < splits; s0 += 4) {
-            float o[4];
+        for (int c = 0; c < chunks; ++c) {
+            float z = 0.0f;
+            for (int s0 = 0; s0 < splits; s0 += 4) {
+                float o[4];
 #pragma unroll
-            for (int s = 0; s < 4; ++s)   // parts past the last are out of range: zero
-                o[s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                                     rs, ((uint32_t)(s0 + s) * kShrinkThreads + threadIdx.x) * 4u, 0, kDeviceScope));
+                for (int s = 0; s < 4; ++s)   // parts past the last are out of range: zero
+                    o[s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                         rs, (uint32_t)(s0 + s) * bytes + (uint32_t)(c * kShrinkThreads + threadIdx.x) * 4u,
+                                                         0, kDeviceScope));
 #pragma unroll
-            for (int s = 0; s < 4; ++s) z += o[s];
+                for (int s = 0; s < 4; ++s) z += o[s];
+            }
+            sums[c][threadIdx.x] = z;
         }
-        if (threadIdx.x == 0) __hip_atomic_store(a.counters + slot, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (threadIdx.x == 0) __hip_atomic_store(a.counters + blockIdx.x, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    // columns past rank are zero, whatever X holds (0 * infinity is not)
-    z = r_base + col < a.rank ? z * a.scales[id] : 0.0f;
-    float top = fabsf(z);
+    const float scale = a.scales[id];
+    float top = 0.0f;
+    for (int c = 0; c < chunks; ++c) {
+        // columns past rank are zero, whatever X holds (0 * infinity is not)
+        const float z = c * kShrinkCols + col < a.rank ? sums[c][threadIdx.x] * scale : 0.0f;
+        sums[c][threadIdx.x] = z;
+        top = fmaxf(top, fabsf(z) < __builtin_inff() ? fabsf(z) : 0.0f);
+    }
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-    // 2^e > top: the scaled values are below 1.  Zeros (and, with nothing to
-    // scale by, infinities) keep factor 1; e stays where 2^-e is a normal number.
+    // 2^e > top, the largest finite entry: the scaled values are below 1.  Zeros
+    // keep factor 1; e stays where 2^-e is a normal number.
     int e = 0;
-    if (top > 0.0f && top < __builtin_inff()) {
+    if (top > 0.0f) {
         (void)frexpf(top, &e);
         e = min(max(e, -125), 125);
     }
-    const float scaled = ldexpf(z, -e);
-    const uint16_t hi = act_cast<DT>(scaled, false);
-    const float rest = scaled - to_float<DT>(hi);
-    if (row < rows) {
-        const size_t m = (size_t)(tile.begin + row);
-        uint16_t* t = a.t + m * (size_t)(2 * a.rank_pad) + r_base + col;
+    if (row >= rows) return;
+    const size_t m = (size_t)(tile.begin + row);
+    uint16_t* t = a.t + m * (size_t)(2 * a.rank_pad) + col;
+    for (int c = 0; c < a.rank_pad / kShrinkCols; ++c, t += kShrinkCols) {
+        const float scaled = c < chunks ? ldexpf(sums[c][threadIdx.x], -e) : 0.0f;
+        const uint16_t hi = act_cast<DT>(scaled, false);
+        const float rest = scaled - to_float<DT>(hi);
         t[0] = hi;
         // an infinite hi leaves inf - inf: such an entry has no second part
         t[a.rank_pad] = fabsf(scaled) < __builtin_inff() ? act_cast<DT>(rest, false) : (uint16_t)0;
-        if (col == 0) a.factor[m * (size_t)(a.rank_pad / 32) + blockIdx.y] = ldexpf(1.0f, e);
     }
+    if (col == 0) a.factor[m] = ldexpf(1.0f, e);
 }
 
 // ---------------------------------------------------------------- register-staged kernel

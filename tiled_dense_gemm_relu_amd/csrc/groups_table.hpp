@@ -20,13 +20,15 @@ struct RowsArgs {
 
 // The low-rank term of each row (v == nullptr: none).  Row m's adapter is
 // row_id[m] (-1: none) and its intermediate t[m][hi | lo][rank_pad] times
-// factor[m][rank_pad / 32], see adapter_shrink.
+// factor[m], see adapter_shrink.
 struct AdapterArgs {
     const uint16_t* v;     // (adapters, rank, N) or (adapters, N, rank)
     const uint16_t* t;
     const float* factor;
     const int* row_id;
-    int rank, rank_pad;
+    const int* ends;       // segments of rows and their adapters
+    const int* ids;
+    int segments, adapters, rank, rank_pad;
     int v_fast;            // V's rows allow the widest loads of a lane of its own: 8 bytes (4 columns), or 16 (8 rank entries)
 };
 
@@ -39,8 +41,8 @@ struct ShrinkArgs {
     uint16_t* t;
     float* factor;
     int* row_id;
-    float* part;           // [row tile][32 columns][split][16 x 32] sums
-    int* counters;         // one for each row tile and 32 columns
+    float* part;           // [row tile][split][32 columns][16 x 32] sums
+    int* counters;         // one for each row tile
     int m, k, segments, adapters, rank, rank_pad;
 };
 
@@ -65,6 +67,7 @@ struct MaskArgs {
 // Load widths with an instance of the register-staged kernels, widest first.
 constexpr int kNumLoadWidths = 4;
 constexpr int kLoadWidths[kNumLoadWidths] = {8, 4, 2, 1};
+constexpr int kMaxRank = 256;
 constexpr int kShrinkRows = 16, kShrinkCols = 32, kShrinkK = 128, kShrinkThreads = 512;
 
 // Square LDS-DMA tiles, by GEMM_RELU_GROUPS_DMA_* order, and their workgroups.
@@ -73,7 +76,7 @@ constexpr int kGroupTile[kNumGroupTiles] = {256, 128, 64};
 constexpr int kGroupThreads[kNumGroupTiles] = {512, 512, 512};
 
 struct GroupKernels {
-    // [tile][B layout][K % 64 != 0][with adapters]; the 256 tile has no adapter instances
+    // [tile][B layout][K % 64 != 0][with adapters]; with adapters the 256 tile takes any K and starts from their terms
     const void* rows_dma[kNumGroupTiles][2][2][2];
     const void* weight_dma[kNumGroupTiles];
     const void* rows_tiled[2][kNumLoadWidths];    // [B layout][load width]
