@@ -25,7 +25,8 @@ KERNEL_TIMELINE_PATH = os.path.join(PKG, "kernel_timeline")
 ARCH = "gfx950"
 
 SOURCES = ["gemm_relu_api.hip", "kernels_f16.hip", "kernels_bf16.hip", "groups_api.hip", "groups_f16.hip",
-           "groups_bf16.hip"]
+           "groups_bf16.hip", "groups_staged_f16_even.hip", "groups_staged_f16_odd.hip", "groups_staged_bf16_even.hip",
+           "groups_staged_bf16_odd.hip"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",

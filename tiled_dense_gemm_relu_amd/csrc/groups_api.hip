@@ -16,6 +16,9 @@ namespace {
 constexpr int64_t kMaxDim = int64_t(1) << 20;
 constexpr int64_t kMaxGroups = 65535;
 
+// Gradients of fewer operations than this take one register-staged launch.
+constexpr double kSmallGrad = 4e9;
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
@@ -67,21 +70,26 @@ int check_workspace(void* workspace, int64_t bytes, int64_t need)
     return !workspace || bytes < need || !aligned(workspace, 256) ? GEMM_RELU_ERR_WORKSPACE : GEMM_RELU_OK;
 }
 
-// Index of the widest load (kLoadWidths) that every given row length and address allows.
-int load_width(std::initializer_list<Span> operands)
-{
-    for (int w = 0; w < kNumLoadWidths; ++w) {
-        bool ok = true;
-        for (const Span& s : operands)   // bytes: here the row length in elements
-            ok = ok && s.bytes % kLoadWidths[w] == 0 && aligned(s.p, 2 * kLoadWidths[w]);
-        if (ok) return w;
-    }
-    return kNumLoadWidths - 1;
-}
+// Whether LDS DMA can read a matrix: rows of whole 16-byte pieces.
+bool dma_rows(const void* p, int64_t row) { return row % 8 == 0 && aligned(p, 16); }
 
 int store_width(const void* c, int64_t n) { return n % 8 == 0 && aligned(c, 16) ? 2 : n % 4 == 0 && aligned(c, 8) ? 1 : 0; }
 
 const GroupKernels& kernels(int dtype) { return dtype == GEMM_RELU_F16 ? group_kernels_f16() : group_kernels_bf16(); }
+
+// The register-staged kernels for matrices with these rows: elements that start
+// inside a dword need more loads and shifts.
+struct Rows {
+    const void* p;
+    int64_t length;
+};
+const StagedKernels& staged_kernels(int dtype, std::initializer_list<Rows> operands)
+{
+    bool even = true;
+    for (const Rows& r : operands) even = even && r.length % 2 == 0 && aligned(r.p, 4);
+    if (dtype == GEMM_RELU_F16) return even ? staged_kernels_f16_even() : staged_kernels_f16_odd();
+    return even ? staged_kernels_bf16_even() : staged_kernels_bf16_odd();
+}
 
 int enqueue(const void* fn, dim3 grid, int threads, void** args, hipStream_t stream)
 {
@@ -112,52 +120,97 @@ int dma_config(int64_t rows, int64_t tiles_256, int64_t tiles_128)
     return GEMM_RELU_GROUPS_DMA_64;
 }
 
+// Rows of a group on average, and the tiles of `tile` x `tile` that this makes.
+struct GroupShape {
+    int64_t used, rows;
+    GroupShape(int64_t m, int64_t groups) : used(std::min(groups, m)), rows(m / used) {}
+    int64_t tiles(int64_t tile, int64_t n) const { return used * ceil_div(rows, tile) * ceil_div(n, tile); }
+};
+
+// Position in kStagedTile of the tile of a register-staged product.
+int staged_tile(int64_t rows, int64_t tiles_128) { return rows >= 96 && tiles_128 >= 128 ? 0 : 1; }
+
+// Persistent workgroups for `tiles` units: as many as run at once (two of the
+// 64 x 64 kernels on a CU).
+int64_t resident(int64_t tile, int64_t tiles, int cus) { return std::min<int64_t>(tiles, tile == 64 ? 2 * cus : cus); }
+
 // A product over row groups (M, N, K > 0).
 int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config, int cus, hipStream_t stream)
 {
     a.c_vec = store_width(a.c, a.n);
-    const int w = load_width({{a.a, a.k}, {a.b, b_layout == GEMM_RELU_B_NK ? a.k : a.n}});
-    if (w > 0) config = GEMM_RELU_GROUPS_TILED;
+    const bool dma = dma_rows(a.a, a.k) && dma_rows(a.b, b_layout == GEMM_RELU_B_NK ? a.k : a.n);
+    int staged = 0;
+    if (!dma) {
+        const GroupShape g(a.m, a.groups);
+        if (config != GEMM_RELU_GROUPS_TILED) staged = staged_tile(g.rows, g.tiles(128, a.n));
+        config = GEMM_RELU_GROUPS_TILED;
+    }
     // With adapters the 256 tile cuts its rows at the segments' ends and streams V
     // like B; the others take rows of many segments.
     const auto auto_config = [&](int64_t groups) {
-        const int64_t used = std::min(groups, (int64_t)a.m), rows = a.m / used;
-        return dma_config(rows, used * ceil_div(rows, 256) * ceil_div(a.n, 256), used * ceil_div(rows, 128) * ceil_div(a.n, 128));
+        const GroupShape g(a.m, groups);
+        return dma_config(g.rows, g.tiles(256, a.n), g.tiles(128, a.n));
     };
     if (config == GEMM_RELU_GROUPS_AUTO) {
         config = auto_config(ad.v ? ad.segments : a.groups);
         if (ad.v && config != GEMM_RELU_GROUPS_DMA_256) config = std::max<int>(auto_config(1), GEMM_RELU_GROUPS_DMA_128);
     }
-    const bool v_rows = b_layout == GEMM_RELU_B_KN || ad.rank % 8 == 0;
-    if (config == GEMM_RELU_GROUPS_DMA_256 && ad.v && !(v_rows && aligned(ad.v, 16))) config = GEMM_RELU_GROUPS_DMA_128;
+    if (config == GEMM_RELU_GROUPS_DMA_256 && ad.v && !dma_rows(ad.v, b_layout == GEMM_RELU_B_NK ? ad.rank : a.n))
+        config = GEMM_RELU_GROUPS_DMA_128;
     const bool first = config == GEMM_RELU_GROUPS_DMA_256 && ad.v;
-    const int64_t rows = config == GEMM_RELU_GROUPS_TILED ? 128 : kGroupTile[config - 1];
+    const int64_t rows = config == GEMM_RELU_GROUPS_TILED ? kStagedTile[staged] : kGroupTile[config - 1];
     const int64_t tiles = most_row_tiles(a.m, first ? ad.segments : a.groups, rows) * ceil_div(a.n, rows);
     if (tiles > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
     void* args[] = {&a, &ad};
+    const dim3 grid((unsigned)resident(rows, tiles, cus));
     if (config == GEMM_RELU_GROUPS_TILED)
-        return enqueue(kernels(dtype).rows_tiled[b_layout][w], dim3((unsigned)tiles), 256, args, stream);
-    // persistent workgroups, one per CU
-    return enqueue(kernels(dtype).rows_dma[config - 1][b_layout][a.k % 64 != 0][ad.v != nullptr],
-                   dim3((unsigned)std::min<int64_t>(tiles, cus)), kGroupThreads[config - 1], args, stream);
+        return enqueue(staged_kernels(dtype, {{a.a, a.k}, {a.b, b_layout == GEMM_RELU_B_NK ? a.k : a.n}})
+                           .rows[staged][b_layout][ad.v != nullptr][a.groups > 64], grid, kStagedThreads, args, stream);
+    return enqueue(kernels(dtype).rows_dma[config - 1][b_layout][a.k % 64 != 0][ad.v != nullptr], grid,
+                   kGroupThreads[config - 1], args, stream);
 }
 
-// Sums over each group's rows (I, J > 0).
+// Sums over each group's rows (I, J > 0), by LDS DMA.
 int launch_weights(WeightArgs a, int dtype, int config, int cus, hipStream_t stream)
 {
-    a.c_vec = store_width(a.out, a.j);
-    const int w = load_width({{a.p, a.i}, {a.q, a.j}});
-    if (w > 0) config = GEMM_RELU_GROUPS_TILED;
     if (config == GEMM_RELU_GROUPS_AUTO)
         config = dma_config(a.i, a.groups * ceil_div(a.i, 256) * ceil_div(a.j, 256),
                             a.groups * ceil_div(a.i, 128) * ceil_div(a.j, 128));
-    const int64_t rows = config == GEMM_RELU_GROUPS_TILED ? 128 : kGroupTile[config - 1];
-    const int64_t tiles = int64_t(a.groups) * ceil_div(a.i, rows) * ceil_div(a.j, rows);
+    const int64_t tile = kGroupTile[config - 1], tiles = int64_t(a.groups) * ceil_div(a.i, tile) * ceil_div(a.j, tile);
     if (tiles > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
     void* args[] = {&a};
-    if (config == GEMM_RELU_GROUPS_TILED) return enqueue(kernels(dtype).weight_tiled[w], dim3((unsigned)tiles), 256, args, stream);
-    return enqueue(kernels(dtype).weight_dma[config - 1], dim3((unsigned)std::min<int64_t>(tiles, cus)), kGroupThreads[config - 1], args,
-                   stream);
+    return enqueue(kernels(dtype).weight_dma[config - 1], dim3((unsigned)resident(tile, tiles, cus)), kGroupThreads[config - 1],
+                   args, stream);
+}
+
+// Both gradients (or one: the other's output is NULL) in one register-staged
+// launch.  b_layout is that of dA's product.  The workgroups are shared out by
+// the two products' K-steps, a tile counting as four more for its start and end.
+int launch_grad_staged(RowsArgs r, WeightArgs w, const uint16_t* mask, int dtype, int b_layout, int config, int cus,
+                       hipStream_t stream)
+{
+    r.c_vec = store_width(r.c, r.n);
+    w.c_vec = store_width(w.out, w.j);
+    const GroupShape g(r.m, r.groups);
+    const auto weight_tiles = [&](int64_t t) { return int64_t(w.groups) * ceil_div(w.i, t) * ceil_div(w.j, t); };
+    const int staged =
+        config == GEMM_RELU_GROUPS_TILED ? 0 : staged_tile(g.rows, std::min(g.tiles(128, r.n), weight_tiles(128)));
+    const int64_t t = kStagedTile[staged];
+    const int64_t tiles_r = r.c ? most_row_tiles(r.m, r.groups, t) * ceil_div(r.n, t) : 0, tiles_w = w.out ? weight_tiles(t) : 0;
+    if (tiles_r > INT32_MAX || tiles_w > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
+    const int64_t room = resident(t, INT32_MAX, cus);
+    const double work_r = tiles_r ? (double)g.tiles(t, r.n) * (double)(ceil_div(r.k, 64) + 4) : 0;
+    const double work_w = (double)tiles_w * (double)(ceil_div(g.rows, 64) + 4);
+    int64_t blocks_r = tiles_r == 0 ? 0 : (int64_t)((double)room * work_r / (work_r + work_w));
+    if (tiles_r > 0) blocks_r = std::min(tiles_r, std::max<int64_t>(1, blocks_r > 8 ? blocks_r / 8 * 8 : blocks_r));
+    if (tiles_w > 0) blocks_r = std::min(blocks_r, room - 1);
+    const int64_t blocks_w = std::min(tiles_w, room - blocks_r);
+    int blocks_rows = (int)blocks_r;
+    void* args[] = {&r, &w, &mask, &blocks_rows};
+    const Rows d{r.a, r.k}, c{mask, r.k}, b{r.c ? r.b : nullptr, b_layout == GEMM_RELU_B_NK ? r.k : r.n};
+    const Rows x{w.out ? (b_layout == GEMM_RELU_B_NK ? w.p : w.q) : nullptr, r.n};
+    return enqueue(staged_kernels(dtype, {d, c, b, x}).grad[staged][b_layout][mask != nullptr][r.groups > 64], dim3((unsigned)(blocks_r + blocks_w)),
+                   kStagedThreads, args, stream);
 }
 
 // Workspace of the adapters: the counters, the intermediates, each row's
@@ -254,28 +307,30 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
         if (want_b && rc == GEMM_RELU_OK) rc = zero_fill(dB, gkn, s);
         return rc;
     }
-    const uint16_t* d = static_cast<const uint16_t*>(dC);
+    const uint16_t *d = static_cast<const uint16_t*>(dC), *c = relu ? static_cast<const uint16_t*>(C) : nullptr;
+    const uint16_t *x = static_cast<const uint16_t*>(A), *b = static_cast<const uint16_t*>(B);
+    // dA = D (M, N) times B^T: B as stored (K, N) is the transposed weight of this product
+    const bool kn = b_layout == GEMM_RELU_B_KN;
+    const int layout_a = kn ? GEMM_RELU_B_NK : GEMM_RELU_B_KN;
+    RowsArgs r{d, b, static_cast<uint16_t*>(dA), ends, (int)M, (int)K, (int)N, (int)groups, 0, 0};
+    WeightArgs w{kn ? x : d, kn ? d : x, static_cast<uint16_t*>(dB), ends, (int)M, (int)(kn ? K : N), (int)(kn ? N : K),
+                 (int)groups, 0};
+    // LDS DMA needs whole 16-byte pieces and D itself in memory.  The register-
+    // staged kernel needs neither, and is one launch instead of two or three.
+    const bool dma = dma_rows(d, N) && (!want_a || dma_rows(b, kn ? N : K)) && (!want_b || dma_rows(x, K));
+    if (config_id == GEMM_RELU_GROUPS_TILED || !dma || (config_id == GEMM_RELU_GROUPS_AUTO && 4.0 * M * N * K < kSmallGrad))
+        return launch_grad_staged(r, w, c, dtype, layout_a, config_id, cus, s);
     if (relu) {
         uint16_t* masked = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + GEMM_RELU_GROUPS_COUNTER_BYTES);
-        MaskArgs m{d, static_cast<const uint16_t*>(C), masked, mn, aligned(dC, 16) && aligned(C, 16)};
+        MaskArgs m{d, c, masked, mn, aligned(C, 16)};
         void* args[] = {&m};
         rc = enqueue(kernels(dtype).mask, dim3((unsigned)std::min<int64_t>(ceil_div(mn, 2048), 4096)), 256, args, s);
-        d = masked;
+        r.a = masked;
+        (kn ? w.q : w.p) = masked;
     }
-    if (want_a && rc == GEMM_RELU_OK) {
-        // D (M, N) times B^T: B as stored (K, N) is the transposed weight of this product
-        RowsArgs a{d, static_cast<const uint16_t*>(B), static_cast<uint16_t*>(dA), ends,
-                   (int)M, (int)K, (int)N, (int)groups, 0, 0};
-        rc = launch_rows(a, AdapterArgs{}, dtype, b_layout == GEMM_RELU_B_KN ? GEMM_RELU_B_NK : GEMM_RELU_B_KN,
-                         config_id, cus, s);
-    }
-    if (want_b && rc == GEMM_RELU_OK && gkn > 0) {
-        const uint16_t* x = static_cast<const uint16_t*>(A);
-        const bool kn = b_layout == GEMM_RELU_B_KN;
-        WeightArgs a{kn ? x : d, kn ? d : x, static_cast<uint16_t*>(dB), ends,
-                     (int)M, (int)(kn ? K : N), (int)(kn ? N : K), (int)groups, 0};
-        rc = launch_weights(a, dtype, config_id, cus, s);
-    }
+    if (want_a && rc == GEMM_RELU_OK) rc = launch_rows(r, AdapterArgs{}, dtype, layout_a, config_id, cus, s);
+    w.c_vec = store_width(w.out, w.j);
+    if (want_b && rc == GEMM_RELU_OK && gkn > 0) rc = launch_weights(w, dtype, config_id, cus, s);
     return rc;
 }
 

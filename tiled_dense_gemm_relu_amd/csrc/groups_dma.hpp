@@ -17,7 +17,8 @@
 
 namespace gemm_relu_hip {
 
-template <int BM_, int BN_, int STAGES_, int WAVES_M_, int WAVES_N_, bool A_KMAJOR_, bool B_KMAJOR_, int PRODUCERS_>
+template <int BM_, int BN_, int STAGES_, int WAVES_M_, int WAVES_N_, bool A_KMAJOR_, bool B_KMAJOR_, int PRODUCERS_,
+          int SETS_ = 0, int MASKED_ = 0, bool ODD_ = true>
 struct GroupDmaConfig {
     static constexpr int BM = BM_, BN = BN_, BK = 64, STAGES = STAGES_, GROUP_M = 4;
     // WAVES compute waves; PRODUCERS > 0 adds waves that only load, else every
@@ -26,6 +27,15 @@ struct GroupDmaConfig {
     static constexpr int PRODUCERS = PRODUCERS_, DMA_WAVES = PRODUCERS > 0 ? PRODUCERS : WAVES;
     static constexpr int THREADS = 64 * (WAVES + PRODUCERS);
     static constexpr bool A_KMAJOR = A_KMAJOR_, B_KMAJOR = B_KMAJOR_;
+    // SETS > 0: the producers load through registers instead (rows of any length
+    // and alignment), with that many steps in flight.  MASKED: the operand (1: A,
+    // 2: B) that is zero where a second matrix of its shape is not above zero.
+    // ODD: elements may start inside a dword (odd row lengths, 2-byte alignment).
+    static constexpr int SETS = SETS_, MASKED = MASKED_;
+    static constexpr bool ODD = ODD_;
+    static constexpr bool STAGED = SETS > 0;
+    static_assert(!STAGED || (PRODUCERS > 0 && STAGES_ == 2), "producers fill the other of two stages");
+    static_assert(STAGED || MASKED == 0, "DMA cannot mask");
     static constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N, FM = WTM / 16, FN = WTN / 16;
     static constexpr int A_ROW = A_KMAJOR ? BM * 2 : BK * 2, B_ROW = B_KMAJOR ? BN * 2 : BK * 2;
     static constexpr int A_STAGE = BM * BK * 2, B_STAGE = BN * BK * 2, B_REGION = STAGES * A_STAGE;
@@ -48,22 +58,85 @@ struct DmaUnit {
     int m0, m_end, n0, group, k0, k_end, adapter;
 };
 
-// The rows' products: unit -> row tile of a group (from the row table) and
-// column tile.  Lane l keeps where group l ends and how many tiles there are up
-// to it; with more than 64 groups a lookup scans `ends` again.
-template <class Cfg>
+// Where a workgroup finds its units in its XCD's list of them: in turn, every
+// second round in the opposite direction, so that the last workgroup of a round,
+// whose unit is the shortest, is the first of the next.
+struct UnitOrder {
+    int xcd, xcds, place, width;      // this workgroup's XCD and place among its workgroups
+
+    __device__ __forceinline__ void init(int block, int blocks)
+    {
+        xcds = blocks % 8 == 0 ? 8 : 1;
+        xcd = block % xcds;
+        place = block / xcds;
+        width = blocks / xcds;
+    }
+    // The first of `total` that belong to XCD x and later ones.
+    __device__ __forceinline__ int64_t part(int64_t total, int x) const { return total * x / xcds; }
+    // Position of this workgroup's i-th unit in the list.
+    __device__ __forceinline__ int position(int i) const { return i * width + ((i & 1) ? width - 1 - place : place); }
+    __device__ __forceinline__ int units(int listed) const
+    {
+        const int whole = listed / width;
+        return whole + (position(whole) < listed ? 1 : 0);
+    }
+};
+
+// The rows' products.  A group's rows are cut into tiles of BM rows, the last of
+// them partial.  The groups' output columns are dealt to the XCDs in order, an
+// eighth of the work to each (in quarter tiles; a partial tile of at most half
+// the rows counts as half), so an XCD has all row tiles of its columns, next to
+// each other in its list: they share the group's weights in its L2.  (Whole
+// tiles first and partial ones after them would balance a round better, but the
+// partial ones then read their weights again, each its own: 1087 against 1003 us
+// for 16384 rows in 16 groups, 4096 x 8192 fp16.)  Lane l keeps what belongs to
+// group l; with more than 64 groups (MANY) a lookup scans `ends` again.
+template <class Cfg, bool MANY>
 struct RowUnits {
+    static constexpr bool RAGGED = true;      // tiles of fewer than BM rows are common
     const int* ends;
     int groups, M, K, tiles_n, lane;
     int listed;              // groups with tiles: all, and with `rest` the rows of none as one more
-    int end, incl;           // per lane, at most 64 groups
-    int row_tiles, rows;     // tiles of all groups; rows in groups
+    int rows;                // rows in groups
+    int units;               // this XCD's
+    int64_t first, last;     // its part of the work
     const int* ids;          // the groups' adapters, or nullptr
     int adapters;
+    UnitOrder order;
+    struct Lane {
+        int begin, end;      // the group's rows
+        int col, cols;       // its columns of tiles on this XCD
+        int incl;            // units up to this group
+    } kept;                  // at most 64 groups
 
-    __device__ __forceinline__ int tiles_of(const GroupRows& r) const { return (r.end - r.begin + Cfg::BM - 1) / Cfg::BM; }
+    __device__ __forceinline__ static int cost(int n) { return n / Cfg::BM * 4 + (n % Cfg::BM > Cfg::BM / 2 ? 4 : n % Cfg::BM ? 2 : 0); }
 
-    __device__ __forceinline__ void init(const RowsArgs& a, const int* ends_, int groups_, bool rest, int lane_)
+    // 64 groups from g0 on, which start at row `start`; `work` and `before`
+    // are what the groups before them have, and are moved on.
+    __device__ __forceinline__ Lane scan(int g0, int& start, int64_t& work, int& units_before) const
+    {
+        const GroupRows r = load_group_rows(ends, groups, M, g0, start, lane);
+        const int n = g0 + lane < listed ? r.end - r.begin : 0, c = cost(n);
+        const int before = wave_scan_sum(c, lane) - c;      // at most 4 (2^20 / 64 + 65536)
+        // the first column whose work starts at or past w
+        auto column = [&](int64_t w) {
+            const int64_t past = w - (work + (int64_t)before * tiles_n);
+            return past <= 0 || c == 0 ? 0 : (int)min((int64_t)tiles_n, (past + c - 1) / c);
+        };
+        Lane k;
+        k.begin = r.begin;
+        k.end = r.end;
+        k.col = column(first);
+        k.cols = max(0, column(last) - k.col);
+        k.incl = units_before + wave_scan_sum((n + Cfg::BM - 1) / Cfg::BM * k.cols, lane);
+        work += (int64_t)__builtin_amdgcn_readlane(before + c, 63) * tiles_n;
+        units_before = __builtin_amdgcn_readlane(k.incl, 63);
+        start = __builtin_amdgcn_readlane(r.end, 63);
+        return k;
+    }
+
+    __device__ __forceinline__ void init(const RowsArgs& a, const int* ends_, int groups_, bool rest, int lane_, int block,
+                                         int blocks)
     {
         ends = ends_;
         groups = groups_;
@@ -73,37 +146,44 @@ struct RowUnits {
         K = a.k;
         tiles_n = (a.n + Cfg::BN - 1) / Cfg::BN;
         lane = lane_;
-        row_tiles = 0;
+        order.init(block, blocks);
+        int64_t total = 0;
         rows = 0;
         for (int g0 = 0; g0 < listed; g0 += 64) {
             const GroupRows r = load_group_rows(ends, groups, M, g0, rows, lane);
-            const bool real = g0 + lane < listed;
-            end = r.end;
-            incl = row_tiles + wave_scan_sum(real ? tiles_of(r) : 0, lane);
-            row_tiles = __builtin_amdgcn_readlane(incl, 63);
+            total += __builtin_amdgcn_readlane(wave_scan_sum(g0 + lane < listed ? cost(r.end - r.begin) : 0, lane), 63);
             rows = __builtin_amdgcn_readlane(r.end, min(listed - 1 - g0, 63));
         }
+        total *= tiles_n;
+        first = order.part(total, order.xcd);
+        last = order.part(total, order.xcd + 1);
+        int start = 0;
+        int64_t work = 0;
+        units = 0;
+        for (int g0 = 0; g0 < listed; g0 += 64) kept = scan(g0, start, work, units);
     }
-    __device__ __forceinline__ int total() const { return row_tiles * tiles_n; }
-    __device__ __forceinline__ DmaUnit unit(int u) const
+    __device__ __forceinline__ int count() const { return order.units(units); }
+    __device__ __forceinline__ DmaUnit unit(int i) const
     {
-        int tm, tn;
-        tile_coords(u, row_tiles, tiles_n, Cfg::GROUP_M, tm, tn);
-        if (listed <= 64) {
-            const int l = __builtin_ctzll(__ballot(tm < incl));
-            const int e = __builtin_amdgcn_readlane(end, l);
-            const int b = l ? __builtin_amdgcn_readlane(end, l - 1) : 0;
-            const int before = l ? __builtin_amdgcn_readlane(incl, l - 1) : 0;
-            const int m0 = b + (tm - before) * Cfg::BM;
-            return DmaUnit{m0, min(m0 + Cfg::BM, e), tn * Cfg::BN, l, 0, K, adapter(l)};
+        const int at = order.position(i);
+        int g0 = 0;
+        Lane k = kept;
+        if (MANY && listed > 64) {
+            int start = 0, before = 0;
+            int64_t work = 0;
+            for (;; g0 += 64) {
+                k = scan(g0, start, work, before);
+                if (at < before) break;
+            }
         }
-        const RowTile t = find_row_tile(ends, groups, M, Cfg::BM, tm, lane);
-        return DmaUnit{t.begin, t.end, tn * Cfg::BN, t.group, 0, K, adapter(t.group)};
-    }
-    __device__ __forceinline__ int adapter(int group) const
-    {
-        const int id = ids && group < groups ? ids[group] : -1;
-        return id < adapters ? id : -1;
+        const int l = __builtin_ctzll(__ballot(at < k.incl));
+        const int b = __builtin_amdgcn_readlane(k.begin, l), e = __builtin_amdgcn_readlane(k.end, l);
+        const int col = __builtin_amdgcn_readlane(k.col, l), cols = __builtin_amdgcn_readlane(k.cols, l);
+        const int tiles = (e - b + Cfg::BM - 1) / Cfg::BM;
+        int tm, tn;
+        tile_coords(at - (__builtin_amdgcn_readlane(k.incl, l) - tiles * cols), tiles, cols, Cfg::GROUP_M, tm, tn, false);
+        const int m0 = b + tm * Cfg::BM, id = ids && g0 + l < groups ? ids[g0 + l] : -1;
+        return DmaUnit{m0, min(m0 + Cfg::BM, e), (col + tn) * Cfg::BN, g0 + l, 0, K, id < adapters ? id : -1};
     }
 };
 
@@ -111,10 +191,13 @@ struct RowUnits {
 // over the group's rows.  An empty group keeps one K-step, of zeros.
 template <class Cfg>
 struct WeightUnits {
+    static constexpr bool RAGGED = false;
     const int* ends;
     int groups, M, I, tiles_i, tiles_j;
+    int first, listed;       // this XCD's units
+    UnitOrder order;
 
-    __device__ __forceinline__ void init(const WeightArgs& a, int)
+    __device__ __forceinline__ void init(const WeightArgs& a, int block, int blocks)
     {
         ends = a.ends;
         groups = a.groups;
@@ -122,15 +205,15 @@ struct WeightUnits {
         I = a.i;
         tiles_i = (a.i + Cfg::BM - 1) / Cfg::BM;
         tiles_j = (a.j + Cfg::BN - 1) / Cfg::BN;
+        order.init(block, blocks);
+        const int total = groups * tiles_i * tiles_j;
+        first = (int)order.part(total, order.xcd);
+        listed = (int)order.part(total, order.xcd + 1) - first;
     }
-    __device__ __forceinline__ int total() const { return groups * tiles_i * tiles_j; }
-    __device__ __forceinline__ DmaUnit unit(int u) const
+    __device__ __forceinline__ int count() const { return order.units(listed); }
+    __device__ __forceinline__ DmaUnit unit(int i) const
     {
-        // Each XCD takes a contiguous range of units, as tile_coords gives it
-        // the tiles of one output; here that is whole groups, mostly.
-        const int all = total(), per_xcd = all / 8;
-        const int pid = u < per_xcd * 8 ? (u % 8) * per_xcd + u / 8 : u;
-        const int tiles = tiles_i * tiles_j, g = pid / tiles;
+        const int pid = first + order.position(i), tiles = tiles_i * tiles_j, g = pid / tiles;
         int ti, tj;
         tile_coords(pid - g * tiles, tiles_i, tiles_j, Cfg::GROUP_M, ti, tj, false);
         const int b = g ? min(max(ends[g - 1], 0), M) : 0;
@@ -141,8 +224,8 @@ struct WeightUnits {
 
 // Store a wave's FN x FM blocks through its 4 KiB LDS strip as whole 128-byte
 // row pieces, 32 rows x 64 columns at a time: store_tile_staged16 with the
-// activation as an argument and the rows ending at m_end.
-template <int DT, int FN, int FM>
+// activation as an argument and the rows ending at m_end, the first FX blocks.
+template <int DT, int FX, int FN, int FM>
 __device__ __forceinline__ void store_rows_staged(uint16_t* __restrict__ C, const floatx4 (&acc)[FN][FM],
                                                   uint8_t* strip, int lane, int m_base, int n_base, int m_end, int N,
                                                   bool relu)
@@ -150,7 +233,7 @@ __device__ __forceinline__ void store_rows_staged(uint16_t* __restrict__ C, cons
     constexpr int kNonTemporal = 2;   // cache policy nt
     const int r16 = lane & 15, g = lane >> 4;
 #pragma unroll
-    for (int jj = 0; jj < FM / 2; ++jj) {
+    for (int jj = 0; jj < FX / 2; ++jj) {
         const int m_strip = m_base + 32 * jj;
         const int rows = max(0, min(32, m_end - m_strip));
         const __amdgpu_buffer_rsrc_t rc =
@@ -196,24 +279,25 @@ template <class Cfg, int DT, bool KTAIL, int ADAPT, class Units>
 __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* __restrict__ A,
                                             const uint16_t* __restrict__ B, uint16_t* __restrict__ C, uint32_t lda,
                                             uint32_t ldb, size_t b_group, size_t c_group, int N, bool relu, int c_vec,
-                                            const AdapterArgs& ad, uint8_t* smem)
+                                            const AdapterArgs& ad, const uint16_t* __restrict__ mask, uint8_t* smem)
 {
     constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK, S = Cfg::STAGES;
     constexpr int QA = Cfg::QA, QB = Cfg::QB, NQ = Cfg::NQ, FM = Cfg::FM, FN = Cfg::FN;
     constexpr int A_ROW = Cfg::A_ROW, B_ROW = Cfg::B_ROW, NKS = BK / 32;
     constexpr bool AK = Cfg::A_KMAJOR, BKM = Cfg::B_KMAJOR, WS = Cfg::PRODUCERS > 0, FIRST = ADAPT == kAdaptFirst;
+    constexpr bool STAGED = Cfg::STAGED;
     static_assert(!FIRST || (KTAIL && !AK), "the rank need not be a multiple of BK");
+    static_assert(!FIRST || !STAGED, "V is streamed by DMA");
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
     const bool producer = WS && wave >= Cfg::WAVES;
     const int dwave = WS ? wave - Cfg::WAVES : wave;
-    const int total = __builtin_amdgcn_readfirstlane(units.total());
-    const int n_units = (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int n_units = __builtin_amdgcn_readfirstlane(units.count());
     if (n_units <= 0) return;
     // Units are the same for all lanes; readfirstlane keeps them in scalar registers.
     auto unit_at = [&](int i) {
-        const DmaUnit u = units.unit((int)blockIdx.x + i * (int)gridDim.x);
+        const DmaUnit u = units.unit(i);
         return DmaUnit{__builtin_amdgcn_readfirstlane(u.m0),    __builtin_amdgcn_readfirstlane(u.m_end),
                        __builtin_amdgcn_readfirstlane(u.n0),    __builtin_amdgcn_readfirstlane(u.group),
                        __builtin_amdgcn_readfirstlane(u.k0),    __builtin_amdgcn_readfirstlane(u.k_end),
@@ -228,10 +312,10 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
     // moves on by the rows between.  k-contiguous operands: the same for every
     // tile.  k-major ones: columns past `limit` are sent out of range, so the
     // offsets are set anew for each tile.  pos: the piece's first k or column.
-    constexpr int PA = QA < 2 ? QA : 2, PB = QB < 2 ? QB : 2;
+    constexpr int PA = QA < 2 || STAGED ? QA : 2, PB = QB < 2 || STAGED ? QB : 2;
     constexpr int A_PAIR = 2048 / A_ROW, B_PAIR = 2048 / B_ROW;    // rows of two instructions
-    static_assert(QA <= 2 || (AK ? A_PAIR % 4 == 0 && 16 % (QA * A_PAIR / 2) == 0 : A_PAIR % 16 == 0), "A swizzle period");
-    static_assert(QB <= 2 || (BKM ? B_PAIR % 4 == 0 && 16 % (QB * B_PAIR / 2) == 0 : B_PAIR % 16 == 0), "B swizzle period");
+    static_assert(STAGED || QA <= 2 || (AK ? A_PAIR % 4 == 0 && 16 % (QA * A_PAIR / 2) == 0 : A_PAIR % 16 == 0), "A swizzle period");
+    static_assert(STAGED || QB <= 2 || (BKM ? B_PAIR % 4 == 0 && 16 % (QB * B_PAIR / 2) == 0 : B_PAIR % 16 == 0), "B swizzle period");
     uint32_t a_voff[PA], b_voff[PB];
     int a_pos[PA], b_pos[PB];
     auto piece = [&](int l, int q, int per_wave, auto kmajor, auto row_bytes, uint32_t ld, int limit, uint32_t& voff,
@@ -268,7 +352,7 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
     int f_unit = 0, f_k = 0, f_left = 0, f_steps = 0, f_rank = 0;
     // k-contiguous: the tile's rows and how many there are; k-major: the step's first row.
     const uint16_t *f_ap = A, *f_bp = B;
-    int f_arows = 0, f_brows = 0;
+    int f_arows = 0, f_brows = 0, f_m0 = 0, f_n0 = 0;
     int f_kb = 0, f_left_b = 0;       // B's place and what it has left, where they differ from f_k and f_left
     const int rank_steps = FIRST ? 2 * ad.rank_pad / BK : 0;
     auto fill_setup = [&](bool start) {
@@ -276,6 +360,8 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
         const DmaUnit u = unit_at(live ? f_unit : n_units - 1);
         const bool low = FIRST && start && live && u.adapter >= 0;
         f_rank = low ? rank_steps : 0;
+        f_m0 = u.m0;
+        f_n0 = u.n0;
         f_k = u.k0;
         f_left = live * (u.k_end - u.k0);
         const uint16_t *a = A, *b = B + (size_t)u.group * b_group;
@@ -363,6 +449,82 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
         }
     };
 
+    // Loads through registers, the step's pieces as the DMA would lay them out:
+    // dword-aligned 16-byte loads, with ODD also the dword after them, since a
+    // piece may start 2 bytes into its first one (`shift` of the operand's
+    // descriptor, and its row's number if the rows are odd: *_odd).  What lies
+    // past the last k is read as it comes and zeroed on the way into LDS.  Nothing
+    // is read past a matrix's last dword.  A load costs its two address
+    // instructions and the way into LDS four shifts: with predicates and shifts
+    // computed for each piece the producers set the pace (ragged bf16 rows of
+    // 4100 and 1100 elements: 1.04 us a step of 128 x 128).
+    constexpr bool ODD = Cfg::ODD;
+    struct Piece {
+        u32x4 v;
+        uint32_t next;
+    };
+    struct LoadSet {
+        Piece a[QA], b[QB], m[Cfg::MASKED == 1 ? QA : Cfg::MASKED == 2 ? QB : 1];
+        int left;
+        uint32_t shift_a, shift_b, shift_m;
+    };
+    auto load_pieces = [&](auto& to, const uint32_t* voff, const AnyRsrc& r) __attribute__((always_inline)) {
+        constexpr int Q = sizeof(to) / sizeof(Piece);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const uint32_t at = ODD ? (voff[q] + r.shift) & ~3u : voff[q];
+            to[q].v = __builtin_amdgcn_raw_buffer_load_b128(r.rsrc, at, 0, 0);
+            if constexpr (ODD) to[q].next = __builtin_amdgcn_raw_buffer_load_b32(r.rsrc, at + 16u, 0, 0);
+        }
+    };
+    auto load_set = [&](LoadSet& set) __attribute__((always_inline)) {
+        set.left = f_left;
+        const uint32_t rows = (uint32_t)min(BK, f_left), past = (uint32_t)f_k * 2u;
+        // up to the end of the last row: k-major operands start inside a row
+        const uint32_t bytes_a = AK ? (rows ? (rows * lda - (uint32_t)f_m0) * 2u : 0u)
+                                    : f_arows ? (uint32_t)f_arows * lda * 2u - past : 0u;
+        const uint32_t bytes_b = BKM ? (rows ? (rows * ldb - (uint32_t)f_n0) * 2u : 0u)
+                                     : f_brows ? (uint32_t)f_brows * ldb * 2u - past : 0u;
+        const uint16_t *pa = AK ? f_ap : f_ap + f_k, *pb = BKM ? f_bp : f_bp + f_k;
+        const AnyRsrc ra = make_any_rsrc(pa, bytes_a), rb = make_any_rsrc(pb, bytes_b);
+        set.shift_a = ra.shift;
+        set.shift_b = rb.shift;
+        load_pieces(set.a, a_voff, ra);
+        load_pieces(set.b, b_voff, rb);
+        if constexpr (Cfg::MASKED != 0) {
+            const AnyRsrc rm = Cfg::MASKED == 1 ? make_any_rsrc(mask + (pa - A), bytes_a) : make_any_rsrc(mask + (pb - B), bytes_b);
+            set.shift_m = rm.shift;
+            load_pieces(set.m, Cfg::MASKED == 1 ? a_voff : b_voff, rm);
+        }
+    };
+    auto piece_value = [&](const Piece& p, uint32_t bits) {
+        if constexpr (!ODD) return p.v;
+        else return chunk_value(AnyChunk{p.v, p.next, bits});
+    };
+    auto take_set = [&](const LoadSet& set, int to) __attribute__((always_inline)) {
+        const bool tail = set.left < BK;
+        uint8_t* const at = smem + lane * 16 + to * Cfg::A_STAGE + dwave * QA * 1024;
+        uint8_t* const bt = smem + lane * 16 + Cfg::B_REGION + to * Cfg::B_STAGE + dwave * QB * 1024;
+#pragma unroll
+        for (int q = 0; q < QA; ++q) {
+            const int row = ((dwave * QA + q) * 64 + lane) * 16 / A_ROW;
+            const uint32_t odd = (uint32_t)row & lda & 1u;
+            u32x4 v = piece_value(set.a[q], ((set.shift_a >> 1) ^ odd) * 16u);
+            if constexpr (Cfg::MASKED == 1) v = mask_chunk<DT>(v, piece_value(set.m[q], ((set.shift_m >> 1) ^ odd) * 16u));
+            if (tail) v = keep_first(v, AK ? (row < set.left ? 8 : 0) : set.left - a_pos[q]);
+            *reinterpret_cast<u32x4*>(at + q * 1024) = v;
+        }
+#pragma unroll
+        for (int q = 0; q < QB; ++q) {
+            const int row = ((dwave * QB + q) * 64 + lane) * 16 / B_ROW;
+            const uint32_t odd = (uint32_t)row & ldb & 1u;
+            u32x4 v = piece_value(set.b[q], ((set.shift_b >> 1) ^ odd) * 16u);
+            if constexpr (Cfg::MASKED == 2) v = mask_chunk<DT>(v, piece_value(set.m[q], ((set.shift_m >> 1) ^ odd) * 16u));
+            if (tail) v = keep_first(v, BKM ? (row < set.left ? 8 : 0) : set.left - b_pos[q]);
+            *reinterpret_cast<u32x4*>(bt + q * 1024) = v;
+        }
+    };
+
     // Fragment reads (gemm_relu_dma, MF = 16).
     const int kb = kgroup16(lane >> 4), g4 = lane >> 4, j16 = lane & 15;
     uint32_t a_off[AK ? FM : NKS], b_off[BKM ? FN : NKS];
@@ -392,20 +554,11 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
         for (int ks = 0; ks < NKS; ++ks)
             b_off[ks] = (uint32_t)(Cfg::B_REGION + row * B_ROW + 16 * ((4 * ks + kb) ^ a_swizzle<B_ROW>(row)));
     }
-    floatx4 acc[FN][FM];
-    auto clear = [&]() {
-#pragma unroll
-        for (int i = 0; i < FN; ++i)
-#pragma unroll
-            for (int j = 0; j < FM; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    };
-    clear();
-    u32x4 fb[2][FN], fa[2][FM];
     auto read_tr = [&](const uint8_t* p, int row) {
         const u32x2 lo = ds_read_tr16(p), hi = ds_read_tr16(p + 4 * row);
         return u32x4{lo.x, lo.y, hi.x, hi.y};
     };
-    auto read_unit = [&](int buf, int slot, int ks, int u) {
+    auto read_unit = [&](u32x4 (&fa)[2][FM], u32x4 (&fb)[2][FN], int buf, int slot, int ks, int u) {
         if (u < FM) {
             const uint8_t* st = smem + slot * Cfg::A_STAGE;
             if constexpr (AK) fa[buf][u] = read_tr(st + a_off[u] + 32 * ks * A_ROW, A_ROW);
@@ -418,8 +571,43 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
     };
     constexpr int NF = FM + FN, NMF = FM * FN;
 
+    if constexpr (STAGED) {
+        if (producer) {
+            // Set r holds step r, then r + SETS, ...; step 0 goes to LDS before the
+            // first barrier, step g + 1 while the others compute step g.
+            constexpr int R = Cfg::SETS;
+            LoadSet sets[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                load_set(sets[r]);
+                fill_advance();
+            }
+            take_set(sets[0], 0);
+            load_set(sets[0]);
+            fill_advance();
+            lds_barrier();
+            // (A round has no way out between its turns, and every load is on every path:
+            // else the compiler waits for all loads in flight at each turn.  Steps past
+            // the last load nothing and are not stored.)
+            int g = 0;
+            bool live = true;
+            while (live) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    LoadSet& set = sets[(r + 1) % R];
+                    live = f_unit < n_units || g < f_steps;
+                    ++g;
+                    if (live) take_set(set, g & 1);
+                    load_set(set);
+                    fill_advance();
+                    if (live) lds_barrier();
+                }
+            }
+            return;
+        }
+    }
     constexpr int PRO = WS ? S - 1 : S;      // steps the prologue issues
-    if (!WS || producer) {
+    if (!STAGED && (!WS || producer)) {
 #pragma unroll
         for (int s = 0; s < PRO; ++s) {
 #pragma unroll
@@ -429,7 +617,7 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
         wait_vmcnt<(PRO - 1) * NQ>();
     }
     lds_barrier();
-    if constexpr (WS) {
+    if constexpr (WS && !STAGED) {
         if (producer) {
             for (int g = 0; f_unit < n_units || g < f_steps; ++g) {
                 const int slot_fill = (g + S - 1) & (S - 1);
@@ -443,8 +631,6 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
             return;
         }
     }
-#pragma unroll
-    for (int u = 0; u < NF; ++u) read_unit(0, 0, 0, u);
     constexpr int NQC = WS ? 0 : NQ;
     constexpr int BAR_T = (!WS && NMF >= 8) ? 4 : 0;
     // Reads and, with early refill, the DMAs after the step barrier, alternately.
@@ -457,72 +643,112 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
     int c_unit = 0, slot = 0;
     DmaUnit c = unit_at(0);
     int c_k = c.k0 - (FIRST && c.adapter >= 0 ? rank_steps * BK : 0);
-    while (true) {
-        const int slot_next = (slot + 1) & (S - 1);
-        auto step_barrier = [&]() {
-            if constexpr (!WS) wait_vmcnt<(S - 2) * NQ>();
-            lds_barrier();
-        };
+    // Of a tile with fewer than BM rows a wave computes what it needs of its own
+    // rows: all 16-row blocks, the first half or none.  Their products are
+    // skipped, and so are their fragment reads (256 rows of 8 waves: a tile of at
+    // most 128 rows takes half the matrix instructions, since every SIMD has a
+    // wave of each half).  Each kind has code of its own for a whole unit, from its
+    // first fragments to its stores, so that nothing in registers passes from
+    // one kind to another.
+    int c_blocks = FM;
+    auto set_blocks = [&]() {
+        if constexpr (Units::RAGGED) {
+            const int live = c.m_end - c.m0 - wm * Cfg::WTM;
+            c_blocks = live > Cfg::WTM / 2 ? FM : live > 0 ? (FM > 1 ? FM / 2 : FM) : 0;
+        }
+    };
+    set_blocks();
+    auto step_barrier = [&]() {
+        if constexpr (!WS) wait_vmcnt<(S - 2) * NQ>();
+        lds_barrier();
+    };
+    // A unit with the first FX of FM blocks of rows.
+    auto run = [&](auto blocks) __attribute__((always_inline)) {
+        constexpr int FX = decltype(blocks)::value;
+        if constexpr (FX == 0) {
+            for (; c_k < c.k_end; c_k += BK) {
+                step_barrier();
+                if constexpr (!WS) {
 #pragma unroll
-        for (int ks = 0; ks < NKS; ++ks) {
-            const int cur = ks & 1, nxt = cur ^ 1;
-            const bool last = ks == NKS - 1;
-            if (last && BAR_T == 0) step_barrier();
-            const bool dma_ks = last;
-            const int n_items = NF + (dma_ks ? NQC : 0);
-#pragma unroll
-            for (int t = 0; t < NMF; ++t) {
-                if (last && BAR_T > 0 && t == BAR_T) step_barrier();
-                const int bi = t / FM, bj = (bi & 1) ? FM - 1 - t % FM : t % FM;
-                acc[bi][bj] = mfma_16x16x32<DT>(fb[cur][bi], fa[cur][bj], acc[bi][bj]);
-                const int t0 = last ? t - BAR_T : t, span = last ? NMF - BAR_T : NMF;
-                if (t0 < 0) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    continue;
+                    for (int q = 0; q < NQ; ++q) dma(slot, q);
+                    fill_advance();
                 }
+                slot = (slot + 1) & (S - 1);
+            }
+            return;
+        } else {
+            floatx4 acc[FN][FM];
+            u32x4 fb[2][FN], fa[2][FM];
 #pragma unroll
-                for (int u0 = t0 * n_items / span; u0 < (t0 + 1) * n_items / span; ++u0) {
-                    const int u = dma_ks ? item(u0) : u0;
-                    if (u < NF) {
-                        if (last) read_unit(nxt, slot_next, 0, u);
-                        else read_unit(nxt, slot, ks + 1, u);
-                    } else {
-                        dma(slot, u - NF);
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int u = 0; u < NF; ++u)
+                if (u < FX || u >= FM) read_unit(fa, fb, 0, slot, 0, u);
+            while (true) {
+                const int slot_next = (slot + 1) & (S - 1);
+#pragma unroll
+                for (int ks = 0; ks < NKS; ++ks) {
+                    const int cur = ks & 1, nxt = cur ^ 1;
+                    const bool last = ks == NKS - 1;
+                    if (last && BAR_T == 0) step_barrier();
+                    const int n_items = NF + (last ? NQC : 0);
+#pragma unroll
+                    for (int t = 0; t < NMF; ++t) {
+                        if (last && BAR_T > 0 && t == BAR_T) step_barrier();
+                        const int bi = t / FM, bj = (bi & 1) ? FM - 1 - t % FM : t % FM;
+                        if (bj < FX) acc[bi][bj] = mfma_16x16x32<DT>(fb[cur][bi], fa[cur][bj], acc[bi][bj]);
+                        const int t0 = last ? t - BAR_T : t, span = last ? NMF - BAR_T : NMF;
+                        if (t0 < 0) {
+                            __builtin_amdgcn_sched_barrier(0);
+                            continue;
+                        }
+#pragma unroll
+                        for (int u0 = t0 * n_items / span; u0 < (t0 + 1) * n_items / span; ++u0) {
+                            const int u = last ? item(u0) : u0;
+                            if (u < NF) {
+                                if (u >= FX && u < FM) continue;
+                                if (last) read_unit(fa, fb, nxt, slot_next, 0, u);
+                                else read_unit(fa, fb, nxt, slot, ks + 1, u);
+                            } else {
+                                dma(slot, u - NF);
+                            }
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
                     }
+                    if (!WS && last) fill_advance();
                 }
-                __builtin_amdgcn_sched_barrier(0);
+                slot = slot_next;
+                c_k += BK;
+                if (FIRST && c_k == 0 && c.adapter >= 0) {
+                    int l = j16;
+                    asm volatile("" : "+v"(l));
+                    float f[FX];
+#pragma unroll
+                    for (int j = 0; j < FX; ++j) {
+                        const int m = c.m0 + wm * Cfg::WTM + 16 * j + l;
+                        f[j] = m < c.m_end ? ad.factor[m] : 1.0f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < FX; ++j)
+#pragma unroll
+                        for (int i = 0; i < FN; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[i][j][e] *= f[j];
+                }
+                if (c_k >= c.k_end) break;
             }
-            if (!WS && dma_ks) fill_advance();
-        }
-        slot = slot_next;
-        c_k += BK;
-        if (FIRST && c_k == 0 && c.adapter >= 0) {
-            int l = j16;
-            asm volatile("" : "+v"(l));
-            float f[FM];
-#pragma unroll
-            for (int j = 0; j < FM; ++j) {
-                const int m = c.m0 + wm * Cfg::WTM + 16 * j + l;
-                f[j] = m < c.m_end ? ad.factor[m] : 1.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < FM; ++j)
-#pragma unroll
-                for (int i = 0; i < FN; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][j][e] *= f[j];
-        }
-        if (c_k >= c.k_end) {
             const int m_base = c.m0 + wm * Cfg::WTM, n_base = c.n0 + wn * Cfg::WTN;
             if constexpr (ADAPT == kAdaptAfter)
-                add_adapters<DT, !BKM>(acc, ad, m_base, c.m_end, n_base, N, lane,
-                                                  smem + Cfg::LDS_BYTES + wave * kAdapterStrip<FN>);
+                add_adapters<DT, !BKM, FX>(acc, ad, m_base, c.m_end, n_base, N, lane,
+                                           smem + Cfg::LDS_BYTES + wave * kAdapterStrip<FN>);
             uint16_t* out = C + (size_t)c.group * c_group;
             bool staged = false;
             if constexpr (Cfg::C_STAGED) {
                 if (c_vec == 2) {
-                    store_rows_staged<DT>(out, acc, smem + Cfg::LDS_BYTES + wave * 4096, lane, m_base, n_base, c.m_end, N,
-                                          relu);
+                    store_rows_staged<DT, FX>(out, acc, smem + Cfg::LDS_BYTES + wave * 4096, lane, m_base, n_base, c.m_end,
+                                              N, relu);
                     staged = true;
                 }
             }
@@ -530,49 +756,54 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
 #pragma unroll
                 for (int i = 0; i < FN; ++i)
 #pragma unroll
-                    for (int j = 0; j < FM; ++j)
+                    for (int j = 0; j < FX; ++j)
                         store_cols<DT>(out, acc[i][j], m_base + 16 * j + j16, n_base + 16 * i + 4 * g4, c.m_end, N, relu,
                                        c_vec);
             }
-            if (++c_unit >= n_units) break;
-            clear();
-            c = unit_at(c_unit);
-            c_k = c.k0 - (FIRST && c.adapter >= 0 ? rank_steps * BK : 0);
-            if constexpr (ADAPT == kAdaptAfter) {   // the registers of the next fragments were free meanwhile
-#pragma unroll
-                for (int u = 0; u < NF; ++u) read_unit(0, slot, 0, u);
-            }
         }
+    };
+    while (true) {
+        if constexpr (Units::RAGGED) {
+            if (c_blocks == FM) run(std::integral_constant<int, FM>{});
+            else if (FM > 1 && c_blocks > 0) run(std::integral_constant<int, FM / 2>{});
+            else run(std::integral_constant<int, 0>{});
+        } else {
+            run(std::integral_constant<int, FM>{});
+        }
+        if (++c_unit >= n_units) break;
+        c = unit_at(c_unit);
+        set_blocks();
+        c_k = c.k0 - (FIRST && c.adapter >= 0 ? rank_steps * BK : 0);
     }
     wait_vmcnt<0>();   // no LDS DMA may outlive the workgroup
 }
 
 // Rows of no group: this launch's workgroups share their zeros.
-__device__ __forceinline__ void zero_rows(const RowsArgs& a, int first)
+__device__ __forceinline__ void zero_rows(const RowsArgs& a, int first, int block, int blocks)
 {
     const size_t n = (size_t)a.n, count = (size_t)(a.m - first) * n;
     uint16_t* p = a.c + (size_t)first * n;
-    const size_t stride = (size_t)gridDim.x * blockDim.x;
-    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < count; i += stride) p[i] = 0;
+    const size_t stride = (size_t)blocks * blockDim.x;
+    for (size_t i = (size_t)block * blockDim.x + threadIdx.x; i < count; i += stride) p[i] = 0;
 }
 
-template <class Cfg, int DT, bool KTAIL, int ADAPT>
+template <class Cfg, int DT, bool KTAIL, int ADAPT, bool MANY = true>
 __global__ __launch_bounds__(Cfg::THREADS, 1) void rows_dma(RowsArgs a, AdapterArgs ad)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t
         smem[Cfg::LDS_BYTES + Cfg::C_STAGE_BYTES + (ADAPT == kAdaptAfter ? Cfg::ADAPT_BYTES : 0)];
-    RowUnits<Cfg> units;
+    RowUnits<Cfg, MANY> units;
     if constexpr (ADAPT == kAdaptFirst) {
-        units.init(a, ad.ends, ad.segments, true, threadIdx.x & 63);
-        units.ids = ad.ids;
+        units.init(a, ad.ends, ad.segments, true, threadIdx.x & 63, blockIdx.x, gridDim.x);
+        units.ids = ad.ids;   // (init leaves none)
         units.adapters = ad.adapters;
     } else {
-        units.init(a, a.ends, a.groups, false, threadIdx.x & 63);
-        if (units.rows < a.m) zero_rows(a, units.rows);
+        units.init(a, a.ends, a.groups, false, threadIdx.x & 63, blockIdx.x, gridDim.x);
+        if (units.rows < a.m) zero_rows(a, units.rows, blockIdx.x, gridDim.x);
     }
     dma_product<Cfg, DT, KTAIL, ADAPT>(units, a.a, a.b, a.c, (uint32_t)a.k, (uint32_t)(Cfg::B_KMAJOR ? a.n : a.k),
                                        ADAPT == kAdaptFirst ? 0 : (size_t)a.k * (size_t)a.n, 0, a.n, a.relu != 0, a.c_vec,
-                                       ad, smem);
+                                       ad, nullptr, smem);
 }
 
 template <class Cfg, int DT>
@@ -580,9 +811,37 @@ __global__ __launch_bounds__(Cfg::THREADS, 1) void weight_dma(WeightArgs a)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES + Cfg::C_STAGE_BYTES];
     WeightUnits<Cfg> units;
-    units.init(a, 0);
+    units.init(a, blockIdx.x, gridDim.x);
     dma_product<Cfg, DT, false, kAdaptNone>(units, a.p, a.q, a.out, (uint32_t)a.i, (uint32_t)a.j, 0,
-                                       (size_t)a.i * (size_t)a.j, a.j, false, a.c_vec, AdapterArgs{}, smem);
+                                       (size_t)a.i * (size_t)a.j, a.j, false, a.c_vec, AdapterArgs{}, nullptr, smem);
+}
+
+// Both gradients of a grouped product in one launch, D = dC masked on the way
+// into LDS: workgroups 0 .. blocks_rows - 1 compute dA (`rows`: A is dC), the
+// others dB (`weights`: p or q is dC, CfgW::MASKED says which).
+template <class CfgR, class CfgW, int DT, bool MANY>
+__global__ __launch_bounds__(CfgR::THREADS, 1) void grad_staged(RowsArgs rows, WeightArgs weights, const uint16_t* mask,
+                                                                int blocks_rows)
+{
+    static_assert(CfgR::THREADS == CfgW::THREADS, "one launch");
+    constexpr int LDS_R = CfgR::LDS_BYTES + CfgR::C_STAGE_BYTES, LDS_W = CfgW::LDS_BYTES + CfgW::C_STAGE_BYTES;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS_R > LDS_W ? LDS_R : LDS_W];
+    const int block = (int)blockIdx.x;
+    if (block < blocks_rows) {
+        RowUnits<CfgR, MANY> units;
+        units.init(rows, rows.ends, rows.groups, false, threadIdx.x & 63, block, blocks_rows);
+        if (units.rows < rows.m) zero_rows(rows, units.rows, block, blocks_rows);
+        dma_product<CfgR, DT, true, kAdaptNone>(units, rows.a, rows.b, rows.c, (uint32_t)rows.k,
+                                                (uint32_t)(CfgR::B_KMAJOR ? rows.n : rows.k),
+                                                (size_t)rows.k * (size_t)rows.n, 0, rows.n, false, rows.c_vec, AdapterArgs{},
+                                                mask, smem);
+    } else {
+        WeightUnits<CfgW> units;
+        units.init(weights, block - blocks_rows, (int)gridDim.x - blocks_rows);
+        dma_product<CfgW, DT, false, kAdaptNone>(units, weights.p, weights.q, weights.out, (uint32_t)weights.i,
+                                                 (uint32_t)weights.j, 0, (size_t)weights.i * (size_t)weights.j, weights.j,
+                                                 false, weights.c_vec, AdapterArgs{}, mask, smem);
+    }
 }
 
 }  // namespace gemm_relu_hip

@@ -1,20 +1,11 @@
-// The kernel instances of gemm_relu_groups.h for one dtype, as a table of
-// kernel addresses (groups_table.hpp); each dtype's translation unit fills one.
+// The kernel instances of gemm_relu_groups.h, as tables of kernel addresses
+// (groups_table.hpp); for each dtype one translation unit fills each.
 #pragma once
 
 #include "groups_dma.hpp"
 #include "groups_kernels.hpp"
 
 namespace gemm_relu_hip {
-
-template <int DT, int W>
-void fill_group_width(GroupKernels& t)
-{
-    constexpr int VEC = kLoadWidths[W];
-    t.rows_tiled[0][W] = (const void*)&rows_tiled<DT, false, VEC>;
-    t.rows_tiled[1][W] = (const void*)&rows_tiled<DT, true, VEC>;
-    t.weight_tiled[W] = (const void*)&weight_tiled<DT, VEC>;
-}
 
 // The LDS-DMA tile of a position of kGroupTile.
 template <int T, bool A_KMAJOR, bool B_KMAJOR>
@@ -50,14 +41,49 @@ void fill_group_tile(GroupKernels& t)
     t.weight_dma[T] = (const void*)&weight_dma<typename GroupTile<T, true, true>::Cfg, DT>;
 }
 
+// The register-staged tiles of a position of kStagedTile.  The large one keeps
+// two steps of loads in flight (three would need more than 256 registers with a
+// mask), the small one three.
+template <int T, bool AK, bool BK, int MASKED, bool ODD>
+using StagedTile = GroupDmaConfig<kStagedTile[T], kStagedTile[T], 2, 2, 2, AK, BK, 4, T == 0 ? 2 : 3, MASKED, ODD>;
+
+template <int DT, int T, bool B_NK, bool ODD, bool MANY>
+void fill_grad(StagedKernels& t)
+{
+    // dA = D @ B^T: for B stored (K, N) B_NK is true here, and dB = A^T @ D (q is D)
+    t.grad[T][B_NK][0][MANY] =
+        (const void*)&grad_staged<StagedTile<T, false, !B_NK, 0, ODD>, StagedTile<T, true, true, 0, ODD>, DT, MANY>;
+    t.grad[T][B_NK][1][MANY] = (const void*)&grad_staged<StagedTile<T, false, !B_NK, 1, ODD>,
+                                                         StagedTile<T, true, true, B_NK ? 2 : 1, ODD>, DT, MANY>;
+}
+
+template <int DT, int T, bool B_NK, bool ODD>
+void fill_staged(StagedKernels& t)
+{
+    using Rows = StagedTile<T, false, !B_NK, 0, ODD>;
+    static_assert(Rows::THREADS == kStagedThreads, "host tile table out of date");
+    t.rows[T][B_NK][0][0] = (const void*)&rows_dma<Rows, DT, true, kAdaptNone, false>;
+    t.rows[T][B_NK][0][1] = (const void*)&rows_dma<Rows, DT, true, kAdaptNone, true>;
+    t.rows[T][B_NK][1][0] = t.rows[T][B_NK][1][1] = (const void*)&rows_dma<Rows, DT, true, kAdaptAfter, false>;
+    fill_grad<DT, T, B_NK, ODD, false>(t);
+    fill_grad<DT, T, B_NK, ODD, true>(t);
+}
+
+template <int DT, bool ODD>
+StagedKernels make_staged_table()
+{
+    StagedKernels t{};
+    fill_staged<DT, 0, false, ODD>(t);
+    fill_staged<DT, 0, true, ODD>(t);
+    fill_staged<DT, 1, false, ODD>(t);
+    fill_staged<DT, 1, true, ODD>(t);
+    return t;
+}
+
 template <int DT>
 GroupKernels make_group_table()
 {
     GroupKernels t{};
-    fill_group_width<DT, 0>(t);
-    fill_group_width<DT, 1>(t);
-    fill_group_width<DT, 2>(t);
-    fill_group_width<DT, 3>(t);
     fill_group_tile<DT, 0>(t);
     fill_group_tile<DT, 1>(t);
     fill_group_tile<DT, 2>(t);

@@ -192,8 +192,8 @@ __device__ __forceinline__ void load_dwords_any(const uint16_t* p, int valid, ui
 template <int FN>
 constexpr int kAdapterStrip = 32 * FN * 16 * 2;
 
-// Add the low-rank terms of rows m_base .. (those below m_end) to FN x FM blocks
-// of C^T, block (i, j): rows m_base + 16j .. +15, columns n_base + 16i .. +15.
+// Add the low-rank terms of rows m_base .. (those below m_end) to the first FX
+// of FN x FM blocks of C^T, block (i, j): rows m_base + 16j .. +15, columns n_base + 16i .. +15.
 //  A row's term is (its intermediate, hi + lo times a power of two) @ (its
 // adapter's V).  Rows of a 16-row block may use several adapters:
 // for each of them the block's product is computed in registers of its own, and
@@ -205,7 +205,7 @@ constexpr int kAdapterStrip = 32 * FN * 16 * 2;
 // requests) would read a V for each, one after the other.  Its lanes compute
 // their own row's 4 columns instead, by fp32 multiply-adds over the rank, with
 // all loads of 8 rank entries in flight together.
-template <int DT, bool B_NK, int FN, int FM>
+template <int DT, bool B_NK, int FX, int FN, int FM>
 __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const AdapterArgs& ad, int m_base, int m_end,
                                              int n_base, int N, int lane, uint8_t* strip)
 {
@@ -215,7 +215,7 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
     const uint32_t t_row = (uint32_t)ad.rank_pad * 4u;
     const __amdgpu_buffer_rsrc_t rt = make_rsrc(ad.t, (uint32_t)m_end * t_row);
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
+    for (int j = 0; j < FX; ++j) {
         floatx4 sum[FN];
 #pragma unroll
         for (int i = 0; i < FN; ++i) sum[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -509,184 +509,6 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs a)
     if (col == 0) a.factor[m] = ldexpf(1.0f, e);
 }
 
-// ---------------------------------------------------------------- register-staged kernel
-
-// One operand of the register-staged kernels: a 128-row tile of a matrix whose
-// product index k runs along its rows (K_ROWS = false: rows of the tile are rows
-// of the matrix, k-contiguous) or down its columns (K_ROWS = true: rows of the
-// matrix are k; transposed on the way into LDS).  Either way LDS holds 128 rows
-// of 64 consecutive k, swizzled by lds_off.
-template <bool K_ROWS, int VEC>
-struct StagedOperand {
-    static constexpr int ROWS = 128, BK = 64, THREADS = 256;
-    const uint16_t* base;   // K_ROWS: the matrix; else the tile's first row
-    uint32_t ld;            // row length of the matrix
-    int first, limit;       // K_ROWS: the tile's first column and their number in all; else 0 and its valid rows
-    u32x4 r[4];
-
-    __device__ __forceinline__ void load(int k0, int k_end, int tid)
-    {
-        if constexpr (K_ROWS) {
-            const int col = first + (tid % 16) * 8, kb = (tid / 16) * 4;
-            const int valid = max(0, min(BK, k_end - k0));
-            const __amdgpu_buffer_rsrc_t rs = make_rsrc(base + (size_t)k0 * ld, (uint32_t)valid * ld * 2u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                r[i] = load_chunk<VEC>(rs, ((uint32_t)(kb + i) * ld + (uint32_t)col) * 2u,
-                                       [&](int p) { return kb + i < valid && col + p * VEC < limit; });
-        } else {
-            const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, (uint32_t)limit * ld * 2u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int q = tid + i * THREADS, row = q / 8, k = k0 + (q % 8) * 8;
-                r[i] = load_chunk<VEC>(rs, ((uint32_t)row * ld + (uint32_t)k) * 2u,
-                                       [&](int p) { return k + p * VEC < k_end; });
-            }
-        }
-    }
-
-    __device__ __forceinline__ void store(uint8_t* lds, int tid) const
-    {
-        if constexpr (K_ROWS) {
-            const int nb = tid % 16, kb = tid / 16;      // 8 columns, 4 k
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                const uint32_t sel = (n & 1) ? 0x07060302u : 0x05040100u;
-                u32x2 v;
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    v[p] = __builtin_amdgcn_perm(r[2 * p + 1][n >> 1], r[2 * p][n >> 1], sel);
-                *reinterpret_cast<u32x2*>(lds + lds_off(nb * 8 + n, kb >> 1) + (kb & 1) * 8) = v;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int q = tid + i * THREADS;
-                *reinterpret_cast<u32x4*>(lds + lds_off(q / 8, q % 8)) = r[i];
-            }
-        }
-    }
-};
-
-// The 128 x 128 product of two staged operands over k_begin .. k_end - 1, by 4
-// waves of 64 x 64: two LDS stages, the next K-step's loads in flight (in
-// registers) while the current one's MFMAs run.
-template <int DT, class OpM, class OpN>
-__device__ __forceinline__ void staged_product(floatx4 (&acc)[4][4], OpM& rows, OpN& cols, int k_begin, int k_end,
-                                               uint8_t* smem)
-{
-    constexpr int TILE = 128 * 128;    // bytes of one operand's stage
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = wave >> 1, wn = wave & 1;
-    const int steps = (k_end - k_begin + 63) / 64;
-    if (steps <= 0) return;
-    rows.load(k_begin, k_end, tid);
-    cols.load(k_begin, k_end, tid);
-    rows.store(smem, tid);
-    cols.store(smem + TILE, tid);
-    __syncthreads();
-    for (int s = 0; s < steps; ++s) {
-        const uint8_t* stage = smem + (s & 1) * 2 * TILE;
-        if (s + 1 < steps) {
-            rows.load(k_begin + 64 * (s + 1), k_end, tid);
-            cols.load(k_begin + 64 * (s + 1), k_end, tid);
-        }
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            const int chunk = ks * 4 + kgroup16(lane >> 4);
-            u32x4 fn[4], fm[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                fn[i] = *reinterpret_cast<const u32x4*>(stage + TILE + lds_off(wn * 64 + i * 16 + (lane & 15), chunk));
-                fm[i] = *reinterpret_cast<const u32x4*>(stage + lds_off(wm * 64 + i * 16 + (lane & 15), chunk));
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = mfma_16x16x32<DT>(fn[i], fm[j], acc[i][j]);
-        }
-        if (s + 1 < steps) {
-            uint8_t* next = smem + ((s + 1) & 1) * 2 * TILE;
-            rows.store(next, tid);
-            cols.store(next + TILE, tid);
-        }
-        __syncthreads();
-    }
-}
-
-// C = act(rows of A @ their group's B [+ their adapters' terms]), 128 x 128
-// tiles, any row length and alignment (VEC: elements per load, dividing the row
-// lengths).  Workgroup b: column tile b % tiles_n of row tile b / tiles_n.
-template <int DT, bool B_NK, int VEC>
-__global__ __launch_bounds__(256) void rows_tiled(RowsArgs a, AdapterArgs ad)
-{
-    __shared__ __attribute__((aligned(16))) uint8_t smem[4 * 128 * 128];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int tiles_n = (a.n + 127) / 128;
-    const RowTile tile = find_row_tile(a.ends, a.groups, a.m, 128, blockIdx.x / tiles_n, lane);
-    if (tile.group < 0) return;
-    const int n0 = (blockIdx.x % tiles_n) * 128;
-    const size_t k_len = (size_t)a.k, n_len = (size_t)a.n;
-
-    floatx4 acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int m_base = tile.begin + (wave >> 1) * 64, n_base = n0 + (wave & 1) * 64;
-    if (tile.group < a.groups) {
-        const uint16_t* b = a.b + (size_t)tile.group * k_len * n_len;
-        StagedOperand<false, VEC> rows{a.a + (size_t)tile.begin * k_len, (uint32_t)a.k, 0, tile.end - tile.begin, {}};
-        StagedOperand<!B_NK, VEC> cols{B_NK ? b + (size_t)n0 * k_len : b, (uint32_t)(B_NK ? a.k : a.n),
-                                       B_NK ? 0 : n0, B_NK ? min(128, a.n - n0) : a.n, {}};
-        staged_product<DT>(acc, rows, cols, 0, a.k, smem);
-        if (ad.v)   // (every wave is past its last read of LDS)
-            add_adapters<DT, B_NK>(acc, ad, m_base, tile.end, n_base, a.n, lane, smem + wave * kAdapterStrip<4>);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            store_cols<DT>(a.c, acc[i][j], m_base + 16 * j + (lane & 15), n_base + 16 * i + 4 * (lane >> 4), tile.end,
-                           a.n, a.relu != 0, a.c_vec);
-}
-
-// out[g] = p^T q over group g's rows, 128 x 128 tiles, any row length and
-// alignment.  Workgroup b: tile b % tiles of group b / tiles.
-template <int DT, int VEC>
-__global__ __launch_bounds__(256) void weight_tiled(WeightArgs a)
-{
-    __shared__ __attribute__((aligned(16))) uint8_t smem[4 * 128 * 128];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int tiles_j = (a.j + 127) / 128, tiles = (a.i + 127) / 128 * tiles_j;
-    const int g = blockIdx.x / tiles, t = blockIdx.x % tiles;
-    const int i0 = t / tiles_j * 128, j0 = t % tiles_j * 128;
-    // The group's rows: the running maximum of the ends before it and with it.
-    int begin = 0, end = 0;
-    for (int g0 = 0, start = 0; g0 <= g; g0 += 64) {
-        const GroupRows r = load_group_rows(a.ends, a.groups, a.m, g0, start, lane);
-        begin = __builtin_amdgcn_readlane(r.begin, min(g - g0, 63));
-        end = __builtin_amdgcn_readlane(r.end, min(g - g0, 63));
-        start = end;
-    }
-    floatx4 acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    StagedOperand<true, VEC> rows{a.p, (uint32_t)a.i, i0, a.i, {}};
-    StagedOperand<true, VEC> cols{a.q, (uint32_t)a.j, j0, a.j, {}};
-    staged_product<DT>(acc, rows, cols, begin, end, smem);
-    const int m_base = i0 + (wave >> 1) * 64, n_base = j0 + (wave & 1) * 64;
-    uint16_t* out = a.out + (size_t)g * (size_t)a.i * (size_t)a.j;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            store_cols<DT>(out, acc[i][j], m_base + 16 * j + (lane & 15), n_base + 16 * i + 4 * (lane >> 4), a.i, a.j,
-                           false, a.c_vec);
-}
-
 // ---------------------------------------------------------------- ReLU's gradient
 
 // d = dc where c > 0, else +0.0 (c's sign decides: 16-bit floats above zero are
@@ -699,19 +521,24 @@ __device__ __forceinline__ uint16_t mask_one(uint16_t dc, uint16_t c)
 }
 
 template <int DT>
+__device__ __forceinline__ u32x4 mask_chunk(u32x4 dc, u32x4 c)
+{
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+        dc[w] = (uint32_t)mask_one<DT>((uint16_t)dc[w], (uint16_t)c[w]) |
+                ((uint32_t)mask_one<DT>((uint16_t)(dc[w] >> 16), (uint16_t)(c[w] >> 16)) << 16);
+    return dc;
+}
+
+template <int DT>
 __global__ __launch_bounds__(256) void relu_mask(MaskArgs a)
 {
     const int64_t stride = (int64_t)gridDim.x * blockDim.x;
     const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int64_t chunks = a.vec ? a.count / 8 : 0;
     for (int64_t q = first; q < chunks; q += stride) {
-        const u32x4 g = reinterpret_cast<const u32x4*>(a.dc)[q], c = reinterpret_cast<const u32x4*>(a.c)[q];
-        u32x4 r;
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-            r[w] = (uint32_t)mask_one<DT>((uint16_t)g[w], (uint16_t)c[w]) |
-                   ((uint32_t)mask_one<DT>((uint16_t)(g[w] >> 16), (uint16_t)(c[w] >> 16)) << 16);
-        reinterpret_cast<u32x4*>(a.d)[q] = r;
+        reinterpret_cast<u32x4*>(a.d)[q] =
+            mask_chunk<DT>(reinterpret_cast<const u32x4*>(a.dc)[q], reinterpret_cast<const u32x4*>(a.c)[q]);
     }
     for (int64_t q = chunks * 8 + first; q < a.count; q += stride) a.d[q] = mask_one<DT>(a.dc[q], a.c[q]);
 }

@@ -64,9 +64,6 @@ struct MaskArgs {
     int vec;               // 16-byte aligned pointers
 };
 
-// Load widths with an instance of the register-staged kernels, widest first.
-constexpr int kNumLoadWidths = 4;
-constexpr int kLoadWidths[kNumLoadWidths] = {8, 4, 2, 1};
 constexpr int kMaxRank = 256;
 constexpr int kShrinkRows = 16, kShrinkCols = 32, kShrinkK = 128, kShrinkThreads = 512;
 
@@ -75,17 +72,34 @@ constexpr int kNumGroupTiles = 3;
 constexpr int kGroupTile[kNumGroupTiles] = {256, 128, 64};
 constexpr int kGroupThreads[kNumGroupTiles] = {512, 512, 512};
 
+// Square tiles staged through registers (GEMM_RELU_GROUPS_TILED), large and small.
+constexpr int kNumStagedTiles = 2;
+constexpr int kStagedTile[kNumStagedTiles] = {128, 64};
+constexpr int kStagedThreads = 512;
+
+// The register-staged kernels: dwords may hold two rows' elements (any row
+// length and 2-byte alignment), or not (even rows, 4-byte alignment).
+struct StagedKernels {
+    const void* rows[kNumStagedTiles][2][2][2];   // [tile][B layout][with adapters][more than 64 groups]
+    // Both gradients: [tile][B layout of dA's product][masked][more than 64 groups].
+    // dA's product reads B stored (K, N) as (N, K) rows and the other way round,
+    // and dB of the one is A^T D, of the other D^T A.
+    const void* grad[kNumStagedTiles][2][2][2];
+};
+
 struct GroupKernels {
     // [tile][B layout][K % 64 != 0][with adapters]; with adapters the 256 tile takes any K and starts from their terms
     const void* rows_dma[kNumGroupTiles][2][2][2];
     const void* weight_dma[kNumGroupTiles];
-    const void* rows_tiled[2][kNumLoadWidths];    // [B layout][load width]
-    const void* weight_tiled[kNumLoadWidths];
     const void* mask;
     const void* shrink[2];                        // [U layout]
 };
 
 const GroupKernels& group_kernels_f16();
 const GroupKernels& group_kernels_bf16();
+const StagedKernels& staged_kernels_f16_even();
+const StagedKernels& staged_kernels_f16_odd();
+const StagedKernels& staged_kernels_bf16_even();
+const StagedKernels& staged_kernels_bf16_odd();
 
 }  // namespace gemm_relu_hip
