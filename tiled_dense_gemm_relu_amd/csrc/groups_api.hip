@@ -73,7 +73,7 @@ int check_workspace(void* workspace, int64_t bytes, int64_t need)
 // Whether LDS DMA can read a matrix: rows of whole 16-byte pieces.
 bool dma_rows(const void* p, int64_t row) { return row % 8 == 0 && aligned(p, 16); }
 
-int store_width(const void* c, int64_t n) { return n % 8 == 0 && aligned(c, 16) ? 2 : n % 4 == 0 && aligned(c, 8) ? 1 : 0; }
+int store_width(const void* c, int64_t n) { return n % 8 == 0 && aligned(c, 16) ? 2 : 0; }
 
 const GroupKernels& kernels(int dtype) { return dtype == GEMM_RELU_F16 ? group_kernels_f16() : group_kernels_bf16(); }
 

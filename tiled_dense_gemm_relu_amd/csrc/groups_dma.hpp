@@ -40,11 +40,11 @@ struct GroupDmaConfig {
     static constexpr int A_ROW = A_KMAJOR ? BM * 2 : BK * 2, B_ROW = B_KMAJOR ? BN * 2 : BK * 2;
     static constexpr int A_STAGE = BM * BK * 2, B_STAGE = BN * BK * 2, B_REGION = STAGES * A_STAGE;
     static constexpr int LDS_BYTES = STAGES * (A_STAGE + B_STAGE);
-    static constexpr bool C_STAGED = WTN % 64 == 0 && WTM % 32 == 0 && LDS_BYTES + WAVES * 4096 <= 160 * 1024;
-    static constexpr int C_STAGE_BYTES = C_STAGED ? WAVES * 4096 : 0;
-    // Adapters stage V there too, or in strips of their own.
-    static constexpr int ADAPT_BYTES = C_STAGED ? 0 : WAVES * kAdapterStrip<FN>;
-    static_assert(!C_STAGED || kAdapterStrip<FN> <= 4096, "V's strip");
+    // Each compute wave's strip of LDS, 32 rows of its columns of C on their way to
+    // memory.  Adapters stage V there.
+    static constexpr int STRIP = 32 * WTN * 2, STRIP_BYTES = WAVES * STRIP;
+    static_assert(WTM % 32 == 0 && (WTN == 64 || WTN == 32) && LDS_BYTES + STRIP_BYTES <= 160 * 1024, "strips");
+    static_assert(kAdapterStrip<FN> <= STRIP, "V's strip");
     static constexpr int QA = A_STAGE / 1024 / DMA_WAVES, QB = B_STAGE / 1024 / DMA_WAVES, NQ = QA + QB;
     static_assert(QA * DMA_WAVES * 1024 == A_STAGE && QB * DMA_WAVES * 1024 == B_STAGE, "whole DMA instructions");
     static_assert((STAGES & (STAGES - 1)) == 0 && STAGES >= 2 && LDS_BYTES <= 160 * 1024, "ring");
@@ -117,7 +117,7 @@ struct RowUnits {
     {
         const GroupRows r = load_group_rows(ends, groups, M, g0, start, lane);
         const int n = g0 + lane < listed ? r.end - r.begin : 0, c = cost(n);
-        const int before = wave_scan_sum(c, lane) - c;      // at most 4 (2^20 / 64 + 65536)
+        const int before = wave_scan_sum(c) - c;      // at most 4 (2^20 / 64 + 65536)
         // the first column whose work starts at or past w
         auto column = [&](int64_t w) {
             const int64_t past = w - (work + (int64_t)before * tiles_n);
@@ -128,7 +128,7 @@ struct RowUnits {
         k.end = r.end;
         k.col = column(first);
         k.cols = max(0, column(last) - k.col);
-        k.incl = units_before + wave_scan_sum((n + Cfg::BM - 1) / Cfg::BM * k.cols, lane);
+        k.incl = units_before + wave_scan_sum((n + Cfg::BM - 1) / Cfg::BM * k.cols);
         work += (int64_t)__builtin_amdgcn_readlane(before + c, 63) * tiles_n;
         units_before = __builtin_amdgcn_readlane(k.incl, 63);
         start = __builtin_amdgcn_readlane(r.end, 63);
@@ -151,7 +151,7 @@ struct RowUnits {
         rows = 0;
         for (int g0 = 0; g0 < listed; g0 += 64) {
             const GroupRows r = load_group_rows(ends, groups, M, g0, rows, lane);
-            total += __builtin_amdgcn_readlane(wave_scan_sum(g0 + lane < listed ? cost(r.end - r.begin) : 0, lane), 63);
+            total += __builtin_amdgcn_readlane(wave_scan_sum(g0 + lane < listed ? cost(r.end - r.begin) : 0), 63);
             rows = __builtin_amdgcn_readlane(r.end, min(listed - 1 - g0, 63));
         }
         total *= tiles_n;
@@ -231,6 +231,7 @@ __device__ __forceinline__ void store_rows_staged(uint16_t* __restrict__ C, cons
                                                   bool relu)
 {
     constexpr int kNonTemporal = 2;   // cache policy nt
+    asm volatile("" : "+v"(lane));    // as in store_rows_any
     const int r16 = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int jj = 0; jj < FX / 2; ++jj) {
@@ -261,6 +262,45 @@ __device__ __forceinline__ void store_rows_staged(uint16_t* __restrict__ C, cons
                 const uint32_t off = n < N ? ((uint32_t)r * (uint32_t)N + (uint32_t)n) * 2u : kOobOffset;
                 __builtin_amdgcn_raw_buffer_store_b128(v, rc, off, 0, kNonTemporal);
             }
+        }
+    }
+}
+
+// The same for rows of any length and alignment: dwords that lie on their
+// boundaries, 32 consecutive ones of a row to half a wave (16 where the wave has
+// 32 columns), and single elements at a piece's ends where a row starts inside a
+// dword.  (Storing each lane's 4 columns element by element made a request of
+// every 2 bytes: 32 against 18.5 us for the gradients of 1000 rows in 7 groups,
+// 517 x 1101 against 512 x 1104.)
+template <int DT, int FX, int FN, int FM>
+__device__ __forceinline__ void store_rows_any(uint16_t* __restrict__ C, const floatx4 (&acc)[FN][FM], uint8_t* strip,
+                                               int lane, int m_base, int n_base, int m_end, int N, bool relu)
+{
+    constexpr int ROW = FN * 32, CHUNKS = ROW / 16, LANES = FN * 8;    // bytes and 16-byte chunks of a strip's row; dwords
+    asm volatile("" : "+v"(lane));   // what follows from it is computed here, not kept through the caller's loop
+    const int r16 = lane & 15, g = lane >> 4;
+    auto at = [](int row, int chunk) { return row * ROW + ((chunk ^ ((row >> 1) & (CHUNKS - 1))) << 4); };
+#pragma unroll
+    for (int jj = 0; jj < (FX + 1) / 2; ++jj) {
+#pragma unroll
+        for (int jh = 0; jh < 2 && 2 * jj + jh < FX; ++jh)
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+                const floatx4& v = acc[i][2 * jj + jh];
+                *reinterpret_cast<u32x2*>(strip + at(16 * jh + r16, 2 * i + (g >> 1)) + 8 * (g & 1)) =
+                    u32x2{(uint32_t)act_cast<DT>(v[0], relu) | ((uint32_t)act_cast<DT>(v[1], relu) << 16),
+                          (uint32_t)act_cast<DT>(v[2], relu) | ((uint32_t)act_cast<DT>(v[3], relu) << 16)};
+            }
+        const int rows = min(2 * jj + 1 < FX ? 32 : 16, m_end - (m_base + 32 * jj)), cols = min(16 * FN, N - n_base);
+        for (int r = lane / LANES; r < rows; r += 64 / LANES) {
+            uint16_t* const p = C + (size_t)(m_base + 32 * jj + r) * (size_t)N + n_base;
+            const int odd = (int)(reinterpret_cast<uintptr_t>(p) >> 1) & 1, e = 2 * (lane % LANES) + odd;
+            auto element = [&](int x) { return *reinterpret_cast<const uint16_t*>(strip + at(r, x >> 3) + 2 * (x & 7)); };
+            if (e + 1 < cols)
+                *reinterpret_cast<uint32_t*>(p + e) = (uint32_t)element(e) | ((uint32_t)element(e + 1) << 16);
+            else if (e < cols)
+                p[e] = element(e);
+            if (odd && e == 1 && cols > 0) p[0] = element(0);
         }
     }
 }
@@ -742,23 +782,19 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
             const int m_base = c.m0 + wm * Cfg::WTM, n_base = c.n0 + wn * Cfg::WTN;
             if constexpr (ADAPT == kAdaptAfter)
                 add_adapters<DT, !BKM, FX>(acc, ad, m_base, c.m_end, n_base, N, lane,
-                                           smem + Cfg::LDS_BYTES + wave * kAdapterStrip<FN>);
+                                           smem + Cfg::LDS_BYTES + wave * Cfg::STRIP);
             uint16_t* out = C + (size_t)c.group * c_group;
-            bool staged = false;
-            if constexpr (Cfg::C_STAGED) {
-                if (c_vec == 2) {
-                    store_rows_staged<DT, FX>(out, acc, smem + Cfg::LDS_BYTES + wave * 4096, lane, m_base, n_base, c.m_end,
-                                              N, relu);
-                    staged = true;
-                }
-            }
-            if (!staged) {
+            uint8_t* const strip = smem + Cfg::LDS_BYTES + wave * Cfg::STRIP;
+            if (c_vec < 2) {
+                store_rows_any<DT, FX>(out, acc, strip, lane, m_base, n_base, c.m_end, N, relu);
+            } else if constexpr (FN % 4 == 0) {
+                store_rows_staged<DT, FX>(out, acc, strip, lane, m_base, n_base, c.m_end, N, relu);
+            } else {
 #pragma unroll
                 for (int i = 0; i < FN; ++i)
 #pragma unroll
                     for (int j = 0; j < FX; ++j)
-                        store_cols<DT>(out, acc[i][j], m_base + 16 * j + j16, n_base + 16 * i + 4 * g4, c.m_end, N, relu,
-                                       c_vec);
+                        store_cols<DT>(out, acc[i][j], m_base + 16 * j + j16, n_base + 16 * i + 4 * g4, c.m_end, N, relu);
             }
         }
     };
@@ -790,8 +826,7 @@ __device__ __forceinline__ void zero_rows(const RowsArgs& a, int first, int bloc
 template <class Cfg, int DT, bool KTAIL, int ADAPT, bool MANY = true>
 __global__ __launch_bounds__(Cfg::THREADS, 1) void rows_dma(RowsArgs a, AdapterArgs ad)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t
-        smem[Cfg::LDS_BYTES + Cfg::C_STAGE_BYTES + (ADAPT == kAdaptAfter ? Cfg::ADAPT_BYTES : 0)];
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES + Cfg::STRIP_BYTES];
     RowUnits<Cfg, MANY> units;
     if constexpr (ADAPT == kAdaptFirst) {
         units.init(a, ad.ends, ad.segments, true, threadIdx.x & 63, blockIdx.x, gridDim.x);
@@ -809,7 +844,7 @@ __global__ __launch_bounds__(Cfg::THREADS, 1) void rows_dma(RowsArgs a, AdapterA
 template <class Cfg, int DT>
 __global__ __launch_bounds__(Cfg::THREADS, 1) void weight_dma(WeightArgs a)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES + Cfg::C_STAGE_BYTES];
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES + Cfg::STRIP_BYTES];
     WeightUnits<Cfg> units;
     units.init(a, blockIdx.x, gridDim.x);
     dma_product<Cfg, DT, false, kAdaptNone>(units, a.p, a.q, a.out, (uint32_t)a.i, (uint32_t)a.j, 0,
@@ -824,7 +859,7 @@ __global__ __launch_bounds__(CfgR::THREADS, 1) void grad_staged(RowsArgs rows, W
                                                                 int blocks_rows)
 {
     static_assert(CfgR::THREADS == CfgW::THREADS, "one launch");
-    constexpr int LDS_R = CfgR::LDS_BYTES + CfgR::C_STAGE_BYTES, LDS_W = CfgW::LDS_BYTES + CfgW::C_STAGE_BYTES;
+    constexpr int LDS_R = CfgR::LDS_BYTES + CfgR::STRIP_BYTES, LDS_W = CfgW::LDS_BYTES + CfgW::STRIP_BYTES;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS_R > LDS_W ? LDS_R : LDS_W];
     const int block = (int)blockIdx.x;
     if (block < blocks_rows) {

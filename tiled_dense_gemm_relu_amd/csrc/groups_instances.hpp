@@ -42,10 +42,10 @@ void fill_group_tile(GroupKernels& t)
 }
 
 // The register-staged tiles of a position of kStagedTile.  The large one keeps
-// two steps of loads in flight (three would need more than 256 registers with a
-// mask), the small one three.
+// four steps of loads in flight, three where a mask or odd rows need more
+// registers, the small one three.
 template <int T, bool AK, bool BK, int MASKED, bool ODD>
-using StagedTile = GroupDmaConfig<kStagedTile[T], kStagedTile[T], 2, 2, 2, AK, BK, 4, T == 0 ? 2 : 3, MASKED, ODD>;
+using StagedTile = GroupDmaConfig<kStagedTile[T], kStagedTile[T], 2, 2, 2, AK, BK, 4, T == 0 && !ODD && MASKED == 0 ? 4 : 3, MASKED, ODD>;
 
 template <int DT, int T, bool B_NK, bool ODD, bool MANY>
 void fill_grad(StagedKernels& t)

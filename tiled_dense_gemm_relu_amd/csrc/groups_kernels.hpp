@@ -27,25 +27,27 @@ struct RowTile {
     int group, begin, end;
 };
 
-// Inclusive scans over the wave's 64 lanes.
-__device__ __forceinline__ int wave_scan_max(int v, int lane)
+// Inclusive scans of non-negative values over the wave's 64 lanes, by DPP moves:
+// within rows of 16 lanes (row_shr 1, 2, 4, 8), then from lane 15 of rows 0 and 2
+// to the row after them, and from lane 31 to rows 2 and 3.  Lanes without a
+// source get 0.
+template <class Op>
+__device__ __forceinline__ int wave_scan(int v, Op op)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int o = __shfl_up(v, d);
-        if (lane >= d) v = max(v, o);
-    }
-    return v;
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));
+    return op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));
 }
-
-__device__ __forceinline__ int wave_scan_sum(int v, int lane)
+__device__ __forceinline__ int wave_scan_max(int v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
-    return v;
+    return wave_scan(v, [](int a, int b) { return max(a, b); });
+}
+__device__ __forceinline__ int wave_scan_sum(int v)
+{
+    return wave_scan(v, [](int a, int b) { return a + b; });
 }
 
 // The rows of lane l's group g0 + l, for 64 groups from g0 on; `start` is where
@@ -60,9 +62,8 @@ __device__ __forceinline__ GroupRows load_group_rows(const int* __restrict__ end
     const int g = g0 + lane;
     int e = M;
     if (g < groups) e = ends ? min(max(ends[g], 0), M) : M;
-    e = max(wave_scan_max(e, lane), start);
-    const int b = __shfl_up(e, 1);
-    return GroupRows{lane == 0 ? start : b, e};
+    e = max(wave_scan_max(e), start);
+    return GroupRows{__builtin_amdgcn_update_dpp(start, e, 0x138, 0xf, 0xf, false), e};   // the lane before's end
 }
 
 // Tile number `unit` when every group's rows are cut into tiles of `rows` rows.
@@ -72,7 +73,7 @@ __device__ inline RowTile find_row_tile(const int* __restrict__ ends, int groups
     for (int g0 = 0; g0 <= groups; g0 += 64) {
         const GroupRows r = load_group_rows(ends, groups, M, g0, start, lane);
         const int tiles = (r.end - r.begin + rows - 1) / rows;
-        const int incl = tiles_before + wave_scan_sum(tiles, lane);
+        const int incl = tiles_before + wave_scan_sum(tiles);
         const uint64_t mask = __ballot(unit < incl);
         if (mask) {
             const int l = __builtin_ctzll(mask);
@@ -109,24 +110,17 @@ __device__ __forceinline__ float to_float(uint16_t h)
 }
 
 // Store one 16x16 block of C^T: lane l holds row m = (block's first row) + l % 16
-// and columns n .. n + 3.  Rows from m_end and columns from n_end on are dropped.
-// c_vec > 0: row lengths and C allow 8-byte stores.
+// and columns n .. n + 3.  Rows from m_end and columns from n_end on are dropped;
+// n_end % 4 == 0 and rows of C are 8-byte aligned.
 template <int DT>
 __device__ __forceinline__ void store_cols(uint16_t* __restrict__ C, floatx4 acc, int m, int n, int m_end, int n_end,
-                                           bool relu, int c_vec)
+                                           bool relu)
 {
-    if (m >= m_end) return;
-    uint16_t* p = C + (size_t)m * (size_t)n_end + n;
+    if (m >= m_end || n >= n_end) return;
     const uint16_t h0 = act_cast<DT>(acc[0], relu), h1 = act_cast<DT>(acc[1], relu);
     const uint16_t h2 = act_cast<DT>(acc[2], relu), h3 = act_cast<DT>(acc[3], relu);
-    if (c_vec > 0 && n + 3 < n_end) {
-        *reinterpret_cast<u32x2*>(p) = u32x2{(uint32_t)h0 | ((uint32_t)h1 << 16), (uint32_t)h2 | ((uint32_t)h3 << 16)};
-    } else {
-        if (n + 0 < n_end) p[0] = h0;
-        if (n + 1 < n_end) p[1] = h1;
-        if (n + 2 < n_end) p[2] = h2;
-        if (n + 3 < n_end) p[3] = h3;
-    }
+    *reinterpret_cast<u32x2*>(C + (size_t)m * (size_t)n_end + n) =
+        u32x2{(uint32_t)h0 | ((uint32_t)h1 << 16), (uint32_t)h2 | ((uint32_t)h3 << 16)};
 }
 
 // ---------------------------------------------------------------- rows of any alignment

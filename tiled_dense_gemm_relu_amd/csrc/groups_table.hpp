@@ -15,7 +15,7 @@ struct RowsArgs {
     const int* ends;
     int m, n, k, groups;
     int relu;
-    int c_vec;             // rows of C allow 2: 16-byte, 1: 8-byte, 0: 2-byte stores
+    int c_vec;             // 2: rows of C allow 16-byte stores, else 0
 };
 
 // The low-rank term of each row (v == nullptr: none).  Row m's adapter is

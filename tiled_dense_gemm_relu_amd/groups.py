@@ -24,6 +24,7 @@ CONFIG_DMA_64 = 3
 
 _lock = threading.Lock()
 _lib = None
+_spaces = {}               # (device, stream handle): the stream's workspace as (pointer, bytes, tensor)
 
 
 def _library():
@@ -75,7 +76,12 @@ def adapters_workspace_bytes(M: int, N: int, K: int, rank: int, adapters: int, s
 
 
 def _check_tensor(name, t, dim, dev, dtype):
+    """A contiguous ``dim``-D tensor of this dtype on device ``dev`` (one look at each property: these
+    checks are a good part of a small call's time on the host)."""
     import torch
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.dim() == dim
+            and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"gemm_relu: {name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -86,8 +92,7 @@ def _check_tensor(name, t, dim, dev, dtype):
         raise ValueError(f"gemm_relu: {name} must be contiguous (row-major)")
     if t.dtype != dtype:
         raise TypeError(f"gemm_relu: {name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"gemm_relu: {name} must be on the same device as the other tensors")
+    raise ValueError(f"gemm_relu: {name} must be on the same device as the other tensors")
 
 
 def _check_shape(name, t, shape):
@@ -113,33 +118,34 @@ def _check_layout(b_layout):
 def _new(shape, like, stream):
     """An output for work on ``stream``: allocated for that stream, so that its memory is not one
     that still belongs to other work there."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+        return like.new_empty(shape)
+    import torch
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+        return like.new_empty(shape)
 
 
-def _workspace(given, need, like, handle, stream):
-    """(pointer, bytes) of the workspace: ``given``, or the cached one of this stream, which
+def _workspace(given, need, like, dev, handle, stream):
+    """(pointer, bytes, tensor) of the workspace: ``given``, or the cached one of this stream, which
     gemm_relu_splitk's calls use too.  A capture takes memory of its own graph, so that replays stay
     valid when the cached buffer is replaced by a larger one."""
-    import torch
     if need == 0:
         return None, 0, None
+    import torch
     if given is None:
         if torch.cuda.is_current_stream_capturing():
             given = torch.empty(need, dtype=torch.uint8, device=like.device)
             given[:COUNTER_BYTES].zero_()
-        else:
-            given = binding._workspaces.get((like.device, handle))
-            if given is None or given.numel() < need:
-                s = stream if stream is not None else torch.cuda.current_stream(like.device)
-                given = binding.splitk_workspace(like.device, s, need)
-        return given.data_ptr(), given.numel(), given
+            return given.data_ptr(), need, given
+        known = _spaces.get((dev, handle))
+        if known is None or known[1] < need:
+            s = stream if stream is not None else torch.cuda.current_stream(like.device)
+            given = binding.splitk_workspace(like.device, s, need)
+            known = _spaces[(dev, handle)] = given.data_ptr(), given.numel(), given
+        return known
     if not isinstance(given, torch.Tensor) or not given.is_cuda or not given.is_contiguous():
         raise TypeError("gemm_relu: workspace must be a contiguous GPU tensor")
-    if given.get_device() != like.get_device():
+    if given.get_device() != dev:
         raise ValueError("gemm_relu: workspace must be on the same device as the other tensors")
     return given.data_ptr(), given.numel() * given.element_size(), given
 
@@ -147,13 +153,19 @@ def _workspace(given, need, like, handle, stream):
 def _call(function, dev, *args):
     """The library launches on the current device: make it the tensors' one."""
     import torch
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         rc = function(*args)
     else:
         with torch.cuda.device(dev):
             rc = function(*args)
     if rc != 0:
         _check(rc)
+
+
+def _current_device() -> int:
+    import torch
+    raw = getattr(torch._C, "_cuda_getDevice", None)
+    return raw() if raw is not None else torch.cuda.current_device()
 
 
 def gemm_relu_grouped(a, b, ends, out=None, b_layout: int = B_KN, relu: bool = True, config: int = CONFIG_AUTO,
@@ -173,8 +185,10 @@ def gemm_relu_grouped(a, b, ends, out=None, b_layout: int = B_KN, relu: bool = T
     _check_tensor("b", b, 3, dev, a.dtype)
     _check_tensor("ends", ends, 1, dev, torch.int32)
     M, K = a.shape
-    groups, N = b.shape[0], b.shape[1 if b_layout == B_NK else 2]
-    if b.shape[2 if b_layout == B_NK else 1] != K:
+    groups, N, k_b = b.shape
+    if b_layout != B_NK:
+        N, k_b = k_b, N
+    if k_b != K:
         raise ValueError(f"gemm_relu: inner dimensions differ: a {tuple(a.shape)}, b {tuple(b.shape)}")
     if ends.shape[0] != groups:
         raise ValueError(f"gemm_relu: ends must have one entry for each of {groups} groups, got {ends.shape[0]}")
@@ -184,8 +198,8 @@ def gemm_relu_grouped(a, b, ends, out=None, b_layout: int = B_KN, relu: bool = T
         _check_tensor("out", out, 2, dev, a.dtype)
         _check_shape("out", out, (M, N))
     handle = _stream_handle(stream, dev)
-    ws, ws_bytes, keep = _workspace(workspace, grouped_workspace_bytes(M, N, K, groups, code, b_layout), a, handle,
-                                    stream)
+    ws, ws_bytes, keep = _workspace(workspace, grouped_workspace_bytes(M, N, K, groups, code, b_layout), a, dev,
+                                    handle, stream)
     _call(_library().gemm_relu_grouped, dev, a.data_ptr(), b.data_ptr(), ends.data_ptr(), out.data_ptr(), M, N, K,
           groups, code, b_layout, 1 if relu else 0, config, ws, ws_bytes, handle or None)
     return out
@@ -235,7 +249,7 @@ def gemm_relu_grouped_backward(dc, c, a, b, ends, b_layout: int = B_KN, relu: bo
             _check_shape("db", db, shape)
     handle = _stream_handle(stream, dev)
     ws, ws_bytes, keep = _workspace(workspace, grouped_backward_workspace_bytes(M, N, K, groups, code, b_layout, relu),
-                                    dc, handle, stream)
+                                    dc, dev, handle, stream)
     # An empty gradient still needs an address to be asked for.
     _call(_library().gemm_relu_grouped_backward, dev, dc.data_ptr(), c.data_ptr() if relu else None,
           a.data_ptr() if need_db else None, b.data_ptr() if need_da else None, ends.data_ptr(),
@@ -282,7 +296,7 @@ def gemm_relu_adapters(x, w, u, v, scales, ends, ids, out=None, b_layout: int = 
         _check_shape("out", out, (M, N))
     handle = _stream_handle(stream, dev)
     ws, ws_bytes, keep = _workspace(workspace, adapters_workspace_bytes(M, N, K, rank, adapters, segments, code,
-                                                                        b_layout), x, handle, stream)
+                                                                        b_layout), x, dev, handle, stream)
     _call(_library().gemm_relu_adapters, dev, x.data_ptr(), w.data_ptr(), u.data_ptr(), v.data_ptr(),
           scales.data_ptr(), ends.data_ptr(), ids.data_ptr(), out.data_ptr(), M, N, K, rank, adapters, segments,
           code, b_layout, 1 if relu else 0, config, ws, ws_bytes, handle or None)
