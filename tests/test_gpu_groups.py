@@ -138,7 +138,8 @@ def test_grouped(shape, dtype, layout, relu):
 # Every kernel on shapes whose rows are 16-byte multiples (the others fall back to TILED): K-steps
 # with and without a tail, fewer steps than stages, tiles that end inside a group, several tiles of
 # work for a workgroup, more than 64 groups.
-CONFIGS = [groups.CONFIG_TILED, groups.CONFIG_DMA_256, groups.CONFIG_DMA_128, groups.CONFIG_DMA_64]
+CONFIGS = [groups.CONFIG_TILED, groups.CONFIG_DMA_256, groups.CONFIG_DMA_128, groups.CONFIG_DMA_64,
+           groups.CONFIG_STREAM]
 CONFIG_SHAPES = [
     ([1, 0, 4], 1, 64, 64),
     ([40, 0, 256, 300], 3, 264, 136),

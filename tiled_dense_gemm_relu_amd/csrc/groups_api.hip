@@ -83,10 +83,15 @@ struct Rows {
     const void* p;
     int64_t length;
 };
+bool even_rows(std::initializer_list<Rows> operands)
+{
+    for (const Rows& r : operands)
+        if (r.length % 2 != 0 || !aligned(r.p, 4)) return false;
+    return true;
+}
 const StagedKernels& staged_kernels(int dtype, std::initializer_list<Rows> operands)
 {
-    bool even = true;
-    for (const Rows& r : operands) even = even && r.length % 2 == 0 && aligned(r.p, 4);
+    const bool even = even_rows(operands);
     if (dtype == GEMM_RELU_F16) return even ? staged_kernels_f16_even() : staged_kernels_f16_odd();
     return even ? staged_kernels_bf16_even() : staged_kernels_bf16_odd();
 }
@@ -109,7 +114,7 @@ int zero_fill(void* p, int64_t halves, hipStream_t stream)
 // whole tiles, and one partial tile for each.
 int64_t most_row_tiles(int64_t M, int64_t groups, int64_t rows) { return std::min(M, M / rows + groups + 1); }
 
-bool known_config(int id) { return id >= GEMM_RELU_GROUPS_AUTO && id <= GEMM_RELU_GROUPS_DMA_64; }
+bool known_config(int id) { return id >= GEMM_RELU_GROUPS_AUTO && id <= GEMM_RELU_GROUPS_STREAM; }
 
 // Tile of an LDS-DMA product: the largest whose tiles are mostly full (`rows`:
 // a group's rows on average) and numerous enough to occupy the CUs.
@@ -134,11 +139,57 @@ int staged_tile(int64_t rows, int64_t tiles_128) { return rows >= 96 && tiles_12
 // 64 x 64 kernels on a CU).
 int64_t resident(int64_t tile, int64_t tiles, int cus) { return std::min<int64_t>(tiles, tile == 64 ? 2 * cus : cus); }
 
-// A product over row groups (M, N, K > 0).
-int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config, int cus, hipStream_t stream)
+// The streaming kernel's part in a product: which one (by kSkinnyBlocks), and
+// into how many parts K is cut: as many as make 512 workgroups, while each of
+// their 8 waves has a piece of K.  A group's rows should mostly fit a
+// workgroup's, since every further workgroup reads the weights again.
+struct SkinnyPlan {
+    int kind = -1;
+    int64_t units = 0, splits = 1, bytes = 0;
+    SkinnyPlan(int64_t m, int64_t n, int64_t k, int64_t groups)
+    {
+        if (m == 0 || n == 0 || k == 0) return;
+        const GroupShape g(m, groups);
+        const int64_t most = groups == 1 ? m : g.rows + g.rows / 2 + 6;     // few groups have more rows
+        kind = most <= 16 ? 0 : most <= 32 ? 1 : 2;
+        units = most_row_tiles(m, groups, 16 * kSkinnyBlocks[kind]) * ceil_div(n, kSkinnyCols);
+        splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(k, 8 * kSkinnyK), 512 / units));
+        if (splits > 1) bytes = units * splits * kSkinnyBlocks[kind] * kSkinnyThreads * 4;
+    }
+};
+
+// Whether to stream.  The streaming kernel starts and ends quicker than the tiles
+// and cuts K where there are few units, but every 32 columns read the rows of A
+// again and it reaches 3 TB/s, where the 64 x 64 tiles reach 5, or a K-step of 64
+// in 0.16 us (0.35 us where rows must go through registers).  Measured, us,
+// streaming against tiles, KN: 1, 8 and 16 rows x 4096 x 4096 bf16 10.9 / 16.2,
+// 15.7 / 16.3, 24.5 / 16.4; 4 rows x 16384 x 4096 55 / 27; 64 rows in 8 groups
+// 512 x 512 4.4 / 6.4; 16 rows x 300 x 8192 7.4 / 49.
+bool streams(int64_t m, int64_t n, int64_t k, int64_t groups, bool dma)
+{
+    const GroupShape g(m, groups);
+    if (g.rows > 64) return false;
+    const double weights = 2.0 * (double)g.used * (double)n * (double)k, again = 2.0 * (double)m * (double)k * (double)ceil_div(n, kSkinnyCols);
+    const double rounds = (double)ceil_div(g.tiles(64, n), 512), step = dma ? 0.16 : 0.35;
+    return 3.0 + (weights + again) / 3.2e6 < 5.5 + std::max(weights / 5e6, rounds * (double)ceil_div(k, 64) * step);
+}
+
+// A product over row groups (M, N, K > 0).  `parts` (may be NULL) and `counters`:
+// space for the streaming kernel's partial sums.
+int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config, int cus, float* parts, int* counters,
+                hipStream_t stream)
 {
     a.c_vec = store_width(a.c, a.n);
-    const bool dma = dma_rows(a.a, a.k) && dma_rows(a.b, b_layout == GEMM_RELU_B_NK ? a.k : a.n);
+    const Rows rows_a{a.a, a.k}, rows_b{a.b, b_layout == GEMM_RELU_B_NK ? a.k : a.n};
+    const bool dma = dma_rows(a.a, a.k) && dma_rows(a.b, rows_b.length);
+    if (config == GEMM_RELU_GROUPS_STREAM || (config == GEMM_RELU_GROUPS_AUTO && streams(a.m, a.n, a.k, a.groups, dma))) {
+        SkinnyPlan plan(a.m, a.n, a.k, a.groups);
+        if (plan.units > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
+        if (!parts) plan.splits = 1;
+        void* args[] = {&a, &ad, &parts, &counters};
+        return enqueue(kernels(dtype).rows_skinny[plan.kind][b_layout][!even_rows({rows_a, rows_b})][ad.v != nullptr],
+                       dim3((unsigned)plan.units, (unsigned)plan.splits), kSkinnyThreads, args, stream);
+    }
     int staged = 0;
     if (!dma) {
         const GroupShape g(a.m, a.groups);
@@ -164,7 +215,7 @@ int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config,
     void* args[] = {&a, &ad};
     const dim3 grid((unsigned)resident(rows, tiles, cus));
     if (config == GEMM_RELU_GROUPS_TILED)
-        return enqueue(staged_kernels(dtype, {{a.a, a.k}, {a.b, b_layout == GEMM_RELU_B_NK ? a.k : a.n}})
+        return enqueue(staged_kernels(dtype, {rows_a, rows_b})
                            .rows[staged][b_layout][ad.v != nullptr][a.groups > 64], grid, kStagedThreads, args, stream);
     return enqueue(kernels(dtype).rows_dma[config - 1][b_layout][a.k % 64 != 0][ad.v != nullptr], grid,
                    kGroupThreads[config - 1], args, stream);
@@ -173,7 +224,7 @@ int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config,
 // Sums over each group's rows (I, J > 0), by LDS DMA.
 int launch_weights(WeightArgs a, int dtype, int config, int cus, hipStream_t stream)
 {
-    if (config == GEMM_RELU_GROUPS_AUTO)
+    if (config == GEMM_RELU_GROUPS_AUTO || config == GEMM_RELU_GROUPS_STREAM)
         config = dma_config(a.i, a.groups * ceil_div(a.i, 256) * ceil_div(a.j, 256),
                             a.groups * ceil_div(a.i, 128) * ceil_div(a.j, 128));
     const int64_t tile = kGroupTile[config - 1], tiles = int64_t(a.groups) * ceil_div(a.i, tile) * ceil_div(a.j, tile);
@@ -217,9 +268,9 @@ int launch_grad_staged(RowsArgs r, WeightArgs w, const uint16_t* mask, int dtype
 // adapter, and the partial sums of a K that is cut into `splits` parts: as many
 // as make 512 workgroups, while each of their 8 waves has a piece of K.
 struct AdapterSpace {
-    int64_t rank_pad, tiles, splits, t, factor, row_id, part, bytes;
+    int64_t rank_pad, tiles, splits, t, factor, row_id, part, bytes;   // part: also the streaming kernel's, afterwards
 };
-AdapterSpace adapter_space(int64_t M, int64_t K, int64_t rank, int64_t segments)
+AdapterSpace adapter_space(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t segments)
 {
     AdapterSpace s;
     s.rank_pad = round_up(rank, 64);
@@ -229,7 +280,8 @@ AdapterSpace adapter_space(int64_t M, int64_t K, int64_t rank, int64_t segments)
     s.factor = s.t + round_up(M * 2 * s.rank_pad * 2, 256);
     s.row_id = s.factor + round_up(M * 4, 256);
     s.part = s.row_id + round_up(M * 4, 256);
-    s.bytes = s.part + (s.splits > 1 ? s.tiles * s.splits * ceil_div(rank, kShrinkCols) * kShrinkThreads * 4 : 0);
+    s.bytes = s.part + std::max(s.splits > 1 ? s.tiles * s.splits * ceil_div(rank, kShrinkCols) * kShrinkThreads * 4 : 0,
+                                SkinnyPlan(M, N, K, 1).bytes);
     return s;
 }
 static_assert(512 * 4 <= GEMM_RELU_GROUPS_COUNTER_BYTES, "a counter for each row tile of a split sum");
@@ -244,7 +296,9 @@ extern "C" {
 int64_t gemm_relu_grouped_workspace(int64_t M, int64_t N, int64_t K, int64_t groups, int dtype, int b_layout)
 {
     const int rc = check_shape(M, N, K, groups, dtype, b_layout);
-    return rc;
+    if (rc != GEMM_RELU_OK) return rc;
+    const int64_t bytes = SkinnyPlan(M, N, K, groups).bytes;
+    return bytes ? GEMM_RELU_GROUPS_COUNTER_BYTES + bytes : 0;
 }
 
 int gemm_relu_grouped(const void* A, const void* B, const int32_t* ends, void* C, int64_t M, int64_t N,
@@ -258,8 +312,9 @@ int gemm_relu_grouped(const void* A, const void* B, const int32_t* ends, void* C
     if (M == 0 || N == 0) return GEMM_RELU_OK;
     const Span in[] = {{A, 2 * M * K}, {B, 2 * groups * K * N}}, words[] = {{ends, 4 * groups}};
     const Span out[] = {{C, 2 * M * N}, {workspace, need}};
-    int rc = check_spans(in, 2, words, 1, out, need > 0 ? 2 : 1);
+    int rc = check_spans(in, 2, words, 1, out, 1);
     if (rc == GEMM_RELU_OK) rc = check_workspace(workspace, workspace_bytes, need);
+    if (rc == GEMM_RELU_OK) rc = check_spans(in, 2, words, 1, out, need > 0 ? 2 : 1);
     if (rc != GEMM_RELU_OK) return rc;
     int cus = 0;
     if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;
@@ -267,7 +322,8 @@ int gemm_relu_grouped(const void* A, const void* B, const int32_t* ends, void* C
     if (K == 0) return zero_fill(C, M * N, s);
     RowsArgs a{static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), static_cast<uint16_t*>(C), ends,
                (int)M, (int)N, (int)K, (int)groups, relu, 0};
-    return launch_rows(a, AdapterArgs{}, dtype, b_layout, config_id, cus, s);
+    float* parts = need ? reinterpret_cast<float*>(static_cast<char*>(workspace) + GEMM_RELU_GROUPS_COUNTER_BYTES) : nullptr;
+    return launch_rows(a, AdapterArgs{}, dtype, b_layout, config_id, cus, parts, static_cast<int*>(workspace), s);
 }
 
 int64_t gemm_relu_grouped_backward_workspace(int64_t M, int64_t N, int64_t K, int64_t groups, int dtype,
@@ -328,7 +384,7 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
         r.a = masked;
         (kn ? w.q : w.p) = masked;
     }
-    if (want_a && rc == GEMM_RELU_OK) rc = launch_rows(r, AdapterArgs{}, dtype, layout_a, config_id, cus, s);
+    if (want_a && rc == GEMM_RELU_OK) rc = launch_rows(r, AdapterArgs{}, dtype, layout_a, config_id, cus, nullptr, nullptr, s);
     w.c_vec = store_width(w.out, w.j);
     if (want_b && rc == GEMM_RELU_OK && gkn > 0) rc = launch_weights(w, dtype, config_id, cus, s);
     return rc;
@@ -341,7 +397,7 @@ int64_t gemm_relu_adapters_workspace(int64_t M, int64_t N, int64_t K, int64_t ra
     if (rc != GEMM_RELU_OK) return rc;
     if (rank < 1 || adapters < 1) return GEMM_RELU_ERR_INVALID_ARG;
     if (rank > kMaxRank || adapters > kMaxGroups) return GEMM_RELU_ERR_TOO_LARGE;
-    return adapter_space(M, K, rank, segments).bytes;
+    return adapter_space(M, N, K, rank, segments).bytes;
 }
 
 int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* V, const float* scales,
@@ -365,7 +421,7 @@ int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* 
     if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (K == 0) return zero_fill(C, M * N, s);
-    const AdapterSpace space = adapter_space(M, K, rank, segments);
+    const AdapterSpace space = adapter_space(M, N, K, rank, segments);
     char* const ws = static_cast<char*>(workspace);
     uint16_t* t = reinterpret_cast<uint16_t*>(ws + space.t);
     float* factor = reinterpret_cast<float*>(ws + space.factor);
@@ -381,7 +437,7 @@ int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* 
     const bool v_fast = b_layout == GEMM_RELU_B_NK ? rank % 8 == 0 && aligned(V, 16) : N % 4 == 0 && aligned(V, 8);
     AdapterArgs ad{static_cast<const uint16_t*>(V), t, factor, row_id, ends, ids, (int)segments, (int)adapters, (int)rank,
                    (int)space.rank_pad, v_fast};
-    return launch_rows(a, ad, dtype, b_layout, config_id, cus, s);
+    return launch_rows(a, ad, dtype, b_layout, config_id, cus, sh.part, sh.counters, s);
 }
 
 }  // extern "C"

@@ -4,6 +4,7 @@
 
 #include "groups_dma.hpp"
 #include "groups_kernels.hpp"
+#include "groups_skinny.hpp"
 
 namespace gemm_relu_hip {
 
@@ -80,10 +81,26 @@ StagedKernels make_staged_table()
     return t;
 }
 
+template <int DT, int S, bool B_NK>
+void fill_skinny(GroupKernels& t)
+{
+    constexpr int MB = kSkinnyBlocks[S];
+    t.rows_skinny[S][B_NK][0][0] = (const void*)&rows_skinny<DT, B_NK, MB, false, false>;
+    t.rows_skinny[S][B_NK][0][1] = (const void*)&rows_skinny<DT, B_NK, MB, false, true>;
+    t.rows_skinny[S][B_NK][1][0] = (const void*)&rows_skinny<DT, B_NK, MB, true, false>;
+    t.rows_skinny[S][B_NK][1][1] = (const void*)&rows_skinny<DT, B_NK, MB, true, true>;
+}
+
 template <int DT>
 GroupKernels make_group_table()
 {
     GroupKernels t{};
+    fill_skinny<DT, 0, false>(t);
+    fill_skinny<DT, 0, true>(t);
+    fill_skinny<DT, 1, false>(t);
+    fill_skinny<DT, 1, true>(t);
+    fill_skinny<DT, 2, false>(t);
+    fill_skinny<DT, 2, true>(t);
     fill_group_tile<DT, 0>(t);
     fill_group_tile<DT, 1>(t);
     fill_group_tile<DT, 2>(t);

@@ -87,10 +87,16 @@ struct StagedKernels {
     const void* grad[kNumStagedTiles][2][2][2];
 };
 
+// Streaming kernels for few rows a group: 16-row blocks a workgroup takes.
+constexpr int kNumSkinny = 3;
+constexpr int kSkinnyBlocks[kNumSkinny] = {1, 2, 4};
+constexpr int kSkinnyCols = 32, kSkinnyK = 128, kSkinnyThreads = 512;
+
 struct GroupKernels {
     // [tile][B layout][K % 64 != 0][with adapters]; with adapters the 256 tile takes any K and starts from their terms
     const void* rows_dma[kNumGroupTiles][2][2][2];
     const void* weight_dma[kNumGroupTiles];
+    const void* rows_skinny[kNumSkinny][2][2][2];   // [blocks][B layout][odd rows][with adapters]
     const void* mask;
     const void* shrink[2];                        // [U layout]
 };

@@ -21,6 +21,7 @@ CONFIG_TILED = 0
 CONFIG_DMA_256 = 1
 CONFIG_DMA_128 = 2
 CONFIG_DMA_64 = 3
+CONFIG_STREAM = 4
 
 _lock = threading.Lock()
 _lib = None
