@@ -25,7 +25,8 @@
  * HIP graph); arguments are checked before anything is launched; negative
  * return codes (GEMM_RELU_ERR_*, gemm_relu_strerror).  Matrices need 2-byte
  * alignment, int32 and float arrays 4-byte.  The fastest kernels want row
- * lengths that are multiples of 8 elements and 16-byte aligned matrices.
+ * lengths that are multiples of 8 elements and 16-byte aligned matrices, the next
+ * ones even lengths and 4-byte alignment.
  *
  * Layouts.  GEMM_RELU_B_KN: weights stored (in, out): B (groups, K, N), W (K, N),
  * U (adapters, K, rank), V (adapters, rank, N).  GEMM_RELU_B_NK: stored (out, in):
@@ -56,9 +57,9 @@ extern "C" {
 #define GEMM_RELU_GROUPS_COUNTER_BYTES ((int64_t)65536)
 
 /* Kernels of the products below (`config_id`).  AUTO picks by size and
- * alignment; the DMA kernels need row lengths that are multiples of 8 elements
- * and 16-byte aligned operands, and a request that the arguments do not allow
- * falls back to TILED.  Sums may be added in another order by another kernel. */
+ * alignment.  DMA_128 and DMA_64 need rows of an even length and 4-byte aligned
+ * operands, DMA_256 multiples of 8 elements and 16-byte alignment; a request that
+ * the arguments do not allow falls back to DMA_128 or TILED.  Sums may be added in another order by another kernel. */
 enum {
     GEMM_RELU_GROUPS_AUTO = -1,
     GEMM_RELU_GROUPS_TILED = 0,   /* 128x128 tiles staged through registers: any row length and alignment */

@@ -146,6 +146,10 @@ CONFIG_SHAPES = [
     ([513, 130], 0, 520, 320),
     ([0, 1, 5, 0, 70] * 17, 2, 136, 200),
     ([2000, 0, 1300], 30, 2056, 64),
+    ([40, 0, 256, 300], 3, 262, 138),      # rows of an even length: K % 8 is 2
+    ([1, 130, 64], 0, 134, 60),            # 4 (and less than a K-step)
+    ([513, 130], 0, 518, 326),             # 6
+    ([300, 40], 1, 261, 137),              # odd
 ]
 
 

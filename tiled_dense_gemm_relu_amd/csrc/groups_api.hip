@@ -70,8 +70,13 @@ int check_workspace(void* workspace, int64_t bytes, int64_t need)
     return !workspace || bytes < need || !aligned(workspace, 256) ? GEMM_RELU_ERR_WORKSPACE : GEMM_RELU_OK;
 }
 
-// Whether LDS DMA can read a matrix: rows of whole 16-byte pieces.
-bool dma_rows(const void* p, int64_t row) { return row % 8 == 0 && aligned(p, 16); }
+// How LDS DMA reads a matrix: rows of whole 16-byte pieces, rows of an even
+// length at 4-byte alignment (the 128 and 64 tiles), or not at all.
+enum DmaRows { kDmaNone = 0, kDmaEven = 1, kDmaWhole = 2 };
+DmaRows dma_rows(const void* p, int64_t row)
+{
+    return row % 8 == 0 && aligned(p, 16) ? kDmaWhole : row % 2 == 0 && aligned(p, 4) ? kDmaEven : kDmaNone;
+}
 
 int store_width(const void* c, int64_t n) { return n % 8 == 0 && aligned(c, 16) ? 2 : 0; }
 
@@ -181,8 +186,8 @@ int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config,
 {
     a.c_vec = store_width(a.c, a.n);
     const Rows rows_a{a.a, a.k}, rows_b{a.b, b_layout == GEMM_RELU_B_NK ? a.k : a.n};
-    const bool dma = dma_rows(a.a, a.k) && dma_rows(a.b, rows_b.length);
-    if (config == GEMM_RELU_GROUPS_STREAM || (config == GEMM_RELU_GROUPS_AUTO && streams(a.m, a.n, a.k, a.groups, dma))) {
+    const DmaRows dma = std::min(dma_rows(a.a, a.k), dma_rows(a.b, rows_b.length));
+    if (config == GEMM_RELU_GROUPS_STREAM || (config == GEMM_RELU_GROUPS_AUTO && streams(a.m, a.n, a.k, a.groups, dma != kDmaNone))) {
         SkinnyPlan plan(a.m, a.n, a.k, a.groups);
         if (plan.units > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
         if (!parts) plan.splits = 1;
@@ -191,7 +196,7 @@ int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config,
                        dim3((unsigned)plan.units, (unsigned)plan.splits), kSkinnyThreads, args, stream);
     }
     int staged = 0;
-    if (!dma) {
+    if (dma == kDmaNone) {
         const GroupShape g(a.m, a.groups);
         if (config != GEMM_RELU_GROUPS_TILED) staged = staged_tile(g.rows, g.tiles(128, a.n));
         config = GEMM_RELU_GROUPS_TILED;
@@ -206,7 +211,8 @@ int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config,
         config = auto_config(ad.v ? ad.segments : a.groups);
         if (ad.v && config != GEMM_RELU_GROUPS_DMA_256) config = std::max<int>(auto_config(1), GEMM_RELU_GROUPS_DMA_128);
     }
-    if (config == GEMM_RELU_GROUPS_DMA_256 && ad.v && !dma_rows(ad.v, b_layout == GEMM_RELU_B_NK ? ad.rank : a.n))
+    if (config == GEMM_RELU_GROUPS_DMA_256 &&
+        (dma < kDmaWhole || (ad.v && dma_rows(ad.v, b_layout == GEMM_RELU_B_NK ? ad.rank : a.n) < kDmaWhole)))
         config = GEMM_RELU_GROUPS_DMA_128;
     const bool first = config == GEMM_RELU_GROUPS_DMA_256 && ad.v;
     const int64_t rows = config == GEMM_RELU_GROUPS_TILED ? kStagedTile[staged] : kGroupTile[config - 1];
@@ -217,7 +223,7 @@ int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config,
     if (config == GEMM_RELU_GROUPS_TILED)
         return enqueue(staged_kernels(dtype, {rows_a, rows_b})
                            .rows[staged][b_layout][ad.v != nullptr][a.groups > 64], grid, kStagedThreads, args, stream);
-    return enqueue(kernels(dtype).rows_dma[config - 1][b_layout][a.k % 64 != 0][ad.v != nullptr], grid,
+    return enqueue(kernels(dtype).rows_dma[config - 1][b_layout][dma < kDmaWhole ? 2 : a.k % 64 != 0][ad.v != nullptr], grid,
                    kGroupThreads[config - 1], args, stream);
 }
 
@@ -227,10 +233,12 @@ int launch_weights(WeightArgs a, int dtype, int config, int cus, hipStream_t str
     if (config == GEMM_RELU_GROUPS_AUTO || config == GEMM_RELU_GROUPS_STREAM)
         config = dma_config(a.i, a.groups * ceil_div(a.i, 256) * ceil_div(a.j, 256),
                             a.groups * ceil_div(a.i, 128) * ceil_div(a.j, 128));
+    const bool whole = std::min(dma_rows(a.p, a.i), dma_rows(a.q, a.j)) == kDmaWhole;
+    if (config == GEMM_RELU_GROUPS_DMA_256 && !whole) config = GEMM_RELU_GROUPS_DMA_128;
     const int64_t tile = kGroupTile[config - 1], tiles = int64_t(a.groups) * ceil_div(a.i, tile) * ceil_div(a.j, tile);
     if (tiles > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
     void* args[] = {&a};
-    return enqueue(kernels(dtype).weight_dma[config - 1], dim3((unsigned)resident(tile, tiles, cus)), kGroupThreads[config - 1],
+    return enqueue(kernels(dtype).weight_dma[config - 1][!whole], dim3((unsigned)resident(tile, tiles, cus)), kGroupThreads[config - 1],
                    args, stream);
 }
 
@@ -371,14 +379,14 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
     RowsArgs r{d, b, static_cast<uint16_t*>(dA), ends, (int)M, (int)K, (int)N, (int)groups, 0, 0};
     WeightArgs w{kn ? x : d, kn ? d : x, static_cast<uint16_t*>(dB), ends, (int)M, (int)(kn ? K : N), (int)(kn ? N : K),
                  (int)groups, 0};
-    // LDS DMA needs whole 16-byte pieces and D itself in memory.  The register-
+    // LDS DMA needs rows of an even length and D itself in memory.  The register-
     // staged kernel needs neither, and is one launch instead of two or three.
-    const bool dma = dma_rows(d, N) && (!want_a || dma_rows(b, kn ? N : K)) && (!want_b || dma_rows(x, K));
+    const bool dma = dma_rows(d, N) && (!want_a || dma_rows(b, kn ? N : K)) && (!want_b || dma_rows(x, K));   // kDmaNone: false
     if (config_id == GEMM_RELU_GROUPS_TILED || !dma || (config_id == GEMM_RELU_GROUPS_AUTO && 4.0 * M * N * K < kSmallGrad))
         return launch_grad_staged(r, w, c, dtype, layout_a, config_id, cus, s);
     if (relu) {
         uint16_t* masked = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + GEMM_RELU_GROUPS_COUNTER_BYTES);
-        MaskArgs m{d, c, masked, mn, aligned(C, 16)};
+        MaskArgs m{d, c, masked, mn, aligned(dC, 16) && aligned(C, 16)};
         void* args[] = {&m};
         rc = enqueue(kernels(dtype).mask, dim3((unsigned)std::min<int64_t>(ceil_div(mn, 2048), 4096)), 256, args, s);
         r.a = masked;

@@ -306,8 +306,12 @@ __device__ __forceinline__ void store_rows_any(uint16_t* __restrict__ C, const f
 }
 
 // The product loop.  A's rows are lda long, B's ldb; `b_group` and `c_group`
-// are the elements from one group's B and C to the next.  KTAIL: k_end need not
-// be a multiple of 64 for k-contiguous operands (but of 8).
+// are the elements from one group's B and C to the next.  KTAIL 0: k-contiguous
+// operands have k_end % 64 == 0.  1: k_end % 8 == 0.  2: rows of any even length
+// at 4-byte alignment (the DMA reads 16 bytes from any dword); a piece that holds
+// elements past k_end as well is cut off in LDS by the lane that loaded it, once
+// it has landed and before the barrier that hands it over, so the products of
+// what lies behind a row (another row's infinity) never enter a sum.
 //  With adapters, kAdaptAfter adds a finished tile's low-rank terms to its sums
 // (add_adapters: tiles may hold rows of many segments).  kAdaptFirst is for
 // tiles cut at the segments' ends: before its K-steps over A and B a tile
@@ -315,7 +319,7 @@ __device__ __forceinline__ void store_rows_any(uint16_t* __restrict__ C, const f
 // ring, multiplies its sums by the rows' factors, and goes on from them, so
 // the low-rank product costs its K-steps and nothing else.
 enum { kAdaptNone = 0, kAdaptAfter = 1, kAdaptFirst = 2 };
-template <class Cfg, int DT, bool KTAIL, int ADAPT, class Units>
+template <class Cfg, int DT, int KTAIL, int ADAPT, class Units>
 __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* __restrict__ A,
                                             const uint16_t* __restrict__ B, uint16_t* __restrict__ C, uint32_t lda,
                                             uint32_t ldb, size_t b_group, size_t c_group, int N, bool relu, int c_vec,
@@ -327,6 +331,8 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
     constexpr bool AK = Cfg::A_KMAJOR, BKM = Cfg::B_KMAJOR, WS = Cfg::PRODUCERS > 0, FIRST = ADAPT == kAdaptFirst;
     constexpr bool STAGED = Cfg::STAGED;
     static_assert(!FIRST || (KTAIL && !AK), "the rank need not be a multiple of BK");
+    constexpr bool EVEN = KTAIL == 2 && !STAGED;
+    static_assert(!EVEN || WS, "the producers cut the pieces off");
     static_assert(!FIRST || !STAGED, "V is streamed by DMA");
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -433,9 +439,13 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
         }
     };
     fill_setup(true);
-    // The descriptor of the rows from `skip` on of a stage with `rows` rows.
-    auto rows_from = [](const uint16_t* p, int rows, int skip, uint32_t ld) {
-        const int32x4_t r = rsrc_words(p + (size_t)skip * ld, (uint32_t)max(0, rows - skip) * ld * 2u);
+    // The descriptor of the rows from `skip` on of a stage with `rows` rows, which
+    // start `col` elements into theirs (k-major; with whole pieces no lane reads
+    // past the last row's end anyway).
+    auto rows_from = [](const uint16_t* p, int rows, int skip, uint32_t ld, int col) {
+        uint32_t bytes = (uint32_t)max(0, rows - skip) * ld * 2u;
+        if constexpr (EVEN) bytes -= bytes ? 2u * (uint32_t)col : 0u;
+        const int32x4_t r = rsrc_words(p + (size_t)skip * ld, bytes);
         return int32x4_t{__builtin_amdgcn_readfirstlane(r[0]), __builtin_amdgcn_readfirstlane(r[1]),
                          __builtin_amdgcn_readfirstlane(r[2]), kBufferFlags};
     };
@@ -444,9 +454,9 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
             const uint32_t lds = lds_base + slot * Cfg::A_STAGE + (dwave * QA + q) * 1024;
             const uint32_t vo = a_voff[q % PA];
             if constexpr (AK)
-                dma_b128(rows_from(f_ap, min(BK, f_left), q / 2 * A_PAIR, lda), lds, vo, 0u);
+                dma_b128(rows_from(f_ap, min(BK, f_left), q / 2 * A_PAIR, lda, f_m0), lds, vo, 0u);
             else   // (the intermediates' rows are whole K-steps)
-                dma_b128(rows_from(f_ap, f_arows, q / 2 * A_PAIR, f_lda), lds,
+                dma_b128(rows_from(f_ap, f_arows, q / 2 * A_PAIR, f_lda, 0), lds,
                          KTAIL && !(FIRST && f_rank) && a_pos[q % PA] >= f_left ? kOobOffset : vo, (uint32_t)f_k * 2u);
         } else {
             const int p = q - QA;
@@ -454,9 +464,9 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
             const uint32_t lds = lds_base + Cfg::B_REGION + slot * Cfg::B_STAGE + (dwave * QB + p) * 1024;
             const uint32_t vo = b_voff[p % PB];
             if constexpr (BKM)
-                dma_b128(rows_from(f_bp, min(BK, left), p / 2 * B_PAIR, ldb), lds, vo, 0u);
+                dma_b128(rows_from(f_bp, min(BK, left), p / 2 * B_PAIR, ldb, f_n0), lds, vo, 0u);
             else
-                dma_b128(rows_from(f_bp, f_brows, p / 2 * B_PAIR, f_ldb), lds,
+                dma_b128(rows_from(f_bp, f_brows, p / 2 * B_PAIR, f_ldb, 0), lds,
                          KTAIL && b_pos[p % PB] >= left ? kOobOffset : vo, (uint32_t)(FIRST ? f_kb : f_k) * 2u);
         }
     };
@@ -647,14 +657,37 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
         }
     }
     constexpr int PRO = WS ? S - 1 : S;      // steps the prologue issues
+    // EVEN: of the steps whose stages are in flight, what they had left.
+    int lefts[PRO];
+    // This wave's pieces that straddle k_end, of a stage that has landed.
+    auto cut_off = [&](int slot, int left) __attribute__((always_inline)) {
+        if (left >= BK || left % 8 == 0) return;
+        auto cut = [&](uint8_t* at, int pos) {
+            if (pos < left && left < pos + 8) {
+                u32x4* const p = reinterpret_cast<u32x4*>(at + lane * 16);
+                *p = keep_first(*p, left - pos);
+            }
+        };
+        if constexpr (!AK) {
+#pragma unroll
+            for (int q = 0; q < QA; ++q) cut(smem + slot * Cfg::A_STAGE + (dwave * QA + q) * 1024, a_pos[q % PA]);
+        }
+        if constexpr (!BKM) {
+#pragma unroll
+            for (int q = 0; q < QB; ++q)
+                cut(smem + Cfg::B_REGION + slot * Cfg::B_STAGE + (dwave * QB + q) * 1024, b_pos[q % PB]);
+        }
+    };
     if (!STAGED && (!WS || producer)) {
 #pragma unroll
         for (int s = 0; s < PRO; ++s) {
+            lefts[s] = f_left;
 #pragma unroll
             for (int q = 0; q < NQ; ++q) dma(s, q);
             fill_advance();
         }
         wait_vmcnt<(PRO - 1) * NQ>();
+        if constexpr (EVEN) cut_off(0, lefts[0]);
     }
     lds_barrier();
     if constexpr (WS && !STAGED) {
@@ -662,9 +695,13 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
             for (int g = 0; f_unit < n_units || g < f_steps; ++g) {
                 const int slot_fill = (g + S - 1) & (S - 1);
 #pragma unroll
+                for (int s = 0; s + 1 < PRO; ++s) lefts[s] = lefts[s + 1];
+                lefts[PRO - 1] = f_left;
+#pragma unroll
                 for (int q = 0; q < NQ; ++q) dma(slot_fill, q);
                 fill_advance();
                 wait_vmcnt<(S - 2) * NQ>();
+                if constexpr (EVEN) cut_off((g + 1) & (S - 1), lefts[0]);
                 lds_barrier();
             }
             wait_vmcnt<0>();   // no LDS DMA may outlive the workgroup
@@ -823,7 +860,7 @@ __device__ __forceinline__ void zero_rows(const RowsArgs& a, int first, int bloc
     for (size_t i = (size_t)block * blockDim.x + threadIdx.x; i < count; i += stride) p[i] = 0;
 }
 
-template <class Cfg, int DT, bool KTAIL, int ADAPT, bool MANY = true>
+template <class Cfg, int DT, int KTAIL, int ADAPT, bool MANY = true>
 __global__ __launch_bounds__(Cfg::THREADS, 1) void rows_dma(RowsArgs a, AdapterArgs ad)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES + Cfg::STRIP_BYTES];
@@ -841,13 +878,13 @@ __global__ __launch_bounds__(Cfg::THREADS, 1) void rows_dma(RowsArgs a, AdapterA
                                        ad, nullptr, smem);
 }
 
-template <class Cfg, int DT>
+template <class Cfg, int DT, int KTAIL>
 __global__ __launch_bounds__(Cfg::THREADS, 1) void weight_dma(WeightArgs a)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES + Cfg::STRIP_BYTES];
     WeightUnits<Cfg> units;
     units.init(a, blockIdx.x, gridDim.x);
-    dma_product<Cfg, DT, false, kAdaptNone>(units, a.p, a.q, a.out, (uint32_t)a.i, (uint32_t)a.j, 0,
+    dma_product<Cfg, DT, KTAIL, kAdaptNone>(units, a.p, a.q, a.out, (uint32_t)a.i, (uint32_t)a.j, 0,
                                        (size_t)a.i * (size_t)a.j, a.j, false, a.c_vec, AdapterArgs{}, nullptr, smem);
 }
 
@@ -866,14 +903,14 @@ __global__ __launch_bounds__(CfgR::THREADS, 1) void grad_staged(RowsArgs rows, W
         RowUnits<CfgR, MANY> units;
         units.init(rows, rows.ends, rows.groups, false, threadIdx.x & 63, block, blocks_rows);
         if (units.rows < rows.m) zero_rows(rows, units.rows, block, blocks_rows);
-        dma_product<CfgR, DT, true, kAdaptNone>(units, rows.a, rows.b, rows.c, (uint32_t)rows.k,
+        dma_product<CfgR, DT, 1, kAdaptNone>(units, rows.a, rows.b, rows.c, (uint32_t)rows.k,
                                                 (uint32_t)(CfgR::B_KMAJOR ? rows.n : rows.k),
                                                 (size_t)rows.k * (size_t)rows.n, 0, rows.n, false, rows.c_vec, AdapterArgs{},
                                                 mask, smem);
     } else {
         WeightUnits<CfgW> units;
         units.init(weights, block - blocks_rows, (int)gridDim.x - blocks_rows);
-        dma_product<CfgW, DT, false, kAdaptNone>(units, weights.p, weights.q, weights.out, (uint32_t)weights.i,
+        dma_product<CfgW, DT, 0, kAdaptNone>(units, weights.p, weights.q, weights.out, (uint32_t)weights.i,
                                                  (uint32_t)weights.j, 0, (size_t)weights.i * (size_t)weights.j, weights.j,
                                                  false, weights.c_vec, AdapterArgs{}, mask, smem);
     }

@@ -24,13 +24,15 @@ void fill_rows_dma(GroupKernels& t)
     using Cfg = typename GroupTile<T, false, !B_NK>::Cfg;
     static_assert(Cfg::BM == kGroupTile[T] && Cfg::BN == kGroupTile[T] && Cfg::THREADS == kGroupThreads[T],
                   "host tile table out of date");
-    t.rows_dma[T][B_NK][0][0] = (const void*)&rows_dma<Cfg, DT, false, kAdaptNone>;
-    t.rows_dma[T][B_NK][1][0] = (const void*)&rows_dma<Cfg, DT, true, kAdaptNone>;
+    t.rows_dma[T][B_NK][0][0] = (const void*)&rows_dma<Cfg, DT, 0, kAdaptNone>;
+    t.rows_dma[T][B_NK][1][0] = (const void*)&rows_dma<Cfg, DT, 1, kAdaptNone>;
     if constexpr (T == 0) {
-        t.rows_dma[T][B_NK][0][1] = t.rows_dma[T][B_NK][1][1] = (const void*)&rows_dma<Cfg, DT, true, kAdaptFirst>;
+        t.rows_dma[T][B_NK][0][1] = t.rows_dma[T][B_NK][1][1] = (const void*)&rows_dma<Cfg, DT, 1, kAdaptFirst>;
     } else {
-        t.rows_dma[T][B_NK][0][1] = (const void*)&rows_dma<Cfg, DT, false, kAdaptAfter>;
-        t.rows_dma[T][B_NK][1][1] = (const void*)&rows_dma<Cfg, DT, true, kAdaptAfter>;
+        t.rows_dma[T][B_NK][2][0] = (const void*)&rows_dma<Cfg, DT, 2, kAdaptNone>;
+        t.rows_dma[T][B_NK][0][1] = (const void*)&rows_dma<Cfg, DT, 0, kAdaptAfter>;
+        t.rows_dma[T][B_NK][1][1] = (const void*)&rows_dma<Cfg, DT, 1, kAdaptAfter>;
+        t.rows_dma[T][B_NK][2][1] = (const void*)&rows_dma<Cfg, DT, 2, kAdaptAfter>;
     }
 }
 
@@ -39,7 +41,8 @@ void fill_group_tile(GroupKernels& t)
 {
     fill_rows_dma<DT, T, false>(t);
     fill_rows_dma<DT, T, true>(t);
-    t.weight_dma[T] = (const void*)&weight_dma<typename GroupTile<T, true, true>::Cfg, DT>;
+    t.weight_dma[T][0] = (const void*)&weight_dma<typename GroupTile<T, true, true>::Cfg, DT, 0>;
+    if constexpr (T > 0) t.weight_dma[T][1] = (const void*)&weight_dma<typename GroupTile<T, true, true>::Cfg, DT, 2>;
 }
 
 // The register-staged tiles of a position of kStagedTile.  The large one keeps
@@ -63,9 +66,9 @@ void fill_staged(StagedKernels& t)
 {
     using Rows = StagedTile<T, false, !B_NK, 0, ODD>;
     static_assert(Rows::THREADS == kStagedThreads, "host tile table out of date");
-    t.rows[T][B_NK][0][0] = (const void*)&rows_dma<Rows, DT, true, kAdaptNone, false>;
-    t.rows[T][B_NK][0][1] = (const void*)&rows_dma<Rows, DT, true, kAdaptNone, true>;
-    t.rows[T][B_NK][1][0] = t.rows[T][B_NK][1][1] = (const void*)&rows_dma<Rows, DT, true, kAdaptAfter, false>;
+    t.rows[T][B_NK][0][0] = (const void*)&rows_dma<Rows, DT, 1, kAdaptNone, false>;
+    t.rows[T][B_NK][0][1] = (const void*)&rows_dma<Rows, DT, 1, kAdaptNone, true>;
+    t.rows[T][B_NK][1][0] = t.rows[T][B_NK][1][1] = (const void*)&rows_dma<Rows, DT, 1, kAdaptAfter, false>;
     fill_grad<DT, T, B_NK, ODD, false>(t);
     fill_grad<DT, T, B_NK, ODD, true>(t);
 }

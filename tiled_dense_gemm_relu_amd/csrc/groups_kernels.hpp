@@ -274,55 +274,59 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
         }
         auto lanes = [&](auto fast) __attribute__((always_inline)) {
             constexpr bool FAST = decltype(fast)::value;
+            constexpr int SIDE = FN < 2 ? FN : 2;       // 16-column blocks whose loads are in flight together
             const uint16_t* vp = ad.v + (size_t)id * (size_t)ad.rank * (size_t)N;
-            for (int r0 = 0; r0 < ad.rank; r0 += 8) {
-                const uint32_t at = m * t_row + (uint32_t)r0 * 2u;
-                const u32x4 t_hi = __builtin_amdgcn_raw_buffer_load_b128(rt, at, 0, 0);
-                const u32x4 t_lo = __builtin_amdgcn_raw_buffer_load_b128(rt, at, ad.rank_pad * 2, 0);
-                float z[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    z[e] = f * (to_float<DT>((uint16_t)(t_hi[e / 2] >> (16 * (e & 1)))) +
-                                to_float<DT>((uint16_t)(t_lo[e / 2] >> (16 * (e & 1)))));
-                const int valid = min(8, ad.rank - r0);
+            for (int i0 = 0; i0 < FN; i0 += SIDE) {
+#pragma unroll B_NK ? 1 : 2
+                for (int r0 = 0; r0 < ad.rank; r0 += 8) {
+                    const int valid = min(8, ad.rank - r0);
+                    // V first: its loads wait for nothing
+                    uint32_t w[SIDE][8][2];             // [k] pairs of columns, or [4 pairs of k, 2 columns at a time]
 #pragma unroll
-                for (int i = 0; i < FN; ++i) {
-                    const int n = n_base + 16 * i + 4 * kg, cols = min(4, N - n);
-                    if (i % 2 == 0) __builtin_amdgcn_sched_barrier(0);   // loads of two blocks in registers at a time
-                    if (cols <= 0) continue;
-                    if constexpr (B_NK) {
+                    for (int i = 0; i < SIDE; ++i) {
+                        // columns past N repeat the last ones: their sums are not stored
+                        const int n = min(n_base + 16 * (i0 + i) + 4 * kg, N - 1), cols = min(4, N - n);
+                        if constexpr (B_NK) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            // columns past N repeat the last one: their sums are not stored
-                            const uint16_t* p = vp + (size_t)(n + min(x, cols - 1)) * (size_t)ad.rank + r0;
-                            uint32_t w[4];
-                            if constexpr (FAST) {
-                                const u32x4 q = *reinterpret_cast<const u32x4*>(p);
-                                w[0] = q[0], w[1] = q[1], w[2] = q[2], w[3] = q[3];
-                            } else {
-                                load_dwords_any<4>(p, valid, w);
+                            for (int x = 0; x < 4; ++x) {
+                                const uint16_t* p = vp + (size_t)(n + min(x, cols - 1)) * (size_t)ad.rank + r0;
+                                uint32_t q[4];
+                                if constexpr (FAST) {
+                                    const u32x4 v = *reinterpret_cast<const u32x4*>(p);
+                                    q[0] = v[0], q[1] = v[1], q[2] = v[2], q[3] = v[3];
+                                } else {
+                                    load_dwords_any<4>(p, valid, q);
+                                }
+#pragma unroll
+                                for (int h = 0; h < 4; ++h) w[i][2 * x + (h >> 1)][h & 1] = q[h];
                             }
+                        } else {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (e < valid) sum[i][x] += z[e] * to_float<DT>((uint16_t)(w[e / 2] >> (16 * (e & 1))));
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const uint16_t* p = vp + (size_t)(r0 + min(e, valid - 1)) * (size_t)N + n;
-                            uint32_t w[2];
-                            if constexpr (FAST) {
-                                const u32x2 q = *reinterpret_cast<const u32x2*>(p);
-                                w[0] = q[0], w[1] = q[1];
-                            } else {
-                                load_dwords_any<2>(p, cols, w);
-                            }
-                            if (e < valid) {
-#pragma unroll
-                                for (int x = 0; x < 4; ++x)
-                                    sum[i][x] += z[e] * to_float<DT>((uint16_t)(w[x / 2] >> (16 * (x & 1))));
+                            for (int e = 0; e < 8; ++e) {
+                                const uint16_t* p = vp + (size_t)(r0 + min(e, valid - 1)) * (size_t)N + n;
+                                if constexpr (FAST) {
+                                    const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+                                    w[i][e][0] = v[0], w[i][e][1] = v[1];
+                                } else {
+                                    load_dwords_any<2>(p, cols, w[i][e]);
+                                }
                             }
                         }
+                    }
+                    const uint32_t at = m * t_row + (uint32_t)r0 * 2u;
+                    const u32x4 t_hi = __builtin_amdgcn_raw_buffer_load_b128(rt, at, 0, 0);
+                    const u32x4 t_lo = __builtin_amdgcn_raw_buffer_load_b128(rt, at, ad.rank_pad * 2, 0);
+                    auto half = [](uint32_t d, int e) { return to_float<DT>((uint16_t)(d >> (16 * (e & 1)))); };
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (e >= valid) break;
+                        const float z = f * (half(t_hi[e / 2], e) + half(t_lo[e / 2], e));
+#pragma unroll
+                        for (int i = 0; i < SIDE; ++i)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                sum[i0 + i][x] += z * (B_NK ? half(w[i][2 * x + (e >> 2)][(e >> 1) & 1], e) : half(w[i][e][x / 2], x));
                     }
                 }
             }

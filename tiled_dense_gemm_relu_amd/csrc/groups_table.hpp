@@ -93,9 +93,11 @@ constexpr int kSkinnyBlocks[kNumSkinny] = {1, 2, 4};
 constexpr int kSkinnyCols = 32, kSkinnyK = 128, kSkinnyThreads = 512;
 
 struct GroupKernels {
-    // [tile][B layout][K % 64 != 0][with adapters]; with adapters the 256 tile takes any K and starts from their terms
-    const void* rows_dma[kNumGroupTiles][2][2][2];
-    const void* weight_dma[kNumGroupTiles];
+    // [tile][B layout][KTAIL][with adapters].  The 256 tile takes rows of whole
+    // 16-byte pieces only (KTAIL < 2); with adapters it takes any such K and starts
+    // from their terms.
+    const void* rows_dma[kNumGroupTiles][2][3][2];
+    const void* weight_dma[kNumGroupTiles][2];    // [tile][rows of any even length]
     const void* rows_skinny[kNumSkinny][2][2][2];   // [blocks][B layout][odd rows][with adapters]
     const void* mask;
     const void* shrink[2];                        // [U layout]
