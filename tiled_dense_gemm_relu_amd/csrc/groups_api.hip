@@ -18,6 +18,8 @@ constexpr int64_t kMaxGroups = 65535;
 
 // Gradients of fewer operations than this take one register-staged launch.
 constexpr double kSmallGrad = 4e9;
+// Rows a group, on average, up to which the weights' gradients are written row by row.
+constexpr int64_t kOuterMost = 8;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
@@ -179,6 +181,32 @@ bool streams(int64_t m, int64_t n, int64_t k, int64_t groups, bool dma)
     return 3.0 + (weights + again) / 3.2e6 < 5.5 + std::max(weights / 5e6, rounds * (double)ceil_div(k, 64) * step);
 }
 
+// The streaming kernel, for A masked by `mask` if that is not NULL.  `parts` (may
+// be NULL) and `counters`: space for partial sums.
+int launch_stream(RowsArgs a, AdapterArgs ad, const uint16_t* mask, int dtype, int b_layout, float* parts, int* counters,
+                  hipStream_t stream)
+{
+    SkinnyPlan plan(a.m, a.n, a.k, a.groups);
+    if (plan.units > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
+    if (!parts) plan.splits = 1;
+    const bool even = even_rows({{a.a, a.k}, {mask, a.k}, {a.b, b_layout == GEMM_RELU_B_NK ? a.k : a.n}});
+    void* args[] = {&a, &ad, &parts, &counters, &mask};
+    return enqueue(kernels(dtype).rows_skinny[plan.kind][b_layout][!even][ad.v ? 1 : mask ? 2 : 0],
+                   dim3((unsigned)plan.units, (unsigned)plan.splits), kSkinnyThreads, args, stream);
+}
+
+// Weights' gradients with few rows a group; `mask` (may be NULL) belongs to w.q if
+// mask_q, else to w.p.
+int launch_outer(WeightArgs w, const uint16_t* mask, bool mask_q, int dtype, hipStream_t stream)
+{
+    const bool whole = w.j % 8 == 0 && aligned(w.q, 16) && aligned(w.out, 16) && (!mask || aligned(mask, 16));
+    const int64_t tiles = int64_t(w.groups) * ceil_div(w.i, kOuterRows) * (whole ? ceil_div(w.j, kOuterCols) : w.j / kOuterCols + 1);
+    if (tiles > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
+    void* args[] = {&w, &mask};
+    return enqueue(kernels(dtype).weight_outer[!mask ? 0 : mask_q ? 2 : 1][whole], dim3((unsigned)tiles), kOuterThreads, args,
+                   stream);
+}
+
 // A product over row groups (M, N, K > 0).  `parts` (may be NULL) and `counters`:
 // space for the streaming kernel's partial sums.
 int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config, int cus, float* parts, int* counters,
@@ -187,14 +215,8 @@ int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config,
     a.c_vec = store_width(a.c, a.n);
     const Rows rows_a{a.a, a.k}, rows_b{a.b, b_layout == GEMM_RELU_B_NK ? a.k : a.n};
     const DmaRows dma = std::min(dma_rows(a.a, a.k), dma_rows(a.b, rows_b.length));
-    if (config == GEMM_RELU_GROUPS_STREAM || (config == GEMM_RELU_GROUPS_AUTO && streams(a.m, a.n, a.k, a.groups, dma != kDmaNone))) {
-        SkinnyPlan plan(a.m, a.n, a.k, a.groups);
-        if (plan.units > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
-        if (!parts) plan.splits = 1;
-        void* args[] = {&a, &ad, &parts, &counters};
-        return enqueue(kernels(dtype).rows_skinny[plan.kind][b_layout][!even_rows({rows_a, rows_b})][ad.v != nullptr],
-                       dim3((unsigned)plan.units, (unsigned)plan.splits), kSkinnyThreads, args, stream);
-    }
+    if (config == GEMM_RELU_GROUPS_STREAM || (config == GEMM_RELU_GROUPS_AUTO && streams(a.m, a.n, a.k, a.groups, dma != kDmaNone)))
+        return launch_stream(a, ad, nullptr, dtype, b_layout, parts, counters, stream);
     int staged = 0;
     if (dma == kDmaNone) {
         const GroupShape g(a.m, a.groups);
@@ -272,6 +294,25 @@ int launch_grad_staged(RowsArgs r, WeightArgs w, const uint16_t* mask, int dtype
                    kStagedThreads, args, stream);
 }
 
+// d = dc where c > 0, else +0.0.
+int launch_mask(const uint16_t* dc, const uint16_t* c, uint16_t* d, int64_t count, int dtype, hipStream_t stream)
+{
+    MaskArgs m{dc, c, d, count, aligned(dc, 16) && aligned(c, 16)};
+    void* args[] = {&m};
+    return enqueue(kernels(dtype).mask, dim3((unsigned)std::min<int64_t>(ceil_div(count, 2048), 4096)), 256, args, stream);
+}
+
+// dA alone: r.a is dC, masked by `c` (unless NULL) on the way, into `masked`.
+int launch_grad_rows(RowsArgs r, const uint16_t* c, uint16_t* masked, int dtype, int b_layout, int config, int cus, hipStream_t stream)
+{
+    if (c) {
+        const int rc = launch_mask(r.a, c, masked, int64_t(r.m) * r.k, dtype, stream);
+        if (rc != GEMM_RELU_OK) return rc;
+        r.a = masked;
+    }
+    return launch_rows(r, AdapterArgs{}, dtype, b_layout, config, cus, nullptr, nullptr, stream);
+}
+
 // Workspace of the adapters: the counters, the intermediates, each row's
 // adapter, and the partial sums of a K that is cut into `splits` parts: as many
 // as make 512 workgroups, while each of their 8 waves has a piece of K.
@@ -340,7 +381,8 @@ int64_t gemm_relu_grouped_backward_workspace(int64_t M, int64_t N, int64_t K, in
     const int rc = check_shape(M, N, K, groups, dtype, b_layout);
     if (rc != GEMM_RELU_OK) return rc;
     if (relu != 0 && relu != 1) return GEMM_RELU_ERR_INVALID_ARG;
-    return GEMM_RELU_GROUPS_COUNTER_BYTES + (relu ? round_up(2 * M * N, 256) : 0);
+    // the masked gradient, and partial sums of dA's product (inner dimension N)
+    return GEMM_RELU_GROUPS_COUNTER_BYTES + (relu ? round_up(2 * M * N, 256) : 0) + SkinnyPlan(M, K, N, groups).bytes;
 }
 
 int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, const void* B, const int32_t* ends,
@@ -375,20 +417,30 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
     const uint16_t *x = static_cast<const uint16_t*>(A), *b = static_cast<const uint16_t*>(B);
     // dA = D (M, N) times B^T: B as stored (K, N) is the transposed weight of this product
     const bool kn = b_layout == GEMM_RELU_B_KN;
+    const int64_t masked_bytes = relu ? round_up(2 * mn, 256) : 0, parts_at = GEMM_RELU_GROUPS_COUNTER_BYTES + masked_bytes;
+    uint16_t* masked = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + GEMM_RELU_GROUPS_COUNTER_BYTES);
     const int layout_a = kn ? GEMM_RELU_B_NK : GEMM_RELU_B_KN;
     RowsArgs r{d, b, static_cast<uint16_t*>(dA), ends, (int)M, (int)K, (int)N, (int)groups, 0, 0};
     WeightArgs w{kn ? x : d, kn ? d : x, static_cast<uint16_t*>(dB), ends, (int)M, (int)(kn ? K : N), (int)(kn ? N : K),
                  (int)groups, 0};
     // LDS DMA needs rows of an even length and D itself in memory.  The register-
     // staged kernel needs neither, and is one launch instead of two or three.
+    // Few rows a group: the weights' gradients are written, the weights read, at memory's pace.
+    const GroupShape shape(M, groups);
+    if (config_id == GEMM_RELU_GROUPS_STREAM || (config_id == GEMM_RELU_GROUPS_AUTO && shape.rows <= kOuterMost)) {
+        float* parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts_at);
+        if (want_a && (config_id == GEMM_RELU_GROUPS_STREAM || streams(M, K, N, groups, std::min(dma_rows(d, N), dma_rows(b, kn ? N : K)))))
+            rc = launch_stream(r, AdapterArgs{}, c, dtype, layout_a, parts, static_cast<int*>(workspace), s);
+        else if (want_a)
+            rc = launch_grad_rows(r, c, masked, dtype, layout_a, config_id, cus, s);
+        if (want_b && rc == GEMM_RELU_OK && gkn > 0) rc = launch_outer(w, c, kn, dtype, s);
+        return rc;
+    }
     const bool dma = dma_rows(d, N) && (!want_a || dma_rows(b, kn ? N : K)) && (!want_b || dma_rows(x, K));   // kDmaNone: false
     if (config_id == GEMM_RELU_GROUPS_TILED || !dma || (config_id == GEMM_RELU_GROUPS_AUTO && 4.0 * M * N * K < kSmallGrad))
         return launch_grad_staged(r, w, c, dtype, layout_a, config_id, cus, s);
     if (relu) {
-        uint16_t* masked = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + GEMM_RELU_GROUPS_COUNTER_BYTES);
-        MaskArgs m{d, c, masked, mn, aligned(dC, 16) && aligned(C, 16)};
-        void* args[] = {&m};
-        rc = enqueue(kernels(dtype).mask, dim3((unsigned)std::min<int64_t>(ceil_div(mn, 2048), 4096)), 256, args, s);
+        rc = launch_mask(d, c, masked, mn, dtype, s);
         r.a = masked;
         (kn ? w.q : w.p) = masked;
     }

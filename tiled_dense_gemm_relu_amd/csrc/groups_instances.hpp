@@ -4,6 +4,7 @@
 
 #include "groups_dma.hpp"
 #include "groups_kernels.hpp"
+#include "groups_outer.hpp"
 #include "groups_skinny.hpp"
 
 namespace gemm_relu_hip {
@@ -88,10 +89,12 @@ template <int DT, int S, bool B_NK>
 void fill_skinny(GroupKernels& t)
 {
     constexpr int MB = kSkinnyBlocks[S];
-    t.rows_skinny[S][B_NK][0][0] = (const void*)&rows_skinny<DT, B_NK, MB, false, false>;
-    t.rows_skinny[S][B_NK][0][1] = (const void*)&rows_skinny<DT, B_NK, MB, false, true>;
-    t.rows_skinny[S][B_NK][1][0] = (const void*)&rows_skinny<DT, B_NK, MB, true, false>;
-    t.rows_skinny[S][B_NK][1][1] = (const void*)&rows_skinny<DT, B_NK, MB, true, true>;
+    t.rows_skinny[S][B_NK][0][0] = (const void*)&rows_skinny<DT, B_NK, MB, false, kSkinnyPlain>;
+    t.rows_skinny[S][B_NK][0][1] = (const void*)&rows_skinny<DT, B_NK, MB, false, kSkinnyAdapters>;
+    t.rows_skinny[S][B_NK][0][2] = (const void*)&rows_skinny<DT, B_NK, MB, false, kSkinnyMasked>;
+    t.rows_skinny[S][B_NK][1][0] = (const void*)&rows_skinny<DT, B_NK, MB, true, kSkinnyPlain>;
+    t.rows_skinny[S][B_NK][1][1] = (const void*)&rows_skinny<DT, B_NK, MB, true, kSkinnyAdapters>;
+    t.rows_skinny[S][B_NK][1][2] = (const void*)&rows_skinny<DT, B_NK, MB, true, kSkinnyMasked>;
 }
 
 template <int DT>
@@ -107,6 +110,12 @@ GroupKernels make_group_table()
     fill_group_tile<DT, 0>(t);
     fill_group_tile<DT, 1>(t);
     fill_group_tile<DT, 2>(t);
+    t.weight_outer[0][0] = (const void*)&weight_outer<DT, 0, false>;
+    t.weight_outer[0][1] = (const void*)&weight_outer<DT, 0, true>;
+    t.weight_outer[1][0] = (const void*)&weight_outer<DT, 1, false>;
+    t.weight_outer[1][1] = (const void*)&weight_outer<DT, 1, true>;
+    t.weight_outer[2][0] = (const void*)&weight_outer<DT, 2, false>;
+    t.weight_outer[2][1] = (const void*)&weight_outer<DT, 2, true>;
     t.mask = (const void*)&relu_mask<DT>;
     t.shrink[0] = (const void*)&adapter_shrink<DT, false>;
     t.shrink[1] = (const void*)&adapter_shrink<DT, true>;

@@ -180,6 +180,40 @@ __device__ __forceinline__ void load_dwords_any(const uint16_t* p, int valid, ui
     for (int i = 0; i < W; ++i) out[i] = __builtin_amdgcn_alignbit(d[i + 1], d[i], 16 * odd);
 }
 
+// ---------------------------------------------------------------- ReLU's gradient
+
+// d = dc where c > 0, else +0.0 (c's sign decides: 16-bit floats above zero are
+// the patterns 0x0001 .. infinity; NaN counts as not above zero).
+template <int DT>
+__device__ __forceinline__ uint16_t mask_one(uint16_t dc, uint16_t c)
+{
+    constexpr uint16_t inf = DT == kF16 ? 0x7c00 : 0x7f80;
+    return (uint16_t)(c - 1) < inf ? dc : (uint16_t)0;
+}
+
+template <int DT>
+__device__ __forceinline__ u32x4 mask_chunk(u32x4 dc, u32x4 c)
+{
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+        dc[w] = (uint32_t)mask_one<DT>((uint16_t)dc[w], (uint16_t)c[w]) |
+                ((uint32_t)mask_one<DT>((uint16_t)(dc[w] >> 16), (uint16_t)(c[w] >> 16)) << 16);
+    return dc;
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void relu_mask(MaskArgs a)
+{
+    const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+    const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const int64_t chunks = a.vec ? a.count / 8 : 0;
+    for (int64_t q = first; q < chunks; q += stride) {
+        reinterpret_cast<u32x4*>(a.d)[q] =
+            mask_chunk<DT>(reinterpret_cast<const u32x4*>(a.dc)[q], reinterpret_cast<const u32x4*>(a.c)[q]);
+    }
+    for (int64_t q = chunks * 8 + first; q < a.count; q += stride) a.d[q] = mask_one<DT>(a.dc[q], a.c[q]);
+}
+
 // ---------------------------------------------------------------- adapters
 
 // Bytes of LDS that add_adapters stages V in, per wave: 32 k of its columns.
@@ -505,40 +539,6 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs a)
         t[a.rank_pad] = fabsf(scaled) < __builtin_inff() ? act_cast<DT>(rest, false) : (uint16_t)0;
     }
     if (col == 0) a.factor[m] = ldexpf(1.0f, e);
-}
-
-// ---------------------------------------------------------------- ReLU's gradient
-
-// d = dc where c > 0, else +0.0 (c's sign decides: 16-bit floats above zero are
-// the patterns 0x0001 .. infinity; NaN counts as not above zero).
-template <int DT>
-__device__ __forceinline__ uint16_t mask_one(uint16_t dc, uint16_t c)
-{
-    constexpr uint16_t inf = DT == kF16 ? 0x7c00 : 0x7f80;
-    return (uint16_t)(c - 1) < inf ? dc : (uint16_t)0;
-}
-
-template <int DT>
-__device__ __forceinline__ u32x4 mask_chunk(u32x4 dc, u32x4 c)
-{
-#pragma unroll
-    for (int w = 0; w < 4; ++w)
-        dc[w] = (uint32_t)mask_one<DT>((uint16_t)dc[w], (uint16_t)c[w]) |
-                ((uint32_t)mask_one<DT>((uint16_t)(dc[w] >> 16), (uint16_t)(c[w] >> 16)) << 16);
-    return dc;
-}
-
-template <int DT>
-__global__ __launch_bounds__(256) void relu_mask(MaskArgs a)
-{
-    const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-    const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int64_t chunks = a.vec ? a.count / 8 : 0;
-    for (int64_t q = first; q < chunks; q += stride) {
-        reinterpret_cast<u32x4*>(a.d)[q] =
-            mask_chunk<DT>(reinterpret_cast<const u32x4*>(a.dc)[q], reinterpret_cast<const u32x4*>(a.c)[q]);
-    }
-    for (int64_t q = chunks * 8 + first; q < a.count; q += stride) a.d[q] = mask_one<DT>(a.dc[q], a.c[q]);
 }
 
 }  // namespace gemm_relu_hip

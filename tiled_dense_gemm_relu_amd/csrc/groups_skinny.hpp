@@ -75,12 +75,16 @@ __device__ __forceinline__ float low_rank_term(const AdapterArgs& ad, int m, int
 // C = act(rows of A @ their group's B [+ their adapters' terms]).  Workgroup b of
 // a part of K: column block and row tile as tile_coords orders them for the
 // XCDs, columns fastest.  With few units K is cut into gridDim.y parts, combined
-// as in adapter_shrink.
-template <int DT, bool B_NK, int MB, bool ODD, bool ADAPT>
-__global__ __launch_bounds__(kSkinnyThreads) void rows_skinny(RowsArgs a, AdapterArgs ad, float* parts, int* counters)
+// as in adapter_shrink.  kSkinnyMasked: A is zero where `mask`, a matrix of its
+// shape, is not above zero.
+enum { kSkinnyPlain = 0, kSkinnyAdapters = 1, kSkinnyMasked = 2 };
+template <int DT, bool B_NK, int MB, bool ODD, int MODE>
+__global__ __launch_bounds__(kSkinnyThreads) void rows_skinny(RowsArgs a, AdapterArgs ad, float* parts, int* counters,
+                                                              const uint16_t* mask)
 {
     constexpr int WAVES = kSkinnyThreads / 64, STEPS = kSkinnyK / 32, ROWS = 16 * MB, ROW = kSkinnyCols * 2;
     constexpr int kDeviceScope = 16;   // cache policy sc1
+    constexpr bool ADAPT = MODE == kSkinnyAdapters, MASKED = MODE == kSkinnyMasked;
     constexpr int PART = kSkinnyCols * (ROWS + 1);
     // the waves' sums, and before that their strips of B (K, N)
     __shared__ __attribute__((aligned(16))) float part[WAVES * PART > WAVES * 512 ? WAVES * PART : WAVES * 512];
@@ -103,6 +107,7 @@ __global__ __launch_bounds__(kSkinnyThreads) void rows_skinny(RowsArgs a, Adapte
         for (int j = 0; j < MB; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     if (real) {
         const AnyRsrc rx = make_any_rsrc(a.a + (size_t)tile.begin * k_len, (uint32_t)rows * (uint32_t)a.k * 2u);
+        const AnyRsrc rm = MASKED ? make_any_rsrc(mask + (size_t)tile.begin * k_len, (uint32_t)rows * (uint32_t)a.k * 2u) : rx;
         const uint16_t* b = a.b + (size_t)tile.group * k_len * n_len;
         const AnyRsrc rb = B_NK ? make_any_rsrc(b + (size_t)n0 * k_len, (uint32_t)min(kSkinnyCols, a.n - n0) * (uint32_t)a.k * 2u)
                                 : AnyRsrc{};
@@ -120,7 +125,7 @@ __global__ __launch_bounds__(kSkinnyThreads) void rows_skinny(RowsArgs a, Adapte
             const AnyRsrc rp = B_NK ? rb
                                     : make_any_rsrc(b + (size_t)k0 * n_len + n0,
                                                     (uint32_t)(min(kSkinnyK, a.k - k0) * a.n - n0) * 2u);
-            SkinnyChunk<ODD> x[STEPS][MB], w[STEPS][2];
+            SkinnyChunk<ODD> x[STEPS][MB], w[STEPS][2], above[MASKED ? STEPS : 1][MASKED ? MB : 1];
             uint32_t x_off[MB], w_off[2];
 #pragma unroll
             for (int j = 0; j < MB; ++j) {
@@ -138,7 +143,10 @@ __global__ __launch_bounds__(kSkinnyThreads) void rows_skinny(RowsArgs a, Adapte
 #pragma unroll
                 for (int i = 0; i < 2; ++i) w[s][i] = load_skinny<ODD>(rp, w_off[i] + (B_NK ? 64u * s : 64u * s * (uint32_t)a.n));
 #pragma unroll
-                for (int j = 0; j < MB; ++j) x[s][j] = load_skinny<ODD>(rx, x_off[j] + 64u * s);
+                for (int j = 0; j < MB; ++j) {
+                    x[s][j] = load_skinny<ODD>(rx, x_off[j] + 64u * s);
+                    if constexpr (MASKED) above[s][j] = load_skinny<ODD>(rm, x_off[j] + 64u * s);
+                }
             }
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
@@ -147,6 +155,7 @@ __global__ __launch_bounds__(kSkinnyThreads) void rows_skinny(RowsArgs a, Adapte
 #pragma unroll
                 for (int j = 0; j < MB; ++j) {
                     xv[j] = skinny_value<ODD>(x[s][j], rx, x_off[j] + 64u * s);
+                    if constexpr (MASKED) xv[j] = mask_chunk<DT>(xv[j], skinny_value<ODD>(above[s][j], rm, x_off[j] + 64u * s));
                     if (tail) xv[j] = keep_first(xv[j], valid);
                 }
 #pragma unroll

@@ -90,6 +90,8 @@ struct StagedKernels {
 // Streaming kernels for few rows a group: 16-row blocks a workgroup takes.
 constexpr int kNumSkinny = 3;
 constexpr int kSkinnyBlocks[kNumSkinny] = {1, 2, 4};
+// Weights' gradients with few rows a group.
+constexpr int kOuterRows = 32, kOuterCols = 512, kOuterThreads = 256;
 constexpr int kSkinnyCols = 32, kSkinnyK = 128, kSkinnyThreads = 512;
 
 struct GroupKernels {
@@ -98,7 +100,8 @@ struct GroupKernels {
     // from their terms.
     const void* rows_dma[kNumGroupTiles][2][3][2];
     const void* weight_dma[kNumGroupTiles][2];    // [tile][rows of any even length]
-    const void* rows_skinny[kNumSkinny][2][2][2];   // [blocks][B layout][odd rows][with adapters]
+    const void* rows_skinny[kNumSkinny][2][2][3];   // [blocks][B layout][odd rows][plain, adapters, masked]
+    const void* weight_outer[3][2];                 // [masked: no, p, q][rows of whole pieces]
     const void* mask;
     const void* shrink[2];                        // [U layout]
 };
