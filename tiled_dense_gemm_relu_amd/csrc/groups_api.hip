@@ -80,7 +80,7 @@ DmaRows dma_rows(const void* p, int64_t row)
     return row % 8 == 0 && aligned(p, 16) ? kDmaWhole : row % 2 == 0 && aligned(p, 4) ? kDmaEven : kDmaNone;
 }
 
-int store_width(const void* c, int64_t n) { return n % 8 == 0 && aligned(c, 16) ? 2 : 0; }
+int store_width(const void* c, int64_t n) { return n % 8 == 0 && aligned(c, 16) ? 2 : n % 4 == 0 && aligned(c, 8) ? 1 : 0; }
 
 const GroupKernels& kernels(int dtype) { return dtype == GEMM_RELU_F16 ? group_kernels_f16() : group_kernels_bf16(); }
 
@@ -490,7 +490,7 @@ int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* 
                   reinterpret_cast<float*>(ws + space.part), reinterpret_cast<int*>(ws), (int)M, (int)K, (int)segments,
                   (int)adapters, (int)rank, (int)space.rank_pad};
     void* args[] = {&sh};
-    rc = enqueue(kernels(dtype).shrink[b_layout], dim3((unsigned)space.tiles, (unsigned)space.splits), kShrinkThreads, args, s);
+    rc = enqueue(kernels(dtype).shrink[b_layout][rank > kShrinkCols], dim3((unsigned)space.tiles, (unsigned)space.splits), kShrinkThreads, args, s);
     if (rc != GEMM_RELU_OK) return rc;
     RowsArgs a{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(W), static_cast<uint16_t*>(C), nullptr,
                (int)M, (int)N, (int)K, 1, relu, 0};

@@ -72,7 +72,7 @@ struct UnitOrder {
         width = blocks / xcds;
     }
     // The first of `total` that belong to XCD x and later ones.
-    __device__ __forceinline__ int64_t part(int64_t total, int x) const { return total * x / xcds; }
+    __device__ __forceinline__ int64_t part(int64_t total, int x) const { return xcds == 8 ? total * x / 8 : total * x; }
     // Position of this workgroup's i-th unit in the list.
     __device__ __forceinline__ int position(int i) const { return i * width + ((i & 1) ? width - 1 - place : place); }
     __device__ __forceinline__ int units(int listed) const
@@ -121,7 +121,8 @@ struct RowUnits {
         // the first column whose work starts at or past w
         auto column = [&](int64_t w) {
             const int64_t past = w - (work + (int64_t)before * tiles_n);
-            return past <= 0 || c == 0 ? 0 : (int)min((int64_t)tiles_n, (past + c - 1) / c);
+            if (past <= 0 || c == 0) return 0;
+            return past >= (int64_t)c * tiles_n ? tiles_n : (int)(((uint32_t)past + c - 1u) / (uint32_t)c);   // c tiles_n <= 2^31
         };
         Lane k;
         k.begin = r.begin;
@@ -678,10 +679,17 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
                 cut(smem + Cfg::B_REGION + slot * Cfg::B_STAGE + (dwave * QB + q) * 1024, b_pos[q % PB]);
         }
     };
-    if (!STAGED && (!WS || producer)) {
+    auto push_left = [&]() __attribute__((always_inline)) {
 #pragma unroll
+        for (int s = 0; s + 1 < PRO; ++s) lefts[s] = lefts[s + 1];
+        lefts[PRO - 1] = f_left;
+    };
+    if (!STAGED && (!WS || producer)) {
+        // (One copy of the code for all stages, here and elsewhere: what does not fit
+        // the instruction cache is fetched again for every tile.)
+#pragma unroll 1
         for (int s = 0; s < PRO; ++s) {
-            lefts[s] = f_left;
+            push_left();
 #pragma unroll
             for (int q = 0; q < NQ; ++q) dma(s, q);
             fill_advance();
@@ -694,9 +702,7 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
         if (producer) {
             for (int g = 0; f_unit < n_units || g < f_steps; ++g) {
                 const int slot_fill = (g + S - 1) & (S - 1);
-#pragma unroll
-                for (int s = 0; s + 1 < PRO; ++s) lefts[s] = lefts[s + 1];
-                lefts[PRO - 1] = f_left;
+                push_left();
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) dma(slot_fill, q);
                 fill_advance();
@@ -727,11 +733,12 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
     // wave of each half).  Each kind has code of its own for a whole unit, from its
     // first fragments to its stores, so that nothing in registers passes from
     // one kind to another.
+    constexpr bool HALVES = FM > 1 && ADAPT != kAdaptAfter;   // (rows of one group: few tiles are partial)
     int c_blocks = FM;
     auto set_blocks = [&]() {
         if constexpr (Units::RAGGED) {
             const int live = c.m_end - c.m0 - wm * Cfg::WTM;
-            c_blocks = live > Cfg::WTM / 2 ? FM : live > 0 ? (FM > 1 ? FM / 2 : FM) : 0;
+            c_blocks = live > (HALVES ? Cfg::WTM / 2 : 0) ? FM : live > 0 ? FM / 2 : 0;
         }
     };
     set_blocks();
@@ -822,10 +829,11 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
                                            smem + Cfg::LDS_BYTES + wave * Cfg::STRIP);
             uint16_t* out = C + (size_t)c.group * c_group;
             uint8_t* const strip = smem + Cfg::LDS_BYTES + wave * Cfg::STRIP;
-            if (c_vec < 2) {
+            if (c_vec == 0) {
                 store_rows_any<DT, FX>(out, acc, strip, lane, m_base, n_base, c.m_end, N, relu);
-            } else if constexpr (FN % 4 == 0) {
-                store_rows_staged<DT, FX>(out, acc, strip, lane, m_base, n_base, c.m_end, N, relu);
+            } else if (FN % 4 == 0 && c_vec == 2) {
+                if constexpr (FN % 4 == 0)
+                    store_rows_staged<DT, FX>(out, acc, strip, lane, m_base, n_base, c.m_end, N, relu);
             } else {
 #pragma unroll
                 for (int i = 0; i < FN; ++i)
@@ -838,7 +846,7 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
     while (true) {
         if constexpr (Units::RAGGED) {
             if (c_blocks == FM) run(std::integral_constant<int, FM>{});
-            else if (FM > 1 && c_blocks > 0) run(std::integral_constant<int, FM / 2>{});
+            else if (HALVES && c_blocks > 0) run(std::integral_constant<int, HALVES ? FM / 2 : 0>{});
             else run(std::integral_constant<int, 0>{});
         } else {
             run(std::integral_constant<int, FM>{});

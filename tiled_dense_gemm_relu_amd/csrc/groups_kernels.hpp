@@ -306,16 +306,18 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
                 }
             }
         }
-        auto lanes = [&](auto fast) __attribute__((always_inline)) {
-            constexpr bool FAST = decltype(fast)::value;
-            constexpr int SIDE = FN < 2 ? FN : 2;       // 16-column blocks whose loads are in flight together
+        if (more && id >= 0) {
+            auto half = [](uint32_t d, int e) { return to_float<DT>((uint16_t)(d >> (16 * (e & 1)))); };
             const uint16_t* vp = ad.v + (size_t)id * (size_t)ad.rank * (size_t)N;
+            constexpr int SIDE = FN < 2 ? FN : 2;       // 16-column blocks whose loads are in flight together
+#pragma unroll 1
+            for (int r0 = 0; r0 < ad.rank; r0 += 8) {
+                const int valid = min(8, ad.rank - r0);
+                const uint32_t at = m * t_row + (uint32_t)r0 * 2u;
+                const u32x4 t_hi = __builtin_amdgcn_raw_buffer_load_b128(rt, at, 0, 0);
+                const u32x4 t_lo = __builtin_amdgcn_raw_buffer_load_b128(rt, at, ad.rank_pad * 2, 0);
 #pragma unroll
-            for (int i0 = 0; i0 < FN; i0 += SIDE) {
-#pragma unroll B_NK ? 1 : 2
-                for (int r0 = 0; r0 < ad.rank; r0 += 8) {
-                    const int valid = min(8, ad.rank - r0);
-                    // V first: its loads wait for nothing
+                for (int i0 = 0; i0 < FN; i0 += SIDE) {
                     uint32_t w[SIDE][8][2];             // [k] pairs of columns, or [4 pairs of k, 2 columns at a time]
 #pragma unroll
                     for (int i = 0; i < SIDE; ++i) {
@@ -326,7 +328,7 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
                             for (int x = 0; x < 4; ++x) {
                                 const uint16_t* p = vp + (size_t)(n + min(x, cols - 1)) * (size_t)ad.rank + r0;
                                 uint32_t q[4];
-                                if constexpr (FAST) {
+                                if (ad.v_fast) {
                                     const u32x4 v = *reinterpret_cast<const u32x4*>(p);
                                     q[0] = v[0], q[1] = v[1], q[2] = v[2], q[3] = v[3];
                                 } else {
@@ -339,7 +341,7 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 const uint16_t* p = vp + (size_t)(r0 + min(e, valid - 1)) * (size_t)N + n;
-                                if constexpr (FAST) {
+                                if (ad.v_fast) {
                                     const u32x2 v = *reinterpret_cast<const u32x2*>(p);
                                     w[i][e][0] = v[0], w[i][e][1] = v[1];
                                 } else {
@@ -348,28 +350,19 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
                             }
                         }
                     }
-                    const uint32_t at = m * t_row + (uint32_t)r0 * 2u;
-                    const u32x4 t_hi = __builtin_amdgcn_raw_buffer_load_b128(rt, at, 0, 0);
-                    const u32x4 t_lo = __builtin_amdgcn_raw_buffer_load_b128(rt, at, ad.rank_pad * 2, 0);
-                    auto half = [](uint32_t d, int e) { return to_float<DT>((uint16_t)(d >> (16 * (e & 1)))); };
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        if (e >= valid) break;
-                        const float z = f * (half(t_hi[e / 2], e) + half(t_lo[e / 2], e));
+                        const float z = e < valid ? f * (half(t_hi[e / 2], e) + half(t_lo[e / 2], e)) : 0.0f;
 #pragma unroll
                         for (int i = 0; i < SIDE; ++i)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                sum[i0 + i][x] += z * (B_NK ? half(w[i][2 * x + (e >> 2)][(e >> 1) & 1], e) : half(w[i][e][x / 2], x));
+                            for (int x = 0; x < 4; ++x) {
+                                const float v = B_NK ? half(w[i][2 * x + (e >> 2)][(e >> 1) & 1], e) : half(w[i][e][x / 2], x);
+                                sum[i0 + i][x] += e < valid ? z * v : 0.0f;
+                            }
                     }
                 }
             }
-        };
-        if (more && id >= 0) {
-            if (ad.v_fast)
-                lanes(std::true_type{});
-            else
-                lanes(std::false_type{});
         }
 #pragma unroll
         for (int i = 0; i < FN; ++i) acc[i][j] += sum[i];
@@ -382,19 +375,19 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
 // factor a power of two of the row's largest |z|, hi the nearest 16-bit value
 // to z / factor (at most 1 in size) and lo that to what is left.  row_id[m] is
 // the row's adapter, -1 for none.
-//  One workgroup per 16 rows of a segment and part of K, 32 columns of rank at
-// a time: its 8 waves take pieces of 128 k in turn, each with all its loads in
+//  One workgroup per 16 rows of a segment and part of K, CHUNKS times 32 columns
+// of rank at a time: its 8 waves take pieces of 128 k in turn, each with all its loads in
 // flight at once, and their sums are added in wave order in LDS.  With few rows
 // K is cut into `splits` parts, whose sums go through device memory
 // (device-scope accesses: the parts run on different XCDs); the part that
 // counts itself last adds them in part order and finishes.  Nothing waits for
 // another workgroup.
-template <int DT, bool U_NK>
+template <int DT, bool U_NK, int CHUNKS>
 __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs a)
 {
     constexpr int WAVES = kShrinkThreads / 64, STEPS = kShrinkK / 32, ROW = kShrinkCols * 2;
     constexpr int kDeviceScope = 16;   // cache policy sc1
-    __shared__ float part[WAVES][kShrinkCols][kShrinkRows + 1];
+    __shared__ float part[CHUNKS][WAVES][kShrinkCols][kShrinkRows + 1];
     __shared__ float sums[kMaxRank / kShrinkCols][kShrinkThreads];
     __shared__ __attribute__((aligned(16))) uint8_t strips[U_NK ? 16 : WAVES * 32 * ROW];
     __shared__ int before;
@@ -417,65 +410,78 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs a)
     const int pieces = (a.k + kShrinkK - 1) / kShrinkK, splits = (int)gridDim.y;
     const int p_begin = (int)((int64_t)pieces * blockIdx.y / splits) + wave;
     const int p_end = (int)((int64_t)pieces * (blockIdx.y + 1) / splits);
-    for (int c = 0; c < chunks; ++c) {
-        const int r_base = c * kShrinkCols;
+    for (int c0 = 0; c0 < chunks; c0 += CHUNKS) {
+        const int r_base = c0 * kShrinkCols;
         // U stored (rank, K): rows r_base .. of U^T
         const AnyRsrc ru = make_any_rsrc(a.u + (size_t)id * k_len * rank + (U_NK ? (size_t)r_base * k_len : 0),
-                                         (uint32_t)(U_NK ? min(kShrinkCols, a.rank - r_base) : a.rank) * (uint32_t)a.k * 2u);
-        floatx4 acc[2] = {floatx4{0}, floatx4{0}};
+                                         (uint32_t)(U_NK ? min(CHUNKS * kShrinkCols, a.rank - r_base) : a.rank) * (uint32_t)a.k * 2u);
+        floatx4 acc[CHUNKS][2];
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) acc[c][0] = acc[c][1] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
         for (int p = p_begin; p < p_end; p += WAVES) {
             const int k0 = p * kShrinkK;
-            AnyChunk x[STEPS], u[STEPS][2];
+            AnyChunk x[STEPS], u[STEPS][CHUNKS][2];
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int k = k0 + 32 * s + 8 * kb;
                 x[s] = load_any(rx, ((uint32_t)r16 * (uint32_t)a.k + (uint32_t)k) * 2u, k < a.k);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if constexpr (U_NK) {
-                        u[s][i] = load_any(ru, ((uint32_t)(16 * i + r16) * (uint32_t)a.k + (uint32_t)k) * 2u, k < a.k);
-                    } else {
-                        const int kr = k0 + 32 * s + 16 * i + (lane >> 2), r = r_base + 8 * (lane & 3);
-                        u[s][i] = load_any(ru, ((uint32_t)kr * (uint32_t)a.rank + (uint32_t)r) * 2u, kr < a.k && r < a.rank);
+                for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if constexpr (U_NK) {
+                            const int r = c * kShrinkCols + 16 * i + r16;
+                            u[s][c][i] = load_any(ru, ((uint32_t)r * (uint32_t)a.k + (uint32_t)k) * 2u, k < a.k && r_base + r < a.rank);
+                        } else {
+                            const int kr = k0 + 32 * s + 16 * i + (lane >> 2), r = r_base + c * kShrinkCols + 8 * (lane & 3);
+                            u[s][c][i] = load_any(ru, ((uint32_t)kr * (uint32_t)a.rank + (uint32_t)r) * 2u, kr < a.k && r < a.rank);
+                        }
                     }
-                }
             }
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int valid = a.k - (k0 + 32 * s + 8 * kb);
                 const u32x4 xv = keep_first(chunk_value(x[s]), valid);
-                u32x4 uv[2];
-                if constexpr (U_NK) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) uv[i] = keep_first(chunk_value(u[s][i]), valid);
-                } else {
+                for (int c = 0; c < CHUNKS; ++c) {
+                    u32x4 uv[2];
+                    if constexpr (U_NK) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int kr = 16 * i + (lane >> 2);
-                        *reinterpret_cast<u32x4*>(strip + kr * ROW + 16 * ((lane & 3) ^ b_swizzle<ROW, 16>(kr))) = chunk_value(u[s][i]);
+                        for (int i = 0; i < 2; ++i) uv[i] = keep_first(chunk_value(u[s][c][i]), valid);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int kr = 16 * i + (lane >> 2);
+                            *reinterpret_cast<u32x4*>(strip + kr * ROW + 16 * ((lane & 3) ^ b_swizzle<ROW, 16>(kr))) = chunk_value(u[s][c][i]);
+                        }
+                        const int kr = 8 * kb + (r16 >> 2);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int r = 16 * i + 4 * (r16 & 3);
+                            const uint8_t* q = strip + kr * ROW + 16 * ((r >> 3) ^ b_swizzle<ROW, 16>(kr)) + 8 * (r16 & 1);
+                            const u32x2 lo = ds_read_tr16(q), hi = ds_read_tr16(q + 4 * ROW);
+                            uv[i] = u32x4{lo.x, lo.y, hi.x, hi.y};
+                        }
                     }
-                    const int kr = 8 * kb + (r16 >> 2);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = 16 * i + 4 * (r16 & 3);
-                        const uint8_t* q = strip + kr * ROW + 16 * ((r >> 3) ^ b_swizzle<ROW, 16>(kr)) + 8 * (r16 & 1);
-                        const u32x2 lo = ds_read_tr16(q), hi = ds_read_tr16(q + 4 * ROW);
-                        uv[i] = u32x4{lo.x, lo.y, hi.x, hi.y};
-                    }
+                    for (int i = 0; i < 2; ++i) acc[c][i] = mfma_16x16x32<DT>(uv[i], xv, acc[c][i]);
                 }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) acc[i] = mfma_16x16x32<DT>(uv[i], xv, acc[i]);
             }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) part[wave][16 * i + 4 * (lane >> 4) + e][r16] = acc[i][e];
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) part[c][wave][16 * i + 4 * (lane >> 4) + e][r16] = acc[c][i][e];
         __syncthreads();
-        float z = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) z += part[w][col][row];
-        sums[c][threadIdx.x] = z;
+        for (int c = 0; c < CHUNKS; ++c) {
+            float z = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) z += part[c][w][col][row];
+            if (c0 + c < chunks) sums[c0 + c][threadIdx.x] = z;
+        }
         __syncthreads();
     }
     if (splits > 1) {

@@ -51,6 +51,7 @@ __device__ __forceinline__ float low_rank_term(const AdapterArgs& ad, int m, int
     const uint16_t* v = ad.v + (size_t)id * (size_t)ad.rank * (size_t)N + (B_NK ? (size_t)n * (size_t)ad.rank : (size_t)n);
     const size_t step = B_NK ? 1 : (size_t)N;
     float sum = 0.0f;
+#pragma unroll 4
     for (int r0 = 0; r0 < ad.rank; r0 += 8) {
         const u32x4 hi = *reinterpret_cast<const u32x4*>(t + r0), lo = *reinterpret_cast<const u32x4*>(t + ad.rank_pad + r0);
         uint16_t w[8];

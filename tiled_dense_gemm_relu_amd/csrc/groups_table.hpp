@@ -15,7 +15,7 @@ struct RowsArgs {
     const int* ends;
     int m, n, k, groups;
     int relu;
-    int c_vec;             // 2: rows of C allow 16-byte stores, else 0
+    int c_vec;             // rows of C allow 2: 16-byte, 1: 8-byte, 0: 2-byte stores
 };
 
 // The low-rank term of each row (v == nullptr: none).  Row m's adapter is
@@ -103,7 +103,7 @@ struct GroupKernels {
     const void* rows_skinny[kNumSkinny][2][2][3];   // [blocks][B layout][odd rows][plain, adapters, masked]
     const void* weight_outer[3][2];                 // [masked: no, p, q][rows of whole pieces]
     const void* mask;
-    const void* shrink[2];                        // [U layout]
+    const void* shrink[2][2];                       // [U layout][rank > 32]
 };
 
 const GroupKernels& group_kernels_f16();
