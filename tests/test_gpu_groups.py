@@ -183,6 +183,46 @@ def test_grouped_kernels(shape, config, layout):
 
 
 @pytest.mark.parametrize("layout", [gr.B_KN, gr.B_NK])
+@pytest.mark.parametrize("N,K", [(1101, 2051), (1100, 2051), (1101, 2048)])
+def test_large_products_of_odd_rows(N, K, layout):
+    # Large enough that rows of an odd length are copied to whole pieces first.
+    sizes, spare, dt = [1100, 0, 900], 3, torch.bfloat16
+    M = sum(sizes) + spare
+    say(f"[odd rows] M={M} N={N} K={K} layout={layout}")
+    a, b = normal((M, K), dt, 15), weights(3, N, K, dt, layout, 16)
+    a[-1] = float("nan")                                           # a row of no group, behind the last group's
+    ends = ends_of(sizes).cuda()
+    ref, err = grouped_reference(a, b, sizes, layout, True)
+    out, whole = guarded((M, N), dt)
+    gr.gemm_relu_grouped(a.cuda(), b.cuda(), ends, out=out, b_layout=layout)
+    torch.cuda.synchronize()
+    assert whole()
+    assert_close(out, ref, err, "C")
+    for relu in (True, False):
+        dc, c = normal((M, N), dt, 17), normal((M, N), dt, 18).clamp_min(0)
+        ra, ea, rb, eb = backward_reference(dc, c, a, b, sizes, layout, relu)
+        da, whole_a = guarded((M, K), dt)
+        db, whole_b = guarded(tuple(b.shape), dt)
+        gr.gemm_relu_grouped_backward(dc.cuda(), c.cuda(), a.cuda(), b.cuda(), ends, b_layout=layout, da=da, db=db, relu=relu)
+        torch.cuda.synchronize()
+        assert whole_a() and whole_b()
+        assert_close(da, ra, ea, "dA")
+        assert_close(db, rb, eb, "dB")
+
+
+@pytest.mark.parametrize("layout", [gr.B_KN, gr.B_NK])
+def test_adapters_of_odd_rows_in_large_products(layout):
+    sizes, N, K = [900, 1, 1, 700, 398], 2051, 1901
+    x, w, u, v, scales, ends, ids = adapter_inputs(sizes, 0, N, K, 20, 3, torch.float16, layout, 66)
+    ref, err = adapter_reference(x, w, u, v, scales, sizes, ids, layout, True)
+    out, whole = guarded((x.shape[0], N), torch.float16)
+    gr.gemm_relu_adapters(*(t.cuda() for t in (x, w, u, v, scales, ends, ids)), out=out, b_layout=layout)
+    torch.cuda.synchronize()
+    assert whole()
+    assert_close(out, ref, err, "C")
+
+
+@pytest.mark.parametrize("layout", [gr.B_KN, gr.B_NK])
 @pytest.mark.parametrize("N,K", [(64, 64), (66, 70), (40, 52)])
 def test_grouped_unaligned_matrices(N, K, layout):
     sizes = [70, 0, 3, 60]

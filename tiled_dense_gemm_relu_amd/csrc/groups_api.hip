@@ -189,7 +189,7 @@ int launch_stream(RowsArgs a, AdapterArgs ad, const uint16_t* mask, int dtype, i
     SkinnyPlan plan(a.m, a.n, a.k, a.groups);
     if (plan.units > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
     if (!parts) plan.splits = 1;
-    const bool even = even_rows({{a.a, a.k}, {mask, a.k}, {a.b, b_layout == GEMM_RELU_B_NK ? a.k : a.n}});
+    const bool even = even_rows({{a.a, a.lda}, {mask, a.lda}, {a.b, a.ldb}});
     void* args[] = {&a, &ad, &parts, &counters, &mask};
     return enqueue(kernels(dtype).rows_skinny[plan.kind][b_layout][!even][ad.v ? 1 : mask ? 2 : 0],
                    dim3((unsigned)plan.units, (unsigned)plan.splits), kSkinnyThreads, args, stream);
@@ -207,16 +207,88 @@ int launch_outer(WeightArgs w, const uint16_t* mask, bool mask_q, int dtype, hip
                    stream);
 }
 
+// Rows of an odd length reach LDS only through registers, at about half the
+// pace.  Where the product is large enough, such operands are first copied to
+// rows of whole cache lines.  The estimates (us): a 128 x 128 x 64 step takes
+// 5.7e-3 of the device through registers and 2.65e-3 by DMA, or, in a chain of
+// steps on 64 x 64 tiles, 0.55 and 0.17; a copy moves 4.2 TB/s.  (1823 rows x
+// 12800 x 2125 fp16 in 3 groups: 290 us through registers, 134 with the copies.)
+int64_t pitch(int64_t row) { return round_up(row, 64); }
+struct PaddedPlan {
+    bool use = false;
+    int64_t bytes = 0;
+    // `steps`: of 128 x 128 x 64; `chain`: rounds of 64 x 64 tiles times their steps
+    void weigh(double steps, double chain, int copies)
+    {
+        const double staged = std::max(5.7e-3 * steps, 0.55 * chain), dma = std::max(2.65e-3 * steps, 0.17 * chain);
+        use = dma + 2.0 * (double)bytes / 4.2e6 + 4.0 * copies < staged;
+        if (!use) bytes = 0;
+    }
+    int64_t add(int64_t rows, int64_t row) { return bytes += row % 2 ? round_up(2 * rows * pitch(row), 256) : 0; }
+};
+struct PaddedRows : PaddedPlan {
+    PaddedRows(int64_t m, int64_t n, int64_t k, int64_t groups, int b_layout)
+    {
+        if (m == 0 || n == 0 || k == 0) return;
+        const bool nk = b_layout == GEMM_RELU_B_NK;
+        add(m, k);
+        add(groups * (nk ? n : k), nk ? k : n);
+        if (bytes == 0) return;
+        const GroupShape g(m, groups);
+        const double ks = (double)ceil_div(k, 64);
+        weigh((double)g.tiles(128, n) * ks, (double)ceil_div(g.tiles(64, n), 512) * ks, k % 2 + (nk ? k : n) % 2);
+    }
+};
+struct PaddedGrad : PaddedPlan {
+    PaddedGrad(int64_t m, int64_t n, int64_t k, int64_t groups, int b_layout)
+    {
+        if (m == 0 || n == 0 || k == 0) return;
+        const bool nk = b_layout == GEMM_RELU_B_NK;
+        add(m, n);
+        add(m, k);
+        add(groups * (nk ? n : k), nk ? k : n);
+        if (bytes == 0 || 4.0 * (double)m * (double)n * (double)k < kSmallGrad) {
+            bytes = 0;
+            return;
+        }
+        const GroupShape g(m, groups);
+        const double ns = (double)ceil_div(n, 64), ms = (double)ceil_div(g.rows, 64);
+        const auto weights = [&](int64_t t) { return (double)groups * (double)ceil_div(k, t) * (double)ceil_div(n, t) * ms; };
+        weigh((double)g.tiles(128, k) * ns + weights(128), ((double)g.tiles(64, k) * ns + weights(64)) / 512, n % 2 + k % 2 + (nk ? k : n) % 2);
+    }
+};
+
+// Copies rows of an odd length to `to`, masked if `mask` is not NULL; `p` and `row`
+// become the copy's, `to` moves past it.
+int launch_pad(const uint16_t*& p, int& row, const uint16_t* mask, int64_t rows, char*& to, int dtype, hipStream_t stream)
+{
+    PadArgs a{p, mask, reinterpret_cast<uint16_t*>(to), rows, row, (int)pitch(row)};
+    void* args[] = {&a};
+    const int rc = enqueue(kernels(dtype).pad, dim3((unsigned)std::min<int64_t>(ceil_div(rows, 4), 4096)), 256, args, stream);
+    to += round_up(2 * rows * a.pitch, 256);
+    p = a.dst;
+    row = a.pitch;
+    return rc;
+}
+
 // A product over row groups (M, N, K > 0).  `parts` (may be NULL) and `counters`:
-// space for the streaming kernel's partial sums.
+// space for the streaming kernel's partial sums, or for the copies of PaddedRows.
 int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config, int cus, float* parts, int* counters,
                 hipStream_t stream)
 {
     a.c_vec = store_width(a.c, a.n);
-    const Rows rows_a{a.a, a.k}, rows_b{a.b, b_layout == GEMM_RELU_B_NK ? a.k : a.n};
-    const DmaRows dma = std::min(dma_rows(a.a, a.k), dma_rows(a.b, rows_b.length));
+    DmaRows dma = std::min(dma_rows(a.a, a.lda), dma_rows(a.b, a.ldb));
     if (config == GEMM_RELU_GROUPS_STREAM || (config == GEMM_RELU_GROUPS_AUTO && streams(a.m, a.n, a.k, a.groups, dma != kDmaNone)))
         return launch_stream(a, ad, nullptr, dtype, b_layout, parts, counters, stream);
+    if (dma == kDmaNone && config != GEMM_RELU_GROUPS_TILED && parts && PaddedRows(a.m, a.n, a.k, a.groups, b_layout).use) {
+        char* to = reinterpret_cast<char*>(parts);
+        int rc = GEMM_RELU_OK;
+        if (a.lda % 2) rc = launch_pad(a.a, a.lda, nullptr, a.m, to, dtype, stream);
+        if (a.ldb % 2 && rc == GEMM_RELU_OK)
+            rc = launch_pad(a.b, a.ldb, nullptr, int64_t(a.groups) * (b_layout == GEMM_RELU_B_NK ? a.n : a.k), to, dtype, stream);
+        if (rc != GEMM_RELU_OK) return rc;
+        dma = std::min(dma_rows(a.a, a.lda), dma_rows(a.b, a.ldb));      // (of even rows one may be misaligned still)
+    }
     int staged = 0;
     if (dma == kDmaNone) {
         const GroupShape g(a.m, a.groups);
@@ -243,7 +315,7 @@ int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config,
     void* args[] = {&a, &ad};
     const dim3 grid((unsigned)resident(rows, tiles, cus));
     if (config == GEMM_RELU_GROUPS_TILED)
-        return enqueue(staged_kernels(dtype, {rows_a, rows_b})
+        return enqueue(staged_kernels(dtype, {{a.a, a.lda}, {a.b, a.ldb}})
                            .rows[staged][b_layout][ad.v != nullptr][a.groups > 64], grid, kStagedThreads, args, stream);
     return enqueue(kernels(dtype).rows_dma[config - 1][b_layout][dma < kDmaWhole ? 2 : a.k % 64 != 0][ad.v != nullptr], grid,
                    kGroupThreads[config - 1], args, stream);
@@ -255,7 +327,7 @@ int launch_weights(WeightArgs a, int dtype, int config, int cus, hipStream_t str
     if (config == GEMM_RELU_GROUPS_AUTO || config == GEMM_RELU_GROUPS_STREAM)
         config = dma_config(a.i, a.groups * ceil_div(a.i, 256) * ceil_div(a.j, 256),
                             a.groups * ceil_div(a.i, 128) * ceil_div(a.j, 128));
-    const bool whole = std::min(dma_rows(a.p, a.i), dma_rows(a.q, a.j)) == kDmaWhole;
+    const bool whole = std::min(dma_rows(a.p, a.ldp), dma_rows(a.q, a.ldq)) == kDmaWhole;
     if (config == GEMM_RELU_GROUPS_DMA_256 && !whole) config = GEMM_RELU_GROUPS_DMA_128;
     const int64_t tile = kGroupTile[config - 1], tiles = int64_t(a.groups) * ceil_div(a.i, tile) * ceil_div(a.j, tile);
     if (tiles > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
@@ -288,8 +360,8 @@ int launch_grad_staged(RowsArgs r, WeightArgs w, const uint16_t* mask, int dtype
     const int64_t blocks_w = std::min(tiles_w, room - blocks_r);
     int blocks_rows = (int)blocks_r;
     void* args[] = {&r, &w, &mask, &blocks_rows};
-    const Rows d{r.a, r.k}, c{mask, r.k}, b{r.c ? r.b : nullptr, b_layout == GEMM_RELU_B_NK ? r.k : r.n};
-    const Rows x{w.out ? (b_layout == GEMM_RELU_B_NK ? w.p : w.q) : nullptr, r.n};
+    const bool nk = b_layout == GEMM_RELU_B_NK;
+    const Rows d{r.a, r.lda}, c{mask, r.lda}, b{r.c ? r.b : nullptr, r.ldb}, x{w.out ? (nk ? w.p : w.q) : nullptr, nk ? w.ldp : w.ldq};
     return enqueue(staged_kernels(dtype, {d, c, b, x}).grad[staged][b_layout][mask != nullptr][r.groups > 64], dim3((unsigned)(blocks_r + blocks_w)),
                    kStagedThreads, args, stream);
 }
@@ -319,7 +391,7 @@ int launch_grad_rows(RowsArgs r, const uint16_t* c, uint16_t* masked, int dtype,
 struct AdapterSpace {
     int64_t rank_pad, tiles, splits, t, factor, row_id, part, bytes;   // part: also the streaming kernel's, afterwards
 };
-AdapterSpace adapter_space(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t segments)
+AdapterSpace adapter_space(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t segments, int b_layout)
 {
     AdapterSpace s;
     s.rank_pad = round_up(rank, 64);
@@ -330,7 +402,7 @@ AdapterSpace adapter_space(int64_t M, int64_t N, int64_t K, int64_t rank, int64_
     s.row_id = s.factor + round_up(M * 4, 256);
     s.part = s.row_id + round_up(M * 4, 256);
     s.bytes = s.part + std::max(s.splits > 1 ? s.tiles * s.splits * ceil_div(rank, kShrinkCols) * kShrinkThreads * 4 : 0,
-                                SkinnyPlan(M, N, K, 1).bytes);
+                                std::max(SkinnyPlan(M, N, K, 1).bytes, PaddedRows(M, N, K, 1, b_layout).bytes));
     return s;
 }
 static_assert(512 * 4 <= GEMM_RELU_GROUPS_COUNTER_BYTES, "a counter for each row tile of a split sum");
@@ -346,7 +418,7 @@ int64_t gemm_relu_grouped_workspace(int64_t M, int64_t N, int64_t K, int64_t gro
 {
     const int rc = check_shape(M, N, K, groups, dtype, b_layout);
     if (rc != GEMM_RELU_OK) return rc;
-    const int64_t bytes = SkinnyPlan(M, N, K, groups).bytes;
+    const int64_t bytes = std::max(SkinnyPlan(M, N, K, groups).bytes, PaddedRows(M, N, K, groups, b_layout).bytes);
     return bytes ? GEMM_RELU_GROUPS_COUNTER_BYTES + bytes : 0;
 }
 
@@ -370,7 +442,7 @@ int gemm_relu_grouped(const void* A, const void* B, const int32_t* ends, void* C
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (K == 0) return zero_fill(C, M * N, s);
     RowsArgs a{static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), static_cast<uint16_t*>(C), ends,
-               (int)M, (int)N, (int)K, (int)groups, relu, 0};
+               (int)M, (int)N, (int)K, (int)groups, relu, (int)K, (int)(b_layout == GEMM_RELU_B_NK ? K : N), 0};
     float* parts = need ? reinterpret_cast<float*>(static_cast<char*>(workspace) + GEMM_RELU_GROUPS_COUNTER_BYTES) : nullptr;
     return launch_rows(a, AdapterArgs{}, dtype, b_layout, config_id, cus, parts, static_cast<int*>(workspace), s);
 }
@@ -381,8 +453,11 @@ int64_t gemm_relu_grouped_backward_workspace(int64_t M, int64_t N, int64_t K, in
     const int rc = check_shape(M, N, K, groups, dtype, b_layout);
     if (rc != GEMM_RELU_OK) return rc;
     if (relu != 0 && relu != 1) return GEMM_RELU_ERR_INVALID_ARG;
-    // the masked gradient, and partial sums of dA's product (inner dimension N)
-    return GEMM_RELU_GROUPS_COUNTER_BYTES + (relu ? round_up(2 * M * N, 256) : 0) + SkinnyPlan(M, K, N, groups).bytes;
+    // the masked gradient and partial sums of dA's product (inner dimension N), or
+    // the copies of operands with odd rows, the masked gradient's among them
+    const int64_t masked = relu ? round_up(2 * M * N, 256) : 0, padded = PaddedGrad(M, N, K, groups, b_layout).bytes;
+    return GEMM_RELU_GROUPS_COUNTER_BYTES +
+           std::max(masked + SkinnyPlan(M, K, N, groups).bytes, padded ? padded + (N % 2 ? 0 : masked) : 0);
 }
 
 int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, const void* B, const int32_t* ends,
@@ -420,11 +495,9 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
     const int64_t masked_bytes = relu ? round_up(2 * mn, 256) : 0, parts_at = GEMM_RELU_GROUPS_COUNTER_BYTES + masked_bytes;
     uint16_t* masked = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + GEMM_RELU_GROUPS_COUNTER_BYTES);
     const int layout_a = kn ? GEMM_RELU_B_NK : GEMM_RELU_B_KN;
-    RowsArgs r{d, b, static_cast<uint16_t*>(dA), ends, (int)M, (int)K, (int)N, (int)groups, 0, 0};
+    RowsArgs r{d, b, static_cast<uint16_t*>(dA), ends, (int)M, (int)K, (int)N, (int)groups, 0, (int)N, (int)(kn ? N : K), 0};
     WeightArgs w{kn ? x : d, kn ? d : x, static_cast<uint16_t*>(dB), ends, (int)M, (int)(kn ? K : N), (int)(kn ? N : K),
-                 (int)groups, 0};
-    // LDS DMA needs rows of an even length and D itself in memory.  The register-
-    // staged kernel needs neither, and is one launch instead of two or three.
+                 (int)groups, (int)(kn ? K : N), (int)(kn ? N : K), 0};
     // Few rows a group: the weights' gradients are written, the weights read, at memory's pace.
     const GroupShape shape(M, groups);
     if (config_id == GEMM_RELU_GROUPS_STREAM || (config_id == GEMM_RELU_GROUPS_AUTO && shape.rows <= kOuterMost)) {
@@ -436,7 +509,31 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
         if (want_b && rc == GEMM_RELU_OK && gkn > 0) rc = launch_outer(w, c, kn, dtype, s);
         return rc;
     }
+    // LDS DMA needs rows of an even length and D itself in memory.  The register-
+    // staged kernel needs neither, and is one launch instead of two or three.
     const bool dma = dma_rows(d, N) && (!want_a || dma_rows(b, kn ? N : K)) && (!want_b || dma_rows(x, K));   // kDmaNone: false
+    if (!dma && config_id != GEMM_RELU_GROUPS_TILED && PaddedGrad(M, N, K, groups, b_layout).use) {
+        char* to = static_cast<char*>(workspace) + GEMM_RELU_GROUPS_COUNTER_BYTES;
+        if (N % 2)
+            rc = launch_pad(r.a, r.lda, c, M, to, dtype, s);
+        else if (relu) {
+            rc = launch_mask(d, c, masked, mn, dtype, s);
+            r.a = masked;
+            to += masked_bytes;
+        }
+        (kn ? w.q : w.p) = r.a;
+        (kn ? w.ldq : w.ldp) = r.lda;
+        if (want_b && K % 2 && rc == GEMM_RELU_OK) rc = launch_pad(kn ? w.p : w.q, kn ? w.ldp : w.ldq, nullptr, M, to, dtype, s);
+        if (want_a && r.ldb % 2 && rc == GEMM_RELU_OK) rc = launch_pad(r.b, r.ldb, nullptr, groups * (kn ? K : N), to, dtype, s);
+        const bool ready = dma_rows(r.a, r.lda) && (!want_a || dma_rows(r.b, r.ldb)) && (!want_b || (dma_rows(w.p, w.ldp) && dma_rows(w.q, w.ldq)));
+        if (rc != GEMM_RELU_OK) return rc;
+        if (!ready)                  // an even operand at an odd address
+            return launch_grad_staged(r, w, nullptr, dtype, layout_a, config_id, cus, s);
+        if (want_a) rc = launch_rows(r, AdapterArgs{}, dtype, layout_a, config_id, cus, nullptr, nullptr, s);
+        w.c_vec = store_width(w.out, w.j);
+        if (want_b && rc == GEMM_RELU_OK) rc = launch_weights(w, dtype, config_id, cus, s);
+        return rc;
+    }
     if (config_id == GEMM_RELU_GROUPS_TILED || !dma || (config_id == GEMM_RELU_GROUPS_AUTO && 4.0 * M * N * K < kSmallGrad))
         return launch_grad_staged(r, w, c, dtype, layout_a, config_id, cus, s);
     if (relu) {
@@ -457,7 +554,7 @@ int64_t gemm_relu_adapters_workspace(int64_t M, int64_t N, int64_t K, int64_t ra
     if (rc != GEMM_RELU_OK) return rc;
     if (rank < 1 || adapters < 1) return GEMM_RELU_ERR_INVALID_ARG;
     if (rank > kMaxRank || adapters > kMaxGroups) return GEMM_RELU_ERR_TOO_LARGE;
-    return adapter_space(M, N, K, rank, segments).bytes;
+    return adapter_space(M, N, K, rank, segments, b_layout).bytes;
 }
 
 int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* V, const float* scales,
@@ -481,7 +578,7 @@ int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* 
     if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (K == 0) return zero_fill(C, M * N, s);
-    const AdapterSpace space = adapter_space(M, N, K, rank, segments);
+    const AdapterSpace space = adapter_space(M, N, K, rank, segments, b_layout);
     char* const ws = static_cast<char*>(workspace);
     uint16_t* t = reinterpret_cast<uint16_t*>(ws + space.t);
     float* factor = reinterpret_cast<float*>(ws + space.factor);
@@ -493,7 +590,7 @@ int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* 
     rc = enqueue(kernels(dtype).shrink[b_layout][rank > kShrinkCols], dim3((unsigned)space.tiles, (unsigned)space.splits), kShrinkThreads, args, s);
     if (rc != GEMM_RELU_OK) return rc;
     RowsArgs a{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(W), static_cast<uint16_t*>(C), nullptr,
-               (int)M, (int)N, (int)K, 1, relu, 0};
+               (int)M, (int)N, (int)K, 1, relu, (int)K, (int)(b_layout == GEMM_RELU_B_NK ? K : N), 0};
     const bool v_fast = b_layout == GEMM_RELU_B_NK ? rank % 8 == 0 && aligned(V, 16) : N % 4 == 0 && aligned(V, 8);
     AdapterArgs ad{static_cast<const uint16_t*>(V), t, factor, row_id, ends, ids, (int)segments, (int)adapters, (int)rank,
                    (int)space.rank_pad, v_fast};

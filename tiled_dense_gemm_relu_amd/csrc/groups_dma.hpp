@@ -881,9 +881,9 @@ __global__ __launch_bounds__(Cfg::THREADS, 1) void rows_dma(RowsArgs a, AdapterA
         units.init(a, a.ends, a.groups, false, threadIdx.x & 63, blockIdx.x, gridDim.x);
         if (units.rows < a.m) zero_rows(a, units.rows, blockIdx.x, gridDim.x);
     }
-    dma_product<Cfg, DT, KTAIL, ADAPT>(units, a.a, a.b, a.c, (uint32_t)a.k, (uint32_t)(Cfg::B_KMAJOR ? a.n : a.k),
-                                       ADAPT == kAdaptFirst ? 0 : (size_t)a.k * (size_t)a.n, 0, a.n, a.relu != 0, a.c_vec,
-                                       ad, nullptr, smem);
+    dma_product<Cfg, DT, KTAIL, ADAPT>(units, a.a, a.b, a.c, (uint32_t)a.lda, (uint32_t)a.ldb,
+                                       ADAPT == kAdaptFirst ? 0 : (size_t)(Cfg::B_KMAJOR ? a.k : a.n) * (size_t)a.ldb, 0, a.n,
+                                       a.relu != 0, a.c_vec, ad, nullptr, smem);
 }
 
 template <class Cfg, int DT, int KTAIL>
@@ -892,7 +892,7 @@ __global__ __launch_bounds__(Cfg::THREADS, 1) void weight_dma(WeightArgs a)
     __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES + Cfg::STRIP_BYTES];
     WeightUnits<Cfg> units;
     units.init(a, blockIdx.x, gridDim.x);
-    dma_product<Cfg, DT, KTAIL, kAdaptNone>(units, a.p, a.q, a.out, (uint32_t)a.i, (uint32_t)a.j, 0,
+    dma_product<Cfg, DT, KTAIL, kAdaptNone>(units, a.p, a.q, a.out, (uint32_t)a.ldp, (uint32_t)a.ldq, 0,
                                        (size_t)a.i * (size_t)a.j, a.j, false, a.c_vec, AdapterArgs{}, nullptr, smem);
 }
 
@@ -911,15 +911,14 @@ __global__ __launch_bounds__(CfgR::THREADS, 1) void grad_staged(RowsArgs rows, W
         RowUnits<CfgR, MANY> units;
         units.init(rows, rows.ends, rows.groups, false, threadIdx.x & 63, block, blocks_rows);
         if (units.rows < rows.m) zero_rows(rows, units.rows, block, blocks_rows);
-        dma_product<CfgR, DT, 1, kAdaptNone>(units, rows.a, rows.b, rows.c, (uint32_t)rows.k,
-                                                (uint32_t)(CfgR::B_KMAJOR ? rows.n : rows.k),
-                                                (size_t)rows.k * (size_t)rows.n, 0, rows.n, false, rows.c_vec, AdapterArgs{},
+        dma_product<CfgR, DT, 1, kAdaptNone>(units, rows.a, rows.b, rows.c, (uint32_t)rows.lda, (uint32_t)rows.ldb,
+                                                (size_t)(CfgR::B_KMAJOR ? rows.k : rows.n) * (size_t)rows.ldb, 0, rows.n, false, rows.c_vec, AdapterArgs{},
                                                 mask, smem);
     } else {
         WeightUnits<CfgW> units;
         units.init(weights, block - blocks_rows, (int)gridDim.x - blocks_rows);
-        dma_product<CfgW, DT, 0, kAdaptNone>(units, weights.p, weights.q, weights.out, (uint32_t)weights.i,
-                                                 (uint32_t)weights.j, 0, (size_t)weights.i * (size_t)weights.j, weights.j,
+        dma_product<CfgW, DT, 0, kAdaptNone>(units, weights.p, weights.q, weights.out, (uint32_t)weights.ldp,
+                                                 (uint32_t)weights.ldq, 0, (size_t)weights.i * (size_t)weights.j, weights.j,
                                                  false, weights.c_vec, AdapterArgs{}, mask, smem);
     }
 }

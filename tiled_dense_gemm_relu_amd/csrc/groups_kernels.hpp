@@ -214,6 +214,23 @@ __global__ __launch_bounds__(256) void relu_mask(MaskArgs a)
     for (int64_t q = chunks * 8 + first; q < a.count; q += stride) a.d[q] = mask_one<DT>(a.dc[q], a.c[q]);
 }
 
+// A wave takes a row at a time, its lanes 8 elements each.
+template <int DT>
+__global__ __launch_bounds__(256) void pad_rows(PadArgs a)
+{
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int64_t row = (int64_t)blockIdx.x * 4 + wave; row < a.rows; row += (int64_t)gridDim.x * 4) {
+        const size_t at = (size_t)row * (size_t)a.cols;
+        const AnyRsrc rs = make_any_rsrc(a.src + at, (uint32_t)a.cols * 2u);
+        const AnyRsrc rm = a.mask ? make_any_rsrc(a.mask + at, (uint32_t)a.cols * 2u) : rs;
+        for (int e = 8 * lane; e < a.pitch; e += 512) {
+            u32x4 v = chunk_value(load_any(rs, (uint32_t)e * 2u, true));
+            if (a.mask) v = mask_chunk<DT>(v, chunk_value(load_any(rm, (uint32_t)e * 2u, true)));
+            *reinterpret_cast<u32x4*>(a.dst + (size_t)row * (size_t)a.pitch + e) = keep_first(v, a.cols - e);
+        }
+    }
+}
+
 // ---------------------------------------------------------------- adapters
 
 // Bytes of LDS that add_adapters stages V in, per wave: 32 k of its columns.

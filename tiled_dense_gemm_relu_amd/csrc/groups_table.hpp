@@ -15,6 +15,7 @@ struct RowsArgs {
     const int* ends;
     int m, n, k, groups;
     int relu;
+    int lda, ldb;          // row lengths of a and b
     int c_vec;             // rows of C allow 2: 16-byte, 1: 8-byte, 0: 2-byte stores
 };
 
@@ -53,7 +54,18 @@ struct WeightArgs {
     uint16_t* out;
     const int* ends;
     int m, i, j, groups;
+    int ldp, ldq;          // row lengths of p and q
     int c_vec;
+};
+
+// Rows of `cols` elements copied to rows of `pitch` (whole 16-byte pieces), zeros
+// after them; mask != nullptr: zero where that is not above zero.
+struct PadArgs {
+    const uint16_t* src;
+    const uint16_t* mask;
+    uint16_t* dst;
+    int64_t rows;
+    int cols, pitch;
 };
 
 struct MaskArgs {
@@ -103,6 +115,7 @@ struct GroupKernels {
     const void* rows_skinny[kNumSkinny][2][2][3];   // [blocks][B layout][odd rows][plain, adapters, masked]
     const void* weight_outer[3][2];                 // [masked: no, p, q][rows of whole pieces]
     const void* mask;
+    const void* pad;
     const void* shrink[2][2];                       // [U layout][rank > 32]
 };
 
