@@ -19,7 +19,7 @@ constexpr int64_t kMaxGroups = 65535;
 // Gradients of fewer operations than this take one register-staged launch.
 constexpr double kSmallGrad = 4e9;
 // Rows a group, on average, up to which the weights' gradients are written row by row.
-constexpr int64_t kOuterMost = 8;
+constexpr int64_t kOuterMost = 16;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
@@ -200,8 +200,8 @@ int launch_stream(RowsArgs a, AdapterArgs ad, const uint16_t* mask, int dtype, i
 int launch_outer(WeightArgs w, const uint16_t* mask, bool mask_q, int dtype, hipStream_t stream)
 {
     const bool whole = w.j % 8 == 0 && aligned(w.q, 16) && aligned(w.out, 16) && (!mask || aligned(mask, 16));
-    const int64_t tiles = int64_t(w.groups) * ceil_div(w.i, kOuterRows) * (whole ? ceil_div(w.j, kOuterCols) : w.j / kOuterCols + 1);
-    if (tiles > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
+    const int64_t one = outer_tiles(w.i, w.j, whole), tiles = one * w.groups;
+    if (tiles > INT32_MAX || one * kOuterThreads > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
     void* args[] = {&w, &mask};
     return enqueue(kernels(dtype).weight_outer[!mask ? 0 : mask_q ? 2 : 1][whole], dim3((unsigned)tiles), kOuterThreads, args,
                    stream);
@@ -334,6 +334,16 @@ int launch_weights(WeightArgs a, int dtype, int config, int cus, hipStream_t str
     void* args[] = {&a};
     return enqueue(kernels(dtype).weight_dma[config - 1][!whole], dim3((unsigned)resident(tile, tiles, cus)), kGroupThreads[config - 1],
                    args, stream);
+}
+
+// Whether both gradients are better computed in one register-staged launch than by
+// a mask and two DMA launches: few operations (the launches cost about 8 us more),
+// unless their chains of K-steps are long (0.4 us a step against 0.17).
+bool small_grad(int64_t m, int64_t n, int64_t k, int64_t groups)
+{
+    const GroupShape g(m, groups);
+    const double chain = (double)ceil_div(g.tiles(64, k), 512) * (double)ceil_div(n, 64);
+    return 4.0 * (double)m * (double)n * (double)k < kSmallGrad && 0.23 * chain < 8.0;
 }
 
 // Both gradients (or one: the other's output is NULL) in one register-staged
@@ -534,7 +544,7 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
         if (want_b && rc == GEMM_RELU_OK) rc = launch_weights(w, dtype, config_id, cus, s);
         return rc;
     }
-    if (config_id == GEMM_RELU_GROUPS_TILED || !dma || (config_id == GEMM_RELU_GROUPS_AUTO && 4.0 * M * N * K < kSmallGrad))
+    if (config_id == GEMM_RELU_GROUPS_TILED || !dma || (config_id == GEMM_RELU_GROUPS_AUTO && small_grad(M, N, K, groups)))
         return launch_grad_staged(r, w, c, dtype, layout_a, config_id, cus, s);
     if (relu) {
         rc = launch_mask(d, c, masked, mn, dtype, s);

@@ -41,36 +41,52 @@ __device__ __forceinline__ u32x4 skinny_value(const SkinnyChunk<ODD>& c, const A
     else return chunk_value(AnyChunk{c.v, c.next, ((off + r.shift) & 2u) * 8u});
 }
 
-// One output's low-rank term: z . V_i[:, n], z = f (hi + lo) from `t`.
-template <int DT, bool B_NK>
-__device__ __forceinline__ float low_rank_term(const AdapterArgs& ad, int m, int n, int N)
+// Add the low-rank terms of rows m, m + 16, ... (below m_end) at column n to z:
+// (hi + lo) . V_i[:, n] times the row's factor, the rows' loads in flight together.
+template <int DT, bool B_NK, int MB>
+__device__ __forceinline__ void add_low_rank(float (&z)[MB], const AdapterArgs& ad, int m, int m_end, int n, int N)
 {
-    const int id = ad.row_id[m];
-    if (id < 0) return 0.0f;
-    const uint16_t* t = ad.t + (size_t)m * (size_t)(2 * ad.rank_pad);
-    const uint16_t* v = ad.v + (size_t)id * (size_t)ad.rank * (size_t)N + (B_NK ? (size_t)n * (size_t)ad.rank : (size_t)n);
     const size_t step = B_NK ? 1 : (size_t)N;
-    float sum = 0.0f;
-#pragma unroll 4
-    for (int r0 = 0; r0 < ad.rank; r0 += 8) {
-        const u32x4 hi = *reinterpret_cast<const u32x4*>(t + r0), lo = *reinterpret_cast<const u32x4*>(t + ad.rank_pad + r0);
-        uint16_t w[8];
-        if (B_NK && ad.v_fast) {
-            const u32x4 q = *reinterpret_cast<const u32x4*>(v + r0);
+    const uint16_t *t[MB], *v[MB];
+    float factor[MB], sum[MB];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = (uint16_t)(q[e / 2] >> (16 * (e & 1)));
-        } else {
-            // entries past the rank repeat the last one
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = v[(size_t)min(r0 + e, ad.rank - 1) * step];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float z = to_float<DT>((uint16_t)(hi[e / 2] >> (16 * (e & 1)))) + to_float<DT>((uint16_t)(lo[e / 2] >> (16 * (e & 1))));
-            if (r0 + e < ad.rank) sum += z * to_float<DT>(w[e]);
-        }
+    for (int j = 0; j < MB; ++j) {
+        const int row = min(m + 16 * j, m_end - 1), id = ad.row_id[row];
+        // without an adapter: V_0, and a factor that drops it
+        factor[j] = id >= 0 && m + 16 * j < m_end ? ad.factor[row] : 0.0f;
+        t[j] = ad.t + (size_t)row * (size_t)(2 * ad.rank_pad);
+        v[j] = ad.v + (size_t)max(id, 0) * (size_t)ad.rank * (size_t)N + (B_NK ? (size_t)n * (size_t)ad.rank : (size_t)n);
+        sum[j] = 0.0f;
     }
-    return ad.factor[m] * sum;
+#pragma unroll MB == 1 ? 4 : MB == 2 ? 2 : 1
+    for (int r0 = 0; r0 < ad.rank; r0 += 8) {
+        u32x4 hi[MB], lo[MB];
+        uint16_t w[MB][8];
+#pragma unroll
+        for (int j = 0; j < MB; ++j) {
+            hi[j] = *reinterpret_cast<const u32x4*>(t[j] + r0);
+            lo[j] = *reinterpret_cast<const u32x4*>(t[j] + ad.rank_pad + r0);
+            if (B_NK && ad.v_fast) {
+                const u32x4 q = *reinterpret_cast<const u32x4*>(v[j] + r0);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[j][e] = (uint16_t)(q[e / 2] >> (16 * (e & 1)));
+            } else {
+                // entries past the rank repeat the last one
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[j][e] = v[j][(size_t)min(r0 + e, ad.rank - 1) * step];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < MB; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = to_float<DT>((uint16_t)(hi[j][e / 2] >> (16 * (e & 1)))) +
+                                to_float<DT>((uint16_t)(lo[j][e / 2] >> (16 * (e & 1))));
+                sum[j] += r0 + e < ad.rank ? x * to_float<DT>(w[j][e]) : 0.0f;
+            }
+    }
+#pragma unroll
+    for (int j = 0; j < MB; ++j) z[j] = factor[j] != 0.0f ? z[j] + factor[j] * sum[j] : z[j];
 }
 
 // C = act(rows of A @ their group's B [+ their adapters' terms]).  Workgroup b of
@@ -240,12 +256,12 @@ __global__ __launch_bounds__(kSkinnyThreads) void rows_skinny(RowsArgs a, Adapte
         }
         if (threadIdx.x == 0) __hip_atomic_store(counters + u, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    if (n0 + col >= a.n) return;
+    if (n0 + col >= a.n || row >= rows) return;
+    if constexpr (ADAPT) add_low_rank<DT, B_NK, MB>(z, ad, tile.begin + row, tile.end, n0 + col, a.n);
 #pragma unroll
     for (int j = 0; j < MB; ++j) {
         if (16 * j + row >= rows) continue;
         const int m = tile.begin + 16 * j + row;
-        if constexpr (ADAPT) z[j] += low_rank_term<DT, B_NK>(ad, m, n0 + col, a.n);
         a.c[(size_t)m * n_len + (size_t)(n0 + col)] = act_cast<DT>(z[j], a.relu != 0);
     }
 }

@@ -103,7 +103,12 @@ struct StagedKernels {
 constexpr int kNumSkinny = 3;
 constexpr int kSkinnyBlocks[kNumSkinny] = {1, 2, 4};
 // Weights' gradients with few rows a group.
-constexpr int kOuterRows = 32, kOuterCols = 512, kOuterThreads = 256;
+constexpr int kOuterThreads = 256;
+// Workgroups of an (i, j) output, 8 x 8 elements to a lane; rows that start inside a dword end one element early.
+constexpr int64_t outer_tiles(int64_t i, int64_t j, bool aligned)
+{
+    return ((i + 7) / 8 * (j / 8 + (aligned ? 0 : 1)) + kOuterThreads - 1) / kOuterThreads;
+}
 constexpr int kSkinnyCols = 32, kSkinnyK = 128, kSkinnyThreads = 512;
 
 struct GroupKernels {
