@@ -103,9 +103,9 @@ const StagedKernels& staged_kernels(int dtype, std::initializer_list<Rows> opera
     return even ? staged_kernels_bf16_even() : staged_kernels_bf16_odd();
 }
 
-int enqueue(const void* fn, dim3 grid, int threads, void** args, hipStream_t stream)
+int enqueue(const void* fn, dim3 grid, int threads, void** args, hipStream_t stream, size_t lds = 0)
 {
-    const hipError_t err = hipLaunchKernel(fn, grid, dim3((unsigned)threads), args, 0, stream);
+    const hipError_t err = hipLaunchKernel(fn, grid, dim3((unsigned)threads), args, lds, stream);
     return err == hipSuccess ? GEMM_RELU_OK : GEMM_RELU_ERR_LAUNCH;
 }
 
@@ -399,19 +399,21 @@ int launch_grad_rows(RowsArgs r, const uint16_t* c, uint16_t* masked, int dtype,
 // adapter, and the partial sums of a K that is cut into `splits` parts: as many
 // as make 512 workgroups, while each of their 8 waves has a piece of K.
 struct AdapterSpace {
-    int64_t rank_pad, tiles, splits, t, factor, row_id, part, bytes;   // part: also the streaming kernel's, afterwards
+    int64_t rank_pad, blocks, tiles, splits, t, factor, row_id, part, bytes;   // part: also the streaming kernel's, afterwards
 };
 AdapterSpace adapter_space(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t segments, int b_layout)
 {
     AdapterSpace s;
     s.rank_pad = round_up(rank, 64);
-    s.tiles = most_row_tiles(M, segments, kShrinkRows);
+    // two blocks of rows a workgroup, which read U once, where segments fill them
+    s.blocks = M > 0 && GroupShape(M, segments).rows >= 48 && M >= 1024 ? 2 : 1;
+    s.tiles = most_row_tiles(M, segments, s.blocks * kShrinkRows);
     s.splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(K, 8 * kShrinkK), s.tiles ? 512 / s.tiles : 1));
     s.t = GEMM_RELU_GROUPS_COUNTER_BYTES;
     s.factor = s.t + round_up(M * 2 * s.rank_pad * 2, 256);
     s.row_id = s.factor + round_up(M * 4, 256);
     s.part = s.row_id + round_up(M * 4, 256);
-    s.bytes = s.part + std::max(s.splits > 1 ? s.tiles * s.splits * ceil_div(rank, kShrinkCols) * kShrinkThreads * 4 : 0,
+    s.bytes = s.part + std::max(s.splits > 1 ? s.tiles * s.splits * ceil_div(rank, kShrinkCols) * s.blocks * kShrinkThreads * 4 : 0,
                                 std::max(SkinnyPlan(M, N, K, 1).bytes, PaddedRows(M, N, K, 1, b_layout).bytes));
     return s;
 }
@@ -597,7 +599,8 @@ int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* 
                   reinterpret_cast<float*>(ws + space.part), reinterpret_cast<int*>(ws), (int)M, (int)K, (int)segments,
                   (int)adapters, (int)rank, (int)space.rank_pad};
     void* args[] = {&sh};
-    rc = enqueue(kernels(dtype).shrink[b_layout][rank > kShrinkCols], dim3((unsigned)space.tiles, (unsigned)space.splits), kShrinkThreads, args, s);
+    rc = enqueue(kernels(dtype).shrink[b_layout][rank > kShrinkCols][space.blocks - 1], dim3((unsigned)space.tiles, (unsigned)space.splits),
+                 kShrinkThreads, args, s, (size_t)(ceil_div(rank, kShrinkCols) * space.blocks * kShrinkThreads * 4));
     if (rc != GEMM_RELU_OK) return rc;
     RowsArgs a{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(W), static_cast<uint16_t*>(C), nullptr,
                (int)M, (int)N, (int)K, 1, relu, (int)K, (int)(b_layout == GEMM_RELU_B_NK ? K : N), 0};

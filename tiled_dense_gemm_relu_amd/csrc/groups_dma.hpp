@@ -89,7 +89,10 @@ struct UnitOrder {
 // each other in its list: they share the group's weights in its L2.  (Whole
 // tiles first and partial ones after them would balance a round better, but the
 // partial ones then read their weights again, each its own: 1087 against 1003 us
-// for 16384 rows in 16 groups, 4096 x 8192 fp16.)  Lane l keeps what belongs to
+// for 16384 rows in 16 groups, 4096 x 8192 fp16.)  With more rows than all
+// groups' columns (tall outputs of few groups), it is the rows of A that are worth
+// sharing: then the XCDs get consecutive units of GROUP_M rows of tiles, column by
+// column.  Lane l keeps what belongs to
 // group l; with more than 64 groups (MANY) a lookup scans `ends` again.
 template <class Cfg, bool MANY>
 struct RowUnits {
@@ -99,13 +102,14 @@ struct RowUnits {
     int listed;              // groups with tiles: all, and with `rest` the rows of none as one more
     int rows;                // rows in groups
     int units;               // this XCD's
-    int64_t first, last;     // its part of the work
+    int64_t first, last;     // its part of the work, or of the units
+    bool by_rows;
     const int* ids;          // the groups' adapters, or nullptr
     int adapters;
     UnitOrder order;
     struct Lane {
         int begin, end;      // the group's rows
-        int col, cols;       // its columns of tiles on this XCD
+        int from, count;     // this XCD's columns of its tiles, or units (by_rows)
         int incl;            // units up to this group
     } kept;                  // at most 64 groups
 
@@ -124,13 +128,19 @@ struct RowUnits {
             if (past <= 0 || c == 0) return 0;
             return past >= (int64_t)c * tiles_n ? tiles_n : (int)(((uint32_t)past + c - 1u) / (uint32_t)c);   // c tiles_n <= 2^31
         };
+        const int tiles = (n + Cfg::BM - 1) / Cfg::BM;
+        // the group's units before unit w of all
+        const int units_before_group = wave_scan_sum(tiles) - tiles;
+        auto unit_at = [&](int64_t w) {
+            return (int)min(max(w - (work + (int64_t)units_before_group * tiles_n), (int64_t)0), (int64_t)tiles * tiles_n);
+        };
         Lane k;
         k.begin = r.begin;
         k.end = r.end;
-        k.col = column(first);
-        k.cols = max(0, column(last) - k.col);
-        k.incl = units_before + wave_scan_sum((n + Cfg::BM - 1) / Cfg::BM * k.cols);
-        work += (int64_t)__builtin_amdgcn_readlane(before + c, 63) * tiles_n;
+        k.from = by_rows ? unit_at(first) : column(first);
+        k.count = max(0, (by_rows ? unit_at(last) : column(last)) - k.from);
+        k.incl = units_before + wave_scan_sum(by_rows ? k.count : tiles * k.count);
+        work += (int64_t)__builtin_amdgcn_readlane(by_rows ? units_before_group + tiles : before + c, 63) * tiles_n;
         units_before = __builtin_amdgcn_readlane(k.incl, 63);
         start = __builtin_amdgcn_readlane(r.end, 63);
         return k;
@@ -148,11 +158,13 @@ struct RowUnits {
         tiles_n = (a.n + Cfg::BN - 1) / Cfg::BN;
         lane = lane_;
         order.init(block, blocks);
+        by_rows = M > (int64_t)groups * a.n;
         int64_t total = 0;
         rows = 0;
         for (int g0 = 0; g0 < listed; g0 += 64) {
             const GroupRows r = load_group_rows(ends, groups, M, g0, rows, lane);
-            total += __builtin_amdgcn_readlane(wave_scan_sum(g0 + lane < listed ? cost(r.end - r.begin) : 0), 63);
+            const int n = g0 + lane < listed ? r.end - r.begin : 0;
+            total += __builtin_amdgcn_readlane(wave_scan_sum(by_rows ? (n + Cfg::BM - 1) / Cfg::BM : cost(n)), 63);
             rows = __builtin_amdgcn_readlane(r.end, min(listed - 1 - g0, 63));
         }
         total *= tiles_n;
@@ -179,12 +191,12 @@ struct RowUnits {
         }
         const int l = __builtin_ctzll(__ballot(at < k.incl));
         const int b = __builtin_amdgcn_readlane(k.begin, l), e = __builtin_amdgcn_readlane(k.end, l);
-        const int col = __builtin_amdgcn_readlane(k.col, l), cols = __builtin_amdgcn_readlane(k.cols, l);
-        const int tiles = (e - b + Cfg::BM - 1) / Cfg::BM;
+        const int from = __builtin_amdgcn_readlane(k.from, l), count = __builtin_amdgcn_readlane(k.count, l);
+        const int tiles = (e - b + Cfg::BM - 1) / Cfg::BM, past = __builtin_amdgcn_readlane(k.incl, l) - at;
         int tm, tn;
-        tile_coords(at - (__builtin_amdgcn_readlane(k.incl, l) - tiles * cols), tiles, cols, Cfg::GROUP_M, tm, tn, false);
+        tile_coords(by_rows ? from + count - past : tiles * count - past, tiles, by_rows ? tiles_n : count, Cfg::GROUP_M, tm, tn, false);
         const int m0 = b + tm * Cfg::BM, id = ids && g0 + l < groups ? ids[g0 + l] : -1;
-        return DmaUnit{m0, min(m0 + Cfg::BM, e), (col + tn) * Cfg::BN, g0 + l, 0, K, id < adapters ? id : -1};
+        return DmaUnit{m0, min(m0 + Cfg::BM, e), (by_rows ? tn : from + tn) * Cfg::BN, g0 + l, 0, K, id < adapters ? id : -1};
     }
 };
 

@@ -118,10 +118,14 @@ GroupKernels make_group_table()
     t.weight_outer[2][1] = (const void*)&weight_outer<DT, 2, true>;
     t.mask = (const void*)&relu_mask<DT>;
     t.pad = (const void*)&pad_rows<DT>;
-    t.shrink[0][0] = (const void*)&adapter_shrink<DT, false, 1>;
-    t.shrink[0][1] = (const void*)&adapter_shrink<DT, false, 2>;
-    t.shrink[1][0] = (const void*)&adapter_shrink<DT, true, 1>;
-    t.shrink[1][1] = (const void*)&adapter_shrink<DT, true, 2>;
+    t.shrink[0][0][0] = (const void*)&adapter_shrink<DT, false, 1, 1>;
+    t.shrink[0][0][1] = (const void*)&adapter_shrink<DT, false, 1, 2>;
+    t.shrink[0][1][0] = (const void*)&adapter_shrink<DT, false, 2, 1>;
+    t.shrink[0][1][1] = (const void*)&adapter_shrink<DT, false, 2, 2>;
+    t.shrink[1][0][0] = (const void*)&adapter_shrink<DT, true, 1, 1>;
+    t.shrink[1][0][1] = (const void*)&adapter_shrink<DT, true, 1, 2>;
+    t.shrink[1][1][0] = (const void*)&adapter_shrink<DT, true, 2, 1>;
+    t.shrink[1][1][1] = (const void*)&adapter_shrink<DT, true, 2, 2>;
     return t;
 }
 

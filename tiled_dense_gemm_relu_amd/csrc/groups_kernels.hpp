@@ -392,24 +392,25 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
 // factor a power of two of the row's largest |z|, hi the nearest 16-bit value
 // to z / factor (at most 1 in size) and lo that to what is left.  row_id[m] is
 // the row's adapter, -1 for none.
-//  One workgroup per 16 rows of a segment and part of K, CHUNKS times 32 columns
-// of rank at a time: its 8 waves take pieces of 128 k in turn, each with all its loads in
+//  One workgroup per 16 MB rows of a segment and part of K, CHUNKS times 32
+// columns of rank at a time: its 8 waves take pieces of 128 k in turn, each with all its loads in
 // flight at once, and their sums are added in wave order in LDS.  With few rows
 // K is cut into `splits` parts, whose sums go through device memory
 // (device-scope accesses: the parts run on different XCDs); the part that
 // counts itself last adds them in part order and finishes.  Nothing waits for
 // another workgroup.
-template <int DT, bool U_NK, int CHUNKS>
+template <int DT, bool U_NK, int CHUNKS, int MB>
 __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs a)
 {
     constexpr int WAVES = kShrinkThreads / 64, STEPS = kShrinkK / 32, ROW = kShrinkCols * 2;
     constexpr int kDeviceScope = 16;   // cache policy sc1
-    __shared__ float part[CHUNKS][WAVES][kShrinkCols][kShrinkRows + 1];
-    __shared__ float sums[kMaxRank / kShrinkCols][kShrinkThreads];
+    constexpr int ROWS = MB * kShrinkRows, SUMS = MB * kShrinkThreads;
+    __shared__ float part[WAVES][kShrinkCols][ROWS + 1];
+    extern __shared__ float sums[];    // [32 columns][SUMS]: each thread's own
     __shared__ __attribute__((aligned(16))) uint8_t strips[U_NK ? 16 : WAVES * 32 * ROW];
     __shared__ int before;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const RowTile tile = find_row_tile(a.ends, a.segments, a.m, kShrinkRows, blockIdx.x, lane);
+    const RowTile tile = find_row_tile(a.ends, a.segments, a.m, ROWS, blockIdx.x, lane);
     if (tile.group < 0) return;
     const int rows = tile.end - tile.begin;
     int id = tile.group < a.segments ? a.ids[tile.group] : -1;
@@ -419,8 +420,9 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs a)
     const int r16 = lane & 15, kb = kgroup16(lane >> 4);
     const size_t k_len = (size_t)a.k, rank = (size_t)a.rank;
     const int chunks = (a.rank + kShrinkCols - 1) / kShrinkCols;
-    // 512 threads: 16 rows x 32 columns; a row's 32 columns are one half of a wave
+    // 512 threads: 16 rows x 32 columns of each block of rows; a row's 32 columns are one half of a wave
     const int row = threadIdx.x >> 5, col = threadIdx.x & 31;
+    auto sum_at = [&](int c, int j) { return c * SUMS + j * kShrinkThreads + (int)threadIdx.x; };
 
     const AnyRsrc rx = make_any_rsrc(a.x + (size_t)tile.begin * k_len, (uint32_t)rows * (uint32_t)a.k * 2u);
     uint8_t* strip = strips + (U_NK ? 0 : wave * 32 * ROW);
@@ -432,16 +434,20 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs a)
         // U stored (rank, K): rows r_base .. of U^T
         const AnyRsrc ru = make_any_rsrc(a.u + (size_t)id * k_len * rank + (U_NK ? (size_t)r_base * k_len : 0),
                                          (uint32_t)(U_NK ? min(CHUNKS * kShrinkCols, a.rank - r_base) : a.rank) * (uint32_t)a.k * 2u);
-        floatx4 acc[CHUNKS][2];
+        floatx4 acc[CHUNKS][2][MB];
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) acc[c][0] = acc[c][1] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+            for (int j = 0; j < MB; ++j) acc[c][0][j] = acc[c][1][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
         for (int p = p_begin; p < p_end; p += WAVES) {
             const int k0 = p * kShrinkK;
-            AnyChunk x[STEPS], u[STEPS][CHUNKS][2];
+            AnyChunk x[STEPS][MB], u[STEPS][CHUNKS][2];
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int k = k0 + 32 * s + 8 * kb;
-                x[s] = load_any(rx, ((uint32_t)r16 * (uint32_t)a.k + (uint32_t)k) * 2u, k < a.k);
+#pragma unroll
+                for (int j = 0; j < MB; ++j)
+                    x[s][j] = load_any(rx, ((uint32_t)(16 * j + r16) * (uint32_t)a.k + (uint32_t)k) * 2u, k < a.k);
 #pragma unroll
                 for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
@@ -458,7 +464,9 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs a)
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int valid = a.k - (k0 + 32 * s + 8 * kb);
-                const u32x4 xv = keep_first(chunk_value(x[s]), valid);
+                u32x4 xv[MB];
+#pragma unroll
+                for (int j = 0; j < MB; ++j) xv[j] = keep_first(chunk_value(x[s][j]), valid);
 #pragma unroll
                 for (int c = 0; c < CHUNKS; ++c) {
                     u32x4 uv[2];
@@ -481,35 +489,42 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs a)
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) acc[c][i] = mfma_16x16x32<DT>(uv[i], xv, acc[c][i]);
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < MB; ++j) acc[c][i][j] = mfma_16x16x32<DT>(uv[i], xv[j], acc[c][i][j]);
                 }
             }
         }
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c)
+        for (int c = 0; c < CHUNKS; ++c) {
+            if (c0 + c >= chunks) break;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) part[c][wave][16 * i + 4 * (lane >> 4) + e][r16] = acc[c][i][e];
-        __syncthreads();
+                for (int j = 0; j < MB; ++j)
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) {
-            float z = 0.0f;
+                    for (int e = 0; e < 4; ++e) part[wave][16 * i + 4 * (lane >> 4) + e][16 * j + r16] = acc[c][i][j][e];
+            __syncthreads();
 #pragma unroll
-            for (int w = 0; w < WAVES; ++w) z += part[c][w][col][row];
-            if (c0 + c < chunks) sums[c0 + c][threadIdx.x] = z;
+            for (int j = 0; j < MB; ++j) {
+                float z = 0.0f;
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) z += part[w][col][16 * j + row];
+                sums[sum_at(c0 + c, j)] = z;
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
     if (splits > 1) {
-        // part s of this row tile, 32 columns c: kShrinkThreads floats at (s * chunks + c) * kShrinkThreads
-        const uint32_t bytes = (uint32_t)chunks * kShrinkThreads * 4u;
+        // part s of this row tile, 32 columns c: SUMS floats at (s * chunks + c) * SUMS
+        const uint32_t bytes = (uint32_t)chunks * SUMS * 4u;
         const __amdgpu_buffer_rsrc_t rs =
             make_rsrc(a.part + (size_t)blockIdx.x * (size_t)splits * (bytes / 4), (uint32_t)splits * bytes);
         for (int c = 0; c < chunks; ++c)
-            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, sums[c][threadIdx.x]), rs,
-                                                  blockIdx.y * bytes + (uint32_t)(c * kShrinkThreads + threadIdx.x) * 4u, 0,
-                                                  kDeviceScope);
+#pragma unroll
+            for (int j = 0; j < MB; ++j)
+                __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, sums[sum_at(c, j)]), rs,
+                                                      blockIdx.y * bytes + (uint32_t)sum_at(c, j) * 4u, 0, kDeviceScope);
         wait_vmcnt<0>();               // this wave's sums have reached device scope
         __syncthreads();
         if (threadIdx.x == 0)
@@ -517,51 +532,55 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs a)
         __syncthreads();
         if (before != splits - 1) return;
         asm volatile("" ::: "memory");   // the loads below stay after the count that allowed them
-        for (int c = 0; c < chunks; ++c) {
-            float z = 0.0f;
-            for (int s0 = 0; s0 < splits; s0 += 4) {
-                float o[4];
+        for (int c = 0; c < chunks; ++c)
 #pragma unroll
-                for (int s = 0; s < 4; ++s)   // parts past the last are out of range: zero
-                    o[s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                                         rs, (uint32_t)(s0 + s) * bytes + (uint32_t)(c * kShrinkThreads + threadIdx.x) * 4u,
-                                                         0, kDeviceScope));
+            for (int j = 0; j < MB; ++j) {
+                float z = 0.0f;
+                for (int s0 = 0; s0 < splits; s0 += 4) {
+                    float o[4];
 #pragma unroll
-                for (int s = 0; s < 4; ++s) z += o[s];
+                    for (int s = 0; s < 4; ++s)   // parts past the last are out of range: zero
+                        o[s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                             rs, (uint32_t)(s0 + s) * bytes + (uint32_t)sum_at(c, j) * 4u, 0, kDeviceScope));
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) z += o[s];
+                }
+                sums[sum_at(c, j)] = z;
             }
-            sums[c][threadIdx.x] = z;
-        }
         if (threadIdx.x == 0) __hip_atomic_store(a.counters + blockIdx.x, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     const float scale = a.scales[id];
-    float top = 0.0f;
-    for (int c = 0; c < chunks; ++c) {
-        // columns past rank are zero, whatever X holds (0 * infinity is not)
-        const float z = c * kShrinkCols + col < a.rank ? sums[c][threadIdx.x] * scale : 0.0f;
-        sums[c][threadIdx.x] = z;
-        top = fmaxf(top, fabsf(z) < __builtin_inff() ? fabsf(z) : 0.0f);
-    }
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-    // 2^e > top, the largest finite entry: the scaled values are below 1.  Zeros
-    // keep factor 1; e stays where 2^-e is a normal number.
-    int e = 0;
-    if (top > 0.0f) {
-        (void)frexpf(top, &e);
-        e = min(max(e, -125), 125);
+    for (int j = 0; j < MB; ++j) {
+        float top = 0.0f;
+        for (int c = 0; c < chunks; ++c) {
+            // columns past rank are zero, whatever X holds (0 * infinity is not)
+            const float z = c * kShrinkCols + col < a.rank ? sums[sum_at(c, j)] * scale : 0.0f;
+            sums[sum_at(c, j)] = z;
+            top = fmaxf(top, fabsf(z) < __builtin_inff() ? fabsf(z) : 0.0f);
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+        // 2^e > top, the largest finite entry: the scaled values are below 1.  Zeros
+        // keep factor 1; e stays where 2^-e is a normal number.
+        int e = 0;
+        if (top > 0.0f) {
+            (void)frexpf(top, &e);
+            e = min(max(e, -125), 125);
+        }
+        if (16 * j + row >= rows) continue;
+        const size_t m = (size_t)(tile.begin + 16 * j + row);
+        uint16_t* t = a.t + m * (size_t)(2 * a.rank_pad) + col;
+        for (int c = 0; c < a.rank_pad / kShrinkCols; ++c, t += kShrinkCols) {
+            const float scaled = c < chunks ? ldexpf(sums[sum_at(c, j)], -e) : 0.0f;
+            const uint16_t hi = act_cast<DT>(scaled, false);
+            const float rest = scaled - to_float<DT>(hi);
+            t[0] = hi;
+            // an infinite hi leaves inf - inf: such an entry has no second part
+            t[a.rank_pad] = fabsf(scaled) < __builtin_inff() ? act_cast<DT>(rest, false) : (uint16_t)0;
+        }
+        if (col == 0) a.factor[m] = ldexpf(1.0f, e);
     }
-    if (row >= rows) return;
-    const size_t m = (size_t)(tile.begin + row);
-    uint16_t* t = a.t + m * (size_t)(2 * a.rank_pad) + col;
-    for (int c = 0; c < a.rank_pad / kShrinkCols; ++c, t += kShrinkCols) {
-        const float scaled = c < chunks ? ldexpf(sums[c][threadIdx.x], -e) : 0.0f;
-        const uint16_t hi = act_cast<DT>(scaled, false);
-        const float rest = scaled - to_float<DT>(hi);
-        t[0] = hi;
-        // an infinite hi leaves inf - inf: such an entry has no second part
-        t[a.rank_pad] = fabsf(scaled) < __builtin_inff() ? act_cast<DT>(rest, false) : (uint16_t)0;
-    }
-    if (col == 0) a.factor[m] = ldexpf(1.0f, e);
 }
 
 }  // namespace gemm_relu_hip

@@ -82,7 +82,10 @@ __global__ __launch_bounds__(kOuterThreads) void weight_outer(WeightArgs a, cons
             for (int i = 0; i < 8; ++i) {
                 const bool odd = ((odd0 ^ ((uint32_t)i & (uint32_t)a.j)) & 1u) != 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[i][e] += p[i] * (odd ? q[e] : q[e + 1]);
+                for (int e = 0; e < 8; ++e) {
+                    const float before = q[e], here = q[e + 1];    // (values: a choice of places would put q in memory)
+                    acc[i][e] += p[i] * (odd ? before : here);
+                }
             }
         }
 #pragma unroll

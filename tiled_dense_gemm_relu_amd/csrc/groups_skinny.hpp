@@ -58,7 +58,7 @@ __device__ __forceinline__ void add_low_rank(float (&z)[MB], const AdapterArgs& 
         v[j] = ad.v + (size_t)max(id, 0) * (size_t)ad.rank * (size_t)N + (B_NK ? (size_t)n * (size_t)ad.rank : (size_t)n);
         sum[j] = 0.0f;
     }
-#pragma unroll MB == 1 ? 4 : MB == 2 ? 2 : 1
+#pragma unroll MB == 1 ? 4 : 2
     for (int r0 = 0; r0 < ad.rank; r0 += 8) {
         u32x4 hi[MB], lo[MB];
         uint16_t w[MB][8];

@@ -42,7 +42,7 @@ struct ShrinkArgs {
     uint16_t* t;
     float* factor;
     int* row_id;
-    float* part;           // [row tile][split][32 columns][16 x 32] sums
+    float* part;           // [row tile][split][32 columns][rows x 32] sums
     int* counters;         // one for each row tile
     int m, k, segments, adapters, rank, rank_pad;
 };
@@ -121,7 +121,7 @@ struct GroupKernels {
     const void* weight_outer[3][2];                 // [masked: no, p, q][rows of whole pieces]
     const void* mask;
     const void* pad;
-    const void* shrink[2][2];                       // [U layout][rank > 32]
+    const void* shrink[2][2][2];                    // [U layout][rank > 32][32 rows]
 };
 
 const GroupKernels& group_kernels_f16();
