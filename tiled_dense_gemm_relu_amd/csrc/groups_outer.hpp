@@ -27,15 +27,16 @@ __global__ __launch_bounds__(kOuterThreads) void weight_outer(WeightArgs a, cons
     const int strip = at / across, j0 = at % across * 8;
     if (strip >= strips) return;
     const int i0 = 8 * strip, is = min(8, a.i - i0);
-    // An element of p or q; columns past the row's end read its last one.
-    auto at_p = [&](int m, int i) {
-        const size_t x = (size_t)m * (size_t)a.i + (size_t)min(i, a.i - 1);
-        return to_float<DT>(MASKED == 1 ? mask_one<DT>(a.p[x], mask[x]) : a.p[x]);
+    // 8 elements from column x on of row m of p or q (zeros, or the next row's, past its end).
+    auto load8 = [&](const uint16_t* of, int cols, int m, int x, bool masked) {
+        const size_t at = (size_t)m * (size_t)cols;
+        const AnyRsrc r = make_any_rsrc(of + at, (uint32_t)cols * 2u);
+        const AnyChunk c = load_any(r, (uint32_t)x * 2u, true);
+        if (!masked) return chunk_value(c);
+        const AnyRsrc rm = make_any_rsrc(mask + at, (uint32_t)cols * 2u);
+        return mask_chunk<DT>(chunk_value(c), chunk_value(load_any(rm, (uint32_t)x * 2u, true)));
     };
-    auto at_q = [&](int m, int j) {
-        const size_t x = (size_t)m * (size_t)a.j + (size_t)min(max(j, 0), a.j - 1);
-        return to_float<DT>(MASKED == 2 ? mask_one<DT>(a.q[x], mask[x]) : a.q[x]);
-    };
+    auto element = [](u32x4 v, int e) { return to_float<DT>((uint16_t)(v[e / 2] >> (16 * (e & 1)))); };
     uint16_t* const out = a.out + ((size_t)g * (size_t)a.i + (size_t)i0) * (size_t)a.j;
     float acc[8][8];
 #pragma unroll
@@ -48,15 +49,11 @@ __global__ __launch_bounds__(kOuterThreads) void weight_outer(WeightArgs a, cons
             const size_t x = (size_t)m * (size_t)a.j + (size_t)j0;
             u32x4 w = *reinterpret_cast<const u32x4*>(a.q + x);
             if constexpr (MASKED == 2) w = mask_chunk<DT>(w, *reinterpret_cast<const u32x4*>(mask + x));
-            float p[8];
+            const u32x4 p = load8(a.p, a.i, m, i0, MASKED == 1);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = at_p(m, i0 + i);
+            for (int e = 0; e < 8; ++e)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float q = to_float<DT>((uint16_t)(w[e / 2] >> (16 * (e & 1))));
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i][e] += p[i] * q;
-            }
+                for (int i = 0; i < 8; ++i) acc[i][e] += element(p, i) * element(w, e);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -73,18 +70,19 @@ __global__ __launch_bounds__(kOuterThreads) void weight_outer(WeightArgs a, cons
         const uint32_t odd0 = (uint32_t)(reinterpret_cast<uintptr_t>(a.out + (size_t)g * (size_t)a.i * (size_t)a.j) >> 1) & 1u;
 #pragma unroll 2
         for (int m = begin; m < end; ++m) {
-            float p[8], q[9];
+            const u32x4 p = load8(a.p, a.i, m, i0, MASKED == 1), w = load8(a.q, a.j, m, j0, MASKED == 2);
+            const size_t x = (size_t)m * (size_t)a.j + (size_t)max(j0 - 1, 0);
+            float q[9];                // from the element before on (of the first column, any: it is not stored)
+            q[0] = to_float<DT>(MASKED == 2 ? mask_one<DT>(a.q[x], mask[x]) : a.q[x]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = at_p(m, i0 + i);
-#pragma unroll
-            for (int e = 0; e < 9; ++e) q[e] = at_q(m, j0 - 1 + e);
+            for (int e = 0; e < 8; ++e) q[e + 1] = element(w, e);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const bool odd = ((odd0 ^ ((uint32_t)i & (uint32_t)a.j)) & 1u) != 0;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float before = q[e], here = q[e + 1];    // (values: a choice of places would put q in memory)
-                    acc[i][e] += p[i] * (odd ? before : here);
+                    acc[i][e] += element(p, i) * (odd ? before : here);
                 }
             }
         }
