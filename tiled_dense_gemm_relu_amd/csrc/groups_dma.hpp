@@ -103,7 +103,7 @@ struct RowUnits {
     int rows;                // rows in groups
     int units;               // this XCD's
     int64_t first, last;     // its part of the work, or of the units
-    bool by_rows;
+    bool by_rows, rotate;
     const int* ids;          // the groups' adapters, or nullptr
     int adapters;
     UnitOrder order;
@@ -159,6 +159,7 @@ struct RowUnits {
         lane = lane_;
         order.init(block, blocks);
         by_rows = M > (int64_t)groups * a.n;
+        rotate = M <= 64 * (int64_t)min(groups, M);
         int64_t total = 0;
         rows = 0;
         for (int g0 = 0; g0 < listed; g0 += 64) {
@@ -282,9 +283,7 @@ __device__ __forceinline__ void store_rows_staged(uint16_t* __restrict__ C, cons
 // The same for rows of any length and alignment: dwords that lie on their
 // boundaries, 32 consecutive ones of a row to half a wave (16 where the wave has
 // 32 columns), and single elements at a piece's ends where a row starts inside a
-// dword.  (Storing each lane's 4 columns element by element made a request of
-// every 2 bytes: 32 against 18.5 us for the gradients of 1000 rows in 7 groups,
-// 517 x 1101 against 512 x 1104.)
+// dword.
 template <int DT, int FX, int FN, int FM>
 __device__ __forceinline__ void store_rows_any(uint16_t* __restrict__ C, const floatx4 (&acc)[FN][FM], uint8_t* strip,
                                                int lane, int m_base, int n_base, int m_end, int N, bool relu)
@@ -413,6 +412,13 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
     const uint16_t *f_ap = A, *f_bp = B;
     int f_arows = 0, f_brows = 0, f_m0 = 0, f_n0 = 0;
     int f_kb = 0, f_left_b = 0;       // B's place and what it has left, where they differ from f_k and f_left
+    // With few rows a group and B stored (N, K), the tiles start their K-steps at
+    // different places and wrap round: with row lengths of a power of two all rows'
+    // pieces of one K-step lie in few memory channels, and tiles in step would all
+    // wait for the same ones.  64 tokens over 64 experts, 2048 x 2048 bf16: 61.5
+    // against 68 us.
+    constexpr bool ROTATE = WS && !STAGED && !AK && !BKM && !FIRST && BM <= 64;
+    int f_todo = 0;                   // K-steps still to load of the unit
     const int rank_steps = FIRST ? 2 * ad.rank_pad / BK : 0;
     auto fill_setup = [&](bool start) {
         const int live = f_unit < n_units ? 1 : 0;
@@ -423,6 +429,14 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
         f_n0 = u.n0;
         f_k = u.k0;
         f_left = live * (u.k_end - u.k0);
+        if constexpr (ROTATE) {
+            const int steps = (u.k_end + BK - 1) / BK;
+            f_todo = live * steps;
+            if (units.rotate) {
+                f_k = (u.n0 / BN + u.group) % steps * BK;
+                f_left = live * (u.k_end - f_k);
+            }
+        }
         const uint16_t *a = A, *b = B + (size_t)u.group * b_group;
         if constexpr (FIRST) {
             f_kb = f_k;
@@ -497,9 +511,12 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
             f_k += BK;
             f_kb = next;
             f_left_b = ad.rank - next;
-        } else if (f_left <= BK) {
+        } else if (ROTATE ? --f_todo == 0 : f_left <= BK) {
             ++f_unit;
             fill_setup(true);
+        } else if (ROTATE && f_left <= BK) {
+            f_left += f_k;            // round to the first k
+            f_k = 0;
         } else {
             f_k += BK;
             f_left -= BK;
@@ -517,10 +534,10 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
     // piece may start 2 bytes into its first one (`shift` of the operand's
     // descriptor, and its row's number if the rows are odd: *_odd).  What lies
     // past the last k is read as it comes and zeroed on the way into LDS.  Nothing
-    // is read past a matrix's last dword.  A load costs its two address
-    // instructions and the way into LDS four shifts: with predicates and shifts
-    // computed for each piece the producers set the pace (ragged bf16 rows of
-    // 4100 and 1100 elements: 1.04 us a step of 128 x 128).
+    // is read past a matrix's last dword.  The producers set the pace here, so a
+    // load costs its two address instructions and the way into LDS four shifts: with
+    // predicates and shifts computed for each piece, 4000 bf16 rows of 4100 elements
+    // times 4100 x 1100 took 129 us instead of 86.
     constexpr bool ODD = Cfg::ODD;
     struct Piece {
         u32x4 v;
