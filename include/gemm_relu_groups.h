@@ -39,6 +39,9 @@
  * that runs to completion leaves them zero, so one buffer serves all calls of
  * one stream, of any shape, and those of gemm_relu_splitk too.  Calls that may
  * overlap in time need different ones.
+ * The rest holds partial sums, the adapters' intermediates, the masked gradient
+ * and, for large products of odd row lengths, copies of the operands on whole
+ * cache lines (as large as the operands); nothing of it is kept between calls.
  *
  * Limits: M, N, K <= 2^20, groups, segments, adapters <= 65535, rank <= 256, and
  * 256 rows of any matrix must be smaller than 2^31 bytes.
