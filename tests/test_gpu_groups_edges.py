@@ -1,0 +1,33 @@
+"""Products whose rows choose their weights, at the edges of the rules that choose their kernels.
+
+References, bars and helpers are test_gpu_groups.py's.
+"""
+import pytest
+import torch
+
+import tiled_dense_gemm_relu_amd as gr
+from test_gpu_groups import assert_close, backward_reference, ends_of, guarded, normal, say, weights
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("relu", [True, False])
+@pytest.mark.parametrize("sizes,N,K", [([64], 12001, 1304), ([63], 13089, 1388), ([50, 0, 90, 12, 70], 15209, 298)])
+def test_backward_of_few_odd_rows_and_a_long_sum(sizes, N, K, relu):
+    # 17 to 64 rows a group of an odd length: copies for dB, while dA's weights are streamed.
+    M, dt = sum(sizes), torch.bfloat16
+    say(f"[odd rows] M={M} N={N} K={K} relu={relu}")
+    a, b = normal((M, K), dt, 201), weights(len(sizes), N, K, dt, gr.B_NK, 202)
+    dc, c = normal((M, N), dt, 203), normal((M, N), dt, 204).clamp_min(0)
+    ra, ea, rb, eb = backward_reference(dc, c, a, b, sizes, gr.B_NK, relu)
+    da, whole_a = guarded((M, K), dt)
+    db, whole_b = guarded(tuple(b.shape), dt)
+    args, ends = (dc.cuda(), c.cuda() if relu else None, a.cuda(), b.cuda()), ends_of(sizes).cuda()
+    gr.gemm_relu_grouped_backward(*args, ends, b_layout=gr.B_NK, relu=relu, da=da, db=db)
+    torch.cuda.synchronize()
+    assert whole_a() and whole_b()
+    assert_close(da, ra, ea, "dA")
+    assert_close(db, rb, eb, "dB")
+    only_a, _ = gr.gemm_relu_grouped_backward(*args, ends, b_layout=gr.B_NK, relu=relu, need_db=False)
+    _, only_b = gr.gemm_relu_grouped_backward(*args, ends, b_layout=gr.B_NK, relu=relu, need_da=False)
+    assert torch.equal(only_a, da) and torch.equal(only_b, db)

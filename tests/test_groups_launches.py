@@ -1,0 +1,102 @@
+"""What the entry points of gemm_relu_groups.h launch, checked against what the kernels assume.
+
+groups_launches.cpp holds the library's own host code with a recorder in the place of the HIP runtime, so
+argument checks, kernel choice, workspace places and launch shapes run as they are, without a GPU.
+"""
+import ctypes
+import json
+import os
+import random
+import subprocess
+
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+KN, NK = 0, 1
+AUTO, TILED, DMA_256, DMA_128, DMA_64, STREAM = -1, 0, 1, 2, 3, 4
+COUNTERS = 65536
+
+# Well separated addresses, never followed.
+A, B, E, C, D, U, V, W = (i << 44 for i in range(1, 9))
+
+
+@pytest.fixture(scope="module")
+def host(tmp_path_factory):
+    so = tmp_path_factory.mktemp("groups_launches") / "groups_launches.so"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-x", "c++", "-w", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include",
+                    "-fno-gnu-unique", "-shared", "-fPIC", "-Wl,-Bsymbolic", os.path.join(HERE, "groups_launches.cpp"),
+                    "-o", str(so)], check=True)
+    lib = ctypes.CDLL(str(so))
+    vp, i64, ci = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    lib.gemm_relu_grouped.argtypes = [vp] * 4 + [i64] * 4 + [ci] * 4 + [vp, i64, vp]
+    lib.gemm_relu_grouped_workspace.argtypes = [i64] * 4 + [ci] * 2
+    lib.gemm_relu_grouped_backward.argtypes = [vp] * 7 + [i64] * 4 + [ci] * 4 + [vp, i64, vp]
+    lib.gemm_relu_grouped_backward_workspace.argtypes = [i64] * 4 + [ci] * 3
+    lib.gemm_relu_adapters.argtypes = [vp] * 8 + [i64] * 6 + [ci] * 4 + [vp, i64, vp]
+    lib.gemm_relu_adapters_workspace.argtypes = [i64] * 6 + [ci] * 2
+    for name in ("grouped", "grouped_backward", "adapters"):
+        getattr(lib, f"gemm_relu_{name}_workspace").restype = i64
+    lib.launches.restype = ctypes.c_char_p
+    return lib
+
+
+def grouped(host, M, N, K, groups, layout=KN, relu=1, config=AUTO, off=0):
+    need = host.gemm_relu_grouped_workspace(M, N, K, groups, 0, layout)
+    rc = host.gemm_relu_grouped(A + off, B + off, E, C + off, M, N, K, groups, 0, layout, relu, config, W, need, None)
+    return rc, need, json.loads(host.launches())
+
+
+def backward(host, M, N, K, groups, layout=KN, relu=1, config=AUTO, off=0, need_a=True, need_b=True):
+    need = host.gemm_relu_grouped_backward_workspace(M, N, K, groups, 0, layout, relu)
+    rc = host.gemm_relu_grouped_backward(D + off, C + off, A + off, B + off, E, U if need_a else None,
+                                         V if need_b else None, M, N, K, groups, 0, layout, relu, config, W, need, None)
+    return rc, need, json.loads(host.launches())
+
+
+def check_streams(launches):
+    """The streaming and outer kernels take rows as long as the product says: never a copy's pitch."""
+    for l in launches:
+        if l["kernel"] == "weight_outer":
+            assert l["ldp"] == l["i"] and l["ldq"] == l["j"], l
+        if l["kernel"] == "rows_skinny":
+            layout = l["place"] // 6 % 2
+            assert l["lda"] == l["k"] and l["ldb"] == (l["k"] if layout == NK else l["n"]), l
+
+
+def _log(rng, lo, hi):
+    return int(round(lo * (hi / lo) ** rng.random()))
+
+
+# (M, N, K, groups, layout): 17 to 64 rows a group, an odd row length, a long inner dimension.
+ODD_STREAMS = [(63, 13089, 1388, 1, NK), (222, 15209, 298, 5, NK), (64, 16385, 960, 1, NK), (32, 50257, 768, 1, NK),
+               (64, 12001, 1304, 1, NK), (17, 24001, 2500, 1, NK), (60, 14461, 1316, 1, NK)]
+
+
+@pytest.mark.parametrize("relu", [0, 1])
+@pytest.mark.parametrize("M,N,K,groups,layout", ODD_STREAMS)
+def test_backward_never_streams_copies_of_odd_rows(host, M, N, K, groups, layout, relu):
+    rc, _, launches = backward(host, M, N, K, groups, layout, relu)
+    assert rc == 0 and launches
+    check_streams(launches)
+
+
+def test_streams_take_whole_rows_over_many_sizes(host):
+    rng = random.Random(5)
+    streamed = padded = 0
+    for _ in range(6000):
+        if rng.random() < 0.5:
+            M, groups = _log(rng, 1, 5000), _log(rng, 1, 128)
+            N, K = _log(rng, 1, 60000), _log(rng, 1, 60000)
+        else:                                      # around ODD_STREAMS
+            groups = rng.randint(1, 6)
+            M, N, K = groups * rng.randint(17, 64), _log(rng, 8000, 60000), _log(rng, 200, 2500)
+        layout, relu, off = rng.choice([KN, NK]), rng.choice([0, 1]), rng.choice([0, 0, 0, 2])
+        config = rng.choice([AUTO] * 5 + [STREAM, DMA_64])
+        for call in (grouped, backward):
+            rc, _, launches = call(host, M, N, K, groups, layout, relu, config, off)
+            assert rc == 0
+            check_streams(launches)
+            kinds = {l["kernel"] for l in launches}
+            streamed += "rows_skinny" in kinds
+            padded += "pad" in kinds
+    assert streamed > 500 and padded > 500

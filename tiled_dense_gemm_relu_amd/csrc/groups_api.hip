@@ -186,8 +186,9 @@ bool streams(int64_t m, int64_t n, int64_t k, int64_t groups, bool dma)
     return 3.0 + (weights + again) / 3.2e6 < 5.5 + std::max(weights / 5e6, rounds * (double)ceil_div(k, 64) * step);
 }
 
-// The streaming kernel, for A masked by `mask` if that is not NULL.  `parts` (may
-// be NULL) and `counters`: space for partial sums.
+// The streaming kernel, for A masked by `mask` if that is not NULL.  Its rows of A
+// and B are as long as the product says (lda == k), never copies with a pitch.
+// `parts` (may be NULL) and `counters`: space for partial sums.
 int launch_stream(RowsArgs a, AdapterArgs ad, const uint16_t* mask, int dtype, int b_layout, float* parts, int* counters,
                   hipStream_t stream)
 {
@@ -283,7 +284,9 @@ int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config,
 {
     a.c_vec = store_width(a.c, a.n);
     DmaRows dma = std::min(dma_rows(a.a, a.lda), dma_rows(a.b, a.ldb));
-    if (config == GEMM_RELU_GROUPS_STREAM || (config == GEMM_RELU_GROUPS_AUTO && streams(a.m, a.n, a.k, a.groups, dma != kDmaNone)))
+    const bool whole_rows = a.lda == a.k && a.ldb == (b_layout == GEMM_RELU_B_NK ? a.k : a.n);
+    if (whole_rows && (config == GEMM_RELU_GROUPS_STREAM ||
+                       (config == GEMM_RELU_GROUPS_AUTO && streams(a.m, a.n, a.k, a.groups, dma != kDmaNone))))
         return launch_stream(a, ad, nullptr, dtype, b_layout, parts, counters, stream);
     if (dma == kDmaNone && config != GEMM_RELU_GROUPS_TILED && parts && PaddedRows(a.m, a.n, a.k, a.groups, b_layout).use) {
         char* to = reinterpret_cast<char*>(parts);
@@ -517,9 +520,12 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
                  (int)groups, (int)(kn ? K : N), (int)(kn ? N : K), 0};
     // Few rows a group: the weights' gradients are written, the weights read, at memory's pace.
     const GroupShape shape(M, groups);
+    float* parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts_at);
+    const bool stream_a =
+        want_a && (config_id == GEMM_RELU_GROUPS_STREAM ||
+                   (config_id == GEMM_RELU_GROUPS_AUTO && streams(M, K, N, groups, std::min(dma_rows(d, N), dma_rows(b, kn ? N : K)))));
     if (config_id == GEMM_RELU_GROUPS_STREAM || (config_id == GEMM_RELU_GROUPS_AUTO && shape.rows <= kOuterMost)) {
-        float* parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts_at);
-        if (want_a && (config_id == GEMM_RELU_GROUPS_STREAM || streams(M, K, N, groups, std::min(dma_rows(d, N), dma_rows(b, kn ? N : K)))))
+        if (stream_a)
             rc = launch_stream(r, AdapterArgs{}, c, dtype, layout_a, parts, static_cast<int*>(workspace), s);
         else if (want_a)
             rc = launch_grad_rows(r, c, masked, dtype, layout_a, config_id, cus, s);
@@ -531,6 +537,13 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
     const bool dma = dma_rows(d, N) && (!want_a || dma_rows(b, kn ? N : K)) && (!want_b || dma_rows(x, K));   // kDmaNone: false
     if (!dma && config_id != GEMM_RELU_GROUPS_TILED && PaddedGrad(M, N, K, groups, b_layout).use) {
         char* to = static_cast<char*>(workspace) + GEMM_RELU_GROUPS_COUNTER_BYTES;
+        bool tiles_a = want_a;
+        if (stream_a) {              // reads the matrices as they are, before the copies take its partial sums' place
+            rc = launch_stream(r, AdapterArgs{}, c, dtype, layout_a, parts, static_cast<int*>(workspace), s);
+            if (rc != GEMM_RELU_OK || !want_b) return rc;
+            tiles_a = false;
+            r.c = nullptr;
+        }
         if (N % 2)
             rc = launch_pad(r.a, r.lda, c, M, to, dtype, s);
         else if (relu) {
@@ -541,12 +554,12 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
         (kn ? w.q : w.p) = r.a;
         (kn ? w.ldq : w.ldp) = r.lda;
         if (want_b && K % 2 && rc == GEMM_RELU_OK) rc = launch_pad(kn ? w.p : w.q, kn ? w.ldp : w.ldq, nullptr, M, to, dtype, s);
-        if (want_a && r.ldb % 2 && rc == GEMM_RELU_OK) rc = launch_pad(r.b, r.ldb, nullptr, groups * (kn ? K : N), to, dtype, s);
-        const bool ready = dma_rows(r.a, r.lda) && (!want_a || dma_rows(r.b, r.ldb)) && (!want_b || (dma_rows(w.p, w.ldp) && dma_rows(w.q, w.ldq)));
+        if (tiles_a && r.ldb % 2 && rc == GEMM_RELU_OK) rc = launch_pad(r.b, r.ldb, nullptr, groups * (kn ? K : N), to, dtype, s);
+        const bool ready = dma_rows(r.a, r.lda) && (!tiles_a || dma_rows(r.b, r.ldb)) && (!want_b || (dma_rows(w.p, w.ldp) && dma_rows(w.q, w.ldq)));
         if (rc != GEMM_RELU_OK) return rc;
         if (!ready)                  // an even operand at an odd address
             return launch_grad_staged(r, w, nullptr, dtype, layout_a, config_id, cus, s);
-        if (want_a) rc = launch_rows(r, AdapterArgs{}, dtype, layout_a, config_id, cus, nullptr, nullptr, s);
+        if (tiles_a) rc = launch_rows(r, AdapterArgs{}, dtype, layout_a, config_id, cus, nullptr, nullptr, s);
         w.c_vec = store_width(w.out, w.j);
         if (want_b && rc == GEMM_RELU_OK) rc = launch_weights(w, dtype, config_id, cus, s);
         return rc;
