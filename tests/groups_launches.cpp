@@ -139,6 +139,8 @@ hipError_t hipLaunchKernel(const void* fn, dim3 grid, dim3 block, void** args, s
     return hipSuccess;
 }
 
+int low_rank_first(int n, int N, int whole) { return low_rank_column(n, N, whole != 0); }
+
 // The launches since the last call, as a JSON list; the next call of this frees it.
 const char* launches()
 {

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import tiled_dense_gemm_relu_amd as gr
-from test_gpu_groups import assert_close, backward_reference, ends_of, guarded, normal, say, weights
+from test_gpu_groups import (CONFIGS, adapter_inputs, adapter_reference, assert_close, backward_reference, ends_of,
+                             guarded, normal, say, weights)
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +32,21 @@ def test_backward_of_few_odd_rows_and_a_long_sum(sizes, N, K, relu):
     only_a, _ = gr.gemm_relu_grouped_backward(*args, ends, b_layout=gr.B_NK, relu=relu, need_db=False)
     _, only_b = gr.gemm_relu_grouped_backward(*args, ends, b_layout=gr.B_NK, relu=relu, need_da=False)
     assert torch.equal(only_a, da) and torch.equal(only_b, db)
+
+
+@pytest.mark.parametrize("layout", [gr.B_KN, gr.B_NK])
+@pytest.mark.parametrize("N", [4, 68, 264, 1872])
+@pytest.mark.parametrize("config", CONFIGS)
+def test_many_adapters_in_a_block_whose_tile_passes_the_last_column(config, N, layout):
+    # A decoding step: 16 rows, more than two adapters, the last of the table among them.
+    sizes, count, dt = [1] * 16, 9, torch.bfloat16
+    say(f"[adapters] N={N} layout={layout} config={config}")
+    x, w, u, v, scales, ends, _ = adapter_inputs(sizes, 0, N, 192, 16, count, dt, layout, 211)
+    ids = torch.arange(16, dtype=torch.int32) % count
+    ref, err = adapter_reference(x, w, u, v, scales, sizes, ids, layout, False)
+    out, whole = guarded((16, N), dt)
+    gr.gemm_relu_adapters(*(t.cuda() for t in (x, w, u, v, scales, ends, ids)), out=out, b_layout=layout, relu=False,
+                          config=config)
+    torch.cuda.synchronize()
+    assert whole()
+    assert_close(out, ref, err, "C")

@@ -100,3 +100,16 @@ def test_streams_take_whole_rows_over_many_sizes(host):
             streamed += "rows_skinny" in kinds
             padded += "pad" in kinds
     assert streamed > 500 and padded > 500
+
+
+@pytest.mark.parametrize("tile", [32, 64, 128])
+def test_lanes_past_the_last_column_read_inside_v(host, tile):
+    # The last rank row of the last adapter ends V: a piece of 4 columns must not pass column N.
+    for N in range(4, 400, 4):
+        for n in range(0, -(-N // tile) * tile, 4):
+            first = host.low_rank_first(n, N, 1)
+            assert 0 <= first and first + 4 <= N and (n >= N or first == n), (N, n, first)
+    for N in range(1, 200):
+        for n in range(0, -(-N // tile) * tile, 4):
+            first = host.low_rank_first(n, N, 0)
+            assert 0 <= first < N and (n >= N or first == n), (N, n, first)

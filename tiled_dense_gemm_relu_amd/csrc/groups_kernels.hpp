@@ -338,8 +338,7 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
                     uint32_t w[SIDE][8][2];             // [k] pairs of columns, or [4 pairs of k, 2 columns at a time]
 #pragma unroll
                     for (int i = 0; i < SIDE; ++i) {
-                        // columns past N repeat the last ones: their sums are not stored
-                        const int n = min(n_base + 16 * (i0 + i) + 4 * kg, N - 1), cols = min(4, N - n);
+                        const int n = low_rank_column(n_base + 16 * (i0 + i) + 4 * kg, N, !B_NK && ad.v_fast), cols = min(4, N - n);
                         if constexpr (B_NK) {
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {

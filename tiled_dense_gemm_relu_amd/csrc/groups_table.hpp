@@ -109,6 +109,10 @@ constexpr int64_t outer_tiles(int64_t i, int64_t j, bool aligned)
 {
     return ((i + 7) / 8 * (j / 8 + (aligned ? 0 : 1)) + kOuterThreads - 1) / kOuterThreads;
 }
+// First of the 4 columns of V that a lane reads for columns n .. n + 3 of its tile, which
+// may lie past the last of N: then some at the end, whose sums are not stored.  `whole`: the
+// 4 are read in one piece (n % 4 == 0 and N % 4 == 0), else one at a time up to N.
+constexpr int low_rank_column(int n, int N, bool whole) { return n < N ? n : whole ? N - 4 : N - 1; }
 constexpr int kSkinnyCols = 32, kSkinnyK = 128, kSkinnyThreads = 512;
 
 struct GroupKernels {
