@@ -6,8 +6,8 @@ import pytest
 import torch
 
 import tiled_dense_gemm_relu_amd as gr
-from test_gpu_groups import (CONFIGS, adapter_inputs, adapter_reference, assert_close, backward_reference, ends_of,
-                             guarded, normal, say, weights)
+from test_gpu_groups import (CONFIGS, adapter_inputs, adapter_reference, assert_close, backward_reference, calls,
+                             ends_of, guarded, normal, say, weights)
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,31 @@ def test_many_adapters_in_a_block_whose_tile_passes_the_last_column(config, N, l
     torch.cuda.synchronize()
     assert whole()
     assert_close(out, ref, err, "C")
+
+
+@pytest.mark.parametrize("which", range(6))
+def test_graph_with_a_forked_side_stream(which):
+    # The captured call runs on a stream forked from the capture's: its workspace is cleared there too.
+    call, ins, outs = calls()[which]
+    call()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        call(stream=side)
+        torch.zeros(1 << 20, device="cuda").add_(7.0)          # memory that the other stream takes meanwhile
+        torch.cuda.current_stream().wait_stream(side)
+    for k in range(4):
+        for t in ins:
+            t.copy_(normal(tuple(t.shape), t.dtype, 220 + k))
+        for t in outs:
+            t.fill_(777.0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        first = [t.clone() for t in outs]
+        for t in outs:
+            t.fill_(777.0)
+        call()                                                 # eager, on the same inputs
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(first, outs)), (which, k)

@@ -6,6 +6,7 @@ As in binding.py this is argument marshalling only, with no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import threading
@@ -23,6 +24,7 @@ CONFIG_DMA_128 = 2
 CONFIG_DMA_64 = 3
 CONFIG_STREAM = 4
 
+_as_it_is = contextlib.nullcontext()
 _lock = threading.Lock()
 _lib = None
 _spaces = {}               # (device, stream handle): the stream's workspace as (pointer, bytes, tensor)
@@ -126,6 +128,14 @@ def _new(shape, like, stream):
         return like.new_empty(shape)
 
 
+def _on(stream, dev):
+    """Makes the stream that the kernels run on the current one."""
+    import torch
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    return _as_it_is if _current_device() == dev else torch.cuda.device(dev)
+
+
 def _workspace(given, need, like, dev, handle, stream):
     """(pointer, bytes, tensor) of the workspace: ``given``, or the cached one of this stream, which
     gemm_relu_splitk's calls use too.  A capture takes memory of its own graph, so that replays stay
@@ -134,10 +144,13 @@ def _workspace(given, need, like, dev, handle, stream):
         return None, 0, None
     import torch
     if given is None:
-        if torch.cuda.is_current_stream_capturing():
-            given = torch.empty(need, dtype=torch.uint8, device=like.device)
-            given[:COUNTER_BYTES].zero_()
-            return given.data_ptr(), need, given
+        # On the kernels' stream, which need not be the current one: nothing else orders the clearing
+        # before them, or keeps the memory from others while they run.
+        with _on(stream, dev):
+            if torch.cuda.is_current_stream_capturing():
+                given = torch.empty(need, dtype=torch.uint8, device=like.device)
+                given[:COUNTER_BYTES].zero_()
+                return given.data_ptr(), need, given
         known = _spaces.get((dev, handle))
         if known is None or known[1] < need:
             s = stream if stream is not None else torch.cuda.current_stream(like.device)
