@@ -78,3 +78,30 @@ def test_graph_with_a_forked_side_stream(which):
         call()                                                 # eager, on the same inputs
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(first, outs)), (which, k)
+
+
+@pytest.mark.parametrize("relu", [True, False])
+@pytest.mark.parametrize("layout", [gr.B_KN, gr.B_NK])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("config", [-1, *CONFIGS])
+@pytest.mark.parametrize("sizes,N", [([1] * 37 + [100, 0, 300], 264), ([1500, 1300], 512)])
+def test_infinities_of_an_adapter_keep_their_sign(sizes, N, config, dtype, layout, relu):
+    # A V with infinities and NaN, in rows that use it: what the products' signs make of them, whatever
+    # the intermediate's parts are.
+    say(f"[adapters] {sizes[-3:]} N={N} {dtype} layout={layout} config={config} relu={relu}")
+    x, w, u, v, scales, ends, ids = adapter_inputs(sizes, 0, N, 136, 16, 3, dtype, layout, 231)
+    ids = torch.arange(len(sizes), dtype=torch.int32) % 3
+    inf, kn = float("inf"), v if layout == gr.B_KN else v.transpose(1, 2)
+    clean = [n for n in range(N) if n not in (5, 40, 41, 77)]
+    ref, err = adapter_reference(x, w, u, v, scales, sizes, ids, layout, relu)
+    kn[0, 3, 5], kn[0, 7, 40], kn[1, 0, 41], kn[1, 9, 41], kn[2, 15, 77] = inf, -inf, inf, -inf, float("nan")
+    want = adapter_reference(x, w, u, v, scales, sizes, ids, layout, False)[0][:, [5, 40, 41, 77]]
+    if relu:
+        want = torch.where(want > 0, want, torch.zeros_like(want))
+    got = gr.gemm_relu_adapters(*(t.cuda() for t in (x, w, u, v, scales, ends, ids)), b_layout=layout, relu=relu,
+                                config=config)
+    assert_close(got[:, clean], ref[:, clean], err[:, clean], "C")
+    got = got[:, [5, 40, 41, 77]].cpu().double()
+    odd = ~torch.isfinite(want)
+    assert odd.sum() > 0.1 * odd.numel() and torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.isfinite(got), ~odd) and torch.equal(got[want.abs() == inf], want[want.abs() == inf])

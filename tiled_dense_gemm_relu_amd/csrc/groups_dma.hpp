@@ -328,7 +328,7 @@ __device__ __forceinline__ void store_rows_any(uint16_t* __restrict__ C, const f
 //  With adapters, kAdaptAfter adds a finished tile's low-rank terms to its sums
 // (add_adapters: tiles may hold rows of many segments).  kAdaptFirst is for
 // tiles cut at the segments' ends: before its K-steps over A and B a tile
-// streams K-steps over the intermediates (hi, then lo) and V through the same
+// streams K-steps over the intermediates (lo, then hi) and V through the same
 // ring, multiplies its sums by the rows' factors, and goes on from them, so
 // the low-rank product costs its K-steps and nothing else.
 enum { kAdaptNone = 0, kAdaptAfter = 1, kAdaptFirst = 2 };
@@ -506,7 +506,7 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
                 fill_setup(false);
                 return;
             }
-            // V's K-steps once for hi, once again for lo
+            // V's K-steps once for lo, once again for hi
             const int next = f_kb + BK < ad.rank_pad ? f_kb + BK : 0;
             if constexpr (BKM) f_bp += (ptrdiff_t)(next - f_kb) * (ptrdiff_t)ldb;
             f_k += BK;
@@ -835,6 +835,12 @@ __device__ __forceinline__ void dma_product(const Units& units, const uint16_t* 
                 }
                 slot = slot_next;
                 c_k += BK;
+                if (FIRST && 2 * c_k == -rank_steps * BK && c.adapter >= 0) {
+#pragma unroll
+                    for (int j = 0; j < FX; ++j)
+#pragma unroll
+                        for (int i = 0; i < FN; ++i) acc[i][j] = finite_low(acc[i][j]);
+                }
                 if (FIRST && c_k == 0 && c.adapter >= 0) {
                     int l = j16;
                     asm volatile("" : "+v"(l));

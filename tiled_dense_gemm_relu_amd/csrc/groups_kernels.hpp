@@ -237,6 +237,19 @@ __global__ __launch_bounds__(256) void pad_rows(PadArgs a)
 template <int FN>
 constexpr int kAdapterStrip = 32 * FN * 16 * 2;
 
+// The products of an intermediate's low parts with V, before those of its high parts
+// are added: infinities and NaN of V become finite, so that a low part of zero or of
+// the other sign does not turn the term into NaN.  Where V is infinite or NaN the
+// high part's product is too, and decides.
+__device__ __forceinline__ floatx4 finite_low(floatx4 p)
+{
+    float most = __FLT_MAX__;
+    asm("" : "+s"(most));            // one scalar register and its negative, not a literal and a vector register
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] = __builtin_amdgcn_fmed3f(p[e], -most, most);
+    return p;
+}
+
 // Add the low-rank terms of rows m_base .. (those below m_end) to the first FX
 // of FN x FM blocks of C^T, block (i, j): rows m_base + 16j .. +15, columns n_base + 16i .. +15.
 //  A row's term is (its intermediate, hi + lo times a power of two) @ (its
@@ -281,8 +294,8 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
                 (uint32_t)(B_NK ? max(0, min(16 * FN, N - n_base)) : N) * (uint32_t)ad.rank * 2u);
             for (int k0 = 0; k0 < ad.rank; k0 += 32) {
                 const uint32_t at = in ? m * t_row + (uint32_t)(k0 + 8 * kb) * 2u : kOobOffset;
-                const u32x4 t_hi = __builtin_amdgcn_raw_buffer_load_b128(rt, at, 0, 0);
-                const u32x4 t_lo = __builtin_amdgcn_raw_buffer_load_b128(rt, at, ad.rank_pad * 2, 0);
+                const u32x4 t_lo = __builtin_amdgcn_raw_buffer_load_b128(rt, at, 0, 0);
+                const u32x4 t_hi = __builtin_amdgcn_raw_buffer_load_b128(rt, at, ad.rank_pad * 2, 0);
                 u32x4 v[FN];
                 if constexpr (B_NK) {
                     const int k = k0 + 8 * kb;
@@ -316,8 +329,8 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
                 }
 #pragma unroll
                 for (int i = 0; i < FN; ++i) {
-                    floatx4 p = mfma_16x16x32<DT>(v[i], t_hi, floatx4{0.0f, 0.0f, 0.0f, 0.0f});
-                    p = mfma_16x16x32<DT>(v[i], t_lo, p);
+                    floatx4 p = mfma_16x16x32<DT>(v[i], t_lo, floatx4{0.0f, 0.0f, 0.0f, 0.0f});
+                    p = mfma_16x16x32<DT>(v[i], t_hi, finite_low(p));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sum[i][e] = in ? sum[i][e] + f * p[e] : sum[i][e];
                 }
@@ -331,8 +344,8 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
             for (int r0 = 0; r0 < ad.rank; r0 += 8) {
                 const int valid = min(8, ad.rank - r0);
                 const uint32_t at = m * t_row + (uint32_t)r0 * 2u;
-                const u32x4 t_hi = __builtin_amdgcn_raw_buffer_load_b128(rt, at, 0, 0);
-                const u32x4 t_lo = __builtin_amdgcn_raw_buffer_load_b128(rt, at, ad.rank_pad * 2, 0);
+                const u32x4 t_lo = __builtin_amdgcn_raw_buffer_load_b128(rt, at, 0, 0);
+                const u32x4 t_hi = __builtin_amdgcn_raw_buffer_load_b128(rt, at, ad.rank_pad * 2, 0);
 #pragma unroll
                 for (int i0 = 0; i0 < FN; i0 += SIDE) {
                     uint32_t w[SIDE][8][2];             // [k] pairs of columns, or [4 pairs of k, 2 columns at a time]
@@ -387,7 +400,7 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
 
 // The intermediates of the low-rank terms.  For row m of a segment with adapter
 // i, z = scales[i] * (X[m] @ U_i) is summed in fp32 and stored as
-//     z = factor[m] * (t[m][hi][..] + t[m][lo][..]),  zeros from rank to rank_pad,
+//     z = factor[m] * (t[m][lo][..] + t[m][hi][..]),  zeros from rank to rank_pad,
 // factor a power of two of the row's largest |z|, hi the nearest 16-bit value
 // to z / factor (at most 1 in size) and lo that to what is left.  row_id[m] is
 // the row's adapter, -1 for none.
@@ -574,9 +587,9 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs a)
             const float scaled = c < chunks ? ldexpf(sums[sum_at(c, j)], -e) : 0.0f;
             const uint16_t hi = act_cast<DT>(scaled, false);
             const float rest = scaled - to_float<DT>(hi);
-            t[0] = hi;
+            t[a.rank_pad] = hi;
             // an infinite hi leaves inf - inf: such an entry has no second part
-            t[a.rank_pad] = fabsf(scaled) < __builtin_inff() ? act_cast<DT>(rest, false) : (uint16_t)0;
+            t[0] = fabsf(scaled) < __builtin_inff() ? act_cast<DT>(rest, false) : (uint16_t)0;
         }
         if (col == 0) a.factor[m] = ldexpf(1.0f, e);
     }

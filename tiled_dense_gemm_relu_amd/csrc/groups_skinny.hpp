@@ -64,8 +64,8 @@ __device__ __forceinline__ void add_low_rank(float (&z)[MB], const AdapterArgs& 
         uint16_t w[MB][8];
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
-            hi[j] = *reinterpret_cast<const u32x4*>(t[j] + r0);
-            lo[j] = *reinterpret_cast<const u32x4*>(t[j] + ad.rank_pad + r0);
+            lo[j] = *reinterpret_cast<const u32x4*>(t[j] + r0);
+            hi[j] = *reinterpret_cast<const u32x4*>(t[j] + ad.rank_pad + r0);
             if (B_NK && ad.v_fast) {
                 const u32x4 q = *reinterpret_cast<const u32x4*>(v[j] + r0);
 #pragma unroll

@@ -20,7 +20,7 @@ struct RowsArgs {
 };
 
 // The low-rank term of each row (v == nullptr: none).  Row m's adapter is
-// row_id[m] (-1: none) and its intermediate t[m][hi | lo][rank_pad] times
+// row_id[m] (-1: none) and its intermediate t[m][lo | hi][rank_pad] times
 // factor[m], see adapter_shrink.
 struct AdapterArgs {
     const uint16_t* v;     // (adapters, rank, N) or (adapters, N, rank)
