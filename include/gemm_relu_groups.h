@@ -70,7 +70,7 @@ enum {
     GEMM_RELU_GROUPS_DMA_128 = 2, /* 128x128 tiles, 4 stages, 4 compute waves and 4 that only load */
     GEMM_RELU_GROUPS_DMA_64 = 3,  /* 64x64 tiles, 4 stages, 4 compute waves and 4 that only load */
     GEMM_RELU_GROUPS_STREAM = 4   /* few rows a group: 16 to 64 rows x 32 columns, weights streamed into registers;
-                                     any row length and alignment (dB has no such kernel: as AUTO) */
+                                     any row length and alignment (of the gradients dA's; dB goes as by AUTO) */
 };
 
 /*

@@ -113,3 +113,22 @@ def test_lanes_past_the_last_column_read_inside_v(host, tile):
         for n in range(0, -(-N // tile) * tile, 4):
             first = host.low_rank_first(n, N, 0)
             assert 0 <= first < N and (n >= N or first == n), (N, n, first)
+
+
+def test_stream_on_request_is_dAs_alone(host):
+    # As the header says: dB goes as by AUTO (one 8192-row group is no work for a lane's loop over rows).
+    rng = random.Random(6)
+    def plain(launches):
+        return [{f: v for f, v in l.items() if f != "c"} for l in launches]
+    for _ in range(1500):
+        groups = _log(rng, 1, 64)
+        args = (_log(rng, 1, 20000), _log(rng, 1, 6000), _log(rng, 1, 6000), groups, rng.choice([KN, NK]), rng.choice([0, 1]))
+        off = rng.choice([0, 2])
+        rc, _, alone = backward(host, *args, AUTO, off, need_a=False)
+        rc_s, _, only_b = backward(host, *args, STREAM, off, need_a=False)
+        rc_a, _, only_a = backward(host, *args, STREAM, off, need_b=False)
+        rc_2, _, both = backward(host, *args, STREAM, off)
+        assert rc == rc_s == rc_a == rc_2 == 0
+        assert [l["kernel"] for l in only_a] == ["rows_skinny"] and both[0] == only_a[0], args
+        assert only_b == alone and plain(both[1:]) == plain(alone), args
+    assert [l["kernel"] for l in backward(host, 8192, 1024, 1024, 1, config=STREAM, relu=0)[2]] == ["rows_skinny", "weight_dma"]

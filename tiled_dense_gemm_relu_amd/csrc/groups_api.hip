@@ -332,7 +332,7 @@ int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config,
 // Sums over each group's rows (I, J > 0), by LDS DMA.
 int launch_weights(WeightArgs a, int dtype, int config, int cus, hipStream_t stream)
 {
-    if (config == GEMM_RELU_GROUPS_AUTO || config == GEMM_RELU_GROUPS_STREAM)
+    if (config == GEMM_RELU_GROUPS_AUTO)
         config = dma_config(a.i, a.groups * ceil_div(a.i, 256) * ceil_div(a.j, 256),
                             a.groups * ceil_div(a.i, 128) * ceil_div(a.j, 128));
     const bool whole = std::min(dma_rows(a.p, a.ldp), dma_rows(a.q, a.ldq)) == kDmaWhole;
@@ -519,31 +519,34 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
     WeightArgs w{kn ? x : d, kn ? d : x, static_cast<uint16_t*>(dB), ends, (int)M, (int)(kn ? K : N), (int)(kn ? N : K),
                  (int)groups, (int)(kn ? K : N), (int)(kn ? N : K), 0};
     // Few rows a group: the weights' gradients are written, the weights read, at memory's pace.
-    const GroupShape shape(M, groups);
+    // (Streaming is dA's: on request all of dA streams, and dB goes as by default.)
+    const bool stream_only = config_id == GEMM_RELU_GROUPS_STREAM;
+    const int config = stream_only ? GEMM_RELU_GROUPS_AUTO : config_id;
+    const bool outer = config == GEMM_RELU_GROUPS_AUTO && GroupShape(M, groups).rows <= kOuterMost;
+    const bool stream_a = want_a && (stream_only || (config == GEMM_RELU_GROUPS_AUTO &&
+                                                     streams(M, K, N, groups, std::min(dma_rows(d, N), dma_rows(b, kn ? N : K)))));
     float* parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts_at);
-    const bool stream_a =
-        want_a && (config_id == GEMM_RELU_GROUPS_STREAM ||
-                   (config_id == GEMM_RELU_GROUPS_AUTO && streams(M, K, N, groups, std::min(dma_rows(d, N), dma_rows(b, kn ? N : K)))));
-    if (config_id == GEMM_RELU_GROUPS_STREAM || (config_id == GEMM_RELU_GROUPS_AUTO && shape.rows <= kOuterMost)) {
-        if (stream_a)
-            rc = launch_stream(r, AdapterArgs{}, c, dtype, layout_a, parts, static_cast<int*>(workspace), s);
-        else if (want_a)
-            rc = launch_grad_rows(r, c, masked, dtype, layout_a, config_id, cus, s);
-        if (want_b && rc == GEMM_RELU_OK && gkn > 0) rc = launch_outer(w, c, kn, dtype, s);
+    bool tiles_a = want_a;
+    const auto stream_rows = [&] {     // dA from the matrices as they are
+        tiles_a = false;
+        const int streamed = launch_stream(r, AdapterArgs{}, c, dtype, layout_a, parts, static_cast<int*>(workspace), s);
+        r.c = nullptr;
+        return streamed;
+    };
+    if (stream_a && (stream_only || outer)) rc = stream_rows();
+    if (outer) {
+        if (tiles_a) rc = launch_grad_rows(r, c, masked, dtype, layout_a, config, cus, s);
+        if (want_b && rc == GEMM_RELU_OK) rc = launch_outer(w, c, kn, dtype, s);
         return rc;
     }
+    if (rc != GEMM_RELU_OK || !(tiles_a || want_b)) return rc;
     // LDS DMA needs rows of an even length and D itself in memory.  The register-
     // staged kernel needs neither, and is one launch instead of two or three.
-    const bool dma = dma_rows(d, N) && (!want_a || dma_rows(b, kn ? N : K)) && (!want_b || dma_rows(x, K));   // kDmaNone: false
-    if (!dma && config_id != GEMM_RELU_GROUPS_TILED && PaddedGrad(M, N, K, groups, b_layout).use) {
+    const bool dma = dma_rows(d, N) && (!tiles_a || dma_rows(b, kn ? N : K)) && (!want_b || dma_rows(x, K));   // kDmaNone: false
+    if (!dma && config != GEMM_RELU_GROUPS_TILED && PaddedGrad(M, N, K, groups, b_layout).use) {
         char* to = static_cast<char*>(workspace) + GEMM_RELU_GROUPS_COUNTER_BYTES;
-        bool tiles_a = want_a;
-        if (stream_a) {              // reads the matrices as they are, before the copies take its partial sums' place
-            rc = launch_stream(r, AdapterArgs{}, c, dtype, layout_a, parts, static_cast<int*>(workspace), s);
-            if (rc != GEMM_RELU_OK || !want_b) return rc;
-            tiles_a = false;
-            r.c = nullptr;
-        }
+        // before the copies take its partial sums' place
+        if (tiles_a && stream_a && ((rc = stream_rows()) != GEMM_RELU_OK || !want_b)) return rc;
         if (N % 2)
             rc = launch_pad(r.a, r.lda, c, M, to, dtype, s);
         else if (relu) {
@@ -558,22 +561,22 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
         const bool ready = dma_rows(r.a, r.lda) && (!tiles_a || dma_rows(r.b, r.ldb)) && (!want_b || (dma_rows(w.p, w.ldp) && dma_rows(w.q, w.ldq)));
         if (rc != GEMM_RELU_OK) return rc;
         if (!ready)                  // an even operand at an odd address
-            return launch_grad_staged(r, w, nullptr, dtype, layout_a, config_id, cus, s);
-        if (tiles_a) rc = launch_rows(r, AdapterArgs{}, dtype, layout_a, config_id, cus, nullptr, nullptr, s);
+            return launch_grad_staged(r, w, nullptr, dtype, layout_a, config, cus, s);
+        if (tiles_a) rc = launch_rows(r, AdapterArgs{}, dtype, layout_a, config, cus, nullptr, nullptr, s);
         w.c_vec = store_width(w.out, w.j);
-        if (want_b && rc == GEMM_RELU_OK) rc = launch_weights(w, dtype, config_id, cus, s);
+        if (want_b && rc == GEMM_RELU_OK) rc = launch_weights(w, dtype, config, cus, s);
         return rc;
     }
-    if (config_id == GEMM_RELU_GROUPS_TILED || !dma || (config_id == GEMM_RELU_GROUPS_AUTO && small_grad(M, N, K, groups)))
-        return launch_grad_staged(r, w, c, dtype, layout_a, config_id, cus, s);
+    if (config == GEMM_RELU_GROUPS_TILED || !dma || (config == GEMM_RELU_GROUPS_AUTO && small_grad(M, N, K, groups)))
+        return launch_grad_staged(r, w, c, dtype, layout_a, config, cus, s);
     if (relu) {
         rc = launch_mask(d, c, masked, mn, dtype, s);
         r.a = masked;
         (kn ? w.q : w.p) = masked;
     }
-    if (want_a && rc == GEMM_RELU_OK) rc = launch_rows(r, AdapterArgs{}, dtype, layout_a, config_id, cus, nullptr, nullptr, s);
+    if (tiles_a && rc == GEMM_RELU_OK) rc = launch_rows(r, AdapterArgs{}, dtype, layout_a, config, cus, nullptr, nullptr, s);
     w.c_vec = store_width(w.out, w.j);
-    if (want_b && rc == GEMM_RELU_OK && gkn > 0) rc = launch_weights(w, dtype, config_id, cus, s);
+    if (want_b && rc == GEMM_RELU_OK) rc = launch_weights(w, dtype, config, cus, s);
     return rc;
 }
 
