@@ -63,6 +63,47 @@ def check_streams(launches):
             assert l["lda"] == l["k"] and l["ldb"] == (l["k"] if layout == NK else l["n"]), l
 
 
+def adapters(host, M, N, K, rank, count, segments, layout=KN, config=AUTO, off=0):
+    need = host.gemm_relu_adapters_workspace(M, N, K, rank, count, segments, 0, layout)
+    rc = host.gemm_relu_adapters(A + off, B + off, U + off, V + off, D, E, E + (1 << 40), C + off, M, N, K, rank, count,
+                                 segments, 0, layout, 1, config, W, need, None)
+    return rc, need, json.loads(host.launches())
+
+
+BLOCKS = (1, 2, 4)                                 # 16-row blocks of the streaming kernels, by their place
+
+
+def check_places(launches, need):
+    """Launches are within the device's limits, and what they write in the workspace is inside it."""
+    def inside(at, nbytes, aligned=256):
+        assert W + COUNTERS <= at and at + nbytes <= W + need and at % aligned == 0, (l, need)
+    for l in launches:
+        assert 0 < l["x"] and l["x"] * l["threads"] < 1 << 32 and 0 < l["y"] < 65536 and l["lds"] <= 160 << 10, l
+        if l["kernel"] == "mask":
+            inside(l["d"], 2 * l["count"])
+        elif l["kernel"] == "pad":
+            assert l["pitch"] >= l["cols"] and l["pitch"] % 64 == 0
+            inside(l["dst"], 2 * l["rows"] * l["pitch"])
+        elif l["kernel"] == "rows_skinny" and l["y"] > 1:
+            inside(l["parts"], l["x"] * l["y"] * BLOCKS[l["place"] // 12] * 512 * 4)
+            assert l["counters"] == W and 4 * l["x"] <= COUNTERS
+        elif l["kernel"] == "shrink":
+            blocks, chunks = 1 + l["place"] % 2, -(-l["rank"] // 32)
+            assert l["rank_pad"] >= l["rank"] and l["rank_pad"] % 64 == 0
+            parts = l["x"] * l["y"] * chunks * blocks * 512 * 4 if l["y"] > 1 else 0
+            spans = [(l["t"], l["m"] * 2 * l["rank_pad"] * 2), (l["factor"], 4 * l["m"]), (l["row_id"], 4 * l["m"]),
+                     (l["part"], parts)]
+            for at, nbytes in spans:
+                inside(at, nbytes)
+            assert all(a + n <= b for (a, n), (b, _) in zip(spans, spans[1:]))
+            assert l["counters"] == W and (l["y"] == 1 or 4 * l["x"] <= COUNTERS) and l["lds"] >= chunks * blocks * 512 * 4
+            below = l["part"]                       # what lives on until the product has read it
+        if l.get("v"):                              # the product after adapter_shrink: its scratch leaves the intermediates
+            assert l["kernel"] != "rows_skinny" or l["y"] == 1 or l["parts"] >= below
+        if l["kernel"] == "pad" and len(launches) > 1 and launches[0]["kernel"] == "shrink":
+            assert l["dst"] >= below
+
+
 def _log(rng, lo, hi):
     return int(round(lo * (hi / lo) ** rng.random()))
 
@@ -132,3 +173,32 @@ def test_stream_on_request_is_dAs_alone(host):
         assert [l["kernel"] for l in only_a] == ["rows_skinny"] and both[0] == only_a[0], args
         assert only_b == alone and plain(both[1:]) == plain(alone), args
     assert [l["kernel"] for l in backward(host, 8192, 1024, 1024, 1, config=STREAM, relu=0)[2]] == ["rows_skinny", "weight_dma"]
+
+
+def any_size(rng, top):
+    return max(1, min(top, int(round(top ** rng.random())) + rng.choice([-1, 0, 0, 1])))
+
+
+def test_launches_and_scratch_stay_within_bounds_over_all_sizes(host):
+    # Up to the header's limits and the card's memory.
+    memory = 288 << 30
+    rng = random.Random(7)
+    seen = {}
+    for i in range(40000):
+        top = 1 << 20 if i % 2 else 20000
+        M, N, K, groups = any_size(rng, top), any_size(rng, top), any_size(rng, top), any_size(rng, 65535 if i % 2 else 256)
+        layout, relu, off = rng.choice([KN, NK]), rng.choice([0, 1]), rng.choice([0, 0, 0, 2])
+        config = rng.choice([AUTO] * 6 + [TILED, DMA_256, DMA_128, DMA_64, STREAM])
+        rank, count = rng.randint(1, 256), any_size(rng, 65535)
+        if 2 * (M * K + groups * K * N + M * N) > memory or 2 * count * rank * (K + N) > memory:
+            continue
+        for rc, need, launches in (grouped(host, M, N, K, groups, layout, relu, config, off),
+                                   backward(host, M, N, K, groups, layout, relu, config, off),
+                                   adapters(host, M, N, K, rank, count, groups, layout, config, off)):
+            assert rc in (0, -7), rc
+            assert rc == 0 or not launches, "refused after a launch"
+            check_places(launches, need)
+            for l in launches:
+                seen[l["kernel"]] = seen.get(l["kernel"], 0) + 1
+    assert min(seen.get(k, 0) for k in ("rows_dma", "weight_dma", "rows_skinny", "weight_outer", "mask", "pad", "shrink",
+                                        "staged_rows", "staged_grad")) > 100, seen

@@ -105,6 +105,9 @@ const StagedKernels& staged_kernels(int dtype, std::initializer_list<Rows> opera
     return even ? staged_kernels_bf16_even() : staged_kernels_bf16_odd();
 }
 
+// Whether one launch can have that many workgroups: their threads are counted in 32 bits.
+bool launchable(int64_t blocks, int threads) { return blocks <= int64_t(UINT32_MAX) / threads; }
+
 int enqueue(const void* fn, dim3 grid, int threads, void** args, hipStream_t stream, size_t lds = 0)
 {
     const hipError_t err = hipLaunchKernel(fn, grid, dim3((unsigned)threads), args, lds, stream);
@@ -168,6 +171,7 @@ struct SkinnyPlan {
         splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(k, 8 * kSkinnyK), 512 / units));
         if (splits > 1) bytes = units * splits * kSkinnyBlocks[kind] * kSkinnyThreads * 4;
     }
+    bool fits() const { return launchable(units, kSkinnyThreads); }
 };
 
 // Whether to stream.  The streaming kernel starts and ends quicker than the tiles
@@ -180,7 +184,7 @@ struct SkinnyPlan {
 bool streams(int64_t m, int64_t n, int64_t k, int64_t groups, bool dma)
 {
     const GroupShape g(m, groups);
-    if (g.rows > 64) return false;
+    if (g.rows > 64 || !SkinnyPlan(m, n, k, groups).fits()) return false;
     const double weights = 2.0 * (double)g.used * (double)n * (double)k, again = 2.0 * (double)m * (double)k * (double)ceil_div(n, kSkinnyCols);
     const double rounds = (double)ceil_div(g.tiles(64, n), 512), step = dma ? 0.16 : 0.35;
     return 3.0 + (weights + again) / 3.2e6 < 5.5 + std::max(weights / 5e6, rounds * (double)ceil_div(k, 64) * step);
@@ -193,7 +197,6 @@ int launch_stream(RowsArgs a, AdapterArgs ad, const uint16_t* mask, int dtype, i
                   hipStream_t stream)
 {
     SkinnyPlan plan(a.m, a.n, a.k, a.groups);
-    if (plan.units > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
     if (!parts) plan.splits = 1;
     const bool even = even_rows({{a.a, a.lda}, {mask, a.lda}, {a.b, a.ldb}});
     void* args[] = {&a, &ad, &parts, &counters, &mask};
@@ -206,8 +209,7 @@ int launch_stream(RowsArgs a, AdapterArgs ad, const uint16_t* mask, int dtype, i
 int launch_outer(WeightArgs w, const uint16_t* mask, bool mask_q, int dtype, hipStream_t stream)
 {
     const bool whole = w.j % 8 == 0 && aligned(w.q, 16) && aligned(w.out, 16) && (!mask || aligned(mask, 16));
-    const int64_t one = outer_tiles(w.i, w.j, whole), tiles = one * w.groups;
-    if (tiles > INT32_MAX || one * kOuterThreads > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
+    const int64_t tiles = outer_tiles(w.i, w.j, whole) * w.groups;
     void* args[] = {&w, &mask};
     return enqueue(kernels(dtype).weight_outer[!mask ? 0 : mask_q ? 2 : 1][whole], dim3((unsigned)tiles), kOuterThreads, args,
                    stream);
@@ -285,6 +287,7 @@ int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config,
     a.c_vec = store_width(a.c, a.n);
     DmaRows dma = std::min(dma_rows(a.a, a.lda), dma_rows(a.b, a.ldb));
     const bool whole_rows = a.lda == a.k && a.ldb == (b_layout == GEMM_RELU_B_NK ? a.k : a.n);
+    if (config == GEMM_RELU_GROUPS_STREAM && !SkinnyPlan(a.m, a.n, a.k, a.groups).fits()) config = GEMM_RELU_GROUPS_AUTO;
     if (whole_rows && (config == GEMM_RELU_GROUPS_STREAM ||
                        (config == GEMM_RELU_GROUPS_AUTO && streams(a.m, a.n, a.k, a.groups, dma != kDmaNone))))
         return launch_stream(a, ad, nullptr, dtype, b_layout, parts, counters, stream);
@@ -520,9 +523,10 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
                  (int)groups, (int)(kn ? K : N), (int)(kn ? N : K), 0};
     // Few rows a group: the weights' gradients are written, the weights read, at memory's pace.
     // (Streaming is dA's: on request all of dA streams, and dB goes as by default.)
-    const bool stream_only = config_id == GEMM_RELU_GROUPS_STREAM;
-    const int config = stream_only ? GEMM_RELU_GROUPS_AUTO : config_id;
-    const bool outer = config == GEMM_RELU_GROUPS_AUTO && GroupShape(M, groups).rows <= kOuterMost;
+    const bool stream_only = config_id == GEMM_RELU_GROUPS_STREAM && SkinnyPlan(M, K, N, groups).fits();
+    const int config = config_id == GEMM_RELU_GROUPS_STREAM ? GEMM_RELU_GROUPS_AUTO : config_id;
+    const bool outer = config == GEMM_RELU_GROUPS_AUTO && GroupShape(M, groups).rows <= kOuterMost &&
+                       outer_tiles(w.i, w.j, false) * groups <= INT32_MAX / kOuterThreads;   // lanes are numbered in an int
     const bool stream_a = want_a && (stream_only || (config == GEMM_RELU_GROUPS_AUTO &&
                                                      streams(M, K, N, groups, std::min(dma_rows(d, N), dma_rows(b, kn ? N : K)))));
     float* parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts_at);
