@@ -164,6 +164,52 @@ def _workspace(given, need, like, dev, handle, stream):
     return given.data_ptr(), given.numel() * given.element_size(), given
 
 
+@functools.lru_cache(maxsize=1)
+def _functions():
+    """The autograd functions behind calls whose inputs require gradients: (grouped, adapters).  Their
+    forward runs with gradients off, so it is the plain call."""
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class Grouped(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, a, b, ends, b_layout, relu, config, workspace):
+            c = gemm_relu_grouped(a, b, ends, b_layout=b_layout, relu=relu, config=config, workspace=workspace)
+            need_a, need_b = ctx.needs_input_grad[:2]
+            ctx.save_for_backward(a if need_b else None, b if need_a else None, ends, c if relu else None)
+            ctx.b_layout, ctx.relu = b_layout, relu
+            return c
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dc):
+            a, b, ends, c = ctx.saved_tensors
+            da, db = gemm_relu_grouped_backward(dc.contiguous(), c, a, b, ends, b_layout=ctx.b_layout, relu=ctx.relu,
+                                                need_da=ctx.needs_input_grad[0], need_db=ctx.needs_input_grad[1])
+            return da, db, None, None, None, None, None
+
+    class Adapters(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w, u, v, scales, ends, ids, b_layout, relu, config, workspace):
+            return gemm_relu_adapters(x, w, u, v, scales, ends, ids, b_layout=b_layout, relu=relu, config=config,
+                                      workspace=workspace)
+
+        @staticmethod
+        def backward(ctx, dc):
+            raise NotImplementedError("gemm_relu: gemm_relu_adapters has no gradient; call it under torch.no_grad()")
+
+    return Grouped, Adapters
+
+
+def _differentiable(function, dev, out, stream, *args):
+    """The call as a node of autograd's graph, on the kernels' stream so that its backward runs there too."""
+    if out is not None:
+        raise RuntimeError("gemm_relu: out= has no gradient, but an input requires one: leave out= away, or call "
+                           "under torch.no_grad()")
+    with _on(stream, dev):
+        return function.apply(*args)
+
+
 def _call(function, dev, *args):
     """The library launches on the current device: make it the tensors' one."""
     import torch
@@ -191,6 +237,8 @@ def gemm_relu_grouped(a, b, ends, out=None, b_layout: int = B_KN, relu: bool = T
     row counts).  Rows past the last end get zeros.  ``out`` (M, N) is written if given.
     ``workspace``: at least grouped_workspace_bytes(...) bytes whose first 65536 are zero, or None
     for a cached one per stream.  ``config``: a kernel (CONFIG_*), by default the library's choice.
+    Where gradients are on and ``a`` or ``b`` requires one, the result carries them
+    (gemm_relu_grouped_backward, on ``stream``); ``out`` is refused then.
     """
     import torch
     code, dev = _first("a", a)
@@ -206,6 +254,8 @@ def gemm_relu_grouped(a, b, ends, out=None, b_layout: int = B_KN, relu: bool = T
         raise ValueError(f"gemm_relu: inner dimensions differ: a {tuple(a.shape)}, b {tuple(b.shape)}")
     if ends.shape[0] != groups:
         raise ValueError(f"gemm_relu: ends must have one entry for each of {groups} groups, got {ends.shape[0]}")
+    if (a.requires_grad or b.requires_grad) and torch.is_grad_enabled():
+        return _differentiable(_functions()[0], dev, out, stream, a, b, ends, b_layout, relu, config, workspace)
     if out is None:
         out = _new((M, N), a, stream)
     else:
@@ -226,7 +276,8 @@ def gemm_relu_grouped_backward(dc, c, a, b, ends, b_layout: int = B_KN, relu: bo
 
     da has a's shape (zeros in rows of no group), db has b's (zeros for empty groups).
     ``need_da=False`` / ``need_db=False`` leave one out (None is returned for it, and ``b`` / ``a``
-    may be None).  ``c`` is only read with ``relu=True`` and may be None without.
+    may be None).  ``c`` is only read with ``relu=True`` and may be None without.  The gradients are
+    plain tensors, whether or not the inputs require gradients themselves.
     """
     import torch
     code, dev = _first("dc", dc)
@@ -280,7 +331,8 @@ def gemm_relu_adapters(x, w, u, v, scales, ends, ids, out=None, b_layout: int = 
     ``w`` (N, K), ``u`` (adapters, rank, K), ``v`` (adapters, N, rank); ``scales`` (adapters,) float32.
     ``ends`` and ``ids`` (segments,) int32: segment s holds rows ends[s-1] .. ends[s]-1 and uses adapter
     ids[s]; an id outside 0 .. adapters-1, and rows past the last end, use none.  ``relu=False``
-    leaves the ReLU out.
+    leaves the ReLU out.  There is no gradient: where gradients are on and an input requires one,
+    ``out`` is refused, and so is a backward pass through the result.
     """
     import torch
     code, dev = _first("x", x)
@@ -303,6 +355,10 @@ def gemm_relu_adapters(x, w, u, v, scales, ends, ids, out=None, b_layout: int = 
     _check_shape("scales", scales, (adapters,))
     segments = ends.shape[0]
     _check_shape("ids", ids, (segments,))
+    if (x.requires_grad or w.requires_grad or u.requires_grad or v.requires_grad
+            or scales.requires_grad) and torch.is_grad_enabled():
+        return _differentiable(_functions()[1], dev, out, stream, x, w, u, v, scales, ends, ids, b_layout, relu, config,
+                               workspace)
     if out is None:
         out = _new((M, N), x, stream)
     else:
