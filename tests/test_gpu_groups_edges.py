@@ -105,3 +105,20 @@ def test_infinities_of_an_adapter_keep_their_sign(sizes, N, config, dtype, layou
     odd = ~torch.isfinite(want)
     assert odd.sum() > 0.1 * odd.numel() and torch.equal(torch.isnan(got), torch.isnan(want))
     assert torch.equal(torch.isfinite(got), ~odd) and torch.equal(got[want.abs() == inf], want[want.abs() == inf])
+
+
+def test_released_workspaces_give_their_memory_back():
+    call, _, outs = calls()[4]
+    call()
+    want = [t.clone() for t in outs]
+    a, b = torch.ones((1500, 2051), device="cuda").half(), torch.ones((2, 2051, 2051), device="cuda").half()
+    gr.gemm_relu_grouped(a, b, torch.tensor([700, 1500]).int().cuda())         # odd rows: copies of a and b
+    torch.cuda.synchronize()
+    held = torch.cuda.memory_allocated()
+    gr.release_workspaces()
+    assert held - torch.cuda.memory_allocated() >= 2 * (a.numel() + b.numel())
+    for t in outs:
+        t.fill_(777.0)
+    call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, outs))

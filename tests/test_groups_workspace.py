@@ -5,7 +5,8 @@ import pytest
 import torch
 from torch.utils._python_dispatch import TorchDispatchMode
 
-from tiled_dense_gemm_relu_amd import groups
+import tiled_dense_gemm_relu_amd as gr
+from tiled_dense_gemm_relu_amd import binding, groups
 
 NEED = groups.COUNTER_BYTES + 4096
 
@@ -53,3 +54,33 @@ def test_capture_of_another_stream_than_the_current_one(monkeypatch):
     Streams(monkeypatch, capturing=("side",))
     first, second = (groups._workspace(None, NEED, torch.zeros(1), 0, 7, "side")[2] for _ in range(2))
     assert first.data_ptr() != second.data_ptr() and (0, 7) not in groups._spaces
+
+
+def test_cached_workspaces_grow_and_are_released(monkeypatch):
+    Streams(monkeypatch)
+    monkeypatch.setattr(groups, "_spaces", {})
+    like = torch.zeros(1)
+    first = groups._workspace(None, NEED, like, 0, 7, "side")
+    assert first[1] == NEED and not first[2][:groups.COUNTER_BYTES].any()
+    assert groups._workspace(None, NEED - 1, like, 0, 7, "side") is first
+    assert groups._workspace(None, NEED, like, 0, 8, None)[0] != first[0]          # another stream's
+    assert groups._workspace(None, 2 * NEED, like, 0, 7, "side")[1] == 2 * NEED
+    gr.release_workspaces()
+    assert not groups._spaces
+    assert not groups._workspace(None, NEED, like, 0, 7, "side")[2][:groups.COUNTER_BYTES].any()
+
+
+def test_splitk_keeps_its_own_workspace(monkeypatch):
+    # A captured gemm_relu_splitk holds the address of its cached buffer: a larger grouped call on the same
+    # stream must not replace it.
+    class Stream(str):
+        cuda_stream = 7
+    side = Stream("side")
+    Streams(monkeypatch)
+    monkeypatch.setattr(groups, "_spaces", {})
+    monkeypatch.setattr(binding, "_workspaces", {})
+    like = torch.zeros(1)
+    mine = binding.splitk_workspace(like.device, side, NEED)
+    assert groups._workspace(None, 8 * NEED, like, 0, 7, side)[0] != mine.data_ptr()
+    gr.release_workspaces()
+    assert binding.splitk_workspace(like.device, side, NEED) is mine

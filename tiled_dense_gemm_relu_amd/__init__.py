@@ -24,4 +24,5 @@ from .groups import (  # noqa: F401
     grouped_workspace_bytes,
     grouped_backward_workspace_bytes,
     adapters_workspace_bytes,
+    release_workspaces,
 )

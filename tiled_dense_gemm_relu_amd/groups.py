@@ -137,9 +137,10 @@ def _on(stream, dev):
 
 
 def _workspace(given, need, like, dev, handle, stream):
-    """(pointer, bytes, tensor) of the workspace: ``given``, or the cached one of this stream, which
-    gemm_relu_splitk's calls use too.  A capture takes memory of its own graph, so that replays stay
-    valid when the cached buffer is replaced by a larger one."""
+    """(pointer, bytes, tensor) of the workspace: ``given``, or the cached one of this stream.  A capture
+    takes memory of its own graph, so that replays stay valid when the cached buffer is replaced by a
+    larger one or released.  (gemm_relu_splitk's captures hold its cached buffer: these calls have one of
+    their own and never replace that.)"""
     if need == 0:
         return None, 0, None
     import torch
@@ -147,15 +148,14 @@ def _workspace(given, need, like, dev, handle, stream):
         # On the kernels' stream, which need not be the current one: nothing else orders the clearing
         # before them, or keeps the memory from others while they run.
         with _on(stream, dev):
-            if torch.cuda.is_current_stream_capturing():
+            capturing = torch.cuda.is_current_stream_capturing()
+            known = None if capturing else _spaces.get((dev, handle))
+            if known is None or known[1] < need:
                 given = torch.empty(need, dtype=torch.uint8, device=like.device)
                 given[:COUNTER_BYTES].zero_()
-                return given.data_ptr(), need, given
-        known = _spaces.get((dev, handle))
-        if known is None or known[1] < need:
-            s = stream if stream is not None else torch.cuda.current_stream(like.device)
-            given = binding.splitk_workspace(like.device, s, need)
-            known = _spaces[(dev, handle)] = given.data_ptr(), given.numel(), given
+                known = given.data_ptr(), need, given
+                if not capturing:
+                    _spaces[(dev, handle)] = known
         return known
     if not isinstance(given, torch.Tensor) or not given.is_cuda or not given.is_contiguous():
         raise TypeError("gemm_relu: workspace must be a contiguous GPU tensor")
@@ -208,6 +208,13 @@ def _differentiable(function, dev, out, stream, *args):
                            "under torch.no_grad()")
     with _on(stream, dev):
         return function.apply(*args)
+
+
+def release_workspaces():
+    """Gives back the cached workspaces: one per stream, as large as its largest call needed (large products
+    of odd row lengths need copies of their operands, all groups' weights among them).  Work already queued
+    keeps its memory until it is done; the next call takes a new one."""
+    _spaces.clear()
 
 
 def _call(function, dev, *args):
