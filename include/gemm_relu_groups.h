@@ -43,8 +43,7 @@
  * and, for large products of odd row lengths, copies of the operands on whole
  * cache lines (as large as the operands); nothing of it is kept between calls.
  *
- * Limits: M, N, K <= 2^20, groups, segments, adapters <= 65535, rank <= 256, and
- * 256 rows of any matrix must be smaller than 2^31 bytes.
+ * Limits: M, N, K <= 2^20, groups, segments, adapters <= 65535, rank <= 256.
  */
 #ifndef GEMM_RELU_GROUPS_H
 #define GEMM_RELU_GROUPS_H
@@ -108,10 +107,17 @@ int64_t gemm_relu_grouped_backward_workspace(int64_t M, int64_t N, int64_t K, in
  * segments' ends; `ids` is int32, `scales` float, one per adapter, all in
  * device memory.  X (M, K), C (M, N).
  *
- * The low-rank intermediate X @ U_i is summed in fp32 and kept as a power of
- * two times a sum of two 16-bit values per entry (22 bits for fp16, 16 for
- * bf16), so it neither overflows nor loses a 16-bit rounding.  The weights of
- * an adapter never reach rows that do not use it, infinities and NaN included.
+ * The low-rank intermediate X @ U_i is summed and scaled in fp32 and kept as a
+ * power of two, one for each row, above the row's largest entry, times a sum of
+ * two 16-bit values for each entry.  So it does not overflow, and an entry z is
+ * off by at most
+ *   bf16: 2^-16 |z|
+ *   fp16: 2^-22 |z| + 2^-25 times that power of two (fp16's smallest steps: an
+ *         entry 2^-12 of the row's largest keeps 12 bits),
+ * which is less than the 24 bits of an fp32 intermediate; the output is rounded
+ * to 8 or 11.  The weights of an adapter never reach rows that do not use it,
+ * infinities and NaN included; in rows that use it, infinities of V come out as
+ * the signs of their products say.
  */
 int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* V, const float* scales,
                        const int32_t* ends, const int32_t* ids, void* C, int64_t M, int64_t N, int64_t K,

@@ -202,3 +202,27 @@ def test_launches_and_scratch_stay_within_bounds_over_all_sizes(host):
                 seen[l["kernel"]] = seen.get(l["kernel"], 0) + 1
     assert min(seen.get(k, 0) for k in ("rows_dma", "weight_dma", "rows_skinny", "weight_outer", "mask", "pad", "shrink",
                                         "staged_rows", "staged_grad")) > 100, seen
+
+
+def test_workspace_sizes_are_what_the_launches_use(host):
+    # The copies, the masked gradient, the partial sums and the intermediates, each where it sets the size.
+    def up(n):
+        return -(-n // 256) * 256
+    rc, need, l = grouped(host, 2003, 1101, 2051, 3, NK)
+    assert [x["kernel"] for x in l] == ["pad", "pad", "rows_dma"]
+    assert need == COUNTERS + up(2 * 2003 * 2112) + up(2 * 3 * 1101 * 2112)     # rows of 2051 to 33 x 64
+    rc, need, l = grouped(host, 1, 4096, 4096, 1, KN)
+    assert [x["kernel"] for x in l] == ["rows_skinny"] and l[0]["y"] > 1
+    assert need == COUNTERS + l[0]["x"] * l[0]["y"] * 512 * 4
+    rc, need, l = backward(host, 2003, 1101, 2051, 3, NK)
+    assert [x["kernel"] for x in l] == ["pad", "pad", "pad", "rows_dma", "weight_dma"]
+    assert need == COUNTERS + up(2 * 2003 * 1152) + up(2 * 2003 * 2112) + up(2 * 3 * 1101 * 2112)
+    rc, need, l = backward(host, 8192, 4096, 2048, 16, KN)
+    assert [x["kernel"] for x in l] == ["mask", "rows_dma", "weight_dma"] and need == COUNTERS + 2 * 8192 * 4096
+    # Rank 12 is kept as 64 entries of two parts; a factor and an adapter for each row; 5 column blocks of
+    # rank 130 make 5 blocks of sums a part.
+    rc, need, l = adapters(host, 64, 64, 32, 12, 4, 4)
+    assert need == COUNTERS + 64 * 64 * 2 * 2 + 64 * 4 + 64 * 4
+    rc, need, l = adapters(host, 64, 16384, 8192, 130, 32, 64)
+    assert l[0]["kernel"] == "shrink" and l[0]["y"] > 1
+    assert need == COUNTERS + 64 * 192 * 2 * 2 + 2 * 64 * 4 + l[0]["x"] * l[0]["y"] * 5 * 512 * 4

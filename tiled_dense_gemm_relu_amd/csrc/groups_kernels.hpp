@@ -403,7 +403,10 @@ __device__ __forceinline__ void add_adapters(floatx4 (&acc)[FN][FM], const Adapt
 //     z = factor[m] * (t[m][lo][..] + t[m][hi][..]),  zeros from rank to rank_pad,
 // factor a power of two of the row's largest |z|, hi the nearest 16-bit value
 // to z / factor (at most 1 in size) and lo that to what is left.  row_id[m] is
-// the row's adapter, -1 for none.
+// the row's adapter, -1 for none.  Two 16-bit parts, since the second product's
+// matrix instructions take 16-bit operands: off by at most 2^-16 of z in bf16, 2^-22
+// of z and 2^-25 of factor in fp16, where the output's own rounding is 2^-8 or 2^-11
+// (a third part would hold fp32's 24 bits, for half as many low-rank products again).
 //  One workgroup per 16 MB rows of a segment and part of K, CHUNKS times 32
 // columns of rank at a time: its 8 waves take pieces of 128 k in turn, each with all its loads in
 // flight at once, and their sums are added in wave order in LDS.  With few rows
