@@ -147,7 +147,15 @@ struct GroupShape {
     int64_t tiles(int64_t tile, int64_t n) const { return used * ceil_div(rows, tile) * ceil_div(n, tile); }
 };
 
-// Position in kStagedTile of the tile of a register-staged product.
+// Position in kStagedTile of the tile of a register-staged product.  Measured, us,
+// bf16 KN, tiles of 128 / 64.  Many rows a group and long sums are for 128: 8192 rows in
+// 16 groups, 2048 x 4096 343 / 513; 4096 in 32, 2048 x 2048 143 / 173; 2048 in one 42 / 58;
+// 1024 in 8, 1024 x 2048 25 / 31.  Too few tiles are not: 700 in 7, 1101 x 517 33 / 18;
+// 512 in 4, 1024 x 1024 24 / 16.  Between them this rule can be wrong, where 128 makes a
+// second round of a few tiles or sums are short: 4096 in 16, 1025 x 1029 59 / 52; 1536 in
+// 16, 513 x 2051 43 / 29; 2000 in 8, 301 x 1501 27 / 20.  Both gradients: 2048 in one,
+// 2048 x 2048 123 / 166; 8192 in 16, 2048 x 4096 1439 / 1574; 4096 in 32, 2048 x 2048 758 /
+// 613 (dB has two K-steps a tile there); 800 in 8, 1024 x 1024 28 / 38, where it takes 64.
 int staged_tile(int64_t rows, int64_t tiles_128) { return rows >= 96 && tiles_128 >= 128 ? 0 : 1; }
 
 // Persistent workgroups for `tiles` units: as many as run at once (two of the
@@ -157,7 +165,19 @@ int64_t resident(int64_t tile, int64_t tiles, int cus) { return std::min<int64_t
 // The streaming kernel's part in a product: which one (by kSkinnyBlocks), and
 // into how many parts K is cut: as many as make 512 workgroups, while each of
 // their 8 waves has a piece of K.  A group's rows should mostly fit a
-// workgroup's, since every further workgroup reads the weights again.
+// workgroup's, since every further workgroup reads the weights again; but small
+// workgroups are more, and fill the CUs where K is not cut.  Measured, us on the
+// device, bf16 KN (NK), workgroups of 16 / 32 / 64 rows:
+//   1 row, 4096 x 4096             12.5 / 13.0 / 16.8   (11.3 / 11.9 / 16.5)
+//   32 rows in 8 groups, 2048 x 1024   13.2 / 13.0 / 16.5   (12.1 / 13.7 / 18.9)
+//   320 in 32, 1024 x 1024         20.8 / 18.9 / 28.1   (22.8 / 23.8 / 29.8)
+//   160 in 8, 512 x 512             4.9 /  4.6 /  5.5   ( 5.5 /  4.9 /  5.6)
+//   100 in 4, 8192 x 300           17.4 / 15.6 / 18.7   (17.4 / 16.4 / 18.6)
+//   64 in one, 2048 x 512           7.8 /  8.7 / 10.9   ( 8.8 /  9.7 / 11.9)
+//   64 in one, 12001 x 1304        55.5 / 45.3 / 29.2   (B^T as in a gradient, KN)
+//   40 in one, 12001 x 2048        80.6 / 75.5 / 48.1   (the same)
+// So 64 rows pay for long sums over wide weights and cost up to two fifths in small
+// products of 20 to 64 rows a group, which this rule does not tell apart.
 struct SkinnyPlan {
     int kind = -1;
     int64_t units = 0, splits = 1, bytes = 0;
@@ -255,6 +275,12 @@ struct PaddedGrad : PaddedPlan {
         add(m, n);
         add(m, k);
         add(groups * (nk ? n : k), nk ? k : n);
+        // Below kSmallGrad the register-staged launch is alone, the copies' way has five.
+        // fp16, us, registers / copies with the mask (without): 1000 rows in 7 groups, 1101 x
+        // 517 35 / 52 (29 / 52); 1000 in one, 1001 x 801 30 / 31 (21 / 30); 400 in 2, 1501 x
+        // 1501 52 / 52 (37 / 51); 2000 in 4, 701 x 701 36 / 44 (27 / 44); 300 in 10, 1101 x
+        // 1101 59 / 54 (45 / 53).  Above: 1500 in 6, 1201 x 1001 63 / 60 (49 / 60), where the
+        // estimate below says registers; 2003 in 3, 2051 x 1101 126 / 87 (91 / 87).
         if (bytes == 0 || 4.0 * (double)m * (double)n * (double)k < kSmallGrad) {
             bytes = 0;
             return;
@@ -314,6 +340,12 @@ int launch_rows(RowsArgs a, AdapterArgs ad, int dtype, int b_layout, int config,
     };
     if (config == GEMM_RELU_GROUPS_AUTO) {
         config = auto_config(ad.v ? ad.segments : a.groups);
+        // 4096 rows, 4096 x 8192 bf16 KN, rank 64, 256 tiles cut at the segments' ends / 128
+        // tiles of many segments, us: 2 to 8 segments 314 / 340-350, 10 339 / 338, 16 395 / 346
+        // (NK, rank 16: 373 / 419), 32 544 / 371; 2048 rows in 4 205 / 180.  So 192 rows a
+        // segment, the bar of dma_config, is too few for KN.  Where 256 tiles are refused, 128
+        // against 64, 4096 x 4096, rank 16: 512 rows in 64 segments 57 / 49, 700 in 40 50 / 61,
+        // 2048 in 256 117 / 148, 4096 in 64 171 / 246.
         if (ad.v && config != GEMM_RELU_GROUPS_DMA_256) config = std::max<int>(auto_config(1), GEMM_RELU_GROUPS_DMA_128);
     }
     if (config == GEMM_RELU_GROUPS_DMA_256 &&
@@ -416,7 +448,13 @@ AdapterSpace adapter_space(int64_t M, int64_t N, int64_t K, int64_t rank, int64_
 {
     AdapterSpace s;
     s.rank_pad = round_up(rank, 64);
-    // two blocks of rows a workgroup, which read U once, where segments fill them
+    // Two blocks of rows a workgroup, which read U once, where segments fill them.  First
+    // product and one of 256 columns, K 4096, bf16 KN (NK), us, one block / two: rank 16:
+    // 1024 rows in 4 segments 31.9 / 32.7 (32.7 / 33.0), 2048 in 8 35.6 / 34.8 (35.4 / 36.6),
+    // 4096 in 6 43.0 / 40.0 (44.7 / 40.5), 8192 in 16 63.4 / 65.8 (82.2 / 85.7), 12000 in 20
+    // 85.2 / 74.1 (104 / 95); rank 64: 1024 36.6 / 37.6 (39.9 / 39.2), 4096 51.1 / 46.6 (65.7 /
+    // 51.9), 12000 108 / 92 (147 / 119).  32 rows a segment (4096 in 128, 1024 columns): rank
+    // 64 92.6 / 95.7.
     s.blocks = M > 0 && GroupShape(M, segments).rows >= 48 && M >= 1024 ? 2 : 1;
     s.tiles = most_row_tiles(M, segments, s.blocks * kShrinkRows);
     s.splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(K, 8 * kShrinkK), s.tiles ? 512 / s.tiles : 1));
