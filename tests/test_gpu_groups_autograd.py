@@ -46,6 +46,37 @@ def test_autograd_on_a_side_stream():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("sizes", [[1, 0, 2, 1], SIZES])
+def test_captured_backward_pass(sizes):
+    # Forward and backward in one graph; no eager graph of the leaves is alive.
+    M = sum(sizes)
+    a, b = normal((M, 512), torch.bfloat16, 341).cuda(), weights(4, 256, 512, torch.bfloat16, gr.B_KN, 342).cuda()
+    ends, dc = ends_of(sizes).cuda(), normal((M, 256), torch.bfloat16, 343).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        gr.gemm_relu_grouped(a, b, ends)
+    torch.cuda.synchronize()
+    a.requires_grad_()
+    b.requires_grad_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = gr.gemm_relu_grouped(a, b, ends)
+        da, db = torch.autograd.grad(y, (a, b), dc)
+    for k in range(4):
+        with torch.no_grad():
+            a.copy_(normal((M, 512), torch.bfloat16, 350 + k))
+            dc.copy_(normal((M, 256), torch.bfloat16, 360 + k))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        with torch.no_grad():
+            c = gr.gemm_relu_grouped(a, b, ends)
+            want = gr.gemm_relu_grouped_backward(dc, c, a, b, ends)
+        torch.cuda.synchronize()
+        assert torch.equal(y, c) and torch.equal(da, want[0]) and torch.equal(db, want[1]), k
+
+
 def test_what_needs_no_graph_gets_none():
     a, b, ends, _ = inputs(torch.float16, gr.B_KN, 321)
     out = torch.empty((a.shape[0], N), dtype=a.dtype, device="cuda")

@@ -245,7 +245,8 @@ def gemm_relu_grouped(a, b, ends, out=None, b_layout: int = B_KN, relu: bool = T
     ``workspace``: at least grouped_workspace_bytes(...) bytes whose first 65536 are zero, or None
     for a cached one per stream.  ``config``: a kernel (CONFIG_*), by default the library's choice.
     Where gradients are on and ``a`` or ``b`` requires one, the result carries them
-    (gemm_relu_grouped_backward, on ``stream``); ``out`` is refused then.
+    (gemm_relu_grouped_backward, on ``stream``); ``out`` is refused then.  A backward pass can be
+    captured; as with torch's own operators, no eager graph of the same leaves may be alive meanwhile.
     """
     import torch
     code, dev = _first("a", a)
