@@ -26,3 +26,10 @@ from .groups import (  # noqa: F401
     adapters_workspace_bytes,
     release_workspaces,
 )
+from .blocks import (  # noqa: F401
+    quantize_blocks,
+    gemm_relu_blocks,
+    gemm_relu_blocks_backward,
+    blocks_workspace_bytes,
+    blocks_backward_workspace_bytes,
+)

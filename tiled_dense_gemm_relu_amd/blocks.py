@@ -1,0 +1,292 @@
+"""Products of 8-bit floating-point matrices scaled by blocks of 128 (the C ABI in include/gemm_relu_blocks.h).
+
+``quantize_blocks`` makes such matrices, ``gemm_relu_blocks`` multiplies them (dense, or grouped by expert),
+``gemm_relu_blocks_backward`` has the gradients of a layer that does.
+As in binding.py this is argument marshalling only, with no fallback.
+
+A quantized matrix is a ``torch.float8_e4m3fn`` or ``torch.float8_e5m2`` tensor whose rows start at multiples
+of 16 bytes (``stride(-2) % 16 == 0``), with float32 scales: by rows ``(blocks, rows)``, one for 128 elements
+of a row, or by tiles ``(row blocks, blocks)``, one for 128 x 128.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+import threading
+
+from . import binding
+from .binding import _check, _dtype_code, _stream_handle
+from .groups import _call, _check_shape, _check_tensor, _first, _new, _on, _workspace
+
+BLOCK = 128                # GEMM_RELU_BLOCK
+
+# Kernels of gemm_relu_blocks (GEMM_RELU_BLOCKS_*).
+CONFIG_AUTO = -1
+CONFIG_256 = 0
+CONFIG_128 = 1
+CONFIG_64 = 2
+CONFIG_STREAM = 3
+
+_lock = threading.Lock()
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        lib = binding.load_library()
+        with _lock:
+            vp, i64, ci = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+            lib.gemm_relu_quantize_blocks.argtypes = [vp] * 6 + [i64] * 5 + [ci] * 4 + [vp]
+            lib.gemm_relu_quantize_blocks.restype = ci
+            lib.gemm_relu_blocks.argtypes = [vp] * 6 + [i64] * 6 + [ci] * 6 + [vp, i64, vp]
+            lib.gemm_relu_blocks.restype = ci
+            lib.gemm_relu_blocks_workspace.argtypes = [i64] * 4
+            lib.gemm_relu_blocks_workspace.restype = i64
+            lib.gemm_relu_blocks_backward.argtypes = [vp] * 8 + [i64] * 5 + [ci] * 5 + [vp, i64, vp]
+            lib.gemm_relu_blocks_backward.restype = ci
+            lib.gemm_relu_blocks_backward_workspace.argtypes = [i64] * 3
+            lib.gemm_relu_blocks_backward_workspace.restype = i64
+            _lib = lib
+    return _lib
+
+
+@functools.lru_cache(maxsize=4096)
+def _bytes(function: str, *args) -> int:
+    """What a *_workspace function returns (pure host arithmetic on the sizes)."""
+    n = getattr(_library(), function)(*args)
+    if n < 0:
+        _check(int(n))
+    return n
+
+
+def blocks_workspace_bytes(M: int, N: int, K: int, groups: int = 1) -> int:
+    """Workspace of gemm_relu_blocks for these sizes (host only)."""
+    return _bytes("gemm_relu_blocks_workspace", M, N, K, groups)
+
+
+def blocks_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Workspace of gemm_relu_blocks_backward for these sizes (host only)."""
+    return _bytes("gemm_relu_blocks_backward_workspace", M, N, K)
+
+
+def _formats():
+    import torch
+    return {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+
+
+def _format_code(name, dtype) -> int:
+    code = _formats().get(dtype)
+    if code is None:
+        raise TypeError(f"gemm_relu: {name} must be float8_e4m3fn or float8_e5m2, got {dtype}")
+    return code
+
+
+def _check_8bit(name, t, dim, dev=None):
+    """(format, pitch) of a ``dim``-D 8-bit tensor: rows at one pitch, a multiple of 16 bytes, matrices of a
+    stack one behind the other, all 16-byte pieces of its rows inside its storage."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"gemm_relu: {name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"gemm_relu: {name} must be a GPU tensor, got {t.device}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"gemm_relu: {name} must be on the same device as the other tensors")
+    if t.dim() != dim:
+        raise ValueError(f"gemm_relu: {name} must be {dim}-D, got shape {tuple(t.shape)}")
+    code = _format_code(name, t.dtype)
+    if t.requires_grad:
+        raise RuntimeError(f"gemm_relu: {name} requires a gradient, but 8-bit operands have none; call under "
+                           "torch.no_grad() on detached tensors, or use linear_blocks")
+    shape, stride = t.shape, t.stride()
+    rows, row = shape[-2], shape[-1]
+    whole = (row + 15) // 16 * 16
+    if t.numel() == 0:
+        return code, whole
+    stacked = dim == 3 and shape[0] > 1
+    pitch = stride[-2] if rows > 1 else stride[0] if stacked else whole
+    if row > 1 and stride[-1] != 1:
+        raise ValueError(f"gemm_relu: {name} must be row-major")
+    if pitch < row or pitch % 16 or t.data_ptr() % 16:
+        raise ValueError(f"gemm_relu: rows of {name} must start at multiples of 16 bytes, got stride {stride}")
+    if stacked and stride[0] != rows * pitch:
+        raise ValueError(f"gemm_relu: the matrices of {name} must lie one behind the other, got stride {stride}")
+    count = rows * (shape[0] if dim == 3 else 1)
+    if t.storage_offset() + (count - 1) * pitch + whole > t.untyped_storage().nbytes():
+        raise ValueError(f"gemm_relu: the last row of {name} must have storage for whole 16-byte pieces")
+    return code, pitch
+
+
+def _blocks(n: int) -> int:
+    return (n + BLOCK - 1) // BLOCK
+
+
+def _empty_8bit(shape, dtype, like, stream):
+    """An 8-bit tensor whose rows start at multiples of 16 bytes."""
+    import torch
+    pitch = (shape[-1] + 15) // 16 * 16
+    with _on(stream, like.get_device()):
+        raw = torch.empty(shape[:-1] + (pitch,), dtype=torch.uint8, device=like.device)
+    return raw[..., : shape[-1]].view(dtype), pitch
+
+
+def _floats(shape, like, stream):
+    import torch
+    with _on(stream, like.get_device()):
+        return torch.empty(shape, dtype=torch.float32, device=like.device)
+
+
+def quantize_blocks(x, dtype=None, tiles: bool = False, mask=None, rows: bool = True, transposed: bool = False,
+                    power_of_two: bool = False, stream=None):
+    """8-bit values and scales of ``x`` (R, C) or a stack (count, R, C) in fp16 or bf16.
+
+    Returns ``(q, scales)``: q of x's shape in ``dtype`` (float8_e4m3fn by default, or float8_e5m2), scales
+    (C/128, R), one for 128 elements of a row, or with ``tiles`` (R/128, C/128); counts of blocks are rounded
+    up.  With ``transposed`` also ``(qt, scales_t)``: qt (C, R) the transposed matrix, quantized along its own
+    rows, scales_t (R/128, C), or with ``tiles`` the same tiles' values, (C/128, R/128).  ``rows=False`` leaves
+    the first pair out.  All from one pass over x.
+
+    A block's scale is its largest finite magnitude (at least 2**-80) over the format's largest value, with
+    ``power_of_two`` rounded up to a power of two; values are x / scale, rounded to fp32 and then to nearest
+    even.  ``mask`` (x's shape and dtype): x counts as zero where it is not above zero (a ReLU's gradient).
+    The outputs carry no gradient.
+    """
+    import torch
+    code, dev = _first("x", x)
+    if x.dim() not in (2, 3):
+        raise ValueError(f"gemm_relu: x must be 2-D or 3-D, got shape {tuple(x.shape)}")
+    _check_tensor("x", x, x.dim(), dev, x.dtype)
+    if mask is not None:
+        _check_tensor("mask", mask, x.dim(), dev, x.dtype)
+        _check_shape("mask", mask, tuple(x.shape))
+    dtype = torch.float8_e4m3fn if dtype is None else dtype
+    fmt = _format_code("dtype", dtype)
+    if not rows and not transposed:
+        raise ValueError("gemm_relu: neither rows nor transposed is asked for")
+    stack, (R, C) = tuple(x.shape[:-2]), x.shape[-2:]
+    count = stack[0] if stack else 1
+    q = s = qt = st = None
+    ldq = ldqt = 0
+    if rows:
+        q, ldq = _empty_8bit(stack + (R, C), dtype, x, stream)
+        s = _floats(stack + ((_blocks(R), _blocks(C)) if tiles else (_blocks(C), R)), x, stream)
+    if transposed:
+        qt, ldqt = _empty_8bit(stack + (C, R), dtype, x, stream)
+        st = _floats(stack + ((_blocks(C), _blocks(R)) if tiles else (_blocks(R), C)), x, stream)
+    if x.numel():
+        handle = _stream_handle(stream, dev)
+        _call(_library().gemm_relu_quantize_blocks, dev, x.data_ptr(), mask.data_ptr() if mask is not None else None,
+              q.data_ptr() if rows else None, s.data_ptr() if rows else None, qt.data_ptr() if transposed else None,
+              st.data_ptr() if transposed else None, count, R, C, ldq, ldqt, code, fmt, 1 if tiles else 0,
+              1 if power_of_two else 0, handle or None)
+    return ((q, s) if rows else ()) + ((qt, st) if transposed else ())
+
+
+def _out_dtype(out, out_dtype):
+    import torch
+    if out is not None and not isinstance(out, torch.Tensor):
+        raise TypeError("gemm_relu: out must be a torch.Tensor")
+    dtype = out.dtype if out is not None else torch.bfloat16 if out_dtype is None else out_dtype
+    if out_dtype is not None and dtype != out_dtype:
+        raise TypeError(f"gemm_relu: out is {dtype}, but out_dtype is {out_dtype}")
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"gemm_relu: the output's dtype must be float16 or bfloat16, got {dtype}")
+    return dtype, 0 if dtype is torch.float16 else 1
+
+
+def gemm_relu_blocks(a, a_scales, b, b_scales, ends=None, out=None, out_dtype=None, relu: bool = True,
+                     b_rows: bool = False, config: int = CONFIG_AUTO, workspace=None, stream=None):
+    """C = ReLU(A @ B^T) of the matrices that 8-bit ``a`` (M, K) and ``b`` (N, K) stand for.
+
+    ``a_scales`` (K/128, M) by rows; ``b_scales`` (N/128, K/128) by tiles, or (K/128, N) with ``b_rows``;
+    counts of blocks are rounded up.  With ``ends`` (groups,) int32 on the GPU, non-decreasing, ``b`` is
+    (groups, N, K), its scales have groups in front, and row m of group g (rows ends[g-1] .. ends[g]-1) is
+    multiplied with b[g]; rows past the last end get zeros.  ``relu=False`` leaves the ReLU out.  C (M, N) is
+    ``out`` if given, else a new tensor of ``out_dtype`` (bfloat16 by default).  ``workspace``: at least
+    blocks_workspace_bytes(...) bytes whose first 65536 are zero, or None for a cached one per stream.
+    ``config``: a kernel (CONFIG_*), by default the library's choice.
+    """
+    import torch
+    fa, lda = _check_8bit("a", a, 2)
+    dev = a.get_device()
+    grouped = ends is not None
+    fb, ldb = _check_8bit("b", b, 3 if grouped else 2, dev)
+    M, K = a.shape
+    N, groups = b.shape[-2], b.shape[0] if grouped else 1
+    if b.shape[-1] != K:
+        raise ValueError(f"gemm_relu: inner dimensions differ: a {tuple(a.shape)}, b {tuple(b.shape)}")
+    kb = _blocks(K)
+    _check_tensor("a_scales", a_scales, 2, dev, torch.float32)
+    _check_shape("a_scales", a_scales, (kb, M))
+    _check_tensor("b_scales", b_scales, 3 if grouped else 2, dev, torch.float32)
+    _check_shape("b_scales", b_scales, ((groups,) if grouped else ()) + ((kb, N) if b_rows else (_blocks(N), kb)))
+    if grouped:
+        _check_tensor("ends", ends, 1, dev, torch.int32)
+        _check_shape("ends", ends, (groups,))
+    dtype, code = _out_dtype(out, out_dtype)
+    if out is None:
+        with _on(stream, dev):
+            out = torch.empty((M, N), dtype=dtype, device=a.device)
+    else:
+        _check_tensor("out", out, 2, dev, dtype)
+        _check_shape("out", out, (M, N))
+    handle = _stream_handle(stream, dev)
+    ws, ws_bytes, keep = _workspace(workspace, blocks_workspace_bytes(M, N, K, groups), a, dev, handle, stream)
+    _call(_library().gemm_relu_blocks, dev, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(),
+          ends.data_ptr() if grouped else None, out.data_ptr(), M, N, K, groups, lda, ldb, fa, fb, 0 if b_rows else 1,
+          code, 1 if relu else 0, config, ws, ws_bytes, handle or None)
+    return out
+
+
+def gemm_relu_blocks_backward(dc, c, xt, xt_scales, wt, wt_scales, relu: bool = True, dtype=None, dx=None, dw=None,
+                              need_dx: bool = True, need_dw: bool = True, workspace=None, stream=None):
+    """Gradients (dx, dw) of C = ReLU(X @ W^T), X (M, K), W (N, K), for C's gradient ``dc``, both (M, N).
+
+    D, dc where c > 0, is quantized to ``dtype`` (float8_e5m2 by default) in blocks of 128 along the summed
+    dimension of each product.  ``xt`` (K, M) with scales (M/128, K) by rows, and ``wt`` (K, N) with scales
+    (K/128, N/128) by tiles, are the transposed outputs of quantize_blocks for X and (tiles=True) W.
+    ``need_dx=False`` / ``need_dw=False`` leave one out (None is returned, and ``wt`` / ``xt`` with their
+    scales may be None).  ``c`` is only read with ``relu=True``.  The gradients have dc's dtype.
+    """
+    import torch
+    code, dev = _first("dc", dc)
+    _check_tensor("dc", dc, 2, dev, dc.dtype)
+    dtype = torch.float8_e5m2 if dtype is None else dtype
+    fmt = _format_code("dtype", dtype)
+    if not need_dx and not need_dw:
+        raise ValueError("gemm_relu: neither gradient is asked for")
+    M, N = dc.shape
+    if relu:
+        _check_tensor("c", c, 2, dev, dc.dtype)
+        _check_shape("c", c, (M, N))
+    fx = fw = ldxt = ldwt = 0
+    if need_dw:
+        fx, ldxt = _check_8bit("xt", xt, 2, dev)
+        K = xt.shape[0]
+        _check_shape("xt", xt, (K, M))
+        _check_tensor("xt_scales", xt_scales, 2, dev, torch.float32)
+        _check_shape("xt_scales", xt_scales, (_blocks(M), K))
+    if need_dx:
+        fw, ldwt = _check_8bit("wt", wt, 2, dev)
+        K = K if need_dw else wt.shape[0]
+        _check_shape("wt", wt, (K, N))
+        _check_tensor("wt_scales", wt_scales, 2, dev, torch.float32)
+        _check_shape("wt_scales", wt_scales, (_blocks(K), _blocks(N)))
+
+    def output(name, t, shape):
+        if t is None:
+            return _new(shape, dc, stream)
+        _check_tensor(name, t, 2, dev, dc.dtype)
+        _check_shape(name, t, shape)
+        return t
+    dx = output("dx", dx, (M, K)) if need_dx else None
+    dw = output("dw", dw, (N, K)) if need_dw else None
+    handle = _stream_handle(stream, dev)
+    ws, ws_bytes, keep = _workspace(workspace, blocks_backward_workspace_bytes(M, N, K), dc, dev, handle, stream)
+    # An empty gradient still needs an address to be asked for.
+    _call(_library().gemm_relu_blocks_backward, dev, dc.data_ptr(), c.data_ptr() if relu else None,
+          xt.data_ptr() if need_dw else None, xt_scales.data_ptr() if need_dw else None,
+          wt.data_ptr() if need_dx else None, wt_scales.data_ptr() if need_dx else None,
+          (dx.data_ptr() or 256) if need_dx else None, (dw.data_ptr() or 256) if need_dw else None, M, N, K, ldxt, ldwt,
+          fmt, fx, fw, code, 1 if relu else 0, ws, ws_bytes, handle or None)
+    return dx, dw

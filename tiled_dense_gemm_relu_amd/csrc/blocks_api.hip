@@ -1,0 +1,250 @@
+// C ABI of the 8-bit products scaled by blocks of 128 (gemm_relu_blocks.h):
+// argument checks, kernel choice and launch.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/gemm_relu_blocks.h"
+#include "blocks_table.hpp"
+#include "checks.hpp"
+
+namespace gemm_relu_hip {
+namespace {
+
+constexpr int64_t kMaxDim = int64_t(1) << 20;
+constexpr int64_t kMaxPitch = int64_t(1) << 21;
+constexpr int64_t kMaxGroups = 65535;
+
+int64_t blocks_of(int64_t n) { return ceil_div(n, kBlock); }
+
+bool known_format(int f) { return f == GEMM_RELU_E4M3 || f == GEMM_RELU_E5M2; }
+bool known_form(int f) { return f == GEMM_RELU_SCALES_ROWS || f == GEMM_RELU_SCALES_TILES; }
+
+int check_dims(std::initializer_list<int64_t> dims)
+{
+    for (int64_t d : dims)
+        if (d < 0) return GEMM_RELU_ERR_INVALID_ARG;
+    for (int64_t d : dims)
+        if (d > kMaxDim) return GEMM_RELU_ERR_TOO_LARGE;
+    return GEMM_RELU_OK;
+}
+
+// The pitch of an 8-bit matrix with rows of `row` bytes.
+int check_pitch(int64_t ld, int64_t row)
+{
+    if (ld < row || ld % 16 != 0) return GEMM_RELU_ERR_MISALIGNED;
+    return ld > kMaxPitch ? GEMM_RELU_ERR_TOO_LARGE : GEMM_RELU_OK;
+}
+
+// The bytes of an 8-bit matrix: its loads take whole 16-byte pieces, its stores do not.
+int64_t read_bytes(int64_t rows, int64_t row, int64_t ld) { return rows && row ? (rows - 1) * ld + round_up(row, 16) : 0; }
+int64_t written_bytes(int64_t rows, int64_t row, int64_t ld) { return rows && row ? (rows - 1) * ld + row : 0; }
+
+const BlocksKernels& kernels(int format_a, int format_b)
+{
+    if (format_a == GEMM_RELU_E4M3) return format_b == GEMM_RELU_E4M3 ? blocks_kernels_e4m3_e4m3() : blocks_kernels_e4m3_e5m2();
+    return format_b == GEMM_RELU_E4M3 ? blocks_kernels_e5m2_e4m3() : blocks_kernels_e5m2_e5m2();
+}
+
+int launch_quantize(QuantizeArgs a, int64_t count, int dtype, int format, int form, hipStream_t stream)
+{
+    a.tiles_r = (int)blocks_of(a.rows);
+    a.tiles_c = (int)blocks_of(a.cols);
+    a.vec = a.cols % 8 == 0 && aligned(a.x, 16) && (!a.mask || aligned(a.mask, 16));
+    const int64_t tiles = count * a.tiles_r * a.tiles_c;
+    if (!launchable(tiles, kQuantizeThreads)) return GEMM_RELU_ERR_TOO_LARGE;
+    void* args[] = {&a};
+    return enqueue(quantize_kernel(dtype, format, form == GEMM_RELU_SCALES_TILES), dim3((unsigned)tiles), kQuantizeThreads, args,
+                   stream);
+}
+
+// Tiles of `tile` x `tile` that a product can have: whole ones, and a partial one for each group.
+int64_t most_tiles(const BlocksArgs& a, int64_t tile)
+{
+    return std::min<int64_t>(a.m, a.m / tile + a.groups) * ceil_div(a.n, tile);
+}
+
+int blocks_config(const BlocksArgs& a)
+{
+    const int64_t used = std::min(a.groups, a.m), rows = a.m / used;
+    const auto tiles = [&](int64_t t) { return used * ceil_div(rows, t) * ceil_div(a.n, t); };
+    if (rows >= 192 && tiles(256) >= 192) return GEMM_RELU_BLOCKS_256;
+    if (rows >= 96 && tiles(128) >= 128) return GEMM_RELU_BLOCKS_128;
+    return GEMM_RELU_BLOCKS_64;
+}
+
+// A product (M, N, K > 0).
+int launch_blocks(BlocksArgs a, int format_a, int format_b, int form_b, int config, int cus, hipStream_t stream)
+{
+    a.c_vec = a.n % 8 == 0 && aligned(a.c, 16);
+    if (config == GEMM_RELU_BLOCKS_AUTO || config == GEMM_RELU_BLOCKS_STREAM) config = blocks_config(a);
+    const int64_t tiles = most_tiles(a, kBlockTile[config]);
+    if (tiles > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
+    const int64_t grid = std::min<int64_t>(tiles, config == GEMM_RELU_BLOCKS_64 ? 2 * cus : cus);
+    void* args[] = {&a};
+    return enqueue(kernels(format_a, format_b).tile[config][form_b == GEMM_RELU_SCALES_ROWS], dim3((unsigned)grid),
+                   kBlockThreads[config], args, stream);
+}
+
+// Places in the backward pass's workspace.
+struct BackwardSpace {
+    int64_t q, s, qt, st, bytes, ldq, ldqt;
+    BackwardSpace(int64_t m, int64_t n)
+    {
+        ldq = round_up(n, 16);
+        ldqt = round_up(m, 16);
+        q = GEMM_RELU_GROUPS_COUNTER_BYTES;
+        s = q + round_up(m * ldq, 256);
+        qt = s + round_up(4 * m * blocks_of(n), 256);
+        st = qt + round_up(n * ldqt, 256);
+        bytes = st + round_up(4 * n * blocks_of(m), 256);
+    }
+};
+
+}  // namespace
+}  // namespace gemm_relu_hip
+
+using namespace gemm_relu_hip;
+
+extern "C" {
+
+int gemm_relu_quantize_blocks(const void* X, const void* mask, void* Q, float* scales, void* QT, float* scales_t,
+                              int64_t count, int64_t R, int64_t C, int64_t ldq, int64_t ldqt, int dtype, int format,
+                              int form, int power_of_two, void* stream)
+{
+    if (dtype != GEMM_RELU_F16 && dtype != GEMM_RELU_BF16) return GEMM_RELU_ERR_BAD_DTYPE;
+    if (!known_format(format)) return GEMM_RELU_ERR_BAD_DTYPE;
+    if (!known_form(form)) return GEMM_RELU_ERR_BAD_LAYOUT;
+    if (power_of_two != 0 && power_of_two != 1) return GEMM_RELU_ERR_INVALID_ARG;
+    int rc = check_dims({count, R, C});
+    if (rc != GEMM_RELU_OK) return rc;
+    if (count > kMaxGroups) return GEMM_RELU_ERR_TOO_LARGE;
+    if (!Q && !QT) return GEMM_RELU_ERR_INVALID_ARG;
+    if (Q && (rc = check_pitch(ldq, C)) != GEMM_RELU_OK) return rc;
+    if (QT && (rc = check_pitch(ldqt, R)) != GEMM_RELU_OK) return rc;
+    if (count == 0 || R == 0 || C == 0) return GEMM_RELU_OK;
+    const bool tiles = form == GEMM_RELU_SCALES_TILES;
+    const int64_t elements = count * R * C, n_tiles = count * blocks_of(R) * blocks_of(C);
+    const Span in[] = {{X, 2 * elements}, {mask, mask ? 2 * elements : 0}};
+    const Span out[] = {{Q, Q ? written_bytes(count * R, C, ldq) : 0}, {QT, QT ? written_bytes(count * C, R, ldqt) : 0},
+                        {scales, !Q ? 0 : 4 * (tiles ? n_tiles : count * R * blocks_of(C))},
+                        {scales_t, !QT ? 0 : 4 * (tiles ? n_tiles : count * C * blocks_of(R))}};
+    if ((rc = check_spans(in, 2, nullptr, 0, out, 4)) != GEMM_RELU_OK) return rc;
+    if ((Q && !aligned(Q, 16)) || (QT && !aligned(QT, 16)) || (Q && !aligned(scales, 4)) || (QT && !aligned(scales_t, 4)))
+        return GEMM_RELU_ERR_MISALIGNED;
+    int cus = 0;
+    if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;
+    QuantizeArgs a{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(mask), static_cast<uint8_t*>(Q), scales,
+                   static_cast<uint8_t*>(QT), scales_t, (int)R, (int)C, 0, 0, ldq, ldqt, power_of_two, 0};
+    return launch_quantize(a, count, dtype, format, form, static_cast<hipStream_t>(stream));
+}
+
+int64_t gemm_relu_blocks_workspace(int64_t M, int64_t N, int64_t K, int64_t groups)
+{
+    const int rc = check_dims({M, N, K});
+    if (rc != GEMM_RELU_OK) return rc;
+    if (groups < 1) return GEMM_RELU_ERR_INVALID_ARG;
+    if (groups > kMaxGroups) return GEMM_RELU_ERR_TOO_LARGE;
+    return 0;
+}
+
+int gemm_relu_blocks(const void* A, const float* scales_a, const void* B, const float* scales_b, const int32_t* ends,
+                     void* C, int64_t M, int64_t N, int64_t K, int64_t groups, int64_t lda, int64_t ldb, int format_a,
+                     int format_b, int form_b, int dtype, int relu, int config_id, void* workspace,
+                     int64_t workspace_bytes, void* stream)
+{
+    if (dtype != GEMM_RELU_F16 && dtype != GEMM_RELU_BF16) return GEMM_RELU_ERR_BAD_DTYPE;
+    if (!known_format(format_a) || !known_format(format_b)) return GEMM_RELU_ERR_BAD_DTYPE;
+    if (!known_form(form_b)) return GEMM_RELU_ERR_BAD_LAYOUT;
+    const int64_t need = gemm_relu_blocks_workspace(M, N, K, groups);
+    if (need < 0) return (int)need;
+    if ((relu != 0 && relu != 1) || (!ends && groups != 1)) return GEMM_RELU_ERR_INVALID_ARG;
+    if (config_id < GEMM_RELU_BLOCKS_AUTO || config_id > GEMM_RELU_BLOCKS_STREAM) return GEMM_RELU_ERR_BAD_CONFIG;
+    int rc = check_pitch(lda, K);
+    if (rc == GEMM_RELU_OK) rc = check_pitch(ldb, K);
+    if (rc != GEMM_RELU_OK) return rc;
+    if (M == 0 || N == 0) return GEMM_RELU_OK;
+    const int64_t kb = blocks_of(K);
+    const Span in[] = {{A, read_bytes(M, K, lda)}, {B, read_bytes(groups * N, K, ldb)}};
+    const Span words[] = {{scales_a, 4 * M * kb},
+                          {scales_b, 4 * groups * kb * (form_b == GEMM_RELU_SCALES_ROWS ? N : blocks_of(N))},
+                          {ends, ends ? 4 * groups : 0}};
+    const Span out[] = {{C, 2 * M * N}, {workspace, need}};
+    rc = check_spans(in, 2, words, 3, out, 1);
+    if (rc == GEMM_RELU_OK && K > 0 && (!aligned(A, 16) || !aligned(B, 16))) rc = GEMM_RELU_ERR_MISALIGNED;
+    if (rc == GEMM_RELU_OK) rc = check_workspace(workspace, workspace_bytes, need);
+    if (rc == GEMM_RELU_OK) rc = check_spans(in, 2, words, 3, out, need > 0 ? 2 : 1);
+    if (rc != GEMM_RELU_OK) return rc;
+    int cus = 0;
+    if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (K == 0) return zero_fill(C, M * N, s);
+    BlocksArgs a{static_cast<const uint8_t*>(A), scales_a, static_cast<const uint8_t*>(B), scales_b, static_cast<uint16_t*>(C),
+                 ends, (int)M, (int)N, (int)K, (int)groups, (uint32_t)lda, (uint32_t)ldb, relu, dtype == GEMM_RELU_BF16, 0};
+    return launch_blocks(a, format_a, format_b, form_b, config_id, cus, s);
+}
+
+int64_t gemm_relu_blocks_backward_workspace(int64_t M, int64_t N, int64_t K)
+{
+    const int rc = check_dims({M, N, K});
+    return rc != GEMM_RELU_OK ? rc : BackwardSpace(M, N).bytes;
+}
+
+int gemm_relu_blocks_backward(const void* dC, const void* C, const void* XT, const float* scales_xt, const void* WT,
+                              const float* scales_wt, void* dX, void* dW, int64_t M, int64_t N, int64_t K, int64_t ldxt,
+                              int64_t ldwt, int format, int format_x, int format_w, int dtype, int relu, void* workspace,
+                              int64_t workspace_bytes, void* stream)
+{
+    if (dtype != GEMM_RELU_F16 && dtype != GEMM_RELU_BF16) return GEMM_RELU_ERR_BAD_DTYPE;
+    if (!known_format(format) || !known_format(format_x) || !known_format(format_w)) return GEMM_RELU_ERR_BAD_DTYPE;
+    const int64_t need = gemm_relu_blocks_backward_workspace(M, N, K);
+    if (need < 0) return (int)need;
+    if (relu != 0 && relu != 1) return GEMM_RELU_ERR_INVALID_ARG;
+    const bool want_x = dX != nullptr, want_w = dW != nullptr;
+    if (!want_x && !want_w && K > 0) return GEMM_RELU_ERR_INVALID_ARG;
+    int rc = want_w ? check_pitch(ldxt, M) : GEMM_RELU_OK;
+    if (rc == GEMM_RELU_OK && want_x) rc = check_pitch(ldwt, N);
+    if (rc != GEMM_RELU_OK) return rc;
+    if (K == 0) return GEMM_RELU_OK;                 // both gradients are empty
+    const int64_t mn = M * N;
+    const Span in[] = {{dC, 2 * mn}, {relu ? C : nullptr, relu ? 2 * mn : 0}, {want_w ? XT : nullptr, want_w ? read_bytes(K, M, ldxt) : 0},
+                       {want_x ? WT : nullptr, want_x ? read_bytes(K, N, ldwt) : 0}};
+    const Span words[] = {{want_w ? scales_xt : nullptr, want_w ? 4 * K * blocks_of(M) : 0},
+                          {want_x ? scales_wt : nullptr, want_x ? 4 * blocks_of(K) * blocks_of(N) : 0}};
+    const Span out[] = {{dX, want_x ? 2 * M * K : 0}, {dW, want_w ? 2 * N * K : 0}, {workspace, need}};
+    rc = check_spans(in, 4, words, 2, out, 2);
+    if (rc == GEMM_RELU_OK && mn > 0 && ((want_w && !aligned(XT, 16)) || (want_x && !aligned(WT, 16)))) rc = GEMM_RELU_ERR_MISALIGNED;
+    if (rc == GEMM_RELU_OK) rc = check_workspace(workspace, workspace_bytes, need);
+    if (rc == GEMM_RELU_OK) rc = check_spans(in, 4, words, 2, out, 3);
+    if (rc != GEMM_RELU_OK) return rc;
+    int cus = 0;
+    if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (mn == 0) {                                   // empty sums
+        if (want_x) rc = zero_fill(dX, M * K, s);
+        if (want_w && rc == GEMM_RELU_OK) rc = zero_fill(dW, N * K, s);
+        return rc;
+    }
+    const BackwardSpace space(M, N);
+    char* const ws = static_cast<char*>(workspace);
+    uint8_t *q = reinterpret_cast<uint8_t*>(ws + space.q), *qt = reinterpret_cast<uint8_t*>(ws + space.qt);
+    float *sq = reinterpret_cast<float*>(ws + space.s), *st = reinterpret_cast<float*>(ws + space.st);
+    QuantizeArgs d{static_cast<const uint16_t*>(dC), relu ? static_cast<const uint16_t*>(C) : nullptr, want_x ? q : nullptr, sq,
+                   want_w ? qt : nullptr, st, (int)M, (int)N, 0, 0, space.ldq, space.ldqt, 0, 0};
+    rc = launch_quantize(d, 1, dtype, format, GEMM_RELU_SCALES_ROWS, s);
+    const int bf16 = dtype == GEMM_RELU_BF16;
+    if (want_x && rc == GEMM_RELU_OK) {
+        BlocksArgs a{q, sq, static_cast<const uint8_t*>(WT), scales_wt, static_cast<uint16_t*>(dX), nullptr, (int)M, (int)K, (int)N, 1,
+                     (uint32_t)space.ldq, (uint32_t)ldwt, 0, bf16, 0};
+        rc = launch_blocks(a, format, format_w, GEMM_RELU_SCALES_TILES, GEMM_RELU_BLOCKS_AUTO, cus, s);
+    }
+    if (want_w && rc == GEMM_RELU_OK) {
+        BlocksArgs a{qt, st, static_cast<const uint8_t*>(XT), scales_xt, static_cast<uint16_t*>(dW), nullptr, (int)N, (int)K, (int)M, 1,
+                     (uint32_t)space.ldqt, (uint32_t)ldxt, 0, bf16, 0};
+        rc = launch_blocks(a, format, format_x, GEMM_RELU_SCALES_ROWS, GEMM_RELU_BLOCKS_AUTO, cus, s);
+    }
+    return rc;
+}
+
+}  // extern "C"

@@ -1,0 +1,329 @@
+// The product of 8-bit matrices scaled by blocks of 128 (gemm_relu_blocks.h), on
+// tiles whose operands stream into LDS by DMA.
+//
+// One v_mfma_f32_16x16x128_f8f6f4 sums a whole scale block of 128 k for 16 x 16
+// outputs, at twice the 16-bit rate.  Its result goes, times the block's two
+// scales, into fp32 sums in registers: 4 multiply-adds a lane beside 32 cycles of
+// the matrix unit, which run on the vector unit meanwhile.
+//
+// A stage is 128 k of the tile's rows of A and B, 128 bytes a row, swizzled and
+// read as the 16-bit kernels' (a_swizzle<128>), and the scales of those rows and
+// columns as floats: with scales by tiles every lane of the scales' DMA fetches
+// its column's tile, so both forms look alike in LDS.
+#pragma once
+
+#include "groups_dma.hpp"
+#include "blocks_table.hpp"
+
+namespace gemm_relu_hip {
+
+
+
+typedef int int32x8_t __attribute__((ext_vector_type(8)));
+
+// 16 x 16 fp32 sums over 128 k: `w` of format FW, `x` of format FX.  A lane holds
+// 32 bytes of one row of each; which k those are only has to agree between them.
+template <int FW, int FX>
+__device__ __forceinline__ floatx4 mfma_block(int32x8_t w, int32x8_t x)
+{
+    const floatx4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, FW, FX, 0, 0, 0, 0);
+}
+
+template <int BM_, int BN_, int STAGES_, int WAVES_M_, int WAVES_N_>
+struct BlockConfig {
+    static constexpr int BM = BM_, BN = BN_, BK = 128, STAGES = STAGES_, GROUP_M = 4;
+    static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, WAVES = WAVES_M * WAVES_N, THREADS = 64 * WAVES;
+    static constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N, FM = WTM / 16, FN = WTN / 16;
+    static constexpr int A_STAGE = BM * BK, B_STAGE = BN * BK, B_REGION = STAGES * A_STAGE;
+    static constexpr int S_STAGE = (BM + BN) * 4, S_REGION = STAGES * (A_STAGE + B_STAGE);
+    // A wave's strip: 16 rows of its columns of C on their way to memory.
+    static constexpr int STRIP = 16 * WTN * 2, STRIPS = S_REGION + STAGES * S_STAGE;
+    static constexpr int LDS_BYTES = STRIPS + WAVES * STRIP;
+    static constexpr int QA = A_STAGE / 1024 / WAVES, QB = B_STAGE / 1024 / WAVES, NQ = QA + QB + 1;
+    static constexpr int SCALE_PIECES = (BM + BN) / 64;
+    static_assert(QA * WAVES * 1024 == A_STAGE && QB * WAVES * 1024 == B_STAGE, "whole DMA instructions");
+    static_assert(QA % 2 == 0 && QB % 2 == 0, "the swizzle repeats every two instructions");
+    static_assert(SCALE_PIECES <= WAVES && WAVES % SCALE_PIECES == 0, "one DMA of scales a wave");
+    static_assert((STAGES & (STAGES - 1)) == 0 && LDS_BYTES <= 160 * 1024 && STAGES * NQ < 64, "ring");
+    static_assert((WTN == 64 || WTN == 32) && 128 % WTN == 0, "a wave's columns lie in one tile of scales");
+};
+
+// Store FN x FM blocks of C^T (store_cols) through the wave's strip, 16 rows at a
+// time: whole 16-byte pieces (c_vec), or dwords that lie on their boundaries and
+// single elements at a row piece's ends.
+template <int DT, int FN, int FM>
+__device__ __forceinline__ void store_strips(uint16_t* __restrict__ C, const floatx4 (&acc)[FN][FM], uint8_t* strip,
+                                             int lane, int m_base, int n_base, int m_end, int N, bool relu, int c_vec)
+{
+    constexpr int kNonTemporal = 2;   // cache policy nt
+    constexpr int ROW = FN * 32, CHUNKS = ROW / 16;
+    asm volatile("" : "+v"(lane));    // what follows from it is computed here, not kept through the caller's loop
+    const int r16 = lane & 15, g = lane >> 4;
+    auto at = [](int row, int chunk) { return row * ROW + ((chunk ^ ((row >> 1) & (CHUNKS - 1))) << 4); };
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+        const int m = m_base + 16 * j, rows = max(0, min(16, m_end - m));
+        if (rows == 0) break;
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+            const floatx4& v = acc[i][j];
+            *reinterpret_cast<u32x2*>(strip + at(r16, 2 * i + (g >> 1)) + 8 * (g & 1)) =
+                u32x2{(uint32_t)act_cast<DT>(v[0], relu) | ((uint32_t)act_cast<DT>(v[1], relu) << 16),
+                      (uint32_t)act_cast<DT>(v[2], relu) | ((uint32_t)act_cast<DT>(v[3], relu) << 16)};
+        }
+        if (c_vec) {
+            const __amdgpu_buffer_rsrc_t rc = make_rsrc(C + (size_t)m * (size_t)N, (uint32_t)rows * (uint32_t)N * 2u);
+#pragma unroll
+            for (int s = 0; s < CHUNKS / 4; ++s) {
+                const int r = s * (64 / CHUNKS) + lane / CHUNKS, c = lane % CHUNKS, n = n_base + 8 * c;
+                const u32x4 v = *reinterpret_cast<const u32x4*>(strip + at(r, c));
+                const uint32_t off = n < N ? ((uint32_t)r * (uint32_t)N + (uint32_t)n) * 2u : kOobOffset;
+                __builtin_amdgcn_raw_buffer_store_b128(v, rc, off, 0, kNonTemporal);
+            }
+        } else {
+            constexpr int LANES = FN * 8;                             // dwords of a strip's row
+            const int cols = min(16 * FN, N - n_base);
+            for (int r = lane / LANES; r < rows; r += 64 / LANES) {
+                uint16_t* const p = C + (size_t)(m + r) * (size_t)N + n_base;
+                const int odd = (int)(reinterpret_cast<uintptr_t>(p) >> 1) & 1, e = 2 * (lane % LANES) + odd;
+                auto element = [&](int x) { return *reinterpret_cast<const uint16_t*>(strip + at(r, x >> 3) + 2 * (x & 7)); };
+                if (e + 1 < cols)
+                    *reinterpret_cast<uint32_t*>(p + e) = (uint32_t)element(e) | ((uint32_t)element(e + 1) << 16);
+                else if (e < cols)
+                    p[e] = element(e);
+                if (odd && e == 1 && cols > 0) p[0] = element(0);
+            }
+        }
+    }
+}
+
+// The first `valid` of 16 bytes, zeros after them.
+__device__ __forceinline__ u32x4 keep_bytes(u32x4 v, int valid)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int left = valid - 4 * i;
+        v[i] = left >= 4 ? v[i] : left > 0 ? v[i] & (0xffffffffu >> (32 - 8 * left)) : 0u;
+    }
+    return v;
+}
+
+template <class Cfg, int FA, int FB, bool B_ROWS>
+__global__ __launch_bounds__(Cfg::THREADS, 1) void blocks_dma(BlocksArgs a)
+{
+    constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK, S = Cfg::STAGES, FM = Cfg::FM, FN = Cfg::FN;
+    constexpr int QA = Cfg::QA, QB = Cfg::QB, NQ = Cfg::NQ;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
+    const int k_blocks = (a.k + BK - 1) / BK, n_tiles = (a.n + kBlock - 1) / kBlock;
+    RowUnits<Cfg, true> units;
+    {
+        RowsArgs r{};
+        r.m = a.m;
+        r.n = a.n;
+        r.k = a.k;
+        units.init(r, a.ends, a.groups, false, lane, blockIdx.x, gridDim.x);
+        if (units.rows < a.m) {
+            r.c = a.c;
+            zero_rows(r, units.rows, blockIdx.x, gridDim.x);
+        }
+    }
+    const int n_units = __builtin_amdgcn_readfirstlane(units.count());
+    if (n_units <= 0) return;
+    auto unit_at = [&](int i) {
+        const DmaUnit u = units.unit(i);
+        return DmaUnit{__builtin_amdgcn_readfirstlane(u.m0), __builtin_amdgcn_readfirstlane(u.m_end),
+                       __builtin_amdgcn_readfirstlane(u.n0), __builtin_amdgcn_readfirstlane(u.group), 0, a.k, -1};
+    };
+    const uint32_t lds_base = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)smem);
+
+    // Where a lane's 16 bytes of a DMA instruction come from: row of the piece and
+    // first k; two instructions (16 rows) on, the swizzle repeats.
+    uint32_t a_voff[2], b_voff[2];
+    int pos[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int row = 8 * q + lane / 8;
+        pos[q] = ((lane % 8) ^ a_swizzle<128>(row)) * 16;
+        a_voff[q] = (uint32_t)row * a.lda + (uint32_t)pos[q];
+        b_voff[q] = (uint32_t)row * a.ldb + (uint32_t)pos[q];
+    }
+    // The scales' DMA: 64 floats of the tile's rows or columns a wave.
+    const int piece = wave % Cfg::SCALE_PIECES;
+    const bool scales_of_a = piece < BM / 64;
+    const uint32_t scales_lds = lds_base + Cfg::S_REGION + 256u * (uint32_t)piece;
+
+    // The load side; past the last unit everything is out of range and fetches nothing.
+    int f_unit = 0, f_k = 0, f_rows = 0, f_cols = 0;
+    const uint8_t *f_a = a.a, *f_b = a.b;
+    const float* f_s = a.sa;          // this wave's scales of block 0
+    uint32_t f_soff = 0, f_sbytes = 0, f_sstep = 0;
+    auto fill_setup = [&]() {
+        const int live = f_unit < n_units ? 1 : 0;
+        const DmaUnit u = unit_at(live ? f_unit : n_units - 1);
+        f_k = 0;
+        f_rows = live * (u.m_end - u.m0);
+        f_cols = live * min(BN, a.n - u.n0);
+        f_a = a.a + (size_t)u.m0 * a.lda;
+        f_b = a.b + ((size_t)u.group * (size_t)a.n + (size_t)u.n0) * a.ldb;
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        if (scales_of_a) {
+            f_s = a.sa + u.m0 + 64 * piece;
+            f_sbytes = 4u * (uint32_t)max(0, min(64, f_rows - 64 * piece));
+            f_sstep = (uint32_t)a.m;
+            f_soff = 4u * (uint32_t)l;
+        } else {
+            const int c = 64 * (piece - BM / 64);                    // first column, from n0 on
+            if constexpr (B_ROWS) {
+                f_s = a.sb + (size_t)u.group * (size_t)k_blocks * (size_t)a.n + (size_t)(u.n0 + c);
+                f_sbytes = 4u * (uint32_t)max(0, min(64, f_cols - c));
+                f_sstep = (uint32_t)a.n;
+                f_soff = 4u * (uint32_t)l;
+            } else {
+                const int tile = (u.n0 + c) / kBlock;                // (64 columns lie in one tile)
+                f_s = a.sb + ((size_t)u.group * (size_t)n_tiles + (size_t)min(tile, n_tiles - 1)) * (size_t)k_blocks;
+                f_sbytes = 4u * (uint32_t)live;
+                f_sstep = 1u;
+                f_soff = 0u;
+            }
+        }
+    };
+    auto rows_from = [](const uint8_t* p, int rows, int skip, uint32_t ld) {
+        const int32x4_t r = rsrc_words(p + (size_t)skip * ld, (uint32_t)max(0, rows - skip) * ld);
+        return int32x4_t{__builtin_amdgcn_readfirstlane(r[0]), __builtin_amdgcn_readfirstlane(r[1]),
+                         __builtin_amdgcn_readfirstlane(r[2]), kBufferFlags};
+    };
+    auto dma = [&](int slot, int q) {
+        const int left = a.k - f_k;
+        if (q < QA) {
+            dma_b128(rows_from(f_a, f_rows, (wave * QA + (q & ~1)) * 8, a.lda), lds_base + slot * Cfg::A_STAGE + (wave * QA + q) * 1024,
+                     pos[q & 1] >= left ? kOobOffset : a_voff[q & 1], (uint32_t)f_k);
+        } else if (q < QA + QB) {
+            const int p = q - QA;
+            dma_b128(rows_from(f_b, f_cols, (wave * QB + (p & ~1)) * 8, a.ldb),
+                     lds_base + Cfg::B_REGION + slot * Cfg::B_STAGE + (wave * QB + p) * 1024,
+                     pos[p & 1] >= left ? kOobOffset : b_voff[p & 1], (uint32_t)f_k);
+        } else {
+            const int32x4_t r = rsrc_words(f_s + (size_t)(f_k / BK) * f_sstep, f_sbytes);
+            dma_b32(int32x4_t{__builtin_amdgcn_readfirstlane(r[0]), __builtin_amdgcn_readfirstlane(r[1]),
+                              __builtin_amdgcn_readfirstlane(r[2]), kBufferFlags},
+                    scales_lds + slot * Cfg::S_STAGE, f_soff, 0u);
+        }
+    };
+    auto fill_advance = [&]() {
+        if (f_unit >= n_units) return;
+        f_k += BK;
+        if (f_k >= a.k) {
+            ++f_unit;
+            fill_setup();
+        }
+    };
+    // This wave's pieces that straddle the end of the rows, of a stage that has
+    // landed: what lies behind a row must not meet the other operand's zeros.
+    auto cut_off = [&](int slot, int left) {
+        if (left >= BK || left % 16 == 0) return;
+        auto cut = [&](uint8_t* at, int first) {
+            if (first < left && left < first + 16) {
+                u32x4* const p = reinterpret_cast<u32x4*>(at + lane * 16);
+                *p = keep_bytes(*p, left - first);
+            }
+        };
+#pragma unroll
+        for (int q = 0; q < QA; ++q) cut(smem + slot * Cfg::A_STAGE + (wave * QA + q) * 1024, pos[q & 1]);
+#pragma unroll
+        for (int q = 0; q < QB; ++q) cut(smem + Cfg::B_REGION + slot * Cfg::B_STAGE + (wave * QB + q) * 1024, pos[q & 1]);
+    };
+
+    // Fragment reads (groups_dma.hpp): 16-byte chunks kb and 4 + kb of a row.
+    const int kb = kgroup16(lane >> 4), g4 = lane >> 4, j16 = lane & 15;
+    uint32_t a_off[2], b_off[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int ra = wm * Cfg::WTM + j16, rb = wn * Cfg::WTN + j16;
+        a_off[h] = (uint32_t)(ra * BK + 16 * ((4 * h + kb) ^ a_swizzle<128>(ra)));
+        b_off[h] = (uint32_t)(Cfg::B_REGION + rb * BK + 16 * ((4 * h + kb) ^ a_swizzle<128>(rb)));
+    }
+    auto fragment = [&](const uint8_t* stage, const uint32_t (&off)[2], int block) {
+        const u32x4 lo = *reinterpret_cast<const u32x4*>(stage + off[0] + block * 16 * BK);
+        const u32x4 hi = *reinterpret_cast<const u32x4*>(stage + off[1] + block * 16 * BK);
+        return int32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    };
+
+    fill_setup();
+#pragma unroll 1
+    for (int s = 0; s < S; ++s) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) dma(s, q);
+        fill_advance();
+    }
+    int slot = 0;
+    for (int c_unit = 0; c_unit < n_units; ++c_unit) {
+        const DmaUnit c = unit_at(c_unit);
+        floatx4 acc[FN][FM];
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = 0; k < a.k; k += BK) {
+            wait_vmcnt<(S - 1) * NQ>();
+            cut_off(slot, a.k - k);
+            lds_barrier();
+            const uint8_t *sa = smem + slot * Cfg::A_STAGE, *sb = smem + slot * Cfg::B_STAGE;
+            const float* sc = reinterpret_cast<const float*>(smem + Cfg::S_REGION + slot * Cfg::S_STAGE);
+            int32x8_t w[FN];
+            floatx4 scale_w[B_ROWS ? FN : 1];
+#pragma unroll
+            for (int i = 0; i < FN; ++i) w[i] = fragment(sb, b_off, i);
+            if constexpr (B_ROWS) {
+#pragma unroll
+                for (int i = 0; i < FN; ++i) scale_w[i] = *reinterpret_cast<const floatx4*>(sc + BM + wn * Cfg::WTN + 16 * i + 4 * g4);
+            } else {
+                scale_w[0][0] = sc[BM + wn * Cfg::WTN];
+            }
+            // A row block's fragment is read while the one before is multiplied, and a
+            // block's product is added while the next LAG are computed.  (The empty
+            // assembly keeps the additions here; the compiler would move all of them,
+            // and the products they wait for, behind the step's last branch.)
+            constexpr int LAG = 3, NMF = FM * FN;
+            int32x8_t x[2];
+            float scale_x[2];
+            floatx4 t[LAG + 1];
+            x[0] = fragment(sa, a_off, 0);
+            scale_x[0] = sc[wm * Cfg::WTM + j16];
+#pragma unroll
+            for (int u = 0; u < NMF + LAG; ++u) {
+                if (u < NMF) {
+                    const int j = u / FN, i = u % FN;
+                    if (i == 0) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        if (j + 1 < FM) x[(j + 1) & 1] = fragment(sa, a_off, j + 1);
+                    }
+                    t[u % (LAG + 1)] = mfma_block<FB, FA>(w[i], x[j & 1]);
+                }
+                if (u >= LAG) {
+                    const int d = u - LAG, j = d / FN, i = d % FN;
+                    if (i == 0 && j + 1 < FM) scale_x[(j + 1) & 1] = sc[wm * Cfg::WTM + 16 * (j + 1) + j16];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[i][j][e] = __builtin_fmaf(t[d % (LAG + 1)][e], scale_x[j & 1] * scale_w[B_ROWS ? i : 0][B_ROWS ? e : 0], acc[i][j][e]);
+                    asm volatile("" : "+v"(acc[i][j]));
+                }
+            }
+            lds_barrier();
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) dma(slot, q);
+            fill_advance();
+            slot = (slot + 1) & (S - 1);
+        }
+        const int m_base = c.m0 + wm * Cfg::WTM, n_base = c.n0 + wn * Cfg::WTN;
+        uint8_t* const strip = smem + Cfg::STRIPS + wave * Cfg::STRIP;
+        if (a.bf16) store_strips<kBF16>(a.c, acc, strip, lane, m_base, n_base, c.m_end, a.n, a.relu != 0, a.c_vec);
+        else store_strips<kF16>(a.c, acc, strip, lane, m_base, n_base, c.m_end, a.n, a.relu != 0, a.c_vec);
+    }
+    wait_vmcnt<0>();   // no LDS DMA may outlive the workgroup
+}
+
+}  // namespace gemm_relu_hip

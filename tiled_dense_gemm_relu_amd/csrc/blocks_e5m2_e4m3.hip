@@ -1,0 +1,10 @@
+// The kernel instances of gemm_relu_blocks for A in e5m2 and B in e4m3.
+#include "blocks_instances.hpp"
+
+namespace gemm_relu_hip {
+const BlocksKernels& blocks_kernels_e5m2_e4m3()
+{
+    static const BlocksKernels t = make_blocks_table<kE5M2, kE4M3>();
+    return t;
+}
+}  // namespace gemm_relu_hip
