@@ -150,7 +150,7 @@ int gemm_relu_experts(const void* X, const void* W1, const float* scales1, const
                       const float* logits, int32_t* ids, float* weights, void* Y, int64_t tokens, int64_t N,
                       int64_t K, int64_t hidden, int64_t experts, int64_t top, int64_t ld1, int64_t ld2, int renormalize,
                       int dtype, int format, int b_layout, void* workspace, int64_t workspace_bytes, void* stream);
-int64_t gemm_relu_experts_workspace(int64_t tokens, int64_t N, int64_t hidden, int64_t top);
+int64_t gemm_relu_experts_workspace(int64_t tokens, int64_t N, int64_t hidden, int64_t experts, int64_t top, int b_layout);
 
 #ifdef __cplusplus
 }

@@ -1,7 +1,8 @@
 """Products of 8-bit floating-point matrices scaled by blocks of 128 (the C ABI in include/gemm_relu_blocks.h).
 
 ``quantize_blocks`` makes such matrices, ``gemm_relu_blocks`` multiplies them (dense, or grouped by expert),
-``gemm_relu_blocks_backward`` has the gradients of a layer that does.
+``gemm_relu_blocks_backward`` has the gradients of a layer that does.  ``gemm_relu_experts`` is a whole expert
+layer for a few tokens, with 16-bit or such 8-bit weights.
 As in binding.py this is argument marshalling only, with no fallback.
 
 A quantized matrix is a ``torch.float8_e4m3fn`` or ``torch.float8_e5m2`` tensor whose rows start at multiples
@@ -15,8 +16,8 @@ import functools
 import threading
 
 from . import binding
-from .binding import _check, _dtype_code, _stream_handle
-from .groups import _call, _check_shape, _check_tensor, _first, _new, _on, _workspace
+from .binding import B_KN, B_NK, _check, _stream_handle
+from .groups import _call, _check_layout, _check_shape, _check_tensor, _first, _new, _on, _workspace
 
 BLOCK = 128                # GEMM_RELU_BLOCK
 
@@ -47,6 +48,10 @@ def _library():
             lib.gemm_relu_blocks_backward.restype = ci
             lib.gemm_relu_blocks_backward_workspace.argtypes = [i64] * 3
             lib.gemm_relu_blocks_backward_workspace.restype = i64
+            lib.gemm_relu_experts.argtypes = [vp] * 9 + [i64] * 8 + [ci] * 4 + [vp, i64, vp]
+            lib.gemm_relu_experts.restype = ci
+            lib.gemm_relu_experts_workspace.argtypes = [i64] * 5 + [ci]
+            lib.gemm_relu_experts_workspace.restype = i64
             _lib = lib
     return _lib
 
@@ -68,6 +73,11 @@ def blocks_workspace_bytes(M: int, N: int, K: int, groups: int = 1) -> int:
 def blocks_backward_workspace_bytes(M: int, N: int, K: int) -> int:
     """Workspace of gemm_relu_blocks_backward for these sizes (host only)."""
     return _bytes("gemm_relu_blocks_backward_workspace", M, N, K)
+
+
+def experts_workspace_bytes(tokens: int, N: int, hidden: int, experts: int, top: int, b_layout: int = B_NK) -> int:
+    """Workspace of gemm_relu_experts for these sizes (host only)."""
+    return _bytes("gemm_relu_experts_workspace", tokens, N, hidden, experts, top, b_layout)
 
 
 def _formats():
@@ -290,3 +300,116 @@ def gemm_relu_blocks_backward(dc, c, xt, xt_scales, wt, wt_scales, relu: bool = 
           (dx.data_ptr() or 256) if need_dx else None, (dw.data_ptr() or 256) if need_dw else None, M, N, K, ldxt, ldwt,
           fmt, fx, fw, code, 1 if relu else 0, ws, ws_bytes, handle or None)
     return dx, dw
+
+
+@functools.lru_cache(maxsize=1)
+def _no_gradient():
+    import torch
+
+    class Experts(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w1, w2, logits, weights, call):
+            return call()
+
+        @staticmethod
+        def backward(ctx, dy):
+            raise NotImplementedError("gemm_relu: gemm_relu_experts has no gradient; call it under torch.no_grad()")
+
+    return Experts
+
+
+def gemm_relu_experts(x, w1, w2, logits=None, top=None, ids=None, weights=None, w1_scales=None, w2_scales=None,
+                      out=None, b_layout: int = B_NK, renormalize: bool = True, workspace=None, stream=None):
+    """A whole expert layer for up to 64 tokens: y[t] = sum_j weights[t, j] ReLU(x[t] @ W1[e]) @ W2[e], e = ids[t, j].
+
+    ``x`` (tokens, K), fp16 or bf16.  ``w1`` (experts, hidden, K) and ``w2`` (experts, N, hidden) with B_NK, or
+    (experts, K, hidden) and (experts, hidden, N) with B_KN, in x's dtype; or with B_NK 8-bit, with
+    ``w1_scales`` (experts, hidden/128, K/128) and ``w2_scales`` (experts, N/128, hidden/128) by tiles, counts
+    rounded up (quantize_blocks with tiles=True).
+
+    Either ``logits`` (tokens, experts) float32 and ``top``, up to 16: each token's ``top`` largest logits
+    (ties to the lowest index, -inf never), weighted by their softmax over the chosen (``renormalize``) or all
+    logits; a token with a logit of NaN or +inf gets a row of NaN.  Or ``ids`` (tokens, top) int32, ids outside
+    0 .. experts-1 skipped, and ``weights`` (tokens, top) float32.  Returns (y, ids, weights), y (tokens, N) in
+    x's dtype (``out`` if given).  There is no gradient: a backward pass is refused, and so is ``out`` where
+    gradients are on and an input requires one.
+    """
+    import torch
+    code, dev = _first("x", x)
+    _check_layout(b_layout)
+    nk = b_layout == B_NK
+    _check_tensor("x", x, 2, dev, x.dtype)
+    if not isinstance(w1, torch.Tensor) or not isinstance(w2, torch.Tensor):
+        raise TypeError("gemm_relu: w1 and w2 must be torch.Tensors")
+    eight = w1.dtype in _formats()
+    fmt, ld1, ld2 = -1, 0, 0
+    if eight:
+        if not nk:
+            raise ValueError("gemm_relu: 8-bit weights must be stored (out, in): b_layout=B_NK")
+        fmt, ld1 = _check_8bit("w1", w1, 3, dev)
+        fmt2, ld2 = _check_8bit("w2", w2, 3, dev)
+        if fmt2 != fmt:
+            raise TypeError(f"gemm_relu: w1 and w2 must have one format, got {w1.dtype} and {w2.dtype}")
+    else:
+        _check_tensor("w1", w1, 3, dev, x.dtype)
+        _check_tensor("w2", w2, 3, dev, x.dtype)
+    tokens, K = x.shape
+    experts, hidden = w1.shape[0], w1.shape[1 if nk else 2]
+    N = w2.shape[1 if nk else 2]
+    _check_shape("w1", w1, (experts, hidden, K) if nk else (experts, K, hidden))
+    _check_shape("w2", w2, (experts, N, hidden) if nk else (experts, hidden, N))
+    if eight:
+        _check_tensor("w1_scales", w1_scales, 3, dev, torch.float32)
+        _check_shape("w1_scales", w1_scales, (experts, _blocks(hidden), _blocks(K)))
+        _check_tensor("w2_scales", w2_scales, 3, dev, torch.float32)
+        _check_shape("w2_scales", w2_scales, (experts, _blocks(N), _blocks(hidden)))
+    elif w1_scales is not None or w2_scales is not None:
+        raise ValueError("gemm_relu: scales are for 8-bit weights")
+    routed = logits is not None
+    if routed:
+        if ids is not None or weights is not None:
+            raise ValueError("gemm_relu: give logits and top, or ids and weights")
+        if top is None:
+            raise ValueError("gemm_relu: logits need top")
+        _check_tensor("logits", logits, 2, dev, torch.float32)
+        _check_shape("logits", logits, (tokens, experts))
+    else:
+        if ids is None or weights is None or top is not None:
+            raise ValueError("gemm_relu: give logits and top, or ids and weights")
+        _check_tensor("ids", ids, 2, dev, torch.int32)
+        top = ids.shape[1]
+        _check_shape("ids", ids, (tokens, top))
+        _check_tensor("weights", weights, 2, dev, torch.float32)
+        _check_shape("weights", weights, (tokens, top))
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, w1, w2, logits, weights)):
+        if out is not None:
+            raise RuntimeError("gemm_relu: out= has no gradient, but an input requires one: leave out= away, or call "
+                               "under torch.no_grad()")
+
+        chosen = []
+
+        def call():
+            y, *rest = gemm_relu_experts(x, w1, w2, logits, top if routed else None, ids, weights, w1_scales, w2_scales,
+                                         None, b_layout, renormalize, workspace, stream)
+            chosen.extend(rest)
+            return y
+        with _on(stream, dev):
+            y = _no_gradient().apply(x, w1, w2, logits, weights, call)
+        return (y, *chosen)
+    need = experts_workspace_bytes(tokens, N, hidden, experts, top, b_layout)
+    if routed:
+        with _on(stream, dev):
+            ids = torch.empty((tokens, top), dtype=torch.int32, device=x.device)
+            weights = torch.empty((tokens, top), dtype=torch.float32, device=x.device)
+    if out is None:
+        out = _new((tokens, N), x, stream)
+    else:
+        _check_tensor("out", out, 2, dev, x.dtype)
+        _check_shape("out", out, (tokens, N))
+    handle = _stream_handle(stream, dev)
+    ws, ws_bytes, keep = _workspace(workspace, need, x, dev, handle, stream)
+    _call(_library().gemm_relu_experts, dev, x.data_ptr(), w1.data_ptr(), w1_scales.data_ptr() if eight else None,
+          w2.data_ptr(), w2_scales.data_ptr() if eight else None, logits.data_ptr() if routed else None,
+          ids.data_ptr(), weights.data_ptr(), out.data_ptr(), tokens, N, K, hidden, experts, top, ld1, ld2,
+          1 if renormalize else 0, code, fmt, b_layout, ws, ws_bytes, handle or None)
+    return out, ids, weights

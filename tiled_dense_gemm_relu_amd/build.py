@@ -27,7 +27,8 @@ ARCH = "gfx950"
 SOURCES = ["gemm_relu_api.hip", "kernels_f16.hip", "kernels_bf16.hip", "groups_api.hip", "groups_f16.hip",
            "groups_bf16.hip", "groups_staged_f16_even.hip", "groups_staged_f16_odd.hip", "groups_staged_bf16_even.hip",
            "groups_staged_bf16_odd.hip", "blocks_api.hip", "blocks_quantize.hip", "blocks_e4m3_e4m3.hip",
-           "blocks_e4m3_e5m2.hip", "blocks_e5m2_e4m3.hip", "blocks_e5m2_e5m2.hip"]
+           "blocks_e4m3_e5m2.hip", "blocks_e5m2_e4m3.hip", "blocks_e5m2_e5m2.hip", "experts_f16.hip",
+           "experts_bf16.hip"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",

@@ -102,6 +102,44 @@ struct BackwardSpace {
     }
 };
 
+// The expert layer: columns of a unit, parts of its second product's K, and places in
+// the workspace.
+struct ExpertsSpace {
+    int wide1, wide2;      // index into kExpertBlocks
+    int64_t blocks1, blocks2, splits, mid_row, mid, part, bytes;
+    ExpertsSpace(int64_t tokens, int64_t n, int64_t hidden, int64_t experts, int64_t top, int b_layout)
+    {
+        const int64_t slots = tokens * top, used = std::min(experts, slots);
+        const auto wide = [&](int64_t out) {
+            return b_layout == GEMM_RELU_B_KN || used * ceil_div(out, 64) >= 512 || ceil_div(out, 16) > kMaxColumnBlocks;
+        };
+        wide1 = wide(hidden);
+        wide2 = wide(n);
+        blocks1 = ceil_div(hidden, 16 * kExpertBlocks[wide1]);
+        blocks2 = ceil_div(n, 16 * kExpertBlocks[wide2]);
+        const int64_t units = used * blocks2;
+        splits = units == 0 ? 1 : std::max<int64_t>(1, std::min<int64_t>(512 / units, blocks_of(hidden) / kPiecesAPart));
+        mid_row = round_up(hidden, 8);
+        mid = GEMM_RELU_GROUPS_COUNTER_BYTES;
+        part = mid + round_up(4 * slots * mid_row, 256);
+        bytes = part + round_up(4 * slots * splits * n, 256);
+    }
+    // A counter for each column block; pieces of K for the 8 waves of each part.
+    static constexpr int64_t kMaxColumnBlocks = GEMM_RELU_GROUPS_COUNTER_BYTES / 4, kPiecesAPart = 8;
+};
+static_assert(((int64_t(1) << 20) + 63) / 64 <= ExpertsSpace::kMaxColumnBlocks, "a counter for each block of 64 columns");
+
+int check_experts(int64_t tokens, int64_t n, int64_t hidden, int64_t experts, int64_t top, int b_layout)
+{
+    if (b_layout != GEMM_RELU_B_KN && b_layout != GEMM_RELU_B_NK) return GEMM_RELU_ERR_BAD_LAYOUT;
+    const int rc = check_dims({tokens, n, hidden});
+    if (rc != GEMM_RELU_OK) return rc;
+    if (experts < 1 || top < 1 || top > experts) return GEMM_RELU_ERR_INVALID_ARG;
+    if (tokens > kMaxTokens || experts > kMaxExperts || top > kMaxTop) return GEMM_RELU_ERR_TOO_LARGE;
+    // the intermediate has one descriptor
+    return 4 * tokens * top * round_up(hidden, 8) > INT32_MAX ? GEMM_RELU_ERR_TOO_LARGE : GEMM_RELU_OK;
+}
+
 }  // namespace
 }  // namespace gemm_relu_hip
 
@@ -245,6 +283,95 @@ int gemm_relu_blocks_backward(const void* dC, const void* C, const void* XT, con
         rc = launch_blocks(a, format, format_x, GEMM_RELU_SCALES_ROWS, GEMM_RELU_BLOCKS_AUTO, cus, s);
     }
     return rc;
+}
+
+int64_t gemm_relu_experts_workspace(int64_t tokens, int64_t N, int64_t hidden, int64_t experts, int64_t top, int b_layout)
+{
+    const int rc = check_experts(tokens, N, hidden, experts, top, b_layout);
+    return rc != GEMM_RELU_OK ? rc : ExpertsSpace(tokens, N, hidden, experts, top, b_layout).bytes;
+}
+
+int gemm_relu_experts(const void* X, const void* W1, const float* scales1, const void* W2, const float* scales2,
+                      const float* logits, int32_t* ids, float* weights, void* Y, int64_t tokens, int64_t N,
+                      int64_t K, int64_t hidden, int64_t experts, int64_t top, int64_t ld1, int64_t ld2, int renormalize,
+                      int dtype, int format, int b_layout, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    if (dtype != GEMM_RELU_F16 && dtype != GEMM_RELU_BF16) return GEMM_RELU_ERR_BAD_DTYPE;
+    if (format != -1 && !known_format(format)) return GEMM_RELU_ERR_BAD_DTYPE;
+    const int64_t need = gemm_relu_experts_workspace(tokens, N, hidden, experts, top, b_layout);
+    if (need < 0) return (int)need;
+    int rc = check_dims({K});
+    if (rc != GEMM_RELU_OK) return rc;
+    if (renormalize != 0 && renormalize != 1) return GEMM_RELU_ERR_INVALID_ARG;
+    const bool bytes = format != -1, kn = b_layout == GEMM_RELU_B_KN;
+    if (bytes) {
+        if (kn) return GEMM_RELU_ERR_BAD_LAYOUT;
+        if ((rc = check_pitch(ld1, K)) != GEMM_RELU_OK || (rc = check_pitch(ld2, hidden)) != GEMM_RELU_OK) return rc;
+    }
+    if (tokens == 0) return GEMM_RELU_OK;
+    const int64_t slots = tokens * top;
+    const Span in[] = {{X, 2 * tokens * K},
+                       {W1, bytes ? read_bytes(experts * hidden, K, ld1) : 2 * experts * hidden * K},
+                       {W2, bytes ? read_bytes(experts * N, hidden, ld2) : 2 * experts * N * hidden}};
+    const Span words[] = {{logits, logits ? 4 * tokens * experts : 0},
+                          {bytes ? scales1 : nullptr, bytes ? 4 * experts * blocks_of(hidden) * blocks_of(K) : 0},
+                          {bytes ? scales2 : nullptr, bytes ? 4 * experts * blocks_of(N) * blocks_of(hidden) : 0},
+                          {ids, 4 * slots},
+                          {weights, 4 * slots}};
+    const Span out[] = {{Y, 2 * tokens * N}, {ids, 4 * slots}, {weights, 4 * slots}, {workspace, need}};
+    // (ids and weights are inputs without logits: then only Y and the workspace are written)
+    const Span written[] = {out[0], out[3]};
+    rc = check_spans(in, 3, words, 5, out, 1);
+    if (rc == GEMM_RELU_OK && logits) rc = check_spans(in, 3, words, 3, out, 3);
+    if (rc == GEMM_RELU_OK && bytes && ((in[1].bytes && !aligned(W1, 16)) || (in[2].bytes && !aligned(W2, 16)))) rc = GEMM_RELU_ERR_MISALIGNED;
+    if (rc == GEMM_RELU_OK) rc = check_workspace(workspace, workspace_bytes, need);
+    if (rc == GEMM_RELU_OK) rc = check_spans(in, 3, words, 5, written, 2);
+    if (rc != GEMM_RELU_OK) return rc;
+    int cus = 0;
+    if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const ExpertsSpace space(tokens, N, hidden, experts, top, b_layout);
+    char* const ws = static_cast<char*>(workspace);
+    const int store = bytes ? 2 + format : kn ? 1 : 0;
+    const ExpertsKernels& kernels = dtype == GEMM_RELU_F16 ? experts_kernels_f16() : experts_kernels_bf16();
+    const auto even = [](const void* p, int64_t row) { return row % 2 == 0 && aligned(p, 4); };
+    const int64_t used = std::min(experts, slots);
+    ExpertsArgs a{};
+    a.x = static_cast<const uint16_t*>(X);
+    a.w = static_cast<const uint8_t*>(W1);
+    a.scales = scales1;
+    a.logits = logits;
+    a.ids = ids;
+    a.weights = weights;
+    a.mid = reinterpret_cast<uint16_t*>(ws + space.mid);
+    a.part = reinterpret_cast<float*>(ws + space.part);
+    a.counters = reinterpret_cast<int*>(ws);
+    a.y = static_cast<uint16_t*>(Y);
+    a.ld = bytes ? ld1 : 2 * (kn ? hidden : K);
+    a.tokens = (int)tokens;
+    a.in = (int)K;
+    a.out = (int)hidden;
+    a.experts = (int)experts;
+    a.top = (int)top;
+    a.mid_row = (int)space.mid_row;
+    a.renormalize = renormalize;
+    a.routed = logits != nullptr;
+    a.splits = 1;
+    void* args[] = {&a};
+    const auto grid = [&](int64_t units) { return dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(units, 2 * cus))); };
+    const bool odd1 = !even(X, K) || (!bytes && !(kn ? even(W1, hidden) : even(W1, K)));
+    rc = enqueue(kernels.products[store][odd1][0][space.wide1], grid(used * space.blocks1), kExpertThreads, args, s);
+    if (rc != GEMM_RELU_OK || N == 0) return rc;
+    a.x = a.mid;
+    a.w = static_cast<const uint8_t*>(W2);
+    a.scales = scales2;
+    a.logits = nullptr;              // the first launch has written its choices
+    a.ld = bytes ? ld2 : 2 * (kn ? N : hidden);
+    a.in = (int)hidden;
+    a.out = (int)N;
+    a.splits = (int)space.splits;
+    const bool odd2 = !bytes && !(kn ? even(W2, N) : even(W2, hidden));
+    return enqueue(kernels.products[store][odd2][1][space.wide2], grid(used * space.blocks2 * space.splits), kExpertThreads, args, s);
 }
 
 }  // extern "C"

@@ -12,6 +12,7 @@
 // its column's tile, so both forms look alike in LDS.
 #pragma once
 
+#include "blocks_bytes.hpp"
 #include "groups_dma.hpp"
 #include "blocks_table.hpp"
 
@@ -96,17 +97,6 @@ __device__ __forceinline__ void store_strips(uint16_t* __restrict__ C, const flo
             }
         }
     }
-}
-
-// The first `valid` of 16 bytes, zeros after them.
-__device__ __forceinline__ u32x4 keep_bytes(u32x4 v, int valid)
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int left = valid - 4 * i;
-        v[i] = left >= 4 ? v[i] : left > 0 ? v[i] & (0xffffffffu >> (32 - 8 * left)) : 0u;
-    }
-    return v;
 }
 
 template <class Cfg, int FA, int FB, bool B_ROWS>

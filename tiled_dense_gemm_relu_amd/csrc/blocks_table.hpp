@@ -58,4 +58,33 @@ const BlocksKernels& blocks_kernels_e5m2_e5m2();
 // [dtype][format][form == tiles]
 const void* quantize_kernel(int dtype, int format, int tiles);
 
+// One of the two products of the expert layer for a few tokens.
+struct ExpertsArgs {
+    const uint16_t* x;     // first: (tokens, in); second: the first's `mid`
+    const uint8_t* w;      // (experts, out, ld) or (experts, in, ld) bytes
+    const float* scales;   // 8-bit weights: (experts, out blocks, in blocks)
+    const float* logits;   // (tokens, experts); nullptr: ids and weights are inputs
+    int* ids;              // (tokens, top)
+    float* weights;
+    uint16_t* mid;         // (tokens top, [high, low], mid_row)
+    float* part;           // second: (tokens top, splits, out)
+    int* counters;         // second: one for each block of columns
+    uint16_t* y;           // second: (tokens, out)
+    int64_t ld;            // bytes from a row of w to the next
+    int tokens, in, out, experts, top, mid_row;
+    int renormalize, routed, splits;
+};
+
+constexpr int kMaxTokens = 64, kMaxTop = 16, kMaxExperts = 1024, kExpertThreads = 512;
+// Columns of a unit, in blocks of 16.
+constexpr int kNumExpertBlocks = 2;
+constexpr int kExpertBlocks[kNumExpertBlocks] = {1, 4};
+
+struct ExpertsKernels {
+    // [storage: NK, KN, e4m3, e5m2][odd rows][second product][columns]; KN has 4 blocks only
+    const void* products[4][2][2][kNumExpertBlocks];
+};
+const ExpertsKernels& experts_kernels_f16();
+const ExpertsKernels& experts_kernels_bf16();
+
 }  // namespace gemm_relu_hip

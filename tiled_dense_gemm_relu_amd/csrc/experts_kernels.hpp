@@ -1,0 +1,502 @@
+// An expert layer for a few tokens (gemm_relu_blocks.h) in two launches: routing
+// and the first products, then the second products and their sum.
+//
+// With a few tokens the time is that of reading the chosen experts' weights, once.
+// Every workgroup makes the routing table for itself (tokens are few), so nothing
+// waits for it, and takes units of one expert and 16 NB output columns; its 8 waves
+// take pieces of 128 k in turn, straight from memory into registers, and add their
+// sums in LDS.  Up to 64 of an expert's rows share a pass over its weights.
+//
+// The first launch leaves weight * ReLU(sum) of every choice as a sum of two 16-bit
+// values, so that the second one's matrix instructions lose nothing of it.  The
+// second launch's units write a choice's products as fp32; the last unit of a column
+// block to end adds each token's in the order of its choices.
+#pragma once
+
+#include "blocks_bytes.hpp"
+#include "blocks_table.hpp"
+#include "groups_skinny.hpp"
+
+namespace gemm_relu_hip {
+
+constexpr int kExpertWaves = kExpertThreads / 64;
+constexpr int kMaxSlots = kMaxTokens * kMaxTop;
+
+// Who goes where: slot t top + j is token t's choice j.
+struct RouteTable {
+    int16_t ids[kMaxSlots];          // -1: none
+    uint16_t sorted[kMaxSlots];      // slots by expert, in order
+    uint16_t start[kMaxExperts];     // where an expert's slots begin in `sorted`
+    uint16_t used[kMaxExperts + 1];  // the experts that have slots
+    float weights[kMaxSlots];
+    int count[kMaxExperts];
+    int n_used;
+};
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    const int m = wave_scan((int)v, [](int a, int b) { return (int)max((uint32_t)a, (uint32_t)b); });
+    return (uint32_t)__builtin_amdgcn_readlane(m, 63);
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    return v;
+}
+
+// One token's choices by one wave: the largest logits, ties to the lowest index,
+// and their softmax weights; lane j gets choice j.  Logits are compared as unsigned
+// keys in their order; key 0 is never chosen (-inf, and what has been chosen).
+__device__ inline void choose(const float* __restrict__ logits, int experts, int top, bool renormalize, int lane, int& id,
+                              float& weight)
+{
+    constexpr int R = kMaxExperts / 64;
+    const int rounds = (experts + 63) / 64;
+    float l[R];
+    uint32_t key[R];
+    bool bad = false;
+    float largest = -__builtin_inff();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        key[r] = 0;
+        l[r] = -__builtin_inff();
+        if (r < rounds && 64 * r + lane < experts) {
+            l[r] = logits[64 * r + lane] + 0.0f;      // (-0 and +0 are equal)
+            const uint32_t bits = __builtin_bit_cast(uint32_t, l[r]);
+            bad |= !(l[r] < __builtin_inff());
+            key[r] = l[r] == -__builtin_inff() ? 0u : (bits & 0x80000000u) ? ~bits : bits | 0x80000000u;
+        }
+    }
+    id = -1;
+    weight = 0.0f;
+    if (__ballot(bad)) {
+        weight = __builtin_nanf("");
+        return;
+    }
+    float mine = 0.0f;
+    for (int j = 0; j < top; ++j) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (r < rounds) m = max(m, key[r]);
+        m = wave_max(m);
+        if (m == 0) break;
+        bool found = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (r >= rounds || found) continue;
+            const uint64_t at = __ballot(key[r] == m);
+            if (!at) continue;
+            found = true;
+            const int who = __builtin_ctzll(at);
+            const float value = __shfl(l[r], who);
+            if (j == 0) largest = value;
+            if (lane == who) key[r] = 0;
+            if (lane == j) {
+                id = 64 * r + who;
+                mine = value;
+            }
+        }
+    }
+    weight = id >= 0 ? expf(mine - largest) : 0.0f;
+    float total;
+    if (renormalize) {
+        total = wave_sum(weight);
+    } else {
+        total = 0.0f;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (r < rounds && l[r] != -__builtin_inff()) total += expf(l[r] - largest);
+        total = wave_sum(total);
+    }
+    if (id >= 0) weight /= total;
+}
+
+// The routing table, by the whole workgroup.  With logits the choices are made here
+// and, by the first workgroup, written.
+__device__ inline void make_table(RouteTable& t, const ExpertsArgs& a, int lane, int wave)
+{
+    const int slots = a.tokens * a.top, tid = threadIdx.x;
+    for (int e = tid; e < a.experts; e += kExpertThreads) t.count[e] = 0;
+    if (a.logits) {
+        for (int token = wave; token < a.tokens; token += kExpertWaves) {
+            int id;
+            float weight;
+            choose(a.logits + (size_t)token * (size_t)a.experts, a.experts, a.top, a.renormalize != 0, lane, id, weight);
+            if (lane < a.top) {
+                const int s = token * a.top + lane;
+                t.ids[s] = (int16_t)id;
+                t.weights[s] = weight;
+                if (blockIdx.x == 0) {
+                    a.ids[s] = id;
+                    a.weights[s] = weight;
+                }
+            }
+        }
+    } else {
+        for (int s = tid; s < slots; s += kExpertThreads) {
+            const int id = a.ids[s];
+            t.ids[s] = (int16_t)(id >= 0 && id < a.experts ? id : -1);
+            t.weights[s] = a.weights[s];
+        }
+    }
+    __syncthreads();
+    for (int s = tid; s < slots; s += kExpertThreads)
+        if (t.ids[s] >= 0) atomicAdd(&t.count[t.ids[s]], 1);
+    __syncthreads();
+    if (wave == 0) {
+        int before = 0, used = 0;
+        for (int e0 = 0; e0 < a.experts; e0 += 64) {
+            const int c = e0 + lane < a.experts ? t.count[e0 + lane] : 0, incl = wave_scan_sum(c);
+            const uint64_t some = __ballot(c > 0);
+            if (c > 0) {
+                t.start[e0 + lane] = (uint16_t)(before + incl - c);
+                t.used[used + __popcll(some & ((uint64_t(1) << lane) - 1))] = (uint16_t)(e0 + lane);
+            }
+            before += __builtin_amdgcn_readlane(incl, 63);
+            used += __popcll(some);
+        }
+        if (lane == 0) t.n_used = used;
+    }
+    __syncthreads();
+    for (int s = tid; s < slots; s += kExpertThreads) {
+        const int id = t.ids[s];
+        if (id < 0) continue;
+        int at = t.start[id];
+        for (int o = 0; o < s; ++o) at += t.ids[o] == id ? 1 : 0;
+        t.sorted[at] = (uint16_t)s;
+    }
+    __syncthreads();
+}
+
+// 8 weights of a lane from 8 bytes, as 16-bit values (exact).
+template <int DT, int FORMAT>
+__device__ __forceinline__ u32x4 widen(uint32_t lo, uint32_t hi)
+{
+    u32x4 r;
+    if constexpr (DT == kF16 && FORMAT == kE4M3) {
+        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false));
+        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true));
+        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false));
+        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true));
+    } else if constexpr (DT == kF16) {
+        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(lo, 1.0f, false));
+        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(lo, 1.0f, true));
+        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(hi, 1.0f, false));
+        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(hi, 1.0f, true));
+    } else if constexpr (FORMAT == kE4M3) {
+        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false));
+        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true));
+        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false));
+        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
+    } else {
+        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, false));
+        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, true));
+        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, false));
+        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, true));
+    }
+    return r;
+}
+
+// Storage of the weights: 16-bit (out, in) or (in, out) in X's dtype, or 8-bit (out, in).
+enum { kStoreNK = 0, kStoreKN = 1, kStoreE4M3 = 2, kStoreE5M2 = 3 };
+
+// A lane's weights of a piece, on their way: 16 columns x 128 k in NB blocks.
+//  NK: [block][k-step] 8 consecutive k of column 16 block + lane % 16.
+//  KN: [k-step][k] 4 consecutive columns 4 (lane % 16) .. of k-step's k 8 kb .., and
+//      with ODD the dword after them.
+//  8-bit: [block][half] 16 consecutive k.
+template <int STORE, bool ODD, int NB>
+struct PieceWeights;
+template <bool ODD, int NB>
+struct PieceWeights<kStoreNK, ODD, NB> {
+    SkinnyChunk<ODD> v[NB][4];
+};
+template <bool ODD>
+struct PieceWeights<kStoreKN, ODD, 4> {
+    u32x2 v[4][8];
+    uint32_t next[ODD ? 4 : 1][ODD ? 8 : 1];
+};
+template <bool ODD, int NB>
+struct PieceWeights<kStoreE4M3, ODD, NB> {
+    u32x4 v[NB][2];
+};
+template <bool ODD, int NB>
+struct PieceWeights<kStoreE5M2, ODD, NB> : PieceWeights<kStoreE4M3, ODD, NB> {};
+
+// The sums over pieces p0 + wave, p0 + wave + 8, .. of a unit's NB x MB blocks.
+//  Rows: lane's row of block j is x_off[j] bytes into rx (kOobOffset: none); with
+//  SPLIT_X also its low parts, x_low bytes on.
+template <int DT, int STORE, bool ODD, bool SPLIT_X, int NB, int MB>
+__device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsrc& rx, const uint32_t (&x_off)[MB], uint32_t x_low,
+                                            const uint8_t* w, const float* scales, int64_t ld, int n0, int in, int out,
+                                            int p0, int p1, int wave, int lane)
+{
+    constexpr bool WIDE = STORE >= kStoreE4M3, ODD_X = ODD && !SPLIT_X;
+    constexpr int KU = NB == 1 && MB == 1 ? 4 : WIDE && MB == 1 ? 2 : 1;     // pieces in flight
+    const int r16 = lane & 15, g = lane >> 4;
+    const int cols = min(16 * NB, out - n0);
+    // NK and 8-bit: rows n0 .. of the expert's weights
+    AnyRsrc rw{};
+    if constexpr (STORE == kStoreNK) rw = make_any_rsrc(reinterpret_cast<const uint16_t*>(w + (size_t)n0 * (size_t)ld), (uint32_t)cols * (uint32_t)ld);
+    if constexpr (WIDE) rw.rsrc = make_rsrc(w + (size_t)n0 * (size_t)ld, (uint32_t)cols * (uint32_t)ld);
+    // 8 k of step s of piece p: 8-bit weights have 16 consecutive ones a lane.
+    auto first_k = [&](int p, int s) { return p * kBlock + (WIDE ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g); };
+    auto load_x = [&](int p, int s, SkinnyChunk<ODD_X>& high, SkinnyChunk<ODD_X>& low, int j) {
+        const int k = first_k(p, s);
+        const uint32_t off = p < p1 && x_off[j] != kOobOffset && k < in ? x_off[j] + (uint32_t)k * 2u : kOobOffset;
+        high = load_skinny<ODD_X>(rx, off);
+        if constexpr (SPLIT_X) low = load_skinny<ODD_X>(rx, off == kOobOffset ? kOobOffset : off + x_low);
+    };
+    for (int i0 = p0 + wave; i0 < p1; i0 += KU * kExpertWaves) {
+        PieceWeights<STORE, ODD, NB> pw[KU];
+        // Rows of X: with one block all of a piece's are in flight with its weights; with
+        // more each step's are read when it comes (from L2, and too many to keep).
+        SkinnyChunk<ODD_X> x[MB == 1 ? KU : 1][MB][4], low[SPLIT_X && MB == 1 ? KU : 1][SPLIT_X ? MB : 1][4];
+        float scale[KU];
+#pragma unroll
+        for (int q = 0; q < KU; ++q) {
+            const int p = i0 + q * kExpertWaves, k0 = p * kBlock;
+            const bool live = p < p1;
+            if constexpr (STORE == kStoreNK) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        pw[q].v[i][s] = load_skinny<ODD>(rw, live ? (uint32_t)(16 * i + r16) * (uint32_t)ld + (uint32_t)(k0 + 32 * s + 8 * g) * 2u : kOobOffset);
+            } else if constexpr (STORE == kStoreKN) {
+                const int k1 = live ? min(k0, in) : 0;
+                const AnyRsrc rp = make_any_rsrc(reinterpret_cast<const uint16_t*>(w) + (size_t)k1 * (size_t)out + n0,
+                                                 live ? (uint32_t)(max(0, min(kBlock, in - k1)) * (int64_t)out - n0) * 2u : 0u);
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t off = 4 * r16 < cols ? ((uint32_t)(32 * s + 8 * g + e) * (uint32_t)out + 4u * (uint32_t)r16) * 2u : kOobOffset;
+                        if constexpr (ODD) {
+                            const uint32_t at = (off + rp.shift) & ~3u;
+                            pw[q].v[s][e] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rp.rsrc, at, 0, 0));
+                            pw[q].next[s][e] = __builtin_amdgcn_raw_buffer_load_b32(rp.rsrc, at + 8u, 0, 0);
+                        } else {
+                            pw[q].v[s][e] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rp.rsrc, off, 0, 0));
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int k = k0 + 64 * h + 16 * g;
+                        pw[q].v[i][h] = __builtin_amdgcn_raw_buffer_load_b128(rw.rsrc, live && k < in ? (uint32_t)(16 * i + r16) * (uint32_t)ld + (uint32_t)k : kOobOffset, 0, 0);
+                    }
+                scale[q] = live ? scales[p] : 0.0f;
+            }
+            if constexpr (MB == 1) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) load_x(p, s, x[q][0][s], low[SPLIT_X ? q : 0][0][s], 0);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < KU; ++q) {
+            const int p = i0 + q * kExpertWaves, k0 = p * kBlock;
+            if (p >= p1) break;
+            const bool tail = k0 + kBlock > in;
+            floatx4 sum[WIDE ? NB : 1][WIDE ? MB : 1];
+            if constexpr (WIDE) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int j = 0; j < MB; ++j) sum[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int k = first_k(p, s), valid = in - k;
+                constexpr int QX = MB == 1 ? 1 : 0;
+                if constexpr (MB > 1) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int j = 0; j < MB; ++j) load_x(p, s, x[0][j][0], low[0][SPLIT_X ? j : 0][0], j);
+                }
+                u32x4 wv[NB];
+                if constexpr (STORE == kStoreNK) {
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        wv[i] = skinny_value<ODD>(pw[q].v[i][s], rw, (uint32_t)(16 * i + r16) * (uint32_t)ld + (uint32_t)k * 2u);
+                        if (tail) wv[i] = keep_first(wv[i], valid);
+                    }
+                } else if constexpr (STORE == kStoreKN) {
+                    // [k] x 4 columns -> [column] x 8 k
+                    const uint32_t base = (uint32_t)((uintptr_t)(reinterpret_cast<const uint16_t*>(w) + (size_t)k0 * (size_t)out + n0)) & 2u;
+                    u32x2 row[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        row[e] = pw[q].v[s][e];
+                        if constexpr (ODD) {
+                            const uint32_t off = ((uint32_t)(32 * s + 8 * g + e) * (uint32_t)out + 4u * (uint32_t)r16) * 2u + base;
+                            const uint32_t bits = (off & 2u) * 8u;
+                            row[e] = u32x2{__builtin_amdgcn_alignbit(row[e].y, row[e].x, bits), __builtin_amdgcn_alignbit(pw[q].next[s][e], row[e].y, bits)};
+                        }
+                        if (tail && e >= valid) row[e] = u32x2{0u, 0u};
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int h = 0; h < 4; ++h)
+                            wv[c][h] = __builtin_amdgcn_perm(row[2 * h + 1][c >> 1], row[2 * h][c >> 1], (c & 1) ? 0x07060302u : 0x05040100u);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        u32x2 b{pw[q].v[i][s >> 1][2 * (s & 1)], pw[q].v[i][s >> 1][2 * (s & 1) + 1]};
+                        if (tail) {
+                            const u32x4 kept = keep_bytes(u32x4{b.x, b.y, 0u, 0u}, valid);
+                            b = u32x2{kept[0], kept[1]};
+                        }
+                        wv[i] = widen<DT, STORE == kStoreE4M3 ? kE4M3 : kE5M2>(b.x, b.y);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < MB; ++j) {
+                    u32x4 xv = skinny_value<ODD_X>(x[QX * q][j][QX * s], rx, x_off[j] + (uint32_t)k * 2u);
+                    if (tail) xv = keep_first(xv, valid);
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        floatx4& to = WIDE ? sum[i][j] : acc[i][j];
+                        to = mfma_16x16x32<DT>(wv[i], xv, to);
+                    }
+                    if constexpr (SPLIT_X) {
+                        u32x4 lv = low[QX * q][j][QX * s].v;
+                        if (tail) lv = keep_first(lv, valid);
+#pragma unroll
+                        for (int i = 0; i < NB; ++i) {
+                            floatx4& to = WIDE ? sum[i][j] : acc[i][j];
+                            to = mfma_16x16x32<DT>(wv[i], lv, to);
+                        }
+                    }
+                }
+            }
+            if constexpr (WIDE) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int j = 0; j < MB; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(scale[q], sum[i][j][e], acc[i][j][e]);
+            }
+        }
+    }
+}
+
+template <int DT, int STORE, bool ODD, bool SECOND, int NB>
+__global__ __launch_bounds__(kExpertThreads, 2) void expert_products(ExpertsArgs a)
+{
+    constexpr int COLS = 16 * NB, PART = COLS * 17;
+    __shared__ RouteTable t;
+    __shared__ float part[kExpertWaves * PART];
+    __shared__ int before;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tid = threadIdx.x;
+    const int r16 = lane & 15, g = lane >> 4;
+    make_table(t, a, lane, wave);
+    const int blocks_n = (a.out + COLS - 1) / COLS, pieces = (a.in + kBlock - 1) / kBlock;
+    const int used = __builtin_amdgcn_readfirstlane(t.n_used);
+    const int units = used * blocks_n * a.splits;
+    // Where column c of a unit's block i sits in its rows of LDS: (K, N) weights give a
+    // lane 4 neighbouring columns, one in each block.
+    auto column = [](int c) { return STORE == kStoreKN ? (c & 3) * 16 + (c >> 2) : c; };
+
+    // Rows of tokens without a choice, where no unit would write them; with logits that
+    // cannot be ranked the row is NaN.
+    auto row_without = [&](int token) {
+        return a.routed && t.ids[token * a.top] < 0 && t.weights[token * a.top] != t.weights[token * a.top] ? __builtin_nanf("") : 0.0f;
+    };
+    if (SECOND && used == 0) {
+        for (int64_t i = (int64_t)blockIdx.x * kExpertThreads + tid; i < (int64_t)a.tokens * a.out; i += (int64_t)gridDim.x * kExpertThreads)
+            a.y[i] = act_cast<DT>(row_without((int)(i / a.out)), false);
+        return;
+    }
+    const AnyRsrc rx = make_any_rsrc(a.x, SECOND ? (uint32_t)(a.tokens * a.top) * (uint32_t)a.mid_row * 4u : (uint32_t)a.tokens * (uint32_t)a.in * 2u);
+    for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int nb = unit % blocks_n, rest = unit / blocks_n, split = rest % a.splits, u = rest / a.splits;
+        const int expert = __builtin_amdgcn_readfirstlane(t.used[u]), n0 = nb * COLS;
+        const int first = __builtin_amdgcn_readfirstlane(t.start[expert]), count = __builtin_amdgcn_readfirstlane(t.count[expert]);
+        const uint8_t* w = a.w + (size_t)expert * (size_t)(STORE == kStoreKN ? a.in : a.out) * (size_t)a.ld;
+        const float* scales = STORE >= kStoreE4M3
+                                  ? a.scales + ((size_t)expert * (size_t)((a.out + kBlock - 1) / kBlock) + (size_t)(n0 / kBlock)) * (size_t)pieces
+                                  : nullptr;
+        const int p0 = (int)((int64_t)pieces * split / a.splits), p1 = (int)((int64_t)pieces * (split + 1) / a.splits);
+        auto pass = [&](auto blocks, int row0) __attribute__((always_inline)) {
+            constexpr int MB = decltype(blocks)::value;
+            floatx4 acc[NB][MB];
+            uint32_t x_off[MB];
+#pragma unroll
+            for (int j = 0; j < MB; ++j) {
+                const int r = row0 + 16 * j + r16;
+                const int slot = t.sorted[first + min(r, count - 1)];
+                x_off[j] = r >= count ? kOobOffset : SECOND ? (uint32_t)slot * (uint32_t)a.mid_row * 4u : (uint32_t)(slot / a.top) * (uint32_t)a.in * 2u;
+#pragma unroll
+                for (int i = 0; i < NB; ++i) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+            expert_sums<DT, STORE, ODD, SECOND, NB, MB>(acc, rx, x_off, (uint32_t)a.mid_row * 2u, w, scales, a.ld, n0, a.in, a.out, p0, p1, wave, lane);
+#pragma unroll
+            for (int j = 0; j < MB; ++j) {
+                if (row0 + 16 * j >= count) break;
+                __syncthreads();       // the sums of the block before are read
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) part[wave * PART + (16 * i + 4 * g + e) * 17 + r16] = acc[i][j][e];
+                __syncthreads();
+                for (int o = tid; o < 16 * COLS; o += kExpertThreads) {
+                    const int row = o / COLS, c = o % COLS, r = row0 + 16 * j + row;
+                    if (r >= count || n0 + c >= a.out) continue;
+                    float z = 0.0f;
+#pragma unroll
+                    for (int v = 0; v < kExpertWaves; ++v) z += part[v * PART + column(c) * 17 + row];
+                    const int slot = t.sorted[first + r];
+                    if constexpr (SECOND) {
+                        __hip_atomic_store(a.part + ((size_t)slot * (size_t)a.splits + (size_t)split) * (size_t)a.out + (size_t)(n0 + c), z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    } else {
+                        const float h = t.weights[slot] * (z > 0.0f ? z : 0.0f);
+                        const uint16_t hi = act_cast<DT>(h, false);
+                        const float back = to_float<DT>(hi);
+                        const uint16_t lo = __builtin_fabsf(back) < __builtin_inff() ? act_cast<DT>(h - back, false) : (uint16_t)0;
+                        uint16_t* const to = a.mid + (size_t)slot * (size_t)a.mid_row * 2 + (size_t)(n0 + c);
+                        to[0] = hi;
+                        to[a.mid_row] = lo;
+                    }
+                }
+            }
+        };
+        if (count <= 16) {
+            pass(std::integral_constant<int, 1>{}, 0);
+        } else {
+            for (int row0 = 0; row0 < count; row0 += 64) pass(std::integral_constant<int, 4>{}, row0);
+        }
+        if constexpr (SECOND) {
+            wait_vmcnt<0>();           // this wave's sums have reached device scope
+            __syncthreads();
+            if (tid == 0) before = __hip_atomic_fetch_add(a.counters + nb, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __syncthreads();
+            if (before == used * a.splits - 1) {
+                asm volatile("" ::: "memory");   // the loads below stay after the count that allowed them
+                for (int o = tid; o < a.tokens * COLS; o += kExpertThreads) {
+                    const int token = o / COLS, c = n0 + o % COLS;
+                    if (c >= a.out) continue;
+                    float z = row_without(token);
+                    for (int j = 0; j < a.top; ++j) {
+                        const int slot = token * a.top + j;
+                        if (t.ids[slot] < 0) continue;
+                        for (int s = 0; s < a.splits; ++s)
+                            z += __hip_atomic_load(a.part + ((size_t)slot * (size_t)a.splits + (size_t)s) * (size_t)a.out + (size_t)c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    }
+                    a.y[(size_t)token * (size_t)a.out + (size_t)c] = act_cast<DT>(z, false);
+                }
+                if (tid == 0) __hip_atomic_store(a.counters + nb, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace gemm_relu_hip
