@@ -26,7 +26,7 @@
  * and errors are negative codes.  16-bit matrices need 2-byte alignment, fp32
  * and int32 arrays 4-byte.
  *
- * Workspace.  As in gemm_relu_groups.h: device memory of at least the bytes that
+ * Workspace.  As in gemm_relu_groups.h (gemm_relu_blocks needs none): device memory of at least the bytes that
  * the *_workspace function returns for the same arguments, 256-byte aligned, its
  * first GEMM_RELU_GROUPS_COUNTER_BYTES zero before the first use and left zero by
  * every call; one buffer serves all calls of one stream, of both headers.
@@ -60,7 +60,7 @@ enum {
     GEMM_RELU_BLOCKS_256 = 0,     /* 256x256 tiles, LDS DMA */
     GEMM_RELU_BLOCKS_128 = 1,     /* 128x128 tiles */
     GEMM_RELU_BLOCKS_64 = 2,      /* 64x64 tiles */
-    GEMM_RELU_BLOCKS_STREAM = 3   /* few rows a group: weights streamed into registers */
+    GEMM_RELU_BLOCKS_STREAM = 3   /* few rows a group, or few operations: 16 to 64 rows x 32 or 64 columns, K cut over waves */
 };
 
 /*
@@ -102,9 +102,7 @@ int gemm_relu_quantize_blocks(const void* X, const void* mask, void* Q, float* s
  */
 int gemm_relu_blocks(const void* A, const float* scales_a, const void* B, const float* scales_b, const int32_t* ends,
                      void* C, int64_t M, int64_t N, int64_t K, int64_t groups, int64_t lda, int64_t ldb, int format_a,
-                     int format_b, int form_b, int dtype, int relu, int config_id, void* workspace,
-                     int64_t workspace_bytes, void* stream);
-int64_t gemm_relu_blocks_workspace(int64_t M, int64_t N, int64_t K, int64_t groups);
+                     int format_b, int form_b, int dtype, int relu, int config_id, void* stream);
 
 /*
  * Gradients of C = act(X @ W^T), X (M, K), W (N, K), for C's gradient dC, both (M, N)

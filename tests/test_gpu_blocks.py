@@ -191,7 +191,7 @@ SHAPES = [(1, 1, 1), (1, 130, 16), (17, 64, 128), (64, 64, 256), (100, 200, 300)
 
 
 @pytest.mark.parametrize("shape", SHAPES)
-@pytest.mark.parametrize("config", [blocks.CONFIG_AUTO, blocks.CONFIG_256, blocks.CONFIG_128, blocks.CONFIG_64])
+@pytest.mark.parametrize("config", [blocks.CONFIG_AUTO, blocks.CONFIG_256, blocks.CONFIG_128, blocks.CONFIG_64, blocks.CONFIG_STREAM])
 @pytest.mark.parametrize("b_rows", [False, True])
 def test_product_exact_on_integers(shape, config, b_rows):
     # small integers times powers of two: every partial sum is exact in fp32
@@ -207,6 +207,32 @@ def test_product_exact_on_integers(shape, config, b_rows):
                                 out_dtype=dtype, b_rows=b_rows, config=config)
         want = (ref.clamp_min(0) if relu else ref).to(dtype)
         assert torch.equal(c.cpu(), want)
+
+
+@pytest.mark.parametrize("shape", [(5, 13000, 130), (3, 25003, 300), (20, 13000, 1100), (20, 26000, 129), (40, 13001, 257),
+                                   (64, 12500, 128), (200, 1700, 1040)])
+@pytest.mark.parametrize("b_rows", [False, True])
+def test_every_streaming_kernel(shape, b_rows):
+    # few rows, so many columns that workgroups of each size are chosen
+    M, N, K = shape
+    g = gen(M + N + K)
+    a = torch.randint(-2, 3, (M, K), generator=g).float().to(E5M2)
+    b = torch.randint(-2, 3, (N, K), generator=g).float().to(E4M3)
+    sa = torch.exp2(torch.randint(-1, 2, (nb(K), M), generator=g).float())
+    sb = torch.exp2(torch.randint(-1, 2, (nb(K), N) if b_rows else (nb(N), nb(K)), generator=g).float())
+    want = (stands_for(a, sa, False) @ stands_for(b, sb, not b_rows).t()).to(torch.bfloat16)
+    args = pitched(a), sa.to(DEV), pitched(b), sb.to(DEV)
+    for config in (blocks.CONFIG_AUTO, blocks.CONFIG_STREAM):
+        assert torch.equal(gr.gemm_relu_blocks(*args, relu=False, b_rows=b_rows, config=config).cpu(), want)
+    # the same as one group among empty ones, with a row of none
+    ends = torch.tensor([0, M - 1, M - 1], dtype=torch.int32, device=DEV)
+    stack = torch.zeros((3,) + tuple(args[2].shape[:1]) + (args[2].stride(0),), dtype=torch.uint8, device=DEV)[..., :K].view(E4M3)
+    stack[1] = args[2]
+    scales = torch.ones((3,) + tuple(args[3].shape), device=DEV)
+    scales[1] = args[3]
+    for config in (blocks.CONFIG_AUTO, blocks.CONFIG_STREAM):
+        c = gr.gemm_relu_blocks(args[0], args[1], stack, scales, ends=ends, relu=False, b_rows=b_rows, config=config).cpu()
+        assert torch.equal(c[: M - 1], want[: M - 1]) and (c[M - 1] == 0).all()
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -227,7 +253,7 @@ def test_product(shape, fa, fb, dtype):
 
 
 @pytest.mark.parametrize("sizes", [[0], [5], [0, 0, 7], [300, 0, 1, 17, 128, 0, 260], [1] * 70, [64] * 5 + [0] * 80 + [3]])
-@pytest.mark.parametrize("config", [blocks.CONFIG_AUTO, blocks.CONFIG_256, blocks.CONFIG_128, blocks.CONFIG_64])
+@pytest.mark.parametrize("config", [blocks.CONFIG_AUTO, blocks.CONFIG_256, blocks.CONFIG_128, blocks.CONFIG_64, blocks.CONFIG_STREAM])
 @pytest.mark.parametrize("b_rows", [False, True])
 def test_grouped(sizes, config, b_rows):
     G, N, K, spare = len(sizes), 200, 144, 9

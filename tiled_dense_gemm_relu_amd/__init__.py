@@ -31,7 +31,6 @@ from .blocks import (  # noqa: F401
     gemm_relu_blocks,
     gemm_relu_blocks_backward,
     gemm_relu_experts,
-    blocks_workspace_bytes,
     blocks_backward_workspace_bytes,
     experts_workspace_bytes,
 )

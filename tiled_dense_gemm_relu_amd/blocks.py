@@ -40,10 +40,8 @@ def _library():
             vp, i64, ci = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
             lib.gemm_relu_quantize_blocks.argtypes = [vp] * 6 + [i64] * 5 + [ci] * 4 + [vp]
             lib.gemm_relu_quantize_blocks.restype = ci
-            lib.gemm_relu_blocks.argtypes = [vp] * 6 + [i64] * 6 + [ci] * 6 + [vp, i64, vp]
+            lib.gemm_relu_blocks.argtypes = [vp] * 6 + [i64] * 6 + [ci] * 6 + [vp]
             lib.gemm_relu_blocks.restype = ci
-            lib.gemm_relu_blocks_workspace.argtypes = [i64] * 4
-            lib.gemm_relu_blocks_workspace.restype = i64
             lib.gemm_relu_blocks_backward.argtypes = [vp] * 8 + [i64] * 5 + [ci] * 5 + [vp, i64, vp]
             lib.gemm_relu_blocks_backward.restype = ci
             lib.gemm_relu_blocks_backward_workspace.argtypes = [i64] * 3
@@ -63,11 +61,6 @@ def _bytes(function: str, *args) -> int:
     if n < 0:
         _check(int(n))
     return n
-
-
-def blocks_workspace_bytes(M: int, N: int, K: int, groups: int = 1) -> int:
-    """Workspace of gemm_relu_blocks for these sizes (host only)."""
-    return _bytes("gemm_relu_blocks_workspace", M, N, K, groups)
 
 
 def blocks_backward_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -205,16 +198,15 @@ def _out_dtype(out, out_dtype):
 
 
 def gemm_relu_blocks(a, a_scales, b, b_scales, ends=None, out=None, out_dtype=None, relu: bool = True,
-                     b_rows: bool = False, config: int = CONFIG_AUTO, workspace=None, stream=None):
+                     b_rows: bool = False, config: int = CONFIG_AUTO, stream=None):
     """C = ReLU(A @ B^T) of the matrices that 8-bit ``a`` (M, K) and ``b`` (N, K) stand for.
 
     ``a_scales`` (K/128, M) by rows; ``b_scales`` (N/128, K/128) by tiles, or (K/128, N) with ``b_rows``;
     counts of blocks are rounded up.  With ``ends`` (groups,) int32 on the GPU, non-decreasing, ``b`` is
     (groups, N, K), its scales have groups in front, and row m of group g (rows ends[g-1] .. ends[g]-1) is
     multiplied with b[g]; rows past the last end get zeros.  ``relu=False`` leaves the ReLU out.  C (M, N) is
-    ``out`` if given, else a new tensor of ``out_dtype`` (bfloat16 by default).  ``workspace``: at least
-    blocks_workspace_bytes(...) bytes whose first 65536 are zero, or None for a cached one per stream.
-    ``config``: a kernel (CONFIG_*), by default the library's choice.
+    ``out`` if given, else a new tensor of ``out_dtype`` (bfloat16 by default).  ``config``: a
+    kernel (CONFIG_*), by default the library's choice.
     """
     import torch
     fa, lda = _check_8bit("a", a, 2)
@@ -241,10 +233,9 @@ def gemm_relu_blocks(a, a_scales, b, b_scales, ends=None, out=None, out_dtype=No
         _check_tensor("out", out, 2, dev, dtype)
         _check_shape("out", out, (M, N))
     handle = _stream_handle(stream, dev)
-    ws, ws_bytes, keep = _workspace(workspace, blocks_workspace_bytes(M, N, K, groups), a, dev, handle, stream)
     _call(_library().gemm_relu_blocks, dev, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(),
           ends.data_ptr() if grouped else None, out.data_ptr(), M, N, K, groups, lda, ldb, fa, fb, 0 if b_rows else 1,
-          code, 1 if relu else 0, config, ws, ws_bytes, handle or None)
+          code, 1 if relu else 0, config, handle or None)
     return out
 
 

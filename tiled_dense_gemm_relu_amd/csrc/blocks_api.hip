@@ -65,26 +65,71 @@ int64_t most_tiles(const BlocksArgs& a, int64_t tile)
     return std::min<int64_t>(a.m, a.m / tile + a.groups) * ceil_div(a.n, tile);
 }
 
-int blocks_config(const BlocksArgs& a)
-{
-    const int64_t used = std::min(a.groups, a.m), rows = a.m / used;
-    const auto tiles = [&](int64_t t) { return used * ceil_div(rows, t) * ceil_div(a.n, t); };
-    if (rows >= 192 && tiles(256) >= 192) return GEMM_RELU_BLOCKS_256;
-    if (rows >= 96 && tiles(128) >= 128) return GEMM_RELU_BLOCKS_128;
-    return GEMM_RELU_BLOCKS_64;
-}
+// Which kernel a product takes: a tile, or GEMM_RELU_BLOCKS_STREAM and which of the
+// streaming kernels (by kStreamRows).
+//  Streaming kernels by the workgroups they make: more rows a workgroup read the weights
+// fewer times, but some 200 workgroups are needed to fill the device; 8 waves where one
+// workgroup a CU is all there is, 4 where several share one.  Measured, us, kernels of
+// 16 rows x 32 (8 waves) / 16 x 64 (8) / 16 x 64 (4) / 32 x 64 (8) / 32 x 64 (4) / 64 x 64 (8),
+// then the 64 x 64 tile and the 128 tile:
+//   1 row, 4096 x 4096             8.1 /  9.2 / 11.7 /  9.7 / 12.3 / 11.5     14.7  23.9
+//   1 row, 1024 x 8192             9.4 / 11.2 / 14.2 / 12.7 / 18.2 / 15.8     22.8  40.9
+//   16 rows, 16384 x 8192         34.2 / 29.2 / 32.6 / 29.7 / 33.3 / 30.3     36.1  45.6
+//   32 rows, 16384 x 8192         53.8 / 48.0 / 35.0 / 30.5 / 34.7 / 31.0     36.3  46.4
+//   64 rows, 16384 x 8192         90.2 / 83.8 / 68.4 / 49.5 / 40.4 / 34.6     37.3  48.7
+//   64 rows, 4096 x 4096          13.4 /  9.5 / 12.2 / 11.0 / 13.3 / 14.3     15.0  25.3
+//   256, 1024 x 1024               9.5 /  6.9 /  7.0 /  7.8 /  8.1 /  9.4      8.6  12.0
+//   512, 1024 x 1024              15.7 / 10.7 /  8.1 /  7.9 /  8.3 /  9.5      8.7  12.2
+//   512, 2048 x 2048              31.8 / 20.9 / 16.4 / 14.4 / 12.0 / 11.7     11.3  17.8
+//   1024, 1024 x 1024             27.9 / 17.9 / 12.1 / 12.4 /  9.8 / 10.1      8.8  12.4
+//   64 in 64 groups, 2048 x 2048  78.5 / 60.8 / 50.4 / 62.7 / 49.5 / 66.5     58.3  53.2
+//   256 in 32, 1024 x 1024        19.9 / 14.4 / 11.1 / 14.4 / 11.5 / 15.3     11.7  12.3
+//   512 in 8, 2048 x 2048         33.8 / 22.6 / 17.5 / 17.5 / 13.9 / 15.5     11.7  17.6
+// Tiles: the largest whose tiles are mostly full and numerous enough to occupy the CUs.
+struct BlocksChoice {
+    int config, stream = -1;
+    BlocksChoice(int64_t m, int64_t n, int64_t groups, bool dense)
+    {
+        const int64_t used = std::min(groups, m), rows = m / used;
+        const auto tiles = [&](int64_t r, int64_t c) { return used * ceil_div(rows, r) * ceil_div(n, c); };
+        if (dense) {
+            const int64_t by16 = tiles(16, 64), by32 = tiles(32, 64), by64 = tiles(64, 64);
+            if (rows > 32 && by64 >= 192) stream = rows <= 64 ? 5 : -1;
+            else if (rows > 16 && by32 >= 192) stream = by32 <= 384 ? 3 : 4;
+            else stream = by16 < 192 ? 0 : by16 <= 384 ? 1 : 2;
+        } else if (rows <= 32) {
+            const int64_t most = rows + rows / 2 + 6;         // few groups have more rows
+            stream = most <= 16 ? (tiles(16, 64) < 192 ? 0 : tiles(16, 64) <= 384 ? 1 : 2) : tiles(32, 64) <= 384 ? 3 : 4;
+        }
+        config = stream >= 0                               ? GEMM_RELU_BLOCKS_STREAM
+                 : rows >= 192 && tiles(256, 256) >= 192   ? GEMM_RELU_BLOCKS_256
+                 : rows >= 96 && tiles(128, 128) >= 128    ? GEMM_RELU_BLOCKS_128
+                                                           : GEMM_RELU_BLOCKS_64;
+        if (stream < 0) stream = rows <= 16 ? 2 : 4;       // on request
+    }
+};
 
 // A product (M, N, K > 0).
 int launch_blocks(BlocksArgs a, int format_a, int format_b, int form_b, int config, int cus, hipStream_t stream)
 {
     a.c_vec = a.n % 8 == 0 && aligned(a.c, 16);
-    if (config == GEMM_RELU_BLOCKS_AUTO || config == GEMM_RELU_BLOCKS_STREAM) config = blocks_config(a);
+    const int rows_b = form_b == GEMM_RELU_SCALES_ROWS;
+    const BlocksChoice choice(a.m, a.n, a.groups, !a.ends);
+    if (config == GEMM_RELU_BLOCKS_AUTO) config = choice.config;
+    void* args[] = {&a};
+    if (config == GEMM_RELU_BLOCKS_STREAM) {
+        const int kind = choice.stream, r = 16 * kStreamRows[kind], threads = 64 * kStreamWaves[kind];
+        // row tiles: whole ones, a partial one of each group, and those of no group's rows
+        const int64_t tiles = a.ends ? std::min<int64_t>(a.m, a.m / r + a.groups + 1) : ceil_div(a.m, r);
+        const int64_t units = tiles * ceil_div(a.n, 16 * kStreamCols[kind]);
+        if (launchable(units, threads))
+            return enqueue(kernels(format_a, format_b).stream[kind][rows_b], dim3((unsigned)units), threads, args, stream);
+        config = GEMM_RELU_BLOCKS_64;
+    }
     const int64_t tiles = most_tiles(a, kBlockTile[config]);
     if (tiles > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
     const int64_t grid = std::min<int64_t>(tiles, config == GEMM_RELU_BLOCKS_64 ? 2 * cus : cus);
-    void* args[] = {&a};
-    return enqueue(kernels(format_a, format_b).tile[config][form_b == GEMM_RELU_SCALES_ROWS], dim3((unsigned)grid),
-                   kBlockThreads[config], args, stream);
+    return enqueue(kernels(format_a, format_b).tile[config][rows_b], dim3((unsigned)grid), kBlockThreads[config], args, stream);
 }
 
 // Places in the backward pass's workspace.
@@ -178,28 +223,19 @@ int gemm_relu_quantize_blocks(const void* X, const void* mask, void* Q, float* s
     return launch_quantize(a, count, dtype, format, form, static_cast<hipStream_t>(stream));
 }
 
-int64_t gemm_relu_blocks_workspace(int64_t M, int64_t N, int64_t K, int64_t groups)
-{
-    const int rc = check_dims({M, N, K});
-    if (rc != GEMM_RELU_OK) return rc;
-    if (groups < 1) return GEMM_RELU_ERR_INVALID_ARG;
-    if (groups > kMaxGroups) return GEMM_RELU_ERR_TOO_LARGE;
-    return 0;
-}
-
 int gemm_relu_blocks(const void* A, const float* scales_a, const void* B, const float* scales_b, const int32_t* ends,
                      void* C, int64_t M, int64_t N, int64_t K, int64_t groups, int64_t lda, int64_t ldb, int format_a,
-                     int format_b, int form_b, int dtype, int relu, int config_id, void* workspace,
-                     int64_t workspace_bytes, void* stream)
+                     int format_b, int form_b, int dtype, int relu, int config_id, void* stream)
 {
     if (dtype != GEMM_RELU_F16 && dtype != GEMM_RELU_BF16) return GEMM_RELU_ERR_BAD_DTYPE;
     if (!known_format(format_a) || !known_format(format_b)) return GEMM_RELU_ERR_BAD_DTYPE;
     if (!known_form(form_b)) return GEMM_RELU_ERR_BAD_LAYOUT;
-    const int64_t need = gemm_relu_blocks_workspace(M, N, K, groups);
-    if (need < 0) return (int)need;
-    if ((relu != 0 && relu != 1) || (!ends && groups != 1)) return GEMM_RELU_ERR_INVALID_ARG;
+    int rc = check_dims({M, N, K});
+    if (rc != GEMM_RELU_OK) return rc;
+    if (groups > kMaxGroups) return GEMM_RELU_ERR_TOO_LARGE;
+    if (groups < 1 || (relu != 0 && relu != 1) || (!ends && groups != 1)) return GEMM_RELU_ERR_INVALID_ARG;
     if (config_id < GEMM_RELU_BLOCKS_AUTO || config_id > GEMM_RELU_BLOCKS_STREAM) return GEMM_RELU_ERR_BAD_CONFIG;
-    int rc = check_pitch(lda, K);
+    rc = check_pitch(lda, K);
     if (rc == GEMM_RELU_OK) rc = check_pitch(ldb, K);
     if (rc != GEMM_RELU_OK) return rc;
     if (M == 0 || N == 0) return GEMM_RELU_OK;
@@ -208,11 +244,9 @@ int gemm_relu_blocks(const void* A, const float* scales_a, const void* B, const 
     const Span words[] = {{scales_a, 4 * M * kb},
                           {scales_b, 4 * groups * kb * (form_b == GEMM_RELU_SCALES_ROWS ? N : blocks_of(N))},
                           {ends, ends ? 4 * groups : 0}};
-    const Span out[] = {{C, 2 * M * N}, {workspace, need}};
+    const Span out[] = {{C, 2 * M * N}};
     rc = check_spans(in, 2, words, 3, out, 1);
     if (rc == GEMM_RELU_OK && K > 0 && (!aligned(A, 16) || !aligned(B, 16))) rc = GEMM_RELU_ERR_MISALIGNED;
-    if (rc == GEMM_RELU_OK) rc = check_workspace(workspace, workspace_bytes, need);
-    if (rc == GEMM_RELU_OK) rc = check_spans(in, 2, words, 3, out, need > 0 ? 2 : 1);
     if (rc != GEMM_RELU_OK) return rc;
     int cus = 0;
     if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;

@@ -31,21 +31,30 @@ __device__ __forceinline__ floatx4 mfma_block(int32x8_t w, int32x8_t x)
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, FW, FX, 0, 0, 0, 0);
 }
 
-template <int BM_, int BN_, int STAGES_, int WAVES_M_, int WAVES_N_>
+// A lane's 32 bytes of a matrix operand.
+__device__ __forceinline__ int32x8_t join(u32x4 lo, u32x4 hi)
+{
+    return int32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+template <int BM_, int BN_, int STAGES_, int WAVES_M_, int WAVES_N_, int PRODUCERS_>
 struct BlockConfig {
     static constexpr int BM = BM_, BN = BN_, BK = 128, STAGES = STAGES_, GROUP_M = 4;
-    static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, WAVES = WAVES_M * WAVES_N, THREADS = 64 * WAVES;
+    // WAVES compute waves; PRODUCERS > 0 adds waves that only load, else every
+    // compute wave loads its share.
+    static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, WAVES = WAVES_M * WAVES_N, PRODUCERS = PRODUCERS_;
+    static constexpr int DMA_WAVES = PRODUCERS > 0 ? PRODUCERS : WAVES, THREADS = 64 * (WAVES + PRODUCERS);
     static constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N, FM = WTM / 16, FN = WTN / 16;
     static constexpr int A_STAGE = BM * BK, B_STAGE = BN * BK, B_REGION = STAGES * A_STAGE;
     static constexpr int S_STAGE = (BM + BN) * 4, S_REGION = STAGES * (A_STAGE + B_STAGE);
     // A wave's strip: 16 rows of its columns of C on their way to memory.
     static constexpr int STRIP = 16 * WTN * 2, STRIPS = S_REGION + STAGES * S_STAGE;
     static constexpr int LDS_BYTES = STRIPS + WAVES * STRIP;
-    static constexpr int QA = A_STAGE / 1024 / WAVES, QB = B_STAGE / 1024 / WAVES, NQ = QA + QB + 1;
+    static constexpr int QA = A_STAGE / 1024 / DMA_WAVES, QB = B_STAGE / 1024 / DMA_WAVES, NQ = QA + QB + 1;
     static constexpr int SCALE_PIECES = (BM + BN) / 64;
-    static_assert(QA * WAVES * 1024 == A_STAGE && QB * WAVES * 1024 == B_STAGE, "whole DMA instructions");
+    static_assert(QA * DMA_WAVES * 1024 == A_STAGE && QB * DMA_WAVES * 1024 == B_STAGE, "whole DMA instructions");
     static_assert(QA % 2 == 0 && QB % 2 == 0, "the swizzle repeats every two instructions");
-    static_assert(SCALE_PIECES <= WAVES && WAVES % SCALE_PIECES == 0, "one DMA of scales a wave");
+    static_assert(SCALE_PIECES <= DMA_WAVES && DMA_WAVES % SCALE_PIECES == 0, "one DMA of scales a wave");
     static_assert((STAGES & (STAGES - 1)) == 0 && LDS_BYTES <= 160 * 1024 && STAGES * NQ < 64, "ring");
     static_assert((WTN == 64 || WTN == 32) && 128 % WTN == 0, "a wave's columns lie in one tile of scales");
 };
@@ -99,6 +108,69 @@ __device__ __forceinline__ void store_strips(uint16_t* __restrict__ C, const flo
     }
 }
 
+// The product's tiles: groups one after the other, a group's tiles in panels of
+// GROUP_M row tiles, column by column (tile_coords), the whole list dealt out in
+// equal parts to the XCDs, so that tiles which share operands share an L2.  (Dealing
+// whole columns of tiles, as RowUnits does, leaves an XCD with half as many again
+// where there are few: 1000 x 1104 x 517, 18 columns of 16 tiles, 13.8 us against 11.4.)
+// Lane l keeps what
+// belongs to group l; with more than 64 groups a lookup scans `ends` again.
+template <class Cfg>
+struct BlockUnits {
+    const int* ends;
+    int groups, M, tiles_n, lane, rows, first, listed;
+    UnitOrder order;
+    struct Lane {
+        int begin, end, incl;      // the group's rows, units up to it
+    } kept;                        // the first 64 groups
+
+    __device__ __forceinline__ Lane scan(int g0, int& start, int& before) const
+    {
+        const GroupRows r = load_group_rows(ends, groups, M, g0, start, lane);
+        const int tiles = g0 + lane < groups ? (r.end - r.begin + Cfg::BM - 1) / Cfg::BM : 0;
+        const Lane k{r.begin, r.end, before + wave_scan_sum(tiles) * tiles_n};
+        before = __builtin_amdgcn_readlane(k.incl, 63);
+        start = __builtin_amdgcn_readlane(r.end, min(groups - 1 - g0, 63));
+        return k;
+    }
+    __device__ __forceinline__ void init(const int* ends_, int groups_, int m, int n, int lane_, int block, int blocks)
+    {
+        ends = ends_;
+        groups = groups_;
+        M = m;
+        tiles_n = (n + Cfg::BN - 1) / Cfg::BN;
+        lane = lane_;
+        order.init(block, blocks);
+        int start = 0, total = 0;
+        kept = scan(0, start, total);
+        for (int g0 = 64; g0 < groups; g0 += 64) scan(g0, start, total);
+        rows = start;
+        first = (int)order.part(total, order.xcd);
+        listed = (int)order.part(total, order.xcd + 1) - first;
+    }
+    __device__ __forceinline__ int count() const { return order.units(listed); }
+    __device__ __forceinline__ DmaUnit unit(int i) const
+    {
+        const int at = first + order.position(i);
+        int g0 = 0, start = 0, before = 0;
+        Lane k = kept;
+        if (groups > 64) {
+            k = scan(0, start, before);
+            while (at >= before) {
+                g0 += 64;
+                k = scan(g0, start, before);
+            }
+        }
+        const int l = __builtin_ctzll(__ballot(at < k.incl));
+        const int b = __builtin_amdgcn_readlane(k.begin, l), e = __builtin_amdgcn_readlane(k.end, l);
+        const int tiles = (e - b + Cfg::BM - 1) / Cfg::BM, past = __builtin_amdgcn_readlane(k.incl, l) - at;
+        int tm, tn;
+        tile_coords(tiles * tiles_n - past, tiles, tiles_n, Cfg::GROUP_M, tm, tn, false);
+        const int m0 = b + tm * Cfg::BM;
+        return DmaUnit{m0, min(m0 + Cfg::BM, e), tn * Cfg::BN, g0 + l, 0, 0, -1};
+    }
+};
+
 template <class Cfg, int FA, int FB, bool B_ROWS>
 __global__ __launch_bounds__(Cfg::THREADS, 1) void blocks_dma(BlocksArgs a)
 {
@@ -107,18 +179,17 @@ __global__ __launch_bounds__(Cfg::THREADS, 1) void blocks_dma(BlocksArgs a)
     __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
+    constexpr bool WS = Cfg::PRODUCERS > 0;
+    const int dwave = WS ? wave - Cfg::WAVES : wave;      // among the waves that load
     const int k_blocks = (a.k + BK - 1) / BK, n_tiles = (a.n + kBlock - 1) / kBlock;
-    RowUnits<Cfg, true> units;
-    {
+    BlockUnits<Cfg> units;
+    units.init(a.ends, a.groups, a.m, a.n, lane, blockIdx.x, gridDim.x);
+    if (units.rows < a.m) {
         RowsArgs r{};
         r.m = a.m;
         r.n = a.n;
-        r.k = a.k;
-        units.init(r, a.ends, a.groups, false, lane, blockIdx.x, gridDim.x);
-        if (units.rows < a.m) {
-            r.c = a.c;
-            zero_rows(r, units.rows, blockIdx.x, gridDim.x);
-        }
+        r.c = a.c;
+        zero_rows(r, units.rows, blockIdx.x, gridDim.x);
     }
     const int n_units = __builtin_amdgcn_readfirstlane(units.count());
     if (n_units <= 0) return;
@@ -141,7 +212,7 @@ __global__ __launch_bounds__(Cfg::THREADS, 1) void blocks_dma(BlocksArgs a)
         b_voff[q] = (uint32_t)row * a.ldb + (uint32_t)pos[q];
     }
     // The scales' DMA: 64 floats of the tile's rows or columns a wave.
-    const int piece = wave % Cfg::SCALE_PIECES;
+    const int piece = dwave & (Cfg::SCALE_PIECES - 1);
     const bool scales_of_a = piece < BM / 64;
     const uint32_t scales_lds = lds_base + Cfg::S_REGION + 256u * (uint32_t)piece;
 
@@ -189,12 +260,12 @@ __global__ __launch_bounds__(Cfg::THREADS, 1) void blocks_dma(BlocksArgs a)
     auto dma = [&](int slot, int q) {
         const int left = a.k - f_k;
         if (q < QA) {
-            dma_b128(rows_from(f_a, f_rows, (wave * QA + (q & ~1)) * 8, a.lda), lds_base + slot * Cfg::A_STAGE + (wave * QA + q) * 1024,
+            dma_b128(rows_from(f_a, f_rows, (dwave * QA + (q & ~1)) * 8, a.lda), lds_base + slot * Cfg::A_STAGE + (dwave * QA + q) * 1024,
                      pos[q & 1] >= left ? kOobOffset : a_voff[q & 1], (uint32_t)f_k);
         } else if (q < QA + QB) {
             const int p = q - QA;
-            dma_b128(rows_from(f_b, f_cols, (wave * QB + (p & ~1)) * 8, a.ldb),
-                     lds_base + Cfg::B_REGION + slot * Cfg::B_STAGE + (wave * QB + p) * 1024,
+            dma_b128(rows_from(f_b, f_cols, (dwave * QB + (p & ~1)) * 8, a.ldb),
+                     lds_base + Cfg::B_REGION + slot * Cfg::B_STAGE + (dwave * QB + p) * 1024,
                      pos[p & 1] >= left ? kOobOffset : b_voff[p & 1], (uint32_t)f_k);
         } else {
             const int32x4_t r = rsrc_words(f_s + (size_t)(f_k / BK) * f_sstep, f_sbytes);
@@ -222,9 +293,9 @@ __global__ __launch_bounds__(Cfg::THREADS, 1) void blocks_dma(BlocksArgs a)
             }
         };
 #pragma unroll
-        for (int q = 0; q < QA; ++q) cut(smem + slot * Cfg::A_STAGE + (wave * QA + q) * 1024, pos[q & 1]);
+        for (int q = 0; q < QA; ++q) cut(smem + slot * Cfg::A_STAGE + (dwave * QA + q) * 1024, pos[q & 1]);
 #pragma unroll
-        for (int q = 0; q < QB; ++q) cut(smem + Cfg::B_REGION + slot * Cfg::B_STAGE + (wave * QB + q) * 1024, pos[q & 1]);
+        for (int q = 0; q < QB; ++q) cut(smem + Cfg::B_REGION + slot * Cfg::B_STAGE + (dwave * QB + q) * 1024, pos[q & 1]);
     };
 
     // Fragment reads (groups_dma.hpp): 16-byte chunks kb and 4 + kb of a row.
@@ -237,83 +308,196 @@ __global__ __launch_bounds__(Cfg::THREADS, 1) void blocks_dma(BlocksArgs a)
         b_off[h] = (uint32_t)(Cfg::B_REGION + rb * BK + 16 * ((4 * h + kb) ^ a_swizzle<128>(rb)));
     }
     auto fragment = [&](const uint8_t* stage, const uint32_t (&off)[2], int block) {
-        const u32x4 lo = *reinterpret_cast<const u32x4*>(stage + off[0] + block * 16 * BK);
-        const u32x4 hi = *reinterpret_cast<const u32x4*>(stage + off[1] + block * 16 * BK);
-        return int32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+        return join(*reinterpret_cast<const u32x4*>(stage + off[0] + block * 16 * BK),
+                    *reinterpret_cast<const u32x4*>(stage + off[1] + block * 16 * BK));
     };
 
-    fill_setup();
+    const int steps = n_units * k_blocks;
+    if constexpr (WS) {
+        // Step g's stage is filled while the step S - 1 before it is computed, and has
+        // landed for every wave at barrier g.
+        if (wave >= Cfg::WAVES) {
+            fill_setup();
 #pragma unroll 1
-    for (int s = 0; s < S; ++s) {
+            for (int s = 0; s < S - 1; ++s) {
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) dma(s, q);
-        fill_advance();
+                for (int q = 0; q < NQ; ++q) dma(s, q);
+                fill_advance();
+            }
+            int k = 0;                 // of the stage that lands
+            for (int g = 0; g < steps; ++g) {
+                wait_vmcnt<(S - 2) * NQ>();
+                cut_off(g & (S - 1), a.k - k);
+                k = k + BK < a.k ? k + BK : 0;
+                lds_barrier();
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) dma((g + S - 1) & (S - 1), q);
+                fill_advance();
+            }
+            wait_vmcnt<0>();           // no LDS DMA may outlive the workgroup
+            lds_barrier();
+            return;
+        }
+    } else {
+        fill_setup();
+#pragma unroll 1
+        for (int s = 0; s < S; ++s) {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) dma(s, q);
+            fill_advance();
+        }
     }
-    int slot = 0;
-    for (int c_unit = 0; c_unit < n_units; ++c_unit) {
-        const DmaUnit c = unit_at(c_unit);
-        floatx4 acc[FN][FM];
+
+    floatx4 acc[FN][FM];
+    auto clear = [&]() {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
             for (int j = 0; j < FM; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int k = 0; k < a.k; k += BK) {
-            wait_vmcnt<(S - 1) * NQ>();
-            cut_off(slot, a.k - k);
-            lds_barrier();
-            const uint8_t *sa = smem + slot * Cfg::A_STAGE, *sb = smem + slot * Cfg::B_STAGE;
-            const float* sc = reinterpret_cast<const float*>(smem + Cfg::S_REGION + slot * Cfg::S_STAGE);
-            int32x8_t w[FN];
-            floatx4 scale_w[B_ROWS ? FN : 1];
+    };
+    // Adds block (i, j)'s product.  (The empty assembly keeps the additions where they
+    // are; the compiler would move all of them, and the products they wait for, behind
+    // the step's last branch.)
+    auto add = [&](int i, int j, const floatx4& t, float scale_x, const floatx4& scale_w) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < FN; ++i) w[i] = fragment(sb, b_off, i);
-            if constexpr (B_ROWS) {
-#pragma unroll
-                for (int i = 0; i < FN; ++i) scale_w[i] = *reinterpret_cast<const floatx4*>(sc + BM + wn * Cfg::WTN + 16 * i + 4 * g4);
-            } else {
-                scale_w[0][0] = sc[BM + wn * Cfg::WTN];
-            }
-            // A row block's fragment is read while the one before is multiplied, and a
-            // block's product is added while the next LAG are computed.  (The empty
-            // assembly keeps the additions here; the compiler would move all of them,
-            // and the products they wait for, behind the step's last branch.)
-            constexpr int LAG = 3, NMF = FM * FN;
-            int32x8_t x[2];
-            float scale_x[2];
-            floatx4 t[LAG + 1];
-            x[0] = fragment(sa, a_off, 0);
-            scale_x[0] = sc[wm * Cfg::WTM + j16];
-#pragma unroll
-            for (int u = 0; u < NMF + LAG; ++u) {
-                if (u < NMF) {
-                    const int j = u / FN, i = u % FN;
-                    if (i == 0) {
-                        __builtin_amdgcn_sched_barrier(0);
-                        if (j + 1 < FM) x[(j + 1) & 1] = fragment(sa, a_off, j + 1);
-                    }
-                    t[u % (LAG + 1)] = mfma_block<FB, FA>(w[i], x[j & 1]);
-                }
-                if (u >= LAG) {
-                    const int d = u - LAG, j = d / FN, i = d % FN;
-                    if (i == 0 && j + 1 < FM) scale_x[(j + 1) & 1] = sc[wm * Cfg::WTM + 16 * (j + 1) + j16];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[i][j][e] = __builtin_fmaf(t[d % (LAG + 1)][e], scale_x[j & 1] * scale_w[B_ROWS ? i : 0][B_ROWS ? e : 0], acc[i][j][e]);
-                    asm volatile("" : "+v"(acc[i][j]));
-                }
-            }
-            lds_barrier();
-#pragma unroll
-            for (int q = 0; q < NQ; ++q) dma(slot, q);
-            fill_advance();
-            slot = (slot + 1) & (S - 1);
-        }
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(t[e], scale_x * scale_w[B_ROWS ? e : 0], acc[i][j][e]);
+        asm volatile("" : "+v"(acc[i][j]));
+    };
+    auto read_scale_w = [&](const float* sc, int i) {
+        if constexpr (B_ROWS) return *reinterpret_cast<const floatx4*>(sc + BM + wn * Cfg::WTN + 16 * i + 4 * g4);
+        const float s = sc[BM + wn * Cfg::WTN];
+        return floatx4{s, s, s, s};
+    };
+    auto store = [&](const DmaUnit& c) {
         const int m_base = c.m0 + wm * Cfg::WTM, n_base = c.n0 + wn * Cfg::WTN;
         uint8_t* const strip = smem + Cfg::STRIPS + wave * Cfg::STRIP;
         if (a.bf16) store_strips<kBF16>(a.c, acc, strip, lane, m_base, n_base, c.m_end, a.n, a.relu != 0, a.c_vec);
         else store_strips<kF16>(a.c, acc, strip, lane, m_base, n_base, c.m_end, a.n, a.relu != 0, a.c_vec);
+    };
+    auto scales = [&](int slot) { return reinterpret_cast<const float*>(smem + Cfg::S_REGION + slot * Cfg::S_STAGE); };
+    constexpr int LAG = FM * FN < 8 || B_ROWS ? 2 : 3, NSW = B_ROWS ? FN : 1;       // blocks whose product is on its way
+    clear();
+
+    if constexpr (WS) {
+        // A step's fragments are read while the step before is multiplied.
+        struct Fragments {
+            int32x8_t w[FN], x[FM];
+            float scale_x[FM];
+            floatx4 scale_w[NSW];
+        } f[2];
+        auto read = [&](Fragments& to, int slot) __attribute__((always_inline)) {
+            const float* sc = scales(slot);
+#pragma unroll
+            for (int i = 0; i < FN; ++i) to.w[i] = fragment(smem + slot * Cfg::B_STAGE, b_off, i);
+#pragma unroll
+            for (int j = 0; j < FM; ++j) to.x[j] = fragment(smem + slot * Cfg::A_STAGE, a_off, j);
+#pragma unroll
+            for (int j = 0; j < FM; ++j) to.scale_x[j] = sc[wm * Cfg::WTM + 16 * j + j16];
+#pragma unroll
+            for (int i = 0; i < NSW; ++i) to.scale_w[i] = read_scale_w(sc, i);
+        };
+        int c_unit = 0, left = k_blocks, g = 0;
+        lds_barrier();
+        read(f[0], 0);
+        // Whether there is a step after this one.
+        auto step = [&](Fragments& now, Fragments& next) __attribute__((always_inline)) {
+            ++g;
+            lds_barrier();                                  // step g has landed, or the last one is done
+            if (g < steps) read(next, g & (S - 1));
+            floatx4 t[LAG + 1];
+#pragma unroll
+            for (int u = 0; u < FM * FN + LAG; ++u) {
+                if (u < FM * FN) t[u % (LAG + 1)] = mfma_block<FB, FA>(now.w[u % FN], now.x[u / FN]);
+                if (u >= LAG) {
+                    const int d = u - LAG, i = d % FN, j = d / FN;
+                    add(i, j, t[d % (LAG + 1)], now.scale_x[j], now.scale_w[B_ROWS ? i : 0]);
+                }
+            }
+            if (--left == 0) {
+                store(unit_at(c_unit++));
+                clear();
+                left = k_blocks;
+            }
+            return g < steps;
+        };
+        while (step(f[0], f[1]) && step(f[1], f[0])) {
+        }
+    } else {
+        // One set of fragments: the columns' are kept for a step, the rows' are read two
+        // blocks ahead.  Before the last two row blocks everything of the slot has been
+        // read: after the barrier there it is filled again, and the next step's first
+        // fragments take the place of those that are done.
+        static_assert(FM % 2 == 0 && FM >= 4, "row blocks");
+        int32x8_t w[FN], x[3];
+        float scale_x[FM];
+        floatx4 scale_w[NSW];
+        wait_vmcnt<(S - 1) * NQ>();
+        cut_off(0, a.k);
+        lds_barrier();
+        auto read_x = [&](int to, int slot, int j) __attribute__((always_inline)) {
+            x[to] = fragment(smem + slot * Cfg::A_STAGE, a_off, j);
+        };
+#pragma unroll
+        for (int i = 0; i < FN; ++i) w[i] = fragment(smem, b_off, i);
+        read_x(2, 0, 0);
+        int slot = 0, c_unit = 0, k = 0;
+        for (int g = 0; g < steps; ++g) {
+            const float* sc = scales(slot);
+#pragma unroll
+            for (int j = 0; j < FM; ++j) scale_x[j] = sc[wm * Cfg::WTM + 16 * j + j16];
+#pragma unroll
+            for (int i = 0; i < NSW; ++i) scale_w[i] = read_scale_w(sc, i);
+            x[0] = x[2];
+            read_x(1, slot, 1);
+            floatx4 t[LAG + 1];
+            auto finish = [&](int u) __attribute__((always_inline)) {      // the addition for product u
+                const bool late = u >= (FM - 2) * FN;
+                const int v = u - (FM - 2) * FN, i = late ? v / 2 : u % FN, j = late ? FM - 2 + (v & 1) : u / FN;
+                add(i, j, t[u % (LAG + 1)], scale_x[j], scale_w[B_ROWS ? i : 0]);
+            };
+            int u = 0;
+#pragma unroll
+            for (int j = 0; j < FM - 2; ++j) {
+                read_x((j + 2) % 3, slot, j + 2);
+#pragma unroll
+                for (int i = 0; i < FN; ++i, ++u) {
+                    t[u % (LAG + 1)] = mfma_block<FB, FA>(w[i], x[j % 3]);
+                    if (u >= LAG) finish(u - LAG);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            const int next = (slot + 1) & (S - 1);
+            const int k_next = k + BK < a.k ? k + BK : 0;
+            wait_vmcnt<(S - 2) * NQ>();
+            cut_off(next, a.k - k_next);
+            lds_barrier();
+            // buffers (FM - 2) % 3 and (FM - 1) % 3 are in use; the third is 2 for FM = 8
+            static_assert((FM - 2) % 3 == 0, "the next step's first fragment goes to x[2]");
+            read_x(2, next, 0);
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+#pragma unroll
+                for (int j = FM - 2; j < FM; ++j, ++u) {
+                    t[u % (LAG + 1)] = mfma_block<FB, FA>(w[i], x[j % 3]);
+                    finish(u - LAG);
+                }
+                w[i] = fragment(smem + next * Cfg::B_STAGE, b_off, i);
+#pragma unroll
+                for (int q = i * NQ / FN; q < (i + 1) * NQ / FN; ++q) dma(slot, q);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int d = FM * FN - LAG; d < FM * FN; ++d) finish(d);
+            fill_advance();
+            slot = next;
+            k = k_next;
+            if (k == 0) {
+                store(unit_at(c_unit++));
+                clear();
+            }
+        }
+        wait_vmcnt<0>();   // no LDS DMA may outlive the workgroup
     }
-    wait_vmcnt<0>();   // no LDS DMA may outlive the workgroup
 }
 
 }  // namespace gemm_relu_hip

@@ -44,10 +44,17 @@ struct BlocksArgs {
 
 constexpr int kNumBlockTiles = 3;
 constexpr int kBlockTile[kNumBlockTiles] = {256, 128, 64};
-constexpr int kBlockThreads[kNumBlockTiles] = {512, 256, 256};
+constexpr int kBlockThreads[kNumBlockTiles] = {512, 512, 512};
+
+// Streaming kernels: 16-row blocks and 16-column blocks of a workgroup, its waves and
+// the scale blocks that each wave's ring holds.
+constexpr int kNumStreams = 6;
+constexpr int kStreamRows[kNumStreams] = {1, 1, 1, 2, 2, 4}, kStreamCols[kNumStreams] = {2, 4, 4, 4, 4, 4};
+constexpr int kStreamWaves[kNumStreams] = {8, 8, 4, 8, 4, 8}, kStreamStages[kNumStreams] = {2, 1, 1, 1, 1, 1};
 
 struct BlocksKernels {
     const void* tile[kNumBlockTiles][2];      // [tile][scales of B by rows]
+    const void* stream[kNumStreams][2];
 };
 // By the formats of A and B.
 const BlocksKernels& blocks_kernels_e4m3_e4m3();
