@@ -73,6 +73,7 @@ def experts_workspace_bytes(tokens: int, N: int, hidden: int, experts: int, top:
     return _bytes("gemm_relu_experts_workspace", tokens, N, hidden, experts, top, b_layout)
 
 
+@functools.lru_cache(maxsize=1)
 def _formats():
     import torch
     return {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
@@ -95,17 +96,19 @@ def _check_8bit(name, t, dim, dev=None):
         raise ValueError(f"gemm_relu: {name} must be a GPU tensor, got {t.device}")
     if dev is not None and t.get_device() != dev:
         raise ValueError(f"gemm_relu: {name} must be on the same device as the other tensors")
-    if t.dim() != dim:
-        raise ValueError(f"gemm_relu: {name} must be {dim}-D, got shape {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != dim:
+        raise ValueError(f"gemm_relu: {name} must be {dim}-D, got shape {tuple(shape)}")
     code = _format_code(name, t.dtype)
     if t.requires_grad:
-        raise RuntimeError(f"gemm_relu: {name} requires a gradient, but 8-bit operands have none; call under "
-                           "torch.no_grad() on detached tensors, or use linear_blocks")
-    shape, stride = t.shape, t.stride()
+        raise RuntimeError(f"gemm_relu: {name} requires a gradient, but 8-bit operands have none; detach it")
     rows, row = shape[-2], shape[-1]
-    whole = (row + 15) // 16 * 16
+    whole = row + 15 & -16
+    if row == whole and rows > 1 and t.is_contiguous() and not t.data_ptr() & 15:
+        return code, row
     if t.numel() == 0:
         return code, whole
+    stride = t.stride()
     stacked = dim == 3 and shape[0] > 1
     pitch = stride[-2] if rows > 1 else stride[0] if stacked else whole
     if row > 1 and stride[-1] != 1:
@@ -124,19 +127,22 @@ def _blocks(n: int) -> int:
     return (n + BLOCK - 1) // BLOCK
 
 
-def _empty_8bit(shape, dtype, like, stream):
-    """An 8-bit tensor whose rows start at multiples of 16 bytes."""
+def _empty(shape, dtype, device, stream):
+    """A new tensor for work on ``stream`` (groups._new)."""
     import torch
-    pitch = (shape[-1] + 15) // 16 * 16
-    with _on(stream, like.get_device()):
-        raw = torch.empty(shape[:-1] + (pitch,), dtype=torch.uint8, device=like.device)
-    return raw[..., : shape[-1]].view(dtype), pitch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _floats(shape, like, stream):
+def _empty_8bit(shape, dtype, device, stream):
+    """An 8-bit tensor whose rows start at multiples of 16 bytes, and its pitch."""
     import torch
-    with _on(stream, like.get_device()):
-        return torch.empty(shape, dtype=torch.float32, device=like.device)
+    pitch = shape[-1] + 15 & -16
+    if pitch == shape[-1]:
+        return _empty(shape, dtype, device, stream), pitch
+    return _empty(shape[:-1] + (pitch,), torch.uint8, device, stream)[..., : shape[-1]].view(dtype), pitch
 
 
 def quantize_blocks(x, dtype=None, tiles: bool = False, mask=None, rows: bool = True, transposed: bool = False,
@@ -156,45 +162,52 @@ def quantize_blocks(x, dtype=None, tiles: bool = False, mask=None, rows: bool = 
     """
     import torch
     code, dev = _first("x", x)
-    if x.dim() not in (2, 3):
-        raise ValueError(f"gemm_relu: x must be 2-D or 3-D, got shape {tuple(x.shape)}")
-    _check_tensor("x", x, x.dim(), dev, x.dtype)
+    shape = tuple(x.shape)
+    if len(shape) not in (2, 3):
+        raise ValueError(f"gemm_relu: x must be 2-D or 3-D, got shape {shape}")
+    _check_tensor("x", x, len(shape), dev, x.dtype)
+    above = None
     if mask is not None:
-        _check_tensor("mask", mask, x.dim(), dev, x.dtype)
-        _check_shape("mask", mask, tuple(x.shape))
+        _check_tensor("mask", mask, len(shape), dev, x.dtype)
+        _check_shape("mask", mask, shape)
+        above = mask.data_ptr()
     dtype = torch.float8_e4m3fn if dtype is None else dtype
     fmt = _format_code("dtype", dtype)
     if not rows and not transposed:
         raise ValueError("gemm_relu: neither rows nor transposed is asked for")
-    stack, (R, C) = tuple(x.shape[:-2]), x.shape[-2:]
-    count = stack[0] if stack else 1
-    q = s = qt = st = None
+    stack, (R, C) = shape[:-2], shape[-2:]
+    br, bc, device = _blocks(R), _blocks(C), x.device
+    qp = sp = qtp = stp = None
     ldq = ldqt = 0
+    out = ()
     if rows:
-        q, ldq = _empty_8bit(stack + (R, C), dtype, x, stream)
-        s = _floats(stack + ((_blocks(R), _blocks(C)) if tiles else (_blocks(C), R)), x, stream)
+        q, ldq = _empty_8bit(shape, dtype, device, stream)
+        s = _empty(stack + ((br, bc) if tiles else (bc, R)), torch.float32, device, stream)
+        qp, sp, out = q.data_ptr(), s.data_ptr(), (q, s)
     if transposed:
-        qt, ldqt = _empty_8bit(stack + (C, R), dtype, x, stream)
-        st = _floats(stack + ((_blocks(C), _blocks(R)) if tiles else (_blocks(R), C)), x, stream)
+        qt, ldqt = _empty_8bit(stack + (C, R), dtype, device, stream)
+        st = _empty(stack + ((bc, br) if tiles else (br, C)), torch.float32, device, stream)
+        qtp, stp, out = qt.data_ptr(), st.data_ptr(), out + (qt, st)
     if x.numel():
-        handle = _stream_handle(stream, dev)
-        _call(_library().gemm_relu_quantize_blocks, dev, x.data_ptr(), mask.data_ptr() if mask is not None else None,
-              q.data_ptr() if rows else None, s.data_ptr() if rows else None, qt.data_ptr() if transposed else None,
-              st.data_ptr() if transposed else None, count, R, C, ldq, ldqt, code, fmt, 1 if tiles else 0,
-              1 if power_of_two else 0, handle or None)
-    return ((q, s) if rows else ()) + ((qt, st) if transposed else ())
+        _call(_library().gemm_relu_quantize_blocks, dev, x.data_ptr(), above, qp, sp, qtp, stp, stack[0] if stack else 1, R,
+              C, ldq, ldqt, code, fmt, 1 if tiles else 0, 1 if power_of_two else 0, _stream_handle(stream, dev) or None)
+    return out
 
 
-def _out_dtype(out, out_dtype):
+def _output(out, out_dtype, shape, dev, device, stream):
+    """(output, dtype code) of gemm_relu_blocks."""
     import torch
-    if out is not None and not isinstance(out, torch.Tensor):
-        raise TypeError("gemm_relu: out must be a torch.Tensor")
-    dtype = out.dtype if out is not None else torch.bfloat16 if out_dtype is None else out_dtype
-    if out_dtype is not None and dtype != out_dtype:
-        raise TypeError(f"gemm_relu: out is {dtype}, but out_dtype is {out_dtype}")
-    if dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError(f"gemm_relu: the output's dtype must be float16 or bfloat16, got {dtype}")
-    return dtype, 0 if dtype is torch.float16 else 1
+    if out is None:
+        out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+        if out_dtype is not torch.bfloat16 and out_dtype is not torch.float16:
+            raise TypeError(f"gemm_relu: the output's dtype must be float16 or bfloat16, got {out_dtype}")
+        return _empty(shape, out_dtype, device, stream), 0 if out_dtype is torch.float16 else 1
+    code = _first("out", out)[0]
+    if out_dtype is not None and out.dtype is not out_dtype:
+        raise TypeError(f"gemm_relu: out is {out.dtype}, but out_dtype is {out_dtype}")
+    _check_tensor("out", out, 2, dev, out.dtype)
+    _check_shape("out", out, shape)
+    return out, code
 
 
 def gemm_relu_blocks(a, a_scales, b, b_scales, ends=None, out=None, out_dtype=None, relu: bool = True,
@@ -225,17 +238,10 @@ def gemm_relu_blocks(a, a_scales, b, b_scales, ends=None, out=None, out_dtype=No
     if grouped:
         _check_tensor("ends", ends, 1, dev, torch.int32)
         _check_shape("ends", ends, (groups,))
-    dtype, code = _out_dtype(out, out_dtype)
-    if out is None:
-        with _on(stream, dev):
-            out = torch.empty((M, N), dtype=dtype, device=a.device)
-    else:
-        _check_tensor("out", out, 2, dev, dtype)
-        _check_shape("out", out, (M, N))
-    handle = _stream_handle(stream, dev)
+    out, code = _output(out, out_dtype, (M, N), dev, a.device, stream)
     _call(_library().gemm_relu_blocks, dev, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(),
           ends.data_ptr() if grouped else None, out.data_ptr(), M, N, K, groups, lda, ldb, fa, fb, 0 if b_rows else 1,
-          code, 1 if relu else 0, config, handle or None)
+          code, 1 if relu else 0, config, _stream_handle(stream, dev) or None)
     return out
 
 
@@ -389,9 +395,8 @@ def gemm_relu_experts(x, w1, w2, logits=None, top=None, ids=None, weights=None, 
         return (y, *chosen)
     need = experts_workspace_bytes(tokens, N, hidden, experts, top, b_layout)
     if routed:
-        with _on(stream, dev):
-            ids = torch.empty((tokens, top), dtype=torch.int32, device=x.device)
-            weights = torch.empty((tokens, top), dtype=torch.float32, device=x.device)
+        ids = _empty((tokens, top), torch.int32, x.device, stream)
+        weights = _empty((tokens, top), torch.float32, x.device, stream)
     if out is None:
         out = _new((tokens, N), x, stream)
     else:

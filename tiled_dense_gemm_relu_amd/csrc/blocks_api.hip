@@ -147,30 +147,31 @@ struct BackwardSpace {
     }
 };
 
-// The expert layer: columns of a unit, parts of its second product's K, and places in
+// The expert layer: kinds of workgroups, parts of its second product's K, and places in
 // the workspace.
 struct ExpertsSpace {
-    int wide1, wide2;      // index into kExpertBlocks
-    int64_t blocks1, blocks2, splits, mid_row, mid, part, bytes;
+    int kind1, kind2;      // index into kExpertBlocks
+    int64_t units1, units2, splits, mid_row, mid, part, bytes;
     ExpertsSpace(int64_t tokens, int64_t n, int64_t hidden, int64_t experts, int64_t top, int b_layout)
     {
         const int64_t slots = tokens * top, used = std::min(experts, slots);
-        const auto wide = [&](int64_t out) {
-            return b_layout == GEMM_RELU_B_KN || used * ceil_div(out, 64) >= 512 || ceil_div(out, 16) > kMaxColumnBlocks;
+        const auto columns = [&](int kind) { return int64_t(16) * (b_layout == GEMM_RELU_B_KN ? 4 : kExpertBlocks[kind]); };
+        const auto kind = [&](int64_t out) {
+            if (tokens > 16 && slots > 12 * used) return 2;
+            return used * ceil_div(out, 64) > 384 || ceil_div(out, 32) > kMaxColumnBlocks ? 1 : 0;
         };
-        wide1 = wide(hidden);
-        wide2 = wide(n);
-        blocks1 = ceil_div(hidden, 16 * kExpertBlocks[wide1]);
-        blocks2 = ceil_div(n, 16 * kExpertBlocks[wide2]);
-        const int64_t units = used * blocks2;
-        splits = units == 0 ? 1 : std::max<int64_t>(1, std::min<int64_t>(512 / units, blocks_of(hidden) / kPiecesAPart));
+        kind1 = kind(hidden);
+        kind2 = kind(n);
+        units1 = used * ceil_div(hidden, columns(kind1));
+        units2 = used * ceil_div(n, columns(kind2));
+        splits = units2 == 0 ? 1 : std::max<int64_t>(1, std::min<int64_t>(256 / units2, blocks_of(hidden) / kBlocksAPart));
         mid_row = round_up(hidden, 8);
         mid = GEMM_RELU_GROUPS_COUNTER_BYTES;
         part = mid + round_up(4 * slots * mid_row, 256);
         bytes = part + round_up(4 * slots * splits * n, 256);
     }
-    // A counter for each column block; pieces of K for the 8 waves of each part.
-    static constexpr int64_t kMaxColumnBlocks = GEMM_RELU_GROUPS_COUNTER_BYTES / 4, kPiecesAPart = 8;
+    // A counter for each column block; scale blocks of K for the waves of each part.
+    static constexpr int64_t kMaxColumnBlocks = GEMM_RELU_GROUPS_COUNTER_BYTES / 4, kBlocksAPart = 8;
 };
 static_assert(((int64_t(1) << 20) + 63) / 64 <= ExpertsSpace::kMaxColumnBlocks, "a counter for each block of 64 columns");
 
@@ -369,7 +370,6 @@ int gemm_relu_experts(const void* X, const void* W1, const float* scales1, const
     const int store = bytes ? 2 + format : kn ? 1 : 0;
     const ExpertsKernels& kernels = dtype == GEMM_RELU_F16 ? experts_kernels_f16() : experts_kernels_bf16();
     const auto even = [](const void* p, int64_t row) { return row % 2 == 0 && aligned(p, 4); };
-    const int64_t used = std::min(experts, slots);
     ExpertsArgs a{};
     a.x = static_cast<const uint16_t*>(X);
     a.w = static_cast<const uint8_t*>(W1);
@@ -392,9 +392,14 @@ int gemm_relu_experts(const void* X, const void* W1, const float* scales1, const
     a.routed = logits != nullptr;
     a.splits = 1;
     void* args[] = {&a};
-    const auto grid = [&](int64_t units) { return dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(units, 2 * cus))); };
+    // As many workgroups as run at once.
+    const auto launch = [&](int odd, int second, int kind, int64_t units) {
+        const int64_t room = (kind == 0 ? 2 : 3) * cus;
+        return enqueue(kernels.products[store][odd][second][kind], dim3((unsigned)std::max<int64_t>(1, std::min(units, room))),
+                       64 * kExpertWaves[kind], args, s, (size_t)route_table_bytes(slots, experts));
+    };
     const bool odd1 = !even(X, K) || (!bytes && !(kn ? even(W1, hidden) : even(W1, K)));
-    rc = enqueue(kernels.products[store][odd1][0][space.wide1], grid(used * space.blocks1), kExpertThreads, args, s);
+    rc = launch(odd1, 0, space.kind1, space.units1);
     if (rc != GEMM_RELU_OK || N == 0) return rc;
     a.x = a.mid;
     a.w = static_cast<const uint8_t*>(W2);
@@ -405,7 +410,7 @@ int gemm_relu_experts(const void* X, const void* W1, const float* scales1, const
     a.out = (int)N;
     a.splits = (int)space.splits;
     const bool odd2 = !bytes && !(kn ? even(W2, N) : even(W2, hidden));
-    return enqueue(kernels.products[store][odd2][1][space.wide2], grid(used * space.blocks2 * space.splits), kExpertThreads, args, s);
+    return launch(odd2, 1, space.kind2, space.units2 * space.splits);
 }
 
 }  // extern "C"

@@ -82,14 +82,17 @@ struct ExpertsArgs {
     int renormalize, routed, splits;
 };
 
-constexpr int kMaxTokens = 64, kMaxTop = 16, kMaxExperts = 1024, kExpertThreads = 512;
-// Columns of a unit, in blocks of 16.
-constexpr int kNumExpertBlocks = 2;
-constexpr int kExpertBlocks[kNumExpertBlocks] = {1, 4};
+constexpr int kMaxTokens = 64, kMaxTop = 16, kMaxExperts = 1024;
+// Workgroups: columns of a unit, in blocks of 16 ((K, N) weights: 4 in all), rows of a
+// pass, in blocks of 16, and waves.  For few units (one workgroup a CU), for many, and
+// for many rows an expert.
+constexpr int kNumExpertKinds = 3;
+constexpr int kExpertBlocks[kNumExpertKinds] = {2, 4, 4}, kExpertRows[kNumExpertKinds] = {1, 1, 2}, kExpertWaves[kNumExpertKinds] = {8, 4, 4};
+constexpr int64_t route_table_bytes(int64_t slots, int64_t experts) { return slots * 8 + experts * 8 + 16; }
 
 struct ExpertsKernels {
-    // [storage: NK, KN, e4m3, e5m2][odd rows][second product][columns]; KN has 4 blocks only
-    const void* products[4][2][2][kNumExpertBlocks];
+    // [storage: NK, KN, e4m3, e5m2][odd rows][second product][kind]
+    const void* products[4][2][2][kNumExpertKinds];
 };
 const ExpertsKernels& experts_kernels_f16();
 const ExpertsKernels& experts_kernels_bf16();

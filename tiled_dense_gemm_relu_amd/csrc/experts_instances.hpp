@@ -5,15 +5,13 @@
 
 namespace gemm_relu_hip {
 
-template <int DT, int STORE, bool ODD>
-constexpr void fill_experts(const void* (&to)[2][kNumExpertBlocks])
+template <int DT, int STORE, bool ODD, int KIND = 0>
+constexpr void fill_experts(const void* (&to)[2][kNumExpertKinds])
 {
-    if constexpr (STORE != kStoreKN) {
-        to[0][0] = (const void*)expert_products<DT, STORE, ODD, false, 1>;
-        to[1][0] = (const void*)expert_products<DT, STORE, ODD, true, 1>;
-    }
-    to[0][1] = (const void*)expert_products<DT, STORE, ODD, false, 4>;
-    to[1][1] = (const void*)expert_products<DT, STORE, ODD, true, 4>;
+    to[0][KIND] = (const void*)expert_products<DT, STORE, ODD, false, KIND>;
+    // (the second product of 8-bit weights has no odd rows)
+    to[1][KIND] = (const void*)expert_products<DT, STORE, ODD && STORE < kStoreE4M3, true, KIND>;
+    if constexpr (KIND + 1 < kNumExpertKinds) fill_experts<DT, STORE, ODD, KIND + 1>(to);
 }
 
 template <int DT>

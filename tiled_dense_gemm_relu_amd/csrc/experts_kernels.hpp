@@ -3,9 +3,11 @@
 //
 // With a few tokens the time is that of reading the chosen experts' weights, once.
 // Every workgroup makes the routing table for itself (tokens are few), so nothing
-// waits for it, and takes units of one expert and 16 NB output columns; its 8 waves
-// take pieces of 128 k in turn, straight from memory into registers, and add their
-// sums in LDS.  Up to 64 of an expert's rows share a pass over its weights.
+// waits for it, and takes units of one expert and 16 NB output columns; its waves
+// take pieces of k in turn and add their sums in LDS.  16 MB of an expert's rows
+// stream with the weights through a ring of each wave's own in LDS, by DMA, as in
+// blocks_stream.hpp (an expert with more rows takes several passes); operands whose
+// rows DMA cannot read (odd lengths, 2-byte alignment) go through registers.
 //
 // The first launch leaves weight * ReLU(sum) of every choice as a sum of two 16-bit
 // values, so that the second one's matrix instructions lose nothing of it.  The
@@ -19,18 +21,27 @@
 
 namespace gemm_relu_hip {
 
-constexpr int kExpertWaves = kExpertThreads / 64;
-constexpr int kMaxSlots = kMaxTokens * kMaxTop;
-
-// Who goes where: slot t top + j is token t's choice j.
+// Who goes where: slot t top + j is token t's choice j.  In dynamic LDS, as large as
+// the call needs (route_table_bytes).
 struct RouteTable {
-    int16_t ids[kMaxSlots];          // -1: none
-    uint16_t sorted[kMaxSlots];      // slots by expert, in order
-    uint16_t start[kMaxExperts];     // where an expert's slots begin in `sorted`
-    uint16_t used[kMaxExperts + 1];  // the experts that have slots
-    float weights[kMaxSlots];
-    int count[kMaxExperts];
-    int n_used;
+    float* weights;          // a slot's weight
+    int* count;              // an expert's slots
+    int* n_used;
+    int16_t* ids;            // a slot's expert, -1: none
+    uint16_t* sorted;        // slots by expert, in order
+    uint16_t* start;         // where an expert's slots begin in `sorted`
+    uint16_t* used;          // the experts that have slots
+
+    __device__ __forceinline__ RouteTable(uint8_t* p, int slots, int experts)
+    {
+        weights = reinterpret_cast<float*>(p);
+        count = reinterpret_cast<int*>(weights + slots);
+        n_used = count + experts;
+        ids = reinterpret_cast<int16_t*>(n_used + 1);
+        sorted = reinterpret_cast<uint16_t*>(ids + slots);
+        start = sorted + slots;
+        used = start + experts;
+    }
 };
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t v)
@@ -116,12 +127,14 @@ __device__ inline void choose(const float* __restrict__ logits, int experts, int
 
 // The routing table, by the whole workgroup.  With logits the choices are made here
 // and, by the first workgroup, written.
-__device__ inline void make_table(RouteTable& t, const ExpertsArgs& a, int lane, int wave)
+template <int WAVES>
+__device__ inline void make_table(const RouteTable& t, const ExpertsArgs& a, int lane, int wave)
 {
+    constexpr int kExpertThreads = 64 * WAVES;
     const int slots = a.tokens * a.top, tid = threadIdx.x;
     for (int e = tid; e < a.experts; e += kExpertThreads) t.count[e] = 0;
     if (a.logits) {
-        for (int token = wave; token < a.tokens; token += kExpertWaves) {
+        for (int token = wave; token < a.tokens; token += WAVES) {
             int id;
             float weight;
             choose(a.logits + (size_t)token * (size_t)a.experts, a.experts, a.top, a.renormalize != 0, lane, id, weight);
@@ -158,7 +171,7 @@ __device__ inline void make_table(RouteTable& t, const ExpertsArgs& a, int lane,
             before += __builtin_amdgcn_readlane(incl, 63);
             used += __popcll(some);
         }
-        if (lane == 0) t.n_used = used;
+        if (lane == 0) *t.n_used = used;
     }
     __syncthreads();
     for (int s = tid; s < slots; s += kExpertThreads) {
@@ -214,8 +227,9 @@ template <bool ODD, int NB>
 struct PieceWeights<kStoreNK, ODD, NB> {
     SkinnyChunk<ODD> v[NB][4];
 };
-template <bool ODD>
-struct PieceWeights<kStoreKN, ODD, 4> {
+template <bool ODD, int NB>
+struct PieceWeights<kStoreKN, ODD, NB> {
+    static_assert(NB == 4, "4 columns a lane");
     u32x2 v[4][8];
     uint32_t next[ODD ? 4 : 1][ODD ? 8 : 1];
 };
@@ -229,13 +243,13 @@ struct PieceWeights<kStoreE5M2, ODD, NB> : PieceWeights<kStoreE4M3, ODD, NB> {};
 // The sums over pieces p0 + wave, p0 + wave + 8, .. of a unit's NB x MB blocks.
 //  Rows: lane's row of block j is x_off[j] bytes into rx (kOobOffset: none); with
 //  SPLIT_X also its low parts, x_low bytes on.
-template <int DT, int STORE, bool ODD, bool SPLIT_X, int NB, int MB>
+template <int DT, int STORE, bool SPLIT_X, int NB, int MB, int WAVES>
 __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsrc& rx, const uint32_t (&x_off)[MB], uint32_t x_low,
                                             const uint8_t* w, const float* scales, int64_t ld, int n0, int in, int out,
                                             int p0, int p1, int wave, int lane)
 {
-    constexpr bool WIDE = STORE >= kStoreE4M3, ODD_X = ODD && !SPLIT_X;
-    constexpr int KU = NB == 1 && MB == 1 ? 4 : WIDE && MB == 1 ? 2 : 1;     // pieces in flight
+    constexpr bool WIDE = STORE >= kStoreE4M3, ODD = !WIDE, ODD_X = !SPLIT_X;
+    constexpr int KU = NB <= 2 && MB == 1 ? 2 : 1;     // pieces in flight
     const int r16 = lane & 15, g = lane >> 4;
     const int cols = min(16 * NB, out - n0);
     // NK and 8-bit: rows n0 .. of the expert's weights
@@ -250,7 +264,7 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
         high = load_skinny<ODD_X>(rx, off);
         if constexpr (SPLIT_X) low = load_skinny<ODD_X>(rx, off == kOobOffset ? kOobOffset : off + x_low);
     };
-    for (int i0 = p0 + wave; i0 < p1; i0 += KU * kExpertWaves) {
+    for (int i0 = p0 + wave; i0 < p1; i0 += KU * WAVES) {
         PieceWeights<STORE, ODD, NB> pw[KU];
         // Rows of X: with one block all of a piece's are in flight with its weights; with
         // more each step's are read when it comes (from L2, and too many to keep).
@@ -258,7 +272,7 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
         float scale[KU];
 #pragma unroll
         for (int q = 0; q < KU; ++q) {
-            const int p = i0 + q * kExpertWaves, k0 = p * kBlock;
+            const int p = i0 + q * WAVES, k0 = p * kBlock;
             const bool live = p < p1;
             if constexpr (STORE == kStoreNK) {
 #pragma unroll
@@ -300,7 +314,7 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
         }
 #pragma unroll
         for (int q = 0; q < KU; ++q) {
-            const int p = i0 + q * kExpertWaves, k0 = p * kBlock;
+            const int p = i0 + q * WAVES, k0 = p * kBlock;
             if (p >= p1) break;
             const bool tail = k0 + kBlock > in;
             floatx4 sum[WIDE ? NB : 1][WIDE ? MB : 1];
@@ -388,22 +402,196 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
     }
 }
 
-template <int DT, int STORE, bool ODD, bool SECOND, int NB>
-__global__ __launch_bounds__(kExpertThreads, 2) void expert_products(ExpertsArgs a)
+// The sums over this wave's pieces (64 k of 16-bit weights, 128 of 8-bit ones: 128
+// bytes of a row of W, or 64 rows of 64 columns) for up to 16 rows, through its ring
+// of S stages: W, then X's rows in halves of 64 k, then their low parts.
+//  x_row[q]: where the row of X of this lane's 16 bytes of DMA instruction q begins,
+// in bytes (kOobOffset: none).
+template <int DT, int STORE, bool SPLIT_X, int NB, int MB, int S, int WAVES>
+__device__ __forceinline__ void expert_stream(floatx4 (&acc)[NB][MB], const uint16_t* x, uint32_t x_bytes, const uint32_t (&x_row)[2 * MB],
+                                              uint32_t x_low, const uint8_t* w, const float* scales, int64_t ld, int n0, int in,
+                                              int out, int p0, int p1, uint8_t* ring, int turn, int wave, int lane)
 {
-    constexpr int COLS = 16 * NB, PART = COLS * 17;
-    __shared__ RouteTable t;
-    __shared__ float part[kExpertWaves * PART];
+    constexpr bool WIDE = STORE >= kStoreE4M3, KN = STORE == kStoreKN;
+    constexpr int K = WIDE ? 128 : 64, HALVES = K / 64, W_BYTES = NB * 2048, X_BYTES = MB * 2048;
+    constexpr int STAGE = W_BYTES + HALVES * X_BYTES * (SPLIT_X ? 2 : 1), NQ = STAGE / 1024;
+    static_assert(!KN || NB == 4, "rows of 128 bytes");
+    const int r16 = lane & 15, g = lane >> 4, kb = kgroup16(g);
+    const int count = p1 - p0, mine = count > wave ? (count - wave + WAVES - 1) / WAVES : 0;
+    const int cols = min(16 * NB, out - n0);
+    const uint32_t ring_lds = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)ring);
+    auto piece_at = [&](int i) {
+        const int p = wave + i * WAVES;
+        return p0 + (p + turn < count ? p + turn : p + turn - count);
+    };
+    // A lane's 16 bytes of an instruction of 8 rows; k-contiguous rows are swizzled by
+    // a_swizzle (period 16 rows), (K, N) rows by b_swizzle (32 rows, two of them alike).
+    uint32_t w_off[2];
+    int pos[2];                   // first byte of the lane's piece in its 128
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int row = 8 * q + lane / 8;
+        pos[q] = ((lane % 8) ^ a_swizzle<128>(row)) * 16;
+        if constexpr (KN) {
+            const int k = 16 * q + lane / 8, c = ((lane % 8) ^ b_swizzle<128, 16>(k)) * 16;   // (k and k + 8 are alike)
+            w_off[q] = c < 2 * cols ? (uint32_t)(lane / 8) * (uint32_t)ld + (uint32_t)c : kOobOffset;
+        } else {
+            w_off[q] = (uint32_t)row * (uint32_t)ld + (uint32_t)pos[q];
+        }
+    }
+    auto uniform = [](const void* p, uint32_t bytes) {
+        const int32x4_t r = rsrc_words(p, bytes);
+        return int32x4_t{__builtin_amdgcn_readfirstlane(r[0]), __builtin_amdgcn_readfirstlane(r[1]),
+                         __builtin_amdgcn_readfirstlane(r[2]), kBufferFlags};
+    };
+    float scale[S];
+    const int32x4_t rx = uniform(x, x_bytes);
+    auto fill = [&](int i, int slot, float& s) __attribute__((always_inline)) {
+        const bool live = i < mine;
+        const int p = __builtin_amdgcn_readfirstlane(piece_at(live ? i : 0)), k0 = p * K, left = live ? in - k0 : 0;   // elements
+        const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)(ring_lds + (uint32_t)(slot * STAGE)));
+        if constexpr (KN) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int k = k0 + 8 * q;
+                // up to the end of the last row
+                const uint32_t bytes = left > 8 * q ? (uint32_t)min(8, left - 8 * q) * (uint32_t)ld - 2u * (uint32_t)n0 : 0u;
+                dma_b128(uniform(w + (size_t)min(k, in) * (size_t)ld + 2 * (size_t)n0, bytes), to + q * 1024, w_off[(q >> 1) & 1], 0u);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2 * NB; ++q) {
+                const int skip = 16 * (q >> 1);
+                dma_b128(uniform(w + (size_t)(n0 + skip) * (size_t)ld, (uint32_t)max(0, cols - skip) * (uint32_t)ld), to + q * 1024,
+                         pos[q & 1] < (WIDE ? left : 2 * left) ? w_off[q & 1] : kOobOffset, (uint32_t)(WIDE ? k0 : 2 * k0));
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+            for (int q = 0; q < 2 * MB; ++q) {
+                const uint32_t off = x_row[q] != kOobOffset && 128 * h + pos[q & 1] < 2 * left ? x_row[q] + (uint32_t)pos[q & 1] : kOobOffset;
+                const uint32_t at = to + W_BYTES + (2 * MB * h + q) * 1024, soff = (uint32_t)(2 * k0 + 128 * h);
+                dma_b128(rx, at, off, soff);
+                if constexpr (SPLIT_X) dma_b128(rx, at + HALVES * X_BYTES, off, soff + x_low);
+            }
+        if constexpr (WIDE) s = live ? scales[p] : 0.0f;
+    };
+#pragma unroll
+    for (int s = 0; s < S; ++s) fill(s, s, scale[s]);
+    for (int i0 = 0; i0 < mine; i0 += S) {
+#pragma unroll
+        for (int slot = 0; slot < S; ++slot) {
+            const int i = i0 + slot;
+            if (i >= mine) break;
+            wait_vmcnt<(S - 1) * NQ>();
+            const uint8_t *const st = ring + slot * STAGE, *const sx = st + W_BYTES;
+            constexpr int STEPS = WIDE ? 4 : 2;                  // of 32 k
+            u32x4 wf[NB][2], xf[MB][STEPS], lf[SPLIT_X ? MB : 1][SPLIT_X ? STEPS : 1];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (KN) {
+                        const int krow = 8 * kb + (r16 >> 2), n = 16 * b + 4 * (r16 & 3);
+                        const uint8_t* q = st + (krow + 32 * h) * 128 + 16 * ((n >> 3) ^ b_swizzle<128, 16>(krow)) + 8 * (r16 & 1);
+                        const u32x2 lo = ds_read_tr16(q), hi = ds_read_tr16(q + 4 * 128);
+                        wf[b][h] = u32x4{lo.x, lo.y, hi.x, hi.y};
+                    } else {
+                        wf[b][h] = *reinterpret_cast<const u32x4*>(st + b * 2048 + r16 * 128 + 16 * ((4 * h + kb) ^ a_swizzle<128>(r16)));
+                    }
+                }
+#pragma unroll
+            for (int j = 0; j < MB; ++j)
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) {
+                    // 8-bit weights have 16 consecutive k a lane
+                    const int half = WIDE ? s >> 1 : 0, chunk = WIDE ? 2 * kb + (s & 1) : 4 * s + kb;
+                    const uint8_t* q = sx + half * X_BYTES + j * 2048 + r16 * 128 + 16 * (chunk ^ a_swizzle<128>(r16));
+                    xf[j][s] = *reinterpret_cast<const u32x4*>(q);
+                    if constexpr (SPLIT_X) lf[j][s] = *reinterpret_cast<const u32x4*>(q + HALVES * X_BYTES);
+                }
+            const float block_scale = WIDE ? scale[slot] : 1.0f;
+            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");     // the slot has been read
+            fill(i + S, slot, scale[slot]);
+            const int k0 = piece_at(i) * K;
+            floatx4 sum[WIDE ? NB : 1][WIDE ? MB : 1];
+            if constexpr (WIDE) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int j = 0; j < MB; ++j) sum[b][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int valid = in - (k0 + (WIDE ? 64 * (s >> 1) + 16 * kb + 8 * (s & 1) : 32 * s + 8 * kb));
+                const bool tail = k0 + K > in;
+                if (tail) {
+#pragma unroll
+                    for (int j = 0; j < MB; ++j) {
+                        xf[j][s] = keep_first(xf[j][s], valid);
+                        if constexpr (SPLIT_X) lf[j][s] = keep_first(lf[j][s], valid);
+                    }
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    u32x4 wv;
+                    if constexpr (WIDE) {
+                        u32x2 v{wf[b][s >> 1][2 * (s & 1)], wf[b][s >> 1][2 * (s & 1) + 1]};
+                        if (tail) {
+                            const u32x4 kept = keep_bytes(u32x4{v.x, v.y, 0u, 0u}, valid);
+                            v = u32x2{kept[0], kept[1]};
+                        }
+                        wv = widen<DT, STORE == kStoreE4M3 ? kE4M3 : kE5M2>(v.x, v.y);
+                    } else {
+                        wv = wf[b][s];
+                        if (tail && !KN) wv = keep_first(wv, valid);    // ((K, N) rows past the last are zeros)
+                    }
+#pragma unroll
+                    for (int j = 0; j < MB; ++j) {
+                        floatx4& to = WIDE ? sum[WIDE ? b : 0][WIDE ? j : 0] : acc[b][j];
+                        if constexpr (SPLIT_X) to = mfma_16x16x32<DT>(wv, lf[j][s], to);
+                        to = mfma_16x16x32<DT>(wv, xf[j][s], to);
+                    }
+                }
+            }
+            if constexpr (WIDE) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int j = 0; j < MB; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[b][j][e] = __builtin_fmaf(block_scale, sum[b][j][e], acc[b][j][e]);
+            }
+        }
+    }
+    wait_vmcnt<0>();              // nothing lands in the ring after this
+}
+
+// KIND: kExpertBlocks columns, kExpertRows rows, kExpertWaves waves.  ODD: everything
+// through registers.
+template <int DT, int STORE, bool ODD, bool SECOND, int KIND>
+__global__ __launch_bounds__(64 * kExpertWaves[KIND], KIND == 1 ? ODD || STORE >= kStoreE4M3 ? 2 : 3 : 1) void expert_products(ExpertsArgs a)
+{
+    constexpr bool WIDE = STORE >= kStoreE4M3, KN = STORE == kStoreKN;
+    constexpr int NB = KN ? 4 : kExpertBlocks[KIND], MB = kExpertRows[KIND], WAVES = kExpertWaves[KIND], THREADS = 64 * WAVES;
+    constexpr int S = KIND == 0 && STORE == kStoreNK ? 2 : 1;
+    constexpr int COLS = 16 * NB, PART = COLS * 17, STAGE = NB * 2048 + MB * (WIDE ? 4096 : 2048) * (SECOND ? 2 : 1);
+    constexpr int PARTS = WAVES * PART * 4, RING = ODD ? 0 : WAVES * S * STAGE;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[RING > PARTS ? RING : PARTS];
     __shared__ int before;
+    extern __shared__ __attribute__((aligned(16))) uint8_t table[];
+    float* const part = reinterpret_cast<float*>(smem);       // the waves' sums, after the rings
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tid = threadIdx.x;
     const int r16 = lane & 15, g = lane >> 4;
-    make_table(t, a, lane, wave);
-    const int blocks_n = (a.out + COLS - 1) / COLS, pieces = (a.in + kBlock - 1) / kBlock;
-    const int used = __builtin_amdgcn_readfirstlane(t.n_used);
+    const RouteTable t(table, a.tokens * a.top, a.experts);
+    make_table<WAVES>(t, a, lane, wave);
+    const int blocks_n = (a.out + COLS - 1) / COLS, scale_blocks = (a.in + kBlock - 1) / kBlock;
+    const int used = __builtin_amdgcn_readfirstlane(*t.n_used);
     const int units = used * blocks_n * a.splits;
-    // Where column c of a unit's block i sits in its rows of LDS: (K, N) weights give a
+    // Where column c of a unit sits in its rows of LDS: in registers (K, N) weights give a
     // lane 4 neighbouring columns, one in each block.
-    auto column = [](int c) { return STORE == kStoreKN ? (c & 3) * 16 + (c >> 2) : c; };
+    auto column = [](int c) { return KN && ODD ? (c & 3) * 16 + (c >> 2) : c; };
 
     // Rows of tokens without a choice, where no unit would write them; with logits that
     // cannot be ranked the row is NaN.
@@ -411,67 +599,80 @@ __global__ __launch_bounds__(kExpertThreads, 2) void expert_products(ExpertsArgs
         return a.routed && t.ids[token * a.top] < 0 && t.weights[token * a.top] != t.weights[token * a.top] ? __builtin_nanf("") : 0.0f;
     };
     if (SECOND && used == 0) {
-        for (int64_t i = (int64_t)blockIdx.x * kExpertThreads + tid; i < (int64_t)a.tokens * a.out; i += (int64_t)gridDim.x * kExpertThreads)
+        for (int64_t i = (int64_t)blockIdx.x * THREADS + tid; i < (int64_t)a.tokens * a.out; i += (int64_t)gridDim.x * THREADS)
             a.y[i] = act_cast<DT>(row_without((int)(i / a.out)), false);
         return;
     }
-    const AnyRsrc rx = make_any_rsrc(a.x, SECOND ? (uint32_t)(a.tokens * a.top) * (uint32_t)a.mid_row * 4u : (uint32_t)a.tokens * (uint32_t)a.in * 2u);
+    const uint32_t x_bytes = SECOND ? (uint32_t)(a.tokens * a.top) * (uint32_t)a.mid_row * 4u : (uint32_t)a.tokens * (uint32_t)a.in * 2u;
+    const AnyRsrc rx = make_any_rsrc(a.x, x_bytes);
     for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
         const int nb = unit % blocks_n, rest = unit / blocks_n, split = rest % a.splits, u = rest / a.splits;
         const int expert = __builtin_amdgcn_readfirstlane(t.used[u]), n0 = nb * COLS;
         const int first = __builtin_amdgcn_readfirstlane(t.start[expert]), count = __builtin_amdgcn_readfirstlane(t.count[expert]);
-        const uint8_t* w = a.w + (size_t)expert * (size_t)(STORE == kStoreKN ? a.in : a.out) * (size_t)a.ld;
-        const float* scales = STORE >= kStoreE4M3
-                                  ? a.scales + ((size_t)expert * (size_t)((a.out + kBlock - 1) / kBlock) + (size_t)(n0 / kBlock)) * (size_t)pieces
-                                  : nullptr;
-        const int p0 = (int)((int64_t)pieces * split / a.splits), p1 = (int)((int64_t)pieces * (split + 1) / a.splits);
-        auto pass = [&](auto blocks, int row0) __attribute__((always_inline)) {
-            constexpr int MB = decltype(blocks)::value;
-            floatx4 acc[NB][MB];
-            uint32_t x_off[MB];
+        const uint8_t* w = a.w + (size_t)expert * (size_t)(KN ? a.in : a.out) * (size_t)a.ld;
+        const float* scales = WIDE ? a.scales + ((size_t)expert * (size_t)((a.out + kBlock - 1) / kBlock) + (size_t)(n0 / kBlock)) * (size_t)scale_blocks
+                                   : nullptr;
+        // where a row of X begins, in bytes
+        auto row_of_x = [&](int r) {
+            const int slot = t.sorted[first + min(r, count - 1)];
+            return r >= count ? kOobOffset : SECOND ? (uint32_t)slot * (uint32_t)a.mid_row * 4u : (uint32_t)(slot / a.top) * (uint32_t)a.in * 2u;
+        };
+        // The unit's share of `pieces` of k.
+        auto from = [&](int pieces, int s) { return (int)((int64_t)pieces * s / a.splits); };
+        // Adds the waves' sums of 16 rows from row0 on and hands them on.
+        auto finish = [&](const floatx4* sums, int row0) __attribute__((always_inline)) {
+            __syncthreads();           // the rings, or the sums of the rows before, are read
 #pragma unroll
-            for (int j = 0; j < MB; ++j) {
-                const int r = row0 + 16 * j + r16;
-                const int slot = t.sorted[first + min(r, count - 1)];
-                x_off[j] = r >= count ? kOobOffset : SECOND ? (uint32_t)slot * (uint32_t)a.mid_row * 4u : (uint32_t)(slot / a.top) * (uint32_t)a.in * 2u;
+            for (int i = 0; i < NB; ++i)
 #pragma unroll
-                for (int i = 0; i < NB; ++i) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-            }
-            expert_sums<DT, STORE, ODD, SECOND, NB, MB>(acc, rx, x_off, (uint32_t)a.mid_row * 2u, w, scales, a.ld, n0, a.in, a.out, p0, p1, wave, lane);
+                for (int e = 0; e < 4; ++e) part[wave * PART + (16 * i + 4 * g + e) * 17 + r16] = sums[i * MB][e];
+            __syncthreads();
+            for (int o = tid; o < 16 * COLS; o += THREADS) {
+                const int row = o / COLS, c = o % COLS, r = row0 + row;
+                if (r >= count || n0 + c >= a.out) continue;
+                float z = 0.0f;
 #pragma unroll
-            for (int j = 0; j < MB; ++j) {
-                if (row0 + 16 * j >= count) break;
-                __syncthreads();       // the sums of the block before are read
-#pragma unroll
-                for (int i = 0; i < NB; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) part[wave * PART + (16 * i + 4 * g + e) * 17 + r16] = acc[i][j][e];
-                __syncthreads();
-                for (int o = tid; o < 16 * COLS; o += kExpertThreads) {
-                    const int row = o / COLS, c = o % COLS, r = row0 + 16 * j + row;
-                    if (r >= count || n0 + c >= a.out) continue;
-                    float z = 0.0f;
-#pragma unroll
-                    for (int v = 0; v < kExpertWaves; ++v) z += part[v * PART + column(c) * 17 + row];
-                    const int slot = t.sorted[first + r];
-                    if constexpr (SECOND) {
-                        __hip_atomic_store(a.part + ((size_t)slot * (size_t)a.splits + (size_t)split) * (size_t)a.out + (size_t)(n0 + c), z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                    } else {
-                        const float h = t.weights[slot] * (z > 0.0f ? z : 0.0f);
-                        const uint16_t hi = act_cast<DT>(h, false);
-                        const float back = to_float<DT>(hi);
-                        const uint16_t lo = __builtin_fabsf(back) < __builtin_inff() ? act_cast<DT>(h - back, false) : (uint16_t)0;
-                        uint16_t* const to = a.mid + (size_t)slot * (size_t)a.mid_row * 2 + (size_t)(n0 + c);
-                        to[0] = hi;
-                        to[a.mid_row] = lo;
-                    }
+                for (int v = 0; v < WAVES; ++v) z += part[v * PART + column(c) * 17 + row];
+                const int slot = t.sorted[first + r];
+                if constexpr (SECOND) {
+                    __hip_atomic_store(a.part + ((size_t)slot * (size_t)a.splits + (size_t)split) * (size_t)a.out + (size_t)(n0 + c), z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                } else {
+                    const float h = t.weights[slot] * (z > 0.0f ? z : 0.0f);
+                    const uint16_t hi = act_cast<DT>(h, false);
+                    const float back = to_float<DT>(hi);
+                    const uint16_t lo = __builtin_fabsf(back) < __builtin_inff() ? act_cast<DT>(h - back, false) : (uint16_t)0;
+                    uint16_t* const to = a.mid + (size_t)slot * (size_t)a.mid_row * 2 + (size_t)(n0 + c);
+                    to[0] = hi;
+                    to[a.mid_row] = lo;
                 }
             }
         };
-        if (count <= 16) {
-            pass(std::integral_constant<int, 1>{}, 0);
-        } else {
-            for (int row0 = 0; row0 < count; row0 += 64) pass(std::integral_constant<int, 4>{}, row0);
+        const int pieces = WIDE || ODD ? scale_blocks : (a.in + 63) / 64, p0 = from(pieces, split), p1 = from(pieces, split + 1);
+        for (int row0 = 0; row0 < count; row0 += 16 * MB) {
+            floatx4 acc[NB][MB];
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int j = 0; j < MB; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (ODD) {
+                uint32_t x_off[MB];
+#pragma unroll
+                for (int j = 0; j < MB; ++j) x_off[j] = row_of_x(row0 + 16 * j + r16);
+                expert_sums<DT, STORE, SECOND, NB, MB, WAVES>(acc, rx, x_off, (uint32_t)a.mid_row * 2u, w, scales, a.ld, n0, a.in, a.out, p0, p1,
+                                                              wave, lane);
+            } else {
+                uint32_t x_row[2 * MB];
+#pragma unroll
+                for (int q = 0; q < 2 * MB; ++q) x_row[q] = row_of_x(row0 + 8 * q + lane / 8);
+                expert_stream<DT, STORE, SECOND, NB, MB, S, WAVES>(acc, a.x, x_bytes, x_row, (uint32_t)a.mid_row * 2u, w, scales, a.ld, n0, a.in,
+                                                                   a.out, p0, p1, smem + wave * (S * STAGE), unit % max(p1 - p0, 1), wave, lane);
+            }
+#pragma unroll
+            for (int j = 0; j < MB; ++j) {
+                if (row0 + 16 * j >= count) break;
+                finish(&acc[0][j], row0 + 16 * j);
+            }
+            if (row0 + 16 * MB < count) __syncthreads();       // the rings are filled again
         }
         if constexpr (SECOND) {
             wait_vmcnt<0>();           // this wave's sums have reached device scope
@@ -480,7 +681,7 @@ __global__ __launch_bounds__(kExpertThreads, 2) void expert_products(ExpertsArgs
             __syncthreads();
             if (before == used * a.splits - 1) {
                 asm volatile("" ::: "memory");   // the loads below stay after the count that allowed them
-                for (int o = tid; o < a.tokens * COLS; o += kExpertThreads) {
+                for (int o = tid; o < a.tokens * COLS; o += THREADS) {
                     const int token = o / COLS, c = n0 + o % COLS;
                     if (c >= a.out) continue;
                     float z = row_without(token);
