@@ -51,12 +51,12 @@ int launch_quantize(QuantizeArgs a, int64_t count, int dtype, int format, int fo
 {
     a.tiles_r = (int)blocks_of(a.rows);
     a.tiles_c = (int)blocks_of(a.cols);
-    a.vec = a.cols % 8 == 0 && aligned(a.x, 16) && (!a.mask || aligned(a.mask, 16));
+    const int vec = a.cols % 8 == 0 && aligned(a.x, 16) && (!a.mask || aligned(a.mask, 16));
     const int64_t tiles = count * a.tiles_r * a.tiles_c;
     if (!launchable(tiles, kQuantizeThreads)) return GEMM_RELU_ERR_TOO_LARGE;
     void* args[] = {&a};
-    return enqueue(quantize_kernel(dtype, format, form == GEMM_RELU_SCALES_TILES), dim3((unsigned)tiles), kQuantizeThreads, args,
-                   stream);
+    return enqueue(quantize_kernel(dtype, format, form == GEMM_RELU_SCALES_TILES, vec), dim3((unsigned)tiles), kQuantizeThreads,
+                   args, stream);
 }
 
 // Tiles of `tile` x `tile` that a product can have: whole ones, and a partial one for each group.
@@ -220,7 +220,7 @@ int gemm_relu_quantize_blocks(const void* X, const void* mask, void* Q, float* s
     int cus = 0;
     if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;
     QuantizeArgs a{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(mask), static_cast<uint8_t*>(Q), scales,
-                   static_cast<uint8_t*>(QT), scales_t, (int)R, (int)C, 0, 0, ldq, ldqt, power_of_two, 0};
+                   static_cast<uint8_t*>(QT), scales_t, (int)R, (int)C, 0, 0, ldq, ldqt, power_of_two};
     return launch_quantize(a, count, dtype, format, form, static_cast<hipStream_t>(stream));
 }
 
@@ -304,7 +304,7 @@ int gemm_relu_blocks_backward(const void* dC, const void* C, const void* XT, con
     uint8_t *q = reinterpret_cast<uint8_t*>(ws + space.q), *qt = reinterpret_cast<uint8_t*>(ws + space.qt);
     float *sq = reinterpret_cast<float*>(ws + space.s), *st = reinterpret_cast<float*>(ws + space.st);
     QuantizeArgs d{static_cast<const uint16_t*>(dC), relu ? static_cast<const uint16_t*>(C) : nullptr, want_x ? q : nullptr, sq,
-                   want_w ? qt : nullptr, st, (int)M, (int)N, 0, 0, space.ldq, space.ldqt, 0, 0};
+                   want_w ? qt : nullptr, st, (int)M, (int)N, 0, 0, space.ldq, space.ldqt, 0};
     rc = launch_quantize(d, 1, dtype, format, GEMM_RELU_SCALES_ROWS, s);
     const int bf16 = dtype == GEMM_RELU_BF16;
     if (want_x && rc == GEMM_RELU_OK) {

@@ -36,13 +36,14 @@ __device__ __forceinline__ Scale make_scale(uint32_t amax, int power_of_two)
 // x / s, correctly rounded: the product with the rounded reciprocal is off by at
 // most two units in the last place, and one step with its exact remainder
 // corrects that.  (x has 8 or 11 bits, and so has the magnitude that s was made
-// of: every pair of them has been compared with the exact quotient.)  Infinities
-// and NaN are left as they are (their remainder is not a number).
+// of: every pair of them has been compared with the exact quotient.)  With CHECK
+// infinities and NaN are left as they are (their remainder is not a number).
+template <bool CHECK>
 __device__ __forceinline__ float divide(float x, Scale c)
 {
     const float t = x * c.inverse;
     const float q = __builtin_fmaf(__builtin_fmaf(-t, c.s, x), c.inverse, t);
-    return __builtin_fabsf(x) < __builtin_inff() ? q : x;
+    return !CHECK || __builtin_fabsf(x) < __builtin_inff() ? q : x;
 }
 
 // Two 8-bit values in the low or high half of `old`.
@@ -55,104 +56,111 @@ __device__ __forceinline__ uint32_t to_8bit(float x, float y, uint32_t old)
         return (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(x, y, (int)old, HIGH);
 }
 
-// The magnitude's bits of a 16-bit float, 0 where it is infinite or NaN.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max_pairs(uint32_t a, uint32_t b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+// The largest within 16 lanes, in all of them.
+__device__ __forceinline__ uint32_t row_max_pairs(uint32_t v)
+{
+    v = max_pairs(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, false));   // row_ror 1, 2, 4, 8
+    v = max_pairs(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, false));
+    v = max_pairs(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
+    return max_pairs(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));
+}
+// The largest over the wave's 4 rows of 16 lanes, in all of them.
+__device__ __forceinline__ uint32_t column_max_pairs(uint32_t v)
+{
+    v = max_pairs(v, (uint32_t)__shfl_xor((int)v, 16));
+    return max_pairs(v, (uint32_t)__shfl_xor((int)v, 32));
+}
+
+// The magnitudes of a pair of 16-bit floats, 0 where infinite or NaN.
 template <int DT>
-__device__ __forceinline__ uint32_t finite_magnitude(uint16_t h)
+__device__ __forceinline__ uint32_t finite_magnitudes(uint32_t pair)
 {
     constexpr uint32_t inf = DT == kF16 ? 0x7c00u : 0x7f80u;
-    const uint32_t m = h & 0x7fffu;
-    return m < inf ? m : 0u;
+    const uint32_t m = pair & 0x7fff7fffu;
+    return ((m & 0xffffu) < inf ? m & 0xffffu : 0u) | ((m >> 16) < inf ? m & 0xffff0000u : 0u);
 }
 
 // Rows of a transposed tile in LDS, 8-byte pieces.
 constexpr int kTransposedRow = 136;
 
-template <int DT, int FORMAT, bool TILES>
-__global__ __launch_bounds__(kQuantizeThreads) void quantize_blocks(QuantizeArgs a)
+struct Shared {
+    __attribute__((aligned(16))) uint8_t turned[kBlock * kTransposedRow];
+    uint32_t column_amax[4][kBlock / 2];      // pairs
+    Scale row_scale[kBlock], column_scale[kBlock];
+};
+
+// What a thread does with its 8 x 8 elements (v[row]: 4 pairs) at (row, col).
+//  CHECK: some of the tile's are infinite or NaN.
+template <int DT, int FORMAT, bool TILES, bool CHECK>
+__device__ __forceinline__ void quantize_tile(const QuantizeArgs& a, const u32x4 (&v)[8], Shared& sh, int64_t matrix, int tr, int tc)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t turned[kBlock * kTransposedRow];
-    __shared__ uint32_t column_amax[4][kBlock];
-    __shared__ Scale column_scale[kBlock];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, cc = tid & 15, rr = tid >> 4;
-    const int64_t tiles = (int64_t)a.tiles_r * a.tiles_c, matrix = (int64_t)blockIdx.x / tiles;
-    const int tile = (int)((int64_t)blockIdx.x - matrix * tiles), tr = tile / a.tiles_c, tc = tile % a.tiles_c;
-    const int row = tr * kBlock + 8 * rr, col = tc * kBlock + 8 * cc;      // this thread's 8 x 8 elements
-    const uint16_t* const x = a.x + (size_t)matrix * (size_t)a.rows * (size_t)a.cols;
-    const uint16_t* const mask = a.mask ? a.mask + (size_t)matrix * (size_t)a.rows * (size_t)a.cols : nullptr;
+    const int row = tr * kBlock + 8 * rr, col = tc * kBlock + 8 * cc;
+    auto element = [&](int i, int j) { return to_float<DT>((uint16_t)(v[i][j >> 1] >> (16 * (j & 1)))); };
+    auto magnitudes = [&](int i, int w) { return CHECK ? finite_magnitudes<DT>(v[i][w]) : v[i][w] & 0x7fff7fffu; };
 
-    u32x4 v[8];
-    if (a.vec) {
+    // pairs of columns: the largest of this thread's rows
+    uint32_t down[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const size_t at = (size_t)(row + i) * (size_t)a.cols + (size_t)col;
-            const bool inside = row + i < a.rows && col < a.cols;
-            v[i] = inside ? *reinterpret_cast<const u32x4*>(x + at) : u32x4{0u, 0u, 0u, 0u};
-            if (mask && inside) v[i] = mask_chunk<DT>(v[i], *reinterpret_cast<const u32x4*>(mask + at));
-        }
-    } else {
+    for (int w = 0; w < 4; ++w) {
+        down[w] = magnitudes(0, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                uint32_t pair = 0;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int c = col + 2 * w + h;
-                    const size_t at = (size_t)(row + i) * (size_t)a.cols + (size_t)c;
-                    if (row + i < a.rows && c < a.cols) {
-                        const uint16_t e = mask ? mask_one<DT>(x[at], mask[at]) : x[at];
-                        pair |= (uint32_t)e << (16 * h);
-                    }
-                }
-                v[i][w] = pair;
-            }
-    }
-    auto element = [&](int i, int j) { return (uint16_t)(v[i][j >> 1] >> (16 * (j & 1))); };
-
-    uint32_t row_amax[8];
-    if (TILES || a.q) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m = max(m, finite_magnitude<DT>(element(i, j)));
-#pragma unroll
-            for (int d = 1; d < 16; d *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-            row_amax[i] = m;
-        }
+        for (int i = 1; i < 8; ++i) down[w] = max_pairs(down[w], magnitudes(i, w));
     }
     Scale whole;      // TILES: the tile's
     if constexpr (TILES) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, row_amax[i]);
-        m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-        m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-        if (lane == 0) column_amax[wave][0] = m;
+        uint32_t m = max_pairs(max_pairs(down[0], down[1]), max_pairs(down[2], down[3]));
+        m = column_max_pairs(row_max_pairs(m));
+        if (lane == 0) sh.column_amax[wave][0] = max(m & 0xffffu, m >> 16);
         __syncthreads();
-        m = max(max(column_amax[0][0], column_amax[1][0]), max(column_amax[2][0], column_amax[3][0]));
+        m = max(max(sh.column_amax[0][0], sh.column_amax[1][0]), max(sh.column_amax[2][0], sh.column_amax[3][0]));
         whole = make_scale<DT, FORMAT>(m, a.power_of_two);
         if (tid == 0) {
+            const int64_t tiles = (int64_t)a.tiles_r * a.tiles_c;
             if (a.q) a.s[matrix * tiles + (int64_t)tr * a.tiles_c + tc] = whole.s;
             if (a.qt) a.st[matrix * tiles + (int64_t)tc * a.tiles_r + tr] = whole.s;
         }
     }
     if (a.q) {
+        if constexpr (!TILES) {
+            // Two rows' largest in a register, then one row's scale a lane, by way of LDS
+            // to the 16 lanes of the row (all in one wave, whose LDS accesses are in order).
+            uint32_t mine = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                uint32_t m[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    m[h] = max_pairs(max_pairs(magnitudes(i + h, 0), magnitudes(i + h, 1)), max_pairs(magnitudes(i + h, 2), magnitudes(i + h, 3)));
+                    m[h] = max(m[h] & 0xffffu, m[h] >> 16);
+                }
+                const uint32_t both = row_max_pairs(m[0] | (m[1] << 16));
+                if ((cc & 7) >> 1 == i >> 1) mine = (cc & 1) ? both >> 16 : both & 0xffffu;
+            }
+            if (cc < 8) {
+                const Scale c = make_scale<DT, FORMAT>(mine, a.power_of_two);
+                sh.row_scale[8 * rr + cc] = c;
+                if (row + cc < a.rows) a.s[(matrix * a.tiles_c + tc) * (int64_t)a.rows + row + cc] = c.s;
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
         uint8_t* const q = a.q + (size_t)matrix * (size_t)a.rows * (size_t)a.ldq;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (row + i >= a.rows) continue;      // (the 16 threads of a row agree)
             Scale c = whole;
-            if constexpr (!TILES) {
-                c = make_scale<DT, FORMAT>(row_amax[i], a.power_of_two);
-                if (cc == i) a.s[(matrix * a.tiles_c + tc) * (int64_t)a.rows + row + i] = c.s;
-            }
-            uint32_t w[2] = {0, 0};
+            if constexpr (!TILES) c = sh.row_scale[8 * rr + i];
+            uint32_t w[2];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                w[p] = to_8bit<FORMAT, false>(divide(to_float<DT>(element(i, 4 * p)), c), divide(to_float<DT>(element(i, 4 * p + 1)), c), 0);
-                w[p] = to_8bit<FORMAT, true>(divide(to_float<DT>(element(i, 4 * p + 2)), c), divide(to_float<DT>(element(i, 4 * p + 3)), c), w[p]);
+                w[p] = to_8bit<FORMAT, false>(divide<CHECK>(element(i, 4 * p), c), divide<CHECK>(element(i, 4 * p + 1), c), 0);
+                w[p] = to_8bit<FORMAT, true>(divide<CHECK>(element(i, 4 * p + 2), c), divide<CHECK>(element(i, 4 * p + 3), c), w[p]);
             }
+            if (row + i >= a.rows) continue;
             uint8_t* const to = q + (size_t)(row + i) * (size_t)a.ldq + (size_t)col;
             if (col + 8 <= a.cols) {
                 *reinterpret_cast<u32x2*>(to) = u32x2{w[0], w[1]};
@@ -166,35 +174,31 @@ __global__ __launch_bounds__(kQuantizeThreads) void quantize_blocks(QuantizeArgs
     if (!a.qt) return;
     if constexpr (!TILES) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, finite_magnitude<DT>(element(i, j)));
-            m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-            m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-            if (lane < 16) column_amax[wave][8 * cc + j] = m;
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t m = column_max_pairs(down[w]);
+            if (lane < 16) sh.column_amax[wave][4 * cc + w] = m;
         }
         __syncthreads();
         if (tid < kBlock) {
-            const uint32_t m = max(max(column_amax[0][tid], column_amax[1][tid]), max(column_amax[2][tid], column_amax[3][tid]));
-            const Scale c = make_scale<DT, FORMAT>(m, a.power_of_two);
-            column_scale[tid] = c;
-            if (tc * kBlock + tid < a.cols)
-                a.st[(matrix * a.tiles_r + tr) * (int64_t)a.cols + tc * kBlock + tid] = c.s;
+            const uint32_t m = max_pairs(max_pairs(sh.column_amax[0][tid >> 1], sh.column_amax[1][tid >> 1]),
+                                         max_pairs(sh.column_amax[2][tid >> 1], sh.column_amax[3][tid >> 1]));
+            const Scale c = make_scale<DT, FORMAT>((tid & 1) ? m >> 16 : m & 0xffffu, a.power_of_two);
+            sh.column_scale[tid] = c;
+            if (tc * kBlock + tid < a.cols) a.st[(matrix * a.tiles_r + tr) * (int64_t)a.cols + tc * kBlock + tid] = c.s;
         }
         __syncthreads();
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         Scale c = whole;
-        if constexpr (!TILES) c = column_scale[8 * cc + j];
-        uint32_t w[2] = {0, 0};
+        if constexpr (!TILES) c = sh.column_scale[8 * cc + j];
+        uint32_t w[2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            w[p] = to_8bit<FORMAT, false>(divide(to_float<DT>(element(4 * p, j)), c), divide(to_float<DT>(element(4 * p + 1, j)), c), 0);
-            w[p] = to_8bit<FORMAT, true>(divide(to_float<DT>(element(4 * p + 2, j)), c), divide(to_float<DT>(element(4 * p + 3, j)), c), w[p]);
+            w[p] = to_8bit<FORMAT, false>(divide<CHECK>(element(4 * p, j), c), divide<CHECK>(element(4 * p + 1, j), c), 0);
+            w[p] = to_8bit<FORMAT, true>(divide<CHECK>(element(4 * p + 2, j), c), divide<CHECK>(element(4 * p + 3, j), c), w[p]);
         }
-        *reinterpret_cast<u32x2*>(turned + (8 * cc + j) * kTransposedRow + 8 * rr) = u32x2{w[0], w[1]};
+        *reinterpret_cast<u32x2*>(sh.turned + (8 * cc + j) * kTransposedRow + 8 * rr) = u32x2{w[0], w[1]};
     }
     __syncthreads();
     uint8_t* const qt = a.qt + (size_t)matrix * (size_t)a.cols * (size_t)a.ldqt;
@@ -203,7 +207,7 @@ __global__ __launch_bounds__(kQuantizeThreads) void quantize_blocks(QuantizeArgs
     for (int s = 0; s < 4; ++s) {
         const int c = 32 * s + (tid >> 3);
         if (tc * kBlock + c >= a.cols || r >= a.rows) continue;
-        const uint8_t* const from = turned + c * kTransposedRow + 16 * (tid & 7);
+        const uint8_t* const from = sh.turned + c * kTransposedRow + 16 * (tid & 7);
         uint8_t* const to = qt + (size_t)(tc * kBlock + c) * (size_t)a.ldqt + (size_t)r;
         const u32x2 lo = *reinterpret_cast<const u32x2*>(from), hi = *reinterpret_cast<const u32x2*>(from + 8);
         if (r + 16 <= a.rows) {
@@ -214,16 +218,80 @@ __global__ __launch_bounds__(kQuantizeThreads) void quantize_blocks(QuantizeArgs
     }
 }
 
+// VEC: x and the mask allow 16-byte loads of 8 elements.
+template <int DT, int FORMAT, bool TILES, bool VEC>
+__global__ __launch_bounds__(kQuantizeThreads, 4) void quantize_blocks(QuantizeArgs a)
+{
+    __shared__ Shared sh;
+    const int tid = threadIdx.x, cc = tid & 15, rr = tid >> 4;
+    const int64_t tiles = (int64_t)a.tiles_r * a.tiles_c, matrix = (int64_t)blockIdx.x / tiles;
+    const int tile = (int)((int64_t)blockIdx.x - matrix * tiles), tr = tile / a.tiles_c, tc = tile % a.tiles_c;
+    // This thread's 8 x 8 elements.  The tile's rows begin inside 2^28 bytes of each other.
+    const int row = 8 * rr, col = 8 * cc, rows = min(kBlock, a.rows - tr * kBlock), cols = min(kBlock, a.cols - tc * kBlock);
+    const size_t origin = ((size_t)matrix * (size_t)a.rows + (size_t)tr * kBlock) * (size_t)a.cols + (size_t)tc * kBlock;
+    const uint32_t bytes = ((uint32_t)(rows - 1) * (uint32_t)a.cols + (uint32_t)cols) * 2u;
+    const uint16_t* const mask = a.mask ? a.mask + origin : a.x + origin;
+    u32x4 v[8];
+    if constexpr (VEC) {
+        const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + origin, bytes), rm = make_rsrc(mask, bytes);
+        u32x4 m[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t at = row + i < rows && col < cols ? ((uint32_t)(row + i) * (uint32_t)a.cols + (uint32_t)col) * 2u : kOobOffset;
+            v[i] = __builtin_amdgcn_raw_buffer_load_b128(rx, at, 0, 0);
+            if (a.mask) m[i] = __builtin_amdgcn_raw_buffer_load_b128(rm, at, 0, 0);
+        }
+        if (a.mask) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = mask_chunk<DT>(v[i], m[i]);
+        }
+    } else {
+        // rows of any length: dwords, shifted into place, zeros behind the row
+        const AnyRsrc rx = make_any_rsrc(a.x + origin, bytes), rm = make_any_rsrc(mask, bytes);
+#pragma unroll
+        for (int i0 = 0; i0 < 8; i0 += 4) {
+            AnyChunk x[4], m[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = row + i0 + i;
+                const uint32_t at = ((uint32_t)r * (uint32_t)a.cols + (uint32_t)col) * 2u;
+                const bool inside = r < rows && col < cols;
+                x[i] = load_any(rx, at, inside);
+                if (a.mask) m[i] = load_any(rm, at, inside);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u32x4 e = chunk_value(x[i]);
+                if (a.mask) e = mask_chunk<DT>(e, chunk_value(m[i]));
+                v[i0 + i] = keep_first(e, row + i0 + i < rows ? cols - col : 0);
+            }
+        }
+    }
+    // Whether all of the tile's elements are finite, which saves their being asked for.
+    constexpr uint32_t inf = DT == kF16 ? 0x7c00u : 0x7f80u;
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) most = max_pairs(most, v[i][w] & 0x7fff7fffu);
+    const bool finite = (most & 0xffffu) < inf && (most >> 16) < inf;
+    if (__syncthreads_and(finite)) quantize_tile<DT, FORMAT, TILES, false>(a, v, sh, matrix, tr, tc);
+    else quantize_tile<DT, FORMAT, TILES, true>(a, v, sh, matrix, tr, tc);
+}
+
+template <int DT, int FORMAT>
+const void* pick(int tiles, int vec)
+{
+    if (tiles) return vec ? (const void*)quantize_blocks<DT, FORMAT, true, true> : (const void*)quantize_blocks<DT, FORMAT, true, false>;
+    return vec ? (const void*)quantize_blocks<DT, FORMAT, false, true> : (const void*)quantize_blocks<DT, FORMAT, false, false>;
+}
+
 }  // namespace
 
-const void* quantize_kernel(int dtype, int format, int tiles)
+const void* quantize_kernel(int dtype, int format, int tiles, int vec)
 {
-    static const void* const t[2][2][2] = {
-        {{(const void*)quantize_blocks<kF16, kE4M3, false>, (const void*)quantize_blocks<kF16, kE4M3, true>},
-         {(const void*)quantize_blocks<kF16, kE5M2, false>, (const void*)quantize_blocks<kF16, kE5M2, true>}},
-        {{(const void*)quantize_blocks<kBF16, kE4M3, false>, (const void*)quantize_blocks<kBF16, kE4M3, true>},
-         {(const void*)quantize_blocks<kBF16, kE5M2, false>, (const void*)quantize_blocks<kBF16, kE5M2, true>}}};
-    return t[dtype][format][tiles];
+    if (dtype == kF16) return format == kE4M3 ? pick<kF16, kE4M3>(tiles, vec) : pick<kF16, kE5M2>(tiles, vec);
+    return format == kE4M3 ? pick<kBF16, kE4M3>(tiles, vec) : pick<kBF16, kE5M2>(tiles, vec);
 }
 
 }  // namespace gemm_relu_hip

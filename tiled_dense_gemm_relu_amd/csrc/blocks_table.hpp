@@ -24,7 +24,6 @@ struct QuantizeArgs {
     int rows, cols, tiles_r, tiles_c;
     int64_t ldq, ldqt;
     int power_of_two;
-    int vec;               // x and mask allow 16-byte loads of 8 elements
 };
 constexpr int kQuantizeThreads = 256;
 
@@ -62,8 +61,8 @@ const BlocksKernels& blocks_kernels_e4m3_e5m2();
 const BlocksKernels& blocks_kernels_e5m2_e4m3();
 const BlocksKernels& blocks_kernels_e5m2_e5m2();
 
-// [dtype][format][form == tiles]
-const void* quantize_kernel(int dtype, int format, int tiles);
+// vec: x and the mask allow 16-byte loads of 8 elements.
+const void* quantize_kernel(int dtype, int format, int tiles, int vec);
 
 // One of the two products of the expert layer for a few tokens.
 struct ExpertsArgs {
