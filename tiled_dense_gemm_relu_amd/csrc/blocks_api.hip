@@ -175,6 +175,8 @@ struct ExpertsSpace {
 };
 static_assert(((int64_t(1) << 20) + 63) / 64 <= ExpertsSpace::kMaxColumnBlocks, "a counter for each block of 64 columns");
 
+bool route_apart(int64_t tokens, int64_t experts, int64_t top) { return tokens * top * ceil_div(experts, 64) > 128; }
+
 int check_experts(int64_t tokens, int64_t n, int64_t hidden, int64_t experts, int64_t top, int b_layout)
 {
     if (b_layout != GEMM_RELU_B_KN && b_layout != GEMM_RELU_B_NK) return GEMM_RELU_ERR_BAD_LAYOUT;
@@ -399,6 +401,13 @@ int gemm_relu_experts(const void* X, const void* W1, const float* scales1, const
                        64 * kExpertWaves[kind], args, s, (size_t)route_table_bytes(slots, experts));
     };
     const bool odd1 = !even(X, K) || (!bytes && !(kn ? even(W1, hidden) : even(W1, K)));
+    // Every workgroup of the first product makes the choices for itself, unless that costs
+    // it more than a launch: a choice takes a wave about 0.1 us, for more than 64 experts longer.
+    if (logits && route_apart(tokens, experts, top)) {
+        rc = enqueue(kernels.route, dim3((unsigned)tokens), 64, args, s);
+        if (rc != GEMM_RELU_OK) return rc;
+        a.logits = nullptr;
+    }
     rc = launch(odd1, 0, space.kind1, space.units1);
     if (rc != GEMM_RELU_OK || N == 0) return rc;
     a.x = a.mid;

@@ -92,19 +92,34 @@ __device__ __forceinline__ void store_strips(uint16_t* __restrict__ C, const flo
                 __builtin_amdgcn_raw_buffer_store_b128(v, rc, off, 0, kNonTemporal);
             }
         } else {
-            constexpr int LANES = FN * 8;                             // dwords of a strip's row
-            const int cols = min(16 * FN, N - n_base);
-            for (int r = lane / LANES; r < rows; r += 64 / LANES) {
+            constexpr int LANES = FN * 8, STEP = 64 / LANES;          // dwords of a strip's row; rows a store
+            const int cols = min(16 * FN, N - n_base), place = lane % LANES;
+#pragma unroll
+            for (int r0 = 0; r0 < 16; r0 += STEP) {
+                const int r = r0 + lane / LANES;
                 uint16_t* const p = C + (size_t)(m + r) * (size_t)N + n_base;
-                const int odd = (int)(reinterpret_cast<uintptr_t>(p) >> 1) & 1, e = 2 * (lane % LANES) + odd;
-                auto element = [&](int x) { return *reinterpret_cast<const uint16_t*>(strip + at(r, x >> 3) + 2 * (x & 7)); };
-                if (e + 1 < cols)
-                    *reinterpret_cast<uint32_t*>(p + e) = (uint32_t)element(e) | ((uint32_t)element(e + 1) << 16);
-                else if (e < cols)
-                    p[e] = element(e);
-                if (odd && e == 1 && cols > 0) p[0] = element(0);
+                const int odd = (int)(reinterpret_cast<uintptr_t>(p) >> 1) & 1, e = 2 * place + odd;
+                auto element = [&](int x) { return *reinterpret_cast<const uint16_t*>(strip + at(r, (x >> 3) & (CHUNKS - 1)) + 2 * (x & 7)); };
+                const uint32_t lo = element(e), hi = element(e + 1), first = element(0);
+                if (r < rows) {
+                    if (e + 1 < cols) *reinterpret_cast<uint32_t*>(p + e) = lo | (hi << 16);
+                    else if (e < cols) p[e] = (uint16_t)lo;
+                    if (odd && place == 0 && cols > 0) p[0] = (uint16_t)first;
+                }
             }
         }
+    }
+}
+
+// Asks the scheduler for N times a matrix instruction and a block's additions: a wave
+// that issues two matrix instructions in a row waits for the first with its additions.
+template <int N>
+__device__ __forceinline__ void interleave()
+{
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);      // matrix
+        __builtin_amdgcn_sched_group_barrier(0x2, 5, 0);      // vector
     }
 }
 
@@ -464,6 +479,7 @@ __global__ __launch_bounds__(Cfg::THREADS, 1) void blocks_dma(BlocksArgs a)
                     t[u % (LAG + 1)] = mfma_block<FB, FA>(w[i], x[j % 3]);
                     if (u >= LAG) finish(u - LAG);
                 }
+                interleave<FN>();
                 __builtin_amdgcn_sched_barrier(0);
             }
             const int next = (slot + 1) & (S - 1);
@@ -481,6 +497,7 @@ __global__ __launch_bounds__(Cfg::THREADS, 1) void blocks_dma(BlocksArgs a)
                     t[u % (LAG + 1)] = mfma_block<FB, FA>(w[i], x[j % 3]);
                     finish(u - LAG);
                 }
+                interleave<2>();
                 w[i] = fragment(smem + next * Cfg::B_STAGE, b_off, i);
 #pragma unroll
                 for (int q = i * NQ / FN; q < (i + 1) * NQ / FN; ++q) dma(slot, q);

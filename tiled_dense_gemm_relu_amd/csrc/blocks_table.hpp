@@ -87,11 +87,12 @@ constexpr int kMaxTokens = 64, kMaxTop = 16, kMaxExperts = 1024;
 // for many rows an expert.
 constexpr int kNumExpertKinds = 3;
 constexpr int kExpertBlocks[kNumExpertKinds] = {2, 4, 4}, kExpertRows[kNumExpertKinds] = {1, 1, 2}, kExpertWaves[kNumExpertKinds] = {8, 4, 4};
-constexpr int64_t route_table_bytes(int64_t slots, int64_t experts) { return slots * 8 + experts * 8 + 16; }
+constexpr int64_t route_table_bytes(int64_t slots, int64_t experts) { return (slots + 7) / 8 * 16 + slots * 6 + experts * 8 + 16; }
 
 struct ExpertsKernels {
     // [storage: NK, KN, e4m3, e5m2][odd rows][second product][kind]
     const void* products[4][2][2][kNumExpertKinds];
+    const void* route;
 };
 const ExpertsKernels& experts_kernels_f16();
 const ExpertsKernels& experts_kernels_bf16();

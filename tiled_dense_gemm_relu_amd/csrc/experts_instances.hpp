@@ -26,6 +26,7 @@ ExpertsKernels make_experts_table()
     fill_experts<DT, kStoreE4M3, true>(t.products[kStoreE4M3][1]);
     fill_experts<DT, kStoreE5M2, false>(t.products[kStoreE5M2][0]);
     fill_experts<DT, kStoreE5M2, true>(t.products[kStoreE5M2][1]);
+    t.route = (const void*)route_tokens;
     return t;
 }
 

@@ -32,13 +32,14 @@ struct RouteTable {
     uint16_t* start;         // where an expert's slots begin in `sorted`
     uint16_t* used;          // the experts that have slots
 
+    // (ids are read 8 at a time)
     __device__ __forceinline__ RouteTable(uint8_t* p, int slots, int experts)
     {
-        weights = reinterpret_cast<float*>(p);
+        ids = reinterpret_cast<int16_t*>(p);
+        weights = reinterpret_cast<float*>(ids + (slots + 7) / 8 * 8);
         count = reinterpret_cast<int*>(weights + slots);
         n_used = count + experts;
-        ids = reinterpret_cast<int16_t*>(n_used + 1);
-        sorted = reinterpret_cast<uint16_t*>(ids + slots);
+        sorted = reinterpret_cast<uint16_t*>(n_used + 1);
         start = sorted + slots;
         used = start + experts;
     }
@@ -52,77 +53,118 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v)
 
 __device__ __forceinline__ float wave_sum(float v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
-    return v;
+    const int s = wave_scan(__builtin_bit_cast(int, v), [](int a, int b) {
+        return __builtin_bit_cast(int, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
+    });
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(s, 63));
 }
 
-// One token's choices by one wave: the largest logits, ties to the lowest index,
-// and their softmax weights; lane j gets choice j.  Logits are compared as unsigned
-// keys in their order; key 0 is never chosen (-inf, and what has been chosen).
-__device__ inline void choose(const float* __restrict__ logits, int experts, int top, bool renormalize, int lane, int& id,
-                              float& weight)
+// The choices of N tokens by one wave: of each token the largest logits, ties to the
+// lowest index, and their softmax weights; lane j gets choice j.  l[n][r] is logit
+// 64 r + lane of token n (-inf past the last).  The tokens' steps are independent, so
+// their chains of moves between lanes overlap.  Logits are compared as unsigned keys in
+// their order; key 0 is never chosen (-inf, and what has been chosen).
+template <int N, int R>
+__device__ __forceinline__ void choose(float (&l)[N][R], int top, bool renormalize, int lane, int (&id)[N], float (&weight)[N])
 {
-    constexpr int R = kMaxExperts / 64;
-    const int rounds = (experts + 63) / 64;
-    float l[R];
-    uint32_t key[R];
-    bool bad = false;
-    float largest = -__builtin_inff();
+    uint32_t key[N][R];
+    bool bad[N];
+    float largest[N], mine[N];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        key[r] = 0;
-        l[r] = -__builtin_inff();
-        if (r < rounds && 64 * r + lane < experts) {
-            l[r] = logits[64 * r + lane] + 0.0f;      // (-0 and +0 are equal)
-            const uint32_t bits = __builtin_bit_cast(uint32_t, l[r]);
-            bad |= !(l[r] < __builtin_inff());
-            key[r] = l[r] == -__builtin_inff() ? 0u : (bits & 0x80000000u) ? ~bits : bits | 0x80000000u;
-        }
-    }
-    id = -1;
-    weight = 0.0f;
-    if (__ballot(bad)) {
-        weight = __builtin_nanf("");
-        return;
-    }
-    float mine = 0.0f;
-    for (int j = 0; j < top; ++j) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (r < rounds) m = max(m, key[r]);
-        m = wave_max(m);
-        if (m == 0) break;
-        bool found = false;
+    for (int n = 0; n < N; ++n) {
+        bad[n] = false;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (r >= rounds || found) continue;
-            const uint64_t at = __ballot(key[r] == m);
-            if (!at) continue;
-            found = true;
-            const int who = __builtin_ctzll(at);
-            const float value = __shfl(l[r], who);
-            if (j == 0) largest = value;
-            if (lane == who) key[r] = 0;
-            if (lane == j) {
-                id = 64 * r + who;
-                mine = value;
+            l[n][r] += 0.0f;                              // (-0 and +0 are equal)
+            const uint32_t bits = __builtin_bit_cast(uint32_t, l[n][r]);
+            bad[n] |= !(l[n][r] < __builtin_inff());
+            key[n][r] = l[n][r] == -__builtin_inff() ? 0u : (bits & 0x80000000u) ? ~bits : bits | 0x80000000u;
+        }
+        bad[n] = __ballot(bad[n]) != 0;
+        id[n] = -1;
+        largest[n] = mine[n] = 0.0f;
+    }
+    for (int j = 0; j < top; ++j) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int r = 0; r < R; ++r) m = max(m, key[n][r]);
+            m = wave_max(m);
+            bool found = m == 0 || bad[n];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint64_t at = __ballot(key[n][r] == m);
+                if (found || !at) continue;
+                found = true;
+                const int who = __builtin_ctzll(at);
+                const float value = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, l[n][r]), who));
+                if (j == 0) largest[n] = value;
+                if (lane == who) key[n][r] = 0;
+                if (lane == j) {
+                    id[n] = 64 * r + who;
+                    mine[n] = value;
+                }
             }
         }
     }
-    weight = id >= 0 ? expf(mine - largest) : 0.0f;
-    float total;
-    if (renormalize) {
-        total = wave_sum(weight);
-    } else {
-        total = 0.0f;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (r < rounds && l[r] != -__builtin_inff()) total += expf(l[r] - largest);
-        total = wave_sum(total);
+    for (int n = 0; n < N; ++n) {
+        const float e = id[n] >= 0 ? expf(mine[n] - largest[n]) : 0.0f;
+        float sum = 0.0f;
+        if (renormalize) {
+            sum = e;
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) sum += l[n][r] == -__builtin_inff() ? 0.0f : expf(l[n][r] - largest[n]);
+        }
+        sum = wave_sum(sum);
+        weight[n] = bad[n] ? __builtin_nanf("") : id[n] >= 0 ? e / sum : 0.0f;
     }
-    if (id >= 0) weight /= total;
+}
+
+// Tokens first, first + stride, ..., of `tokens`, by one wave.
+template <int N, int R, class Put>
+__device__ __forceinline__ void route(const float* __restrict__ logits, int tokens, int experts, int top, bool renormalize, int first,
+                                      int stride, int lane, Put put)
+{
+    for (int token = first; token < tokens; token += N * stride) {
+        float l[N][R];
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                l[n][r] = 64 * r + lane < experts && token + n * stride < tokens
+                              ? logits[(size_t)(token + n * stride) * (size_t)experts + (size_t)(64 * r + lane)] : -__builtin_inff();
+        int id[N];
+        float weight[N];
+        choose<N, R>(l, top, renormalize, lane, id, weight);
+        if (lane < top) {
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                if (token + n * stride < tokens) put((token + n * stride) * top + lane, id[n], weight[n]);
+        }
+    }
+}
+
+template <class Put>
+__device__ __forceinline__ void route_any(const float* logits, int tokens, int experts, int top, bool renormalize, int first, int stride,
+                                          int lane, Put put)
+{
+    if (experts <= 64) route<4, 1>(logits, tokens, experts, top, renormalize, first, stride, lane, put);
+    else if (experts <= 256) route<1, 4>(logits, tokens, experts, top, renormalize, first, stride, lane, put);
+    else route<1, kMaxExperts / 64>(logits, tokens, experts, top, renormalize, first, stride, lane, put);
+}
+
+// Routing by itself, a wave a token: where every workgroup's doing it again would cost more
+// than a launch.
+static __global__ __launch_bounds__(64) void route_tokens(ExpertsArgs a)
+{
+    route_any(a.logits, a.tokens, a.experts, a.top, a.renormalize != 0, (int)blockIdx.x, (int)gridDim.x, (int)threadIdx.x,
+              [&](int slot, int id, float weight) {
+                  a.ids[slot] = id;
+                  a.weights[slot] = weight;
+              });
 }
 
 // The routing table, by the whole workgroup.  With logits the choices are made here
@@ -130,33 +172,27 @@ __device__ inline void choose(const float* __restrict__ logits, int experts, int
 template <int WAVES>
 __device__ inline void make_table(const RouteTable& t, const ExpertsArgs& a, int lane, int wave)
 {
-    constexpr int kExpertThreads = 64 * WAVES;
+    constexpr int THREADS = 64 * WAVES;
     const int slots = a.tokens * a.top, tid = threadIdx.x;
-    for (int e = tid; e < a.experts; e += kExpertThreads) t.count[e] = 0;
+    for (int e = tid; e < a.experts; e += THREADS) t.count[e] = 0;
     if (a.logits) {
-        for (int token = wave; token < a.tokens; token += WAVES) {
-            int id;
-            float weight;
-            choose(a.logits + (size_t)token * (size_t)a.experts, a.experts, a.top, a.renormalize != 0, lane, id, weight);
-            if (lane < a.top) {
-                const int s = token * a.top + lane;
-                t.ids[s] = (int16_t)id;
-                t.weights[s] = weight;
-                if (blockIdx.x == 0) {
-                    a.ids[s] = id;
-                    a.weights[s] = weight;
-                }
+        route_any(a.logits, a.tokens, a.experts, a.top, a.renormalize != 0, wave, WAVES, lane, [&](int slot, int id, float weight) {
+            t.ids[slot] = (int16_t)id;
+            t.weights[slot] = weight;
+            if (blockIdx.x == 0) {
+                a.ids[slot] = id;
+                a.weights[slot] = weight;
             }
-        }
+        });
     } else {
-        for (int s = tid; s < slots; s += kExpertThreads) {
+        for (int s = tid; s < slots; s += THREADS) {
             const int id = a.ids[s];
             t.ids[s] = (int16_t)(id >= 0 && id < a.experts ? id : -1);
             t.weights[s] = a.weights[s];
         }
     }
     __syncthreads();
-    for (int s = tid; s < slots; s += kExpertThreads)
+    for (int s = tid; s < slots; s += THREADS)
         if (t.ids[s] >= 0) atomicAdd(&t.count[t.ids[s]], 1);
     __syncthreads();
     if (wave == 0) {
@@ -174,11 +210,19 @@ __device__ inline void make_table(const RouteTable& t, const ExpertsArgs& a, int
         if (lane == 0) *t.n_used = used;
     }
     __syncthreads();
-    for (int s = tid; s < slots; s += kExpertThreads) {
+    for (int s = tid; s < slots; s += THREADS) {
         const int id = t.ids[s];
         if (id < 0) continue;
+        // the slots before this one with the same expert, 8 at a time
         int at = t.start[id];
-        for (int o = 0; o < s; ++o) at += t.ids[o] == id ? 1 : 0;
+        for (int o = 0; o < s; o += 8) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(t.ids + o);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                at += (int16_t)v[w] == id && o + 2 * w < s ? 1 : 0;
+                at += (int16_t)(v[w] >> 16) == id && o + 2 * w + 1 < s ? 1 : 0;
+            }
+        }
         t.sorted[at] = (uint16_t)s;
     }
     __syncthreads();
