@@ -31,8 +31,10 @@
  * first GEMM_RELU_GROUPS_COUNTER_BYTES zero before the first use and left zero by
  * every call; one buffer serves all calls of one stream, of both headers.
  *
- * Limits: M, N, K <= 2^20, groups, experts <= 65535 (gemm_relu_experts: tokens
- * <= 64, experts <= 1024, top <= 16).
+ * Limits: M, N, K <= 2^20, groups, matrices <= 65535, pitches <= 2^21;
+ * gemm_relu_experts: tokens <= 64, experts <= 1024, top <= 16, and less than 2^31
+ * bytes for the intermediate (4 tokens top hidden) and the partial sums (4 tokens
+ * top N, times the parts that K is cut into).
  */
 #ifndef GEMM_RELU_BLOCKS_H
 #define GEMM_RELU_BLOCKS_H

@@ -151,31 +151,35 @@ struct BackwardSpace {
 // the workspace.
 struct ExpertsSpace {
     int kind1, kind2;      // index into kExpertBlocks
-    int64_t units1, units2, splits, mid_row, mid, part, bytes;
+    int64_t units1, units2, splits, mid_row, mid, part, part_bytes, bytes;
     ExpertsSpace(int64_t tokens, int64_t n, int64_t hidden, int64_t experts, int64_t top, int b_layout)
     {
         const int64_t slots = tokens * top, used = std::min(experts, slots);
         const auto columns = [&](int kind) { return int64_t(16) * (b_layout == GEMM_RELU_B_KN ? 4 : kExpertBlocks[kind]); };
         const auto kind = [&](int64_t out) {
-            if (tokens > 16 && slots > 12 * used) return 2;
-            return used * ceil_div(out, 64) > 384 || ceil_div(out, 32) > kMaxColumnBlocks ? 1 : 0;
+            if (ceil_div(out, 32) > kMaxColumnBlocks) return 1;
+            return (used + slots / kExpertRows) * ceil_div(out, 64) <= (b_layout == GEMM_RELU_B_KN ? 384 : 160) ? 0 : 1;
         };
+        // row tiles: one for each expert that has rows, and one more for every 16 of them
+        const auto units = [&](int64_t out, int kind) { return (used + slots / kExpertRows) * ceil_div(out, columns(kind)); };
         kind1 = kind(hidden);
         kind2 = kind(n);
-        units1 = used * ceil_div(hidden, columns(kind1));
-        units2 = used * ceil_div(n, columns(kind2));
-        splits = units2 == 0 ? 1 : std::max<int64_t>(1, std::min<int64_t>(256 / units2, blocks_of(hidden) / kBlocksAPart));
+        units1 = units(hidden, kind1);
+        units2 = units(n, kind2);
+        const int64_t least = std::max<int64_t>(1, used * ceil_div(n, columns(kind2)));
+        splits = std::max<int64_t>(1, std::min<int64_t>(256 / least, blocks_of(hidden) / kBlocksAPart));
         mid_row = round_up(hidden, 8);
         mid = GEMM_RELU_GROUPS_COUNTER_BYTES;
         part = mid + round_up(4 * slots * mid_row, 256);
-        bytes = part + round_up(4 * slots * splits * n, 256);
+        part_bytes = 4 * slots * splits * n;
+        bytes = part + round_up(part_bytes, 256);
     }
     // A counter for each column block; scale blocks of K for the waves of each part.
     static constexpr int64_t kMaxColumnBlocks = GEMM_RELU_GROUPS_COUNTER_BYTES / 4, kBlocksAPart = 8;
 };
 static_assert(((int64_t(1) << 20) + 63) / 64 <= ExpertsSpace::kMaxColumnBlocks, "a counter for each block of 64 columns");
 
-bool route_apart(int64_t tokens, int64_t experts, int64_t top) { return tokens * top * ceil_div(experts, 64) > 128; }
+bool route_apart(int64_t tokens, int64_t experts, int64_t top) { return tokens > 16 || tokens * top * ceil_div(experts, 64) > 128; }
 
 int check_experts(int64_t tokens, int64_t n, int64_t hidden, int64_t experts, int64_t top, int b_layout)
 {
@@ -184,8 +188,9 @@ int check_experts(int64_t tokens, int64_t n, int64_t hidden, int64_t experts, in
     if (rc != GEMM_RELU_OK) return rc;
     if (experts < 1 || top < 1 || top > experts) return GEMM_RELU_ERR_INVALID_ARG;
     if (tokens > kMaxTokens || experts > kMaxExperts || top > kMaxTop) return GEMM_RELU_ERR_TOO_LARGE;
-    // the intermediate has one descriptor
-    return 4 * tokens * top * round_up(hidden, 8) > INT32_MAX ? GEMM_RELU_ERR_TOO_LARGE : GEMM_RELU_OK;
+    // the intermediate and the partial sums have one descriptor each
+    if (4 * tokens * top * round_up(hidden, 8) > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
+    return tokens > 0 && ExpertsSpace(tokens, n, hidden, experts, top, b_layout).part_bytes > INT32_MAX ? GEMM_RELU_ERR_TOO_LARGE : GEMM_RELU_OK;
 }
 
 }  // namespace

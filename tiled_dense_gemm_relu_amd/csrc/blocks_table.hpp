@@ -82,12 +82,14 @@ struct ExpertsArgs {
 };
 
 constexpr int kMaxTokens = 64, kMaxTop = 16, kMaxExperts = 1024;
-// Workgroups: columns of a unit, in blocks of 16 ((K, N) weights: 4 in all), rows of a
-// pass, in blocks of 16, and waves.  For few units (one workgroup a CU), for many, and
-// for many rows an expert.
-constexpr int kNumExpertKinds = 3;
-constexpr int kExpertBlocks[kNumExpertKinds] = {2, 4, 4}, kExpertRows[kNumExpertKinds] = {1, 1, 2}, kExpertWaves[kNumExpertKinds] = {8, 4, 4};
-constexpr int64_t route_table_bytes(int64_t slots, int64_t experts) { return (slots + 7) / 8 * 16 + slots * 6 + experts * 8 + 16; }
+// Workgroups: columns of a unit, in blocks of 16 ((K, N) weights: 4 in both), and waves.
+// For few units (one workgroup a CU), and for many.  A unit has 16 rows.
+constexpr int kNumExpertKinds = 2, kExpertRows = 16;
+constexpr int kExpertBlocks[kNumExpertKinds] = {2, 4}, kExpertWaves[kNumExpertKinds] = {8, 4};
+constexpr int64_t route_table_bytes(int64_t slots, int64_t experts)
+{
+    return (slots + 1) / 2 * 4 + slots * 6 + experts * 6 + ((experts < slots ? experts : slots) + slots / 16 + 1) * 4;
+}
 
 struct ExpertsKernels {
     // [storage: NK, KN, e4m3, e5m2][odd rows][second product][kind]

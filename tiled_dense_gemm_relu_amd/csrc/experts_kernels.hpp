@@ -24,24 +24,23 @@ namespace gemm_relu_hip {
 // Who goes where: slot t top + j is token t's choice j.  In dynamic LDS, as large as
 // the call needs (route_table_bytes).
 struct RouteTable {
+    int16_t* ids;            // a slot's expert, -1: none
     float* weights;          // a slot's weight
     int* count;              // an expert's slots
-    int* n_used;
-    int16_t* ids;            // a slot's expert, -1: none
+    uint32_t* tiles;         // row tiles of the experts that have slots: expert, and first row << 16
+    int* n_tiles;
     uint16_t* sorted;        // slots by expert, in order
-    uint16_t* start;         // where an expert's slots begin in `sorted`
-    uint16_t* used;          // the experts that have slots
+    uint16_t* end;           // where an expert's slots end in `sorted`
 
-    // (ids are read 8 at a time)
     __device__ __forceinline__ RouteTable(uint8_t* p, int slots, int experts)
     {
         ids = reinterpret_cast<int16_t*>(p);
-        weights = reinterpret_cast<float*>(ids + (slots + 7) / 8 * 8);
+        weights = reinterpret_cast<float*>(ids + (slots + 1) / 2 * 2);
         count = reinterpret_cast<int*>(weights + slots);
-        n_used = count + experts;
-        sorted = reinterpret_cast<uint16_t*>(n_used + 1);
-        start = sorted + slots;
-        used = start + experts;
+        tiles = reinterpret_cast<uint32_t*>(count + experts);
+        n_tiles = reinterpret_cast<int*>(tiles + min(experts, slots) + slots / 16);
+        sorted = reinterpret_cast<uint16_t*>(n_tiles + 1);
+        end = sorted + slots;
     }
 };
 
@@ -167,9 +166,9 @@ static __global__ __launch_bounds__(64) void route_tokens(ExpertsArgs a)
               });
 }
 
-// The routing table, by the whole workgroup.  With logits the choices are made here
-// and, by the first workgroup, written.
-template <int WAVES>
+// The routing table, by the whole workgroup, with row tiles of ROWS rows.  With logits
+// the choices are made here and, by the first workgroup, written.
+template <int WAVES, int ROWS>
 __device__ inline void make_table(const RouteTable& t, const ExpertsArgs& a, int lane, int wave)
 {
     constexpr int THREADS = 64 * WAVES;
@@ -196,34 +195,35 @@ __device__ inline void make_table(const RouteTable& t, const ExpertsArgs& a, int
         if (t.ids[s] >= 0) atomicAdd(&t.count[t.ids[s]], 1);
     __syncthreads();
     if (wave == 0) {
-        int before = 0, used = 0;
+        int before = 0, tiles = 0;
         for (int e0 = 0; e0 < a.experts; e0 += 64) {
             const int c = e0 + lane < a.experts ? t.count[e0 + lane] : 0, incl = wave_scan_sum(c);
-            const uint64_t some = __ballot(c > 0);
+            const int n = (c + ROWS - 1) / ROWS, at = wave_scan_sum(n);
             if (c > 0) {
-                t.start[e0 + lane] = (uint16_t)(before + incl - c);
-                t.used[used + __popcll(some & ((uint64_t(1) << lane) - 1))] = (uint16_t)(e0 + lane);
+                t.end[e0 + lane] = (uint16_t)(before + incl - c);
+                for (int i = 0; i < n; ++i) t.tiles[tiles + at - n + i] = (uint32_t)(e0 + lane) | ((uint32_t)(i * ROWS) << 16);
             }
             before += __builtin_amdgcn_readlane(incl, 63);
-            used += __popcll(some);
+            tiles += __builtin_amdgcn_readlane(at, 63);
         }
-        if (lane == 0) *t.n_used = used;
-    }
-    __syncthreads();
-    for (int s = tid; s < slots; s += THREADS) {
-        const int id = t.ids[s];
-        if (id < 0) continue;
-        // the slots before this one with the same expert, 8 at a time
-        int at = t.start[id];
-        for (int o = 0; o < s; o += 8) {
-            const u32x4 v = *reinterpret_cast<const u32x4*>(t.ids + o);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                at += (int16_t)v[w] == id && o + 2 * w < s ? 1 : 0;
-                at += (int16_t)(v[w] >> 16) == id && o + 2 * w + 1 < s ? 1 : 0;
+        if (lane == 0) *t.n_tiles = tiles;
+        // The slots in order, 64 at a time: those of one expert find each other by the bits of
+        // its number, and `end`, where they begin at first, moves on past them.
+        const int bits = 32 - __builtin_clz(a.experts);
+        for (int s0 = 0; s0 < slots; s0 += 64) {
+            const int s = s0 + lane, id = s < slots ? t.ids[s] : -1;
+            uint64_t same = __ballot(id >= 0);
+            for (int b = 0; b < bits; ++b) {
+                const uint64_t set = __ballot((id >> b) & 1);
+                same &= (id >> b) & 1 ? set : ~set;
             }
+            if (id >= 0) {
+                const int at = t.end[id], rank = __popcll(same & ((uint64_t(1) << lane) - 1)), n = __popcll(same);
+                t.sorted[at + rank] = (uint16_t)s;
+                if (rank == n - 1) t.end[id] = (uint16_t)(at + n);
+            }
+            __builtin_amdgcn_wave_barrier();
         }
-        t.sorted[at] = (uint16_t)s;
     }
     __syncthreads();
 }
@@ -612,15 +612,15 @@ __device__ __forceinline__ void expert_stream(floatx4 (&acc)[NB][MB], const uint
     wait_vmcnt<0>();              // nothing lands in the ring after this
 }
 
-// KIND: kExpertBlocks columns, kExpertRows rows, kExpertWaves waves.  ODD: everything
-// through registers.
+// KIND: kExpertBlocks columns, kExpertWaves waves.  ODD: everything through registers.
 template <int DT, int STORE, bool ODD, bool SECOND, int KIND>
 __global__ __launch_bounds__(64 * kExpertWaves[KIND], KIND == 1 ? ODD || STORE >= kStoreE4M3 ? 2 : 3 : 1) void expert_products(ExpertsArgs a)
 {
     constexpr bool WIDE = STORE >= kStoreE4M3, KN = STORE == kStoreKN;
-    constexpr int NB = KN ? 4 : kExpertBlocks[KIND], MB = kExpertRows[KIND], WAVES = kExpertWaves[KIND], THREADS = 64 * WAVES;
-    constexpr int S = KIND == 0 && STORE == kStoreNK ? 2 : 1;
+    constexpr int kDeviceScope = 16;   // cache policy sc1
+    constexpr int NB = KN ? 4 : kExpertBlocks[KIND], MB = 1, WAVES = kExpertWaves[KIND], THREADS = 64 * WAVES;
     constexpr int COLS = 16 * NB, PART = COLS * 17, STAGE = NB * 2048 + MB * (WIDE ? 4096 : 2048) * (SECOND ? 2 : 1);
+    constexpr int S = KIND == 0 && STORE == kStoreNK ? 2 : 1;
     constexpr int PARTS = WAVES * PART * 4, RING = ODD ? 0 : WAVES * S * STAGE;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[RING > PARTS ? RING : PARTS];
     __shared__ int before;
@@ -629,10 +629,10 @@ __global__ __launch_bounds__(64 * kExpertWaves[KIND], KIND == 1 ? ODD || STORE >
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tid = threadIdx.x;
     const int r16 = lane & 15, g = lane >> 4;
     const RouteTable t(table, a.tokens * a.top, a.experts);
-    make_table<WAVES>(t, a, lane, wave);
+    make_table<WAVES, 16 * MB>(t, a, lane, wave);
     const int blocks_n = (a.out + COLS - 1) / COLS, scale_blocks = (a.in + kBlock - 1) / kBlock;
-    const int used = __builtin_amdgcn_readfirstlane(*t.n_used);
-    const int units = used * blocks_n * a.splits;
+    const int tiles = __builtin_amdgcn_readfirstlane(*t.n_tiles);
+    const int units = tiles * blocks_n * a.splits;
     // Where column c of a unit sits in its rows of LDS: in registers (K, N) weights give a
     // lane 4 neighbouring columns, one in each block.
     auto column = [](int c) { return KN && ODD ? (c & 3) * 16 + (c >> 2) : c; };
@@ -642,7 +642,7 @@ __global__ __launch_bounds__(64 * kExpertWaves[KIND], KIND == 1 ? ODD || STORE >
     auto row_without = [&](int token) {
         return a.routed && t.ids[token * a.top] < 0 && t.weights[token * a.top] != t.weights[token * a.top] ? __builtin_nanf("") : 0.0f;
     };
-    if (SECOND && used == 0) {
+    if (SECOND && tiles == 0) {
         for (int64_t i = (int64_t)blockIdx.x * THREADS + tid; i < (int64_t)a.tokens * a.out; i += (int64_t)gridDim.x * THREADS)
             a.y[i] = act_cast<DT>(row_without((int)(i / a.out)), false);
         return;
@@ -650,9 +650,10 @@ __global__ __launch_bounds__(64 * kExpertWaves[KIND], KIND == 1 ? ODD || STORE >
     const uint32_t x_bytes = SECOND ? (uint32_t)(a.tokens * a.top) * (uint32_t)a.mid_row * 4u : (uint32_t)a.tokens * (uint32_t)a.in * 2u;
     const AnyRsrc rx = make_any_rsrc(a.x, x_bytes);
     for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int nb = unit % blocks_n, rest = unit / blocks_n, split = rest % a.splits, u = rest / a.splits;
-        const int expert = __builtin_amdgcn_readfirstlane(t.used[u]), n0 = nb * COLS;
-        const int first = __builtin_amdgcn_readfirstlane(t.start[expert]), count = __builtin_amdgcn_readfirstlane(t.count[expert]);
+        const int nb = unit % blocks_n, rest = unit / blocks_n, split = rest % a.splits, n0 = nb * COLS;
+        const uint32_t tile = (uint32_t)__builtin_amdgcn_readfirstlane((int)t.tiles[rest / a.splits]);
+        const int expert = (int)(tile & 0xffffu), row0 = (int)(tile >> 16);
+        const int count = __builtin_amdgcn_readfirstlane(t.count[expert]), first = __builtin_amdgcn_readfirstlane(t.end[expert]) - count;
         const uint8_t* w = a.w + (size_t)expert * (size_t)(KN ? a.in : a.out) * (size_t)a.ld;
         const float* scales = WIDE ? a.scales + ((size_t)expert * (size_t)((a.out + kBlock - 1) / kBlock) + (size_t)(n0 / kBlock)) * (size_t)scale_blocks
                                    : nullptr;
@@ -663,8 +664,8 @@ __global__ __launch_bounds__(64 * kExpertWaves[KIND], KIND == 1 ? ODD || STORE >
         };
         // The unit's share of `pieces` of k.
         auto from = [&](int pieces, int s) { return (int)((int64_t)pieces * s / a.splits); };
-        // Adds the waves' sums of 16 rows from row0 on and hands them on.
-        auto finish = [&](const floatx4* sums, int row0) __attribute__((always_inline)) {
+        // Adds the waves' sums of 16 rows from row1 on and hands them on.
+        auto finish = [&](const floatx4* sums, int row1) __attribute__((always_inline)) {
             __syncthreads();           // the rings, or the sums of the rows before, are read
 #pragma unroll
             for (int i = 0; i < NB; ++i)
@@ -672,7 +673,7 @@ __global__ __launch_bounds__(64 * kExpertWaves[KIND], KIND == 1 ? ODD || STORE >
                 for (int e = 0; e < 4; ++e) part[wave * PART + (16 * i + 4 * g + e) * 17 + r16] = sums[i * MB][e];
             __syncthreads();
             for (int o = tid; o < 16 * COLS; o += THREADS) {
-                const int row = o / COLS, c = o % COLS, r = row0 + row;
+                const int row = o / COLS, c = o % COLS, r = row1 + row;
                 if (r >= count || n0 + c >= a.out) continue;
                 float z = 0.0f;
 #pragma unroll
@@ -692,50 +693,66 @@ __global__ __launch_bounds__(64 * kExpertWaves[KIND], KIND == 1 ? ODD || STORE >
             }
         };
         const int pieces = WIDE || ODD ? scale_blocks : (a.in + 63) / 64, p0 = from(pieces, split), p1 = from(pieces, split + 1);
-        for (int row0 = 0; row0 < count; row0 += 16 * MB) {
-            floatx4 acc[NB][MB];
+        floatx4 acc[NB][MB];
 #pragma unroll
-            for (int i = 0; i < NB; ++i)
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
-                for (int j = 0; j < MB; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-            if constexpr (ODD) {
-                uint32_t x_off[MB];
+            for (int j = 0; j < MB; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (ODD) {
+            uint32_t x_off[MB];
 #pragma unroll
-                for (int j = 0; j < MB; ++j) x_off[j] = row_of_x(row0 + 16 * j + r16);
-                expert_sums<DT, STORE, SECOND, NB, MB, WAVES>(acc, rx, x_off, (uint32_t)a.mid_row * 2u, w, scales, a.ld, n0, a.in, a.out, p0, p1,
-                                                              wave, lane);
-            } else {
-                uint32_t x_row[2 * MB];
+            for (int j = 0; j < MB; ++j) x_off[j] = row_of_x(row0 + 16 * j + r16);
+            expert_sums<DT, STORE, SECOND, NB, MB, WAVES>(acc, rx, x_off, (uint32_t)a.mid_row * 2u, w, scales, a.ld, n0, a.in, a.out, p0, p1,
+                                                          wave, lane);
+        } else {
+            uint32_t x_row[2 * MB];
 #pragma unroll
-                for (int q = 0; q < 2 * MB; ++q) x_row[q] = row_of_x(row0 + 8 * q + lane / 8);
-                expert_stream<DT, STORE, SECOND, NB, MB, S, WAVES>(acc, a.x, x_bytes, x_row, (uint32_t)a.mid_row * 2u, w, scales, a.ld, n0, a.in,
-                                                                   a.out, p0, p1, smem + wave * (S * STAGE), unit % max(p1 - p0, 1), wave, lane);
-            }
+            for (int q = 0; q < 2 * MB; ++q) x_row[q] = row_of_x(row0 + 8 * q + lane / 8);
+            expert_stream<DT, STORE, SECOND, NB, MB, S, WAVES>(acc, a.x, x_bytes, x_row, (uint32_t)a.mid_row * 2u, w, scales, a.ld, n0, a.in,
+                                                               a.out, p0, p1, smem + wave * (S * STAGE), unit % max(p1 - p0, 1), wave, lane);
+        }
 #pragma unroll
-            for (int j = 0; j < MB; ++j) {
-                if (row0 + 16 * j >= count) break;
-                finish(&acc[0][j], row0 + 16 * j);
-            }
-            if (row0 + 16 * MB < count) __syncthreads();       // the rings are filled again
+        for (int j = 0; j < MB; ++j) {
+            if (row0 + 16 * j >= count) break;
+            finish(&acc[0][j], row0 + 16 * j);
         }
         if constexpr (SECOND) {
             wait_vmcnt<0>();           // this wave's sums have reached device scope
             __syncthreads();
             if (tid == 0) before = __hip_atomic_fetch_add(a.counters + nb, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             __syncthreads();
-            if (before == used * a.splits - 1) {
+            if (before == tiles * a.splits - 1) {
                 asm volatile("" ::: "memory");   // the loads below stay after the count that allowed them
-                for (int o = tid; o < a.tokens * COLS; o += THREADS) {
-                    const int token = o / COLS, c = n0 + o % COLS;
-                    if (c >= a.out) continue;
-                    float z = row_without(token);
-                    for (int j = 0; j < a.top; ++j) {
-                        const int slot = token * a.top + j;
-                        if (t.ids[slot] < 0) continue;
-                        for (int s = 0; s < a.splits; ++s)
-                            z += __hip_atomic_load(a.part + ((size_t)slot * (size_t)a.splits + (size_t)s) * (size_t)a.out + (size_t)c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                // A token's parts are neighbours: (choice, part of k).  Several are loaded at once.
+                const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.part, (uint32_t)(a.tokens * a.top * a.splits) * (uint32_t)a.out * 4u);
+                const int parts = a.top * a.splits;
+                constexpr int OUTS = 4;          // outputs a thread has on their way
+                for (int o0 = tid; o0 < a.tokens * COLS; o0 += OUTS * THREADS) {
+                    float z[OUTS];
+#pragma unroll
+                    for (int q = 0; q < OUTS; ++q) z[q] = row_without(min((o0 + q * THREADS) / COLS, a.tokens - 1));
+                    for (int i0 = 0; i0 < parts; i0 += 4) {
+                        float v[OUTS][4];
+#pragma unroll
+                        for (int q = 0; q < OUTS; ++q)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int o = o0 + q * THREADS, token = min(o / COLS, a.tokens - 1), c = n0 + o % COLS;
+                                const bool live = o < a.tokens * COLS && i0 + i < parts && c < a.out &&
+                                                  t.ids[token * a.top + min(i0 + i, parts - 1) / a.splits] >= 0;
+                                const uint32_t at = ((uint32_t)(token * parts + i0 + i) * (uint32_t)a.out + (uint32_t)c) * 4u;
+                                v[q][i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, live ? at : kOobOffset, 0, kDeviceScope));
+                            }
+#pragma unroll
+                        for (int q = 0; q < OUTS; ++q)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) z[q] += v[q][i];
                     }
-                    a.y[(size_t)token * (size_t)a.out + (size_t)c] = act_cast<DT>(z, false);
+#pragma unroll
+                    for (int q = 0; q < OUTS; ++q) {
+                        const int o = o0 + q * THREADS, token = o / COLS, c = n0 + o % COLS;
+                        if (o < a.tokens * COLS && c < a.out) a.y[(size_t)token * (size_t)a.out + (size_t)c] = act_cast<DT>(z[q], false);
+                    }
                 }
                 if (tid == 0) __hip_atomic_store(a.counters + nb, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
