@@ -1,0 +1,265 @@
+"""The 8-bit products and the expert layer for a few tokens as programs use them: through autograd, in graphs, on
+side streams, two at once, and together as a served layer."""
+import pytest
+import torch
+
+import tiled_dense_gemm_relu_amd as gr
+from tiled_dense_gemm_relu_amd import blocks
+
+from test_gpu_blocks import E4M3, E5M2, check_close, gen, nb, pitched, reference_quantize, stands_for
+from test_gpu_experts import Layer
+from test_gpu_experts import check_close as check_layer
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def randn(shape, seed, dtype=torch.bfloat16, scale=1.0):
+    return (torch.randn(shape, generator=gen(seed)) * scale).to(dtype)
+
+
+# ---------------------------------------------------------------- autograd
+
+
+@pytest.mark.parametrize("relu", [True, False])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_linear_and_gradients_match_the_formulas(relu, dtype):
+    M, N, K = 200, 150, 300
+    x, w, dc = randn((M, K), 1, dtype), randn((N, K), 2, dtype, K ** -0.5), randn((M, N), 3, dtype)
+    xg, wg = x.to(DEV).requires_grad_(), w.to(DEV).requires_grad_()
+    c = gr.linear_blocks(xg, wg, relu=relu)
+    c.backward(dc.to(DEV))
+    qx, qw = (stands_for(*reference_quantize(t, E4M3, tiles, False), tiles) for t, tiles in ((x, False), (w, True)))
+    check_close(c.detach(), qx, qw, relu)
+    # gradients of what was kept: x along its columns, w's tiles, the masked gradient both ways
+    d = torch.where(c.detach().cpu() > 0, dc, torch.zeros_like(dc)) if relu else dc
+    d_rows, d_columns = (stands_for(*reference_quantize(t, E5M2, False, False), False) for t in (d, d.t()))
+    x_columns = stands_for(*reference_quantize(x.t(), E4M3, False, False), False)
+    check_close(xg.grad, d_rows, qw.t().contiguous())
+    check_close(wg.grad, d_columns, x_columns)
+    # one gradient alone is the same
+    for which in (0, 1):
+        xs, ws = x.to(DEV).requires_grad_(which == 0), w.to(DEV).requires_grad_(which == 1)
+        gr.linear_blocks(xs, ws, relu=relu).backward(dc.to(DEV))
+        assert torch.equal((xs, ws)[which].grad, (xg, wg)[which].grad) and (xs, ws)[1 - which].grad is None
+    with torch.no_grad():
+        assert torch.equal(gr.linear_blocks(xg, wg, relu=relu), c)
+
+
+def test_gradients_match_differences():
+    """Values that 8 bits hold exactly (integers up to 15 in blocks whose largest is 448, gradients of 1 and 2):
+    there the layer is the product itself, so a step of 1 changes sum(dc c) by exactly the gradient's entry."""
+    M, N, K = 5, 130, 140
+    g = gen(7)
+    x, w = (torch.randint(-7, 8, (r, K), generator=g).to(torch.float16) for r in (M, N))
+    # each row's, column's and tile's largest magnitude: rows and columns of their own, so steps leave the scales alone
+    x[:, 0] = x[:, 128] = 448
+    x[4] = 448
+    w[::128, ::128] = 448
+    dc = torch.randint(1, 3, (M, N), generator=g).to(torch.float16)
+    dc[:, 0] = dc[:, 128] = 2
+    dc[4] = 2
+
+    def total(x, w):
+        # 64-bit sums of exact outputs (integers below 2^24 in fp32; c itself is rounded to fp16, so sum it by parts)
+        q, s = gr.quantize_blocks(x.to(DEV))
+        qw, sw = gr.quantize_blocks(w.to(DEV), tiles=True)
+        return float((dc.double() * (stands_for(q, s, False) @ stands_for(qw, sw, True).t())).sum())
+    xg, wg = x.to(DEV).requires_grad_(), w.to(DEV).requires_grad_()
+    gr.linear_blocks(xg, wg, relu=False).backward(dc.to(DEV))
+    base = total(x, w)
+    for (m, k) in ((0, 1), (1, 60), (3, 139), (2, 129)):
+        step = x.clone()
+        step[m, k] += 1
+        assert total(step, w) - base == float((dc[m].double() @ w[:, k].double()))
+        assert float(xg.grad[m, k]) == float(torch.tensor(total(step, w) - base).half())
+    for (n, k) in ((1, 1), (60, 61), (129, 139), (2, 129)):
+        step = w.clone()
+        step[n, k] += 1
+        assert float(wg.grad[n, k]) == float(torch.tensor(total(x, step) - base).half())
+
+
+def test_refusals_of_gradients():
+    x, w = randn((4, 32), 1).to(DEV), randn((2, 16, 32), 2).to(DEV)
+    w2, logits = randn((2, 32, 16), 3).to(DEV), torch.zeros((4, 2), device=DEV)
+    y, ids, weights = gr.gemm_relu_experts(x.requires_grad_(), w, w2, logits, 1)
+    assert y.requires_grad and not weights.requires_grad
+    with pytest.raises(NotImplementedError, match="no gradient"):
+        y.sum().backward()
+    with pytest.raises(RuntimeError, match="out="):
+        gr.gemm_relu_experts(x, w, w2, logits, 1, out=torch.empty_like(x))
+    with torch.no_grad():
+        again = gr.gemm_relu_experts(x, w, w2, logits, 1, out=torch.empty((4, 32), dtype=x.dtype, device=DEV))[0]
+    assert torch.equal(again, y)
+    q, s = gr.quantize_blocks(x.detach())
+    with pytest.raises(RuntimeError, match="requires a gradient"):
+        gr.gemm_relu_blocks(q.requires_grad_(), s, q.detach(), torch.ones((1, 1), device=DEV))
+
+
+@pytest.mark.parametrize("what", ["strided", "short storage", "wrong scales", "odd pitch", "other device", "formats", "layout",
+                                  "both routes", "no route", "out dtype"])
+def test_python_refusals(what):
+    q, s = gr.quantize_blocks(randn((8, 40), 1).to(DEV))
+    w, sw = gr.quantize_blocks(randn((6, 40), 2).to(DEV), tiles=True)
+    x, w1, w2 = randn((4, 32), 1).to(DEV), randn((2, 16, 32), 2).to(DEV), randn((2, 32, 16), 3).to(DEV)
+    logits = torch.zeros((4, 2), device=DEV)
+    stack = pitched(torch.zeros((2, 16, 32), dtype=E4M3))
+    ones = torch.ones((2, 1, 1), device=DEV)
+    calls = {
+        "strided": lambda: gr.gemm_relu_blocks(pitched(torch.zeros((40, 8), dtype=E4M3)).t(), s, w, sw),
+        "short storage": lambda: gr.gemm_relu_blocks(torch.zeros(7 * 48 + 40, dtype=torch.uint8, device=DEV).view(E4M3).as_strided((8, 40), (48, 1)), s, w, sw),
+        "wrong scales": lambda: gr.gemm_relu_blocks(q, s.t().contiguous(), w, sw),
+        "odd pitch": lambda: gr.gemm_relu_blocks(torch.zeros((8, 40), dtype=torch.uint8, device=DEV).view(E4M3), s, w, sw),
+        "other device": lambda: gr.gemm_relu_blocks(q, s, w.cpu(), sw),
+        "formats": lambda: gr.gemm_relu_experts(x, stack, stack.view(torch.uint8).view(E5M2), logits, 1, w1_scales=ones, w2_scales=ones),
+        "layout": lambda: gr.gemm_relu_experts(x, stack, stack, logits, 1, w1_scales=ones, w2_scales=ones, b_layout=gr.B_KN),
+        "both routes": lambda: gr.gemm_relu_experts(x, w1, w2, logits, 1, ids=torch.zeros((4, 1), dtype=torch.int32, device=DEV)),
+        "no route": lambda: gr.gemm_relu_experts(x, w1, w2),
+        "out dtype": lambda: gr.gemm_relu_blocks(q, s, w, sw, out_dtype=torch.float32),
+    }
+    with pytest.raises((ValueError, TypeError)):
+        calls[what]()
+
+
+# ---------------------------------------------------------------- streams and graphs
+
+
+class Work:
+    """Calls of every operator on buffers whose contents can be replaced, and their eager results."""
+
+    def __init__(self):
+        M, N, K = 96, 160, 272
+        self.x, self.w = torch.empty((M, K), dtype=torch.bfloat16, device=DEV), torch.empty((N, K), dtype=torch.bfloat16, device=DEV)
+        self.dc, self.c = (torch.empty((M, N), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        self.logits = torch.empty((40, 6), device=DEV)
+        self.w1, self.w2 = (torch.empty(s, dtype=torch.bfloat16, device=DEV) for s in ((6, 130, K), (6, K, 130)))
+        self.ends = torch.tensor([40, 40, M - 3], dtype=torch.int32, device=DEV)
+
+    def fill(self, seed):
+        for i, t in enumerate((self.x, self.w, self.dc, self.c, self.logits, self.w1, self.w2)):
+            t.copy_(torch.randn(t.shape, generator=gen(10 * seed + i)) * (t.shape[-1] ** -0.5 if t.dim() == 3 else 1.0))
+
+    def __call__(self, **kw):
+        q, s, xt, sxt = gr.quantize_blocks(self.x, transposed=True, **kw)
+        qw, sw, wt, swt = gr.quantize_blocks(self.w, tiles=True, transposed=True, **kw)
+        out = [q.view(torch.uint8), s, xt.view(torch.uint8), sxt]
+        for config in (blocks.CONFIG_AUTO, blocks.CONFIG_256, blocks.CONFIG_128, blocks.CONFIG_64):
+            out.append(gr.gemm_relu_blocks(q, s, qw, sw, config=config, **kw))
+        q1, s1 = gr.quantize_blocks(self.w1, tiles=True, **kw)
+        out.append(gr.gemm_relu_blocks(q, s, q1[:3], s1[:3].contiguous(), ends=self.ends, relu=False, **kw))
+        out += gr.gemm_relu_blocks_backward(self.dc, self.c, xt, sxt, wt, swt, **kw)
+        for tokens in (1, 8, 40):
+            out += gr.gemm_relu_experts(self.x[:tokens], self.w1, self.w2, self.logits[:tokens], 2, **kw)
+        q2, s2 = gr.quantize_blocks(self.w2, tiles=True, **kw)
+        out += gr.gemm_relu_experts(self.x[:8], q1, q2, self.logits[:8], 3, w1_scales=s1, w2_scales=s2, **kw)
+        return out
+
+
+def same(a, b):
+    return all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_graph_replays_match_eager_calls():
+    work = Work()
+    work.fill(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = work()
+    for seed in range(1, 6):
+        work.fill(seed)
+        torch.cuda.synchronize()
+        graph.replay()
+        eager = work()
+        torch.cuda.synchronize()
+        assert same(captured, eager), f"replay {seed}"
+        assert same(work(), eager)                      # and run to run
+
+
+def test_two_graphs_and_eager_calls_share_nothing():
+    # captured on one stream, replayed on another, with eager calls between and a larger workspace taken
+    work, other = Work(), Work()
+    work.fill(1)
+    other.fill(2)
+    graphs = []
+    for w in (work, other):
+        w()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = w()
+        graphs.append((g, out, w))
+    gr.release_workspaces()
+    big = Layer("nk", torch.bfloat16, 2, 64, 4096, 4096, 1)
+    big(torch.ones((64, 64), dtype=torch.bfloat16, device=DEV), torch.zeros((64, 2), device=DEV), 2)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(3):
+        torch.cuda.synchronize()
+        for (g, _, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for g, out, w in graphs:
+            assert same(out, w())
+
+
+def test_side_stream_and_two_streams_at_once():
+    work, other = Work(), Work()
+    work.fill(3)
+    other.fill(4)
+    want, want_other = work(), other()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        got = [w(stream=s) for w, s in zip((work, other), streams)]
+        torch.cuda.synchronize()
+        assert same(got[0], want) and same(got[1], want_other)
+
+
+def test_own_workspace_is_left_clean():
+    layer = Layer("nk", torch.bfloat16, 5, 136, 200, 520, 3)
+    x, logits = randn((9, 136), 1).to(DEV), torch.randn((9, 5), generator=gen(2)).to(DEV)
+    need = gr.experts_workspace_bytes(9, 520, 200, 5, 2)
+    space = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+    space[:65536] = 0
+    want = layer(x, logits, 2)
+    for _ in range(3):
+        assert same(layer(x, logits, 2, workspace=space), want)
+        assert not space[:65536].any()
+    with pytest.raises(gr.GemmReluError, match="WORKSPACE"):
+        layer(x, logits, 2, workspace=space[:-256])
+
+
+# ---------------------------------------------------------------- together
+
+
+def test_served_layer():
+    from tiled_dense_gemm_relu_amd.expert_layer import ServedExperts, serve_experts
+    decoded, prompt, layer, (x, logits) = serve_experts(tokens=24, prompt=300, experts=8, width=136, hidden=200, top=2)
+    served = ServedExperts(layer, 2)
+    w1, w2 = (torch.stack([stands_for(q, s, True) for q, s in zip(w, sc)]) for w, sc in ((served.w1, served.s1), (served.w2, served.s2)))
+    for e in range(8):
+        # (out, in), as the training weights (in, out) transposed, half a step of e4m3 of a tile's largest away
+        trained = layer.weights[0][e].t().cpu().double()
+        assert ((w1[e] - trained).abs() <= trained.abs() * 2.0 ** -4 + trained.abs().max() * 2.0 ** -9 / 448).all()
+
+    class Wide:
+        wide = [w1.transpose(1, 2).contiguous(), w2.transpose(1, 2).contiguous()]
+    best, ids = logits.cpu().topk(2, dim=1)
+    check_layer(decoded, x[:24].cpu(), Wide, ids[:24], best.double().softmax(1)[:24])
+    # the prompt's activations are quantized twice: half a step of e4m3 (2^-4) of each, and the sums' signs vary
+    y = torch.stack([sum(p * ((x[t].cpu().double() @ Wide.wide[0][e]).relu() @ Wide.wide[1][e])
+                         for e, p in zip(ids[t].tolist(), best.double().softmax(1)[t].tolist())) for t in range(300)])
+    assert float((prompt.cpu().double() - y).norm() / y.norm()) <= 2 * 2.0 ** -4
+    served.decode(x[:1], logits[:1])
+
+
+def test_module_runs():
+    from tiled_dense_gemm_relu_amd import expert_layer
+    decoded, prompt, _, _ = expert_layer.serve_experts()
+    assert decoded.isfinite().all() and prompt.isfinite().all() and prompt.shape == (500, 256)

@@ -31,6 +31,7 @@ from .blocks import (  # noqa: F401
     gemm_relu_blocks,
     gemm_relu_blocks_backward,
     gemm_relu_experts,
+    linear_blocks,
     blocks_backward_workspace_bytes,
     experts_workspace_bytes,
 )

@@ -1,7 +1,8 @@
 """Products of 8-bit floating-point matrices scaled by blocks of 128 (the C ABI in include/gemm_relu_blocks.h).
 
 ``quantize_blocks`` makes such matrices, ``gemm_relu_blocks`` multiplies them (dense, or grouped by expert),
-``gemm_relu_blocks_backward`` has the gradients of a layer that does.  ``gemm_relu_experts`` is a whole expert
+``gemm_relu_blocks_backward`` has the gradients of a layer that does, and ``linear_blocks`` is such a layer as a
+node of autograd's graph.  ``gemm_relu_experts`` is a whole expert
 layer for a few tokens, with 16-bit or such 8-bit weights.
 As in binding.py this is argument marshalling only, with no fallback.
 
@@ -297,6 +298,57 @@ def gemm_relu_blocks_backward(dc, c, xt, xt_scales, wt, wt_scales, relu: bool = 
           (dx.data_ptr() or 256) if need_dx else None, (dw.data_ptr() or 256) if need_dw else None, M, N, K, ldxt, ldwt,
           fmt, fx, fw, code, 1 if relu else 0, ws, ws_bytes, handle or None)
     return dx, dw
+
+
+@functools.lru_cache(maxsize=1)
+def _linear():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class Linear(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w, relu, dtype, grad_dtype):
+            need_x, need_w = ctx.needs_input_grad[:2]
+            # one pass over each matrix writes what forward and backward read
+            q, s, xt, sxt = quantize_blocks(x, dtype, transposed=True) if need_w else quantize_blocks(x, dtype) + (None, None)
+            qw, sw, wt, swt = (quantize_blocks(w, dtype, tiles=True, transposed=True) if need_x
+                               else quantize_blocks(w, dtype, tiles=True) + (None, None))
+            c = gemm_relu_blocks(q, s, qw, sw, out_dtype=x.dtype, relu=relu)
+            ctx.save_for_backward(c if relu else None, xt, sxt, wt, swt)
+            ctx.relu, ctx.grad_dtype = relu, grad_dtype
+            return c
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dc):
+            c, xt, sxt, wt, swt = ctx.saved_tensors
+            need_x, need_w = ctx.needs_input_grad[:2]
+            dx, dw = gemm_relu_blocks_backward(dc.contiguous(), c, xt, sxt, wt, swt, relu=ctx.relu, dtype=ctx.grad_dtype,
+                                               need_dx=need_x, need_dw=need_w)
+            return dx, dw, None, None, None
+
+    return Linear
+
+
+def linear_blocks(x, w, relu: bool = True, dtype=None, grad_dtype=None, stream=None):
+    """ReLU(x @ w^T) in 8 bits, with gradients: x (M, K) and w (N, K) in fp16 or bf16.
+
+    x is quantized by rows and w by tiles to ``dtype`` (float8_e4m3fn by default), the gradient of the result
+    by rows to ``grad_dtype`` (float8_e5m2); gradients pass the rounding of x and w unchanged.  What backward
+    needs of x and w is kept in 8 bits.  Forward and backward run on ``stream``, or the current one.
+    """
+    _, dev = _first("x", x)
+    _check_tensor("x", x, 2, dev, x.dtype)
+    _check_tensor("w", w, 2, dev, x.dtype)
+    if w.shape[1] != x.shape[1]:
+        raise ValueError(f"gemm_relu: inner dimensions differ: x {tuple(x.shape)}, w {tuple(w.shape)}")
+    import torch
+    dtype = torch.float8_e4m3fn if dtype is None else dtype
+    grad_dtype = torch.float8_e5m2 if grad_dtype is None else grad_dtype
+    _format_code("dtype", dtype)
+    _format_code("grad_dtype", grad_dtype)
+    with _on(stream, dev):
+        return _linear().apply(x, w, bool(relu), dtype, grad_dtype)
 
 
 @functools.lru_cache(maxsize=1)

@@ -1,15 +1,17 @@
-"""An expert layer trained for a few steps, then a projection served with adapters.
+"""An expert layer trained for a few steps and served in 8 bits, then a projection served with adapters.
 
     python -m tiled_dense_gemm_relu_amd.expert_layer
 
 The layer routes each token to one of ``experts`` two-matrix networks, y = ReLU(x @ B1[e]) @ B2[e].
 Tokens are sorted by expert once; the running sum of the experts' token counts, made and kept on the
-GPU, is the row table of both products and of all four gradients.
+GPU, is the row table of both products and of all four gradients.  For serving its weights are quantized
+once: prompts take the same products on 8-bit matrices, a few tokens the whole layer in one call.
 """
 from __future__ import annotations
 
 import torch
 
+from .blocks import gemm_relu_blocks, gemm_relu_experts, quantize_blocks
 from .groups import gemm_relu_adapters, gemm_relu_grouped, gemm_relu_grouped_backward
 
 
@@ -57,6 +59,33 @@ class ExpertLayer:
             weight.copy_(master)
 
 
+class ServedExperts:
+    """An ExpertLayer's weights in 8 bits, stored (out, in), with the softmax of its chosen experts' logits.
+
+    ``prompt`` sorts the chosen (token, expert) pairs by expert and multiplies quantized rows; ``decode`` takes
+    up to 64 tokens, whose activations it does not quantize.
+    """
+
+    def __init__(self, layer: ExpertLayer, top: int, dtype=torch.float8_e4m3fn):
+        self.top, self.experts, self.dtype = top, layer.experts, dtype
+        (self.w1, self.s1), (self.w2, self.s2) = (quantize_blocks(w, dtype, tiles=True, rows=False, transposed=True)
+                                                  for w in layer.weights)
+
+    def decode(self, x: torch.Tensor, logits: torch.Tensor):
+        return gemm_relu_experts(x, self.w1, self.w2, logits, self.top, w1_scales=self.s1, w2_scales=self.s2)[0]
+
+    def prompt(self, x: torch.Tensor, logits: torch.Tensor):
+        best, ids = logits.topk(self.top, dim=1)
+        share = best.softmax(dim=1)
+        expert, order = ids.reshape(-1).sort(stable=True)
+        ends = torch.searchsorted(expert, torch.arange(self.experts, device=x.device), right=True).to(torch.int32)
+        rows = order // self.top
+        hidden = gemm_relu_blocks(*quantize_blocks(x[rows], self.dtype), self.w1, self.s1, ends=ends, out_dtype=x.dtype)
+        y = gemm_relu_blocks(*quantize_blocks(hidden, self.dtype), self.w2, self.s2, ends=ends, out_dtype=x.dtype, relu=False)
+        out = torch.zeros(x.shape, dtype=torch.float32, device=x.device)
+        return out.index_add_(0, rows, y.float() * share.reshape(-1)[order][:, None]).to(x.dtype)
+
+
 def train(steps: int = 8, tokens: int = 512, experts: int = 8, width: int = 128, hidden: int = 256, rate: float = 0.1):
     """Fits a fixed random target; returns the mean squared error before each step."""
     torch.manual_seed(1)
@@ -72,6 +101,16 @@ def train(steps: int = 8, tokens: int = 512, experts: int = 8, width: int = 128,
         _, gradients = layer.backward((off * (2.0 / tokens)).bfloat16(), saved)
         layer.step(gradients, rate)
     return losses
+
+
+def serve_experts(tokens: int = 24, prompt: int = 500, experts: int = 8, width: int = 256, hidden: int = 512, top: int = 2):
+    """A decoding step and a prompt through one layer in 8 bits: (decoded, prompt's outputs, layer, inputs)."""
+    layer = ExpertLayer(experts, width, hidden, seed=3)
+    served = ServedExperts(layer, top)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(prompt, width, generator=g, device="cuda").bfloat16()
+    logits = torch.randn(prompt, experts, generator=g, device="cuda")
+    return served.decode(x[:tokens], logits[:tokens]), served.prompt(x, logits), layer, (x, logits)
 
 
 def serve(requests=((0, 5), (2, 1), (-1, 3), (2, 1)), width: int = 256, out: int = 512, rank: int = 16, adapters: int = 3):
@@ -90,5 +129,8 @@ def serve(requests=((0, 5), (2, 1), (-1, 3), (2, 1)), width: int = 256, out: int
 if __name__ == "__main__":
     losses = train()
     print("mean squared error by step: " + " ".join(f"{v:.4f}" for v in losses))
+    decoded, prompt, _, _ = serve_experts()
+    off = float((decoded.float() - prompt[: len(decoded)].float()).norm() / decoded.float().norm())
+    print(f"8-bit experts: {len(decoded)} tokens decoded, {len(prompt)} of a prompt; activations in 8 bits change {off:.1%}")
     y, _ = serve()
     print(f"served {y.shape[0]} tokens of 4 requests: outputs {tuple(y.shape)}, mean {float(y.float().mean()):.4f}")
