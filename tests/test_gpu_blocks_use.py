@@ -46,6 +46,57 @@ def test_linear_and_gradients_match_the_formulas(relu, dtype):
         assert torch.equal(gr.linear_blocks(xg, wg, relu=relu), c)
 
 
+def test_captured_backward_pass():
+    # Forward and backward in one graph; no eager graph of the leaves is alive.
+    M, N, K = 130, 144, 200
+    x, w, dc = (torch.zeros(s, dtype=torch.bfloat16, device=DEV) for s in ((M, K), (N, K), (M, N)))
+    x.requires_grad_()
+    w.requires_grad_()
+    gr.linear_blocks(x.detach(), w.detach())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dx, dw = torch.autograd.grad(gr.linear_blocks(x, w), (x, w), dc)
+    for seed in range(1, 6):
+        with torch.no_grad():
+            for i, t in enumerate((x, w, dc)):
+                t.copy_(randn(t.shape, 20 * seed + i))
+            torch.cuda.synchronize()
+            graph.replay()
+            q, s, xt, sxt = gr.quantize_blocks(x, transposed=True)
+            qw, sw, wt, swt = gr.quantize_blocks(w, tiles=True, transposed=True)
+            c = gr.gemm_relu_blocks(q, s, qw, sw)
+            want = gr.gemm_relu_blocks_backward(dc, c, xt, sxt, wt, swt)
+            torch.cuda.synchronize()
+            assert torch.equal(dx, want[0]) and torch.equal(dw, want[1]) and want[0].any() and want[1].any()
+
+
+@pytest.mark.parametrize("shape", [(0, 5, 7), (5, 0, 7), (5, 7, 0), (1, 1, 1)])
+def test_linear_of_nothing(shape):
+    M, N, K = shape
+    x, w = (torch.ones(s, dtype=torch.float16, device=DEV, requires_grad=True) for s in ((M, K), (N, K)))
+    c = gr.linear_blocks(x, w)
+    assert c.shape == (M, N) and (c == K).all()
+    c.backward(torch.ones_like(c))
+    assert (x.grad == N).all() and (w.grad == M).all() and x.grad.shape == x.shape and w.grad.shape == w.shape
+
+
+def test_linear_on_a_side_stream():
+    M, N, K = 520, 300, 700
+    x, w, dc = randn((M, K), 1).to(DEV), randn((N, K), 2).to(DEV), randn((M, N), 3).to(DEV)
+    results = []
+    for stream in (None, torch.cuda.Stream()):
+        xg, wg = x.clone().requires_grad_(), w.clone().requires_grad_()
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        c = gr.linear_blocks(xg, wg, stream=stream)
+        if stream is not None:
+            torch.cuda.current_stream().wait_stream(stream)
+        results.append((c.detach(),) + torch.autograd.grad(c, (xg, wg), dc))
+        torch.cuda.synchronize()
+    assert same(*results)
+
+
 def test_gradients_match_differences():
     """Values that 8 bits hold exactly (integers up to 15 in blocks whose largest is 448, gradients of 1 and 2):
     there the layer is the product itself, so a step of 1 changes sum(dc c) by exactly the gradient's entry."""

@@ -2,8 +2,8 @@
 
 ``quantize_blocks`` makes such matrices, ``gemm_relu_blocks`` multiplies them (dense, or grouped by expert),
 ``gemm_relu_blocks_backward`` has the gradients of a layer that does, and ``linear_blocks`` is such a layer as a
-node of autograd's graph.  ``gemm_relu_experts`` is a whole expert
-layer for a few tokens, with 16-bit or such 8-bit weights.
+node of autograd's graph.  ``gemm_relu_experts`` is a whole expert layer for a few tokens, with 16-bit or such
+8-bit weights.
 As in binding.py this is argument marshalling only, with no fallback.
 
 A quantized matrix is a ``torch.float8_e4m3fn`` or ``torch.float8_e5m2`` tensor whose rows start at multiples
@@ -335,7 +335,8 @@ def linear_blocks(x, w, relu: bool = True, dtype=None, grad_dtype=None, stream=N
 
     x is quantized by rows and w by tiles to ``dtype`` (float8_e4m3fn by default), the gradient of the result
     by rows to ``grad_dtype`` (float8_e5m2); gradients pass the rounding of x and w unchanged.  What backward
-    needs of x and w is kept in 8 bits.  Forward and backward run on ``stream``, or the current one.
+    needs of x and w is kept in 8 bits.  Forward and backward run on ``stream``, or the current one.  A backward
+    pass can be captured; as with torch's own operators, no eager graph of the same leaves may be alive meanwhile.
     """
     _, dev = _first("x", x)
     _check_tensor("x", x, 2, dev, x.dtype)
@@ -348,7 +349,10 @@ def linear_blocks(x, w, relu: bool = True, dtype=None, grad_dtype=None, stream=N
     _format_code("dtype", dtype)
     _format_code("grad_dtype", grad_dtype)
     with _on(stream, dev):
-        return _linear().apply(x, w, bool(relu), dtype, grad_dtype)
+        if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
+            return _linear().apply(x, w, bool(relu), dtype, grad_dtype)
+        return gemm_relu_blocks(*quantize_blocks(x, dtype), *quantize_blocks(w, dtype, tiles=True), out_dtype=x.dtype,
+                                relu=relu)
 
 
 @functools.lru_cache(maxsize=1)
