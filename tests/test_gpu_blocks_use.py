@@ -6,7 +6,7 @@ import torch
 import tiled_dense_gemm_relu_amd as gr
 from tiled_dense_gemm_relu_amd import blocks
 
-from test_gpu_blocks import E4M3, E5M2, check_close, gen, nb, pitched, reference_quantize, stands_for
+from test_gpu_blocks import E4M3, E5M2, check_close, gen, pitched, reference_quantize, stands_for
 from test_gpu_experts import Layer
 from test_gpu_experts import check_close as check_layer
 
@@ -314,3 +314,93 @@ def test_module_runs():
     from tiled_dense_gemm_relu_amd import expert_layer
     decoded, prompt, _, _ = expert_layer.serve_experts()
     assert decoded.isfinite().all() and prompt.isfinite().all() and prompt.shape == (500, 256)
+
+
+# ---------------------------------------------------------------- compiled marshalling
+
+
+class NotCompiled:
+    """Leaves every call to Python."""
+
+    def quantize(self, *args):
+        return None
+
+    multiply = quantize
+
+
+def both_routes(monkeypatch, call):
+    """What a call returns through the compiled marshalling (which has to take it) and through Python's."""
+    class Counting:
+        taken = 0
+
+        def __init__(self, calls):
+            self.calls = calls
+
+        def _call(self, name, args):
+            out = getattr(self.calls, name)(*args)
+            Counting.taken += out is not None
+            return out
+
+        def quantize(self, *args):
+            return self._call("quantize", args)
+
+        def multiply(self, *args):
+            return self._call("multiply", args)
+    with monkeypatch.context() as m:
+        m.setattr(blocks, "_calls", Counting(blocks._compiled()))
+        compiled = call()
+        m.setattr(blocks, "_calls", NotCompiled())
+        return compiled, call(), Counting.taken
+
+
+def same_tensors(u, v):
+    assert u.shape == v.shape and u.dtype == v.dtype and u.stride() == v.stride() and not u.requires_grad
+    return torch.equal(u.view(torch.uint8) if u.element_size() == 1 else u, v.view(torch.uint8) if v.element_size() == 1 else v)
+
+
+@pytest.mark.parametrize("shape", [(1, 16), (48, 160), (3, 32, 144)])
+@pytest.mark.parametrize("kw", [{}, {"tiles": True, "transposed": True}, {"rows": False, "transposed": True, "power_of_two": True},
+                                {"dtype": E5M2, "masked": True, "transposed": True}])
+def test_compiled_quantizer_is_the_same(monkeypatch, shape, kw):
+    kw = dict(kw)
+    x = randn(shape, 1).to(DEV).requires_grad_()
+    if kw.pop("masked", False):
+        kw["mask"] = randn(shape, 2).to(DEV)
+    a, b, taken = both_routes(monkeypatch, lambda: gr.quantize_blocks(x, **kw))
+    assert taken == (shape[-2] % 16 == 0 or not kw.get("transposed", False)) and len(a) == len(b)
+    assert all(same_tensors(u, v) for u, v in zip(a, b))
+
+
+@pytest.mark.parametrize("K", [32, 150])
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("kw", [{}, {"out_dtype": torch.float16, "relu": False}, {"b_rows": True, "config": blocks.CONFIG_64}])
+def test_compiled_product_is_the_same(monkeypatch, K, grouped, kw):
+    q, s = gr.quantize_blocks(randn((40, K), 1).to(DEV))
+    w, sw = gr.quantize_blocks(randn((2, 24, K) if grouped else (24, K), 2).to(DEV), E5M2, tiles=not kw.get("b_rows", False))
+    ends = torch.tensor([10, 37], dtype=torch.int32, device=DEV) if grouped else None
+    a, b, taken = both_routes(monkeypatch, lambda: gr.gemm_relu_blocks(q, s, w, sw, ends=ends, **kw))
+    assert taken == 1 and same_tensors(a, b)
+
+
+def test_compiled_marshalling_refuses_what_python_refuses(monkeypatch):
+    x = randn((32, 32), 1).to(DEV)
+    q, s = gr.quantize_blocks(x)
+    w, sw = gr.quantize_blocks(x, tiles=True)
+    short = torch.zeros(31 * 48 + 20, dtype=torch.uint8, device=DEV).view(E4M3).as_strided((32, 20), (48, 1))
+    bad = [lambda: gr.quantize_blocks(x.float()), lambda: gr.quantize_blocks(x, torch.float16), lambda: gr.quantize_blocks(x.t()),
+           lambda: gr.quantize_blocks(x.cpu()), lambda: gr.quantize_blocks(x[0]), lambda: gr.quantize_blocks(x, mask=x[:16]),
+           lambda: gr.quantize_blocks(x, rows=False), lambda: gr.quantize_blocks(None), lambda: gr.quantize_blocks(x, mask=3),
+           lambda: gr.gemm_relu_blocks(q, s, w, sw.cpu()), lambda: gr.gemm_relu_blocks(q, s[:, :16], w, sw),
+           lambda: gr.gemm_relu_blocks(q, s, w, sw, ends=sw), lambda: gr.gemm_relu_blocks(q, s, w[:, :16], sw),
+           lambda: gr.gemm_relu_blocks(q, s, w, sw, config=9), lambda: gr.gemm_relu_blocks(x, s, w, sw),
+           lambda: gr.gemm_relu_blocks(q, s, w, s), lambda: gr.gemm_relu_blocks(q, s, w, sw, b_rows=True),
+           lambda: gr.gemm_relu_blocks(short, s, short, sw), lambda: gr.gemm_relu_blocks(q.t(), s, w, sw)]
+    for i, call in enumerate(bad):
+        errors = []
+        for calls in (blocks._compiled(), NotCompiled()):
+            with monkeypatch.context() as m:
+                m.setattr(blocks, "_calls", calls)
+                with pytest.raises(Exception) as e:
+                    call()
+                errors.append((type(e.value), str(e.value)))
+        assert errors[0] == errors[1], i

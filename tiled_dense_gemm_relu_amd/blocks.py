@@ -4,7 +4,8 @@
 ``gemm_relu_blocks_backward`` has the gradients of a layer that does, and ``linear_blocks`` is such a layer as a
 node of autograd's graph.  ``gemm_relu_experts`` is a whole expert layer for a few tokens, with 16-bit or such
 8-bit weights.
-As in binding.py this is argument marshalling only, with no fallback.
+As in binding.py this is argument marshalling only, with no fallback.  The marshalling of an ordinary call of the first
+two is compiled (csrc/blocks_calls.cpp), for what takes the GPU less time than Python; it leaves all others to this file.
 
 A quantized matrix is a ``torch.float8_e4m3fn`` or ``torch.float8_e5m2`` tensor whose rows start at multiples
 of 16 bytes (``stride(-2) % 16 == 0``), with float32 scales: by rows ``(blocks, rows)``, one for 128 elements
@@ -53,6 +54,24 @@ def _library():
             lib.gemm_relu_experts_workspace.restype = i64
             _lib = lib
     return _lib
+
+
+_calls = None
+
+
+def _compiled():
+    """The compiled calls, with the entry points of the loaded library."""
+    global _calls
+    if _calls is None:
+        import torch  # noqa: F401  (its libraries are the extension's)
+        lib = _library()
+        try:
+            from . import _blocks_calls as calls
+        except ImportError as e:
+            raise RuntimeError("gemm_relu: _blocks_calls.so is missing or does not fit this torch: build the package again") from e
+        calls.use(*(ctypes.cast(f, ctypes.c_void_p).value for f in (lib.gemm_relu_quantize_blocks, lib.gemm_relu_blocks)))
+        _calls = calls
+    return _calls
 
 
 @functools.lru_cache(maxsize=4096)
@@ -161,6 +180,11 @@ def quantize_blocks(x, dtype=None, tiles: bool = False, mask=None, rows: bool = 
     even.  ``mask`` (x's shape and dtype): x counts as zero where it is not above zero (a ReLU's gradient).
     The outputs carry no gradient.
     """
+    if stream is None:
+        out = (_calls or _compiled()).quantize(x, 0 if dtype is None else _formats().get(dtype), tiles, mask, rows, transposed,
+                                               power_of_two)
+        if out is not None:
+            return out
     import torch
     code, dev = _first("x", x)
     shape = tuple(x.shape)
@@ -223,6 +247,10 @@ def gemm_relu_blocks(a, a_scales, b, b_scales, ends=None, out=None, out_dtype=No
     kernel (CONFIG_*), by default the library's choice.
     """
     import torch
+    if stream is None and out is None and (out_dtype is None or out_dtype is torch.bfloat16 or out_dtype is torch.float16):
+        out = (_calls or _compiled()).multiply(a, a_scales, b, b_scales, ends, out_dtype is not torch.float16, relu, b_rows, config)
+        if out is not None:
+            return out
     fa, lda = _check_8bit("a", a, 2)
     dev = a.get_device()
     grouped = ends is not None

@@ -2,7 +2,7 @@
 
 Each .hip translation unit is compiled to an object in parallel, then linked
 into ``tiled_dense_gemm_relu_amd/libgemm_relu.so`` (in-tree, so it travels with
-the source tree).  Run ``python -m tiled_dense_gemm_relu_amd.build``.
+the source tree), and ``_blocks_calls.so``, compiled argument marshalling, beside it.  Run ``python -m tiled_dense_gemm_relu_amd.build``.
 """
 from __future__ import annotations
 
@@ -22,6 +22,7 @@ ABLATION_PATH = os.path.join(PKG, "layout_ablation")
 MFMA_FORM_PATH = os.path.join(PKG, "mfma_form")
 STREAM_CEILING_PATH = os.path.join(PKG, "stream_ceiling")
 KERNEL_TIMELINE_PATH = os.path.join(PKG, "kernel_timeline")
+CALLS_PATH = os.path.join(PKG, "_blocks_calls.so")
 ARCH = "gfx950"
 
 SOURCES = ["gemm_relu_api.hip", "kernels_f16.hip", "kernels_bf16.hip", "groups_api.hip", "groups_f16.hip",
@@ -98,12 +99,36 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def build_calls() -> str:
+    """Compile the extension module that blocks.py's smallest calls go through (host code, with torch's headers)."""
+    import sysconfig
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("g++ not found: it is required to build _blocks_calls.so")
+    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{home}/include",
+           f"-I{home}/include/torch/csrc/api/include", f"-I{sysconfig.get_paths()['include']}", f"-I{rocm}/include",
+           os.path.join(CSRC, "blocks_calls.cpp"), f"-L{home}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip",
+           "-o", tmp]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for blocks_calls.cpp:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, CALLS_PATH)
+    return CALLS_PATH
+
+
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     """Compile every HIP source and link the shared library.  Returns its path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     extra = list(extra or [])
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as ex:
+        calls = ex.submit(build_calls)
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
+        calls.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)

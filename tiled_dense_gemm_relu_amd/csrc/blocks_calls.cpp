@@ -1,0 +1,172 @@
+// The marshalling of blocks.py's two smallest calls, compiled: where a kernel takes
+// 4 us, checks and allocations made in Python are what a call costs (one row of 4096
+// quantized: 9.4 us a call so, 4.8 here, 2.9 of them the launch).
+//
+// Only the ordinary call is taken: tensors of the right types and shapes on the current
+// device and stream, outputs to be allocated.  For anything else, errors among it, the
+// result is None, and blocks.py's own route does the call or says what is wrong with it.
+#include <Python.h>
+
+#include <ATen/ops/empty.h>
+#include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "../../include/gemm_relu_blocks.h"
+
+namespace {
+
+decltype(&gemm_relu_quantize_blocks) quantize_blocks;
+decltype(&gemm_relu_blocks) product;
+
+constexpr int64_t kBlock = 128;
+int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
+
+const at::Tensor* tensor_of(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
+
+// A contiguous tensor of this type on this device.
+bool plain(const at::Tensor* t, int64_t dim, at::ScalarType type, int device)
+{
+    return t && t->is_cuda() && t->layout() == at::kStrided && t->scalar_type() == type && t->dim() == dim && t->is_contiguous() &&
+           t->get_device() == device;
+}
+
+int dtype_code(at::ScalarType t) { return t == at::kHalf ? GEMM_RELU_F16 : t == at::kBFloat16 ? GEMM_RELU_BF16 : -1; }
+
+at::ScalarType format_type(int64_t format) { return format == GEMM_RELU_E4M3 ? at::kFloat8_e4m3fn : at::kFloat8_e5m2; }
+
+// Pitch of an 8-bit matrix or stack with elements, 0 where Python has to look at it.
+int64_t pitch_of(const at::Tensor* t, int64_t dim, int device, int& format)
+{
+    if (!t || !t->is_cuda() || t->layout() != at::kStrided || t->dim() != dim || t->get_device() != device || t->requires_grad() || t->numel() == 0)
+        return 0;
+    format = t->scalar_type() == at::kFloat8_e4m3fn ? GEMM_RELU_E4M3 : t->scalar_type() == at::kFloat8_e5m2 ? GEMM_RELU_E5M2 : -1;
+    if (format < 0 || reinterpret_cast<uintptr_t>(t->data_ptr()) % 16 != 0) return 0;
+    const int64_t rows = t->size(dim - 2), row = t->size(dim - 1), whole = (row + 15) / 16 * 16;
+    if (row == whole && t->is_contiguous()) return row;
+    const int64_t pitch = t->stride(dim - 2), count = rows * (dim == 3 ? t->size(0) : 1);
+    if (rows < 2 || t->stride(dim - 1) != 1 || pitch < row || pitch % 16 != 0 || (dim == 3 && t->stride(0) != rows * pitch)) return 0;
+    return t->storage_offset() + (count - 1) * pitch + whole <= (int64_t)t->storage().nbytes() ? pitch : 0;
+}
+
+bool sizes_are(const at::Tensor* t, at::IntArrayRef want) { return t->sizes() == want; }
+
+// An argument of another kind than the ordinary call's.
+PyObject* not_here()
+{
+    PyErr_Clear();
+    Py_RETURN_NONE;
+}
+
+// A call of the library without the interpreter's lock: a full queue makes a launch wait.
+template <typename F>
+int unlocked(F&& call)
+{
+    int rc = 0;
+    Py_BEGIN_ALLOW_THREADS
+    rc = call();
+    Py_END_ALLOW_THREADS
+    return rc;
+}
+
+// quantize(x, format, tiles, mask, rows, transposed, power_of_two)
+PyObject* quantize(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 7 || !quantize_blocks) Py_RETURN_NONE;
+    const at::Tensor *x = tensor_of(args[0]), *mask = args[3] == Py_None ? nullptr : tensor_of(args[3]);
+    const long format = PyLong_AsLong(args[1]);
+    const int tiles = PyObject_IsTrue(args[2]), rows = PyObject_IsTrue(args[4]), transposed = PyObject_IsTrue(args[5]),
+              power = PyObject_IsTrue(args[6]);
+    if (PyErr_Occurred()) return not_here();
+    if (!x || !x->is_cuda()) Py_RETURN_NONE;           // (without a GPU there is no current device)
+    const int device = c10::hip::current_device(), code = dtype_code(x->scalar_type());
+    const int64_t dim = x->dim();
+    if (code < 0 || (dim != 2 && dim != 3) || (format != 0 && format != 1) || (!rows && !transposed)) Py_RETURN_NONE;
+    if (!plain(x, dim, x->scalar_type(), device) || x->numel() == 0) Py_RETURN_NONE;
+    if (args[3] != Py_None && !(plain(mask, dim, x->scalar_type(), device) && sizes_are(mask, x->sizes()))) Py_RETURN_NONE;
+    const int64_t R = x->size(dim - 2), C = x->size(dim - 1), count = dim == 3 ? x->size(0) : 1, br = blocks_of(R), bc = blocks_of(C);
+    if ((rows && C % 16 != 0) || (transposed && R % 16 != 0)) Py_RETURN_NONE;
+    const auto bytes = x->options().dtype(format_type(format)).requires_grad(false), words = bytes.dtype(at::kFloat);
+    const auto make = [&](int64_t r, int64_t c, const at::TensorOptions& o) { return dim == 3 ? at::empty({count, r, c}, o) : at::empty({r, c}, o); };
+    at::Tensor q, s, qt, st;
+    if (rows) {
+        q = make(R, C, bytes);
+        s = tiles ? make(br, bc, words) : make(bc, R, words);
+    }
+    if (transposed) {
+        qt = make(C, R, bytes);
+        st = tiles ? make(bc, br, words) : make(br, C, words);
+    }
+    void* const stream = c10::hip::getCurrentHIPStream(device).stream();
+    const int rc = unlocked([&] {
+        return quantize_blocks(x->data_ptr(), mask ? mask->data_ptr() : nullptr, rows ? q.data_ptr() : nullptr,
+                               rows ? static_cast<float*>(s.data_ptr()) : nullptr, transposed ? qt.data_ptr() : nullptr,
+                               transposed ? static_cast<float*>(st.data_ptr()) : nullptr, count, R, C, C, R, code, (int)format, tiles,
+                               power, stream);
+    });
+    if (rc != GEMM_RELU_OK) Py_RETURN_NONE;
+    PyObject* const out = PyTuple_New(2 * (rows + transposed));
+    if (!out) return nullptr;
+    Py_ssize_t at = 0;
+    for (at::Tensor* t : {&q, &s, &qt, &st})
+        if (t->defined()) PyTuple_SET_ITEM(out, at++, THPVariable_Wrap(std::move(*t)));
+    return out;
+    END_HANDLE_TH_ERRORS
+}
+
+// multiply(a, a_scales, b, b_scales, ends, bf16, relu, b_rows, config)
+PyObject* multiply(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 9 || !product) Py_RETURN_NONE;
+    const at::Tensor *a = tensor_of(args[0]), *sa = tensor_of(args[1]), *b = tensor_of(args[2]), *sb = tensor_of(args[3]);
+    const bool grouped = args[4] != Py_None;
+    const at::Tensor* ends = grouped ? tensor_of(args[4]) : nullptr;
+    const int bf16 = PyObject_IsTrue(args[5]), relu = PyObject_IsTrue(args[6]), b_rows = PyObject_IsTrue(args[7]);
+    const long config = PyLong_AsLong(args[8]);
+    if (PyErr_Occurred()) return not_here();
+    if (!a || !a->is_cuda()) Py_RETURN_NONE;
+    const int device = c10::hip::current_device();
+    int fa = 0, fb = 0;
+    const int64_t lda = pitch_of(a, 2, device, fa), ldb = pitch_of(b, grouped ? 3 : 2, device, fb);
+    if (!lda || !ldb) Py_RETURN_NONE;
+    const int64_t M = a->size(0), K = a->size(1), N = b->size(-2), groups = grouped ? b->size(0) : 1, kb = blocks_of(K);
+    if (b->size(-1) != K || config != (int)config) Py_RETURN_NONE;
+    if (!plain(sa, 2, at::kFloat, device) || !sizes_are(sa, {kb, M}) || !plain(sb, grouped ? 3 : 2, at::kFloat, device)) Py_RETURN_NONE;
+    const int64_t s0 = b_rows ? kb : blocks_of(N), s1 = b_rows ? N : kb;
+    if (grouped ? !sizes_are(sb, {groups, s0, s1}) : !sizes_are(sb, {s0, s1})) Py_RETURN_NONE;
+    if (grouped && !(plain(ends, 1, at::kInt, device) && ends->size(0) == groups)) Py_RETURN_NONE;
+    at::Tensor c = at::empty({M, N}, sa->options().dtype(bf16 ? at::kBFloat16 : at::kHalf).requires_grad(false));
+    void* const stream = c10::hip::getCurrentHIPStream(device).stream();
+    const int rc = unlocked([&] {
+        return product(a->data_ptr(), static_cast<const float*>(sa->data_ptr()), b->data_ptr(), static_cast<const float*>(sb->data_ptr()),
+                       grouped ? static_cast<const int32_t*>(ends->data_ptr()) : nullptr, c.data_ptr(), M, N, K, groups, lda, ldb, fa, fb,
+                       b_rows ? GEMM_RELU_SCALES_ROWS : GEMM_RELU_SCALES_TILES, bf16 ? GEMM_RELU_BF16 : GEMM_RELU_F16, relu, (int)config,
+                       stream);
+    });
+    if (rc != GEMM_RELU_OK) Py_RETURN_NONE;
+    return THPVariable_Wrap(std::move(c));
+    END_HANDLE_TH_ERRORS
+}
+
+// use(quantize, product): addresses of the library's entry points
+PyObject* use(PyObject*, PyObject* args)
+{
+    unsigned long long q = 0, p = 0;
+    if (!PyArg_ParseTuple(args, "KK", &q, &p)) return nullptr;
+    quantize_blocks = reinterpret_cast<decltype(quantize_blocks)>(q);
+    product = reinterpret_cast<decltype(product)>(p);
+    Py_RETURN_NONE;
+}
+
+PyMethodDef methods[] = {{"quantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quantize)), METH_FASTCALL, nullptr},
+                         {"multiply", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(multiply)), METH_FASTCALL, nullptr},
+                         {"use", use, METH_VARARGS, nullptr},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_blocks_calls", nullptr, -1, methods};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__blocks_calls() { return PyModule_Create(&module); }
