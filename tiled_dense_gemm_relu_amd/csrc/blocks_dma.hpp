@@ -186,25 +186,25 @@ struct BlockUnits {
     }
 };
 
+// What workgroup `block` of the `blocks` that share a product does.
 template <class Cfg, int FA, int FB, bool B_ROWS>
-__global__ __launch_bounds__(Cfg::THREADS, 1) void blocks_dma(BlocksArgs a)
+__device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int blocks, uint8_t* smem)
 {
     constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK, S = Cfg::STAGES, FM = Cfg::FM, FN = Cfg::FN;
     constexpr int QA = Cfg::QA, QB = Cfg::QB, NQ = Cfg::NQ;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
     constexpr bool WS = Cfg::PRODUCERS > 0;
     const int dwave = WS ? wave - Cfg::WAVES : wave;      // among the waves that load
     const int k_blocks = (a.k + BK - 1) / BK, n_tiles = (a.n + kBlock - 1) / kBlock;
     BlockUnits<Cfg> units;
-    units.init(a.ends, a.groups, a.m, a.n, lane, blockIdx.x, gridDim.x);
+    units.init(a.ends, a.groups, a.m, a.n, lane, block, blocks);
     if (units.rows < a.m) {
         RowsArgs r{};
         r.m = a.m;
         r.n = a.n;
         r.c = a.c;
-        zero_rows(r, units.rows, blockIdx.x, gridDim.x);
+        zero_rows(r, units.rows, block, blocks);
     }
     const int n_units = __builtin_amdgcn_readfirstlane(units.count());
     if (n_units <= 0) return;
@@ -515,6 +515,23 @@ __global__ __launch_bounds__(Cfg::THREADS, 1) void blocks_dma(BlocksArgs a)
         }
         wait_vmcnt<0>();   // no LDS DMA may outlive the workgroup
     }
+}
+
+template <class Cfg, int FA, int FB, bool B_ROWS>
+__global__ __launch_bounds__(Cfg::THREADS, 1) void blocks_dma(BlocksArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES];
+    blocks_tiles<Cfg, FA, FB, B_ROWS>(a, blockIdx.x, gridDim.x, smem);
+}
+
+// Two products in one launch, the second with scales of B by rows.
+template <class Cfg, int FA, int FB>
+__global__ __launch_bounds__(Cfg::THREADS, 1) void blocks_pair(BlocksPair p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES];
+    const int block = blockIdx.x;
+    if (block < p.blocks[0]) blocks_tiles<Cfg, FA, FB, false>(p.product[0], block, p.blocks[0], smem);
+    else blocks_tiles<Cfg, FA, FB, true>(p.product[1], block - p.blocks[0], p.blocks[1], smem);
 }
 
 }  // namespace gemm_relu_hip

@@ -26,7 +26,8 @@ BlocksKernels make_blocks_table()
 {
     BlocksKernels t{{{(const void*)blocks_dma<Blocks256, FA, FB, false>, (const void*)blocks_dma<Blocks256, FA, FB, true>},
                           {(const void*)blocks_dma<Blocks128, FA, FB, false>, (const void*)blocks_dma<Blocks128, FA, FB, true>},
-                          {(const void*)blocks_dma<Blocks64, FA, FB, false>, (const void*)blocks_dma<Blocks64, FA, FB, true>}}, {}};
+                          {(const void*)blocks_dma<Blocks64, FA, FB, false>, (const void*)blocks_dma<Blocks64, FA, FB, true>}}, {},
+                    (const void*)blocks_pair<Blocks64, FA, FB>};
     fill_stream<FA, FB, 0>(t);
     return t;
 }

@@ -222,10 +222,16 @@ __device__ __forceinline__ void quantize_tile(const QuantizeArgs& a, const u32x4
 template <int DT, int FORMAT, bool TILES, bool VEC>
 __global__ __launch_bounds__(kQuantizeThreads, 4) void quantize_blocks(QuantizeArgs a)
 {
+    int64_t block = blockIdx.x;
+    if (a.apart > 0) {
+        if (block < a.apart) a.qt = nullptr;
+        else a.q = nullptr;
+        block = block < a.apart ? block : block - a.apart;
+    }
     __shared__ Shared sh;
     const int tid = threadIdx.x, cc = tid & 15, rr = tid >> 4;
-    const int64_t tiles = (int64_t)a.tiles_r * a.tiles_c, matrix = (int64_t)blockIdx.x / tiles;
-    const int tile = (int)((int64_t)blockIdx.x - matrix * tiles), tr = tile / a.tiles_c, tc = tile % a.tiles_c;
+    const int64_t tiles = (int64_t)a.tiles_r * a.tiles_c, matrix = block / tiles;
+    const int tile = (int)(block - matrix * tiles), tr = tile / a.tiles_c, tc = tile % a.tiles_c;
     // This thread's 8 x 8 elements.  The tile's rows begin inside 2^28 bytes of each other.
     const int row = 8 * rr, col = 8 * cc, rows = min(kBlock, a.rows - tr * kBlock), cols = min(kBlock, a.cols - tc * kBlock);
     const size_t origin = ((size_t)matrix * (size_t)a.rows + (size_t)tr * kBlock) * (size_t)a.cols + (size_t)tc * kBlock;
@@ -248,23 +254,19 @@ __global__ __launch_bounds__(kQuantizeThreads, 4) void quantize_blocks(QuantizeA
     } else {
         // rows of any length: dwords, shifted into place, zeros behind the row
         const AnyRsrc rx = make_any_rsrc(a.x + origin, bytes), rm = make_any_rsrc(mask, bytes);
+        AnyChunk x[8], m[8];
 #pragma unroll
-        for (int i0 = 0; i0 < 8; i0 += 4) {
-            AnyChunk x[4], m[4];
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t at = ((uint32_t)(row + i) * (uint32_t)a.cols + (uint32_t)col) * 2u;
+            const bool inside = row + i < rows && col < cols;
+            x[i] = load_any(rx, at, inside);
+            if (a.mask) m[i] = load_any(rm, at, inside);
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = row + i0 + i;
-                const uint32_t at = ((uint32_t)r * (uint32_t)a.cols + (uint32_t)col) * 2u;
-                const bool inside = r < rows && col < cols;
-                x[i] = load_any(rx, at, inside);
-                if (a.mask) m[i] = load_any(rm, at, inside);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                u32x4 e = chunk_value(x[i]);
-                if (a.mask) e = mask_chunk<DT>(e, chunk_value(m[i]));
-                v[i0 + i] = keep_first(e, row + i0 + i < rows ? cols - col : 0);
-            }
+        for (int i = 0; i < 8; ++i) {
+            u32x4 e = chunk_value(x[i]);
+            if (a.mask) e = mask_chunk<DT>(e, chunk_value(m[i]));
+            v[i] = keep_first(e, row + i < rows ? cols - col : 0);
         }
     }
     // Whether all of the tile's elements are finite, which saves their being asked for.

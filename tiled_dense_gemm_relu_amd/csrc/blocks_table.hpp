@@ -13,7 +13,7 @@ constexpr int kBlock = 128;
 // Formats of 8-bit matrices (GEMM_RELU_E4M3, _E5M2; the matrix instructions' codes).
 enum { kE4M3 = 0, kE5M2 = 1 };
 
-// One launch quantizes both ways what it reads once; q or qt may be nullptr.
+// One launch quantizes both ways; q or qt may be nullptr.
 struct QuantizeArgs {
     const uint16_t* x;
     const uint16_t* mask;  // nullptr: none
@@ -24,6 +24,7 @@ struct QuantizeArgs {
     int rows, cols, tiles_r, tiles_c;
     int64_t ldq, ldqt;
     int power_of_two;
+    int apart;             // > 0: so many workgroups write q, and as many after them qt
 };
 constexpr int kQuantizeThreads = 256;
 
@@ -41,6 +42,12 @@ struct BlocksArgs {
     int c_vec;             // rows of C allow 16-byte stores
 };
 
+// Two products of small size in one launch of tiles of 64: workgroups of each.
+struct BlocksPair {
+    BlocksArgs product[2];
+    int blocks[2];
+};
+
 constexpr int kNumBlockTiles = 3;
 constexpr int kBlockTile[kNumBlockTiles] = {256, 128, 64};
 constexpr int kBlockThreads[kNumBlockTiles] = {512, 512, 512};
@@ -54,6 +61,7 @@ constexpr int kStreamWaves[kNumStreams] = {8, 8, 4, 8, 4, 8}, kStreamStages[kNum
 struct BlocksKernels {
     const void* tile[kNumBlockTiles][2];      // [tile][scales of B by rows]
     const void* stream[kNumStreams][2];
+    const void* pair;
 };
 // By the formats of A and B.
 const BlocksKernels& blocks_kernels_e4m3_e4m3();
