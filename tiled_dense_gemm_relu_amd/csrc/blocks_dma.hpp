@@ -18,8 +18,6 @@
 
 namespace gemm_relu_hip {
 
-
-
 typedef int int32x8_t __attribute__((ext_vector_type(8)));
 
 // 16 x 16 fp32 sums over 128 k: `w` of format FW, `x` of format FX.  A lane holds
@@ -127,9 +125,8 @@ __device__ __forceinline__ void interleave()
 // GROUP_M row tiles, column by column (tile_coords), the whole list dealt out in
 // equal parts to the XCDs, so that tiles which share operands share an L2.  (Dealing
 // whole columns of tiles, as RowUnits does, leaves an XCD with half as many again
-// where there are few: 1000 x 1104 x 517, 18 columns of 16 tiles, 13.8 us against 11.4.)
-// Lane l keeps what
-// belongs to group l; with more than 64 groups a lookup scans `ends` again.
+// where there are few: 1000 x 1104 x 517, 18 columns of 16 tiles, 13.8 us against 11.4.)  Lane l keeps
+// what belongs to group l; with more than 64 groups a lookup scans `ends` again.
 template <class Cfg>
 struct BlockUnits {
     const int* ends;
