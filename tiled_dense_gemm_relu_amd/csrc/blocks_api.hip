@@ -62,6 +62,12 @@ int launch_quantize(QuantizeArgs a, int64_t count, int dtype, int format, int fo
                    kQuantizeThreads, args, stream);
 }
 
+// Whether weights of so many bytes are streamed past the caches.  From memory they come
+// faster so, from the cache beside it (256 MB) slower: few rows x 16384 x 8192 28.2 us and
+// 24.2, 32 groups of 2048 x 2048 29.7 and 27.3; but 8192 x 8192 12.7 and 16.9 where they
+// stay there, 18.0 and 16.5 where they do not.
+constexpr int64_t kStreamOnce = int64_t(96) << 20;
+
 // Tiles of `tile` x `tile` that a product can have: whole ones, and a partial one for each group.
 int64_t most_tiles(const BlocksArgs& a, int64_t tile)
 {
@@ -125,6 +131,7 @@ int launch_blocks(BlocksArgs a, int format_a, int format_b, int form_b, int conf
         // row tiles: whole ones, a partial one of each group, and those of no group's rows
         const int64_t tiles = a.ends ? std::min<int64_t>(a.m, a.m / r + a.groups + 1) : ceil_div(a.m, r);
         const int64_t units = tiles * ceil_div(a.n, 16 * kStreamCols[kind]);
+        a.once = (int64_t)std::min(a.groups, a.m) * a.n * a.ldb >= kStreamOnce;
         if (launchable(units, threads))
             return enqueue(kernels(format_a, format_b).stream[kind][rows_b], dim3((unsigned)units), threads, args, stream);
         config = GEMM_RELU_BLOCKS_64;
@@ -290,7 +297,7 @@ int gemm_relu_blocks(const void* A, const float* scales_a, const void* B, const 
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (K == 0) return zero_fill(C, M * N, s);
     BlocksArgs a{static_cast<const uint8_t*>(A), scales_a, static_cast<const uint8_t*>(B), scales_b, static_cast<uint16_t*>(C),
-                 ends, (int)M, (int)N, (int)K, (int)groups, (uint32_t)lda, (uint32_t)ldb, relu, dtype == GEMM_RELU_BF16, 0};
+                 ends, (int)M, (int)N, (int)K, (int)groups, (uint32_t)lda, (uint32_t)ldb, relu, dtype == GEMM_RELU_BF16, 0, 0};
     return launch_blocks(a, format_a, format_b, form_b, config_id, cus, s);
 }
 
@@ -344,7 +351,7 @@ int gemm_relu_blocks_backward(const void* dC, const void* C, const void* XT, con
     rc = launch_quantize(d, 1, dtype, format, GEMM_RELU_SCALES_ROWS, s);
     const int bf16 = dtype == GEMM_RELU_BF16;
     const BlocksPair both{{{q, sq, static_cast<const uint8_t*>(WT), scales_wt, static_cast<uint16_t*>(dX), nullptr, (int)M, (int)K, (int)N, 1,
-                            (uint32_t)space.ldq, (uint32_t)ldwt, 0, bf16, 0},
+                            (uint32_t)space.ldq, (uint32_t)ldwt, 0, bf16, 0, 0},
                            {qt, st, static_cast<const uint8_t*>(XT), scales_xt, static_cast<uint16_t*>(dW), nullptr, (int)N, (int)K, (int)M, 1,
                             (uint32_t)space.ldqt, (uint32_t)ldxt, 0, bf16, 0}},
                           {}};
@@ -432,6 +439,7 @@ int gemm_relu_experts(const void* X, const void* W1, const float* scales1, const
     // As many workgroups as run at once.
     const auto launch = [&](int odd, int second, int kind, int64_t units) {
         const int64_t room = (kind == 0 ? 2 : 3) * cus;
+        a.once = std::min(experts, slots) * (kn ? a.in : a.out) * a.ld >= kStreamOnce;
         return enqueue(kernels.products[store][odd][second][kind], dim3((unsigned)std::max<int64_t>(1, std::min(units, room))),
                        64 * kExpertWaves[kind], args, s, (size_t)route_table_bytes(slots, experts));
     };

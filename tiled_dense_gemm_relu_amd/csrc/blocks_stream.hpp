@@ -87,9 +87,13 @@ __global__ __launch_bounds__(64 * kStreamWaves[KIND], 1) void blocks_stream(Bloc
 #pragma unroll
                 for (int j = 0; j < MB; ++j)
                     dma_b128(uniform(xp + (size_t)(16 * j) * a.lda, (uint32_t)max(0, rows - 16 * j) * a.lda), to + (2 * j + h) * 1024, xo, (uint32_t)k0);
+                const auto weights = [&](auto&& load) __attribute__((always_inline)) {
 #pragma unroll
-                for (int i2 = 0; i2 < NB; ++i2)
-                    dma_b128(uniform(wp + (size_t)(16 * i2) * a.ldb, (uint32_t)max(0, cols - 16 * i2) * a.ldb), to + X_BYTES + (2 * i2 + h) * 1024, wo, (uint32_t)k0);
+                    for (int i2 = 0; i2 < NB; ++i2)
+                        load(uniform(wp + (size_t)(16 * i2) * a.ldb, (uint32_t)max(0, cols - 16 * i2) * a.ldb), to + X_BYTES + (2 * i2 + h) * 1024, wo, (uint32_t)k0);
+                };
+                if (a.once) weights(dma_b128_once);
+                else weights(dma_b128);
             }
             dma_b32(uniform(a.sa + (size_t)b * (size_t)a.m + (size_t)tile.begin, (live ? (uint32_t)rows : 0u) * 4u), to + X_BYTES + W_BYTES, 4u * (uint32_t)lane, 0u);
             dma_b32(uniform(B_ROWS ? sb + (size_t)b * (size_t)a.n : sb + b, live ? B_ROWS ? (uint32_t)cols * 4u : 4u : 0u),

@@ -40,6 +40,7 @@ struct BlocksArgs {
     uint32_t lda, ldb;
     int relu, bf16;
     int c_vec;             // rows of C allow 16-byte stores
+    int once;              // streaming kernels: the weights do not stay in the caches
 };
 
 // Two products of small size in one launch of tiles of 64: workgroups of each.
@@ -87,6 +88,7 @@ struct ExpertsArgs {
     int64_t ld;            // bytes from a row of w to the next
     int tokens, in, out, experts, top, mid_row;
     int renormalize, routed, splits;
+    int once;              // with many units: the weights do not stay in the caches
 };
 
 constexpr int kMaxTokens = 64, kMaxTop = 16, kMaxExperts = 1024;

@@ -15,6 +15,8 @@
 // block to end adds each token's in the order of its choices.
 #pragma once
 
+#include <type_traits>
+
 #include "blocks_bytes.hpp"
 #include "blocks_table.hpp"
 #include "groups_skinny.hpp"
@@ -451,7 +453,8 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
 // of S stages: W, then X's rows in halves of 64 k, then their low parts.
 //  x_row[q]: where the row of X of this lane's 16 bytes of DMA instruction q begins,
 // in bytes (kOobOffset: none).
-template <int DT, int STORE, bool SPLIT_X, int NB, int MB, int S, int WAVES>
+// ONCE: W does not stay in the caches.
+template <int DT, int STORE, bool SPLIT_X, bool ONCE, int NB, int MB, int S, int WAVES>
 __device__ __forceinline__ void expert_stream(floatx4 (&acc)[NB][MB], const uint16_t* x, uint32_t x_bytes, const uint32_t (&x_row)[2 * MB],
                                               uint32_t x_low, const uint8_t* w, const float* scales, int64_t ld, int n0, int in,
                                               int out, int p0, int p1, uint8_t* ring, int turn, int wave, int lane)
@@ -494,22 +497,26 @@ __device__ __forceinline__ void expert_stream(floatx4 (&acc)[NB][MB], const uint
         const bool live = i < mine;
         const int p = __builtin_amdgcn_readfirstlane(piece_at(live ? i : 0)), k0 = p * K, left = live ? in - k0 : 0;   // elements
         const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)(ring_lds + (uint32_t)(slot * STAGE)));
-        if constexpr (KN) {
+        const auto weights = [&](auto&& load) __attribute__((always_inline)) {
+            if constexpr (KN) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int k = k0 + 8 * q;
-                // up to the end of the last row
-                const uint32_t bytes = left > 8 * q ? (uint32_t)min(8, left - 8 * q) * (uint32_t)ld - 2u * (uint32_t)n0 : 0u;
-                dma_b128(uniform(w + (size_t)min(k, in) * (size_t)ld + 2 * (size_t)n0, bytes), to + q * 1024, w_off[(q >> 1) & 1], 0u);
-            }
-        } else {
+                for (int q = 0; q < 8; ++q) {
+                    const int k = k0 + 8 * q;
+                    // up to the end of the last row
+                    const uint32_t bytes = left > 8 * q ? (uint32_t)min(8, left - 8 * q) * (uint32_t)ld - 2u * (uint32_t)n0 : 0u;
+                    load(uniform(w + (size_t)min(k, in) * (size_t)ld + 2 * (size_t)n0, bytes), to + q * 1024, w_off[(q >> 1) & 1], 0u);
+                }
+            } else {
 #pragma unroll
-            for (int q = 0; q < 2 * NB; ++q) {
-                const int skip = 16 * (q >> 1);
-                dma_b128(uniform(w + (size_t)(n0 + skip) * (size_t)ld, (uint32_t)max(0, cols - skip) * (uint32_t)ld), to + q * 1024,
+                for (int q = 0; q < 2 * NB; ++q) {
+                    const int skip = 16 * (q >> 1);
+                    load(uniform(w + (size_t)(n0 + skip) * (size_t)ld, (uint32_t)max(0, cols - skip) * (uint32_t)ld), to + q * 1024,
                          pos[q & 1] < (WIDE ? left : 2 * left) ? w_off[q & 1] : kOobOffset, (uint32_t)(WIDE ? k0 : 2 * k0));
+                }
             }
-        }
+        };
+        if constexpr (ONCE) weights(dma_b128_once);
+        else weights(dma_b128);
 #pragma unroll
         for (int h = 0; h < HALVES; ++h)
 #pragma unroll
@@ -708,8 +715,18 @@ __global__ __launch_bounds__(64 * kExpertWaves[KIND], KIND == 1 ? ODD || STORE >
             uint32_t x_row[2 * MB];
 #pragma unroll
             for (int q = 0; q < 2 * MB; ++q) x_row[q] = row_of_x(row0 + 8 * q + lane / 8);
-            expert_stream<DT, STORE, SECOND, NB, MB, S, WAVES>(acc, a.x, x_bytes, x_row, (uint32_t)a.mid_row * 2u, w, scales, a.ld, n0, a.in,
-                                                               a.out, p0, p1, smem + wave * (S * STAGE), unit % max(p1 - p0, 1), wave, lane);
+            const auto stream = [&](auto once) __attribute__((always_inline)) {
+                expert_stream<DT, STORE, SECOND, once.value, NB, MB, S, WAVES>(acc, a.x, x_bytes, x_row, (uint32_t)a.mid_row * 2u, w, scales, a.ld,
+                                                                               n0, a.in, a.out, p0, p1, smem + wave * (S * STAGE),
+                                                                               unit % max(p1 - p0, 1), wave, lane);
+            };
+            // (A branch for every piece costs 24 tokens 131 -> 140 us, both loops one token 24.3 -> 25.4.)
+            if constexpr (KIND == 1) {
+                if (a.once) stream(std::true_type{});
+                else stream(std::false_type{});
+            } else {
+                stream(std::false_type{});
+            }
         }
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
