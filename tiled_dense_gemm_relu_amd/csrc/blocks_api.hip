@@ -125,17 +125,21 @@ int launch_blocks(BlocksArgs a, int format_a, int format_b, int form_b, int conf
     const int rows_b = form_b == GEMM_RELU_SCALES_ROWS;
     const BlocksChoice choice(a.m, a.n, a.groups, !a.ends);
     if (config == GEMM_RELU_BLOCKS_AUTO) config = choice.config;
+    const bool heavy = (int64_t)std::min(a.groups, a.m) * a.n * a.ldb >= kStreamOnce;
     void* args[] = {&a};
     if (config == GEMM_RELU_BLOCKS_STREAM) {
         const int kind = choice.stream, r = 16 * kStreamRows[kind], threads = 64 * kStreamWaves[kind];
         // row tiles: whole ones, a partial one of each group, and those of no group's rows
         const int64_t tiles = a.ends ? std::min<int64_t>(a.m, a.m / r + a.groups + 1) : ceil_div(a.m, r);
         const int64_t units = tiles * ceil_div(a.n, 16 * kStreamCols[kind]);
-        a.once = (int64_t)std::min(a.groups, a.m) * a.n * a.ldb >= kStreamOnce;
+        a.once = heavy;
         if (launchable(units, threads))
             return enqueue(kernels(format_a, format_b).stream[kind][rows_b], dim3((unsigned)units), threads, args, stream);
         config = GEMM_RELU_BLOCKS_64;
     }
+    // Groups whose rows make a tile or two read their weights about once (one product of 1024 rows
+    // x 4096 x 4096 would take 27 instead of 25.5 us).
+    a.once = heavy && a.ends && config != GEMM_RELU_BLOCKS_256;
     const int64_t tiles = most_tiles(a, kBlockTile[config]);
     if (tiles > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
     const int64_t grid = std::min<int64_t>(tiles, config == GEMM_RELU_BLOCKS_64 ? 2 * cus : cus);

@@ -229,14 +229,19 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
     const uint32_t scales_lds = lds_base + Cfg::S_REGION + 256u * (uint32_t)piece;
 
     // The load side; past the last unit everything is out of range and fetches nothing.
-    int f_unit = 0, f_k = 0, f_rows = 0, f_cols = 0;
+    int f_unit = 0, f_k = 0, f_left = 0, f_turn = 0, f_rows = 0, f_cols = 0;
     const uint8_t *f_a = a.a, *f_b = a.b;
     const float* f_s = a.sa;          // this wave's scales of block 0
     uint32_t f_soff = 0, f_sbytes = 0, f_sstep = 0;
     auto fill_setup = [&]() {
         const int live = f_unit < n_units ? 1 : 0;
         const DmaUnit u = unit_at(live ? f_unit : n_units - 1);
-        f_k = 0;
+        // Weights from memory: every column of tiles starts at another block of its rows (as in
+        // blocks_stream.hpp), and has passed the caches once its rows' tiles have read it.  64
+        // groups of 64 rows x 2048 x 4096: 123 -> 117 us past the caches, 103 so.
+        if constexpr (WS) f_turn = a.once && k_blocks >= 2 * S ? (u.n0 / BN + 3 * u.group) % k_blocks * BK : 0;
+        f_k = f_turn;
+        f_left = k_blocks;
         f_rows = live * (u.m_end - u.m0);
         f_cols = live * min(BN, a.n - u.n0);
         f_a = a.a + (size_t)u.m0 * a.lda;
@@ -276,9 +281,13 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
                      pos[q & 1] >= left ? kOobOffset : a_voff[q & 1], (uint32_t)f_k);
         } else if (q < QA + QB) {
             const int p = q - QA;
-            dma_b128(rows_from(f_b, f_cols, (dwave * QB + (p & ~1)) * 8, a.ldb),
-                     lds_base + Cfg::B_REGION + slot * Cfg::B_STAGE + (dwave * QB + p) * 1024,
-                     pos[p & 1] >= left ? kOobOffset : b_voff[p & 1], (uint32_t)f_k);
+            const auto load = [&](auto&& dma) __attribute__((always_inline)) {
+                dma(rows_from(f_b, f_cols, (dwave * QB + (p & ~1)) * 8, a.ldb),
+                    lds_base + Cfg::B_REGION + slot * Cfg::B_STAGE + (dwave * QB + p) * 1024,
+                    pos[p & 1] >= left ? kOobOffset : b_voff[p & 1], (uint32_t)f_k);
+            };
+            if (WS && a.once) load(dma_b128_once);
+            else load(dma_b128);
         } else {
             const int32x4_t r = rsrc_words(f_s + (size_t)(f_k / BK) * f_sstep, f_sbytes);
             dma_b32(int32x4_t{__builtin_amdgcn_readfirstlane(r[0]), __builtin_amdgcn_readfirstlane(r[1]),
@@ -288,8 +297,8 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
     };
     auto fill_advance = [&]() {
         if (f_unit >= n_units) return;
-        f_k += BK;
-        if (f_k >= a.k) {
+        f_k = f_k + BK < a.k ? f_k + BK : 0;
+        if (--f_left == 0) {
             ++f_unit;
             fill_setup();
         }
@@ -336,7 +345,7 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
                 for (int q = 0; q < NQ; ++q) dma(s, q);
                 fill_advance();
             }
-            int k = 0;                 // of the stage that lands
+            int k = f_turn, left = k_blocks;                 // of the stage that lands
             for (int g = 0; g < steps; ++g) {
                 wait_vmcnt<(S - 2) * NQ>();
                 cut_off(g & (S - 1), a.k - k);
@@ -345,6 +354,10 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) dma((g + S - 1) & (S - 1), q);
                 fill_advance();
+                if (--left == 0) {     // (the loads are less than a unit ahead, or turn is 0 for all)
+                    k = f_turn;
+                    left = k_blocks;
+                }
             }
             wait_vmcnt<0>();           // no LDS DMA may outlive the workgroup
             lds_barrier();

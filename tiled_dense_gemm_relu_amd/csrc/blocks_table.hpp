@@ -40,7 +40,7 @@ struct BlocksArgs {
     uint32_t lda, ldb;
     int relu, bf16;
     int c_vec;             // rows of C allow 16-byte stores
-    int once;              // streaming kernels: the weights do not stay in the caches
+    int once;              // all tiles but 256: the weights do not stay in the caches
 };
 
 // Two products of small size in one launch of tiles of 64: workgroups of each.
