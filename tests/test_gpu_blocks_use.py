@@ -325,7 +325,7 @@ class NotCompiled:
     def quantize(self, *args):
         return None
 
-    multiply = quantize
+    multiply = backward = experts = quantize
 
 
 def both_routes(monkeypatch, call):
@@ -336,16 +336,12 @@ def both_routes(monkeypatch, call):
         def __init__(self, calls):
             self.calls = calls
 
-        def _call(self, name, args):
-            out = getattr(self.calls, name)(*args)
-            Counting.taken += out is not None
-            return out
-
-        def quantize(self, *args):
-            return self._call("quantize", args)
-
-        def multiply(self, *args):
-            return self._call("multiply", args)
+        def __getattr__(self, name):
+            def call(*args):
+                out = getattr(self.calls, name)(*args)
+                Counting.taken += out is not None
+                return out
+            return call
     with monkeypatch.context() as m:
         m.setattr(blocks, "_calls", Counting(blocks._compiled()))
         compiled = call()
@@ -382,10 +378,43 @@ def test_compiled_product_is_the_same(monkeypatch, K, grouped, kw):
     assert taken == 1 and same_tensors(a, b)
 
 
+@pytest.mark.parametrize("shape", [(32, 48, 64), (33, 50, 70)])
+@pytest.mark.parametrize("kw", [{}, {"relu": False}, {"dtype": E4M3}])
+def test_compiled_gradients_are_the_same(monkeypatch, shape, kw):
+    M, N, K = shape
+    xt, sx = gr.quantize_blocks(randn((M, K), 1).to(DEV), rows=False, transposed=True)
+    wt, sw = gr.quantize_blocks(randn((N, K), 2).to(DEV), tiles=True, rows=False, transposed=True)
+    dc, c = randn((M, N), 3).to(DEV).requires_grad_(), randn((M, N), 4).to(DEV)
+    call = lambda: gr.gemm_relu_blocks_backward(dc, c if kw.get("relu", True) else None, xt, sx, wt, sw, **kw)  # noqa: E731
+    call()                                               # takes the stream's workspace
+    a, b, taken = both_routes(monkeypatch, call)
+    assert taken == 1 and all(same_tensors(u, v) for u, v in zip(a, b))
+    gr.release_workspaces()
+    again, _, taken = both_routes(monkeypatch, call)     # without one Python does the call
+    assert taken == 0 and all(same_tensors(u, v) for u, v in zip(a, again))
+
+
+@pytest.mark.parametrize("kind", ["nk", "kn", "e4m3"])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_compiled_expert_layer_is_the_same(monkeypatch, kind, renormalize):
+    layer = Layer(kind, torch.bfloat16, 6, 100, 70, 90, 5)
+    x, logits = randn((5, 100), 1).to(DEV), torch.randn((5, 6), generator=gen(2)).to(DEV)
+    call = lambda: layer(x, logits, 2, renormalize=renormalize)  # noqa: E731
+    call()
+    a, b, taken = both_routes(monkeypatch, call)
+    assert taken == 1 and len(a) == len(b) == 3 and all(same_tensors(u, v) for u, v in zip(a, b))
+    x.requires_grad_()
+    a, b, taken = both_routes(monkeypatch, call)         # (taken inside the node of autograd's graph)
+    assert taken == 1 and a[0].requires_grad and b[0].requires_grad and torch.equal(a[0], b[0])
+    with torch.no_grad():
+        assert both_routes(monkeypatch, call)[2] == 1
+
+
 def test_compiled_marshalling_refuses_what_python_refuses(monkeypatch):
     x = randn((32, 32), 1).to(DEV)
     q, s = gr.quantize_blocks(x)
     w, sw = gr.quantize_blocks(x, tiles=True)
+    e, logits = x.expand(2, 32, 32).contiguous(), torch.zeros((32, 2), device=DEV)
     short = torch.zeros(31 * 48 + 20, dtype=torch.uint8, device=DEV).view(E4M3).as_strided((32, 20), (48, 1))
     bad = [lambda: gr.quantize_blocks(x.float()), lambda: gr.quantize_blocks(x, torch.float16), lambda: gr.quantize_blocks(x.t()),
            lambda: gr.quantize_blocks(x.cpu()), lambda: gr.quantize_blocks(x[0]), lambda: gr.quantize_blocks(x, mask=x[:16]),
@@ -394,7 +423,16 @@ def test_compiled_marshalling_refuses_what_python_refuses(monkeypatch):
            lambda: gr.gemm_relu_blocks(q, s, w, sw, ends=sw), lambda: gr.gemm_relu_blocks(q, s, w[:, :16], sw),
            lambda: gr.gemm_relu_blocks(q, s, w, sw, config=9), lambda: gr.gemm_relu_blocks(x, s, w, sw),
            lambda: gr.gemm_relu_blocks(q, s, w, s), lambda: gr.gemm_relu_blocks(q, s, w, sw, b_rows=True),
-           lambda: gr.gemm_relu_blocks(short, s, short, sw), lambda: gr.gemm_relu_blocks(q.t(), s, w, sw)]
+           lambda: gr.gemm_relu_blocks(short, s, short, sw), lambda: gr.gemm_relu_blocks(q.t(), s, w, sw),
+           lambda: gr.gemm_relu_blocks_backward(x, x, q, s, w, sw[:, :0]), lambda: gr.gemm_relu_blocks_backward(x, None, q, s, w, sw),
+           lambda: gr.gemm_relu_blocks_backward(x, x[:16], q, s, w, sw), lambda: gr.gemm_relu_blocks_backward(x, x, q, s, w[:16], sw),
+           lambda: gr.gemm_relu_blocks_backward(x, x, q, s, w, sw, dtype=torch.float16),
+           lambda: gr.gemm_relu_blocks_backward(x.float(), x, q, s, w, sw),
+           lambda: gr.gemm_relu_experts(x, e, e, logits, 3), lambda: gr.gemm_relu_experts(x, e, e, logits, None),
+           lambda: gr.gemm_relu_experts(x, e, e, logits[:, :1], 1), lambda: gr.gemm_relu_experts(x, e, e.half(), logits, 1),
+           lambda: gr.gemm_relu_experts(x, e, e, logits, 1, w1_scales=s), lambda: gr.gemm_relu_experts(x, e, e, logits, 1, b_layout=7),
+           lambda: gr.gemm_relu_experts(x, e, e[:, :16], logits, 1), lambda: gr.gemm_relu_experts(x, q, q, logits, 1),
+           lambda: gr.gemm_relu_experts(x.repeat(3, 1), e, e, logits.repeat(3, 1), 1)]
     for i, call in enumerate(bad):
         errors = []
         for calls in (blocks._compiled(), NotCompiled()):

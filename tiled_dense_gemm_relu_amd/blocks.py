@@ -4,8 +4,8 @@
 ``gemm_relu_blocks_backward`` has the gradients of a layer that does, and ``linear_blocks`` is such a layer as a
 node of autograd's graph.  ``gemm_relu_experts`` is a whole expert layer for a few tokens, with 16-bit or such
 8-bit weights.
-As in binding.py this is argument marshalling only, with no fallback.  The marshalling of an ordinary call of the first
-two is compiled (csrc/blocks_calls.cpp), for what takes the GPU less time than Python; it leaves all others to this file.
+As in binding.py this is argument marshalling only, with no fallback.  The marshalling of ordinary calls is compiled
+(csrc/blocks_calls.cpp), for what takes the GPU less time than Python; it leaves all others to this file.
 
 A quantized matrix is a ``torch.float8_e4m3fn`` or ``torch.float8_e5m2`` tensor whose rows start at multiples
 of 16 bytes (``stride(-2) % 16 == 0``), with float32 scales: by rows ``(blocks, rows)``, one for 128 elements
@@ -19,7 +19,7 @@ import threading
 
 from . import binding
 from .binding import B_KN, B_NK, _check, _stream_handle
-from .groups import _call, _check_layout, _check_shape, _check_tensor, _first, _new, _on, _workspace
+from .groups import _call, _check_layout, _check_shape, _check_tensor, _first, _new, _on, _spaces, _workspace
 
 BLOCK = 128                # GEMM_RELU_BLOCK
 
@@ -69,7 +69,9 @@ def _compiled():
             from . import _blocks_calls as calls
         except ImportError as e:
             raise RuntimeError("gemm_relu: _blocks_calls.so is missing or does not fit this torch: build the package again") from e
-        calls.use(*(ctypes.cast(f, ctypes.c_void_p).value for f in (lib.gemm_relu_quantize_blocks, lib.gemm_relu_blocks)))
+        calls.use(*(ctypes.cast(f, ctypes.c_void_p).value
+                    for f in (lib.gemm_relu_quantize_blocks, lib.gemm_relu_blocks, lib.gemm_relu_blocks_backward,
+                              lib.gemm_relu_blocks_backward_workspace, lib.gemm_relu_experts, lib.gemm_relu_experts_workspace)))
         _calls = calls
     return _calls
 
@@ -284,6 +286,11 @@ def gemm_relu_blocks_backward(dc, c, xt, xt_scales, wt, wt_scales, relu: bool = 
     ``need_dx=False`` / ``need_dw=False`` leave one out (None is returned, and ``wt`` / ``xt`` with their
     scales may be None).  ``c`` is only read with ``relu=True``.  The gradients have dc's dtype.
     """
+    if stream is None and workspace is None and dx is None and dw is None and need_dx and need_dw:
+        out = (_calls or _compiled()).backward(dc, c, xt, xt_scales, wt, wt_scales, relu,
+                                               1 if dtype is None else _formats().get(dtype), _spaces)
+        if out is not None:
+            return out
     import torch
     code, dev = _first("dc", dc)
     _check_tensor("dc", dc, 2, dev, dc.dtype)
@@ -415,6 +422,10 @@ def gemm_relu_experts(x, w1, w2, logits=None, top=None, ids=None, weights=None, 
     x's dtype (``out`` if given).  There is no gradient: a backward pass is refused, and so is ``out`` where
     gradients are on and an input requires one.
     """
+    if stream is None and workspace is None and out is None and ids is None and weights is None:
+        result = (_calls or _compiled()).experts(x, w1, w2, logits, top, w1_scales, w2_scales, b_layout, renormalize, _spaces)
+        if result is not None:
+            return result
     import torch
     code, dev = _first("x", x)
     _check_layout(b_layout)
