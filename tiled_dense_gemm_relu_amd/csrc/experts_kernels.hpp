@@ -262,10 +262,12 @@ __device__ __forceinline__ u32x4 widen(uint32_t lo, uint32_t hi)
 // Storage of the weights: 16-bit (out, in) or (in, out) in X's dtype, or 8-bit (out, in).
 enum { kStoreNK = 0, kStoreKN = 1, kStoreE4M3 = 2, kStoreE5M2 = 3 };
 
+typedef uint32_t u32x3 __attribute__((ext_vector_type(3)));
+
 // A lane's weights of a piece, on their way: 16 columns x 128 k in NB blocks.
 //  NK: [block][k-step] 8 consecutive k of column 16 block + lane % 16.
-//  KN: [k-step][k] 4 consecutive columns 4 (lane % 16) .. of k-step's k 8 kb .., and
-//      with ODD the dword after them.
+//  KN: [k-step][k] 4 consecutive columns 4 (lane % 16) .. of k-step's k 8 kb .., in 3
+//      dwords, which hold them at 2-byte alignment too.
 //  8-bit: [block][half] 16 consecutive k.
 template <int STORE, bool ODD, int NB>
 struct PieceWeights;
@@ -276,8 +278,7 @@ struct PieceWeights<kStoreNK, ODD, NB> {
 template <bool ODD, int NB>
 struct PieceWeights<kStoreKN, ODD, NB> {
     static_assert(NB == 4, "4 columns a lane");
-    u32x2 v[4][8];
-    uint32_t next[ODD ? 4 : 1][ODD ? 8 : 1];
+    u32x3 v[4][8];
 };
 template <bool ODD, int NB>
 struct PieceWeights<kStoreE4M3, ODD, NB> {
@@ -335,13 +336,7 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const uint32_t off = 4 * r16 < cols ? ((uint32_t)(32 * s + 8 * g + e) * (uint32_t)out + 4u * (uint32_t)r16) * 2u : kOobOffset;
-                        if constexpr (ODD) {
-                            const uint32_t at = (off + rp.shift) & ~3u;
-                            pw[q].v[s][e] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rp.rsrc, at, 0, 0));
-                            pw[q].next[s][e] = __builtin_amdgcn_raw_buffer_load_b32(rp.rsrc, at + 8u, 0, 0);
-                        } else {
-                            pw[q].v[s][e] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rp.rsrc, off, 0, 0));
-                        }
+                        pw[q].v[s][e] = __builtin_amdgcn_raw_buffer_load_b96(rp.rsrc, (off + rp.shift) & ~3u, 0, 0);
                     }
             } else {
 #pragma unroll
@@ -392,12 +387,10 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
                     u32x2 row[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        row[e] = pw[q].v[s][e];
-                        if constexpr (ODD) {
-                            const uint32_t off = ((uint32_t)(32 * s + 8 * g + e) * (uint32_t)out + 4u * (uint32_t)r16) * 2u + base;
-                            const uint32_t bits = (off & 2u) * 8u;
-                            row[e] = u32x2{__builtin_amdgcn_alignbit(row[e].y, row[e].x, bits), __builtin_amdgcn_alignbit(pw[q].next[s][e], row[e].y, bits)};
-                        }
+                        const u32x3 v = pw[q].v[s][e];
+                        const uint32_t off = ((uint32_t)(32 * s + 8 * g + e) * (uint32_t)out + 4u * (uint32_t)r16) * 2u + base;
+                        const uint32_t bits = (off & 2u) * 8u;
+                        row[e] = u32x2{__builtin_amdgcn_alignbit(v.y, v.x, bits), __builtin_amdgcn_alignbit(v.z, v.y, bits)};
                         if (tail && e >= valid) row[e] = u32x2{0u, 0u};
                     }
 #pragma unroll
