@@ -94,26 +94,38 @@ int64_t most_tiles(const BlocksArgs& a, int64_t tile)
 //   64 in 64 groups, 2048 x 2048  78.5 / 60.8 / 50.4 / 62.7 / 49.5 / 66.5     58.3  53.2
 //   256 in 32, 1024 x 1024        19.9 / 14.4 / 11.1 / 14.4 / 11.5 / 15.3     11.7  12.3
 //   512 in 8, 2048 x 2048         33.8 / 22.6 / 17.5 / 17.5 / 13.9 / 15.5     11.7  17.6
+//  More than 32 rows and more than one workgroup a CU: tiles of 64, us streaming and so
+// (64 rows): 65536 x 1024 30.0 / 16.8, 32768 x 2048 20.2 / 15.6, 24576 x 8192 54.6 / 50.4,
+// 17000 x 1024 14.4 / 10.3; at one a CU the longer sums stream, 16384 x 4096 16.0 / 15.2,
+// x 8192 30.7 / 31.4.  Groups of up to 32 rows likewise, 8 groups x 8192 x 512 13.5 / 11.2,
+// 16 x 1024 x 2048 11.6 / 10.0, 8 x 1024 x 4096 10.8 / 14.5.
+//  Groups of few rows with weights from memory: the deepest ring reads them fastest where
+// its units go round three times, us streaming, tiles of 64 and of 128 (32 rows a group):
+// 64 x 2048 x 4096 115 / 107 / 102, 16 x 16384 x 4096 217 / 212 / 198, 16 x 4096 x 4096
+// 59.8 / 50.9 / 50.7, 32 x 2048 x 2048 30.9 / 26.8 / 30.0.
 // Tiles: the largest whose tiles are mostly full and numerous enough to occupy the CUs.
 struct BlocksChoice {
     int config, stream = -1;
-    BlocksChoice(int64_t m, int64_t n, int64_t groups, bool dense)
+    BlocksChoice(int64_t m, int64_t n, int64_t k, int64_t groups, bool dense, bool heavy)
     {
         const int64_t used = std::min(groups, m), rows = m / used;
         const auto tiles = [&](int64_t r, int64_t c) { return used * ceil_div(rows, r) * ceil_div(n, c); };
         if (dense) {
             const int64_t by16 = tiles(16, 64), by32 = tiles(32, 64), by64 = tiles(64, 64);
-            if (rows > 32 && by64 >= 192) stream = rows <= 64 ? 5 : -1;
+            if (rows > 32 && by64 >= 192) stream = rows <= 64 && by64 <= 256 && k > 4096 ? 5 : -1;
             else if (rows > 16 && by32 >= 192) stream = by32 <= 384 ? 3 : 4;
             else stream = by16 < 192 ? 0 : by16 <= 384 ? 1 : 2;
-        } else if (rows <= 32) {
+        } else if (rows <= 32 && !heavy) {
             const int64_t most = rows + rows / 2 + 6;         // few groups have more rows
-            stream = most <= 16 ? (tiles(16, 64) < 192 ? 0 : tiles(16, 64) <= 384 ? 1 : 2) : tiles(32, 64) <= 384 ? 3 : 4;
+            const int64_t by16 = tiles(16, 64);
+            if (most <= 16) stream = by16 < 192 ? 0 : by16 <= 384 ? 1 : by16 <= 512 ? 2 : -1;
+            else if (tiles(32, 64) < 256) stream = 3;
         }
-        config = stream >= 0                               ? GEMM_RELU_BLOCKS_STREAM
-                 : rows >= 192 && tiles(256, 256) >= 192   ? GEMM_RELU_BLOCKS_256
-                 : rows >= 96 && tiles(128, 128) >= 128    ? GEMM_RELU_BLOCKS_128
-                                                           : GEMM_RELU_BLOCKS_64;
+        config = stream >= 0                                                         ? GEMM_RELU_BLOCKS_STREAM
+                 : rows >= 192 && tiles(256, 256) >= 192                             ? GEMM_RELU_BLOCKS_256
+                 : rows >= 96 && tiles(128, 128) >= 128                              ? GEMM_RELU_BLOCKS_128
+                 : !dense && heavy && tiles(128, 128) >= 768                         ? GEMM_RELU_BLOCKS_128
+                                                                                     : GEMM_RELU_BLOCKS_64;
         if (stream < 0) stream = rows <= 16 ? 2 : 4;       // on request
     }
 };
@@ -123,9 +135,9 @@ int launch_blocks(BlocksArgs a, int format_a, int format_b, int form_b, int conf
 {
     a.c_vec = a.n % 8 == 0 && aligned(a.c, 16);
     const int rows_b = form_b == GEMM_RELU_SCALES_ROWS;
-    const BlocksChoice choice(a.m, a.n, a.groups, !a.ends);
-    if (config == GEMM_RELU_BLOCKS_AUTO) config = choice.config;
     const bool heavy = (int64_t)std::min(a.groups, a.m) * a.n * a.ldb >= kStreamOnce;
+    const BlocksChoice choice(a.m, a.n, a.k, a.groups, !a.ends, heavy);
+    if (config == GEMM_RELU_BLOCKS_AUTO) config = choice.config;
     void* args[] = {&a};
     if (config == GEMM_RELU_BLOCKS_STREAM) {
         const int kind = choice.stream, r = 16 * kStreamRows[kind], threads = 64 * kStreamWaves[kind];
@@ -137,9 +149,9 @@ int launch_blocks(BlocksArgs a, int format_a, int format_b, int form_b, int conf
             return enqueue(kernels(format_a, format_b).stream[kind][rows_b], dim3((unsigned)units), threads, args, stream);
         config = GEMM_RELU_BLOCKS_64;
     }
-    // Groups whose rows make a tile or two read their weights about once (one product of 1024 rows
+    // Rows that make a tile or two a group read their weights about once (one product of 1024 rows
     // x 4096 x 4096 would take 27 instead of 25.5 us).
-    a.once = heavy && a.ends && config != GEMM_RELU_BLOCKS_256;
+    a.once = heavy && (a.ends || a.m <= kBlockTile[config]) && config != GEMM_RELU_BLOCKS_256;
     const int64_t tiles = most_tiles(a, kBlockTile[config]);
     if (tiles > INT32_MAX) return GEMM_RELU_ERR_TOO_LARGE;
     const int64_t grid = std::min<int64_t>(tiles, config == GEMM_RELU_BLOCKS_64 ? 2 * cus : cus);
@@ -189,6 +201,17 @@ struct BackwardSpace {
 
 // The expert layer: kinds of workgroups, parts of its second product's K, and places in
 // the workspace.
+//  8 waves for few units, where one workgroup a CU is all there is; 4, and 64 columns, for
+// many.  Measured, us a layer with 8 waves and with 4 (tokens x top of experts, K = N x hidden;
+// units of 64 columns):
+//   1 x 4 of 64,  2048 x 2048     128    24.8 /  26.8        8-bit  4 x 2 of 16, 1024 x 1024   128    17.4 /  20.6
+//   1 x 2 of 8,   4096 x 4096     128    33.0 /  35.8        8-bit  8 x 2 of 32, 2048 x 2048   544    46.4 /  36.8
+//   4 x 2 of 16,  1024 x 1024     128    19.1 /  21.1        8-bit 24 x 4 of 64                4480   213  / 171
+//   2 x 4 of 64,  2048 x 2048     256    45.4 /  38.0        (K, N)  4 x 2 of 16, 1024 x 1024  128    20.3 /  20.6
+//   8 x 2 of 32,  1024 x 1024     272    33.3 /  25.8        (K, N)  8 x 2 of 32, 1024 x 1024  272    25.7 /  25.5
+//  16 x 4 of 64,  2048 x 2048    2176     157 / 122          (K, N) 16 x 2 of 32, 2048 x 2048  1088   99.8 /  86.6
+//  The second product's K is cut where its units leave CUs without work: 1 x 1 of 8,
+// 512 x 8192, 23.5 us whole and 17.7 in 8 parts; 1 x 2 of 8, 1024 x 4096, 21.0 and 20.5.
 struct ExpertsSpace {
     int kind1, kind2;      // index into kExpertBlocks
     int64_t units1, units2, splits, mid_row, mid, part, part_bytes, bytes;
@@ -219,6 +242,11 @@ struct ExpertsSpace {
 };
 static_assert(((int64_t(1) << 20) + 63) / 64 <= ExpertsSpace::kMaxColumnBlocks, "a counter for each block of 64 columns");
 
+// Every workgroup of the first product makes the choices for itself, unless that costs it more
+// than a launch: a choice takes a wave about 0.1 us, for more than 64 experts longer.  Measured,
+// us a layer without and with a launch for them: 8 tokens x 4 of 64 21.9 / 23.5, 16 x 4 of 64
+// 26.3 / 27.5, 8 x 4 of 256 24.8 / 25.1; 17 x 4 of 64 30.8 / 29.8, 64 x 4 of 64 50.6 / 43.0,
+// 16 x 8 of 256 34.5 / 29.5, 4 x 8 of 1024 39.1 / 34.4.
 bool route_apart(int64_t tokens, int64_t experts, int64_t top) { return tokens > 16 || tokens * top * ceil_div(experts, 64) > 128; }
 
 int check_experts(int64_t tokens, int64_t n, int64_t hidden, int64_t experts, int64_t top, int b_layout)
@@ -448,8 +476,6 @@ int gemm_relu_experts(const void* X, const void* W1, const float* scales1, const
                        64 * kExpertWaves[kind], args, s, (size_t)route_table_bytes(slots, experts));
     };
     const bool odd1 = !even(X, K) || (!bytes && !(kn ? even(W1, hidden) : even(W1, K)));
-    // Every workgroup of the first product makes the choices for itself, unless that costs
-    // it more than a launch: a choice takes a wave about 0.1 us, for more than 64 experts longer.
     if (logits && route_apart(tokens, experts, top)) {
         rc = enqueue(kernels.route, dim3((unsigned)tokens), 64, args, s);
         if (rc != GEMM_RELU_OK) return rc;

@@ -11,6 +11,7 @@
 
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/narrow.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
@@ -95,23 +96,24 @@ PyObject* quantize(PyObject*, PyObject* const* args, Py_ssize_t n)
     if (!plain(x, dim, x->scalar_type(), device) || x->numel() == 0) Py_RETURN_NONE;
     if (args[3] != Py_None && !(plain(mask, dim, x->scalar_type(), device) && sizes_are(mask, x->sizes()))) Py_RETURN_NONE;
     const int64_t R = x->size(dim - 2), C = x->size(dim - 1), count = dim == 3 ? x->size(0) : 1, br = blocks_of(R), bc = blocks_of(C);
-    if ((rows && C % 16 != 0) || (transposed && R % 16 != 0)) Py_RETURN_NONE;
+    const int64_t ldq = (C + 15) / 16 * 16, ldqt = (R + 15) / 16 * 16;
     const auto bytes = x->options().dtype(format_type(format)).requires_grad(false), words = bytes.dtype(at::kFloat);
     const auto make = [&](int64_t r, int64_t c, const at::TensorOptions& o) { return dim == 3 ? at::empty({count, r, c}, o) : at::empty({r, c}, o); };
+    const auto pitched = [&](int64_t r, int64_t c, int64_t ld) { return ld == c ? make(r, c, bytes) : make(r, ld, bytes).narrow(-1, 0, c); };
     at::Tensor q, s, qt, st;
     if (rows) {
-        q = make(R, C, bytes);
+        q = pitched(R, C, ldq);
         s = tiles ? make(br, bc, words) : make(bc, R, words);
     }
     if (transposed) {
-        qt = make(C, R, bytes);
+        qt = pitched(C, R, ldqt);
         st = tiles ? make(bc, br, words) : make(br, C, words);
     }
     void* const stream = c10::hip::getCurrentHIPStream(device).stream();
     const int rc = unlocked([&] {
         return quantize_blocks(x->data_ptr(), mask ? mask->data_ptr() : nullptr, rows ? q.data_ptr() : nullptr,
                                rows ? static_cast<float*>(s.data_ptr()) : nullptr, transposed ? qt.data_ptr() : nullptr,
-                               transposed ? static_cast<float*>(st.data_ptr()) : nullptr, count, R, C, C, R, code, (int)format, tiles,
+                               transposed ? static_cast<float*>(st.data_ptr()) : nullptr, count, R, C, ldq, ldqt, code, (int)format, tiles,
                                power, stream);
     });
     if (rc != GEMM_RELU_OK) Py_RETURN_NONE;

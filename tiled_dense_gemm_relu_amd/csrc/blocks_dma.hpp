@@ -10,6 +10,12 @@
 // read as the 16-bit kernels' (a_swizzle<128>), and the scales of those rows and
 // columns as floats: with scales by tiles every lane of the scales' DMA fetches
 // its column's tile, so both forms look alike in LDS.
+//
+// The 256 tile at 8192^3 on normal data: 464-490 us, 2.25-2.37 PFLOP/s, where a library
+// product with one scale a matrix takes 410-419.  Without the additions it takes 428,
+// without DMA 392; loads by all waves with one barrier a step, and matrix instructions
+// interleaved with additions, are what it got there by.  The smaller tiles have waves
+// that only load: 64 groups of 64 rows x 2048 x 4096 103 us, 5.5 TB/s.
 #pragma once
 
 #include "blocks_bytes.hpp"

@@ -13,6 +13,10 @@
 // values, so that the second one's matrix instructions lose nothing of it.  The
 // second launch's units write a choice's products as fp32; the last unit of a column
 // block to end adds each token's in the order of its choices.
+//
+// 24 tokens, 4 of 64 experts, 8-bit 2048 x 4096: 139 us, 6 TB/s of the chosen experts'
+// weights.  One token, 4 experts, 16-bit 2048 x 2048: two launches of 12.5 us, each a
+// chain of launch, table, first bytes and 33 MB.
 #pragma once
 
 #include <type_traits>
