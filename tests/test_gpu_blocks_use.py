@@ -354,7 +354,7 @@ def same_tensors(u, v):
     return torch.equal(u.view(torch.uint8) if u.element_size() == 1 else u, v.view(torch.uint8) if v.element_size() == 1 else v)
 
 
-@pytest.mark.parametrize("shape", [(1, 16), (48, 160), (3, 32, 144), (1, 1), (17, 130), (2, 33, 31)])
+@pytest.mark.parametrize("shape", [(1, 16), (48, 160), (3, 32, 144), (1, 1), (17, 130), (2, 33, 31), (3, 1040), (1100, 5), (2, 20, 2049)])
 @pytest.mark.parametrize("kw", [{}, {"tiles": True, "transposed": True}, {"rows": False, "transposed": True, "power_of_two": True},
                                 {"dtype": E5M2, "masked": True, "transposed": True}])
 def test_compiled_quantizer_is_the_same(monkeypatch, shape, kw):

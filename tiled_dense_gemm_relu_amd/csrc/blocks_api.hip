@@ -189,8 +189,9 @@ struct BackwardSpace {
     int64_t q, s, qt, st, bytes, ldq, ldqt;
     BackwardSpace(int64_t m, int64_t n)
     {
-        ldq = round_up(n, 16);
-        ldqt = round_up(m, 16);
+        // long rows start at whole cache lines, so that no piece of 128 bytes lies in two
+        ldq = round_up(n, n <= 1024 ? 16 : 128);
+        ldqt = round_up(m, m <= 1024 ? 16 : 128);
         q = GEMM_RELU_GROUPS_COUNTER_BYTES;
         s = q + round_up(m * ldq, 256);
         qt = s + round_up(4 * m * blocks_of(n), 256);

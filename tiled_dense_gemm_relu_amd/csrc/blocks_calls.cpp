@@ -96,7 +96,9 @@ PyObject* quantize(PyObject*, PyObject* const* args, Py_ssize_t n)
     if (!plain(x, dim, x->scalar_type(), device) || x->numel() == 0) Py_RETURN_NONE;
     if (args[3] != Py_None && !(plain(mask, dim, x->scalar_type(), device) && sizes_are(mask, x->sizes()))) Py_RETURN_NONE;
     const int64_t R = x->size(dim - 2), C = x->size(dim - 1), count = dim == 3 ? x->size(0) : 1, br = blocks_of(R), bc = blocks_of(C);
-    const int64_t ldq = (C + 15) / 16 * 16, ldqt = (R + 15) / 16 * 16;
+    // (long rows start at whole cache lines, as blocks.py's do)
+    const auto pitch = [](int64_t row) { return row <= 1024 ? (row + 15) / 16 * 16 : (row + 127) / 128 * 128; };
+    const int64_t ldq = pitch(C), ldqt = pitch(R);
     const auto bytes = x->options().dtype(format_type(format)).requires_grad(false), words = bytes.dtype(at::kFloat);
     const auto make = [&](int64_t r, int64_t c, const at::TensorOptions& o) { return dim == 3 ? at::empty({count, r, c}, o) : at::empty({r, c}, o); };
     const auto pitched = [&](int64_t r, int64_t c, int64_t ld) { return ld == c ? make(r, c, bytes) : make(r, ld, bytes).narrow(-1, 0, c); };
