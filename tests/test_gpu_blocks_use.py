@@ -272,6 +272,33 @@ def test_side_stream_and_two_streams_at_once():
         assert same(got[0], want) and same(got[1], want_other)
 
 
+def test_two_threads_on_one_stream():
+    # They share the stream's workspace: the launches of a call stay together.
+    import threading
+    layer = Layer("nk", torch.bfloat16, 6, 100, 300, 90, 5)
+    M, N, K = 96, 160, 272
+    jobs = []
+    for seed in (1, 2):
+        x, logits = randn((20, 100), seed).to(DEV), torch.randn((20, 6), generator=gen(10 + seed)).to(DEV)
+        xt, sx = gr.quantize_blocks(randn((M, K), 20 + seed).to(DEV), rows=False, transposed=True)
+        wt, sw = gr.quantize_blocks(randn((N, K), 30 + seed).to(DEV), tiles=True, rows=False, transposed=True)
+        dc, c = randn((M, N), 40 + seed).to(DEV), randn((M, N), 50 + seed).to(DEV)
+        jobs.append(lambda x=x, logits=logits: layer(x, logits, 2))
+        jobs.append(lambda dc=dc, c=c, xt=xt, sx=sx, wt=wt, sw=sw: gr.gemm_relu_blocks_backward(dc, c, xt, sx, wt, sw))
+    want, wrong = [job() for job in jobs], []
+
+    def run(i):
+        for _ in range(100):
+            if not same(jobs[i](), want[i]):
+                wrong.append(i)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_own_workspace_is_left_clean():
     layer = Layer("nk", torch.bfloat16, 5, 136, 200, 520, 3)
     x, logits = randn((9, 136), 1).to(DEV), torch.randn((9, 5), generator=gen(2)).to(DEV)
