@@ -89,3 +89,89 @@ def test_expert_layer(kind, tokens):
             hidden = (wide[0][e].double() @ x[t].double()).clamp_min(0) * float(weights[t, j])
             want[t] += wide[1][e].double() @ hidden
     assert torch.equal(y, want.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("config", [blocks.CONFIG_64, blocks.CONFIG_128, blocks.CONFIG_STREAM])
+@pytest.mark.parametrize("M", [3, 64, 100])
+def test_dense_by_every_kernel(config, M):
+    N, K = 12345, 8200
+    a, b, sa, sb = integers((M, K), 21), integers((N, K), 22), scale_tiles((65, M), 23), scale_tiles((97, 65), 24)
+    c = gr.gemm_relu_blocks(eight_bit(a), sa, eight_bit(b), sb, config=config)
+    wide_a = a.float() * sa.t().repeat_interleave(128, 1)[:, :K]
+    assert torch.equal(c, (wide_a @ (b.float() * spread(sb, N, K)).t()).relu().to(torch.bfloat16))
+
+
+# ---------------------------------------------------------------- the longest rows, and places past 2^32 bytes
+
+
+@pytest.mark.parametrize("M,N", [(3, 5), (70, 65), (300, 20)])
+def test_longest_sums(M, N):
+    K = 1 << 20
+    a, b = integers((M, K), 31, -1, 1), integers((N, K), 32, -1, 1)
+    ones = torch.ones((K // 128, M), device=DEV), torch.ones((1, K // 128), device=DEV)
+    c = gr.gemm_relu_blocks(eight_bit(a), ones[0], eight_bit(b), ones[1], relu=False, out_dtype=torch.float16)
+    assert torch.equal(c, (a.float() @ b.float().t()).half())
+
+
+def test_longest_rows_of_an_expert_layer():
+    for K, H, N in ((1 << 20, 3, 70), (70, 1 << 20, 3), (3, 70, 1 << 20)):
+        x, w1, w2 = (integers(s, 33 + i, -1, 1).to(torch.bfloat16) for i, s in enumerate(((2, K), (2, H, K), (2, N, H))))
+        ids, weights = torch.tensor([[1], [0]], dtype=torch.int32, device=DEV), torch.ones((2, 1), device=DEV)
+        y = gr.gemm_relu_experts(x, w1, w2, ids=ids, weights=weights)[0]
+        for t, e in ((0, 1), (1, 0)):
+            hidden = (w1[e].double() @ x[t].double()).clamp_min(0)
+            assert torch.equal(y[t], (w2[e].double() @ hidden).to(torch.bfloat16)), (K, H, N)
+
+
+def test_quantizer_past_32_bits():
+    R, C = 140000, 16384                                  # 4.6 GB
+    x = torch.randint(-30000, 30000, (R, C), dtype=torch.int16, generator=torch.Generator(device=DEV).manual_seed(41), device=DEV)
+    x = x.view(torch.bfloat16)                           # every finite magnitude (and no NaN: below 0x7f80)
+    q, s, qt, st = gr.quantize_blocks(x, transposed=True)
+    for r, c in ((0, 0), (139904, 16256), (139904, 0), (70016, 8192), (131072, 16256)):
+        part = x[r:r + 128, c:c + 128].contiguous()
+        pq, ps, pqt, pst = gr.quantize_blocks(part, transposed=True)
+        rows = part.shape[0]
+        assert torch.equal(q[r:r + 128, c:c + 128].view(torch.uint8), pq.view(torch.uint8)) and torch.equal(s[c // 128, r:r + 128], ps[0])
+        assert torch.equal(qt[c:c + 128, r:r + 128].view(torch.uint8), pqt.view(torch.uint8)) and torch.equal(st[r // 128, c:c + 128], pst[0])
+        assert rows == min(128, R - r)
+
+
+@pytest.mark.parametrize("rows", [5, 100, 300])
+def test_weights_past_32_bits(rows):
+    G, N, K = 20, 16384, 16384                            # 5.4 GB
+    a = integers((3 * rows, K), 51)
+    b = torch.empty((G, N, K), dtype=torch.uint8, device=DEV)
+    for g in (0, 16, 19):
+        b[g] = eight_bit(integers((N, K), 52 + g)).view(torch.uint8)
+    ends = torch.tensor([rows] * 16 + [2 * rows] * 3 + [3 * rows], dtype=torch.int32, device=DEV)
+    ones = torch.ones((128, 3 * rows), device=DEV), torch.ones((G, 128, 128), device=DEV)
+    c = gr.gemm_relu_blocks(eight_bit(a), ones[0], b.view(E4M3), ones[1], ends=ends, relu=False)
+    for i, g in enumerate((0, 16, 19)):
+        part = slice(i * rows, (i + 1) * rows)
+        assert torch.equal(c[part], (a[part].float() @ b[g].view(E4M3).float().t()).to(torch.bfloat16)), g
+
+
+def test_results_past_32_bits():
+    M, N, K = 70000, 32800, 40                            # 4.6 GB of results
+    a, b = integers((M, K), 61), integers((N, K), 62)
+    for config in (blocks.CONFIG_AUTO, blocks.CONFIG_64):
+        c = gr.gemm_relu_blocks(eight_bit(a), torch.ones((1, M), device=DEV), eight_bit(b), torch.ones((257, 1), device=DEV),
+                                relu=False, config=config)
+        for m in (0, 65400, M - 200):
+            assert torch.equal(c[m:m + 200], (a[m:m + 200].float() @ b.float().t()).to(torch.bfloat16)), (config, m)
+        del c
+
+
+@pytest.mark.parametrize("kind", ["nk", "kn"])
+def test_expert_layer_past_32_bits(kind):
+    E, K, H = 18, 16384, 8192                             # 4.8 GB a stack
+    x, logits = integers((3, K), 71, -1, 1).to(torch.bfloat16), torch.zeros((3, E), device=DEV)
+    logits[0, 17] = logits[1, 16] = logits[2, 0] = 50.0
+    w1, w2 = (torch.randint(-1, 2, s, dtype=torch.int8, generator=torch.Generator(device=DEV).manual_seed(72), device=DEV).to(torch.bfloat16)
+              for s in (((E, H, K), (E, K, H)) if kind == "nk" else ((E, K, H), (E, H, K))))
+    y = gr.gemm_relu_experts(x, w1, w2, logits, 1, b_layout=gr.B_NK if kind == "nk" else gr.B_KN)[0]
+    for t, e in ((0, 17), (1, 16), (2, 0)):
+        first, second = (w[e].double() if kind == "nk" else w[e].double().t() for w in (w1, w2))
+        want = (second @ (first @ x[t].double()).clamp_min(0))
+        assert torch.equal(y[t], want.to(torch.bfloat16)), t

@@ -270,6 +270,13 @@ def test_side_stream_and_two_streams_at_once():
         got = [w(stream=s) for w, s in zip((work, other), streams)]
         torch.cuda.synchronize()
         assert same(got[0], want) and same(got[1], want_other)
+    for _ in range(4):                                   # and as the current streams
+        got = []
+        for w, s in zip((work, other), streams):
+            with torch.cuda.stream(s):
+                got.append(w())
+        torch.cuda.synchronize()
+        assert same(got[0], want) and same(got[1], want_other)
 
 
 def test_two_threads_on_one_stream():
@@ -314,6 +321,47 @@ def test_own_workspace_is_left_clean():
 
 
 # ---------------------------------------------------------------- together
+
+
+def test_masked_places_may_hold_anything():
+    # A ReLU's gradient: infinities and NaN where the output is not above zero change nothing.
+    M, N, K = 140, 150, 130
+    xt, sx = gr.quantize_blocks(randn((M, K), 1).to(DEV), rows=False, transposed=True)
+    wt, sw = gr.quantize_blocks(randn((N, K), 2).to(DEV), tiles=True, rows=False, transposed=True)
+    dc, c = randn((M, N), 3), randn((M, N), 4)
+    c[7] = -1.0                                          # a row and a column without any
+    c[:, 9] = 0.0
+    c[3, 5], c[4, 6] = float("nan"), -float("inf")       # not above zero either
+    bad = dc.clone()
+    holes = ~(c > 0)
+    bad[holes] = torch.tensor([float("inf"), -float("inf"), float("nan"), torch.finfo(torch.bfloat16).min])[
+        torch.arange(int(holes.sum())) % 4].to(torch.bfloat16)
+    clean = torch.where(holes, torch.zeros_like(dc), dc)
+    for f in (lambda d: gr.gemm_relu_blocks_backward(d.to(DEV), c.to(DEV), xt, sx, wt, sw),
+              lambda d: gr.quantize_blocks(d.to(DEV), E5M2, mask=c.to(DEV), transposed=True)):
+        got, want = f(bad), f(clean)
+        assert all(same_tensors(u, v) for u, v in zip(got, want))
+    dx, dw = gr.gemm_relu_blocks_backward(bad.to(DEV), c.to(DEV), xt, sx, wt, sw)
+    assert not dx[7].any() and not dw[9].any() and dx.isfinite().all() and dw.isfinite().all()
+
+
+def test_calls_as_the_documentation_has_them():
+    M, N, K, top = 33, 70, 150, 2
+    x, w, dc = randn((M, K), 1).to(DEV), randn((N, K), 2).to(DEV), randn((M, N), 3).to(DEV)
+    q, s, qt, st = gr.quantize_blocks(x, transposed=True)
+    qw, sw, wt, sw_t = gr.quantize_blocks(w, tiles=True, transposed=True)
+    c = gr.gemm_relu_blocks(q, s, qw, sw)
+    dx, dw = gr.gemm_relu_blocks_backward(dc, c, qt, st, wt, sw_t)
+    x.requires_grad_()
+    w.requires_grad_()
+    layer = gr.linear_blocks(x, w)
+    assert torch.equal(layer, c)
+    layer.backward(dc)
+    assert torch.equal(x.grad, dx) and torch.equal(w.grad, dw)
+    w1, w2, logits = randn((4, 20, K), 4).to(DEV), randn((4, K, 20), 5).to(DEV), randn((M, 4), 6).float().to(DEV)
+    with torch.no_grad():
+        y, ids, weights = gr.gemm_relu_experts(x, w1, w2, logits, top)
+    assert y.shape == x.shape and ids.shape == weights.shape == (M, top)
 
 
 def test_served_layer():
