@@ -29,8 +29,7 @@
  * Workspace.  As in gemm_relu_groups.h (gemm_relu_blocks needs none): device memory of at least the bytes that
  * the *_workspace function returns for the same arguments, 256-byte aligned, its
  * first GEMM_RELU_GROUPS_COUNTER_BYTES zero before the first use and left zero by
- * every call; one buffer serves all calls of one stream, of both headers.  The launches of
- * a call of this header follow each other on the stream also when threads share it.
+ * every call; one buffer serves all calls of one stream, of both headers.
  *
  * Limits: M, N, K <= 2^20, groups, matrices <= 65535, pitches <= 2^21;
  * gemm_relu_experts: tokens <= 64, experts <= 1024, top <= 16, and less than 2^31

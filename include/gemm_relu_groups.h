@@ -37,8 +37,10 @@
  * overlapping any other argument; NULL where that is 0).  Its first
  * GEMM_RELU_GROUPS_COUNTER_BYTES must be zero before the first use; every call
  * that runs to completion leaves them zero, so one buffer serves all calls of
- * one stream, of any shape, and those of gemm_relu_splitk too.  Calls that may
- * overlap in time need different ones.
+ * one stream, of any shape, and those of gemm_relu_splitk too, also when threads
+ * share the stream: a call's launches follow each other, and a call that finds its
+ * workspace in another thread's launches waits (on the host) until they are enqueued.
+ * Calls that may overlap in time on the device need different ones.
  * The rest holds partial sums, the adapters' intermediates, the masked gradient
  * and, for large products of odd row lengths, copies of the operands on whole
  * cache lines (as large as the operands); nothing of it is kept between calls.

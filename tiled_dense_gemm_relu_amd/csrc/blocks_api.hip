@@ -3,13 +3,12 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cstdint>
-#include <thread>
 
 #include "../../include/gemm_relu_blocks.h"
 #include "blocks_table.hpp"
 #include "checks.hpp"
+#include "turns.hpp"
 
 namespace gemm_relu_hip {
 namespace {
@@ -185,24 +184,6 @@ int launch_pair(BlocksPair p, int format_a, int format_b, hipStream_t stream)
     return enqueue(kernels(format_a, format_b).pair, dim3((unsigned)(p.blocks[0] + p.blocks[1])), kBlockThreads[GEMM_RELU_BLOCKS_64],
                    args, stream);
 }
-
-// Holds while a call with a workspace launches: its kernels follow each other on their
-// stream also when threads share the stream, and with it the workspace.
-class Together {
-    static std::atomic_flag& busy()
-    {
-        static std::atomic_flag flag = ATOMIC_FLAG_INIT;
-        return flag;
-    }
-
-public:
-    Together()
-    {
-        while (busy().test_and_set(std::memory_order_acquire)) std::this_thread::yield();
-    }
-    Together(const Together&) = delete;
-    ~Together() { busy().clear(std::memory_order_release); }
-};
 
 // Places in the backward pass's workspace.
 struct BackwardSpace {
@@ -395,7 +376,7 @@ int gemm_relu_blocks_backward(const void* dC, const void* C, const void* XT, con
         if (want_w && rc == GEMM_RELU_OK) rc = zero_fill(dW, N * K, s);
         return rc;
     }
-    const Together together;
+    const WorkspaceTurn turn(workspace);
     const BackwardSpace space(M, N);
     char* const ws = static_cast<char*>(workspace);
     uint8_t *q = reinterpret_cast<uint8_t*>(ws + space.q), *qt = reinterpret_cast<uint8_t*>(ws + space.qt);
@@ -463,7 +444,7 @@ int gemm_relu_experts(const void* X, const void* W1, const float* scales1, const
     int cus = 0;
     if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    const Together together;
+    const WorkspaceTurn turn(workspace);
     const ExpertsSpace space(tokens, N, hidden, experts, top, b_layout);
     char* const ws = static_cast<char*>(workspace);
     const int store = bytes ? 2 + format : kn ? 1 : 0;

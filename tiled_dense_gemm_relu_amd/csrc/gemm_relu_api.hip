@@ -10,6 +10,7 @@
 #include "../../include/gemm_relu.h"
 #include "device.hpp"
 #include "kernel_table.hpp"
+#include "turns.hpp"
 
 namespace gemm_relu_hip {
 namespace {
@@ -492,6 +493,7 @@ int gemm_relu_splitk(const void* A, const void* B, void* C, int64_t M, int64_t N
             overlaps(workspace, need, B, 2 * K * N))
             return GEMM_RELU_ERR_ALIAS;
     }
+    const WorkspaceTurn turn(p.splits > 1 ? workspace : nullptr);
     return run(p, A, B, C, M, N, K, dtype, workspace, stream);
 }
 

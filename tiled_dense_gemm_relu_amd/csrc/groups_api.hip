@@ -10,6 +10,7 @@
 #include "device.hpp"
 #include "groups_table.hpp"
 #include "kernel_table.hpp"
+#include "turns.hpp"
 
 namespace gemm_relu_hip {
 namespace {
@@ -444,6 +445,7 @@ int gemm_relu_grouped(const void* A, const void* B, const int32_t* ends, void* C
     if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (K == 0) return zero_fill(C, M * N, s);
+    const WorkspaceTurn turn(need ? workspace : nullptr);
     RowsArgs a{static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), static_cast<uint16_t*>(C), ends,
                (int)M, (int)N, (int)K, (int)groups, relu, (int)K, (int)(b_layout == GEMM_RELU_B_NK ? K : N), 0};
     float* parts = need ? reinterpret_cast<float*>(static_cast<char*>(workspace) + GEMM_RELU_GROUPS_COUNTER_BYTES) : nullptr;
@@ -491,6 +493,7 @@ int gemm_relu_grouped_backward(const void* dC, const void* C, const void* A, con
         if (want_b && rc == GEMM_RELU_OK) rc = zero_fill(dB, gkn, s);
         return rc;
     }
+    const WorkspaceTurn turn(workspace);
     const uint16_t *d = static_cast<const uint16_t*>(dC), *c = relu ? static_cast<const uint16_t*>(C) : nullptr;
     const uint16_t *x = static_cast<const uint16_t*>(A), *b = static_cast<const uint16_t*>(B);
     // dA = D (M, N) times B^T: B as stored (K, N) is the transposed weight of this product
@@ -595,6 +598,7 @@ int gemm_relu_adapters(const void* X, const void* W, const void* U, const void* 
     if ((rc = check_device(&cus)) != GEMM_RELU_OK) return rc;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (K == 0) return zero_fill(C, M * N, s);
+    const WorkspaceTurn turn(workspace);
     const AdapterSpace space = adapter_space(M, N, K, rank, segments, b_layout);
     char* const ws = static_cast<char*>(workspace);
     uint16_t* t = reinterpret_cast<uint16_t*>(ws + space.t);
