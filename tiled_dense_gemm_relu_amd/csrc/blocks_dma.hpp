@@ -9,11 +9,13 @@
 // A stage is 128 k of the tile's rows of A and B, 128 bytes a row, swizzled and
 // read as the 16-bit kernels' (a_swizzle<128>), and the scales of those rows and
 // columns as floats: with scales by tiles every lane of the scales' DMA fetches
-// its column's tile, so both forms look alike in LDS.
+// its column's tile, so both forms look alike in LDS.  The wave that brought a piece
+// of them splits it there, for all, into mantissas and exponents (split_scale).
 //
-// The 256 tile at 8192^3 on normal data: 464-490 us, 2.25-2.37 PFLOP/s, where a library
-// product with one scale a matrix takes 410-419.  Without the additions it takes 428,
-// without DMA 392; loads by all waves with one barrier a step, and matrix instructions
+// The 256 tile at 8192^3 on normal data: 487-492 us, 2.24-2.26 PFLOP/s, where a library
+// product with one scale a matrix takes 410-419.  With the scales' exponents left to the
+// vector unit, which loses what lies outside a float's range, it takes 471-472 on the same
+// card; without the additions 428 then, without DMA 392; loads by all waves with one barrier a step, and matrix instructions
 // interleaved with additions, are what it got there by.  The smaller tiles have waves
 // that only load: 64 groups of 64 rows x 2048 x 4096 103 us, 5.5 TB/s.
 #pragma once
@@ -26,13 +28,41 @@ namespace gemm_relu_hip {
 
 typedef int int32x8_t __attribute__((ext_vector_type(8)));
 
-// 16 x 16 fp32 sums over 128 k: `w` of format FW, `x` of format FX.  A lane holds
-// 32 bytes of one row of each; which k those are only has to agree between them.
+// A scale as m 2^(e - 127), e from 0 to 254, the exponents of the matrix instruction.  m is
+// of magnitude 1 to 2, less for a subnormal scale, and what the scale is where that is
+// zero, infinite or NaN.  (Exact.)
+struct SplitScale {
+    float m;
+    uint32_t e;
+};
+__device__ __forceinline__ SplitScale split_scale(float s)
+{
+    const uint32_t e = min((__builtin_bit_cast(uint32_t, s) >> 23) & 0xffu, 254u);
+    return SplitScale{__builtin_ldexpf(s, 127 - (int)e), e};
+}
+
+// 16 x 16 fp32 sums over 128 k, times two powers of two: `w` of format FW, `x` of format
+// FX.  A lane holds 32 bytes of one row of each; which k those are only has to agree
+// between them.  The exponents of a lane's rows are byte `bw` of `ew` and byte `bx` of `ex`
+// (constants once loops are unrolled).  With them applied here the sums are multiplied by
+// two numbers between 1 and 2; the product of two scales could be subnormal, zero or
+// infinite where the result is not.  (Where it is none of these the bits are the same.
+// This costs 8192^3 3%, the 128 tile with scales of B by rows 14%; a second body of the loop
+// for steps whose scales need it, 30%, by its registers.)
 template <int FW, int FX>
-__device__ __forceinline__ floatx4 mfma_block(int32x8_t w, int32x8_t x)
+__device__ __forceinline__ floatx4 mfma_block(int32x8_t w, int32x8_t x, uint32_t ew, int bw, uint32_t ex, int bx)
 {
     const floatx4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, FW, FX, 0, 0, 0, 0);
+#define GEMM_RELU_BYTES(W, X) \
+    case 4 * W + X: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, FW, FX, W, (int)ew, X, (int)ex);
+    switch (4 * bw + bx) {
+        GEMM_RELU_BYTES(0, 0) GEMM_RELU_BYTES(0, 1) GEMM_RELU_BYTES(0, 2) GEMM_RELU_BYTES(0, 3)
+        GEMM_RELU_BYTES(1, 0) GEMM_RELU_BYTES(1, 1) GEMM_RELU_BYTES(1, 2) GEMM_RELU_BYTES(1, 3)
+        GEMM_RELU_BYTES(2, 0) GEMM_RELU_BYTES(2, 1) GEMM_RELU_BYTES(2, 2) GEMM_RELU_BYTES(2, 3)
+        GEMM_RELU_BYTES(3, 0) GEMM_RELU_BYTES(3, 1) GEMM_RELU_BYTES(3, 2) GEMM_RELU_BYTES(3, 3)
+    }
+#undef GEMM_RELU_BYTES
+    __builtin_unreachable();
 }
 
 // A lane's 32 bytes of a matrix operand.
@@ -50,9 +80,14 @@ struct BlockConfig {
     static constexpr int DMA_WAVES = PRODUCERS > 0 ? PRODUCERS : WAVES, THREADS = 64 * (WAVES + PRODUCERS);
     static constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N, FM = WTM / 16, FN = WTN / 16;
     static constexpr int A_STAGE = BM * BK, B_STAGE = BN * BK, B_REGION = STAGES * A_STAGE;
-    static constexpr int S_STAGE = (BM + BN) * 4, S_REGION = STAGES * (A_STAGE + B_STAGE);
+    // Every wave that loads brings a piece of 64 scales; those past the last one bring a piece
+    // again, to a place that nobody reads (pieces are rewritten once they have landed).
+    static constexpr int S_STAGE = DMA_WAVES * 256, S_REGION = STAGES * (A_STAGE + B_STAGE);
+    // The scales' exponents, a byte each: of a wave's rows 16 j + r for each r those of all j
+    // (FM bytes), after the rows the columns' likewise (FN bytes).
+    static constexpr int E_STAGE = BM + BN, E_REGION = S_REGION + STAGES * S_STAGE;
     // A wave's strip: 16 rows of its columns of C on their way to memory.
-    static constexpr int STRIP = 16 * WTN * 2, STRIPS = S_REGION + STAGES * S_STAGE;
+    static constexpr int STRIP = 16 * WTN * 2, STRIPS = E_REGION + STAGES * E_STAGE;
     static constexpr int LDS_BYTES = STRIPS + WAVES * STRIP;
     static constexpr int QA = A_STAGE / 1024 / DMA_WAVES, QB = B_STAGE / 1024 / DMA_WAVES, NQ = QA + QB + 1;
     static constexpr int SCALE_PIECES = (BM + BN) / 64;
@@ -232,7 +267,7 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
     // The scales' DMA: 64 floats of the tile's rows or columns a wave.
     const int piece = dwave & (Cfg::SCALE_PIECES - 1);
     const bool scales_of_a = piece < BM / 64;
-    const uint32_t scales_lds = lds_base + Cfg::S_REGION + 256u * (uint32_t)piece;
+    const uint32_t scales_lds = lds_base + Cfg::S_REGION + 256u * (uint32_t)dwave;
 
     // The load side; past the last unit everything is out of range and fetches nothing.
     int f_unit = 0, f_k = 0, f_left = 0, f_turn = 0, f_rows = 0, f_cols = 0;
@@ -325,6 +360,21 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
         for (int q = 0; q < QB; ++q) cut(smem + Cfg::B_REGION + slot * Cfg::B_STAGE + (dwave * QB + q) * 1024, pos[q & 1]);
     };
 
+    // This wave's piece of the scales, of a stage that has landed: mantissas in their place,
+    // and exponents.
+    const auto exponent_at = [](int i) {
+        constexpr int FM = Cfg::FM, FN = Cfg::FN;
+        const int r = i < BM ? i : i - BM, n = i < BM ? FM : FN;
+        return i - r + r / (16 * n) * (16 * n) + (r % 16) * n + r / 16 % n;
+    };
+    const int piece_at = 64 * piece + lane, exponent_to = exponent_at(piece_at);
+    auto read_piece = [&](int slot) { return *reinterpret_cast<const float*>(smem + Cfg::S_REGION + slot * Cfg::S_STAGE + 4 * piece_at); };
+    auto split_piece = [&](int slot, float s) {
+        const SplitScale v = split_scale(s);
+        *reinterpret_cast<float*>(smem + Cfg::S_REGION + slot * Cfg::S_STAGE + 4 * piece_at) = v.m;
+        smem[Cfg::E_REGION + slot * Cfg::E_STAGE + exponent_to] = (uint8_t)v.e;
+    };
+
     // Fragment reads (groups_dma.hpp): 16-byte chunks kb and 4 + kb of a row.
     const int kb = kgroup16(lane >> 4), g4 = lane >> 4, j16 = lane & 15;
     uint32_t a_off[2], b_off[2];
@@ -354,6 +404,7 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
             int k = f_turn, left = k_blocks;                 // of the stage that lands
             for (int g = 0; g < steps; ++g) {
                 wait_vmcnt<(S - 2) * NQ>();
+                if (dwave < Cfg::SCALE_PIECES) split_piece(g & (S - 1), read_piece(g & (S - 1)));
                 cut_off(g & (S - 1), a.k - k);
                 k = k + BK < a.k ? k + BK : 0;
                 lds_barrier();
@@ -399,6 +450,27 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
         const float s = sc[BM + wn * Cfg::WTN];
         return floatx4{s, s, s, s};
     };
+    // The exponents of this lane's rows and columns, packed.
+    struct Exponents {
+        uint32_t w, x[(FM + 3) / 4];
+    };
+    auto read_exponents = [&](int slot) {
+        const uint8_t* const e = smem + Cfg::E_REGION + slot * Cfg::E_STAGE;
+        const uint8_t *const ex = e + wm * Cfg::WTM + j16 * FM, *const ew = e + BM + wn * Cfg::WTN + j16 * FN;
+        Exponents v;
+        v.w = FN == 4 ? *reinterpret_cast<const uint32_t*>(ew) : *reinterpret_cast<const uint16_t*>(ew);
+        if constexpr (FM == 8) {
+            const u32x2 both = *reinterpret_cast<const u32x2*>(ex);
+            v.x[0] = both.x;
+            v.x[1] = both.y;
+        } else {
+            v.x[0] = FM == 4 ? *reinterpret_cast<const uint32_t*>(ex) : *reinterpret_cast<const uint16_t*>(ex);
+        }
+        return v;
+    };
+    auto product = [&](int32x8_t w, int32x8_t x, const Exponents& e, int i, int j) __attribute__((always_inline)) {
+        return mfma_block<FB, FA>(w, x, e.w, i, e.x[j / 4], j % 4);
+    };
     auto store = [&](const DmaUnit& c) {
         const int m_base = c.m0 + wm * Cfg::WTM, n_base = c.n0 + wn * Cfg::WTN;
         uint8_t* const strip = smem + Cfg::STRIPS + wave * Cfg::STRIP;
@@ -415,6 +487,7 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
             int32x8_t w[FN], x[FM];
             float scale_x[FM];
             floatx4 scale_w[NSW];
+            Exponents exponents;
         } f[2];
         auto read = [&](Fragments& to, int slot) __attribute__((always_inline)) {
             const float* sc = scales(slot);
@@ -426,6 +499,7 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
             for (int j = 0; j < FM; ++j) to.scale_x[j] = sc[wm * Cfg::WTM + 16 * j + j16];
 #pragma unroll
             for (int i = 0; i < NSW; ++i) to.scale_w[i] = read_scale_w(sc, i);
+            to.exponents = read_exponents(slot);
         };
         int c_unit = 0, left = k_blocks, g = 0;
         lds_barrier();
@@ -438,7 +512,7 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
             floatx4 t[LAG + 1];
 #pragma unroll
             for (int u = 0; u < FM * FN + LAG; ++u) {
-                if (u < FM * FN) t[u % (LAG + 1)] = mfma_block<FB, FA>(now.w[u % FN], now.x[u / FN]);
+                if (u < FM * FN) t[u % (LAG + 1)] = product(now.w[u % FN], now.x[u / FN], now.exponents, u % FN, u / FN);
                 if (u >= LAG) {
                     const int d = u - LAG, i = d % FN, j = d / FN;
                     add(i, j, t[d % (LAG + 1)], now.scale_x[j], now.scale_w[B_ROWS ? i : 0]);
@@ -463,6 +537,7 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
         float scale_x[FM];
         floatx4 scale_w[NSW];
         wait_vmcnt<(S - 1) * NQ>();
+        split_piece(0, read_piece(0));
         cut_off(0, a.k);
         lds_barrier();
         auto read_x = [&](int to, int slot, int j) __attribute__((always_inline)) {
@@ -478,6 +553,7 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
             for (int j = 0; j < FM; ++j) scale_x[j] = sc[wm * Cfg::WTM + 16 * j + j16];
 #pragma unroll
             for (int i = 0; i < NSW; ++i) scale_w[i] = read_scale_w(sc, i);
+            const Exponents exponents = read_exponents(slot);
             x[0] = x[2];
             read_x(1, slot, 1);
             floatx4 t[LAG + 1];
@@ -487,20 +563,25 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
                 add(i, j, t[u % (LAG + 1)], scale_x[j], scale_w[B_ROWS ? i : 0]);
             };
             int u = 0;
+            const int next = (slot + 1) & (S - 1);
+            float landed = 0.0f;
 #pragma unroll
             for (int j = 0; j < FM - 2; ++j) {
+                if (j == FM - 3) {            // the next stage's scales, on their way while this is multiplied
+                    wait_vmcnt<(S - 2) * NQ>();
+                    landed = read_piece(next);
+                }
                 read_x((j + 2) % 3, slot, j + 2);
 #pragma unroll
                 for (int i = 0; i < FN; ++i, ++u) {
-                    t[u % (LAG + 1)] = mfma_block<FB, FA>(w[i], x[j % 3]);
+                    t[u % (LAG + 1)] = product(w[i], x[j % 3], exponents, i, j);
                     if (u >= LAG) finish(u - LAG);
                 }
                 interleave<FN>();
                 __builtin_amdgcn_sched_barrier(0);
             }
-            const int next = (slot + 1) & (S - 1);
             const int k_next = k + BK < a.k ? k + BK : 0;
-            wait_vmcnt<(S - 2) * NQ>();
+            split_piece(next, landed);
             cut_off(next, a.k - k_next);
             lds_barrier();
             // buffers (FM - 2) % 3 and (FM - 1) % 3 are in use; the third is 2 for FM = 8
@@ -510,7 +591,7 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
             for (int i = 0; i < FN; ++i) {
 #pragma unroll
                 for (int j = FM - 2; j < FM; ++j, ++u) {
-                    t[u % (LAG + 1)] = mfma_block<FB, FA>(w[i], x[j % 3]);
+                    t[u % (LAG + 1)] = product(w[i], x[j % 3], exponents, i, j);
                     finish(u - LAG);
                 }
                 interleave<2>();

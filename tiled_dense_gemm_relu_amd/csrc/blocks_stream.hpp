@@ -111,8 +111,9 @@ __global__ __launch_bounds__(64 * kStreamWaves[KIND], 1) void blocks_stream(Bloc
             const uint8_t* const st = ring + slot * STAGE;
             const float *const sx = reinterpret_cast<const float*>(st + X_BYTES + W_BYTES), *const sw = sx + 64;
             u32x4 x[MB][2], w[NB][2];
-            float scale_x[MB];
+            SplitScale scale_x[MB];
             floatx4 scale_w[B_ROWS ? NB : 1];
+            uint32_t exponent_w[B_ROWS ? NB : 1];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -121,12 +122,19 @@ __global__ __launch_bounds__(64 * kStreamWaves[KIND], 1) void blocks_stream(Bloc
                 for (int i2 = 0; i2 < NB; ++i2) w[i2][h] = *reinterpret_cast<const u32x4*>(st + X_BYTES + off[h] + i2 * 2048);
             }
 #pragma unroll
-            for (int j = 0; j < MB; ++j) scale_x[j] = sx[16 * j + r16];
+            for (int j = 0; j < MB; ++j) scale_x[j] = split_scale(sx[16 * j + r16]);
             if constexpr (B_ROWS) {
 #pragma unroll
-                for (int i2 = 0; i2 < NB; ++i2) scale_w[i2] = *reinterpret_cast<const floatx4*>(sw + 16 * i2 + 4 * g);
+                for (int i2 = 0; i2 < NB; ++i2) {
+                    const floatx4 s4 = *reinterpret_cast<const floatx4*>(sw + 16 * i2 + 4 * g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) scale_w[i2][e] = split_scale(s4[e]).m;
+                    exponent_w[i2] = split_scale(sw[16 * i2 + r16]).e;
+                }
             } else {
-                scale_w[0][0] = sw[0];
+                const SplitScale s = split_scale(sw[0]);
+                scale_w[0][0] = s.m;
+                exponent_w[0] = s.e;
             }
             asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");     // the slot has been read
             fill(i + S, slot);
@@ -146,10 +154,11 @@ __global__ __launch_bounds__(64 * kStreamWaves[KIND], 1) void blocks_stream(Bloc
             for (int j = 0; j < MB; ++j)
 #pragma unroll
                 for (int i2 = 0; i2 < NB; ++i2) {
-                    const floatx4 t = mfma_block<FB, FA>(join(w[i2][0], w[i2][1]), join(x[j][0], x[j][1]));
+                    const floatx4 t = mfma_block<FB, FA>(join(w[i2][0], w[i2][1]), join(x[j][0], x[j][1]), exponent_w[B_ROWS ? i2 : 0], 0,
+                                                         scale_x[j].e, 0);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        acc[i2][j][e] = __builtin_fmaf(t[e], scale_x[j] * scale_w[B_ROWS ? i2 : 0][B_ROWS ? e : 0], acc[i2][j][e]);
+                        acc[i2][j][e] = __builtin_fmaf(t[e], scale_x[j].m * scale_w[B_ROWS ? i2 : 0][B_ROWS ? e : 0], acc[i2][j][e]);
                 }
         }
         wait_vmcnt<0>();                       // nothing lands in the rings after this
