@@ -234,32 +234,43 @@ __device__ inline void make_table(const RouteTable& t, const ExpertsArgs& a, int
     __syncthreads();
 }
 
-// 8 weights of a lane from 8 bytes, as 16-bit values (exact).
+// The scale of a block of 8-bit weights as two factors: a power of two that the widened
+// weights take, and the rest, which their sum does.  bf16 weights take all of the exponent
+// that they can hold: rows times stored values alone could be out of a float's range where
+// the products are not.  fp16 rows times stored values are at most 2^32 a product.
+struct WeightScale {
+    float power, rest;
+};
 template <int DT, int FORMAT>
-__device__ __forceinline__ u32x4 widen(uint32_t lo, uint32_t hi)
+__device__ __forceinline__ WeightScale weight_scale(float s)
+{
+    if constexpr (DT == kF16) return WeightScale{1.0f, s};
+    // 448 2^118 and 57344 2^111 are below 2^127; 2^-9 2^-117 and 2^-16 2^-110 are normal
+    constexpr int most = FORMAT == kE4M3 ? 118 : 111, least = FORMAT == kE4M3 ? -117 : -110;
+    const int e = min(max((int)((__builtin_bit_cast(uint32_t, s) >> 23) & 0xffu) - 127, least), most);
+    return WeightScale{__builtin_bit_cast(float, (uint32_t)(e + 127) << 23), __builtin_ldexpf(s, -e)};
+}
+
+// 8 weights of a lane from 8 bytes, times a power of two, as 16-bit values (exact).
+template <int DT, int FORMAT>
+__device__ __forceinline__ u32x4 widen(uint32_t lo, uint32_t hi, float power)
 {
     u32x4 r;
+#define GEMM_RELU_WIDEN(NAME) \
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_##NAME(lo, power, false)); \
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_##NAME(lo, power, true)); \
+    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_##NAME(hi, power, false)); \
+    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_##NAME(hi, power, true));
     if constexpr (DT == kF16 && FORMAT == kE4M3) {
-        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false));
-        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true));
-        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false));
-        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true));
+        GEMM_RELU_WIDEN(f16_fp8)
     } else if constexpr (DT == kF16) {
-        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(lo, 1.0f, false));
-        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(lo, 1.0f, true));
-        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(hi, 1.0f, false));
-        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(hi, 1.0f, true));
+        GEMM_RELU_WIDEN(f16_bf8)
     } else if constexpr (FORMAT == kE4M3) {
-        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false));
-        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true));
-        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false));
-        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
+        GEMM_RELU_WIDEN(bf16_fp8)
     } else {
-        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, false));
-        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, true));
-        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, false));
-        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, true));
+        GEMM_RELU_WIDEN(bf16_bf8)
     }
+#undef GEMM_RELU_WIDEN
     return r;
 }
 
@@ -300,6 +311,7 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
                                             int p0, int p1, int wave, int lane)
 {
     constexpr bool WIDE = STORE >= kStoreE4M3, ODD = !WIDE, ODD_X = !SPLIT_X;
+    constexpr int FORMAT = STORE == kStoreE4M3 ? kE4M3 : kE5M2;
     constexpr int KU = NB <= 2 && MB == 1 ? 2 : 1;     // pieces in flight
     const int r16 = lane & 15, g = lane >> 4;
     const int cols = min(16 * NB, out - n0);
@@ -363,7 +375,9 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
             if (p >= p1) break;
             const bool tail = k0 + kBlock > in;
             floatx4 sum[WIDE ? NB : 1][WIDE ? MB : 1];
+            WeightScale block_scale{1.0f, 1.0f};
             if constexpr (WIDE) {
+                block_scale = weight_scale<DT, FORMAT>(scale[q]);
 #pragma unroll
                 for (int i = 0; i < NB; ++i)
 #pragma unroll
@@ -410,7 +424,7 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
                             const u32x4 kept = keep_bytes(u32x4{b.x, b.y, 0u, 0u}, valid);
                             b = u32x2{kept[0], kept[1]};
                         }
-                        wv[i] = widen<DT, STORE == kStoreE4M3 ? kE4M3 : kE5M2>(b.x, b.y);
+                        wv[i] = widen<DT, FORMAT>(b.x, b.y, block_scale.power);
                     }
                 }
 #pragma unroll
@@ -439,7 +453,7 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
 #pragma unroll
                     for (int j = 0; j < MB; ++j)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(scale[q], sum[i][j][e], acc[i][j][e]);
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(block_scale.rest, sum[i][j][e], acc[i][j][e]);
             }
         }
     }
@@ -457,6 +471,7 @@ __device__ __forceinline__ void expert_stream(floatx4 (&acc)[NB][MB], const uint
                                               int out, int p0, int p1, uint8_t* ring, int turn, int wave, int lane)
 {
     constexpr bool WIDE = STORE >= kStoreE4M3, KN = STORE == kStoreKN;
+    constexpr int FORMAT = STORE == kStoreE4M3 ? kE4M3 : kE5M2;
     constexpr int K = WIDE ? 128 : 64, HALVES = K / 64, W_BYTES = NB * 2048, X_BYTES = MB * 2048;
     constexpr int STAGE = W_BYTES + HALVES * X_BYTES * (SPLIT_X ? 2 : 1), NQ = STAGE / 1024;
     static_assert(!KN || NB == 4, "rows of 128 bytes");
@@ -533,6 +548,12 @@ __device__ __forceinline__ void expert_stream(floatx4 (&acc)[NB][MB], const uint
             const int i = i0 + slot;
             if (i >= mine) break;
             wait_vmcnt<(S - 1) * NQ>();
+            WeightScale block_scale{1.0f, 1.0f};
+            if constexpr (WIDE) {
+                // (taken from its load here: a wait for it behind the next fill would wait for that too)
+                block_scale = weight_scale<DT, FORMAT>(scale[slot]);
+                asm volatile("" : "+v"(block_scale.power), "+v"(block_scale.rest));
+            }
             const uint8_t *const st = ring + slot * STAGE, *const sx = st + W_BYTES;
             constexpr int STEPS = WIDE ? 4 : 2;                  // of 32 k
             u32x4 wf[NB][2], xf[MB][STEPS], lf[SPLIT_X ? MB : 1][SPLIT_X ? STEPS : 1];
@@ -559,7 +580,6 @@ __device__ __forceinline__ void expert_stream(floatx4 (&acc)[NB][MB], const uint
                     xf[j][s] = *reinterpret_cast<const u32x4*>(q);
                     if constexpr (SPLIT_X) lf[j][s] = *reinterpret_cast<const u32x4*>(q + HALVES * X_BYTES);
                 }
-            const float block_scale = WIDE ? scale[slot] : 1.0f;
             asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");     // the slot has been read
             fill(i + S, slot, scale[slot]);
             const int k0 = piece_at(i) * K;
@@ -590,7 +610,7 @@ __device__ __forceinline__ void expert_stream(floatx4 (&acc)[NB][MB], const uint
                             const u32x4 kept = keep_bytes(u32x4{v.x, v.y, 0u, 0u}, valid);
                             v = u32x2{kept[0], kept[1]};
                         }
-                        wv = widen<DT, STORE == kStoreE4M3 ? kE4M3 : kE5M2>(v.x, v.y);
+                        wv = widen<DT, FORMAT>(v.x, v.y, block_scale.power);
                     } else {
                         wv = wf[b][s];
                         if (tail && !KN) wv = keep_first(wv, valid);    // ((K, N) rows past the last are zeros)
@@ -609,7 +629,7 @@ __device__ __forceinline__ void expert_stream(floatx4 (&acc)[NB][MB], const uint
 #pragma unroll
                     for (int j = 0; j < MB; ++j)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[b][j][e] = __builtin_fmaf(block_scale, sum[b][j][e], acc[b][j][e]);
+                        for (int e = 0; e < 4; ++e) acc[b][j][e] = __builtin_fmaf(block_scale.rest, sum[b][j][e], acc[b][j][e]);
             }
         }
     }
