@@ -38,13 +38,15 @@ __device__ __forceinline__ Scale make_scale(uint32_t amax, int power_of_two)
 // x / s, correctly rounded: the product with the rounded reciprocal is off by at
 // most two units in the last place, and one step with its exact remainder
 // corrects that.  (x has 8 or 11 bits, and so has the magnitude that s was made
-// of: every pair of them has been compared with the exact quotient.)  With CHECK
-// infinities and NaN are left as they are (their remainder is not a number).
+// of: every pair of them has been compared with the exact quotient.)  The remainder is
+// taken with its sign turned: that of a zero is then +0, which leaves a quotient of -0
+// as it is.  With CHECK infinities and NaN are left as they are (their remainder is not
+// a number).
 template <bool CHECK>
 __device__ __forceinline__ float divide(float x, Scale c)
 {
     const float t = x * c.inverse;
-    const float q = __builtin_fmaf(__builtin_fmaf(-t, c.s, x), c.inverse, t);
+    const float q = __builtin_fmaf(-__builtin_fmaf(t, c.s, -x), c.inverse, t);
     return !CHECK || __builtin_fabsf(x) < __builtin_inff() ? q : x;
 }
 
