@@ -145,6 +145,15 @@ def _check_8bit(name, t, dim, dev=None):
     return code, pitch
 
 
+def _check_scales(name, t, dim, dev, shape):
+    """float32 scales of this shape, which have no gradient any more than the values they belong to."""
+    import torch
+    _check_tensor(name, t, dim, dev, torch.float32)
+    _check_shape(name, t, shape)
+    if t.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError(f"gemm_relu: {name} requires a gradient, but 8-bit operands have none; detach it")
+
+
 def _blocks(n: int) -> int:
     return (n + BLOCK - 1) // BLOCK
 
@@ -249,7 +258,8 @@ def gemm_relu_blocks(a, a_scales, b, b_scales, ends=None, out=None, out_dtype=No
     (groups, N, K), its scales have groups in front, and row m of group g (rows ends[g-1] .. ends[g]-1) is
     multiplied with b[g]; rows past the last end get zeros.  ``relu=False`` leaves the ReLU out.  C (M, N) is
     ``out`` if given, else a new tensor of ``out_dtype`` (bfloat16 by default).  ``config``: a
-    kernel (CONFIG_*), by default the library's choice.
+    kernel (CONFIG_*), by default the library's choice.  8-bit values and their scales have no gradient;
+    one that requires it is refused.
     """
     import torch
     if stream is None and out is None and (out_dtype is None or out_dtype is torch.bfloat16 or out_dtype is torch.float16):
@@ -265,10 +275,9 @@ def gemm_relu_blocks(a, a_scales, b, b_scales, ends=None, out=None, out_dtype=No
     if b.shape[-1] != K:
         raise ValueError(f"gemm_relu: inner dimensions differ: a {tuple(a.shape)}, b {tuple(b.shape)}")
     kb = _blocks(K)
-    _check_tensor("a_scales", a_scales, 2, dev, torch.float32)
-    _check_shape("a_scales", a_scales, (kb, M))
-    _check_tensor("b_scales", b_scales, 3 if grouped else 2, dev, torch.float32)
-    _check_shape("b_scales", b_scales, ((groups,) if grouped else ()) + ((kb, N) if b_rows else (_blocks(N), kb)))
+    _check_scales("a_scales", a_scales, 2, dev, (kb, M))
+    _check_scales("b_scales", b_scales, 3 if grouped else 2, dev,
+                  ((groups,) if grouped else ()) + ((kb, N) if b_rows else (_blocks(N), kb)))
     if grouped:
         _check_tensor("ends", ends, 1, dev, torch.int32)
         _check_shape("ends", ends, (groups,))
@@ -310,14 +319,12 @@ def gemm_relu_blocks_backward(dc, c, xt, xt_scales, wt, wt_scales, relu: bool = 
         fx, ldxt = _check_8bit("xt", xt, 2, dev)
         K = xt.shape[0]
         _check_shape("xt", xt, (K, M))
-        _check_tensor("xt_scales", xt_scales, 2, dev, torch.float32)
-        _check_shape("xt_scales", xt_scales, (_blocks(M), K))
+        _check_scales("xt_scales", xt_scales, 2, dev, (_blocks(M), K))
     if need_dx:
         fw, ldwt = _check_8bit("wt", wt, 2, dev)
         K = K if need_dw else wt.shape[0]
         _check_shape("wt", wt, (K, N))
-        _check_tensor("wt_scales", wt_scales, 2, dev, torch.float32)
-        _check_shape("wt_scales", wt_scales, (_blocks(K), _blocks(N)))
+        _check_scales("wt_scales", wt_scales, 2, dev, (_blocks(K), _blocks(N)))
 
     def output(name, t, shape):
         if t is None:
@@ -399,7 +406,7 @@ def _no_gradient():
 
     class Experts(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, x, w1, w2, logits, weights, call):
+        def forward(ctx, x, w1, w2, logits, weights, w1_scales, w2_scales, call):
             return call()
 
         @staticmethod
@@ -476,7 +483,8 @@ def gemm_relu_experts(x, w1, w2, logits=None, top=None, ids=None, weights=None, 
         _check_shape("ids", ids, (tokens, top))
         _check_tensor("weights", weights, 2, dev, torch.float32)
         _check_shape("weights", weights, (tokens, top))
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, w1, w2, logits, weights)):
+    inputs = x, w1, w2, logits, weights, w1_scales, w2_scales
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
         if out is not None:
             raise RuntimeError("gemm_relu: out= has no gradient, but an input requires one: leave out= away, or call "
                                "under torch.no_grad()")
@@ -489,7 +497,7 @@ def gemm_relu_experts(x, w1, w2, logits=None, top=None, ids=None, weights=None, 
             chosen.extend(rest)
             return y
         with _on(stream, dev):
-            y = _no_gradient().apply(x, w1, w2, logits, weights, call)
+            y = _no_gradient().apply(*inputs, call)
         return (y, *chosen)
     need = experts_workspace_bytes(tokens, N, hidden, experts, top, b_layout)
     if routed:

@@ -59,6 +59,9 @@ int64_t pitch_of(const at::Tensor* t, int64_t dim, int device, int& format)
     return t->storage_offset() + (count - 1) * pitch + whole <= (int64_t)t->storage().nbytes() ? pitch : 0;
 }
 
+// Whether autograd asks for a gradient of one of these scales, which have none.
+bool wanted(const at::Tensor* s, const at::Tensor* t) { return at::GradMode::is_enabled() && (s->requires_grad() || t->requires_grad()); }
+
 bool sizes_are(const at::Tensor* t, at::IntArrayRef want) { return t->sizes() == want; }
 
 // An argument of another kind than the ordinary call's.
@@ -149,6 +152,7 @@ PyObject* multiply(PyObject*, PyObject* const* args, Py_ssize_t n)
     if (!plain(sa, 2, at::kFloat, device) || !sizes_are(sa, {kb, M}) || !plain(sb, grouped ? 3 : 2, at::kFloat, device)) Py_RETURN_NONE;
     const int64_t s0 = b_rows ? kb : blocks_of(N), s1 = b_rows ? N : kb;
     if (grouped ? !sizes_are(sb, {groups, s0, s1}) : !sizes_are(sb, {s0, s1})) Py_RETURN_NONE;
+    if (wanted(sa, sb)) Py_RETURN_NONE;
     if (grouped && !(plain(ends, 1, at::kInt, device) && ends->size(0) == groups)) Py_RETURN_NONE;
     at::Tensor c = at::empty({M, N}, sa->options().dtype(bf16 ? at::kBFloat16 : at::kHalf).requires_grad(false));
     void* const stream = c10::hip::getCurrentHIPStream(device).stream();
@@ -212,7 +216,7 @@ PyObject* backward(PyObject*, PyObject* const* args, Py_ssize_t n)
     if (!ldx || !ldw) Py_RETURN_NONE;
     const int64_t K = xt->size(0);
     if (xt->size(1) != M || !sizes_are(wt, {K, N}) || !plain(sx, 2, at::kFloat, device) || !sizes_are(sx, {blocks_of(M), K}) ||
-        !plain(sw, 2, at::kFloat, device) || !sizes_are(sw, {blocks_of(K), blocks_of(N)}))
+        !plain(sw, 2, at::kFloat, device) || !sizes_are(sw, {blocks_of(K), blocks_of(N)}) || wanted(sx, sw))
         Py_RETURN_NONE;
     void* const stream = c10::hip::getCurrentHIPStream(device).stream();
     const Space space(args[8], device, stream, backward_space(M, N, K));
@@ -259,7 +263,7 @@ PyObject* experts(PyObject*, PyObject* const* args, Py_ssize_t n)
     if (!sizes_are(logits, {tokens, E})) Py_RETURN_NONE;
     if (eight) {
         if (!plain(s1, 3, at::kFloat, device) || !sizes_are(s1, {E, blocks_of(H), blocks_of(K)}) || !plain(s2, 3, at::kFloat, device) ||
-            !sizes_are(s2, {E, blocks_of(N), blocks_of(H)}))
+            !sizes_are(s2, {E, blocks_of(N), blocks_of(H)}) || wanted(s1, s2))
             Py_RETURN_NONE;
     } else if (args[5] != Py_None || args[6] != Py_None) {
         Py_RETURN_NONE;
