@@ -1,4 +1,4 @@
-"""What has no derivative says so: fp32 scales of 8-bit operands."""
+"""What has no derivative says so: fp32 scales of 8-bit operands, and tangents of forward mode."""
 import pytest
 import torch
 
@@ -61,3 +61,34 @@ def test_scales_of_an_expert_layer(route):
         with torch.no_grad():
             assert not call()[0].requires_grad
         s.requires_grad_(False)
+
+
+def test_forward_mode(route):
+    from torch.autograd import forward_ad
+    x, w = randn((32, 48), 1).to(DEV), randn((16, 48), 2).to(DEV)
+    w1, w2, logits = randn((2, 16, 48), 3).to(DEV), randn((2, 48, 16), 4).to(DEV), torch.zeros((32, 2), device=DEV)
+    ends = torch.tensor([10, 32], dtype=torch.int32, device=DEV)
+    q, s = gr.quantize_blocks(x)
+    qw, sw = gr.quantize_blocks(w, tiles=True)
+    scales, ids, one = torch.ones(1, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV), randn((1, 48, 8), 5).to(DEV)
+    square, v = randn((48, 24), 6).to(DEV), randn((1, 8, 24), 7).to(DEV)
+    calls = {
+        "linear_blocks, x": (x, lambda t: gr.linear_blocks(t, w)), "linear_blocks, w": (w, lambda t: gr.linear_blocks(x, t)),
+        "experts, x": (x, lambda t: gr.gemm_relu_experts(t, w1, w2, logits, 1)),
+        "experts, w1": (w1, lambda t: gr.gemm_relu_experts(x, t, w2, logits, 1)),
+        "experts, logits": (logits, lambda t: gr.gemm_relu_experts(x, w1, w2, t, 1)),
+        "product, a_scales": (s, lambda t: gr.gemm_relu_blocks(q, t, qw, sw)),
+        "product, b_scales": (sw, lambda t: gr.gemm_relu_blocks(q, s, qw, t)),
+        "grouped, a": (x, lambda t: gr.gemm_relu_grouped(t, w2.transpose(1, 2).contiguous(), ends, b_layout=gr.B_NK)),
+        "adapters, x": (x, lambda t: gr.gemm_relu_adapters(t, square, one, v, scales, ends, ids)),
+    }
+    for name, (t, call) in calls.items():
+        call(t)                                          # takes the stream's workspace
+        for enabled in (True, False):
+            with torch.set_grad_enabled(enabled), forward_ad.dual_level():
+                dual = forward_ad.make_dual(t, torch.ones_like(t))
+                with pytest.raises(NotImplementedError, match="forward-mode"):
+                    call(dual)
+                call(t)                                  # others pass while a level is open
+    with torch.no_grad():
+        assert gr.linear_blocks(x, w).isfinite().all()

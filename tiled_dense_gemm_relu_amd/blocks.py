@@ -19,7 +19,8 @@ import threading
 
 from . import binding
 from .binding import B_KN, B_NK, _check, _stream_handle
-from .groups import _call, _check_layout, _check_shape, _check_tensor, _first, _new, _on, _spaces, _workspace
+from .groups import (_call, _check_layout, _check_shape, _check_tensor, _first, _new, _on, _refuse_tangents, _spaces,
+                     _workspace)
 
 BLOCK = 128                # GEMM_RELU_BLOCK
 
@@ -152,6 +153,7 @@ def _check_scales(name, t, dim, dev, shape):
     _check_shape(name, t, shape)
     if t.requires_grad and torch.is_grad_enabled():
         raise RuntimeError(f"gemm_relu: {name} requires a gradient, but 8-bit operands have none; detach it")
+    _refuse_tangents(name, t)
 
 
 def _blocks(n: int) -> int:
@@ -382,6 +384,7 @@ def linear_blocks(x, w, relu: bool = True, dtype=None, grad_dtype=None, stream=N
     by rows to ``grad_dtype`` (float8_e5m2); gradients pass the rounding of x and w unchanged.  What backward
     needs of x and w is kept in 8 bits.  Forward and backward run on ``stream``, or the current one.  A backward
     pass can be captured; as with torch's own operators, no eager graph of the same leaves may be alive meanwhile.
+    Tangents of forward mode are refused.
     """
     _, dev = _first("x", x)
     _check_tensor("x", x, 2, dev, x.dtype)
@@ -393,6 +396,7 @@ def linear_blocks(x, w, relu: bool = True, dtype=None, grad_dtype=None, stream=N
     grad_dtype = torch.float8_e5m2 if grad_dtype is None else grad_dtype
     _format_code("dtype", dtype)
     _format_code("grad_dtype", grad_dtype)
+    _refuse_tangents("linear_blocks", x, w)
     with _on(stream, dev):
         if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
             return _linear().apply(x, w, bool(relu), dtype, grad_dtype)
@@ -484,6 +488,7 @@ def gemm_relu_experts(x, w1, w2, logits=None, top=None, ids=None, weights=None, 
         _check_tensor("weights", weights, 2, dev, torch.float32)
         _check_shape("weights", weights, (tokens, top))
     inputs = x, w1, w2, logits, weights, w1_scales, w2_scales
+    _refuse_tangents("gemm_relu_experts", *inputs)
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
         if out is not None:
             raise RuntimeError("gemm_relu: out= has no gradient, but an input requires one: leave out= away, or call "

@@ -59,8 +59,13 @@ int64_t pitch_of(const at::Tensor* t, int64_t dim, int device, int& format)
     return t->storage_offset() + (count - 1) * pitch + whole <= (int64_t)t->storage().nbytes() ? pitch : 0;
 }
 
-// Whether autograd asks for a gradient of one of these scales, which have none.
-bool wanted(const at::Tensor* s, const at::Tensor* t) { return at::GradMode::is_enabled() && (s->requires_grad() || t->requires_grad()); }
+// Whether autograd asks for a derivative with respect to one of these.
+bool wanted(std::initializer_list<const at::Tensor*> tensors)
+{
+    for (const at::Tensor* t : tensors)
+        if (t && ((at::GradMode::is_enabled() && t->requires_grad()) || t->_fw_grad(0).defined())) return true;
+    return false;
+}
 
 bool sizes_are(const at::Tensor* t, at::IntArrayRef want) { return t->sizes() == want; }
 
@@ -152,7 +157,7 @@ PyObject* multiply(PyObject*, PyObject* const* args, Py_ssize_t n)
     if (!plain(sa, 2, at::kFloat, device) || !sizes_are(sa, {kb, M}) || !plain(sb, grouped ? 3 : 2, at::kFloat, device)) Py_RETURN_NONE;
     const int64_t s0 = b_rows ? kb : blocks_of(N), s1 = b_rows ? N : kb;
     if (grouped ? !sizes_are(sb, {groups, s0, s1}) : !sizes_are(sb, {s0, s1})) Py_RETURN_NONE;
-    if (wanted(sa, sb)) Py_RETURN_NONE;
+    if (wanted({sa, sb})) Py_RETURN_NONE;
     if (grouped && !(plain(ends, 1, at::kInt, device) && ends->size(0) == groups)) Py_RETURN_NONE;
     at::Tensor c = at::empty({M, N}, sa->options().dtype(bf16 ? at::kBFloat16 : at::kHalf).requires_grad(false));
     void* const stream = c10::hip::getCurrentHIPStream(device).stream();
@@ -216,7 +221,7 @@ PyObject* backward(PyObject*, PyObject* const* args, Py_ssize_t n)
     if (!ldx || !ldw) Py_RETURN_NONE;
     const int64_t K = xt->size(0);
     if (xt->size(1) != M || !sizes_are(wt, {K, N}) || !plain(sx, 2, at::kFloat, device) || !sizes_are(sx, {blocks_of(M), K}) ||
-        !plain(sw, 2, at::kFloat, device) || !sizes_are(sw, {blocks_of(K), blocks_of(N)}) || wanted(sx, sw))
+        !plain(sw, 2, at::kFloat, device) || !sizes_are(sw, {blocks_of(K), blocks_of(N)}) || wanted({sx, sw}))
         Py_RETURN_NONE;
     void* const stream = c10::hip::getCurrentHIPStream(device).stream();
     const Space space(args[8], device, stream, backward_space(M, N, K));
@@ -246,8 +251,7 @@ PyObject* experts(PyObject*, PyObject* const* args, Py_ssize_t n)
     if (!x || !w1 || !w2 || !logits || !x->is_cuda() || (layout != GEMM_RELU_B_KN && layout != GEMM_RELU_B_NK)) Py_RETURN_NONE;
     const int device = c10::hip::current_device(), code = dtype_code(x->scalar_type());
     if (code < 0 || !plain(x, 2, x->scalar_type(), device) || !plain(logits, 2, at::kFloat, device) || x->numel() == 0) Py_RETURN_NONE;
-    if (at::GradMode::is_enabled() && (x->requires_grad() || w1->requires_grad() || w2->requires_grad() || logits->requires_grad()))
-        Py_RETURN_NONE;
+    if (wanted({x, w1, w2, logits, s1, s2})) Py_RETURN_NONE;
     const bool eight = w1->scalar_type() == at::kFloat8_e4m3fn || w1->scalar_type() == at::kFloat8_e5m2, nk = layout == GEMM_RELU_B_NK;
     int f1 = -1, f2 = -1;
     int64_t ld1 = 0, ld2 = 0;
@@ -263,7 +267,7 @@ PyObject* experts(PyObject*, PyObject* const* args, Py_ssize_t n)
     if (!sizes_are(logits, {tokens, E})) Py_RETURN_NONE;
     if (eight) {
         if (!plain(s1, 3, at::kFloat, device) || !sizes_are(s1, {E, blocks_of(H), blocks_of(K)}) || !plain(s2, 3, at::kFloat, device) ||
-            !sizes_are(s2, {E, blocks_of(N), blocks_of(H)}) || wanted(s1, s2))
+            !sizes_are(s2, {E, blocks_of(N), blocks_of(H)}))
             Py_RETURN_NONE;
     } else if (args[5] != Py_None || args[6] != Py_None) {
         Py_RETURN_NONE;

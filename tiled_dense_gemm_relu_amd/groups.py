@@ -118,6 +118,16 @@ def _check_layout(b_layout):
         raise ValueError(f"gemm_relu: b_layout must be B_KN or B_NK, got {b_layout}")
 
 
+def _refuse_tangents(what, *tensors):
+    """Forward-mode derivatives of ``what``'s inputs are refused: there is none to pass on."""
+    from torch.autograd import forward_ad
+    if forward_ad._current_level < 0:         # no dual tensors without a level
+        return
+    import torch
+    if any(isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError(f"gemm_relu: {what} has no forward-mode derivative; pass the primal")
+
+
 def _new(shape, like, stream):
     """An output for work on ``stream``: allocated for that stream, so that its memory is not one
     that still belongs to other work there."""
@@ -262,6 +272,7 @@ def gemm_relu_grouped(a, b, ends, out=None, b_layout: int = B_KN, relu: bool = T
         raise ValueError(f"gemm_relu: inner dimensions differ: a {tuple(a.shape)}, b {tuple(b.shape)}")
     if ends.shape[0] != groups:
         raise ValueError(f"gemm_relu: ends must have one entry for each of {groups} groups, got {ends.shape[0]}")
+    _refuse_tangents("gemm_relu_grouped", a, b)
     if (a.requires_grad or b.requires_grad) and torch.is_grad_enabled():
         return _differentiable(_functions()[0], dev, out, stream, a, b, ends, b_layout, relu, config, workspace)
     if out is None:
@@ -363,6 +374,7 @@ def gemm_relu_adapters(x, w, u, v, scales, ends, ids, out=None, b_layout: int = 
     _check_shape("scales", scales, (adapters,))
     segments = ends.shape[0]
     _check_shape("ids", ids, (segments,))
+    _refuse_tangents("gemm_relu_adapters", x, w, u, v, scales)
     if (x.requires_grad or w.requires_grad or u.requires_grad or v.requires_grad
             or scales.requires_grad) and torch.is_grad_enabled():
         return _differentiable(_functions()[1], dev, out, stream, x, w, u, v, scales, ends, ids, b_layout, relu, config,
