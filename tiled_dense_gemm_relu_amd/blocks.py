@@ -5,7 +5,8 @@
 node of autograd's graph.  ``gemm_relu_experts`` is a whole expert layer for a few tokens, with 16-bit or such
 8-bit weights.
 As in binding.py this is argument marshalling only, with no fallback.  The marshalling of ordinary calls is compiled
-(csrc/blocks_calls.cpp), for what takes the GPU less time than Python; it leaves all others to this file.
+(csrc/blocks_calls.cpp), for what takes the GPU less time than Python; it leaves all others to this file.  Where it
+was not built for the torch that runs, this file marshals every call to the same library.
 
 A quantized matrix is a ``torch.float8_e4m3fn`` or ``torch.float8_e5m2`` tensor whose rows start at multiples
 of 16 bytes (``stride(-2) % 16 == 0``), with float32 scales: by rows ``(blocks, rows)``, one for 128 elements
@@ -60,16 +61,34 @@ def _library():
 _calls = None
 
 
+class _NotCompiled:
+    """Leaves every call to Python."""
+
+    @staticmethod
+    def quantize(*args):
+        return None
+
+    multiply = backward = experts = quantize
+
+
 def _compiled():
-    """The compiled calls, with the entry points of the loaded library."""
+    """The compiled calls, with the entry points of the loaded library; where they were not built, or for another
+    torch, a stand-in that leaves all calls to Python (some 5 to 9 us more a call on the host)."""
     global _calls
     if _calls is None:
-        import torch  # noqa: F401  (its libraries are the extension's)
+        import torch
         lib = _library()
         try:
             from . import _blocks_calls as calls
+            built_for = getattr(calls, "torch_version", "unknown")
+            if built_for != torch.__version__:
+                raise ImportError(f"built for torch {built_for}, this is {torch.__version__}")
         except ImportError as e:
-            raise RuntimeError("gemm_relu: _blocks_calls.so is missing or does not fit this torch: build the package again") from e
+            import warnings
+            warnings.warn(f"gemm_relu: the compiled marshalling of 8-bit calls is not used ({e}); build the package again "
+                          "for shorter calls", RuntimeWarning, stacklevel=3)
+            _calls = _NotCompiled()
+            return _calls
         calls.use(*(ctypes.cast(f, ctypes.c_void_p).value
                     for f in (lib.gemm_relu_quantize_blocks, lib.gemm_relu_blocks, lib.gemm_relu_blocks_backward,
                               lib.gemm_relu_blocks_backward_workspace, lib.gemm_relu_experts, lib.gemm_relu_experts_workspace)))

@@ -2,7 +2,9 @@
 
 Each .hip translation unit is compiled to an object in parallel, then linked
 into ``tiled_dense_gemm_relu_amd/libgemm_relu.so`` (in-tree, so it travels with
-the source tree), and ``_blocks_calls.so``, compiled argument marshalling, beside it.  Run ``python -m tiled_dense_gemm_relu_amd.build``.
+the source tree).  ``_blocks_calls.so`` beside it, compiled argument marshalling of
+the 8-bit calls, needs g++ and the headers of Python and torch; without them the
+library is built all the same.  Run ``python -m tiled_dense_gemm_relu_amd.build``.
 """
 from __future__ import annotations
 
@@ -110,7 +112,8 @@ def build_calls() -> str:
     tmp = CALLS_PATH + f".tmp{os.getpid()}"
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{home}/include",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DGEMM_RELU_TORCH_VERSION="{torch.__version__}"', f"-I{home}/include",
            f"-I{home}/include/torch/csrc/api/include", f"-I{sysconfig.get_paths()['include']}", f"-I{rocm}/include",
            os.path.join(CSRC, "blocks_calls.cpp"), f"-L{home}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip",
            "-o", tmp]
@@ -121,14 +124,24 @@ def build_calls() -> str:
     return CALLS_PATH
 
 
+def _try_calls():
+    """build_calls, or why it could not be done; then none is left of an earlier build either."""
+    try:
+        build_calls()
+    except (ImportError, OSError, RuntimeError) as e:
+        if os.path.exists(CALLS_PATH):
+            os.remove(CALLS_PATH)
+        return e
+    return None
+
+
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     """Compile every HIP source and link the shared library.  Returns its path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     extra = list(extra or [])
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as ex:
-        calls = ex.submit(build_calls)
+        calls = ex.submit(_try_calls)
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
-        calls.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -147,6 +160,9 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
         if res.returncode != 0:
             raise RuntimeError(f"hipcc failed for {src}:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
         os.replace(tmp, path)
+    if calls.result() is not None:
+        import warnings
+        warnings.warn(f"{os.path.basename(CALLS_PATH)} was not built, 8-bit calls are marshalled in Python: {calls.result()}", RuntimeWarning)
     if verbose:
         print(f"built {LIB_PATH} and " + ", ".join(path for _, path in programs))
     return LIB_PATH

@@ -316,4 +316,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_blocks_calls", nullptr, -1, metho
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__blocks_calls() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__blocks_calls()
+{
+    PyObject* const m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", GEMM_RELU_TORCH_VERSION) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
