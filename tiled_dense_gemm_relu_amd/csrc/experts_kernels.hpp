@@ -3,15 +3,17 @@
 //
 // With a few tokens the time is that of reading the chosen experts' weights, once.
 // Every workgroup makes the routing table for itself (tokens are few), so nothing
-// waits for it, and takes units of one expert and 16 NB output columns; its waves
-// take pieces of k in turn and add their sums in LDS.  16 MB of an expert's rows
-// stream with the weights through a ring of each wave's own in LDS, by DMA, as in
-// blocks_stream.hpp (an expert with more rows takes several passes); operands whose
-// rows DMA cannot read (odd lengths, 2-byte alignment) go through registers.
+// waits for it, and takes units of 16 of an expert's rows (an expert with more has
+// several) and 16 NB output columns; its waves take pieces of k in turn and add their
+// sums in LDS.  The rows stream with the weights through a ring of each wave's own in
+// LDS, by DMA, as in blocks_stream.hpp; operands whose rows DMA cannot read (odd
+// lengths, 2-byte alignment) go through registers.
 //
 // The first launch leaves weight * ReLU(sum) of every choice as a sum of two 16-bit
-// values, so that the second one's matrix instructions lose nothing of it.  The
-// second launch's units write a choice's products as fp32; the last unit of a column
+// values, for the second one's matrix instructions: off by at most 2^-16 of the value
+// with bf16, with fp16 by 2^-22 or 2^-25, and infinite past 65504 (one value would be off
+// by 2^-9 and 2^-12; a third takes half as much again of the rings' room for rows).
+// The second launch's units write a choice's products as fp32; the last unit of a column
 // block to end adds each token's in the order of its choices.
 //
 // 24 tokens, 4 of 64 experts, 8-bit 2048 x 4096: 139 us, 6 TB/s of the chosen experts'
@@ -302,17 +304,17 @@ struct PieceWeights<kStoreE4M3, ODD, NB> {
 template <bool ODD, int NB>
 struct PieceWeights<kStoreE5M2, ODD, NB> : PieceWeights<kStoreE4M3, ODD, NB> {};
 
-// The sums over pieces p0 + wave, p0 + wave + 8, .. of a unit's NB x MB blocks.
-//  Rows: lane's row of block j is x_off[j] bytes into rx (kOobOffset: none); with
-//  SPLIT_X also its low parts, x_low bytes on.
-template <int DT, int STORE, bool SPLIT_X, int NB, int MB, int WAVES>
-__device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsrc& rx, const uint32_t (&x_off)[MB], uint32_t x_low,
+// The sums over pieces p0 + wave, p0 + wave + WAVES, .. of a unit's NB blocks of columns.
+//  Rows: lane's row is x_off bytes into rx (kOobOffset: none); with SPLIT_X also its low
+//  parts, x_low bytes on.
+template <int DT, int STORE, bool SPLIT_X, int NB, int WAVES>
+__device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB], const AnyRsrc& rx, uint32_t x_off, uint32_t x_low,
                                             const uint8_t* w, const float* scales, int64_t ld, int n0, int in, int out,
                                             int p0, int p1, int wave, int lane)
 {
     constexpr bool WIDE = STORE >= kStoreE4M3, ODD = !WIDE, ODD_X = !SPLIT_X;
     constexpr int FORMAT = STORE == kStoreE4M3 ? kE4M3 : kE5M2;
-    constexpr int KU = NB <= 2 && MB == 1 ? 2 : 1;     // pieces in flight
+    constexpr int KU = NB <= 2 ? 2 : 1;                // pieces in flight
     const int r16 = lane & 15, g = lane >> 4;
     const int cols = min(16 * NB, out - n0);
     // NK and 8-bit: rows n0 .. of the expert's weights
@@ -321,17 +323,16 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
     if constexpr (WIDE) rw.rsrc = make_rsrc(w + (size_t)n0 * (size_t)ld, (uint32_t)cols * (uint32_t)ld);
     // 8 k of step s of piece p: 8-bit weights have 16 consecutive ones a lane.
     auto first_k = [&](int p, int s) { return p * kBlock + (WIDE ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g); };
-    auto load_x = [&](int p, int s, SkinnyChunk<ODD_X>& high, SkinnyChunk<ODD_X>& low, int j) {
+    auto load_x = [&](int p, int s, SkinnyChunk<ODD_X>& high, SkinnyChunk<ODD_X>& low) {
         const int k = first_k(p, s);
-        const uint32_t off = p < p1 && x_off[j] != kOobOffset && k < in ? x_off[j] + (uint32_t)k * 2u : kOobOffset;
+        const uint32_t off = p < p1 && x_off != kOobOffset && k < in ? x_off + (uint32_t)k * 2u : kOobOffset;
         high = load_skinny<ODD_X>(rx, off);
         if constexpr (SPLIT_X) low = load_skinny<ODD_X>(rx, off == kOobOffset ? kOobOffset : off + x_low);
     };
     for (int i0 = p0 + wave; i0 < p1; i0 += KU * WAVES) {
         PieceWeights<STORE, ODD, NB> pw[KU];
-        // Rows of X: with one block all of a piece's are in flight with its weights; with
-        // more each step's are read when it comes (from L2, and too many to keep).
-        SkinnyChunk<ODD_X> x[MB == 1 ? KU : 1][MB][4], low[SPLIT_X && MB == 1 ? KU : 1][SPLIT_X ? MB : 1][4];
+        // A piece's rows of X are in flight with its weights.
+        SkinnyChunk<ODD_X> x[KU][4], low[SPLIT_X ? KU : 1][4];
         float scale[KU];
 #pragma unroll
         for (int q = 0; q < KU; ++q) {
@@ -364,34 +365,24 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
                     }
                 scale[q] = live ? scales[p] : 0.0f;
             }
-            if constexpr (MB == 1) {
 #pragma unroll
-                for (int s = 0; s < 4; ++s) load_x(p, s, x[q][0][s], low[SPLIT_X ? q : 0][0][s], 0);
-            }
+            for (int s = 0; s < 4; ++s) load_x(p, s, x[q][s], low[SPLIT_X ? q : 0][s]);
         }
 #pragma unroll
         for (int q = 0; q < KU; ++q) {
             const int p = i0 + q * WAVES, k0 = p * kBlock;
             if (p >= p1) break;
             const bool tail = k0 + kBlock > in;
-            floatx4 sum[WIDE ? NB : 1][WIDE ? MB : 1];
+            floatx4 sum[WIDE ? NB : 1];
             WeightScale block_scale{1.0f, 1.0f};
             if constexpr (WIDE) {
                 block_scale = weight_scale<DT, FORMAT>(scale[q]);
 #pragma unroll
-                for (int i = 0; i < NB; ++i)
-#pragma unroll
-                    for (int j = 0; j < MB; ++j) sum[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int i = 0; i < NB; ++i) sum[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
             }
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 const int k = first_k(p, s), valid = in - k;
-                constexpr int QX = MB == 1 ? 1 : 0;
-                if constexpr (MB > 1) {
-                    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                    for (int j = 0; j < MB; ++j) load_x(p, s, x[0][j][0], low[0][SPLIT_X ? j : 0][0], j);
-                }
                 u32x4 wv[NB];
                 if constexpr (STORE == kStoreNK) {
 #pragma unroll
@@ -406,8 +397,7 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const u32x3 v = pw[q].v[s][e];
-                        const uint32_t off = ((uint32_t)(32 * s + 8 * g + e) * (uint32_t)out + 4u * (uint32_t)r16) * 2u + base;
-                        const uint32_t bits = (off & 2u) * 8u;
+                        const uint32_t bits = ((uint32_t)(e & 1) * (uint32_t)out * 2u + base & 2u) * 8u;      // (even rows are alike)
                         row[e] = u32x2{__builtin_amdgcn_alignbit(v.y, v.x, bits), __builtin_amdgcn_alignbit(v.z, v.y, bits)};
                         if (tail && e >= valid) row[e] = u32x2{0u, 0u};
                     }
@@ -427,23 +417,20 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
                         wv[i] = widen<DT, FORMAT>(b.x, b.y, block_scale.power);
                     }
                 }
+                u32x4 xv = skinny_value<ODD_X>(x[q][s], rx, x_off + (uint32_t)k * 2u);
+                if (tail) xv = keep_first(xv, valid);
 #pragma unroll
-                for (int j = 0; j < MB; ++j) {
-                    u32x4 xv = skinny_value<ODD_X>(x[QX * q][j][QX * s], rx, x_off[j] + (uint32_t)k * 2u);
-                    if (tail) xv = keep_first(xv, valid);
+                for (int i = 0; i < NB; ++i) {
+                    floatx4& to = WIDE ? sum[WIDE ? i : 0] : acc[i];
+                    to = mfma_16x16x32<DT>(wv[i], xv, to);
+                }
+                if constexpr (SPLIT_X) {
+                    u32x4 lv = low[q][s].v;
+                    if (tail) lv = keep_first(lv, valid);
 #pragma unroll
                     for (int i = 0; i < NB; ++i) {
-                        floatx4& to = WIDE ? sum[i][j] : acc[i][j];
-                        to = mfma_16x16x32<DT>(wv[i], xv, to);
-                    }
-                    if constexpr (SPLIT_X) {
-                        u32x4 lv = low[QX * q][j][QX * s].v;
-                        if (tail) lv = keep_first(lv, valid);
-#pragma unroll
-                        for (int i = 0; i < NB; ++i) {
-                            floatx4& to = WIDE ? sum[i][j] : acc[i][j];
-                            to = mfma_16x16x32<DT>(wv[i], lv, to);
-                        }
+                        floatx4& to = WIDE ? sum[WIDE ? i : 0] : acc[i];
+                        to = mfma_16x16x32<DT>(wv[i], lv, to);
                     }
                 }
             }
@@ -451,9 +438,7 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
 #pragma unroll
                 for (int i = 0; i < NB; ++i)
 #pragma unroll
-                    for (int j = 0; j < MB; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(block_scale.rest, sum[i][j][e], acc[i][j][e]);
+                    for (int e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(block_scale.rest, sum[i][e], acc[i][e]);
             }
         }
     }
@@ -465,14 +450,14 @@ __device__ __forceinline__ void expert_sums(floatx4 (&acc)[NB][MB], const AnyRsr
 //  x_row[q]: where the row of X of this lane's 16 bytes of DMA instruction q begins,
 // in bytes (kOobOffset: none).
 // ONCE: W does not stay in the caches.
-template <int DT, int STORE, bool SPLIT_X, bool ONCE, int NB, int MB, int S, int WAVES>
-__device__ __forceinline__ void expert_stream(floatx4 (&acc)[NB][MB], const uint16_t* x, uint32_t x_bytes, const uint32_t (&x_row)[2 * MB],
+template <int DT, int STORE, bool SPLIT_X, bool ONCE, int NB, int S, int WAVES>
+__device__ __forceinline__ void expert_stream(floatx4 (&acc)[NB], const uint16_t* x, uint32_t x_bytes, const uint32_t (&x_row)[2],
                                               uint32_t x_low, const uint8_t* w, const float* scales, int64_t ld, int n0, int in,
                                               int out, int p0, int p1, uint8_t* ring, int turn, int wave, int lane)
 {
     constexpr bool WIDE = STORE >= kStoreE4M3, KN = STORE == kStoreKN;
     constexpr int FORMAT = STORE == kStoreE4M3 ? kE4M3 : kE5M2;
-    constexpr int K = WIDE ? 128 : 64, HALVES = K / 64, W_BYTES = NB * 2048, X_BYTES = MB * 2048;
+    constexpr int K = WIDE ? 128 : 64, HALVES = K / 64, W_BYTES = NB * 2048, X_BYTES = 2048;
     constexpr int STAGE = W_BYTES + HALVES * X_BYTES * (SPLIT_X ? 2 : 1), NQ = STAGE / 1024;
     static_assert(!KN || NB == 4, "rows of 128 bytes");
     const int r16 = lane & 15, g = lane >> 4, kb = kgroup16(g);
@@ -532,9 +517,9 @@ __device__ __forceinline__ void expert_stream(floatx4 (&acc)[NB][MB], const uint
 #pragma unroll
         for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-            for (int q = 0; q < 2 * MB; ++q) {
-                const uint32_t off = x_row[q] != kOobOffset && 128 * h + pos[q & 1] < 2 * left ? x_row[q] + (uint32_t)pos[q & 1] : kOobOffset;
-                const uint32_t at = to + W_BYTES + (2 * MB * h + q) * 1024, soff = (uint32_t)(2 * k0 + 128 * h);
+            for (int q = 0; q < 2; ++q) {
+                const uint32_t off = x_row[q] != kOobOffset && 128 * h + pos[q] < 2 * left ? x_row[q] + (uint32_t)pos[q] : kOobOffset;
+                const uint32_t at = to + W_BYTES + (2 * h + q) * 1024, soff = (uint32_t)(2 * k0 + 128 * h);
                 dma_b128(rx, at, off, soff);
                 if constexpr (SPLIT_X) dma_b128(rx, at + HALVES * X_BYTES, off, soff + x_low);
             }
@@ -556,7 +541,7 @@ __device__ __forceinline__ void expert_stream(floatx4 (&acc)[NB][MB], const uint
             }
             const uint8_t *const st = ring + slot * STAGE, *const sx = st + W_BYTES;
             constexpr int STEPS = WIDE ? 4 : 2;                  // of 32 k
-            u32x4 wf[NB][2], xf[MB][STEPS], lf[SPLIT_X ? MB : 1][SPLIT_X ? STEPS : 1];
+            u32x4 wf[NB][2], xf[STEPS], lf[SPLIT_X ? STEPS : 1];
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -571,35 +556,28 @@ __device__ __forceinline__ void expert_stream(floatx4 (&acc)[NB][MB], const uint
                     }
                 }
 #pragma unroll
-            for (int j = 0; j < MB; ++j)
-#pragma unroll
-                for (int s = 0; s < STEPS; ++s) {
-                    // 8-bit weights have 16 consecutive k a lane
-                    const int half = WIDE ? s >> 1 : 0, chunk = WIDE ? 2 * kb + (s & 1) : 4 * s + kb;
-                    const uint8_t* q = sx + half * X_BYTES + j * 2048 + r16 * 128 + 16 * (chunk ^ a_swizzle<128>(r16));
-                    xf[j][s] = *reinterpret_cast<const u32x4*>(q);
-                    if constexpr (SPLIT_X) lf[j][s] = *reinterpret_cast<const u32x4*>(q + HALVES * X_BYTES);
-                }
+            for (int s = 0; s < STEPS; ++s) {
+                // 8-bit weights have 16 consecutive k a lane
+                const int half = WIDE ? s >> 1 : 0, chunk = WIDE ? 2 * kb + (s & 1) : 4 * s + kb;
+                const uint8_t* q = sx + half * X_BYTES + r16 * 128 + 16 * (chunk ^ a_swizzle<128>(r16));
+                xf[s] = *reinterpret_cast<const u32x4*>(q);
+                if constexpr (SPLIT_X) lf[s] = *reinterpret_cast<const u32x4*>(q + HALVES * X_BYTES);
+            }
             asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");     // the slot has been read
             fill(i + S, slot, scale[slot]);
             const int k0 = piece_at(i) * K;
-            floatx4 sum[WIDE ? NB : 1][WIDE ? MB : 1];
+            floatx4 sum[WIDE ? NB : 1];
             if constexpr (WIDE) {
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int j = 0; j < MB; ++j) sum[b][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int b = 0; b < NB; ++b) sum[b] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
             }
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int valid = in - (k0 + (WIDE ? 64 * (s >> 1) + 16 * kb + 8 * (s & 1) : 32 * s + 8 * kb));
                 const bool tail = k0 + K > in;
                 if (tail) {
-#pragma unroll
-                    for (int j = 0; j < MB; ++j) {
-                        xf[j][s] = keep_first(xf[j][s], valid);
-                        if constexpr (SPLIT_X) lf[j][s] = keep_first(lf[j][s], valid);
-                    }
+                    xf[s] = keep_first(xf[s], valid);
+                    if constexpr (SPLIT_X) lf[s] = keep_first(lf[s], valid);
                 }
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
@@ -615,21 +593,16 @@ __device__ __forceinline__ void expert_stream(floatx4 (&acc)[NB][MB], const uint
                         wv = wf[b][s];
                         if (tail && !KN) wv = keep_first(wv, valid);    // ((K, N) rows past the last are zeros)
                     }
-#pragma unroll
-                    for (int j = 0; j < MB; ++j) {
-                        floatx4& to = WIDE ? sum[WIDE ? b : 0][WIDE ? j : 0] : acc[b][j];
-                        if constexpr (SPLIT_X) to = mfma_16x16x32<DT>(wv, lf[j][s], to);
-                        to = mfma_16x16x32<DT>(wv, xf[j][s], to);
-                    }
+                    floatx4& to = WIDE ? sum[WIDE ? b : 0] : acc[b];
+                    if constexpr (SPLIT_X) to = mfma_16x16x32<DT>(wv, lf[s], to);
+                    to = mfma_16x16x32<DT>(wv, xf[s], to);
                 }
             }
             if constexpr (WIDE) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int j = 0; j < MB; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[b][j][e] = __builtin_fmaf(block_scale.rest, sum[b][j][e], acc[b][j][e]);
+                    for (int e = 0; e < 4; ++e) acc[b][e] = __builtin_fmaf(block_scale.rest, sum[b][e], acc[b][e]);
             }
         }
     }
@@ -642,8 +615,8 @@ __global__ __launch_bounds__(64 * kExpertWaves[KIND], KIND == 1 ? ODD || STORE >
 {
     constexpr bool WIDE = STORE >= kStoreE4M3, KN = STORE == kStoreKN;
     constexpr int kDeviceScope = 16;   // cache policy sc1
-    constexpr int NB = KN ? 4 : kExpertBlocks[KIND], MB = 1, WAVES = kExpertWaves[KIND], THREADS = 64 * WAVES;
-    constexpr int COLS = 16 * NB, PART = COLS * 17, STAGE = NB * 2048 + MB * (WIDE ? 4096 : 2048) * (SECOND ? 2 : 1);
+    constexpr int NB = KN ? 4 : kExpertBlocks[KIND], WAVES = kExpertWaves[KIND], THREADS = 64 * WAVES;
+    constexpr int COLS = 16 * NB, PART = COLS * 17, STAGE = NB * 2048 + (WIDE ? 4096 : 2048) * (SECOND ? 2 : 1);
     constexpr int S = KIND == 0 && STORE == kStoreNK ? 2 : 1;
     constexpr int PARTS = WAVES * PART * 4, RING = ODD ? 0 : WAVES * S * STAGE;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[RING > PARTS ? RING : PARTS];
@@ -653,7 +626,7 @@ __global__ __launch_bounds__(64 * kExpertWaves[KIND], KIND == 1 ? ODD || STORE >
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tid = threadIdx.x;
     const int r16 = lane & 15, g = lane >> 4;
     const RouteTable t(table, a.tokens * a.top, a.experts);
-    make_table<WAVES, 16 * MB>(t, a, lane, wave);
+    make_table<WAVES, kExpertRows>(t, a, lane, wave);
     const int blocks_n = (a.out + COLS - 1) / COLS, scale_blocks = (a.in + kBlock - 1) / kBlock;
     const int tiles = __builtin_amdgcn_readfirstlane(*t.n_tiles);
     const int units = tiles * blocks_n * a.splits;
@@ -688,16 +661,16 @@ __global__ __launch_bounds__(64 * kExpertWaves[KIND], KIND == 1 ? ODD || STORE >
         };
         // The unit's share of `pieces` of k.
         auto from = [&](int pieces, int s) { return (int)((int64_t)pieces * s / a.splits); };
-        // Adds the waves' sums of 16 rows from row1 on and hands them on.
-        auto finish = [&](const floatx4* sums, int row1) __attribute__((always_inline)) {
-            __syncthreads();           // the rings, or the sums of the rows before, are read
+        // Adds the waves' sums and hands them on.
+        auto finish = [&](const floatx4 (&sums)[NB]) __attribute__((always_inline)) {
+            __syncthreads();           // the rings are read
 #pragma unroll
             for (int i = 0; i < NB; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) part[wave * PART + (16 * i + 4 * g + e) * 17 + r16] = sums[i * MB][e];
+                for (int e = 0; e < 4; ++e) part[wave * PART + (16 * i + 4 * g + e) * 17 + r16] = sums[i][e];
             __syncthreads();
             for (int o = tid; o < 16 * COLS; o += THREADS) {
-                const int row = o / COLS, c = o % COLS, r = row1 + row;
+                const int row = o / COLS, c = o % COLS, r = row0 + row;
                 if (r >= count || n0 + c >= a.out) continue;
                 float z = 0.0f;
 #pragma unroll
@@ -717,25 +690,18 @@ __global__ __launch_bounds__(64 * kExpertWaves[KIND], KIND == 1 ? ODD || STORE >
             }
         };
         const int pieces = WIDE || ODD ? scale_blocks : (a.in + 63) / 64, p0 = from(pieces, split), p1 = from(pieces, split + 1);
-        floatx4 acc[NB][MB];
+        floatx4 acc[NB];
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-            for (int j = 0; j < MB; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < NB; ++i) acc[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
         if constexpr (ODD) {
-            uint32_t x_off[MB];
-#pragma unroll
-            for (int j = 0; j < MB; ++j) x_off[j] = row_of_x(row0 + 16 * j + r16);
-            expert_sums<DT, STORE, SECOND, NB, MB, WAVES>(acc, rx, x_off, (uint32_t)a.mid_row * 2u, w, scales, a.ld, n0, a.in, a.out, p0, p1,
-                                                          wave, lane);
+            expert_sums<DT, STORE, SECOND, NB, WAVES>(acc, rx, row_of_x(row0 + r16), (uint32_t)a.mid_row * 2u, w, scales, a.ld, n0, a.in, a.out,
+                                                      p0, p1, wave, lane);
         } else {
-            uint32_t x_row[2 * MB];
-#pragma unroll
-            for (int q = 0; q < 2 * MB; ++q) x_row[q] = row_of_x(row0 + 8 * q + lane / 8);
+            const uint32_t x_row[2] = {row_of_x(row0 + lane / 8), row_of_x(row0 + 8 + lane / 8)};
             const auto stream = [&](auto once) __attribute__((always_inline)) {
-                expert_stream<DT, STORE, SECOND, once.value, NB, MB, S, WAVES>(acc, a.x, x_bytes, x_row, (uint32_t)a.mid_row * 2u, w, scales, a.ld,
-                                                                               n0, a.in, a.out, p0, p1, smem + wave * (S * STAGE),
-                                                                               unit % max(p1 - p0, 1), wave, lane);
+                expert_stream<DT, STORE, SECOND, once.value, NB, S, WAVES>(acc, a.x, x_bytes, x_row, (uint32_t)a.mid_row * 2u, w, scales, a.ld,
+                                                                           n0, a.in, a.out, p0, p1, smem + wave * (S * STAGE),
+                                                                           unit % max(p1 - p0, 1), wave, lane);
             };
             // (A branch for every piece costs 24 tokens 131 -> 140 us, both loops one token 24.3 -> 25.4.)
             if constexpr (KIND == 1) {
@@ -745,11 +711,7 @@ __global__ __launch_bounds__(64 * kExpertWaves[KIND], KIND == 1 ? ODD || STORE >
                 stream(std::false_type{});
             }
         }
-#pragma unroll
-        for (int j = 0; j < MB; ++j) {
-            if (row0 + 16 * j >= count) break;
-            finish(&acc[0][j], row0 + 16 * j);
-        }
+        finish(acc);
         if constexpr (SECOND) {
             wait_vmcnt<0>();           // this wave's sums have reached device scope
             __syncthreads();
