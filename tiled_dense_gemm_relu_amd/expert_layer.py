@@ -63,7 +63,8 @@ class ServedExperts:
     """An ExpertLayer's weights in 8 bits, stored (out, in), with the softmax of its chosen experts' logits.
 
     ``prompt`` sorts the chosen (token, expert) pairs by expert and multiplies quantized rows; ``decode`` takes
-    up to 64 tokens, whose activations it does not quantize.
+    up to 64 tokens, whose activations it does not quantize.  Both choose alike: ties to the lowest index, logits
+    of -inf never, rows of zeros for tokens without a choice and of NaN for those with a logit of NaN or +inf.
     """
 
     def __init__(self, layer: ExpertLayer, top: int, dtype=torch.float8_e4m3fn):
@@ -75,15 +76,16 @@ class ServedExperts:
         return gemm_relu_experts(x, self.w1, self.w2, logits, self.top, w1_scales=self.s1, w2_scales=self.s2)[0]
 
     def prompt(self, x: torch.Tensor, logits: torch.Tensor):
-        best, ids = logits.topk(self.top, dim=1)
-        share = best.softmax(dim=1)
+        best, ids = (t[:, : self.top] for t in logits.sort(dim=1, descending=True, stable=True))
+        share, none = best.softmax(dim=1).reshape(-1), (best == -float("inf")).reshape(-1)
         expert, order = ids.reshape(-1).sort(stable=True)
         ends = torch.searchsorted(expert, torch.arange(self.experts, device=x.device), right=True).to(torch.int32)
         rows = order // self.top
         hidden = gemm_relu_blocks(*quantize_blocks(x[rows], self.dtype), self.w1, self.s1, ends=ends, out_dtype=x.dtype)
         y = gemm_relu_blocks(*quantize_blocks(hidden, self.dtype), self.w2, self.s2, ends=ends, out_dtype=x.dtype, relu=False)
-        out = torch.zeros(x.shape, dtype=torch.float32, device=x.device)
-        return out.index_add_(0, rows, y.float() * share.reshape(-1)[order][:, None]).to(x.dtype)
+        parts = torch.empty(y.shape, dtype=torch.float32, device=x.device)
+        parts[order] = (y.float() * share[order][:, None]).masked_fill_(none[order][:, None], 0.0)
+        return parts.view(*ids.shape, -1).sum(dim=1).to(x.dtype)      # (in the order of the choices, every time)
 
 
 def train(steps: int = 8, tokens: int = 512, experts: int = 8, width: int = 128, hidden: int = 256, rate: float = 0.1):
