@@ -103,6 +103,23 @@ def test_blocks_of_zeros_under_large_scales(config, b_rows):
     assert torch.equal(op(sa, sb, config), want)
 
 
+@pytest.mark.parametrize("config", CONFIGS)
+@pytest.mark.parametrize("b_rows", [False, True])
+@pytest.mark.parametrize("fa,fb", list(SMALL))
+def test_terms_that_cancel_under_large_scales(config, b_rows, fa, fb):
+    # Terms past the largest float, of a sum that is not: block sums are taken before they are scaled.
+    M, N, K = 70, 200, 256
+    op = Operands(M, N, K, fa, fb, b_rows, 17)
+    a, b = torch.zeros((M, K)), torch.zeros((N, K))
+    a[:, 0::128], a[:, 1::128], b[:, 0::128], b[:, 1::128] = 448.0, -448.0, 448.0, 448.0
+    a[:, 9::128], b[:, 9::128] = 16.0 * torch.randint(1, 4, (M, 1), generator=gen(1)), 2.0
+    op.pa, op.pb = pitched(a.to(fa)), pitched(b.to(fb))
+    base = op(op.sa, op.sb, config)
+    assert ((base >= 16) & (base <= 512)).all()
+    for p, q in ((119, -1), (59, 58), (-1, 117), (30, 85)):
+        assert torch.equal(op(times(op.sa, p), times(op.sb, q), config).double(), base.double() * 2.0 ** (p + q)), (p, q)
+
+
 @pytest.mark.parametrize("sizes", [[300, 0, 1, 17, 128, 0, 260], [1] * 70, [64] * 5 + [0] * 80 + [3]])
 @pytest.mark.parametrize("config", CONFIGS)
 def test_groups(sizes, config):

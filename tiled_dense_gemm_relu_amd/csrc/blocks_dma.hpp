@@ -10,7 +10,7 @@
 // read as the 16-bit kernels' (a_swizzle<128>), and the scales of those rows and
 // columns as floats: with scales by tiles every lane of the scales' DMA fetches
 // its column's tile, so both forms look alike in LDS.  The wave that brought a piece
-// of them splits it there, for all, into mantissas and exponents (split_scale).
+// of them splits it there, for all, into factors and exponents (split_scale).
 //
 // The 256 tile at 8192^3 on normal data: 487-492 us, 2.24-2.26 PFLOP/s, where a library
 // product with one scale a matrix takes 410-419.  With the scales' exponents left to the
@@ -28,27 +28,29 @@ namespace gemm_relu_hip {
 
 typedef int int32x8_t __attribute__((ext_vector_type(8)));
 
-// A scale as m 2^(e - 127), e from 0 to 254, the exponents of the matrix instruction.  m is
-// of magnitude 1 to 2, less for a subnormal scale, and what the scale is where that is
-// zero, infinite or NaN.  (Exact.)
+// A scale as m 2^(e - 127), exactly: e, for the matrix instruction, has what the scale's
+// exponent is beyond -40 .. 40, so the product of two m is a normal float (if neither scale
+// is zero, infinite or NaN, as which m is the same).  A block's sum, 2^-32 to 2^39, and its
+// partial sums stay normal when they are multiplied by the two powers of two, wherever the
+// scales' own product is normal: the bits are then those of sums multiplied afterwards.
 struct SplitScale {
     float m;
     uint32_t e;
 };
 __device__ __forceinline__ SplitScale split_scale(float s)
 {
-    const uint32_t e = min((__builtin_bit_cast(uint32_t, s) >> 23) & 0xffu, 254u);
-    return SplitScale{__builtin_ldexpf(s, 127 - (int)e), e};
+    const int exponent = min((int)((__builtin_bit_cast(uint32_t, s) >> 23) & 0xffu), 254) - 127;
+    const int moved = exponent - min(max(exponent, -40), 40);
+    return SplitScale{__builtin_ldexpf(s, -moved), (uint32_t)(moved + 127)};
 }
 
 // 16 x 16 fp32 sums over 128 k, times two powers of two: `w` of format FW, `x` of format
 // FX.  A lane holds 32 bytes of one row of each; which k those are only has to agree
 // between them.  The exponents of a lane's rows are byte `bw` of `ew` and byte `bx` of `ex`
-// (constants once loops are unrolled).  With them applied here the sums are multiplied by
-// two numbers between 1 and 2; the product of two scales could be subnormal, zero or
-// infinite where the result is not.  (Where it is none of these the bits are the same.
-// This costs 8192^3 3%, the 128 tile with scales of B by rows 14%; a second body of the loop
-// for steps whose scales need it, 30%, by its registers.)
+// (constants once loops are unrolled).  The product of two scales alone could be subnormal,
+// zero or infinite where the result is not.  (This costs 8192^3 3%, the 128 tile with scales
+// of B by rows 14%; a second body of the loop for steps whose scales need it, 30%, by its
+// registers.)
 template <int FW, int FX>
 __device__ __forceinline__ floatx4 mfma_block(int32x8_t w, int32x8_t x, uint32_t ew, int bw, uint32_t ex, int bx)
 {
@@ -360,8 +362,8 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
         for (int q = 0; q < QB; ++q) cut(smem + Cfg::B_REGION + slot * Cfg::B_STAGE + (dwave * QB + q) * 1024, pos[q & 1]);
     };
 
-    // This wave's piece of the scales, of a stage that has landed: mantissas in their place,
-    // and exponents.
+    // This wave's piece of the scales, of a stage that has landed: what is left of them in
+    // their place, and their exponents.
     const auto exponent_at = [](int i) {
         constexpr int FM = Cfg::FM, FN = Cfg::FN;
         const int r = i < BM ? i : i - BM, n = i < BM ? FM : FN;
