@@ -106,12 +106,13 @@ def test_blocks_of_zeros_under_large_scales(config, b_rows):
 @pytest.mark.parametrize("config", CONFIGS)
 @pytest.mark.parametrize("b_rows", [False, True])
 @pytest.mark.parametrize("fa,fb", list(SMALL))
-def test_terms_that_cancel_under_large_scales(config, b_rows, fa, fb):
+@pytest.mark.parametrize("apart", [1, 8, 64])
+def test_terms_that_cancel_under_large_scales(config, b_rows, fa, fb, apart):
     # Terms past the largest float, of a sum that is not: block sums are taken before they are scaled.
     M, N, K = 70, 200, 256
     op = Operands(M, N, K, fa, fb, b_rows, 17)
     a, b = torch.zeros((M, K)), torch.zeros((N, K))
-    a[:, 0::128], a[:, 1::128], b[:, 0::128], b[:, 1::128] = 448.0, -448.0, 448.0, 448.0
+    a[:, 0::128], a[:, apart::128], b[:, 0::128], b[:, apart::128] = 448.0, -448.0, 448.0, 448.0
     a[:, 9::128], b[:, 9::128] = 16.0 * torch.randint(1, 4, (M, 1), generator=gen(1)), 2.0
     op.pa, op.pb = pitched(a.to(fa)), pitched(b.to(fb))
     base = op(op.sa, op.sb, config)
