@@ -144,7 +144,7 @@ int64_t gemm_relu_blocks_backward_workspace(int64_t M, int64_t N, int64_t K);
  * with scales in form tiles; they are multiplied as they are, X is not quantized.
  *
  * weights[t][j] ReLU(..) is computed in fp32 and kept as a sum of two values of X's
- * dtype, off by at most 2^-16 (bf16) or 2^-22 (fp16) of the value, or 2^-25 in fp16;
+ * dtype, off by at most 2^-16 (bf16) or 2^-22 (fp16) of the value, or 2^-134 and 2^-25;
  * fp16 values past 65504 are infinite, as in a layer of two products.
  */
 int gemm_relu_experts(const void* X, const void* W1, const float* scales1, const void* W2, const float* scales2,

@@ -35,6 +35,29 @@ def test_powers_of_two(shape, kind):
         assert torch.equal(got.double(), want), (px, p1, p2, int((got.double() != want).sum()), want.numel())
 
 
+@pytest.mark.parametrize("K", [256, 301])
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
+def test_terms_that_cancel_under_large_scales(K, kind):
+    # Terms past the largest float, of a sum that is not: block sums are taken before they are scaled.
+    layer = Layer(kind, torch.bfloat16, 2, K, 128, 64, 3)
+    x = torch.zeros((3, K))
+    w = torch.zeros((2, 128, K))
+    x[:, 0], x[:, 70], w[:, :, 0], w[:, :, 70] = 1024.0, -1024.0, 256.0, 256.0
+    x[:, 9], w[:, :, 9] = 1.0, 0.25
+    layer.w[0][..., :] = w.to(layer.w[0].dtype).to(DEV)
+    layer.args["w1_scales"] = torch.full_like(layer.args["w1_scales"], 0.75)
+    s1, s2 = layer.args["w1_scales"].clone(), layer.args["w2_scales"].clone()
+    x, logits = x.bfloat16().to(DEV), torch.zeros((3, 2), device=DEV)
+
+    def call(power):
+        layer.args["w1_scales"], layer.args["w2_scales"] = times(s1, power), times(s2, -power)
+        return layer(x, logits, 1)[0].cpu()
+    base = call(0)
+    assert base.isfinite().all() and base.any()
+    for power in (60, 110, 115):
+        assert torch.equal(call(power), base), power
+
+
 def test_scales_without_an_exponent():
     layer = Layer("e4m3", torch.bfloat16, 4, 128, 128, 64, 3)
     x, logits = torch.ones((2, 128), dtype=torch.bfloat16, device=DEV), torch.zeros((2, 4), device=DEV)

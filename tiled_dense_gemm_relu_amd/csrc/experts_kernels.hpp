@@ -10,8 +10,8 @@
 // lengths, 2-byte alignment) go through registers.
 //
 // The first launch leaves weight * ReLU(sum) of every choice as a sum of two 16-bit
-// values, for the second one's matrix instructions: off by at most 2^-16 of the value
-// with bf16, with fp16 by 2^-22 or 2^-25, and infinite past 65504 (one value would be off
+// values, for the second one's matrix instructions: off by at most 2^-16 of the value or
+// 2^-134 with bf16, with fp16 by 2^-22 or 2^-25, and infinite past 65504 (one value would be off
 // by 2^-9 and 2^-12; a third takes half as much again of the rings' room for rows).
 // The second launch's units write a choice's products as fp32; the last unit of a column
 // block to end adds each token's in the order of its choices.
@@ -237,9 +237,11 @@ __device__ inline void make_table(const RouteTable& t, const ExpertsArgs& a, int
 }
 
 // The scale of a block of 8-bit weights as two factors: a power of two that the widened
-// weights take, and the rest, which their sum does.  bf16 weights take all of the exponent
-// that they can hold: rows times stored values alone could be out of a float's range where
-// the products are not.  fp16 rows times stored values are at most 2^32 a product.
+// weights take, and the rest, which their sum does.  bf16 rows times stored values could
+// pass the largest float where the products do not: weights with small scales take as much
+// of them as keeps 128 products of any rows below it.  (Small rows need nothing: the
+// products of 8 and 4 bits are exact, subnormal ones too.  Nor do fp16 rows, whose products
+// are at most 2^32.)
 struct WeightScale {
     float power, rest;
 };
@@ -247,9 +249,8 @@ template <int DT, int FORMAT>
 __device__ __forceinline__ WeightScale weight_scale(float s)
 {
     if constexpr (DT == kF16) return WeightScale{1.0f, s};
-    // 448 2^118 and 57344 2^111 are below 2^127; 2^-9 2^-117 and 2^-16 2^-110 are normal
-    constexpr int most = FORMAT == kE4M3 ? 118 : 111, least = FORMAT == kE4M3 ? -117 : -110;
-    const int e = min(max((int)((__builtin_bit_cast(uint32_t, s) >> 23) & 0xffu) - 127, least), most);
+    constexpr int least = FORMAT == kE4M3 ? -16 : -23;      // 128 448 2^128 2^-16 < 2^128; 128 57344 2^128 2^-23 < 2^128
+    const int e = min(max((int)((__builtin_bit_cast(uint32_t, s) >> 23) & 0xffu) - 127, least), 0);
     return WeightScale{__builtin_bit_cast(float, (uint32_t)(e + 127) << 23), __builtin_ldexpf(s, -e)};
 }
 
