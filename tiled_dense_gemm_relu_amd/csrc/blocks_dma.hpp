@@ -9,13 +9,17 @@
 // A stage is 128 k of the tile's rows of A and B, 128 bytes a row, swizzled and
 // read as the 16-bit kernels' (a_swizzle<128>), and the scales of those rows and
 // columns as floats: with scales by tiles every lane of the scales' DMA fetches
-// its column's tile, so both forms look alike in LDS.  The wave that brought a piece
-// of them splits it there, for all, into factors and exponents (split_scale).
+// its column's tile, so both forms look alike in LDS.  They are split into factors and
+// exponents (split_scale): by the wave that brought them, in LDS, for all; in the 64
+// tile by each compute wave, in registers, as there the waves that load have no time to
+// spare.  us in LDS and in registers: tiles of 64, 64 x 4096 x 4096 17.0 / 15.8, 512 x 2048 x
+// 2048 11.8 / 10.8; of 128, 32 groups of 128 rows x 2048 x 2048 39.2 / 39.2, with scales of B
+// by rows 65 / 82.
 //
-// The 256 tile at 8192^3 on normal data: 487-492 us, 2.24-2.26 PFLOP/s, where a library
-// product with one scale a matrix takes 410-419.  With the scales' exponents left to the
-// vector unit, which loses what lies outside a float's range, it takes 471-472 on the same
-// card; without the additions 428 then, without DMA 392; loads by all waves with one barrier a step, and matrix instructions
+// The 256 tile at 8192^3 on normal data: 483-496 us, 2.22-2.27 PFLOP/s, where a library
+// product with one scale a matrix takes 410-419.  With scales multiplied as they are, which
+// loses what lies outside a float's range, it takes 472-478 on the same card; without the
+// additions 428 then, without DMA 392; loads by all waves with one barrier a step, and matrix instructions
 // interleaved with additions, are what it got there by.  The smaller tiles have waves
 // that only load: 64 groups of 64 rows x 2048 x 4096 103 us, 5.5 TB/s.
 #pragma once
@@ -82,12 +86,11 @@ struct BlockConfig {
     static constexpr int DMA_WAVES = PRODUCERS > 0 ? PRODUCERS : WAVES, THREADS = 64 * (WAVES + PRODUCERS);
     static constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N, FM = WTM / 16, FN = WTN / 16;
     static constexpr int A_STAGE = BM * BK, B_STAGE = BN * BK, B_REGION = STAGES * A_STAGE;
-    // Every wave that loads brings a piece of 64 scales; those past the last one bring a piece
-    // again, to a place that nobody reads (pieces are rewritten once they have landed).
-    static constexpr int S_STAGE = DMA_WAVES * 256, S_REGION = STAGES * (A_STAGE + B_STAGE);
-    // The scales' exponents, a byte each: of a wave's rows 16 j + r for each r those of all j
-    // (FM bytes), after the rows the columns' likewise (FN bytes).
-    static constexpr int E_STAGE = BM + BN, E_REGION = S_REGION + STAGES * S_STAGE;
+    static constexpr int S_STAGE = (BM + BN) * 4, S_REGION = STAGES * (A_STAGE + B_STAGE);
+    // SPLIT: scales are split in LDS.  Their exponents are a byte each: of a wave's rows
+    // 16 j + r for each r those of all j (FM bytes), after the rows the columns' likewise (FN).
+    static constexpr bool SPLIT = BM > 64;
+    static constexpr int E_STAGE = SPLIT ? BM + BN : 0, E_REGION = S_REGION + STAGES * S_STAGE;
     // A wave's strip: 16 rows of its columns of C on their way to memory.
     static constexpr int STRIP = 16 * WTN * 2, STRIPS = E_REGION + STAGES * E_STAGE;
     static constexpr int LDS_BYTES = STRIPS + WAVES * STRIP;
@@ -96,6 +99,7 @@ struct BlockConfig {
     static_assert(QA * DMA_WAVES * 1024 == A_STAGE && QB * DMA_WAVES * 1024 == B_STAGE, "whole DMA instructions");
     static_assert(QA % 2 == 0 && QB % 2 == 0, "the swizzle repeats every two instructions");
     static_assert(SCALE_PIECES <= DMA_WAVES && DMA_WAVES % SCALE_PIECES == 0, "one DMA of scales a wave");
+    static_assert(!SPLIT || SCALE_PIECES == DMA_WAVES, "a piece that is rewritten is brought once");
     static_assert((STAGES & (STAGES - 1)) == 0 && LDS_BYTES <= 160 * 1024 && STAGES * NQ < 64, "ring");
     static_assert((WTN == 64 || WTN == 32) && 128 % WTN == 0, "a wave's columns lie in one tile of scales");
 };
@@ -269,7 +273,7 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
     // The scales' DMA: 64 floats of the tile's rows or columns a wave.
     const int piece = dwave & (Cfg::SCALE_PIECES - 1);
     const bool scales_of_a = piece < BM / 64;
-    const uint32_t scales_lds = lds_base + Cfg::S_REGION + 256u * (uint32_t)dwave;
+    const uint32_t scales_lds = lds_base + Cfg::S_REGION + 256u * (uint32_t)piece;
 
     // The load side; past the last unit everything is out of range and fetches nothing.
     int f_unit = 0, f_k = 0, f_left = 0, f_turn = 0, f_rows = 0, f_cols = 0;
@@ -406,7 +410,7 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
             int k = f_turn, left = k_blocks;                 // of the stage that lands
             for (int g = 0; g < steps; ++g) {
                 wait_vmcnt<(S - 2) * NQ>();
-                if (dwave < Cfg::SCALE_PIECES) split_piece(g & (S - 1), read_piece(g & (S - 1)));
+                if constexpr (Cfg::SPLIT) split_piece(g & (S - 1), read_piece(g & (S - 1)));
                 cut_off(g & (S - 1), a.k - k);
                 k = k + BK < a.k ? k + BK : 0;
                 lds_barrier();
@@ -452,27 +456,6 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
         const float s = sc[BM + wn * Cfg::WTN];
         return floatx4{s, s, s, s};
     };
-    // The exponents of this lane's rows and columns, packed.
-    struct Exponents {
-        uint32_t w, x[(FM + 3) / 4];
-    };
-    auto read_exponents = [&](int slot) {
-        const uint8_t* const e = smem + Cfg::E_REGION + slot * Cfg::E_STAGE;
-        const uint8_t *const ex = e + wm * Cfg::WTM + j16 * FM, *const ew = e + BM + wn * Cfg::WTN + j16 * FN;
-        Exponents v;
-        v.w = FN == 4 ? *reinterpret_cast<const uint32_t*>(ew) : *reinterpret_cast<const uint16_t*>(ew);
-        if constexpr (FM == 8) {
-            const u32x2 both = *reinterpret_cast<const u32x2*>(ex);
-            v.x[0] = both.x;
-            v.x[1] = both.y;
-        } else {
-            v.x[0] = FM == 4 ? *reinterpret_cast<const uint32_t*>(ex) : *reinterpret_cast<const uint16_t*>(ex);
-        }
-        return v;
-    };
-    auto product = [&](int32x8_t w, int32x8_t x, const Exponents& e, int i, int j) __attribute__((always_inline)) {
-        return mfma_block<FB, FA>(w, x, e.w, i, e.x[j / 4], j % 4);
-    };
     auto store = [&](const DmaUnit& c) {
         const int m_base = c.m0 + wm * Cfg::WTM, n_base = c.n0 + wn * Cfg::WTN;
         uint8_t* const strip = smem + Cfg::STRIPS + wave * Cfg::STRIP;
@@ -489,7 +472,8 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
             int32x8_t w[FN], x[FM];
             float scale_x[FM];
             floatx4 scale_w[NSW];
-            Exponents exponents;
+            uint32_t exponent_w[NSW], exponent_x[FM];      // (SPLIT: packed, in the first)
+            float scale_own[NSW];                          // not SPLIT: that of the operand's row in this lane
         } f[2];
         auto read = [&](Fragments& to, int slot) __attribute__((always_inline)) {
             const float* sc = scales(slot);
@@ -501,7 +485,15 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
             for (int j = 0; j < FM; ++j) to.scale_x[j] = sc[wm * Cfg::WTM + 16 * j + j16];
 #pragma unroll
             for (int i = 0; i < NSW; ++i) to.scale_w[i] = read_scale_w(sc, i);
-            to.exponents = read_exponents(slot);
+            if constexpr (Cfg::SPLIT) {
+                static_assert(!Cfg::SPLIT || (FM == 4 && FN == 4), "bytes of exponents a lane");
+                const uint8_t* const e = smem + Cfg::E_REGION + slot * Cfg::E_STAGE;
+                to.exponent_x[0] = *reinterpret_cast<const uint32_t*>(e + wm * Cfg::WTM + j16 * FM);
+                to.exponent_w[0] = *reinterpret_cast<const uint32_t*>(e + BM + wn * Cfg::WTN + j16 * FN);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NSW; ++i) to.scale_own[i] = B_ROWS ? sc[BM + wn * Cfg::WTN + 16 * i + j16] : to.scale_w[i][0];
+            }
         };
         int c_unit = 0, left = k_blocks, g = 0;
         lds_barrier();
@@ -511,10 +503,28 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
             ++g;
             lds_barrier();                                  // step g has landed, or the last one is done
             if (g < steps) read(next, g & (S - 1));
+            if constexpr (!Cfg::SPLIT) {
+#pragma unroll
+                for (int j = 0; j < FM; ++j) {
+                    const SplitScale s = split_scale(now.scale_x[j]);
+                    now.scale_x[j] = s.m;
+                    now.exponent_x[j] = s.e;
+                }
+#pragma unroll
+                for (int i = 0; i < NSW; ++i) {
+                    now.exponent_w[i] = split_scale(now.scale_own[i]).e;
+#pragma unroll
+                    for (int e = 0; e < (B_ROWS ? 4 : 1); ++e) now.scale_w[i][e] = split_scale(now.scale_w[i][e]).m;
+                }
+            }
             floatx4 t[LAG + 1];
 #pragma unroll
             for (int u = 0; u < FM * FN + LAG; ++u) {
-                if (u < FM * FN) t[u % (LAG + 1)] = product(now.w[u % FN], now.x[u / FN], now.exponents, u % FN, u / FN);
+                if (u < FM * FN) {
+                    const int i = u % FN, j = u / FN;
+                    if constexpr (Cfg::SPLIT) t[u % (LAG + 1)] = mfma_block<FB, FA>(now.w[i], now.x[j], now.exponent_w[0], i, now.exponent_x[0], j);
+                    else t[u % (LAG + 1)] = mfma_block<FB, FA>(now.w[i], now.x[j], now.exponent_w[B_ROWS ? i : 0], 0, now.exponent_x[j], 0);
+                }
                 if (u >= LAG) {
                     const int d = u - LAG, i = d % FN, j = d / FN;
                     add(i, j, t[d % (LAG + 1)], now.scale_x[j], now.scale_w[B_ROWS ? i : 0]);
@@ -555,7 +565,14 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
             for (int j = 0; j < FM; ++j) scale_x[j] = sc[wm * Cfg::WTM + 16 * j + j16];
 #pragma unroll
             for (int i = 0; i < NSW; ++i) scale_w[i] = read_scale_w(sc, i);
-            const Exponents exponents = read_exponents(slot);
+            // exponents of this lane's rows and columns, packed
+            const uint8_t* const ep = smem + Cfg::E_REGION + slot * Cfg::E_STAGE;
+            const u32x2 ex = *reinterpret_cast<const u32x2*>(ep + wm * Cfg::WTM + j16 * FM);
+            const uint32_t ew = *reinterpret_cast<const uint32_t*>(ep + BM + wn * Cfg::WTN + j16 * FN);
+            static_assert(FM == 8 && FN == 4, "bytes of exponents a lane");
+            const auto product = [&](int i, int j) __attribute__((always_inline)) {
+                return mfma_block<FB, FA>(w[i], x[j % 3], ew, i, ex[j / 4], j % 4);
+            };
             x[0] = x[2];
             read_x(1, slot, 1);
             floatx4 t[LAG + 1];
@@ -576,7 +593,7 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
                 read_x((j + 2) % 3, slot, j + 2);
 #pragma unroll
                 for (int i = 0; i < FN; ++i, ++u) {
-                    t[u % (LAG + 1)] = product(w[i], x[j % 3], exponents, i, j);
+                    t[u % (LAG + 1)] = product(i, j);
                     if (u >= LAG) finish(u - LAG);
                 }
                 interleave<FN>();
@@ -593,7 +610,7 @@ __device__ __forceinline__ void blocks_tiles(const BlocksArgs& a, int block, int
             for (int i = 0; i < FN; ++i) {
 #pragma unroll
                 for (int j = FM - 2; j < FM; ++j, ++u) {
-                    t[u % (LAG + 1)] = product(w[i], x[j % 3], exponents, i, j);
+                    t[u % (LAG + 1)] = product(i, j);
                     finish(u - LAG);
                 }
                 interleave<2>();
