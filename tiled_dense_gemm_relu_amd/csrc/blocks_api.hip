@@ -64,9 +64,18 @@ int launch_quantize(QuantizeArgs a, int64_t count, int dtype, int format, int fo
 }
 
 // Whether weights of so many bytes are streamed past the caches.  From memory they come
-// faster so, from the cache beside it (256 MB) slower: few rows x 16384 x 8192 28.2 us and
-// 24.2, 32 groups of 2048 x 2048 29.7 and 27.3; but 8192 x 8192 12.7 and 16.9 where they
-// stay there, 18.0 and 16.5 where they do not.
+// faster so, from the cache beside it (256 MB) slower, and a model's layers take turns in
+// that.  us through the caches and past them, of weights from memory / that stay in the
+// cache from the call before:
+//   64 MB   few rows x 8192 x 8192           18.0 16.5 / 12.7 16.9
+//   96      16 rows x 12288 x 8192           21.9 20.5 / 17.2 18.9
+//  128      16 rows x 16384 x 8192           26.8 23.7 / 21.6 23.2
+//           64 rows x 16384 x 8192           33.9 31.8 / 25.1 32.7
+//           1024 in 32 groups, 2048 x 2048   34.2 29.1 / 25.5 30.0
+//  192      16 rows x 24576 x 8192           44.1 40.8 / 32.6 41.0
+//           2048 in 24 groups, 4096 x 2048   69.5 47.5 / 61.2 48.8
+//  234      16 rows x 30000 x 8192           49.7 45.1 / 38.2 41.2
+// Weights of 64 MB lose too much where several layers' stay there together.
 constexpr int64_t kStreamOnce = int64_t(96) << 20;
 
 // Tiles of `tile` x `tile` that a product can have: whole ones, and a partial one for each group.
@@ -97,14 +106,21 @@ int64_t most_tiles(const BlocksArgs& a, int64_t tile)
 //   512 in 8, 2048 x 2048         33.8 / 22.6 / 17.5 / 17.5 / 13.9 / 15.5     11.7  17.6
 //  More than 32 rows and more than one workgroup a CU: tiles of 64, us streaming and so
 // (64 rows): 65536 x 1024 30.0 / 16.8, 32768 x 2048 20.2 / 15.6, 24576 x 8192 54.6 / 50.4,
-// 17000 x 1024 14.4 / 10.3; at one a CU the longer sums stream, 16384 x 4096 16.0 / 15.2,
-// x 8192 30.7 / 31.4.  Groups of up to 32 rows likewise, 8 groups x 8192 x 512 13.5 / 11.2,
+// 17000 x 1024 14.4 / 10.3; at one a CU the longer sums stream, 64 rows and 40, us streaming
+// and in tiles of 64: 16384 x 4096 16.0 / 15.2, x 6144 26.1 / 27.0 and 22.9 / 26.3, x 8192 30.9 /
+// 32.6 and 27.0 / 34.0, x 16384 58.8 / 61.8 and 47.7 / 61.8, 12300 x 8192 30.8 / 30.6, x 16384
+// 52.3 / 58.9.  Groups of up to 32 rows likewise, 8 groups x 8192 x 512 13.5 / 11.2,
 // 16 x 1024 x 2048 11.6 / 10.0, 8 x 1024 x 4096 10.8 / 14.5.
 //  Groups of few rows with weights from memory: the deepest ring reads them fastest where
 // its units go round three times, us streaming, tiles of 64 and of 128 (32 rows a group):
 // 64 x 2048 x 4096 115 / 107 / 102, 16 x 16384 x 4096 217 / 212 / 198, 16 x 4096 x 4096
 // 59.8 / 50.9 / 50.7, 32 x 2048 x 2048 30.9 / 26.8 / 30.0.
 // Tiles: the largest whose tiles are mostly full and numerous enough to occupy the CUs.
+//  (Most of these were measured with scales multiplied as they are.  Splitting them adds 1 to
+// 10% to tiles of 64, 3 to 6% to those of 128 and 256 and 0 to 6% to streams; what a rule takes
+// is the faster side still, or within 4% of it: 64 x 4096 x 4096 8.2 streaming / 15.7 / -, 512 x 1024 x 1024 5.9 / 7.6,
+// 512 x 2048 x 2048 10.4 / 10.8 / 16.1, 1024 x 1024 x 1024 7.7 / 7.8 / 11.2, 512 in 8 groups
+// x 2048 x 2048 12.0 / 11.0, 64 x 65536 x 1024 28.0 / 17.0.)
 struct BlocksChoice {
     int config, stream = -1;
     BlocksChoice(int64_t m, int64_t n, int64_t k, int64_t groups, bool dense, bool heavy)

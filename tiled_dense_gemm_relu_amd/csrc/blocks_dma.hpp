@@ -21,7 +21,8 @@
 // loses what lies outside a float's range, it takes 472-478 on the same card; without the
 // additions 428 then, without DMA 392; loads by all waves with one barrier a step, and matrix instructions
 // interleaved with additions, are what it got there by.  The smaller tiles have waves
-// that only load: 64 groups of 64 rows x 2048 x 4096 103 us, 5.5 TB/s.
+// that only load: 64 groups of 64 rows x 2048 x 4096 112-116 us, 4.8 TB/s (109 with scales
+// multiplied as they are).
 #pragma once
 
 #include "blocks_bytes.hpp"

@@ -7,8 +7,9 @@
 // conversion of two rows' elements of a column fills two bytes of the transposed
 // row, and the transposed tile passes through LDS as 8-byte pieces.  Loads that do not
 // stay in the caches leave them to what is written, which the product reads next
-// (8192 x 4096 with a mask, both ways: 47 -> 43 us, 192 MiB, and a layer's forward and
-// backward pass around it 477 -> 460; stores that do not stay: 44, but 499 for the layer).
+// (8192 x 4096 with a mask, both ways, over four matrices in turn: 46-47 -> 43 us, 192 MiB,
+// and a layer's forward and backward pass around it 477 -> 460; stores that do not stay: 44,
+// but 499 for the layer).
 #include "groups_kernels.hpp"
 #include "blocks_table.hpp"
 
