@@ -54,3 +54,14 @@ def test_an_expert_that_is_never_chosen_may_hold_anything():
     logits[:, 3] = -math.inf
     logits[::2, 2] = -math.inf                           # fewer than three to choose from
     assert served.decode(x, logits).isfinite().all() and served.prompt(x, logits).isfinite().all()
+
+
+def test_no_tokens_one_token_and_too_many_choices(served):
+    x, logits = inputs(3)
+    assert served.prompt(x[:0], logits[:0]).shape == (0, 128)
+    # (products of other sizes may take other kernels, whose sums differ in fp32: a rounding to bf16 and to e4m3 can turn)
+    one = served.prompt(x[:1], logits[:1]).float()
+    assert float((one - served.prompt(x, logits)[:1].float()).norm() / one.norm()) <= 2.0 ** -5
+    for top in (0, 9):
+        with pytest.raises(ValueError, match="top"):
+            ServedExperts(ExpertLayer(8, 128, 256, seed=5), top)

@@ -68,6 +68,8 @@ class ServedExperts:
     """
 
     def __init__(self, layer: ExpertLayer, top: int, dtype=torch.float8_e4m3fn):
+        if not 1 <= top <= layer.experts:
+            raise ValueError(f"top must be 1 to {layer.experts}, got {top}")
         self.top, self.experts, self.dtype = top, layer.experts, dtype
         (self.w1, self.s1), (self.w2, self.s2) = (quantize_blocks(w, dtype, tiles=True, rows=False, transposed=True)
                                                   for w in layer.weights)
@@ -85,7 +87,7 @@ class ServedExperts:
         y = gemm_relu_blocks(*quantize_blocks(hidden, self.dtype), self.w2, self.s2, ends=ends, out_dtype=x.dtype, relu=False)
         parts = torch.empty(y.shape, dtype=torch.float32, device=x.device)
         parts[order] = (y.float() * share[order][:, None]).masked_fill_(none[order][:, None], 0.0)
-        return parts.view(*ids.shape, -1).sum(dim=1).to(x.dtype)      # (in the order of the choices, every time)
+        return parts.view(*ids.shape, y.shape[1]).sum(dim=1).to(x.dtype)      # (in the order of the choices, every time)
 
 
 def train(steps: int = 8, tokens: int = 512, experts: int = 8, width: int = 128, hidden: int = 256, rate: float = 0.1):
